@@ -59,6 +59,16 @@ enum kvp_table_mode {
   KVP_BLOCK_TABLE = 0,   /* table[row][logical page] = physical page, -1 hole */
   KVP_RAW_LOCATIONS = 1  /* table[row][position] = flat token slot, -1 hole   */
 };
+enum kvp_rotary_layout {
+  KVP_ROTARY_HALF = 0,        /* pair i: entries i and i + rotary_dim / 2     */
+  KVP_ROTARY_INTERLEAVED = 1  /* pair i: entries 2 i and 2 i + 1              */
+};
+enum kvp_rotary_scaling { /* of the frequencies theta_i = base^(-2 i / rotary_dim) */
+  KVP_ROTARY_PLAIN = 0,    /* as they are                                      */
+  KVP_ROTARY_LINEAR = 1,   /* theta_i / factor                                 */
+  KVP_ROTARY_NTK = 2,      /* base * factor^(rotary_dim / (rotary_dim - 2))    */
+  KVP_ROTARY_BY_PARTS = 3  /* slow pairs / factor, fast ones kept, see below   */
+};
 
 typedef struct kvp_pool kvp_pool;
 
@@ -84,6 +94,26 @@ int kv_pool_create(int num_pages, int page_size, int kv_heads, int head_dim,
                    int dtype, int num_layers, void* kv_buffer,
                    int32_t* error_word, kvp_pool** out);
 int kv_pool_destroy(kvp_pool* pool);
+
+/* ------------------------------------------------------------------------
+ * kv_latent_pool_create: describe a caller-owned buffer of latent rows, the
+ * cache of latent attention: one row [latent (latent_dim) | shared rotated
+ * key part (rope_dim)] per token, for all heads.
+ *   buffer      device, (num_layers, num_pages, page_size, latent_dim +
+ *               rope_dim) elements of ``dtype``, C-contiguous, 16-byte aligned.
+ *   latent_dim  1 .. 1024, rope_dim 0 .. 1024; a row's bytes must be a
+ *               multiple of 16.
+ * The descriptor is a kvp_pool with pages, slots and tables as any other:
+ * page_table_write, copy_pages(_device_count), gather_indices, kvp_sync_error,
+ * kvp_host_* and kvp_dev_* take it or serve it. rotary_store_latent and
+ * paged_latent_attention take only such pools; store_cache, the decode, verify
+ * and prefill attention and the whole-step calls (kvp_decode_step,
+ * kvp_decode_step_device(_io), kvp_verify_step_device_io) refuse them with
+ * KVP_ERR_INVALID_ARG. Destroyed by kv_pool_destroy. Errors as kv_pool_create.
+ * ---------------------------------------------------------------------- */
+int kv_latent_pool_create(int num_pages, int page_size, int latent_dim,
+                          int rope_dim, int dtype, int num_layers, void* buffer,
+                          int32_t* error_word, kvp_pool** out);
 
 /* ------------------------------------------------------------------------
  * store_cache: K[layer][out_loc[i]] = k[i], V[layer][out_loc[i]] = v[i] for
@@ -123,7 +153,7 @@ int page_table_write(int32_t* table, int table_rows_total, int table_cols,
 /* ------------------------------------------------------------------------
  * copy_pages: copy-on-write (chapter 15, section "The model": a shared tail
  * page is copied whole before a private write). For i < n, every layer, K
- * and V: page dst[i] <- page src[i]. src/dst device int32 [n]; a page
+ * and V (or the latent rows): page dst[i] <- page src[i]. src/dst device int32 [n]; a page
  * outside [0, num_pages) sets KVP_ERR_BAD_INDEX and is skipped. Pairs must
  * not overlap (no page is both a source and a destination).
  * ---------------------------------------------------------------------- */
@@ -232,6 +262,165 @@ int paged_prefill_attention(const kvp_pool* pool, int layer, const void* q,
                             int table_mode, const int32_t* table_rows,
                             const int32_t* context_lens, int window,
                             int sinks, float scale, void* out, void* stream);
+
+/* ------------------------------------------------------------------------
+ * kvp_rotary_frequencies: the frequencies of rotary_store_cache and
+ * rotary_store_latent, in turns: freqs[i] = theta_i / (2 pi) mod 1, times 2^64,
+ * for the rotary_dim / 2 pairs (host arithmetic in doubles; freqs is a HOST
+ * array, the caller copies it to the device once). theta_i = base^(-2 i /
+ * rotary_dim), scaled for long contexts:
+ *   KVP_ROTARY_PLAIN    as it is (the other parameters are ignored)
+ *   KVP_ROTARY_LINEAR   theta_i / factor
+ *   KVP_ROTARY_NTK      base replaced by base * factor^(d / (d - 2)), d =
+ *                       rotary_dim > 2: the slowest pair slows by factor, the
+ *                       fastest not at all
+ *   KVP_ROTARY_BY_PARTS theta_i (keep + (1 - keep) / factor), keep =
+ *                       clamp((n - low_turns) / (high_turns - low_turns), 0, 1),
+ *                       n = original_len theta_i / (2 pi), the turns the pair
+ *                       makes over the original context
+ * Errors: INVALID_ARG (odd or non-positive rotary_dim, base or factor not
+ * positive and finite, low_turns >= high_turns).
+ * ---------------------------------------------------------------------- */
+int kvp_rotary_frequencies(int rotary_dim, double base, int scaling,
+                           double factor, double original_len,
+                           double low_turns, double high_turns,
+                           uint64_t* freqs);
+
+/* ------------------------------------------------------------------------
+ * rotary_store_cache: rotary positions of a step's queries and keys, and
+ * store_cache of the rotated keys and the values, in one launch. For token
+ * i < n and pair (x, y) of the first rotary_dim entries of a head:
+ *     (x, y) -> attn_factor * (x cos a - y sin a, y cos a + x sin a),
+ *     a = positions[i] * theta_pair,
+ * the other entries as they are; then
+ *     q_out[i] = rotated q[i];  K[layer][out_loc[i]] = rotated k[i];
+ *     V[layer][out_loc[i]] = v[i].
+ * Angles are exact for every int32 position (fixed-point turns mod 1); the
+ * rotation is computed in fp32 and rounded once to the pool's dtype.
+ *   q, q_out  device, token i's head h at q + i * q_stride + h * q_head_stride
+ *             (strides in ELEMENTS, not negative), head_dim entries each.
+ *             q_out's rows do not overlap; it may be q with the same strides,
+ *             and may not overlap it otherwise. q NULL: only the store.
+ *   k, v      device, token i's kv_heads * head_dim contiguous entries at
+ *             k + i * k_stride. Both NULL: only q (out_loc may be NULL).
+ *   positions device int32 [n], any value.
+ *   out_loc   device int32 [n], as store_cache; a slot outside the pool sets
+ *             KVP_ERR_BAD_INDEX and that row is not stored (its q is rotated).
+ *   freqs     device uint64 [rotary_dim / 2] (kvp_rotary_frequencies).
+ *   rotary_dim  even, 0 .. head_dim (0: nothing turns).
+ *   layout    kvp_rotary_layout.
+ * Any element alignment is taken; rows, strides and head blocks that start on
+ * 16 bytes go 16 bytes at a time. n == 0 launches nothing. The pool's device
+ * must be current.
+ * ---------------------------------------------------------------------- */
+int rotary_store_cache(const kvp_pool* pool, int layer, const void* q,
+                       long long q_stride, long long q_head_stride,
+                       int num_q_heads, const void* k, long long k_stride,
+                       const void* v, long long v_stride,
+                       const int32_t* positions, const int32_t* out_loc, int n,
+                       const uint64_t* freqs, int rotary_dim, int layout,
+                       float attn_factor, void* q_out, long long q_out_stride,
+                       long long q_out_head_stride, void* stream);
+
+/* ------------------------------------------------------------------------
+ * rotary_store_latent: the same step on a latent pool. For token i < n:
+ *     q_pe_out[i] = rotated q_pe[i] (rope_dim entries per query head);
+ *     row[layer][out_loc[i]] = [latent[i] | rotated k_pe[i]].
+ *   q_pe, q_pe_out  device, strides as rotary_store_cache's q; q_pe_out is
+ *             usually the tail of each head of the absorbed queries
+ *             [n, num_q_heads, latent_dim + rope_dim]. q_pe NULL: only the store.
+ *   latent    device, latent_dim contiguous entries at latent + i * stride.
+ *   k_pe      device, rope_dim contiguous entries at k_pe + i * stride.
+ *             latent and k_pe both NULL: only q_pe.
+ * rotary_dim is even, 0 .. rope_dim. Everything else as rotary_store_cache.
+ * ---------------------------------------------------------------------- */
+int rotary_store_latent(const kvp_pool* pool, int layer, const void* q_pe,
+                        long long q_stride, long long q_head_stride,
+                        int num_q_heads, const void* latent,
+                        long long latent_stride, const void* k_pe,
+                        long long k_pe_stride, const int32_t* positions,
+                        const int32_t* out_loc, int n, const uint64_t* freqs,
+                        int rotary_dim, int layout, float attn_factor,
+                        void* q_pe_out, long long q_out_stride,
+                        long long q_out_head_stride, void* stream);
+
+/* ------------------------------------------------------------------------
+ * paged_latent_attention: attention over a latent pool in absorbed form, for
+ * decode (chunk 1), multi-token verify and chunks. With the key projection
+ * moved to the query (q = [W_K^T q_nope | rotated q_pe]) and the value
+ * projection to the output, every head attends the same rows: request b's
+ * query j (position p = L - q_lens[b] + j, L = context_lens[b], its tokens
+ * already stored) attends what a one-token decode step with context p + 1
+ * attends (causal; window and sinks as paged_decode_attention):
+ *     s_t = scale * <q[b][j][h], row[slot(b, t)]>
+ *     out[b][j][h] = sum_t softmax(s)_t * row[slot(b, t)][0 : latent_dim]
+ * A row is read once for its key and its value.
+ *   q    device [batch, chunk, num_q_heads, latent_dim + rope_dim], pool dtype,
+ *        contiguous, 16-byte aligned.
+ *   out  device [batch, chunk, num_q_heads, latent_dim], likewise; rows
+ *        j >= q_lens[b] are not written.
+ *   q_lens  device int32 [batch], 1 <= q_lens[b] <= min(chunk, L), or NULL
+ *        (chunk each).
+ *   workspace  device, >= paged_latent_attention_workspace_size() bytes,
+ *        256-byte aligned; contents need no initialisation and are clobbered;
+ *        calls that may overlap on the GPU (captured graphs among them) need
+ *        separate ones.
+ * Device-detected errors set KVP_ERR_BAD_INDEX: the rows of a request whose
+ * length, q_lens entry or table row is invalid are zero-filled; an attended
+ * table entry that is a hole or out of range is skipped (nothing is read
+ * through it) and that request's output is otherwise unspecified. The pool's
+ * device must be current. The rows that any of a request's queries attends
+ * must be finite for the others; rows past the context and in other pages may
+ * hold anything.
+ * ---------------------------------------------------------------------- */
+int paged_latent_attention_workspace_size(const kvp_pool* pool, int batch,
+                                          int chunk, int num_q_heads,
+                                          size_t* bytes);
+int paged_latent_attention(const kvp_pool* pool, int layer, const void* q,
+                           int batch, int chunk, int num_q_heads,
+                           const int32_t* q_lens, const int32_t* table,
+                           int table_rows_total, int table_cols,
+                           int table_mode, const int32_t* table_rows,
+                           const int32_t* context_lens, int window, int sinks,
+                           float scale, void* out, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * latent_prefill_attention: causal attention of ragged prompts in expanded
+ * form, for chunks long enough that projecting keys and values up once costs
+ * less than attending in the latent space (absorbed scores and values are
+ * latent_dim + rope_dim and latent_dim wide, expanded ones nope_dim + rope_dim
+ * and v_dim). The caller projects the latents (of a context in pages: the rows
+ * gather_indices names); the shared key part stays one row per token:
+ *     s_t = scale * (<q[0 : nope_dim], k[t][h]> + <q[nope_dim :], k_pe[t]>)
+ *     out = sum_t softmax(s)_t * v[t][h]
+ * Request b owns query rows q_start[b] .. q_start[b+1] - 1 and key rows
+ * k_start[b] .. k_start[b+1] - 1; its queries are its newest tokens: query j
+ * attends keys t <= (key rows - query rows) + j.
+ *   q     device, [total_q] rows, head h at + h * q_head_stride, nope_dim +
+ *         rope_dim entries; strides in ELEMENTS, not negative (views of a
+ *         projection's output; zero: one head or row for all).
+ *   k, v  device, [total_k] rows, nope_dim / v_dim entries per head.
+ *   k_pe  device, [total_k] rows of rope_dim entries (NULL when rope_dim is 0).
+ *   q_start, k_start  device int32 [batch + 1], ascending.
+ *   max_q the longest request's query rows (an upper bound is fine).
+ *   nope_dim, rope_dim, v_dim  up to 512 each (rope_dim may be 0).
+ *   out   device [total_q, num_heads, v_dim], contiguous.
+ * A request without queries is fine; rows of out that no request owns are not
+ * written. A request whose offsets are out of order or out of range, or that
+ * has more query rows than max_q or than key rows, sets KVP_ERR_BAD_INDEX in
+ * error_word (device int32 or NULL) and is skipped.
+ * ---------------------------------------------------------------------- */
+int latent_prefill_attention(const void* q, long long q_stride,
+                             long long q_head_stride, const void* k,
+                             long long k_stride, long long k_head_stride,
+                             const void* k_pe, long long k_pe_stride,
+                             const void* v, long long v_stride,
+                             long long v_head_stride, const int32_t* q_start,
+                             const int32_t* k_start, int batch, int num_heads,
+                             int max_q, int total_q, int total_k, int nope_dim,
+                             int rope_dim, int v_dim, int dtype, float scale,
+                             void* out, int32_t* error_word, void* stream);
 
 /* ------------------------------------------------------------------------
  * store_cache_and_attention: one layer of a decode step in one launch:

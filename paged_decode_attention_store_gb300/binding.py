@@ -25,6 +25,8 @@ KVP_ERR_TIMEOUT = -5
 
 KVP_F32, KVP_BF16 = 0, 1
 KVP_BLOCK_TABLE, KVP_RAW_LOCATIONS = 0, 1
+KVP_ROTARY_HALF, KVP_ROTARY_INTERLEAVED = 0, 1
+KVP_ROTARY_PLAIN, KVP_ROTARY_LINEAR, KVP_ROTARY_NTK, KVP_ROTARY_BY_PARTS = 0, 1, 2, 3
 
 _ERR_NAMES = {
     KVP_ERR_INVALID_ARG: "KVP_ERR_INVALID_ARG",
@@ -36,6 +38,7 @@ _ERR_NAMES = {
 
 # Every symbol the header declares, with its C signature.
 _vp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_ll, _d = ctypes.c_longlong, ctypes.c_double
 _ip = ctypes.POINTER(ctypes.c_int)
 _szp = ctypes.POINTER(ctypes.c_size_t)
 SIGNATURES = {
@@ -52,6 +55,16 @@ SIGNATURES = {
     "paged_decode_attention_noalloc": [_vp, _i, _vp, _i, _i, _vp, _i, _i, _i, _vp, _vp, _i, _i, _f, _vp, _vp],
     "store_cache_and_attention": [_vp, _i, _vp, _vp, _vp, _vp, _i, _i, _vp, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _i,
                                   _i, _i, _f, _vp, _vp, _sz, _vp],
+    "kv_latent_pool_create": [_i, _i, _i, _i, _i, _i, _vp, _vp, ctypes.POINTER(_vp)],
+    "kvp_rotary_frequencies": [_i, _d, _i, _d, _d, _d, _d, _vp],
+    "rotary_store_cache": [_vp, _i, _vp, _ll, _ll, _i, _vp, _ll, _vp, _ll, _vp, _vp, _i, _vp, _i, _i, _f, _vp, _ll, _ll,
+                           _vp],
+    "rotary_store_latent": [_vp, _i, _vp, _ll, _ll, _i, _vp, _ll, _vp, _ll, _vp, _vp, _i, _vp, _i, _i, _f, _vp, _ll, _ll,
+                            _vp],
+    "paged_latent_attention_workspace_size": [_vp, _i, _i, _i, _szp],
+    "paged_latent_attention": [_vp, _i, _vp, _i, _i, _i, _vp, _vp, _i, _i, _i, _vp, _vp, _i, _i, _f, _vp, _vp, _sz, _vp],
+    "latent_prefill_attention": [_vp, _ll, _ll, _vp, _ll, _ll, _vp, _ll, _vp, _ll, _ll, _vp, _vp, _i, _i, _i, _i, _i, _i,
+                                 _i, _i, _i, _f, _vp, _vp, _vp],
     "gather_indices": [_vp, _vp, _i, _i, _i, _vp, _vp, _i, _i, _i, _vp, _i, _vp],
     "kvp_sync_error": [_vp, _vp, _ip],
     "kvp_selftest_wait": [ctypes.c_longlong, _i, _vp, _vp],
@@ -188,6 +201,228 @@ def kv_pool_create(num_pages, page_size, kv_heads, head_dim, dtype, num_layers, 
         kv_buffer = torch.empty((2, num_layers, num_pages, page_size, kv_heads, head_dim),
                                 dtype=_TORCH_DTYPE[dtype], device=device)
     return Pool(kv_buffer, page_size, dtype)
+
+
+class LatentPool:
+    """A kvp_pool over a caller-owned buffer of latent rows (kept alive here):
+    (layers, num_pages, page_size, latent_dim + rope_dim), see
+    include/pagedkv.h, kv_latent_pool_create."""
+
+    def __init__(self, buffer, latent_dim, dtype, error_word=None):
+        _dev(buffer, _TORCH_DTYPE[dtype], "buffer")
+        if buffer.dim() != 4 or not 0 < latent_dim <= buffer.shape[3]:
+            raise ValueError("buffer must be (layers, num_pages, page_size, latent_dim + rope_dim)")
+        self.num_layers, self.num_pages, self.page_size, width = buffer.shape
+        self.latent_dim, self.rope_dim, self.kv_heads, self.head_dim = latent_dim, width - latent_dim, 1, width
+        self.dtype = dtype
+        self.kv_buffer = buffer
+        self.error_word = (torch.zeros(1, dtype=torch.int32, device=buffer.device)
+                           if error_word is None else _dev(error_word, torch.int32, "error_word"))
+        h = ctypes.c_void_p()
+        with torch.cuda.device(buffer.device):
+            _check(lib().kv_latent_pool_create(self.num_pages, self.page_size, latent_dim, self.rope_dim, dtype,
+                                               self.num_layers, _ptr(buffer), _ptr(self.error_word), ctypes.byref(h)),
+                   "kv_latent_pool_create")
+        self.handle = h
+
+    def __del__(self):
+        h = getattr(self, "handle", None)
+        if h is not None and _lib is not None:
+            _lib.kv_pool_destroy(h)
+            self.handle = None
+
+
+_SCALINGS = {"none": KVP_ROTARY_PLAIN, "linear": KVP_ROTARY_LINEAR, "ntk": KVP_ROTARY_NTK, "by_parts": KVP_ROTARY_BY_PARTS}
+_LAYOUTS = {"half": KVP_ROTARY_HALF, "interleaved": KVP_ROTARY_INTERLEAVED}
+
+
+def rotary_frequencies(rotary_dim, base=10000.0, scaling="none", factor=1.0, original_len=4096, low_turns=1.0,
+                       high_turns=32.0):
+    """kvp_rotary_frequencies: the pairs' frequencies as turns * 2^64 (list of ints, host)."""
+    if scaling not in _SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(_SCALINGS)}, got {scaling!r}")
+    out = (ctypes.c_uint64 * max(1, rotary_dim // 2))()
+    _check(lib().kvp_rotary_frequencies(int(rotary_dim), float(base), _SCALINGS[scaling], float(factor),
+                                        float(original_len), float(low_turns), float(high_turns), out),
+           "kvp_rotary_frequencies")
+    return list(out)
+
+
+class RotaryPlan:
+    """Frequencies on the device, layout and factor of rotary_store_cache and
+    rotary_store_latent. ``layout``: "half" or "interleaved"; ``scaling``:
+    "none", "linear", "ntk" or "by_parts" (see include/pagedkv.h,
+    kvp_rotary_frequencies); ``attn_factor`` multiplies what is rotated."""
+
+    def __init__(self, rotary_dim, base=10000.0, layout="half", scaling="none", factor=1.0, original_len=4096,
+                 low_turns=1.0, high_turns=32.0, attn_factor=1.0, device="cuda"):
+        if layout not in _LAYOUTS:
+            raise ValueError(f"layout must be one of {sorted(_LAYOUTS)}, got {layout!r}")
+        self.rotary_dim, self.layout, self.attn_factor = int(rotary_dim), _LAYOUTS[layout], float(attn_factor)
+        f = rotary_frequencies(rotary_dim, base, scaling, factor, original_len, low_turns, high_turns)
+        signed = [x - (1 << 64) if x >= 1 << 63 else x for x in f]
+        self.freqs = torch.tensor(signed, dtype=torch.int64).to(device)
+
+
+def _heads_view(t, dt, name, heads, width):
+    """(strides of token and head) of a [n, heads, width] view whose last axis is contiguous."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dt:
+        raise TypeError(f"{name} must be {dt}, got {t.dtype}")
+    if t.dim() != 3 or t.shape[2] != width or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must be [n, {'heads' if heads is None else heads}, {width}], got {tuple(t.shape)}")
+    n, h, w = t.shape
+    st, sh, se = t.stride()
+    sh = sh if h > 1 else w  # the stride of an axis of one entry says nothing
+    st = st if n > 1 else max(st, (h - 1) * sh + w)
+    if w > 1 and se != 1:
+        raise ValueError(f"{name}'s last axis must be contiguous")
+    return st, sh
+
+
+def _rotary_args(pool, q, k, v, kw, vw, positions, out_loc, rope, q_out, width, names):
+    dt = _TORCH_DTYPE[pool.dtype]
+    _dev(positions, torch.int32, "positions")
+    n = positions.numel()
+    if q is None and k is None:
+        raise ValueError("neither queries nor keys")
+    if (k is None) != (v is None):
+        raise ValueError(f"{names[1]} and {names[2]} come together")
+    if rope.rotary_dim > width:
+        raise ValueError(f"the plan turns {rope.rotary_dim} entries of {width}")
+    if q is not None:
+        qs = _heads_view(q, dt, names[0], None, width)
+        qo = _heads_view(q_out, dt, names[0] + "_out", q.shape[1], width)
+        if q.shape[0] != n or q_out.shape[0] != n:
+            raise ValueError(f"{names[0]} and {names[0]}_out must hold one row per position")
+        qargs = (_ptr(q), *qs, q.shape[1])
+        oargs = (_ptr(q_out), *qo)
+    else:
+        qargs, oargs = (None, 0, 0, 0), (None, 0, 0)
+    if k is not None:
+        _dev(out_loc, torch.int32, "out_loc")
+        if out_loc.numel() != n:
+            raise ValueError("out_loc and positions must have the same length")
+        rows = []
+        for t, nm, (h, w) in ((k, names[1], kw), (v, names[2], vw)):
+            if t.dim() == 2 and h == 1:
+                t = t[:, None]
+            st, sh = _heads_view(t, dt, nm, h, w)
+            if t.shape[0] != n or (h > 1 and sh != w):
+                raise ValueError(f"{nm} must be [n, {h}, {w}] with each token's row contiguous")
+            rows.append((_ptr(t), st))
+        kargs, vargs = rows
+    else:
+        kargs = vargs = (None, 0)
+    loc = _ptr(out_loc) if k is not None else None
+    return n, qargs, kargs, vargs, loc, oargs
+
+
+def rotary_store_cache(pool, layer, q, k, v, positions, out_loc, rope, q_out, stream=None):
+    """Rotary positions of a step's q and k, and the store of the rotated k and
+    of v, in one launch. q, q_out [n, Hq, D] (any token and head strides;
+    q_out may be q), k, v [n, kv_heads, D] (any token stride), positions and
+    out_loc int32 [n], ``rope`` a RotaryPlan. q and q_out None: only the store;
+    k, v and out_loc None: only q. See include/pagedkv.h."""
+    kw = (pool.kv_heads, pool.head_dim)
+    n, qa, ka, va, loc, oa = _rotary_args(pool, q, k, v, kw, kw, positions, out_loc, rope, q_out, pool.head_dim,
+                                          ("q", "k", "v"))
+    _check(lib().rotary_store_cache(pool.handle, layer, *qa, *ka, *va, _ptr(positions), loc, n, _ptr(rope.freqs),
+                                    rope.rotary_dim, rope.layout, rope.attn_factor, *oa, _stream(stream)),
+           "rotary_store_cache")
+
+
+def rotary_store_latent(pool, layer, q_pe, latent, k_pe, positions, out_loc, rope, q_pe_out, stream=None):
+    """rotary_store_cache of a LatentPool: q_pe, q_pe_out [n, Hq, rope_dim]
+    (q_pe_out usually the tail of the absorbed queries), latent [n,
+    latent_dim] and k_pe [n, rope_dim] with any token stride. q_pe and
+    q_pe_out None: only the store; latent, k_pe and out_loc None: only q_pe."""
+    n, qa, ka, va, loc, oa = _rotary_args(pool, q_pe, k_pe, latent, (1, pool.rope_dim), (1, pool.latent_dim), positions,
+                                          out_loc, rope, q_pe_out, pool.rope_dim, ("q_pe", "k_pe", "latent"))
+    _check(lib().rotary_store_latent(pool.handle, layer, *qa, *va, *ka, _ptr(positions), loc, n, _ptr(rope.freqs),
+                                     rope.rotary_dim, rope.layout, rope.attn_factor, *oa, _stream(stream)),
+           "rotary_store_latent")
+
+
+def paged_latent_attention_workspace_size(pool, batch, chunk, num_q_heads):
+    n = ctypes.c_size_t()
+    _check(lib().paged_latent_attention_workspace_size(pool.handle, batch, chunk, num_q_heads, ctypes.byref(n)),
+           "paged_latent_attention_workspace_size")
+    return n.value
+
+
+def alloc_latent_workspace(pool, batch, chunk, num_q_heads, device="cuda"):
+    nbytes = paged_latent_attention_workspace_size(pool, batch, chunk, num_q_heads)
+    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def paged_latent_attention(pool, layer, q, table, table_mode, context_lens, window, scale, out, workspace, q_lens=None,
+                           table_rows=None, stream=None, sinks=0):
+    """Absorbed latent attention over a LatentPool: q [B, C, Hq, latent_dim +
+    rope_dim], out [B, C, Hq, latent_dim]; query j of request b sits at position
+    context_lens[b] - q_lens[b] + j (q_lens None: C) and attends causally
+    (decode: C = 1). Rows j >= q_lens[b] are not written. See
+    include/pagedkv.h."""
+    dt = _TORCH_DTYPE[pool.dtype]
+    _dev(q, dt, "q")
+    _dev(out, dt, "out")
+    _dev(table, torch.int32, "table")
+    _dev(context_lens, torch.int32, "context_lens")
+    for t, nm in ((q_lens, "q_lens"), (table_rows, "table_rows")):
+        if t is not None:
+            _dev(t, torch.int32, nm)
+    if q.dim() != 4 or q.shape[3] != pool.head_dim or out.shape != (*q.shape[:3], pool.latent_dim):
+        raise ValueError("q must be [B, C, Hq, latent_dim + rope_dim] and out [B, C, Hq, latent_dim]")
+    B, C, Hq = q.shape[0], q.shape[1], q.shape[2]
+    if context_lens.numel() != B or any(t is not None and t.numel() != B for t in (q_lens, table_rows)):
+        raise ValueError("context_lens, q_lens and table_rows must be [B]")
+    ws_ptr, ws_bytes = (None, 0) if workspace is None else (_ptr(workspace), workspace.numel() * workspace.element_size())
+    _check(lib().paged_latent_attention(pool.handle, layer, _ptr(q), B, C, Hq, _ptr(q_lens), _ptr(table),
+                                        table.shape[0], table.shape[1], table_mode, _ptr(table_rows),
+                                        _ptr(context_lens), int(window or 0), int(sinks), float(scale), _ptr(out),
+                                        ws_ptr, ws_bytes, _stream(stream)), "paged_latent_attention")
+
+
+def latent_prefill_attention(q, k, k_pe, v, q_start, k_start, max_q, scale, out, error_word=None, stream=None):
+    """Causal attention of ragged prompts in expanded form: q [total_q, H, dn +
+    dr], k [total_k, H, dn], k_pe [total_k, dr] (None when dr is 0), v
+    [total_k, H, dv] (views with any token and head strides), out [total_q, H,
+    dv] contiguous, q_start/k_start int32 [B + 1]; query j of a request attends
+    its keys up to (key rows - query rows) + j. See include/pagedkv.h."""
+    dt = q.dtype
+    if dt not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"q must be float32 or bfloat16, got {dt}")
+    if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
+        raise ValueError("q, k and v must be [tokens, heads, entries]")
+    tq, H, width = q.shape
+    tk, _, dn = k.shape
+    dv = v.shape[2]
+    dr = width - dn
+    qs, ks, vs = _heads_view(q, dt, "q", None, width), _heads_view(k, dt, "k", H, dn), _heads_view(v, dt, "v", H, dv)
+    if dr < 0 or (dr > 0) != (k_pe is not None):
+        raise ValueError("q must be as wide as k and k_pe together")
+    ps = 0
+    if k_pe is not None:
+        if k_pe.dim() != 2:
+            raise ValueError("k_pe must be [tokens, entries]")
+        ps = _heads_view(k_pe[:, None], dt, "k_pe", 1, dr)[0]
+        if k_pe.shape[0] != tk:
+            raise ValueError("k and k_pe must hold the same tokens")
+    _dev(out, dt, "out")
+    _dev(q_start, torch.int32, "q_start")
+    _dev(k_start, torch.int32, "k_start")
+    if error_word is not None:
+        _dev(error_word, torch.int32, "error_word")
+    B = q_start.numel() - 1
+    if v.shape[0] != tk or out.shape != (tq, H, dv) or B < 0 or k_start.numel() != B + 1:
+        raise ValueError("v must hold k's tokens, out be [total_q, H, dv], q_start and k_start [B + 1]")
+    if B == 0:
+        return
+    _check(lib().latent_prefill_attention(_ptr(q), *qs, _ptr(k), *ks, _ptr(k_pe), ps, _ptr(v), *vs, _ptr(q_start),
+                                          _ptr(k_start), B, H, int(max_q), tq, tk, dn, dr, dv,
+                                          KVP_F32 if dt == torch.float32 else KVP_BF16, float(scale), _ptr(out),
+                                          _ptr(error_word), _stream(stream)), "latent_prefill_attention")
 
 
 def store_cache(pool, layer, k, v, out_loc, stream=None):

@@ -156,4 +156,29 @@ int launch_prefill_tc(const kvp_pool* pool, int layer, const void* q, int batch,
 // kernel after it, both as programmatic dependents.
 cudaError_t launch_tc(const TcArgs& a, const CombineArgs& c, cudaStream_t stream, void* ev_before, void* ev_after);
 
+
+// ---------------------------------------------------------------------------
+// Latent pools (latent.cu, latent_tc.cu) and expanded prompts (expanded.cu).
+// ---------------------------------------------------------------------------
+constexpr int kLatentMaxDim = 1024;  // the general kernel's registers hold 32 floats a lane
+
+TableRef make_table(const kvp_pool* pool, const int32_t* table, int rows_total, int cols, int mode);
+// Whether the pool's device is the current one.
+bool pool_device_current(const kvp_pool* pool);
+
+// One call of paged_latent_attention.
+struct LatentCall {
+  const kvp_pool* pool;
+  int layer;
+  const void* q;  // [B, C, H, width]
+  void* out;      // [B, C, H, latent_dim]
+  int B, C, H;
+  const int32_t* q_lens;
+  TableRef T;
+  const int32_t* table_rows;
+  const int32_t* context_lens;
+  int window, sinks;
+  float scale;
+  void* workspace;
+};
 }  // namespace kvp

@@ -1,10 +1,14 @@
 // Pool descriptor and device error word of libpagedkv.
 #include <new>
 
-#include "common.cuh"
+#include "attention.cuh"
 
-extern "C" int kv_pool_create(int num_pages, int page_size, int kv_heads, int head_dim, int dtype, int num_layers,
-                              void* kv_buffer, int32_t* error_word, kvp_pool** out) {
+namespace {
+
+// The descriptor both kinds of pool share: ``planes`` buffers of num_layers
+// layers of num_slots rows of kv_heads * head_dim elements.
+int pool_create(int num_pages, int page_size, int kv_heads, int head_dim, int latent_dim, int dtype, int num_layers,
+                void* kv_buffer, int32_t* error_word, kvp_pool** out) {
   if (!out || !kv_buffer || !error_word) return KVP_ERR_INVALID_ARG;
   if (num_pages <= 0 || page_size <= 0 || kv_heads <= 0 || head_dim <= 0 || num_layers <= 0) return KVP_ERR_INVALID_ARG;
   if (dtype != KVP_F32 && dtype != KVP_BF16) return KVP_ERR_INVALID_ARG;
@@ -25,13 +29,15 @@ extern "C" int kv_pool_create(int num_pages, int page_size, int kv_heads, int he
   p->page_size = page_size;
   p->kv_heads = kv_heads;
   p->head_dim = head_dim;
+  p->latent_dim = latent_dim;
+  p->planes = latent_dim ? 1 : 2;
   p->dtype = dtype;
   p->num_layers = num_layers;
   p->elem = elem;
   p->num_slots = (int)slots;
   p->row_bytes = row_bytes;
   p->layer_bytes = (size_t)slots * row_bytes;
-  p->kv_bytes = p->layer_bytes * num_layers;
+  p->kv_bytes = latent_dim ? 0 : p->layer_bytes * num_layers;
   p->buf = static_cast<char*>(kv_buffer);
   p->err = error_word;
   p->num_sms = sms;
@@ -40,8 +46,24 @@ extern "C" int kv_pool_create(int num_pages, int page_size, int kv_heads, int he
   p->ev_after = nullptr;
   p->tmap_hg = 0;
   p->tmap1_state = 0;
+  p->lat_maps = 0;
   *out = p;
   return KVP_OK;
+}
+
+}  // namespace
+
+extern "C" int kv_pool_create(int num_pages, int page_size, int kv_heads, int head_dim, int dtype, int num_layers,
+                              void* kv_buffer, int32_t* error_word, kvp_pool** out) {
+  return pool_create(num_pages, page_size, kv_heads, head_dim, 0, dtype, num_layers, kv_buffer, error_word, out);
+}
+
+extern "C" int kv_latent_pool_create(int num_pages, int page_size, int latent_dim, int rope_dim, int dtype,
+                                     int num_layers, void* buffer, int32_t* error_word, kvp_pool** out) {
+  if (latent_dim <= 0 || rope_dim < 0 || latent_dim > kvp::kLatentMaxDim || rope_dim > kvp::kLatentMaxDim)
+    return KVP_ERR_INVALID_ARG;
+  return pool_create(num_pages, page_size, 1, latent_dim + rope_dim, latent_dim, dtype, num_layers, buffer, error_word,
+                     out);
 }
 
 extern "C" int kv_pool_destroy(kvp_pool* pool) {

@@ -12,7 +12,9 @@ struct kvp_pool {
   int num_pages;    // pages in the buffer (dummy page included)
   int page_size;
   int kv_heads;
-  int head_dim;
+  int head_dim;     // latent pools: latent_dim + rope_dim, with kv_heads 1
+  int latent_dim;   // 0: K and V planes; else one plane of rows [latent | shared key part]
+  int planes;       // buffers of num_layers layers: 2 (K, V), or 1 (latent)
   int dtype;        // kvp_dtype
   int num_layers;
   int elem;         // bytes per element
@@ -31,6 +33,9 @@ struct kvp_pool {
   CUtensorMap tmap1; // the buffer as (d % 64, slot, d / 64, head, K/V x layer), for the prefill kernel:
   CUtensorMap tmap2; //   box (64, 16, 2, 1, 1) (tmap1, V) and box (64, 16, 1, 1, 1) (tmap2, K halves)
   int tmap1_state;   // 0: not encoded yet, 1: both encoded, -1: refused
+  CUtensorMap lat_box;     // latent pools: (d % 64, slot, d / 64, layer), box (64, 8, width / 64, 1), and
+  CUtensorMap lat_gather;  //   (d, layer x slot), box (64, 1) for row gathers
+  int lat_maps;            // 1: both encoded (at creation), 0: the pool's shape does not take them
 };
 
 namespace kvp {

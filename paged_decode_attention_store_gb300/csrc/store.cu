@@ -33,20 +33,21 @@ __global__ void store_cache_kernel(char* __restrict__ kbase, size_t kv_bytes, co
   }
 }
 
-// Pair p, layer l, K or V: page dst[p] <- page src[p]; one page of one layer
-// is page_size contiguous rows.
+// Pair p, layer l, K or V (or the latent rows): page dst[p] <- page src[p]; one
+// page of one layer is page_size contiguous rows. ``planes``: layers, times two
+// where K and V are apart.
 // With n_dev, the number of pairs is read on the device (at most n).
-__global__ void copy_pages_kernel(char* __restrict__ buf, size_t layer_bytes, int num_layers,
+__global__ void copy_pages_kernel(char* __restrict__ buf, size_t layer_bytes, int planes,
                                   const int32_t* __restrict__ src, const int32_t* __restrict__ dst, int n,
                                   const int32_t* __restrict__ n_dev, int page_chunks, int num_pages, int32_t* err) {
   if (n_dev) n = min(n, max(0, __ldg(n_dev)));
-  const long long total = (long long)n * num_layers * 2 * page_chunks;
+  const long long total = (long long)n * planes * page_chunks;
   for (long long u = blockIdx.x * (long long)blockDim.x + threadIdx.x; u < total;
        u += (long long)gridDim.x * blockDim.x) {
     const int c = (int)(u % page_chunks);
     long long rest = u / page_chunks;
-    const int kvl = (int)(rest % (2LL * num_layers));  // kv * num_layers + layer
-    const int p = (int)(rest / (2LL * num_layers));
+    const int kvl = (int)(rest % planes);  // kv * num_layers + layer
+    const int p = (int)(rest / planes);
     const int s = __ldg(src + p), d = __ldg(dst + p);
     if ((unsigned)s >= (unsigned)num_pages || (unsigned)d >= (unsigned)num_pages) {
       if (c == 0 && kvl == 0) set_error(err, KVP_ERR_BAD_INDEX);
@@ -95,7 +96,7 @@ static int sm_count_current() {
 
 extern "C" int store_cache(const kvp_pool* pool, int layer, const void* k, const void* v, const int32_t* out_loc,
                            int n, void* stream) {
-  if (!pool || n < 0 || layer < 0 || layer >= pool->num_layers) return KVP_ERR_INVALID_ARG;
+  if (!pool || pool->latent_dim || n < 0 || layer < 0 || layer >= pool->num_layers) return KVP_ERR_INVALID_ARG;
   if (n == 0) return KVP_OK;
   if (!k || !v || !out_loc) return KVP_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 15) return KVP_ERR_INVALID_ARG;
@@ -113,10 +114,10 @@ extern "C" int copy_pages(const kvp_pool* pool, const int32_t* src, const int32_
   if (n == 0) return KVP_OK;
   if (!src || !dst) return KVP_ERR_INVALID_ARG;
   const int page_chunks = (int)(pool->row_bytes * pool->page_size / 16);
-  const long long work = (long long)n * pool->num_layers * 2 * page_chunks;
+  const long long work = (long long)n * pool->num_layers * pool->planes * page_chunks;
   const int threads = 256;
   kvp::copy_pages_kernel<<<kvp::grid_for(work, threads, pool->num_sms), threads, 0, (cudaStream_t)stream>>>(
-      pool->buf, pool->layer_bytes, pool->num_layers, src, dst, n, nullptr, page_chunks, pool->num_pages, pool->err);
+      pool->buf, pool->layer_bytes, pool->num_layers * pool->planes, src, dst, n, nullptr, page_chunks, pool->num_pages, pool->err);
   return cudaGetLastError() == cudaSuccess ? KVP_OK : KVP_ERR_CUDA;
 }
 
@@ -125,10 +126,10 @@ extern "C" int copy_pages_device_count(const kvp_pool* pool, const int32_t* src,
   if (!pool || max_n < 0 || (max_n > 0 && (!src || !dst || !n_dev))) return KVP_ERR_INVALID_ARG;
   if (max_n == 0) return KVP_OK;
   const int page_chunks = (int)(pool->row_bytes * pool->page_size / 16);
-  const long long work = (long long)max_n * pool->num_layers * 2 * page_chunks;
+  const long long work = (long long)max_n * pool->num_layers * pool->planes * page_chunks;
   const int threads = 256;
   kvp::copy_pages_kernel<<<kvp::grid_for(work, threads, pool->num_sms), threads, 0, (cudaStream_t)stream>>>(
-      pool->buf, pool->layer_bytes, pool->num_layers, src, dst, max_n, n_dev, page_chunks, pool->num_pages,
+      pool->buf, pool->layer_bytes, pool->num_layers * pool->planes, src, dst, max_n, n_dev, page_chunks, pool->num_pages,
       pool->err);
   return cudaGetLastError() == cudaSuccess ? KVP_OK : KVP_ERR_CUDA;
 }

@@ -44,9 +44,7 @@ class PagedKVCache:
         self.dev = torch.device(device)
         extra = 1 if self.raw else 0  # dummy page of the raw-location layout
         alloc = torch.zeros if zero else torch.empty
-        self.kv = alloc((2, num_layers, num_pages + extra, page_size, kv_heads, head_dim), dtype=self.tdt,
-                        device=self.dev)
-        self.pool = kb.Pool(self.kv, page_size, kdt)
+        self._make_pool(alloc, num_pages + extra, kdt)
         self.host = kb.HostPageTable(num_pages, page_size, max_requests, free_stack)
         self.max_requests = max_requests
         max_seq_len = max_seq_len or num_pages * page_size
@@ -63,6 +61,10 @@ class PagedKVCache:
         self.lengths = np.zeros(max_requests, np.int64)  # tokens appended, per request (the caller's count)
         self.copies = 0
         self.h2d_bytes = 0  # bytes this driver has copied host -> device
+
+    def _make_pool(self, alloc, pages, kdt):
+        self.kv = alloc((2, self.layers, pages, self.P, self.Hkv, self.D), dtype=self.tdt, device=self.dev)
+        self.pool = kb.Pool(self.kv, self.P, kdt)
 
     # -- host-side staging -------------------------------------------------
     def _to_device(self, flat):
@@ -125,6 +127,16 @@ class PagedKVCache:
 
     def store(self, layer, k, v, out_loc):
         kb.store_cache(self.pool, layer, k, v, out_loc)
+
+    def rotary_store(self, layer, q, k, v, positions, out_loc, rope, q_out=None):
+        """Rotary positions of q and k and the store of the rotated k and of v
+        in one launch; returns the rotated q (``q_out``, or q itself when it
+        is None). ``positions`` int32 [n] on the device, ``rope`` a
+        binding.RotaryPlan; q [n, Hq, D], k/v [n, Hkv, D] may be views of one
+        projection's output."""
+        q_out = q if q_out is None else q_out
+        kb.rotary_store_cache(self.pool, layer, q, k, v, positions, out_loc, rope, q_out)
+        return q_out
 
     def workspace(self, batch, num_q_heads):
         key = (batch, num_q_heads)
@@ -348,6 +360,106 @@ class PagedKVCache:
         torch.cuda.synchronize(self.dev)
         self._steps[key] = st
         return st
+
+
+class PagedLatentCache(PagedKVCache):
+    """A paged cache of latent rows [latent | shared rotated key part], one per
+    token for all heads, with the page bookkeeping of :class:`PagedKVCache`
+    (new, fork, append with copy-on-write, trim, rewind, release).
+
+    A step appends its tokens (:meth:`append`), then per layer writes their
+    rows and rotates the queries' key part (:meth:`store`) and attends in the
+    latent space (:meth:`attend`: decode, multi-token verify and chunks). Long
+    prompts are cheaper in expanded form: project :meth:`rows` up and call
+    :func:`binding.latent_prefill_attention`."""
+
+    def __init__(self, num_pages, page_size, latent_dim, rope_dim, num_layers, dtype="bf16", max_requests=256,
+                 table_mode="block", max_seq_len=None, free_stack=None, device="cuda", zero=True):
+        self.latent_dim, self.rope_dim = latent_dim, rope_dim
+        super().__init__(num_pages, page_size, 1, latent_dim + rope_dim, num_layers, dtype=dtype,
+                         max_requests=max_requests, table_mode=table_mode, max_seq_len=max_seq_len,
+                         free_stack=free_stack, device=device, zero=zero)
+
+    def _make_pool(self, alloc, pages, kdt):
+        self.kv = alloc((self.layers, pages, self.P, self.D), dtype=self.tdt, device=self.dev)
+        self.pool = kb.LatentPool(self.kv, self.latent_dim, kdt)
+
+    def store(self, layer, q_pe, latent, k_pe, positions, out_loc, rope, q):
+        """Write the tokens' rows and the rotated ``q_pe`` into the tail of the
+        absorbed queries ``q`` [n, Hq, latent_dim + rope_dim], in one launch."""
+        kb.rotary_store_latent(self.pool, layer, q_pe, latent, k_pe, positions, out_loc, rope,
+                               q[..., self.latent_dim:])
+
+    def workspace(self, batch, num_q_heads, chunk=1):
+        key = (batch, num_q_heads, chunk)
+        if key not in self._ws:
+            self._ws[key] = kb.alloc_latent_workspace(self.pool, batch, chunk, num_q_heads, device=self.dev)
+        return self._ws[key]
+
+    def attend(self, layer, q, context_lens, window, scale, out, q_lens=None, table_rows=None, sinks=0):
+        """Absorbed attention: q [B, C, Hq, latent_dim + rope_dim], out [B, C,
+        Hq, latent_dim]; query j of request b sits at position context_lens[b]
+        - q_lens[b] + j (its rows stored)."""
+        ws = self.workspace(q.shape[0], q.shape[2], q.shape[1])
+        kb.paged_latent_attention(self.pool, layer, q, self.table, self.table_mode, context_lens, window, scale, out,
+                                  ws, q_lens=q_lens, table_rows=table_rows, sinks=sinks)
+
+    def step(self, rids, q, q_pe, latent, k_pe, rope, out, window, scale, sinks=0):
+        """One step for requests ``rids``, all layers, C new tokens each (C = 1:
+        decode): append, then per layer store and attend. Per-layer device
+        tensors: ``q`` [B, C, Hq, latent_dim + rope_dim] (absorbed; the tails are
+        filled from ``q_pe`` [B, C, Hq, rope_dim] rotated), ``latent`` [B * C,
+        latent_dim], ``k_pe`` [B * C, rope_dim] (request-major), ``out`` [B, C,
+        Hq, latent_dim]. With a window, the pages it leaves are released
+        afterwards. Asynchronous on the current stream."""
+        B, C, Hq, W = q[0].shape
+        r = np.ascontiguousarray(rids, dtype=np.int32)
+        before = self.lengths[r].copy()
+        out_loc = self.append(np.repeat(r, C))
+        flat = np.concatenate((before + C, r, (before[:, None] + np.arange(C)).ravel()))
+        d = self._to_device(flat)
+        lens, rows, positions = d[:B], d[B:2 * B], d[2 * B:]
+        for layer in range(self.layers):
+            self.store(layer, q_pe[layer].view(B * C, Hq, self.rope_dim), latent[layer], k_pe[layer], positions,
+                       out_loc, rope, q[layer].view(B * C, Hq, W))
+            self.attend(layer, q[layer], lens, window, scale, out[layer], table_rows=rows, sinks=sinks)
+        if window and window > 0:
+            for i, rid in enumerate(r):
+                self.trim(int(rid), max(0, int(before[i]) + C + 1 - (window - sinks)), sinks=sinks)
+
+    def rows(self, layer, rids):
+        """The stored rows of requests ``rids`` in logical order, [total,
+        latent_dim + rope_dim], and their offsets int32 [len(rids) + 1]: what
+        the projections of the expanded form take."""
+        r = np.ascontiguousarray(rids, dtype=np.int32)
+        lens = self.lengths[r]
+        d = self._to_device(np.concatenate((lens, r, [0], np.cumsum(lens))))
+        n = len(r)
+        slots = torch.empty((n, max(1, int(lens.max(initial=0)))), dtype=torch.int32, device=self.dev)
+        kb.gather_indices(self.pool, self.table, self.table_mode, d[:n], 0, slots, table_rows=d[n:2 * n])
+        live = torch.arange(slots.shape[1], device=self.dev)[None, :] < d[:n, None]
+        return self.kv[layer].view(-1, self.D)[slots[live].long()], d[2 * n:]
+
+    def _unsupported(self, what):
+        raise TypeError(f"{what} reads separate K and V: a latent cache uses store, attend and step")
+
+    def rotary_store(self, *args, **kwargs):
+        self._unsupported("rotary_store")
+
+    def store_and_attend(self, *args, **kwargs):
+        self._unsupported("store_and_attend")
+
+    def verify(self, *args, **kwargs):
+        self._unsupported("verify")
+
+    def prefill(self, *args, **kwargs):
+        self._unsupported("prefill")
+
+    def _multi_step(self, kind, *args, **kwargs):
+        self._unsupported(kind + "_step")
+
+    def decode_step(self, *args, **kwargs):
+        self._unsupported("decode_step")
 
 
 class DevicePagedKVCache:

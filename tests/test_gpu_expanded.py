@@ -1,0 +1,284 @@
+"""latent_prefill_attention against the 64-bit formulas, and against the absorbed form."""
+
+import math
+
+import pytest
+import torch
+
+import operator_reference as R
+from libbuild import ensure_built
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+@pytest.fixture(scope="module")
+def kb():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA GPU")
+    return ensure_built()
+
+
+class Case:
+    def __init__(self, kb, dtype, ql, kl, H, dn, dr, dv, seed=0, extra=0):
+        g = torch.Generator().manual_seed(seed)
+        self.kb, self.dt, self.ql, self.kl, self.H, self.dn, self.dr, self.dv = kb, DT[dtype], ql, kl, H, dn, dr, dv
+        tq, tk = sum(ql) + extra, sum(kl) + extra
+        rnd = lambda *s: torch.randn(s, generator=g).to(self.dt).to(DEV)  # noqa: E731
+        up = rnd(tk, H, dn + dv)
+        self.k, self.v = up[..., :dn], up[..., dn:]
+        self.pe = rnd(tk, 40 + dr)[:, 40:] if dr else None
+        self.q = rnd(tq, H, dn + dr)
+        if extra:  # rows that no request owns
+            self.q[-extra:] = float("nan")
+            up[-extra:] = float("nan")
+            if dr:
+                self.pe[-extra:] = float("nan")
+        start = lambda xs: [sum(xs[:i]) for i in range(len(xs) + 1)]  # noqa: E731
+        self.q0, self.k0 = start(ql), start(kl)
+        self.qs = torch.tensor(self.q0, dtype=torch.int32, device=DEV)
+        self.ks = torch.tensor(self.k0, dtype=torch.int32, device=DEV)
+        self.out = torch.full((tq, H, dv), 5.0, dtype=self.dt, device=DEV)
+        self.err = torch.zeros(1, dtype=torch.int32, device=DEV)
+        self.scale, self.max_q = 1.0 / math.sqrt(dn + dr), max(ql)
+
+    def run(self, **kw):
+        self.kb.latent_prefill_attention(self.q, self.k, self.pe, self.v, self.qs, self.ks, self.max_q, self.scale, self.out,
+                                         error_word=self.err, **kw)
+        torch.cuda.synchronize()
+
+    def verify(self, only=None):
+        out, q, v = self.out.cpu(), self.q.double().cpu(), self.v.double().cpu()
+        key = self.k.double().cpu()
+        if self.dr:
+            key = torch.cat((key, self.pe.double().cpu()[:, None].expand(-1, self.H, -1)), -1)
+        for b in range(len(self.ql)) if only is None else only:
+            n, m = self.ql[b], self.kl[b]
+            js = range(n) if n <= 16 else sorted({0, 1, 16, n // 2, n - 2, n - 1, min(127, n - 1), min(128, n - 1)})
+            for j in js:
+                keys = slice(self.k0[b], self.k0[b] + m - n + j + 1)
+                w, bound = R.attend(q[self.q0[b] + j], key[keys], v[keys], self.scale, self.dt)
+                R.check(out[self.q0[b] + j], w, bound, f"request {b} query {j}")
+        assert bool((out[sum(self.ql):] == 5.0).all()), "rows behind the last request were written"
+
+
+CASES = [
+    # dtype, query rows, key rows, H, dn, dr, dv, extra rows
+    ("bf16", [1], [1], 1, 128, 64, 128, 0),
+    ("bf16", [1, 2, 5], [1, 2, 5], 4, 128, 64, 128, 3),
+    ("bf16", [127, 128, 129], [127, 128, 129], 2, 128, 64, 128, 1),
+    ("bf16", [33, 1, 600, 257], [33, 1, 600, 257], 16, 128, 64, 128, 0),
+    ("bf16", [1, 1, 1], [1000, 128, 129], 8, 128, 64, 128, 0),       # single new tokens on long prefixes
+    ("bf16", [64, 200, 3], [700, 200, 515], 5, 128, 64, 128, 200),
+    ("bf16", [0, 40, 0, 7], [0, 40, 9, 300], 3, 128, 64, 128, 2),    # requests without queries, or without anything
+    ("bf16", [300], [5000], 2, 128, 64, 128, 0),
+    ("bf16", [40, 9], [40, 100], 3, 64, 32, 64, 1),                  # other dims: the general kernel
+    ("bf16", [17], [30], 2, 192, 0, 100, 1),
+    ("bf16", [5], [30], 2, 7, 5, 3, 1),
+    ("f32", [33, 1, 100], [33, 50, 300], 4, 128, 64, 128, 2),
+    ("f32", [20, 4], [20, 33], 2, 40, 8, 512, 0),
+]
+
+
+@pytest.mark.parametrize("dtype,ql,kl,H,dn,dr,dv,extra", CASES)
+def test_expanded_attention_is_the_formula(kb, dtype, ql, kl, H, dn, dr, dv, extra):
+    c = Case(kb, dtype, ql, kl, H, dn, dr, dv, seed=H, extra=extra)
+    c.run()
+    c.verify()
+    assert int(c.err) == 0
+    c.max_q += 1000  # an upper bound is fine
+    first = c.out.clone()
+    c.out.fill_(5.0)
+    c.run()
+    assert torch.equal(first, c.out) and int(c.err) == 0
+
+
+def test_strides(kb):
+    """Heads before tokens, odd token strides, and rows that do not start on 16 bytes."""
+    a = Case(kb, "bf16", [70, 130], [100, 130], 4, 128, 64, 128, seed=2)
+    a.run()
+    a.verify()
+    want = a.out.clone()
+    one = torch.zeros_like(a.k[:, :1]).expand(-1, 4, -1)  # one key part for all heads, by a head stride of zero
+    a.k = one
+    a.run()
+    a.verify()
+    a = Case(kb, "bf16", [70, 130], [100, 130], 4, 128, 64, 128, seed=2)
+    a.run()
+    for f in (lambda t: t.transpose(0, 1).contiguous().transpose(0, 1),
+              lambda t: torch.nn.functional.pad(t, (0, 8))[..., :t.shape[-1]],
+              lambda t: torch.nn.functional.pad(t, (3, 2))[..., 3:3 + t.shape[-1]]):
+        c = Case(kb, "bf16", [70, 130], [100, 130], 4, 128, 64, 128, seed=2)
+        c.q, c.k, c.v = f(c.q), f(c.k), f(c.v)
+        c.pe = f(c.pe[:, None])[:, 0]
+        c.run()
+        c.verify()
+    assert torch.equal(a.out, want)
+
+
+def test_bad_offsets_skip_their_request(kb):
+    for dn, dr, dv in ((128, 64, 128), (32, 16, 32)):
+        for which, what in ((0, [0, 40, 20, 100]), (0, [0, -3, 70, 100]), (0, [0, 40, 70, 101]), (1, [0, 40, 90, 131]),
+                            (1, [0, 40, 30, 130])):
+            c = Case(kb, "bf16", [40, 30, 30], [40, 50, 40], 2, dn, dr, dv, seed=4)
+            (c.qs if which == 0 else c.ks).copy_(torch.tensor(what, dtype=torch.int32))
+            c.run()
+            assert int(c.err) == kb.KVP_ERR_BAD_INDEX
+        c = Case(kb, "bf16", [40, 30, 30], [40, 50, 40], 2, dn, dr, dv, seed=4)
+        c.max_q = 35  # the first request has more rows
+        c.run()
+        assert int(c.err) == kb.KVP_ERR_BAD_INDEX
+        assert bool((c.out[:40] == 5.0).all())
+        c.verify(only=[1, 2])
+        c = Case(kb, "bf16", [40, 30, 30], [40, 50, 40], 2, dn, dr, dv, seed=4)
+        c.ks.copy_(torch.tensor([0, 40, 60, 130], dtype=torch.int32))  # 30 queries on 20 keys
+        c.k0 = [0, 40, 60]
+        c.kl = [40, 20, 70]
+        c.run()
+        assert int(c.err) == kb.KVP_ERR_BAD_INDEX
+        assert bool((c.out[40:70] == 5.0).all())
+        c.verify(only=[0, 2])
+
+
+def test_stream_and_graph(kb):
+    c = Case(kb, "bf16", [200, 64], [333, 64], 4, 128, 64, 128, seed=5)
+    c.run()
+    c.verify()
+    want = c.out.clone()
+    s = torch.cuda.Stream()
+    c.out.fill_(5.0)
+    torch.cuda.synchronize()
+    c.run(stream=s)
+    assert torch.equal(c.out, want)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        kb.latent_prefill_attention(c.q, c.k, c.pe, c.v, c.qs, c.ks, c.max_q, c.scale, c.out, error_word=c.err)
+    c.out.fill_(5.0)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(c.out, want)
+
+
+def test_large_scores_and_late_maximum(kb):
+    c = Case(kb, "bf16", [150], [400], 2, 128, 64, 128, seed=6)
+    ramp = torch.linspace(0.01, 8.0, 400, device=DEV)[:, None, None]
+    c.k.copy_((c.q[149:150, :, :128].float() * ramp).to(c.dt))
+    c.run()
+    c.verify()
+
+
+def test_refusals(kb):
+    c = Case(kb, "bf16", [10], [20], 2, 128, 64, 128)
+    call = lambda q=c.q, k=c.k, pe=c.pe, v=c.v, qs=c.qs, ks=c.ks, out=c.out, scale=1.0, max_q=10: (  # noqa: E731
+        kb.latent_prefill_attention(q, k, pe, v, qs, ks, max_q, scale, out))
+    for kw in (dict(q=c.q.half()), dict(k=c.k.float()), dict(qs=c.qs.long()), dict(out=c.out.float())):
+        with pytest.raises(TypeError):
+            call(**kw)
+    for kw in (dict(pe=None), dict(q=c.q[..., :150]), dict(k=c.k[:, :1]), dict(v=c.v[:19]), dict(out=c.out[:9]),
+               dict(ks=torch.cat((c.ks, c.ks))), dict(pe=c.pe[:19]), dict(k=c.k[..., ::2])):
+        with pytest.raises(ValueError):
+            call(**kw)
+    with pytest.raises(kb.KvpError):
+        call(scale=float("nan"))
+    with pytest.raises(kb.KvpError):
+        call(max_q=-1)
+    assert bool((c.out == 5.0).all())
+
+
+def test_both_forms_agree_on_a_paged_prompt(kb):
+    """A prompt through the latent cache: rows stored in pages and read back, the expanded form of the projected rows
+    against the absorbed form, W_K moved to the query and W_V to the output."""
+    from paged_decode_attention_store_gb300.engine import PagedLatentCache
+
+    H, dn, dr, dc, dv, n = 4, 128, 64, 512, 128, 150
+    g = torch.Generator().manual_seed(1)
+    rnd = lambda *s: torch.randn(s, generator=g).to(DEV)  # noqa: E731
+    cache = PagedLatentCache(64, 16, dc, dr, 2, max_requests=4)
+    rope = kb.RotaryPlan(dr, layout="interleaved", device=DEV)
+    wk, wv = rnd(H, dn, dc) / math.sqrt(dc), rnd(H, dv, dc) / math.sqrt(dc)
+    cache.new(1)
+    loc = cache.append([1] * n)
+    pos = torch.arange(n, dtype=torch.int32, device=DEV)
+    latent, k_pe = rnd(n, dc).bfloat16(), rnd(n, dr).bfloat16()
+    q_nope, q_pe = rnd(n, H, dn).bfloat16(), rnd(n, H, dr).bfloat16()
+    q = torch.empty((1, n, H, dc + dr), dtype=torch.bfloat16, device=DEV)
+    q[0, ..., :dc] = torch.einsum("nhd,hdc->nhc", q_nope.float(), wk).bfloat16()
+    cache.store(1, q_pe, latent, k_pe, pos, loc, rope, q[0])
+    scale = 1.0 / math.sqrt(dn + dr)
+    out = torch.empty((1, n, H, dc), dtype=torch.bfloat16, device=DEV)
+    cache.attend(1, q, torch.tensor([n], dtype=torch.int32, device=DEV), 0, scale, out,
+                 table_rows=torch.tensor([1], dtype=torch.int32, device=DEV))
+    absorbed = torch.einsum("nhc,hvc->nhv", out[0].float(), wv)
+    rows, start = cache.rows(1, [1])
+    assert torch.equal(rows[:, :dc], latent) and start.tolist() == [0, n]
+    k = torch.einsum("nc,hdc->nhd", rows[:, :dc].float(), wk).bfloat16()
+    v = torch.einsum("nc,hvc->nhv", rows[:, :dc].float(), wv).bfloat16()
+    ex = torch.empty((n, H, dv), dtype=torch.bfloat16, device=DEV)
+    kb.latent_prefill_attention(torch.cat((q_nope, q[0, ..., dc:]), -1), k, rows[:, dc:], v, start, start, n, scale, ex)
+    cache.check()
+    # both sides carry a handful of bf16 roundings (q or k projected, weights, output: each 2^-8 of its operand at
+    # most); a score of size s is moved by 2^-8 sqrt(s^2 / W) ~ 2^-8 each, so 2 % of the output's size holds both
+    d = (ex.float() - absorbed).norm() / absorbed.norm()
+    assert d < 0.02, float(d)
+
+
+def test_latent_cache_steps(kb):
+    """Prompt chunk, decode steps with a window, fork with copy-on-write, rewind: the engine's step against rows kept
+    by the test."""
+    from paged_decode_attention_store_gb300.engine import PagedLatentCache
+
+    H, dc, dr, layers = 8, 512, 64, 2
+    W = dc + dr
+    g = torch.Generator().manual_seed(5)
+    cache = PagedLatentCache(96, 16, dc, dr, layers, max_requests=6, table_mode="raw", max_seq_len=512)
+    rope = kb.RotaryPlan(dr, device=DEV)
+    theta = R.thetas(dr)
+    kept = {}
+    scale = W ** -0.5
+
+    def step(rids, C, window=0, sinks=0):
+        B = len(rids)
+        rnd = lambda *s: torch.randn(s, generator=g).bfloat16().to(DEV)  # noqa: E731
+        q = [rnd(B, C, H, W) for _ in range(layers)]
+        q_pe = [rnd(B, C, H, dr) for _ in range(layers)]
+        lat, pe = [rnd(B * C, dc) for _ in range(layers)], [rnd(B * C, dr) for _ in range(layers)]
+        out = [torch.empty((B, C, H, dc), dtype=torch.bfloat16, device=DEV) for _ in range(layers)]
+        base = [int(cache.lengths[r]) for r in rids]
+        cache.step(rids, q, q_pe, lat, pe, rope, out, window, scale, sinks=sinks)
+        cache.check()
+        for i, r in enumerate(rids):
+            pos = torch.arange(base[i], base[i] + C, dtype=torch.int32)
+            for layer in range(layers):
+                turned, _ = R.rotate(pe[layer][i * C:(i + 1) * C, None], pos, theta, "half")
+                new = torch.cat((lat[layer][i * C:(i + 1) * C].cpu(), turned[:, 0].to(torch.bfloat16)), -1)
+                kept[r, layer] = torch.cat((kept.get((r, layer), torch.empty((0, W), dtype=torch.bfloat16)), new))
+                for j in {0, C - 1}:
+                    p = base[i] + j
+                    x = kept[r, layer][R.span(p, window, sinks)].double()
+                    w, bound = R.attend(q[layer][i, j].double().cpu(), x, x[:, :dc], scale, torch.bfloat16)
+                    # the stored key part may round to the other neighbour (2^-8 of an entry); 64 of them move a
+                    # score by at most that times its size, and the weights by as much
+                    slack = 2.0 ** -7 * (q[layer][i, j, :, dc:].double().cpu().abs() @ x[:, dc:].abs().T).amax() * scale
+                    R.check(out[layer][i, j], w, bound + 2 * slack * x[:, :dc].abs().amax(0), f"request {r} query {j}")
+
+    for r in (0, 3):
+        cache.new(r)
+    step([0, 3], 37)
+    step([3, 0], 1)
+    step([0], 20)
+    cache.fork(3, 1)
+    for layer in range(layers):
+        kept[1, layer] = kept[3, layer].clone()
+    step([1, 3], 1)
+    assert cache.last_copies == 1
+    step([0, 1, 3], 5)
+    cache.rewind(1, 3)
+    for layer in range(layers):
+        kept[1, layer] = kept[1, layer][:-3]
+    step([1], 2)
+    for _ in range(20):
+        step([0, 1, 3], 1, window=24, sinks=2)
+    for what in ("decode_step", "verify_step", "prefill_step"):
+        with pytest.raises(TypeError):
+            getattr(cache, what)([0], [torch.empty((1, 1, H, W), device=DEV)], None, None, None, 0, 1.0)

@@ -1,0 +1,269 @@
+"""paged_latent_attention against the 64-bit formulas."""
+
+import math
+
+import pytest
+import torch
+
+import operator_reference as R
+from libbuild import ensure_built
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+@pytest.fixture(scope="module")
+def kb():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA GPU")
+    return ensure_built()
+
+
+class Case:
+    """Requests of the given lengths on shuffled pages; every slot that holds no token is NaN."""
+
+    def __init__(self, kb, dtype, lens, C, H, dc, dr, P, raw=False, seed=0, layers=1, layer=0, spare=3, mag=1.0):
+        g = torch.Generator().manual_seed(seed)
+        self.kb, self.dt, self.lens, self.C, self.H, self.dc, self.W, self.P, self.raw = (kb, DT[dtype], list(lens), C, H, dc,
+                                                                                          dc + dr, P, raw)
+        need = [-(-max(L, 1) // P) for L in lens]
+        pages = sum(need) + spare
+        self.buf = torch.full((layers, pages, P, self.W), float("nan"), dtype=self.dt)
+        order = torch.randperm(pages, generator=g).tolist()
+        B, cols = len(lens), max(need) + 1
+        table = torch.full((B, cols * (P if raw else 1)), -1, dtype=torch.int32)
+        self.slots, at = [], 0
+        for b, L in enumerate(lens):
+            mine = order[at:at + need[b]]
+            at += need[b]
+            sl = [mine[t // P] * P + t % P for t in range(L)]
+            self.slots.append(sl)
+            rows = torch.randn((L, self.W), generator=g) * mag
+            self.buf[layer].view(-1, self.W)[torch.tensor(sl, dtype=torch.long)] = rows.to(self.dt)
+            if raw:
+                table[b, :len(mine) * P] = torch.tensor([p * P + o for p in mine for o in range(P)])
+            else:
+                table[b, :len(mine)] = torch.tensor(mine)
+        self.layer = layer
+        self.buf, self.table = self.buf.to(DEV), table.to(DEV)
+        self.pool = kb.LatentPool(self.buf, dc, kb.KVP_BF16 if dtype == "bf16" else kb.KVP_F32)
+        self.q = torch.randn((B, C, H, self.W), generator=g).to(self.dt).to(DEV)
+        self.out = torch.full((B, C, H, dc), 5.0, dtype=self.dt, device=DEV)
+        self.scale = 1.0 / math.sqrt(self.W)
+        self.ws = kb.alloc_latent_workspace(self.pool, B, C, H, device=DEV)
+        self.ws.fill_(0xFF)  # NaN as floats: its contents must not matter
+        self.clens = torch.tensor(self.lens, dtype=torch.int32, device=DEV)
+
+    def run(self, window=0, sinks=0, q_lens=None, **kw):
+        self.kb.paged_latent_attention(self.pool, self.layer, self.q, self.table,
+                                       self.kb.KVP_RAW_LOCATIONS if self.raw else self.kb.KVP_BLOCK_TABLE, self.clens,
+                                       window, self.scale, self.out, self.ws, sinks=sinks,
+                                       q_lens=None if q_lens is None else torch.tensor(q_lens, dtype=torch.int32, device=DEV),
+                                       **kw)
+        torch.cuda.synchronize()
+        return self.out
+
+    def want(self, b, j, ql, window=0, sinks=0):
+        p = self.lens[b] - ql + j
+        sl = torch.tensor([self.slots[b][t] for t in R.span(p, window, sinks)], device=DEV)
+        x = self.buf[self.layer].view(-1, self.W)[sl].double().cpu()
+        return R.attend(self.q[b, j].double().cpu(), x, x[:, :self.dc], self.scale, self.dt)
+
+    def verify(self, window=0, sinks=0, q_lens=None, only=None):
+        out = self.out.cpu()
+        for b in range(len(self.lens)) if only is None else only:
+            ql = self.C if q_lens is None else q_lens[b]
+            js = range(ql) if ql <= 12 else sorted({0, 1, ql // 3, ql // 2, ql - 2, ql - 1})
+            for j in js:
+                w, bound = self.want(b, j, ql, window, sinks)
+                R.check(out[b, j], w, bound, f"request {b} query {j}")
+            assert bool((out[b, ql:] == 5.0).all()), f"request {b}: rows past its queries were written"
+
+
+CASES = [
+    # dtype, lens, C, H, dc, dr, P, raw, window, sinks
+    ("bf16", [1], 1, 16, 512, 64, 16, False, 0, 0),
+    ("bf16", [777], 1, 16, 512, 64, 16, False, 0, 0),
+    ("bf16", [1, 7, 8, 9, 63, 64, 65, 127, 128, 129, 200], 1, 16, 512, 64, 16, False, 0, 0),
+    ("bf16", [1, 2, 63, 64, 65, 1000], 1, 64, 512, 64, 16, False, 0, 0),
+    ("bf16", [5, 300, 4097], 1, 32, 512, 64, 64, False, 0, 0),
+    ("bf16", [64, 900, 33], 1, 128, 512, 64, 16, False, 0, 0),      # two row tiles of a token
+    ("bf16", [500, 130], 1, 40, 512, 64, 16, False, 0, 0),          # a tile with idle rows
+    ("bf16", [500, 130], 1, 1, 512, 64, 16, False, 0, 0),
+    ("bf16", [500, 130], 1, 3, 512, 64, 16, False, 0, 0),
+    ("bf16", [500, 130, 71], 1, 16, 512, 64, 1, True, 0, 0),        # scattered rows
+    ("bf16", [500, 130, 71], 1, 16, 512, 64, 1, False, 0, 0),
+    ("bf16", [500, 130, 71], 1, 16, 512, 64, 4, False, 0, 0),       # pages smaller than a group
+    ("bf16", [500, 130, 71], 1, 16, 512, 64, 12, False, 0, 0),      # and not a multiple of it
+    ("bf16", [500, 130, 71], 1, 16, 512, 64, 24, True, 0, 0),
+    ("bf16", [500, 130, 71], 1, 48, 512, 64, 8, False, 0, 0),
+    ("bf16", [4, 66, 700], 4, 64, 512, 64, 16, False, 0, 0),        # verify
+    ("bf16", [7, 70, 350], 7, 8, 512, 64, 16, False, 0, 0),
+    ("bf16", [5, 64, 69], 5, 40, 512, 64, 16, False, 0, 0),         # tiles that cut a token's heads
+    ("bf16", [300, 411], 130, 16, 512, 64, 16, False, 0, 0),        # a chunk: many tiles a request
+    ("bf16", [260], 100, 128, 512, 64, 16, False, 0, 0),
+    ("bf16", [3, 64, 100, 1000], 1, 16, 512, 64, 16, False, 50, 0),  # window
+    ("bf16", [3, 64, 100, 1000], 1, 16, 512, 64, 16, False, 50, 2),  # and sinks
+    ("bf16", [3, 64, 100, 1000], 3, 32, 512, 64, 16, False, 70, 17),
+    ("bf16", [300, 411], 130, 16, 512, 64, 4, True, 33, 5),
+    ("bf16", [5, 90], 1, 4, 128, 32, 4, False, 0, 0),               # other dims: the general kernel
+    ("bf16", [5, 90], 2, 4, 100, 12, 4, True, 20, 3),
+    ("bf16", [5, 90], 1, 2, 1024, 0, 4, False, 0, 0),
+    ("f32", [1, 33, 300], 1, 16, 512, 64, 16, False, 0, 0),
+    ("f32", [2, 40, 77], 2, 4, 64, 16, 4, True, 0, 0),
+    ("f32", [2, 40, 77], 2, 4, 64, 16, 4, False, 9, 2),
+]
+
+
+@pytest.mark.parametrize("dtype,lens,C,H,dc,dr,P,raw,window,sinks", CASES)
+def test_latent_attention_is_the_formula(kb, dtype, lens, C, H, dc, dr, P, raw, window, sinks):
+    c = Case(kb, dtype, lens, C, H, dc, dr, P, raw, seed=C + H)
+    c.run(window, sinks)
+    c.verify(window, sinks)
+    assert kb.kvp_sync_error(c.pool) == 0
+
+
+def test_one_long_request_is_split(kb):
+    """One request over every SM: partials and their join, twice, on a workspace of NaN."""
+    c = Case(kb, "bf16", [30011], 1, 16, 512, 64, 16, seed=3)
+    c.run()
+    first = c.out.clone()
+    c.verify()
+    c.run()
+    assert torch.equal(first, c.out), "the same call gives the same bits"
+
+
+def test_more_requests_than_threads(kb):
+    lens = [1 + (37 * i) % 90 for i in range(1500)]
+    c = Case(kb, "bf16", lens, 1, 8, 512, 64, 16, seed=5)
+    c.run()
+    c.verify(only=list(range(0, 1500, 97)) + [1498, 1499])
+
+
+def test_ragged_chunks_and_table_rows(kb):
+    c = Case(kb, "bf16", [40, 300, 129, 64], 20, 16, 512, 64, 16, seed=6)
+    ql = [20, 1, 13, 7]
+    c.run(q_lens=ql)
+    c.verify(q_lens=ql)
+    perm = [2, 0, 3, 1]
+    rows = torch.tensor(perm, dtype=torch.int32, device=DEV)
+    table = torch.full_like(c.table, -1)
+    for b, r in enumerate(perm):
+        table[r] = c.table[b]
+    keep, c.table = c.out.clone(), table
+    c.out.fill_(5.0)
+    c.run(q_lens=ql, table_rows=rows)
+    assert torch.equal(keep, c.out)
+
+
+def test_large_scores_and_late_maximum(kb):
+    """Scores of hundreds, the largest at the end of the context: the running maximum grows block after block."""
+    c = Case(kb, "bf16", [700, 90], 2, 16, 512, 64, 16, seed=7)
+    flat = c.buf[0].view(-1, c.W)
+    for b, L in enumerate(c.lens):
+        sl = torch.tensor(c.slots[b], device=DEV)
+        ramp = torch.linspace(0.01, 6.0, L, device=DEV)[:, None]
+        flat[sl] = (c.q[b, 0, 0].float()[None] * ramp + 0.01 * flat[sl].float()).to(c.dt)
+    c.run()
+    c.verify()
+
+
+def test_bad_requests_and_pages(kb):
+    """An invalid length or table row zero-fills its request, a hole is skipped, and the others are untouched by it."""
+    for dc, dr, H in ((512, 64, 16), (128, 32, 4)):
+        lens = [100, 50, 300, 64]
+        c = Case(kb, "bf16", lens, 1, H, dc, dr, 16, seed=9)
+        c.clens[1] = 0
+        c.run()
+        assert kb.kvp_sync_error(c.pool) == kb.KVP_ERR_BAD_INDEX
+        c.verify(only=[0, 2, 3])
+        assert bool((c.out[1] == 0).all())
+        c.clens[1] = c.table.shape[1] * 16 + 1
+        c.run()
+        assert kb.kvp_sync_error(c.pool) == kb.KVP_ERR_BAD_INDEX
+        c.verify(only=[0, 2, 3])
+        assert bool((c.out[1] == 0).all())
+        c.clens[1] = 50
+        c.run(table_rows=torch.tensor([0, 4, 2, -1], dtype=torch.int32, device=DEV))
+        assert kb.kvp_sync_error(c.pool) == kb.KVP_ERR_BAD_INDEX
+        c.verify(only=[0, 2])
+        assert bool((c.out[1] == 0).all()) and bool((c.out[3] == 0).all())
+        for bad in (-1, c.pool.num_pages, 2 ** 31 - 1):
+            c.table[2, 3] = bad
+            c.run()
+            assert kb.kvp_sync_error(c.pool) == kb.KVP_ERR_BAD_INDEX
+            c.verify(only=[0, 1, 3])
+        q_lens = [1, 2, 1, 1]
+        c.table[2, 3] = c.table[2, 2]
+        c.run(q_lens=q_lens)
+        assert kb.kvp_sync_error(c.pool) == kb.KVP_ERR_BAD_INDEX
+        assert bool((c.out[1] == 0).all())
+
+
+def test_layers_streams_and_graphs(kb):
+    a = Case(kb, "bf16", [333, 64, 1200], 1, 32, 512, 64, 16, seed=11, layers=3, layer=1)
+    b = Case(kb, "bf16", [900, 10], 2, 64, 512, 64, 4, raw=True, seed=12)
+    a.run(), b.run()
+    a.verify(), b.verify()
+    wa, wb = a.out.clone(), b.out.clone()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for o in (a.out, b.out):
+        o.fill_(5.0)
+    torch.cuda.synchronize()
+    call = lambda c, s=None: kb.paged_latent_attention(c.pool, c.layer, c.q, c.table,  # noqa: E731
+                                                       kb.KVP_RAW_LOCATIONS if c.raw else kb.KVP_BLOCK_TABLE, c.clens, 0,
+                                                       c.scale, c.out, c.ws, stream=s)
+    for _ in range(5):  # two calls at once, each with its own workspace
+        call(a, s1)
+        call(b, s2)
+    torch.cuda.synchronize()
+    assert torch.equal(a.out, wa) and torch.equal(b.out, wb)
+    graphs = []
+    for c in (a, b):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call(c)
+            call(c)
+        graphs.append(g)
+    for o in (a.out, b.out):
+        o.fill_(5.0)
+    for g in graphs:
+        g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(a.out, wa) and torch.equal(b.out, wb)
+    a.clens -= 7  # a replay follows the lengths
+    a.lens = [x - 7 for x in a.lens]
+    graphs[0].replay()
+    torch.cuda.synchronize()
+    a.verify()
+
+
+def test_refusals(kb):
+    c = Case(kb, "bf16", [100], 1, 16, 512, 64, 16, seed=1)
+    call = lambda q=c.q, out=c.out, ws=c.ws, lens=c.clens, scale=1.0, window=0, sinks=0, layer=0, mode=0, pool=c.pool: (  # noqa: E731
+        kb.paged_latent_attention(pool, layer, q, c.table, mode, lens, window, scale, out, ws, sinks=sinks))
+    for kw in (dict(q=c.q.float()), dict(out=c.out.float()), dict(lens=c.clens.long())):
+        with pytest.raises(TypeError):
+            call(**kw)
+    for kw in (dict(q=c.q[..., :512]), dict(out=c.q), dict(lens=torch.cat((c.clens, c.clens)))):
+        with pytest.raises(ValueError):
+            call(**kw)
+    for kw in (dict(ws=None), dict(ws=c.ws[:128]), dict(ws=c.ws[1:]), dict(scale=float("nan")), dict(scale=float("inf")),
+               dict(window=4, sinks=4), dict(sinks=-1), dict(layer=1), dict(layer=-1), dict(mode=2)):
+        with pytest.raises(kb.KvpError) as e:
+            call(**kw)
+        assert e.value.code == kb.KVP_ERR_INVALID_ARG
+    kv = kb.Pool(torch.zeros((2, 1, 4, 16, 1, 576), dtype=torch.bfloat16, device=DEV), 16, kb.KVP_BF16)
+    with pytest.raises(AttributeError):
+        call(pool=kv)
+    torch.cuda.synchronize()
+    assert bool((c.out == 5.0).all()) and kb.kvp_sync_error(c.pool) == 0
+
+
+def test_negative_and_zero_scale(kb):
+    for scale in (-0.05, 0.0):
+        c = Case(kb, "bf16", [100, 37], 1, 16, 512, 64, 16, seed=2)
+        c.scale = scale
+        c.run()
+        c.verify()
