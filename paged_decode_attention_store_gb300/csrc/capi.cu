@@ -62,8 +62,10 @@ extern "C" int kv_latent_pool_create(int num_pages, int page_size, int latent_di
                                      int num_layers, void* buffer, int32_t* error_word, kvp_pool** out) {
   if (latent_dim <= 0 || rope_dim < 0 || latent_dim > kvp::kLatentMaxDim || rope_dim > kvp::kLatentMaxDim)
     return KVP_ERR_INVALID_ARG;
-  return pool_create(num_pages, page_size, 1, latent_dim + rope_dim, latent_dim, dtype, num_layers, buffer, error_word,
-                     out);
+  const int rc = pool_create(num_pages, page_size, 1, latent_dim + rope_dim, latent_dim, dtype, num_layers, buffer,
+                             error_word, out);
+  if (rc == KVP_OK) kvp::latent_encode_maps(*out);
+  return rc;
 }
 
 extern "C" int kv_pool_destroy(kvp_pool* pool) {

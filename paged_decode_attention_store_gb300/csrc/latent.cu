@@ -141,7 +141,8 @@ using namespace kvp;
 extern "C" int paged_latent_attention_workspace_size(const kvp_pool* pool, int batch, int chunk, int num_q_heads,
                                                      size_t* bytes) {
   if (!pool || !pool->latent_dim || !bytes || batch <= 0 || chunk <= 0 || num_q_heads <= 0) return KVP_ERR_INVALID_ARG;
-  *bytes = 256;  // the general kernel needs no scratch
+  // the general kernel needs no scratch
+  *bytes = latent_tc_eligible(pool, chunk, num_q_heads) ? latent_tc_workspace(pool, chunk, num_q_heads) : 256;
   return KVP_OK;
 }
 
@@ -165,6 +166,25 @@ extern "C" int paged_latent_attention(const kvp_pool* pool, int layer, const voi
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255) || workspace_bytes < need) return KVP_ERR_INVALID_ARG;
   if (!pool_device_current(pool)) return KVP_ERR_INVALID_ARG;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (scale > 0.f && latent_tc_eligible(pool, chunk, num_q_heads)) {  // its row maxima are of unscaled scores
+    LatentCall c;
+    c.pool = pool;
+    c.layer = layer;
+    c.q = q;
+    c.out = out;
+    c.B = batch;
+    c.C = chunk;
+    c.H = num_q_heads;
+    c.q_lens = q_lens;
+    c.T = make_table(pool, table, table_rows_total, table_cols, table_mode);
+    c.table_rows = table_rows;
+    c.context_lens = context_lens;
+    c.window = window;
+    c.sinks = sinks;
+    c.scale = scale;
+    c.workspace = workspace;
+    return launch_latent_tc(c, st);
+  }
   LatGenArgs g;
   g.T = make_table(pool, table, table_rows_total, table_cols, table_mode);
   g.layer = pool->buf + (size_t)layer * pool->layer_bytes;

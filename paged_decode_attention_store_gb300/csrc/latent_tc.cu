@@ -1,0 +1,806 @@
+// Absorbed latent attention on the fifth-generation tensor cores: bf16 rows of
+// latent_dim 512 + rope_dim 64, any head count, decode, verify and chunks.
+//
+// Mathematics (latent.cu): every (token, head) row of a request's queries
+// attends the same rows x_t = [c_t | r_t]: s = scale <q, x_t>, o = sum
+// softmax(s)_t c_t. A row of 1152 bytes does 2 (576 + 512) flops per query row:
+// 1.9 flops a byte and query row. With the measured 281 flops a byte between the
+// tensor cores' rate and the memory's, up to about 150 query rows per latent
+// row are bound by memory, more by the tensor cores.
+//
+// Shape. A tile is R query rows (16, 32 or 64: the least that holds chunk *
+// heads, else 64) of one request in one CTA; keys come in blocks of 64.
+//  * S (64 x 64) = Q X^T: 36 M 64 N 64 K 16 MMAs (16 ns each, 0.59 us a block).
+//    Query rows lie on TMEM lanes (16 a warp quadrant), so a row's maximum and
+//    sum stay within two threads. When R < 64 the A tile reads past Q into the
+//    next bytes of shared memory: those rows of S are never read.
+//  * O^T (512 x R) += X_c^T P^T: latent entries on the M axis, four M 128 blocks
+//    of N = R, so that O takes 4 R <= 256 TMEM columns on all 128 lanes (O with
+//    rows on the lanes would take all 512 columns at M 64) and a small R costs
+//    little. X's block in shared memory serves both products: K-major for S,
+//    MN-major for O^T. 16 MMAs of 20-25 ns, 0.32-0.40 us a block.
+//  * Together at most 0.98 us of tensor time per block, against 1.65 us that one
+//    SM's share of the memory rate takes for the block's 72 KB: one CTA an SM
+//    with two block stages keeps the memory busy.
+//  * Layout of a block: groups of 8 keys, 9 KB each: 9 chunks of 64 entries, 8
+//    rows of 128 bytes (128-byte swizzle). Eight consecutive slots are one TMA
+//    box; any other rows come by TMA row gathers (four rows of one chunk each),
+//    with rows past the span, and rows behind holes, read as zeros (an
+//    out-of-range row index): whatever lies there never meets a weight of 0.
+//
+// Work split. A request's tiles are taken ``Gs`` at a time; such an item's key
+// blocks, the union over its tiles, laid end to end over all items, are divided
+// evenly over NG = SMs / Gs groups of Gs CTAs: CTA (g, t) walks group g's range
+// for tile t, the CTAs of a group read the same rows at the same time (L2 serves
+// all but one). A cut item leaves fp32 partials (slot 0: the group's first
+// piece, slot 1: its last), which latent_combine_kernel joins in block order.
+//
+// Warps: 0 loads, 1 issues S, 2 issues O, 4..11 run the softmax (quadrant =
+// warp % 4, two warps a quadrant, 32 keys of a block each) and the epilogue.
+// Every wait is bounded (2 s), as in the other kernels.
+#include <cstring>
+
+#include "attention.cuh"
+#include "tcgen05.cuh"
+
+namespace kvp {
+
+namespace {
+
+constexpr int kDc = 512, kDr = 64, kW = kDc + kDr;
+constexpr int kChunks = kW / 64;
+constexpr int kKeys = 64;                          // keys per block
+constexpr uint32_t kGroup = 8 * kW * 2;            // 8 keys
+constexpr uint32_t kStage = kKeys / 8 * kGroup;    // 73,728
+constexpr int kStages = 2;
+constexpr int kThreads = 384;
+constexpr int kSoft0 = 4, kSoftWarps = 8;
+constexpr int kMaxR = 64;
+constexpr int kMaxGs = 8;
+constexpr uint64_t kWaitNs = 2000000000ull;
+
+struct LatArgs {
+  CUtensorMap qmap;  // q as (d % 64, row, d / 64), box (64, R, 9)
+  CUtensorMap box;   // the pool's lat_box
+  CUtensorMap gat;   // the pool's lat_gather
+  TableRef T;
+  int layer;
+  int zero_row;      // a row index past the gather map's end: read as zeros
+  int row0;          // the layer's first row in the gather map
+  __nv_bfloat16* out;
+  const int32_t* context_lens;
+  const int32_t* table_rows;
+  const int32_t* q_lens;
+  int B, C, H, Gs, NG, window, sinks;
+  float scale_log2;
+  int4* merge;      // [CTAs]: {b, tile group, last group of CTAs, slot of the first piece}, b = -1: none
+  float2* part_ml;  // [CTAs][2][R]
+  float* part_o;    // [CTAs][2][R][512]
+  int32_t* err;
+};
+
+struct LatBars {
+  uint64_t q_full, q_free;
+  uint64_t full[kStages], empty[kStages];
+  uint64_t s_full[2], s_free[2];
+  uint64_t p_full, pv_done, o_free, drain, xbar;
+  uint32_t taddr;
+  int abort;
+  int late;  // raised by a wait for copies in flight that ran out
+  int b0;
+  long long off0;
+  int slots[kKeys];
+  float xch[2][2][kMaxR];
+};
+
+__device__ __forceinline__ bool lwait(uint64_t* bar, int k, volatile int* abort_flag, int32_t* err) {
+  return mbar_wait_bounded(bar, (uint32_t)(k & 1), abort_flag, err, kWaitNs);
+}
+
+// Request b's lengths; q tokens 0 when it is invalid.
+struct LatReq {
+  int L, ql, row;
+};
+__device__ __forceinline__ LatReq request(const LatArgs& a, int b) {
+  LatReq r;
+  r.L = __ldg(a.context_lens + b);
+  r.ql = a.q_lens ? __ldg(a.q_lens + b) : a.C;
+  r.row = a.table_rows ? __ldg(a.table_rows + b) : b;
+  if (r.ql < 1 || r.ql > a.C || r.L < r.ql || r.L > table_capacity(a.T) || r.row < 0 || r.row >= a.T.rows_total) r.ql = 0;
+  return r;
+}
+
+// An item's keys: the union of the spans of its query tokens j0 .. j1.
+struct LatItem {
+  Span u;
+  int n_keys, nblk;
+};
+template <int R>
+__device__ __forceinline__ LatItem item_of(const LatArgs& a, const LatReq& r, int tg) {
+  const int rows = r.ql * a.H, per = a.Gs * R;
+  const int j0 = tg * per / a.H, j1 = (min((tg + 1) * per, rows) - 1) / a.H;
+  const int p0 = r.L - r.ql + j0, p1 = r.L - r.ql + j1;
+  LatItem it;
+  it.u = attend_span(p1 + 1, a.window > 0 ? a.window + (p1 - p0) : 0, a.sinks);
+  it.n_keys = it.u.se + (p1 + 1 - it.u.lo);
+  it.nblk = (it.n_keys + kKeys - 1) / kKeys;
+  return it;
+}
+template <int R>
+__device__ __forceinline__ int groups_of(const LatArgs& a, int ql) {
+  const int per = a.Gs * R;
+  return (ql * a.H + per - 1) / per;
+}
+
+// Walks the pieces of this CTA's range; every role walks the same ones.
+template <int R>
+struct Pieces {
+  const LatArgs& a;
+  int b, tg, ng, t;
+  long long off, left;
+  LatReq r;
+  // the current piece
+  LatItem it;
+  int k0, k1, tile;
+  __device__ Pieces(const LatArgs& args, int t_, int b0, long long off0, long long n)
+      : a(args), b(b0), tg(0), t(t_), off(off0), left(n) {
+    r = request(a, b);
+    ng = groups_of<R>(a, r.ql);
+  }
+  // The next piece whose tile exists; false at the range's end.
+  __device__ bool next() {
+    while (left > 0) {
+      while (tg >= ng) {
+        if (++b >= a.B) return false;
+        r = request(a, b);
+        ng = groups_of<R>(a, r.ql);
+        tg = 0;
+      }
+      it = item_of<R>(a, r, tg);
+      if (off >= it.nblk) {  // only before the first piece: the range starts in a later item of the request
+        off -= it.nblk;
+        ++tg;
+        continue;
+      }
+      k0 = (int)off;
+      const long long end = off + left;
+      k1 = end < it.nblk ? (int)end : it.nblk;
+      left -= k1 - k0;
+      off = 0;
+      tile = tg * a.Gs + t;
+      ++tg;
+      if (tile * R < r.ql * a.H) return true;
+    }
+    return false;
+  }
+};
+
+__device__ __forceinline__ long long range_start(long long total, int g, int NG) { return NG ? total * g / NG : 0; }
+
+template <int R>
+constexpr size_t lat_smem() {
+  return (size_t)R * kW * 2 + kStages * kStage + R * 128 + 1024;
+}
+
+template <int R>
+__global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_constant__ LatArgs a) {
+  extern __shared__ __align__(1024) unsigned char lat_raw[];
+  __shared__ LatBars sb;
+  unsigned char* smem = lat_raw + ((1024u - (smem_u32(lat_raw) & 1023u)) & 1023u);
+  unsigned char* sQ = smem;                  // [9][R][128 B]
+  unsigned char* sP = sQ + R * kW * 2;       // [R][128 B]
+  unsigned char* sX = sP + R * 128;          // stages
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  volatile int* abort_flag = &sb.abort;
+  const int cta = blockIdx.x, g = cta / a.Gs, t = cta % a.Gs;
+
+  griddep_wait();
+  griddep_launch_dependents();
+
+  // ---- invalid requests: error word, rows of zeros -------------------------
+  for (int b = cta; b < a.B; b += gridDim.x) {
+    if (request(a, b).ql) continue;
+    if (tid == 0) set_error(a.err, KVP_ERR_BAD_INDEX);
+    uint4* o = reinterpret_cast<uint4*>(a.out + (size_t)b * a.C * a.H * kDc);
+    for (size_t x = tid; x < (size_t)a.C * a.H * (kDc / 8); x += kThreads) o[x] = make_uint4(0u, 0u, 0u, 0u);
+  }
+
+  // ---- this group's range of key blocks ------------------------------------
+  // Pass 0 sums all requests' blocks, pass 1 finds the request the range starts in.
+  auto blocks_of = [&](int b) -> long long {
+    long long n = 0;
+    if (b < a.B) {
+      const LatReq r = request(a, b);
+      const int ng = groups_of<R>(a, r.ql);
+      for (int tg = 0; tg < ng; ++tg) n += item_of<R>(a, r, tg).nblk;
+    }
+    return n;
+  };
+  const long long mine0 = blocks_of(tid);
+  long long total = 0;
+  for (int pass = 0; pass < 2; ++pass) {
+    long long base = 0;
+    const long long want = pass ? range_start(total, g, a.NG < total ? a.NG : (int)total) : 0;
+    for (int c0 = 0; c0 < a.B; c0 += kThreads) {
+      const long long n = c0 ? blocks_of(c0 + tid) : mine0;
+      long long sum;
+      const long long before = base + block_exclusive_scan(n, &sum);
+      if (pass && want >= before && want < before + n) {
+        sb.b0 = c0 + tid;
+        sb.off0 = want - before;
+      }
+      base += sum;
+    }
+    total = base;
+  }
+  // no more groups than blocks: the groups in use are the first ones, none of them empty
+  const int ng_used = a.NG < total ? a.NG : (int)total;
+  const long long r0 = range_start(total, g, ng_used), r1 = range_start(total, g + 1, ng_used);
+  if (g >= ng_used) {
+    if (tid == 0) a.merge[cta] = make_int4(-1, 0, 0, 0);
+    return;
+  }
+
+  if (tid == 0) {
+    mbar_init(&sb.q_full, 1);
+    mbar_init(&sb.q_free, 1);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&sb.full[s], 1);
+      mbar_init(&sb.empty[s], 1);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&sb.s_full[x], 1);
+      mbar_init(&sb.s_free[x], kSoftWarps);
+    }
+    mbar_init(&sb.p_full, kSoftWarps);
+    mbar_init(&sb.pv_done, 1);
+    mbar_init(&sb.o_free, kSoftWarps);
+    mbar_init(&sb.drain, 2);
+    mbar_init(&sb.xbar, kSoftWarps);
+    sb.abort = sb.late = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0) tc5::alloc512(&sb.taddr);
+  tc5::fence_before();
+  __syncthreads();
+  tc5::fence_after();
+  // TMEM: O^T at columns 0 .. 4 R - 1 (block j of 128 entries at j R), S buffers at 256 and 320
+  const uint32_t tbase = sb.taddr;
+  Pieces<R> pc(a, t, sb.b0, sb.off0, r1 - r0);
+
+  if (warp == 0) {
+    // ======================= loader ===========================================
+    int n = 0, np = 0;  // blocks and pieces issued
+    bool ok = true;
+    // Eight consecutive positions of a block table whose pages hold a multiple
+    // of eight, from a multiple of eight on, lie in one page: one table read.
+    const bool paged8 = !a.T.raw && (a.T.page_size & 7) == 0;
+    while (ok && pc.next()) {
+      if (np > 0) ok = __all_sync(0xffffffffu, lwait(&sb.q_free, np - 1, abort_flag, a.err));
+      if (!ok) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&sb.q_full, (uint32_t)R * kW * 2);
+        tc5::tma_3d(sQ, &a.qmap, 0, pc.b * a.C * a.H + pc.tile * R, 0, &sb.q_full);
+      }
+      ++np;
+      __syncwarp();
+      for (int i = pc.k0; i < pc.k1; ++i, ++n) {
+        const int st = n % kStages;
+        const Span u = pc.it.u;
+        const int o0 = i * kKeys;
+        unsigned boxes = 0;  // groups that are eight consecutive slots
+        int s0 = -1;         // lane gi < 8: group gi's first slot
+        bool fast = false;
+        if (paged8) {
+          const int og = o0 + 8 * lane;
+          if (lane < 8 && og + 7 < pc.it.n_keys && (og >= u.se || og + 7 < u.se)) {
+            const int p = span_pos(u, og);
+            if ((p & 7) == 0) s0 = resolve_slot(a.T, pc.r.row, p, a.err);
+          }
+          boxes = __ballot_sync(0xffffffffu, s0 >= 0) & 0xFFu;
+          fast = boxes == 0xFFu;
+        }
+        if (!fast) {
+          // lane l resolves keys 2 l and 2 l + 1; group gi is lanes 4 gi .. 4 gi + 3
+          int sl[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int o = o0 + 2 * lane + k;
+            sl[k] = o < pc.it.n_keys ? resolve_slot(a.T, pc.r.row, span_pos(u, o), a.err) : -1;
+          }
+          __syncwarp();  // this warp's previous copies have read the slot list
+          sb.slots[2 * lane] = sl[0];
+          sb.slots[2 * lane + 1] = sl[1];
+          const int g0 = __shfl_sync(0xffffffffu, sl[0], lane & ~3);
+          const unsigned run = __ballot_sync(0xffffffffu, sl[0] >= 0 && sl[1] == sl[0] + 1 && sl[0] == g0 + 2 * (lane & 3));
+          boxes = 0;
+#pragma unroll
+          for (int gi = 0; gi < 8; ++gi)
+            if (((run >> (4 * gi)) & 0xFu) == 0xFu) boxes |= 1u << gi;
+          __syncwarp();
+          if (lane < 8) s0 = sb.slots[8 * lane];
+        }
+        if (n >= kStages) ok = __all_sync(0xffffffffu, lwait(&sb.empty[st], n / kStages - 1, abort_flag, a.err));
+        if (!ok) break;
+        unsigned char* dst = sX + st * kStage;
+        if (lane == 0) mbar_arrive_expect_tx(&sb.full[st], kStage);
+        __syncwarp();
+        if (lane < 8 && ((boxes >> lane) & 1)) tma_load_4d(dst + lane * kGroup, &a.box, 0, s0, 0, a.layer, &sb.full[st]);
+        if (boxes != 0xFFu) {
+          // rows of the other groups: (group, half of four rows, chunk) per copy
+          for (int x = lane; x < 8 * 2 * kChunks; x += 32) {
+            const int gi = x / (2 * kChunks), y = x % (2 * kChunks), hf = y / kChunks, c = y % kChunks;
+            if ((boxes >> gi) & 1) continue;
+            int rr[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int s = sb.slots[8 * gi + 4 * hf + k];
+              rr[k] = s < 0 ? a.zero_row : a.row0 + s;
+            }
+            tc5::tma_gather4(dst + gi * kGroup + c * 1024 + hf * 512, &a.gat, 64 * c, rr[0], rr[1], rr[2], rr[3],
+                             &sb.full[st]);
+          }
+        }
+        __syncwarp();
+      }
+    }
+    // what was issued has landed (bounded) before the shared memory goes away
+    if (np > 0) lwait(&sb.q_full, np - 1, &sb.late, a.err);
+    for (int s = 0; s < kStages; ++s) {
+      const int cnt = (n + kStages - 1 - s) / kStages;
+      if (cnt > 0) lwait(&sb.full[s], cnt - 1, &sb.late, a.err);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ======================= S issuer =========================================
+    int n = 0, np = 0;
+    bool ok = true;
+    constexpr uint32_t id = tc5::idesc(64, kKeys, 0, 0);
+    const uint64_t dq = tc5::desc(smem_u32(sQ), 16, 1024);
+    while (ok && pc.next()) {
+      ok = __all_sync(0xffffffffu, lwait(&sb.q_full, np, abort_flag, a.err));
+      ++np;
+      for (int i = pc.k0; ok && i < pc.k1; ++i, ++n) {
+        const int st = n % kStages, buf = n & 1;
+        ok = __all_sync(0xffffffffu, lwait(&sb.full[st], n / kStages, abort_flag, a.err));
+        if (ok && n >= 2) ok = __all_sync(0xffffffffu, lwait(&sb.s_free[buf], n / 2 - 1, abort_flag, a.err));
+        if (!ok) break;
+        tc5::fence_after();
+        const uint64_t dx = tc5::desc(smem_u32(sX) + st * kStage, 16, kGroup);
+        const uint32_t ts = tbase + 256u + 64u * (uint32_t)buf;
+        if (tc5::elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < kW / 16; ++kk)
+            tc5::mma_ss(ts, dq + (uint64_t)(((kk >> 2) * R * 128 + (kk & 3) * 32) >> 4),
+                        dx + (uint64_t)(((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), id, kk > 0);
+          tc5::commit(&sb.s_full[buf]);
+          if (i + 1 == pc.k1) tc5::commit(&sb.q_free);
+        }
+        __syncwarp();
+      }
+    }
+    if (tc5::elect_one()) tc5::commit(&sb.drain);
+    __syncwarp();
+  } else if (warp == 2) {
+    // ======================= O issuer =========================================
+    int n = 0, np = 0;
+    bool ok = true;
+    constexpr uint32_t id = tc5::idesc(128, R, 1, 0);
+    const uint64_t dp = tc5::desc(smem_u32(sP), 16, 1024);
+    while (ok && pc.next()) {
+      if (np > 0) ok = __all_sync(0xffffffffu, lwait(&sb.o_free, np - 1, abort_flag, a.err));
+      ++np;
+      for (int i = pc.k0; ok && i < pc.k1; ++i, ++n) {
+        const int st = n % kStages;
+        ok = __all_sync(0xffffffffu, lwait(&sb.full[st], n / kStages, abort_flag, a.err));
+        if (ok) ok = __all_sync(0xffffffffu, lwait(&sb.p_full, n, abort_flag, a.err));
+        if (!ok) break;
+        tc5::fence_after();
+        const uint64_t dx = tc5::desc(smem_u32(sX) + st * kStage, 1024, kGroup);
+        const uint32_t first = i == pc.k0;
+        if (tc5::elect_one()) {
+#pragma unroll
+          for (int ks = 0; ks < kKeys / 16; ++ks)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              tc5::mma_ss(tbase + (uint32_t)(j * R), dx + (uint64_t)((2 * j * 1024 + ks * 2 * kGroup) >> 4),
+                          dp + (uint64_t)((ks * 32) >> 4), id, (first && ks == 0) ? 0u : 1u);
+          tc5::commit(&sb.pv_done);
+          tc5::commit(&sb.empty[st]);
+        }
+        __syncwarp();
+      }
+    }
+    if (tc5::elect_one()) tc5::commit(&sb.drain);
+    __syncwarp();
+  } else if (warp >= kSoft0) {
+    // ======================= softmax ==========================================
+    // Thread (quadrant, lane < 16, part): query row 16 quadrant + lane, keys
+    // 32 part .. 32 part + 31 of each block. The running maxima of rows lane and
+    // lane + 32 are kept by every warp alike (m0, m1), since all eight rescale O.
+    const int quad = warp & 3, part = (warp - kSoft0) >> 2;
+    const int row = 16 * quad + (lane & 15);
+    const bool mine = row < R;                 // warp-uniform: R is a multiple of 16
+    const bool active = mine && lane < 16;
+    const uint32_t lanes = (uint32_t)(32 * quad) << 16;
+    const float sl2 = a.scale_log2;
+    int n = 0, nx = 0;  // blocks, exchanges
+    int4 merge = make_int4(-1, 0, 0, 0);
+    bool ok = true;
+    auto exchange = [&](float v, float& x00, float& x01, float& x10, float& x11) -> bool {
+      volatile float* xc = &sb.xch[nx & 1][0][0];
+      if (active) xc[part * kMaxR + row] = v;
+      __threadfence_block();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sb.xbar);
+      const bool done = __all_sync(0xffffffffu, lwait(&sb.xbar, nx, abort_flag, a.err));
+      ++nx;
+      if (!done) return false;
+      x00 = xc[lane], x10 = xc[kMaxR + lane];
+      if (R > 32) x01 = xc[lane + 32], x11 = xc[kMaxR + lane + 32];
+      return true;
+    };
+    while (ok && pc.next()) {
+      const int rr = pc.tile * R + row;
+      const bool rv = rr < pc.r.ql * a.H;
+      const int p = pc.r.L - pc.r.ql + rr / a.H;
+      const Span u = pc.it.u, sr0 = attend_span(p + 1, a.window, a.sinks);
+      // the row attends key offsets [0, se) and [wb, we] of the item's span
+      const int se = rv ? sr0.se : 0;
+      const int wb0 = rv ? u.se + (sr0.lo - u.lo) : 1 << 30, we0 = rv ? u.se + (p - u.lo) : -1;
+      float m0 = -INFINITY, m1 = -INFINITY, lsum = 0.f;
+      for (int i = pc.k0; i < pc.k1; ++i, ++n) {
+        const int buf = n & 1;
+        ok = __all_sync(0xffffffffu, lwait(&sb.s_full[buf], n >> 1, abort_flag, a.err));
+        if (!ok) break;
+        float sv[32];
+        float mx = -INFINITY;
+        if (mine) {
+          tc5::fence_after();
+          const uint32_t ts = tbase + 256u + 64u * (uint32_t)buf + lanes + 32u * (uint32_t)part;
+          tc5::ld16(ts, sv);
+          tc5::ld16(ts + 16, sv + 16);
+          tc5::wait_ld();
+          tc5::fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sb.s_free[buf]);
+        if (mine) {
+          const int o0 = i * kKeys + 32 * part;
+          const int ea = se - o0, wb = wb0 - o0, we = we0 - o0;
+          if (!__all_sync(0xffffffffu, wb <= 0 && we >= 31)) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (!(c < ea || (c >= wb && c <= we))) sv[c] = -INFINITY;
+          }
+          float mt[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            mt[q] = tc5::max3(tc5::max3(sv[8 * q], sv[8 * q + 1], sv[8 * q + 2]),
+                              tc5::max3(sv[8 * q + 3], sv[8 * q + 4], sv[8 * q + 5]), fmaxf(sv[8 * q + 6], sv[8 * q + 7]));
+          mx = fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3])) * sl2;  // scale > 0
+        }
+        float a0 = -INFINITY, a1 = -INFINITY, b0 = -INFINITY, b1 = -INFINITY;
+        if (!(ok = exchange(mx, a0, a1, b0, b1))) break;
+        // rows lane and lane + 32: a new maximum once it is 8 above the old (P <= 256 fits bf16's exponent with ease)
+        float f0 = 1.f, f1 = 1.f;
+        const float x0 = fmaxf(a0, b0), x1 = R > 32 ? fmaxf(a1, b1) : -INFINITY;
+        if ((R >= 32 || lane < R) && x0 > m0 + 8.f) {
+          if (m0 > -INFINITY) f0 = exp2f(m0 - x0);
+          m0 = x0;
+        }
+        if (R > 32 && x1 > m1 + 8.f) {
+          if (m1 > -INFINITY) f1 = exp2f(m1 - x1);
+          m1 = x1;
+        }
+        const bool rescale = __any_sync(0xffffffffu, f0 != 1.f || f1 != 1.f);
+        uint4 w[4];
+        if (mine) {
+          const float mlo = __shfl_sync(0xffffffffu, m0, row & 31), mhi = R > 32 ? __shfl_sync(0xffffffffu, m1, row & 31) : 0.f;
+          const float flo = __shfl_sync(0xffffffffu, f0, row & 31), fhi = R > 32 ? __shfl_sync(0xffffffffu, f1, row & 31) : 1.f;
+          const float m = row < 32 ? mlo : mhi, f = row < 32 ? flo : fhi;
+          const float msub = m == -INFINITY ? 0.f : m;  // nothing kept yet: 2^-inf = 0
+          float ps0 = 0.f, ps1 = 0.f;
+          uint32_t* wp = reinterpret_cast<uint32_t*>(w);
+#pragma unroll
+          for (int x = 0; x < 16; ++x) {
+            float y0, y1;
+            tc5::fma2(y0, y1, sv[2 * x], sv[2 * x + 1], sl2, -msub);
+            const float p0 = tc5::ex2(y0), p1 = tc5::ex2(y1);
+            wp[x] = pack_bf16(p0, p1);
+            tc5::add2(ps0, ps1, p0, p1);
+          }
+          lsum = lsum * f + (ps0 + ps1);
+        }
+        if (n > 0) {  // O += P X of the block before is done: P's buffer is free and O may be scaled
+          ok = __all_sync(0xffffffffu, lwait(&sb.pv_done, n - 1, abort_flag, a.err));
+          if (!ok) break;
+        }
+        if (active) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<uint4*>(sP + row * 128 + (((4 * part + q) ^ (row & 7)) << 4)) = w[q];
+        }
+        if (rescale) {  // only rows with a maximum before, so O holds blocks of this piece
+          tc5::fence_after();
+#pragma unroll
+          for (int jj = 0; jj < 2; ++jj)
+#pragma unroll
+            for (int c0 = 0; c0 < R; c0 += 16) {
+              const uint32_t to = tbase + lanes + (uint32_t)((2 * part + jj) * R + c0);
+              float ov[16];
+              tc5::ld16(to, ov);
+              tc5::wait_ld();
+#pragma unroll
+              for (int c = 0; c < 16; ++c) ov[c] *= __shfl_sync(0xffffffffu, c0 + c < 32 ? f0 : f1, (c0 + c) & 31);
+              tc5::st16(to, ov);
+            }
+          tc5::wait_st();
+        }
+        fence_proxy_async_smem();
+        tc5::fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sb.p_full);
+      }
+      if (!ok) break;
+      // ---- the piece's end: O / l to the output, or (m, l, O) to a partial
+      ok = __all_sync(0xffffffffu, lwait(&sb.pv_done, n - 1, abort_flag, a.err));
+      if (!ok) break;
+      tc5::fence_after();
+      float a0 = 0.f, a1 = 0.f, b0 = 0.f, b1 = 0.f;
+      if (!(ok = exchange(lsum, a0, a1, b0, b1))) break;
+      const float l0 = a0 + b0, l1 = a1 + b1;
+      const bool whole = pc.k0 == 0 && pc.k1 == pc.it.nblk;
+      const int rows = min(R, pc.r.ql * a.H - pc.tile * R);
+      // a NaN sum is the answer of a NaN score; a sum of zero belongs to a row that attends nothing here
+      const float i0 = !whole ? 1.f : l0 == 0.f ? 0.f : 1.f / l0, i1 = !whole ? 1.f : l1 == 0.f ? 0.f : 1.f / l1;
+      // the range's first piece is the one that starts where the range does
+      const int slot = pc.left + (pc.k1 - pc.k0) == r1 - r0 ? 0 : 1;
+      const size_t pbase = (size_t)(2 * cta + slot) * R;
+      if (!whole && warp == kSoft0) {
+        if (lane < R) a.part_ml[pbase + lane] = make_float2(m0, l0);
+        if (R > 32) a.part_ml[pbase + lane + 32] = make_float2(m1, l1);
+        if (pc.k0 == 0) {
+          // this group starts the item: the last group is the first whose range reaches the item's end
+          const long long e = r1 - pc.left - (pc.k1 - pc.k0) + pc.it.nblk;
+          int gl = g;
+          while (range_start(total, gl + 1, ng_used) < e) ++gl;
+          merge = make_int4(pc.b, pc.tile, gl, slot);
+        }
+      }
+      __nv_bfloat16* orow = a.out + ((size_t)pc.b * a.C * a.H + (size_t)pc.tile * R) * kDc;
+      float* prow = a.part_o + pbase * kDc;
+#pragma unroll
+      for (int jj = 0; jj < 2; ++jj) {
+        const int d = 128 * (2 * part + jj) + 32 * quad + lane;
+#pragma unroll
+        for (int c0 = 0; c0 < R; c0 += 16) {
+          float ov[16];
+          tc5::ld16(tbase + lanes + (uint32_t)((2 * part + jj) * R + c0), ov);
+          tc5::wait_ld();
+          if (whole) {
+#pragma unroll
+            for (int c = 0; c < 16; ++c) ov[c] *= __shfl_sync(0xffffffffu, c0 + c < 32 ? i0 : i1, (c0 + c) & 31);
+            // lanes 2 i and 2 i + 1 trade columns, so that each stores two entries of one row
+#pragma unroll
+            for (int c = 0; c < 16; c += 2) {
+              const bool odd = lane & 1;
+              const float got = __shfl_xor_sync(0xffffffffu, odd ? ov[c] : ov[c + 1], 1);
+              const uint32_t v = odd ? pack_bf16(got, ov[c + 1]) : pack_bf16(ov[c], got);
+              const int rw = c0 + c + (odd ? 1 : 0);
+              if (rw < rows) *reinterpret_cast<uint32_t*>(orow + (size_t)rw * kDc + (d & ~1)) = v;
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < 16; ++c)
+              if (c0 + c < rows) prow[(size_t)(c0 + c) * kDc + d] = ov[c];
+          }
+        }
+      }
+      tc5::fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sb.o_free);
+    }
+    if (warp == kSoft0 && lane == 0) a.merge[cta] = merge;
+  }
+  // everything issued is done (bounded) before TMEM goes back
+  {
+    const uint64_t t0 = global_timer_ns();
+    while (!mbar_try_wait(&sb.drain, 0u))
+      if (global_timer_ns() - t0 > 2 * kWaitNs) {
+        set_error(a.err, KVP_ERR_TIMEOUT);
+        break;
+      }
+  }
+  tc5::fence_before();
+  __syncthreads();
+  if (warp == 0) tc5::dealloc512(tbase);
+}
+
+// Joins the partials of the items that a range boundary cut: block (x, y) takes
+// rows 4 y .. 4 y + 3 of the item that CTA x started and did not finish.
+template <int R>
+__global__ void __launch_bounds__(kDc / 4) latent_combine_kernel(const LatArgs a) {
+  griddep_wait();
+  const int cta = blockIdx.x, t = cta % a.Gs, g = cta / a.Gs;
+  const int4 mg = a.merge[cta];
+  if (mg.x < 0) return;
+  const int rows = request(a, mg.x).ql * a.H - mg.y * R;
+  const int n = mg.z - g + 1;
+  for (int r = 4 * blockIdx.y; r < min(4 * (int)blockIdx.y + 4, min(R, rows)); ++r) {
+    auto at = [&](int k) { return (size_t)(2 * ((g + k) * a.Gs + t) + (k ? 0 : mg.w)) * R + r; };
+    float m = -INFINITY;
+    for (int k = 0; k < n; ++k) m = fmaxf(m, a.part_ml[at(k)].x);
+    float l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int k = 0; k < n; ++k) {
+      const float2 ml = a.part_ml[at(k)];
+      const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - m);
+      const float4 x = reinterpret_cast<const float4*>(a.part_o + at(k) * kDc)[threadIdx.x];
+      l = fmaf(f, ml.y, l);
+      o.x = fmaf(f, x.x, o.x);
+      o.y = fmaf(f, x.y, o.y);
+      o.z = fmaf(f, x.z, o.z);
+      o.w = fmaf(f, x.w, o.w);
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    __nv_bfloat16* out = a.out + ((size_t)mg.x * a.C * a.H + (size_t)mg.y * R + r) * kDc + 4 * threadIdx.x;
+    *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+  }
+}
+
+struct LatShape {
+  int R, Gs, NG;
+};
+
+// The least tile that holds a request's rows, else 64. A request's tiles are
+// walked together, up to eight at a time: of 8 .. 5, the number that leaves
+// the fewest CTAs idle in a request's last group.
+LatShape lat_shape(const kvp_pool* pool, int C, int H) {
+  LatShape s;
+  const long long rows = (long long)C * H;
+  s.R = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  const long long tiles = (rows + s.R - 1) / s.R;
+  s.Gs = (int)(tiles < kMaxGs ? tiles : kMaxGs);
+  if (tiles > kMaxGs) {
+    long long best = -1;
+    for (int gs = kMaxGs; gs > kMaxGs / 2; --gs) {
+      const long long idle = (tiles + gs - 1) / gs * gs - tiles;
+      if (best < 0 || idle < best) {
+        best = idle;
+        s.Gs = gs;
+      }
+    }
+  }
+  if (s.Gs > pool->num_sms) s.Gs = pool->num_sms;
+  s.NG = pool->num_sms / s.Gs;
+  return s;
+}
+
+struct LatWs {
+  size_t merge, part_ml, part_o, total;
+};
+LatWs lat_ws(const LatShape& s) {
+  LatWs w;
+  const size_t ctas = (size_t)s.Gs * s.NG;
+  w.merge = 0;
+  w.part_ml = align256(ctas * sizeof(int4));
+  w.part_o = align256(w.part_ml + ctas * 2 * s.R * sizeof(float2));
+  w.total = align256(w.part_o + ctas * 2 * s.R * kDc * sizeof(float));
+  return w;
+}
+
+template <int R>
+cudaError_t launch_lat(const LatArgs& a, int ctas, cudaStream_t stream) {
+  // set at every call: it belongs to the current context
+  cudaError_t e = cudaFuncSetAttribute(latent_tc_kernel<R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)lat_smem<R>());
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3((unsigned)ctas);
+  c.blockDim = dim3(kThreads);
+  c.dynamicSmemBytes = lat_smem<R>();
+  c.stream = stream;
+  c.attrs = at;
+  c.numAttrs = 1;
+  e = cudaLaunchKernelEx(&c, latent_tc_kernel<R>, a);
+  if (e != cudaSuccess) return e;
+  c.gridDim = dim3((unsigned)ctas, R / 4);
+  c.blockDim = dim3(kDc / 4);
+  c.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&c, latent_combine_kernel<R>, a);
+}
+
+}  // namespace
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+  void* fn = nullptr;
+  cudaDriverEntryPointQueryResult qr;
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &qr) != cudaSuccess ||
+      qr != cudaDriverEntryPointSuccess)
+    return nullptr;
+  return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+}
+
+// The pool's two maps (see common.cuh), for the shapes the kernel takes.
+void latent_encode_maps(kvp_pool* pool) {
+  pool->lat_maps = 0;
+  if (pool->dtype != KVP_BF16 || pool->latent_dim != kDc || pool->head_dim != kW) return;
+  const long long rows = (long long)pool->num_layers * pool->num_slots;
+  if (rows >= 0x7fffffffLL) return;
+  const auto encode = tensor_map_encoder();
+  if (!encode) return;
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  const cuuint64_t bd[4] = {64, (cuuint64_t)pool->num_slots, kChunks, (cuuint64_t)pool->num_layers};
+  const cuuint64_t bs[3] = {kW * 2, 128, (cuuint64_t)pool->layer_bytes};
+  const cuuint32_t bb[4] = {64, 8, kChunks, 1};
+  const cuuint64_t gd[2] = {kW, (cuuint64_t)rows};
+  const cuuint64_t gs[1] = {kW * 2};
+  const cuuint32_t gb[2] = {64, 1};
+  if (encode(&pool->lat_box, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, pool->buf, bd, bs, bb, one,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return;
+  if (encode(&pool->lat_gather, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, pool->buf, gd, gs, gb, one,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return;
+  pool->lat_maps = 1;
+}
+
+bool latent_tc_eligible(const kvp_pool* pool, int C, int H) {
+  // row indices of a request stay in int
+  return pool->lat_maps == 1 && (long long)C * H <= 0x3fffffffLL;
+}
+
+size_t latent_tc_workspace(const kvp_pool* pool, int C, int H) { return lat_ws(lat_shape(pool, C, H)).total; }
+
+int launch_latent_tc(const LatentCall& c, cudaStream_t stream) {
+  const LatShape s = lat_shape(c.pool, c.C, c.H);
+  const LatWs w = lat_ws(s);
+  LatArgs a;
+  const auto encode = tensor_map_encoder();
+  if (!encode) return KVP_ERR_CUDA;
+  const cuuint32_t one[3] = {1, 1, 1};
+  const cuuint64_t qd[3] = {64, (cuuint64_t)c.B * c.C * c.H, kChunks};
+  const cuuint64_t qs[2] = {kW * 2, 128};
+  const cuuint32_t qb[3] = {64, (cuuint32_t)s.R, kChunks};
+  if (encode(&a.qmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(c.q), qd, qs, qb, one,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return KVP_ERR_CUDA;
+  a.box = c.pool->lat_box;
+  a.gat = c.pool->lat_gather;
+  a.T = c.T;
+  a.layer = c.layer;
+  a.row0 = c.layer * c.pool->num_slots;
+  a.zero_row = c.pool->num_layers * c.pool->num_slots;
+  a.out = static_cast<__nv_bfloat16*>(c.out);
+  a.context_lens = c.context_lens;
+  a.table_rows = c.table_rows;
+  a.q_lens = c.q_lens;
+  a.B = c.B;
+  a.C = c.C;
+  a.H = c.H;
+  a.Gs = s.Gs;
+  a.NG = s.NG;
+  a.window = c.window;
+  a.sinks = c.sinks;
+  a.scale_log2 = c.scale * 1.4426950408889634f;
+  char* ws = static_cast<char*>(c.workspace);
+  a.merge = reinterpret_cast<int4*>(ws + w.merge);
+  a.part_ml = reinterpret_cast<float2*>(ws + w.part_ml);
+  a.part_o = reinterpret_cast<float*>(ws + w.part_o);
+  a.err = c.pool->err;
+  const int ctas = s.Gs * s.NG;
+  const cudaError_t e = s.R == 16   ? launch_lat<16>(a, ctas, stream)
+                        : s.R == 32 ? launch_lat<32>(a, ctas, stream)
+                                    : launch_lat<64>(a, ctas, stream);
+  return e == cudaSuccess ? KVP_OK : KVP_ERR_CUDA;
+}
+
+}  // namespace kvp
