@@ -264,59 +264,79 @@ class RotaryPlan:
         self.freqs = torch.tensor(signed, dtype=torch.int64).to(device)
 
 
+def _current_stream():
+    """The current stream's handle (torch.cuda.current_stream() builds a Stream object: 3 us a call)."""
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+
+
+def _raw_stream(stream):
+    if stream is None:
+        return _current_stream()
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
 def _heads_view(t, dt, name, heads, width):
-    """(strides of token and head) of a [n, heads, width] view whose last axis is contiguous."""
+    """(address, stride of a token, stride of a head, heads) of a [n, heads, width] view whose last axis is contiguous."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != dt:
         raise TypeError(f"{name} must be {dt}, got {t.dtype}")
-    if t.dim() != 3 or t.shape[2] != width or (heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name} must be [n, {'heads' if heads is None else heads}, {width}], got {tuple(t.shape)}")
-    n, h, w = t.shape
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != width or (heads is not None and shape[1] != heads):
+        raise ValueError(f"{name} must be [n, {'heads' if heads is None else heads}, {width}], got {tuple(shape)}")
+    n, h, w = shape
     st, sh, se = t.stride()
-    sh = sh if h > 1 else w  # the stride of an axis of one entry says nothing
-    st = st if n > 1 else max(st, (h - 1) * sh + w)
-    if w > 1 and se != 1:
+    if h <= 1:
+        sh = w  # the stride of an axis of one entry says nothing
+    if n <= 1:
+        st = max(st, (h - 1) * sh + w)
+    if se != 1 and w > 1:
         raise ValueError(f"{name}'s last axis must be contiguous")
-    return st, sh
+    return t.data_ptr(), st, sh, h
 
 
-def _rotary_args(pool, q, k, v, kw, vw, positions, out_loc, rope, q_out, width, names):
+def _rows_view(t, dt, name, n, heads, width):
+    """(address, stride of a token) of [n, heads, width] (or, for one head, [n, width]) with each token's row contiguous."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dt:
+        raise TypeError(f"{name} must be {dt}, got {t.dtype}")
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 3 and shape[1] == heads and shape[2] == width:
+        good = (width == 1 or stride[2] == 1) and (heads == 1 or stride[1] == width)
+    else:
+        good = heads == 1 and len(shape) == 2 and shape[1] == width and (width == 1 or stride[1] == 1)
+    if not good or shape[0] != n:
+        raise ValueError(f"{name} must be [{n}, {heads}, {width}] with each token's row contiguous, got {tuple(shape)}")
+    return t.data_ptr(), stride[0] if n > 1 else heads * width
+
+
+def _rotary_call(fn, what, pool, layer, q, first, second, positions, out_loc, rope, q_out, width, stream):
+    """Marshals rotary_store_cache and rotary_store_latent: ``first`` and ``second`` are the two row inputs in the
+    order of the C call, each (tensor, name, heads, width)."""
     dt = _TORCH_DTYPE[pool.dtype]
-    _dev(positions, torch.int32, "positions")
-    n = positions.numel()
-    if q is None and k is None:
-        raise ValueError("neither queries nor keys")
+    n = _dev(positions, torch.int32, "positions").numel()
+    k, v = first[0], second[0]
     if (k is None) != (v is None):
-        raise ValueError(f"{names[1]} and {names[2]} come together")
+        raise ValueError(f"{first[1]} and {second[1]} come together")
     if rope.rotary_dim > width:
         raise ValueError(f"the plan turns {rope.rotary_dim} entries of {width}")
+    qp = qt = qh = heads = op = ot = oh = kp = kt = vp = vt = loc = 0
     if q is not None:
-        qs = _heads_view(q, dt, names[0], None, width)
-        qo = _heads_view(q_out, dt, names[0] + "_out", q.shape[1], width)
+        qp, qt, qh, heads = _heads_view(q, dt, "q", None, width)
+        op, ot, oh, _ = _heads_view(q_out, dt, "q_out", heads, width)
         if q.shape[0] != n or q_out.shape[0] != n:
-            raise ValueError(f"{names[0]} and {names[0]}_out must hold one row per position")
-        qargs = (_ptr(q), *qs, q.shape[1])
-        oargs = (_ptr(q_out), *qo)
-    else:
-        qargs, oargs = (None, 0, 0, 0), (None, 0, 0)
+            raise ValueError("the queries and their output must hold one row per position")
+    elif k is None:
+        raise ValueError("neither queries nor keys")
     if k is not None:
-        _dev(out_loc, torch.int32, "out_loc")
-        if out_loc.numel() != n:
+        kp, kt = _rows_view(k, dt, first[1], n, first[2], first[3])
+        vp, vt = _rows_view(v, dt, second[1], n, second[2], second[3])
+        if _dev(out_loc, torch.int32, "out_loc").numel() != n:
             raise ValueError("out_loc and positions must have the same length")
-        rows = []
-        for t, nm, (h, w) in ((k, names[1], kw), (v, names[2], vw)):
-            if t.dim() == 2 and h == 1:
-                t = t[:, None]
-            st, sh = _heads_view(t, dt, nm, h, w)
-            if t.shape[0] != n or (h > 1 and sh != w):
-                raise ValueError(f"{nm} must be [n, {h}, {w}] with each token's row contiguous")
-            rows.append((_ptr(t), st))
-        kargs, vargs = rows
-    else:
-        kargs = vargs = (None, 0)
-    loc = _ptr(out_loc) if k is not None else None
-    return n, qargs, kargs, vargs, loc, oargs
+        loc = out_loc.data_ptr()
+    _check(fn(pool.handle, layer, qp, qt, qh, heads, kp, kt, vp, vt, positions.data_ptr(), loc, n, rope.freqs.data_ptr(),
+              rope.rotary_dim, rope.layout, rope.attn_factor, op, ot, oh, _raw_stream(stream)), what)
 
 
 def rotary_store_cache(pool, layer, q, k, v, positions, out_loc, rope, q_out, stream=None):
@@ -325,12 +345,9 @@ def rotary_store_cache(pool, layer, q, k, v, positions, out_loc, rope, q_out, st
     q_out may be q), k, v [n, kv_heads, D] (any token stride), positions and
     out_loc int32 [n], ``rope`` a RotaryPlan. q and q_out None: only the store;
     k, v and out_loc None: only q. See include/pagedkv.h."""
-    kw = (pool.kv_heads, pool.head_dim)
-    n, qa, ka, va, loc, oa = _rotary_args(pool, q, k, v, kw, kw, positions, out_loc, rope, q_out, pool.head_dim,
-                                          ("q", "k", "v"))
-    _check(lib().rotary_store_cache(pool.handle, layer, *qa, *ka, *va, _ptr(positions), loc, n, _ptr(rope.freqs),
-                                    rope.rotary_dim, rope.layout, rope.attn_factor, *oa, _stream(stream)),
-           "rotary_store_cache")
+    h, d = pool.kv_heads, pool.head_dim
+    _rotary_call(lib().rotary_store_cache, "rotary_store_cache", pool, layer, q, (k, "k", h, d), (v, "v", h, d), positions,
+                 out_loc, rope, q_out, d, stream)
 
 
 def rotary_store_latent(pool, layer, q_pe, latent, k_pe, positions, out_loc, rope, q_pe_out, stream=None):
@@ -338,11 +355,8 @@ def rotary_store_latent(pool, layer, q_pe, latent, k_pe, positions, out_loc, rop
     (q_pe_out usually the tail of the absorbed queries), latent [n,
     latent_dim] and k_pe [n, rope_dim] with any token stride. q_pe and
     q_pe_out None: only the store; latent, k_pe and out_loc None: only q_pe."""
-    n, qa, ka, va, loc, oa = _rotary_args(pool, q_pe, k_pe, latent, (1, pool.rope_dim), (1, pool.latent_dim), positions,
-                                          out_loc, rope, q_pe_out, pool.rope_dim, ("q_pe", "k_pe", "latent"))
-    _check(lib().rotary_store_latent(pool.handle, layer, *qa, *va, *ka, _ptr(positions), loc, n, _ptr(rope.freqs),
-                                     rope.rotary_dim, rope.layout, rope.attn_factor, *oa, _stream(stream)),
-           "rotary_store_latent")
+    _rotary_call(lib().rotary_store_latent, "rotary_store_latent", pool, layer, q_pe, (latent, "latent", 1, pool.latent_dim),
+                 (k_pe, "k_pe", 1, pool.rope_dim), positions, out_loc, rope, q_pe_out, pool.rope_dim, stream)
 
 
 def paged_latent_attention_workspace_size(pool, batch, chunk, num_q_heads):
@@ -369,19 +383,24 @@ def paged_latent_attention(pool, layer, q, table, table_mode, context_lens, wind
     _dev(out, dt, "out")
     _dev(table, torch.int32, "table")
     _dev(context_lens, torch.int32, "context_lens")
-    for t, nm in ((q_lens, "q_lens"), (table_rows, "table_rows")):
-        if t is not None:
-            _dev(t, torch.int32, nm)
-    if q.dim() != 4 or q.shape[3] != pool.head_dim or out.shape != (*q.shape[:3], pool.latent_dim):
+    shape = q.shape
+    if len(shape) != 4 or shape[3] != pool.head_dim or out.shape != (*shape[:3], pool.latent_dim):
         raise ValueError("q must be [B, C, Hq, latent_dim + rope_dim] and out [B, C, Hq, latent_dim]")
-    B, C, Hq = q.shape[0], q.shape[1], q.shape[2]
-    if context_lens.numel() != B or any(t is not None and t.numel() != B for t in (q_lens, table_rows)):
-        raise ValueError("context_lens, q_lens and table_rows must be [B]")
-    ws_ptr, ws_bytes = (None, 0) if workspace is None else (_ptr(workspace), workspace.numel() * workspace.element_size())
-    _check(lib().paged_latent_attention(pool.handle, layer, _ptr(q), B, C, Hq, _ptr(q_lens), _ptr(table),
-                                        table.shape[0], table.shape[1], table_mode, _ptr(table_rows),
-                                        _ptr(context_lens), int(window or 0), int(sinks), float(scale), _ptr(out),
-                                        ws_ptr, ws_bytes, _stream(stream)), "paged_latent_attention")
+    B, C, Hq, _ = shape
+    per = [0, 0]
+    for i, (t, nm) in enumerate(((q_lens, "q_lens"), (table_rows, "table_rows"))):
+        if t is not None:
+            if _dev(t, torch.int32, nm).numel() != B:
+                raise ValueError(f"{nm} must be [B]")
+            per[i] = t.data_ptr()
+    if context_lens.numel() != B:
+        raise ValueError("context_lens must be [B]")
+    rows, cols = table.shape
+    ws_ptr, ws_bytes = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
+    _check(lib().paged_latent_attention(pool.handle, layer, q.data_ptr(), B, C, Hq, per[0], table.data_ptr(), rows, cols,
+                                        table_mode, per[1], context_lens.data_ptr(), int(window or 0), int(sinks),
+                                        float(scale), out.data_ptr(), ws_ptr, ws_bytes, _raw_stream(stream)),
+           "paged_latent_attention")
 
 
 def latent_prefill_attention(q, k, k_pe, v, q_start, k_start, max_q, scale, out, error_word=None, stream=None):
@@ -399,30 +418,24 @@ def latent_prefill_attention(q, k, k_pe, v, q_start, k_start, max_q, scale, out,
     tk, _, dn = k.shape
     dv = v.shape[2]
     dr = width - dn
-    qs, ks, vs = _heads_view(q, dt, "q", None, width), _heads_view(k, dt, "k", H, dn), _heads_view(v, dt, "v", H, dv)
     if dr < 0 or (dr > 0) != (k_pe is not None):
         raise ValueError("q must be as wide as k and k_pe together")
-    ps = 0
-    if k_pe is not None:
-        if k_pe.dim() != 2:
-            raise ValueError("k_pe must be [tokens, entries]")
-        ps = _heads_view(k_pe[:, None], dt, "k_pe", 1, dr)[0]
-        if k_pe.shape[0] != tk:
-            raise ValueError("k and k_pe must hold the same tokens")
+    qa = _heads_view(q, dt, "q", None, width)[:3]
+    ka = _heads_view(k, dt, "k", H, dn)[:3]
+    va = _heads_view(v, dt, "v", H, dv)[:3]
+    pa = (0, 0) if k_pe is None else _rows_view(k_pe, dt, "k_pe", tk, 1, dr)
     _dev(out, dt, "out")
     _dev(q_start, torch.int32, "q_start")
     _dev(k_start, torch.int32, "k_start")
-    if error_word is not None:
-        _dev(error_word, torch.int32, "error_word")
     B = q_start.numel() - 1
     if v.shape[0] != tk or out.shape != (tq, H, dv) or B < 0 or k_start.numel() != B + 1:
         raise ValueError("v must hold k's tokens, out be [total_q, H, dv], q_start and k_start [B + 1]")
     if B == 0:
         return
-    _check(lib().latent_prefill_attention(_ptr(q), *qs, _ptr(k), *ks, _ptr(k_pe), ps, _ptr(v), *vs, _ptr(q_start),
-                                          _ptr(k_start), B, H, int(max_q), tq, tk, dn, dr, dv,
-                                          KVP_F32 if dt == torch.float32 else KVP_BF16, float(scale), _ptr(out),
-                                          _ptr(error_word), _stream(stream)), "latent_prefill_attention")
+    err = 0 if error_word is None else _dev(error_word, torch.int32, "error_word").data_ptr()
+    _check(lib().latent_prefill_attention(*qa, *ka, *pa, *va, q_start.data_ptr(), k_start.data_ptr(), B, H, int(max_q), tq,
+                                          tk, dn, dr, dv, KVP_F32 if dt == torch.float32 else KVP_BF16, float(scale),
+                                          out.data_ptr(), err, _raw_stream(stream)), "latent_prefill_attention")
 
 
 def store_cache(pool, layer, k, v, out_loc, stream=None):

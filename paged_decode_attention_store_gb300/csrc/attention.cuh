@@ -181,9 +181,9 @@ struct LatentCall {
   float scale;
   void* workspace;
 };
-// The tcgen05 kernel (latent_tc.cu): the tensor maps of a pool it takes, whether
+// The tcgen05 kernel (latent_tc.cu): the tensor map of a pool it takes, whether
 // it takes a call's shape, its scratch, its launch (scale > 0).
-void latent_encode_maps(kvp_pool* pool);
+void latent_encode_map(kvp_pool* pool);
 bool latent_tc_eligible(const kvp_pool* pool, int C, int H);
 size_t latent_tc_workspace(const kvp_pool* pool, int C, int H);
 int launch_latent_tc(const LatentCall& c, cudaStream_t stream);

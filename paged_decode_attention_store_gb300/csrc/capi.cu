@@ -46,7 +46,7 @@ int pool_create(int num_pages, int page_size, int kv_heads, int head_dim, int la
   p->ev_after = nullptr;
   p->tmap_hg = 0;
   p->tmap1_state = 0;
-  p->lat_maps = 0;
+  p->lat_map_ok = 0;
   *out = p;
   return KVP_OK;
 }
@@ -64,7 +64,7 @@ extern "C" int kv_latent_pool_create(int num_pages, int page_size, int latent_di
     return KVP_ERR_INVALID_ARG;
   const int rc = pool_create(num_pages, page_size, 1, latent_dim + rope_dim, latent_dim, dtype, num_layers, buffer,
                              error_word, out);
-  if (rc == KVP_OK) kvp::latent_encode_maps(*out);
+  if (rc == KVP_OK) kvp::latent_encode_map(*out);
   return rc;
 }
 

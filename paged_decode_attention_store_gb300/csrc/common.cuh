@@ -33,9 +33,8 @@ struct kvp_pool {
   CUtensorMap tmap1; // the buffer as (d % 64, slot, d / 64, head, K/V x layer), for the prefill kernel:
   CUtensorMap tmap2; //   box (64, 16, 2, 1, 1) (tmap1, V) and box (64, 16, 1, 1, 1) (tmap2, K halves)
   int tmap1_state;   // 0: not encoded yet, 1: both encoded, -1: refused
-  CUtensorMap lat_box;     // latent pools: (d % 64, slot, d / 64, layer), box (64, 8, width / 64, 1), and
-  CUtensorMap lat_gather;  //   (d, layer x slot), box (64, 1) for row gathers
-  int lat_maps;            // 1: both encoded (at creation), 0: the pool's shape does not take them
+  CUtensorMap lat_box;  // latent pools: (d % 64, slot, d / 64, layer), box (64, 8, width / 64, 1)
+  int lat_map_ok;       // 1: encoded (at creation), 0: the pool's shape does not take it
 };
 
 namespace kvp {

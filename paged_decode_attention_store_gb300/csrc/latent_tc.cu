@@ -24,9 +24,12 @@
 //    with two block stages keeps the memory busy.
 //  * Layout of a block: groups of 8 keys, 9 KB each: 9 chunks of 64 entries, 8
 //    rows of 128 bytes (128-byte swizzle). Eight consecutive slots are one TMA
-//    box; any other rows come by TMA row gathers (four rows of one chunk each),
-//    with rows past the span, and rows behind holes, read as zeros (an
-//    out-of-range row index): whatever lies there never meets a weight of 0.
+//    box; any other rows are copied by a warp with 16-byte asynchronous
+//    copies (TMA row gathers of 4 x 128 bytes took 41 ns each, 6 us a block),
+//    rows past the span and behind holes as zeros: whatever lies in their place
+//    must not meet a weight of 0.
+//  * The loader names the rows of two blocks beyond those in shared memory and
+//    prefetches them to L2, which so serves as the deeper part of the ring.
 //
 // Work split. A request's tiles are taken ``Gs`` at a time; such an item's key
 // blocks, the union over its tiles, laid end to end over all items, are divided
@@ -35,8 +38,9 @@
 // all but one). A cut item leaves fp32 partials (slot 0: the group's first
 // piece, slot 1: its last), which latent_combine_kernel joins in block order.
 //
-// Warps: 0 loads, 1 issues S, 2 issues O, 4..11 run the softmax (quadrant =
-// warp % 4, two warps a quadrant, 32 keys of a block each) and the epilogue.
+// Warps: 0 loads, 1 issues S, 2 issues O, 3 copies scattered rows, 4..11 run the
+// softmax (quadrant = warp % 4, two warps a quadrant, 32 keys of a block each)
+// and the epilogue.
 // Every wait is bounded (2 s), as in the other kernels.
 #include <cstring>
 
@@ -54,6 +58,7 @@ constexpr uint32_t kGroup = 8 * kW * 2;            // 8 keys
 constexpr uint32_t kStage = kKeys / 8 * kGroup;    // 73,728
 constexpr int kStages = 2;
 constexpr int kThreads = 384;
+constexpr int kAhead = 2;  // blocks prefetched to L2 beyond the stages
 constexpr int kSoft0 = 4, kSoftWarps = 8;
 constexpr int kMaxR = 64;
 constexpr int kMaxGs = 8;
@@ -62,18 +67,17 @@ constexpr uint64_t kWaitNs = 2000000000ull;
 struct LatArgs {
   CUtensorMap qmap;  // q as (d % 64, row, d / 64), box (64, R, 9)
   CUtensorMap box;   // the pool's lat_box
-  CUtensorMap gat;   // the pool's lat_gather
   TableRef T;
   int layer;
-  int zero_row;      // a row index past the gather map's end: read as zeros
-  int row0;          // the layer's first row in the gather map
+  const char* rows;  // the layer's slot 0
   __nv_bfloat16* out;
   const int32_t* context_lens;
   const int32_t* table_rows;
   const int32_t* q_lens;
   int B, C, H, Gs, NG, window, sinks;
   float scale_log2;
-  int4* merge;      // [CTAs]: {b, tile group, last group of CTAs, slot of the first piece}, b = -1: none
+  int4* merge;      // [CTAs]: the item a CTA starts and does not finish: {first output row, rows, last group of
+                    // CTAs, slot of the first piece}; x = -1: none
   float2* part_ml;  // [CTAs][2][R]
   float* part_o;    // [CTAs][2][R][512]
   int32_t* err;
@@ -81,7 +85,9 @@ struct LatArgs {
 
 struct LatBars {
   uint64_t q_full, q_free;
-  uint64_t full[kStages], empty[kStages];
+  uint64_t job[kStages];    // loader -> copier: slots and boxes of the stage's block are set
+  uint64_t full[kStages];   // loader (boxes' bytes) and copier -> issuers: the block is in
+  uint64_t empty[kStages];  // O issuer (commit) -> loader
   uint64_t s_full[2], s_free[2];
   uint64_t p_full, pv_done, o_free, drain, xbar;
   uint32_t taddr;
@@ -89,7 +95,8 @@ struct LatBars {
   int late;  // raised by a wait for copies in flight that ran out
   int b0;
   long long off0;
-  int slots[kKeys];
+  int slots[kStages][kKeys];
+  int boxes[kStages];  // groups that come as boxes; -1: no more blocks
   float xch[2][2][kMaxR];
 };
 
@@ -179,73 +186,27 @@ __device__ __forceinline__ long long range_start(long long total, int g, int NG)
 
 template <int R>
 constexpr size_t lat_smem() {
-  return (size_t)R * kW * 2 + kStages * kStage + R * 128 + 1024;
+  return (size_t)R * kW * 2 + kStages * kStage + R * 128;
 }
 
 template <int R>
 __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_constant__ LatArgs a) {
   extern __shared__ __align__(1024) unsigned char lat_raw[];
   __shared__ LatBars sb;
-  unsigned char* smem = lat_raw + ((1024u - (smem_u32(lat_raw) & 1023u)) & 1023u);
-  unsigned char* sQ = smem;                  // [9][R][128 B]
+  unsigned char* sQ = lat_raw;               // [9][R][128 B]
   unsigned char* sP = sQ + R * kW * 2;       // [R][128 B]
   unsigned char* sX = sP + R * 128;          // stages
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   volatile int* abort_flag = &sb.abort;
   const int cta = blockIdx.x, g = cta / a.Gs, t = cta % a.Gs;
 
-  griddep_wait();
-  griddep_launch_dependents();
-
-  // ---- invalid requests: error word, rows of zeros -------------------------
-  for (int b = cta; b < a.B; b += gridDim.x) {
-    if (request(a, b).ql) continue;
-    if (tid == 0) set_error(a.err, KVP_ERR_BAD_INDEX);
-    uint4* o = reinterpret_cast<uint4*>(a.out + (size_t)b * a.C * a.H * kDc);
-    for (size_t x = tid; x < (size_t)a.C * a.H * (kDc / 8); x += kThreads) o[x] = make_uint4(0u, 0u, 0u, 0u);
-  }
-
-  // ---- this group's range of key blocks ------------------------------------
-  // Pass 0 sums all requests' blocks, pass 1 finds the request the range starts in.
-  auto blocks_of = [&](int b) -> long long {
-    long long n = 0;
-    if (b < a.B) {
-      const LatReq r = request(a, b);
-      const int ng = groups_of<R>(a, r.ql);
-      for (int tg = 0; tg < ng; ++tg) n += item_of<R>(a, r, tg).nblk;
-    }
-    return n;
-  };
-  const long long mine0 = blocks_of(tid);
-  long long total = 0;
-  for (int pass = 0; pass < 2; ++pass) {
-    long long base = 0;
-    const long long want = pass ? range_start(total, g, a.NG < total ? a.NG : (int)total) : 0;
-    for (int c0 = 0; c0 < a.B; c0 += kThreads) {
-      const long long n = c0 ? blocks_of(c0 + tid) : mine0;
-      long long sum;
-      const long long before = base + block_exclusive_scan(n, &sum);
-      if (pass && want >= before && want < before + n) {
-        sb.b0 = c0 + tid;
-        sb.off0 = want - before;
-      }
-      base += sum;
-    }
-    total = base;
-  }
-  // no more groups than blocks: the groups in use are the first ones, none of them empty
-  const int ng_used = a.NG < total ? a.NG : (int)total;
-  const long long r0 = range_start(total, g, ng_used), r1 = range_start(total, g + 1, ng_used);
-  if (g >= ng_used) {
-    if (tid == 0) a.merge[cta] = make_int4(-1, 0, 0, 0);
-    return;
-  }
-
+  // before the wait for the stream's previous kernel: nothing here touches global memory
   if (tid == 0) {
     mbar_init(&sb.q_full, 1);
     mbar_init(&sb.q_free, 1);
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&sb.full[s], 1);
+      mbar_init(&sb.job[s], 1);
+      mbar_init(&sb.full[s], 2);
       mbar_init(&sb.empty[s], 1);
     }
     for (int x = 0; x < 2; ++x) {
@@ -261,9 +222,60 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
     fence_mbar_init();
   }
   if (warp == 0) tc5::alloc512(&sb.taddr);
+  griddep_wait();
+  griddep_launch_dependents();
+
+  // ---- invalid requests: error word, rows of zeros -------------------------
+  for (int b = cta; b < a.B; b += gridDim.x) {
+    if (request(a, b).ql) continue;
+    if (tid == 0) set_error(a.err, KVP_ERR_BAD_INDEX);
+    uint4* o = reinterpret_cast<uint4*>(a.out + (size_t)b * a.C * a.H * kDc);
+    for (size_t x = tid; x < (size_t)a.C * a.H * (kDc / 8); x += kThreads) o[x] = make_uint4(0u, 0u, 0u, 0u);
+  }
+
+  // ---- this group's range of key blocks ------------------------------------
+  auto blocks_of = [&](int b) -> long long {
+    long long n = 0;
+    if (b < a.B) {
+      const LatReq r = request(a, b);
+      const int ng = groups_of<R>(a, r.ql);
+      for (int tg = 0; tg < ng; ++tg) n += item_of<R>(a, r, tg).nblk;
+    }
+    return n;
+  };
+  const long long n0 = blocks_of(tid);
+  long long total, before0 = block_exclusive_scan(n0, &total);
+  for (int c0 = kThreads; c0 < a.B; c0 += kThreads) {
+    long long sum;
+    block_exclusive_scan(blocks_of(c0 + tid), &sum);
+    total += sum;
+  }
+  // no more groups than blocks: the groups in use are the first ones, none of them empty
+  const int ng_used = a.NG < total ? a.NG : (int)total;
+  const long long r0 = range_start(total, g, ng_used), r1 = range_start(total, g + 1, ng_used);
+  const bool busy = g < ng_used;
+  // the request the range starts in
+  long long base = 0;
+  for (int c0 = 0; busy && c0 < a.B && base <= r0; c0 += kThreads) {
+    long long n = n0, before = before0, sum = total;
+    if (a.B > kThreads) {
+      n = c0 ? blocks_of(c0 + tid) : n0;
+      before = base + block_exclusive_scan(n, &sum);
+    }
+    if (r0 >= before && r0 < before + n) {
+      sb.b0 = c0 + tid;
+      sb.off0 = r0 - before;
+    }
+    base += sum;
+  }
   tc5::fence_before();
   __syncthreads();
   tc5::fence_after();
+  if (!busy) {
+    if (tid == 0) a.merge[cta] = make_int4(-1, 0, 0, 0);
+    if (warp == 0) tc5::dealloc512(sb.taddr);
+    return;
+  }
   // TMEM: O^T at columns 0 .. 4 R - 1 (block j of 128 entries at j R), S buffers at 256 and 320
   const uint32_t tbase = sb.taddr;
   Pieces<R> pc(a, t, sb.b0, sb.off0, r1 - r0);
@@ -275,6 +287,53 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
     // Eight consecutive positions of a block table whose pages hold a multiple
     // of eight, from a multiple of eight on, lie in one page: one table read.
     const bool paged8 = !a.T.raw && (a.T.page_size & 7) == 0;
+    // Blocks are resolved up to 1 + kAhead before they are loaded. Lane l holds
+    // the slots of keys 2 l and 2 l + 1 (group gi is lanes 4 gi .. 4 gi + 3; -1:
+    // nothing to read) and the mask of groups that are eight consecutive slots.
+    struct Named {
+      int s0, s1;
+      unsigned boxes;
+    } ring[2 + kAhead];
+    int named = 0;
+    Pieces<R> pr = pc;
+    bool more = pr.next();
+    int ri = more ? pr.k0 : 0;
+    auto name_next = [&](Named& w) {
+      const Span u = pr.it.u;
+      const int o0 = ri * kKeys, nk = pr.it.n_keys;
+      w.boxes = 0;
+      if (paged8) {
+        const int og = o0 + 8 * lane;
+        int s = -1;
+        if (lane < 8 && og + 7 < nk && (og >= u.se || og + 7 < u.se)) {
+          const int p = span_pos(u, og);
+          if ((p & 7) == 0) s = resolve_slot(a.T, pr.r.row, p, a.err);
+        }
+        w.boxes = __ballot_sync(0xffffffffu, s >= 0) & 0xFFu;
+        w.s0 = __shfl_sync(0xffffffffu, s, lane >> 2) + 2 * (lane & 3);
+        w.s1 = w.s0 + 1;
+      }
+      if (w.boxes != 0xFFu) {
+        int sl[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int o = o0 + 2 * lane + k;
+          sl[k] = o < nk ? resolve_slot(a.T, pr.r.row, span_pos(u, o), a.err) : -1;
+        }
+        w.s0 = sl[0];
+        w.s1 = sl[1];
+        const int g0 = __shfl_sync(0xffffffffu, sl[0], lane & ~3);
+        const unsigned run = __ballot_sync(0xffffffffu, sl[0] >= 0 && sl[1] == sl[0] + 1 && sl[0] == g0 + 2 * (lane & 3));
+        w.boxes = 0;
+#pragma unroll
+        for (int gi = 0; gi < 8; ++gi)
+          if (((run >> (4 * gi)) & 0xFu) == 0xFu) w.boxes |= 1u << gi;
+      }
+      if (++ri == pr.k1) {
+        more = pr.next();
+        ri = more ? pr.k0 : 0;
+      }
+    };
     while (ok && pc.next()) {
       if (np > 0) ok = __all_sync(0xffffffffu, lwait(&sb.q_free, np - 1, abort_flag, a.err));
       if (!ok) break;
@@ -286,62 +345,42 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
       __syncwarp();
       for (int i = pc.k0; i < pc.k1; ++i, ++n) {
         const int st = n % kStages;
-        const Span u = pc.it.u;
-        const int o0 = i * kKeys;
-        unsigned boxes = 0;  // groups that are eight consecutive slots
-        int s0 = -1;         // lane gi < 8: group gi's first slot
-        bool fast = false;
-        if (paged8) {
-          const int og = o0 + 8 * lane;
-          if (lane < 8 && og + 7 < pc.it.n_keys && (og >= u.se || og + 7 < u.se)) {
-            const int p = span_pos(u, og);
-            if ((p & 7) == 0) s0 = resolve_slot(a.T, pc.r.row, p, a.err);
-          }
-          boxes = __ballot_sync(0xffffffffu, s0 >= 0) & 0xFFu;
-          fast = boxes == 0xFFu;
+        if (named == n) {  // the first block; later ones are named in the loop below
+          name_next(ring[0]);
+          ++named;
         }
-        if (!fast) {
-          // lane l resolves keys 2 l and 2 l + 1; group gi is lanes 4 gi .. 4 gi + 3
-          int sl[2];
+        const Named w = ring[0];
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int o = o0 + 2 * lane + k;
-            sl[k] = o < pc.it.n_keys ? resolve_slot(a.T, pc.r.row, span_pos(u, o), a.err) : -1;
-          }
-          __syncwarp();  // this warp's previous copies have read the slot list
-          sb.slots[2 * lane] = sl[0];
-          sb.slots[2 * lane + 1] = sl[1];
-          const int g0 = __shfl_sync(0xffffffffu, sl[0], lane & ~3);
-          const unsigned run = __ballot_sync(0xffffffffu, sl[0] >= 0 && sl[1] == sl[0] + 1 && sl[0] == g0 + 2 * (lane & 3));
-          boxes = 0;
-#pragma unroll
-          for (int gi = 0; gi < 8; ++gi)
-            if (((run >> (4 * gi)) & 0xFu) == 0xFu) boxes |= 1u << gi;
-          __syncwarp();
-          if (lane < 8) s0 = sb.slots[8 * lane];
-        }
+        for (int x = 0; x < 1 + kAhead; ++x) ring[x] = ring[x + 1];
         if (n >= kStages) ok = __all_sync(0xffffffffu, lwait(&sb.empty[st], n / kStages - 1, abort_flag, a.err));
         if (!ok) break;
-        unsigned char* dst = sX + st * kStage;
-        if (lane == 0) mbar_arrive_expect_tx(&sb.full[st], kStage);
-        __syncwarp();
-        if (lane < 8 && ((boxes >> lane) & 1)) tma_load_4d(dst + lane * kGroup, &a.box, 0, s0, 0, a.layer, &sb.full[st]);
-        if (boxes != 0xFFu) {
-          // rows of the other groups: (group, half of four rows, chunk) per copy
-          for (int x = lane; x < 8 * 2 * kChunks; x += 32) {
-            const int gi = x / (2 * kChunks), y = x % (2 * kChunks), hf = y / kChunks, c = y % kChunks;
-            if ((boxes >> gi) & 1) continue;
-            int rr[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int s = sb.slots[8 * gi + 4 * hf + k];
-              rr[k] = s < 0 ? a.zero_row : a.row0 + s;
-            }
-            tc5::tma_gather4(dst + gi * kGroup + c * 1024 + hf * 512, &a.gat, 64 * c, rr[0], rr[1], rr[2], rr[3],
-                             &sb.full[st]);
-          }
+        const int s8 = __shfl_sync(0xffffffffu, w.s0, (4 * lane) & 31);  // lane gi < 8: group gi's first slot
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&sb.full[st], (uint32_t)__popc(w.boxes) * kGroup);
+          if (w.boxes == 0xFFu) mbar_arrive(&sb.full[st]);  // nothing for the copier
         }
         __syncwarp();
+        if (lane < 8 && ((w.boxes >> lane) & 1))
+          tma_load_4d(sX + st * kStage + lane * kGroup, &a.box, 0, s8, 0, a.layer, &sb.full[st]);
+        sb.slots[st][2 * lane] = w.s0;
+        sb.slots[st][2 * lane + 1] = w.s1;
+        if (lane == 0) sb.boxes[st] = (int)w.boxes;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sb.job[st]);
+        // name the blocks ahead: the next one only while the first is on its way
+        while (more && named < n + 2 + (n ? kAhead : 0)) {
+          Named v;
+          name_next(v);
+#pragma unroll
+          for (int x = 0; x < 1 + kAhead; ++x)
+            if (x == named - n - 1) ring[x] = v;
+          // one CTA of a group prefetches the boxes (scattered rows gained nothing: 2.8 us a block without, 3.1 with)
+          if (named >= kStages && t == 0 && v.boxes == 0xFFu) {
+            const int p8 = __shfl_sync(0xffffffffu, v.s0, (4 * lane) & 31);
+            if (lane < 8) tc5::tma_prefetch_4d(&a.box, 0, p8, 0, a.layer);
+          }
+          ++named;
+        }
       }
     }
     // what was issued has landed (bounded) before the shared memory goes away
@@ -350,6 +389,55 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
       const int cnt = (n + kStages - 1 - s) / kStages;
       if (cnt > 0) lwait(&sb.full[s], cnt - 1, &sb.late, a.err);
     }
+    __syncwarp();
+    if (lane < kStages) {  // the copiers have read their last slots
+      sb.boxes[lane] = -1;
+      mbar_arrive(&sb.job[lane]);
+    }
+    __syncwarp();
+  } else if (warp == 3) {
+    // ======================= copier of scattered rows ==========================
+    // A block's copies are one group. The block before is handed on once its
+    // copies are in: before waiting for the next job, or, when that is there
+    // already, after issuing its copies. Blocks of boxes alone need nothing.
+    int before = -1;  // the stage whose copies are on their way
+    for (int k = 0;; ++k) {
+      const int st = k % kStages;
+      if (before >= 0 && !__all_sync(0xffffffffu, mbar_test_wait(&sb.job[st], (uint32_t)(k / kStages) & 1))) {
+        cp_async_wait<0>();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sb.full[before]);
+        before = -1;
+      }
+      if (!__all_sync(0xffffffffu, lwait(&sb.job[st], k / kStages, abort_flag, a.err))) break;
+      const int boxes = *(volatile int*)&sb.boxes[st];
+      const bool copy = boxes >= 0 && boxes != 0xFF;
+      if (copy) {
+        // a copy is 4 rows x 128 bytes a warp: lane = 8 row + 16-byte piece
+        const int piece = lane & 7;
+        for (int h = 0; h < 16; ++h) {
+          if ((boxes >> (h >> 1)) & 1) continue;
+          const int key = 4 * h + (lane >> 3), r = key & 7;
+          const int s = *(volatile int*)&sb.slots[st][key];
+          const char* src = a.rows + (size_t)max(s, 0) * (kW * 2) + piece * 16;
+          const uint32_t dst = smem_u32(sX) + st * kStage + (uint32_t)(key >> 3) * kGroup + r * 128 + ((piece ^ r) << 4);
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c) tc5::cp_async16(dst + c * 1024, src + c * 128, s < 0 ? 0 : 16);
+        }
+        cp_async_commit();
+      }
+      if (before >= 0) {
+        if (copy) cp_async_wait<1>();
+        else cp_async_wait<0>();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sb.full[before]);
+      }
+      before = copy ? st : -1;
+      if (boxes < 0) break;
+    }
+    cp_async_wait<0>();
     __syncwarp();
   } else if (warp == 1) {
     // ======================= S issuer =========================================
@@ -413,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
     }
     if (tc5::elect_one()) tc5::commit(&sb.drain);
     __syncwarp();
-  } else if (warp >= kSoft0) {
+  } else {
     // ======================= softmax ==========================================
     // Thread (quadrant, lane < 16, part): query row 16 quadrant + lane, keys
     // 32 part .. 32 part + 31 of each block. The running maxima of rows lane and
@@ -565,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
           const long long e = r1 - pc.left - (pc.k1 - pc.k0) + pc.it.nblk;
           int gl = g;
           while (range_start(total, gl + 1, ng_used) < e) ++gl;
-          merge = make_int4(pc.b, pc.tile, gl, slot);
+          merge = make_int4(pc.b * a.C * a.H + pc.tile * R, rows, gl, slot);
         }
       }
       __nv_bfloat16* orow = a.out + ((size_t)pc.b * a.C * a.H + (size_t)pc.tile * R) * kDc;
@@ -617,37 +705,118 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
   if (warp == 0) tc5::dealloc512(tbase);
 }
 
-// Joins the partials of the items that a range boundary cut: block (x, y) takes
-// rows 4 y .. 4 y + 3 of the item that CTA x started and did not finish.
-template <int R>
-__global__ void __launch_bounds__(kDc / 4) latent_combine_kernel(const LatArgs a) {
+// Joins the partials of the items that a range boundary cut. Block (x, y) takes
+// the x-th cut item of the records. With SPLIT (few items, many pieces each) it
+// takes row y, its eight warps every eighth piece, joined through shared
+// memory; else rows 8 y .. 8 y + 7, a warp each. A lane holds 16 of a row's 512
+// entries.
+constexpr int kCombWarps = 8;
+template <int R, bool SPLIT>
+__global__ void __launch_bounds__(32 * kCombWarps) latent_combine_kernel(const LatArgs a) {
+  __shared__ int counts[kCombWarps];
+  __shared__ int4 rec;
+  __shared__ int rec_cta;
+  __shared__ float sm[SPLIT ? kCombWarps : 1], sl[SPLIT ? kCombWarps : 1];
+  __shared__ float4 so[SPLIT ? kCombWarps : 1][SPLIT ? kDc / 4 : 1];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   griddep_wait();
-  const int cta = blockIdx.x, t = cta % a.Gs, g = cta / a.Gs;
-  const int4 mg = a.merge[cta];
-  if (mg.x < 0) return;
-  const int rows = request(a, mg.x).ql * a.H - mg.y * R;
-  const int n = mg.z - g + 1;
-  for (int r = 4 * blockIdx.y; r < min(4 * (int)blockIdx.y + 4, min(R, rows)); ++r) {
-    auto at = [&](int k) { return (size_t)(2 * ((g + k) * a.Gs + t) + (k ? 0 : mg.w)) * R + r; };
-    float m = -INFINITY;
-    for (int k = 0; k < n; ++k) m = fmaxf(m, a.part_ml[at(k)].x);
-    float l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int k = 0; k < n; ++k) {
-      const float2 ml = a.part_ml[at(k)];
-      const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - m);
-      const float4 x = reinterpret_cast<const float4*>(a.part_o + at(k) * kDc)[threadIdx.x];
-      l = fmaf(f, ml.y, l);
-      o.x = fmaf(f, x.x, o.x);
-      o.y = fmaf(f, x.y, o.y);
-      o.z = fmaf(f, x.z, o.z);
-      o.w = fmaf(f, x.w, o.w);
+  const int ctas = a.NG * a.Gs;
+  int seen = 0;
+  if (tid == 0) rec_cta = -1;
+  for (int c0 = 0; c0 < ctas; c0 += 32 * kCombWarps) {
+    const int c = c0 + tid;
+    const int4 mg = c < ctas ? a.merge[c] : make_int4(-1, 0, 0, 0);
+    const unsigned has = __ballot_sync(0xffffffffu, mg.x >= 0);
+    __syncthreads();
+    if (lane == 0) counts[warp] = __popc(has);
+    __syncthreads();
+    int before = seen;
+    for (int w = 0; w < kCombWarps; ++w) {
+      if (w < warp) before += counts[w];
+      seen += counts[w];
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    __nv_bfloat16* out = a.out + ((size_t)mg.x * a.C * a.H + (size_t)mg.y * R + r) * kDc + 4 * threadIdx.x;
-    *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+    if (mg.x >= 0 && before + __popc(has & ((1u << lane) - 1)) == (int)blockIdx.x) {
+      rec = mg;
+      rec_cta = c;
+    }
   }
+  __syncthreads();
+  if (rec_cta < 0) return;
+  const int4 mg = rec;  // {first output row, rows, last group, slot of the first piece}
+  const int t = rec_cta % a.Gs, g = rec_cta / a.Gs, n = mg.z - g + 1;
+  const int r = SPLIT ? (int)blockIdx.y : kCombWarps * (int)blockIdx.y + warp;
+  if (r >= mg.y) return;  // SPLIT: the whole block
+  auto at = [&](int k) { return (size_t)(2 * ((g + k) * a.Gs + t) + (k ? 0 : mg.w)) * R + r; };
+  float m = -INFINITY, l = 0.f;
+  float4 o[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) o[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int step = SPLIT ? kCombWarps : 1;
+  const int mine = SPLIT ? (n - warp + kCombWarps - 1) / kCombWarps : n;  // pieces of this warp: first + step i
+  const int first = SPLIT ? warp : 0;
+  for (int k0 = 0; k0 < mine; k0 += 32) {
+    // 32 pieces' maxima and sums at once, then their entries
+    const float2 ml = k0 + lane < mine ? a.part_ml[at(first + step * (k0 + lane))] : make_float2(-INFINITY, 0.f);
+    float mx = ml.x;
+#pragma unroll
+    for (int sh = 16; sh > 0; sh >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
+    const float mn = fmaxf(m, mx);
+    const float old = m == -INFINITY ? 0.f : exp2f(m - mn);
+    const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - mn);
+    m = mn;
+    l *= old;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) o[q].x *= old, o[q].y *= old, o[q].z *= old, o[q].w *= old;
+    float ls = f * ml.y;
+#pragma unroll
+    for (int sh = 16; sh > 0; sh >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, sh);
+    l += ls;
+    const int nk = min(32, mine - k0);
+#pragma unroll 2
+    for (int k = 0; k < nk; ++k) {
+      const float fk = __shfl_sync(0xffffffffu, f, k);
+      const float4* x = reinterpret_cast<const float4*>(a.part_o + at(first + step * (k0 + k)) * kDc) + lane;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float4 v = x[32 * q];
+        o[q].x = fmaf(fk, v.x, o[q].x);
+        o[q].y = fmaf(fk, v.y, o[q].y);
+        o[q].z = fmaf(fk, v.z, o[q].z);
+        o[q].w = fmaf(fk, v.w, o[q].w);
+      }
+    }
+  }
+  __nv_bfloat16* out = a.out + ((size_t)mg.x + r) * kDc;
+  if (!SPLIT) {
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      reinterpret_cast<uint2*>(out)[lane + 32 * q] =
+          make_uint2(pack_bf16(o[q].x * inv, o[q].y * inv), pack_bf16(o[q].z * inv, o[q].w * inv));
+    return;
+  }
+  if (lane == 0) sm[warp] = m, sl[warp] = l;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) so[warp][lane + 32 * q] = o[q];
+  __syncthreads();
+  if (tid >= kDc / 4) return;
+  float mx = sm[0];
+#pragma unroll
+  for (int w = 1; w < kCombWarps; ++w) mx = fmaxf(mx, sm[w]);
+  float tot = 0.f;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int w = 0; w < kCombWarps; ++w) {
+    const float f = sm[w] == -INFINITY ? 0.f : exp2f(sm[w] - mx);
+    const float4 v = so[w][tid];
+    tot = fmaf(f, sl[w], tot);
+    s.x = fmaf(f, v.x, s.x);
+    s.y = fmaf(f, v.y, s.y);
+    s.z = fmaf(f, v.z, s.z);
+    s.w = fmaf(f, v.w, s.w);
+  }
+  const float inv = tot == 0.f ? 0.f : 1.f / tot;
+  reinterpret_cast<uint2*>(out)[tid] = make_uint2(pack_bf16(s.x * inv, s.y * inv), pack_bf16(s.z * inv, s.w * inv));
 }
 
 struct LatShape {
@@ -709,52 +878,53 @@ cudaError_t launch_lat(const LatArgs& a, int ctas, cudaStream_t stream) {
   c.numAttrs = 1;
   e = cudaLaunchKernelEx(&c, latent_tc_kernel<R>, a);
   if (e != cudaSuccess) return e;
-  c.gridDim = dim3((unsigned)ctas, R / 4);
-  c.blockDim = dim3(kDc / 4);
+  // at most one cut item per boundary between ranges and per tile of a group, and no more than there are items
+  const long long items = (long long)a.B * (((long long)a.C * a.H + (long long)a.Gs * R - 1) / ((long long)a.Gs * R));
+  const unsigned cut = (unsigned)((items < a.NG ? items : a.NG) * a.Gs);
+  c.blockDim = dim3(32 * kCombWarps);
   c.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&c, latent_combine_kernel<R>, a);
+  if (items * 8 <= a.NG) {  // about eight pieces an item or more: a block per row
+    c.gridDim = dim3(cut, R);
+    return cudaLaunchKernelEx(&c, latent_combine_kernel<R, true>, a);
+  }
+  c.gridDim = dim3(cut, R / kCombWarps);
+  return cudaLaunchKernelEx(&c, latent_combine_kernel<R, false>, a);
 }
 
 }  // namespace
 
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-  void* fn = nullptr;
-  cudaDriverEntryPointQueryResult qr;
-  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &qr) != cudaSuccess ||
-      qr != cudaDriverEntryPointSuccess)
-    return nullptr;
-  return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult qr;
+    const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &qr) ==
+                        cudaSuccess &&
+                    qr == cudaDriverEntryPointSuccess;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ok ? fn : nullptr);
+  }();
+  return encode;
 }
 
-// The pool's two maps (see common.cuh), for the shapes the kernel takes.
-void latent_encode_maps(kvp_pool* pool) {
-  pool->lat_maps = 0;
+// The pool's map (see common.cuh), for the shapes the kernel takes.
+void latent_encode_map(kvp_pool* pool) {
+  pool->lat_map_ok = 0;
   if (pool->dtype != KVP_BF16 || pool->latent_dim != kDc || pool->head_dim != kW) return;
-  const long long rows = (long long)pool->num_layers * pool->num_slots;
-  if (rows >= 0x7fffffffLL) return;
   const auto encode = tensor_map_encoder();
   if (!encode) return;
   const cuuint32_t one[4] = {1, 1, 1, 1};
   const cuuint64_t bd[4] = {64, (cuuint64_t)pool->num_slots, kChunks, (cuuint64_t)pool->num_layers};
   const cuuint64_t bs[3] = {kW * 2, 128, (cuuint64_t)pool->layer_bytes};
   const cuuint32_t bb[4] = {64, 8, kChunks, 1};
-  const cuuint64_t gd[2] = {kW, (cuuint64_t)rows};
-  const cuuint64_t gs[1] = {kW * 2};
-  const cuuint32_t gb[2] = {64, 1};
   if (encode(&pool->lat_box, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, pool->buf, bd, bs, bb, one,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return;
-  if (encode(&pool->lat_gather, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, pool->buf, gd, gs, gb, one,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-    return;
-  pool->lat_maps = 1;
+  pool->lat_map_ok = 1;
 }
 
 bool latent_tc_eligible(const kvp_pool* pool, int C, int H) {
   // row indices of a request stay in int
-  return pool->lat_maps == 1 && (long long)C * H <= 0x3fffffffLL;
+  return pool->lat_map_ok == 1 && (long long)C * H <= 0x3fffffffLL;
 }
 
 size_t latent_tc_workspace(const kvp_pool* pool, int C, int H) { return lat_ws(lat_shape(pool, C, H)).total; }
@@ -774,11 +944,9 @@ int launch_latent_tc(const LatentCall& c, cudaStream_t stream) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return KVP_ERR_CUDA;
   a.box = c.pool->lat_box;
-  a.gat = c.pool->lat_gather;
   a.T = c.T;
   a.layer = c.layer;
-  a.row0 = c.layer * c.pool->num_slots;
-  a.zero_row = c.pool->num_layers * c.pool->num_slots;
+  a.rows = c.pool->buf + (size_t)c.layer * c.pool->layer_bytes;
   a.out = static_cast<__nv_bfloat16*>(c.out);
   a.context_lens = c.context_lens;
   a.table_rows = c.table_rows;

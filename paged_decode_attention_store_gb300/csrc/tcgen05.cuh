@@ -19,6 +19,21 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// Whether the phase with the given parity is complete, without waiting.
+}  // namespace tc5
+__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+namespace tc5 {
+
 // Shared-memory matrix descriptor, 128-byte swizzle (8-row atoms of 1 KB).
 // K-major: ``sbo`` bytes between 8-row groups, ``lbo`` unused. MN-major: ``lbo``
 // bytes between blocks of 64 MN entries, ``sbo`` between groups of 8 K rows.
@@ -103,14 +118,15 @@ __device__ __forceinline__ void tma_3d(void* dst, const void* tmap, int c0, int 
       : "memory");
 }
 
-// Four rows r0..r3 of 64 entries from column c0 of a 2-D map whose box is one row high.
-__device__ __forceinline__ void tma_gather4(void* dst, const void* tmap, int c0, int r0, int r1, int r2, int r3,
-                                            uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
-      "%4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
-      "l"(tmap), "r"(c0), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(smem_u32(bar))
-      : "memory");
+// Prefetch of a box of a 4-D map to L2.
+__device__ __forceinline__ void tma_prefetch_4d(const void* tmap, int c0, int c1, int c2, int c3) {
+  asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(tmap), "r"(c0), "r"(c1),
+               "r"(c2), "r"(c3)
+               : "memory");
+}
+// 16-byte asynchronous copy global -> shared past L1; ``size`` 0 writes zeros and reads nothing.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int size) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(size) : "memory");
 }
 
 // (d0, d1) = (a0, a1) * (b, b) + (c, c) and (d0, d1) += (a0, a1): packed fp32.

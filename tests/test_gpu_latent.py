@@ -256,7 +256,7 @@ def test_refusals(kb):
         assert e.value.code == kb.KVP_ERR_INVALID_ARG
     kv = kb.Pool(torch.zeros((2, 1, 4, 16, 1, 576), dtype=torch.bfloat16, device=DEV), 16, kb.KVP_BF16)
     with pytest.raises(AttributeError):
-        call(pool=kv)
+        call(pool=kv)  # a K/V pool has no latent_dim
     torch.cuda.synchronize()
     assert bool((c.out == 5.0).all()) and kb.kvp_sync_error(c.pool) == 0
 
