@@ -156,6 +156,7 @@ extern "C" int latent_prefill_attention(const void* q, long long q_stride, long 
   a.scale = scale;
   a.err = error_word;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (expanded_tc_eligible(a, dtype)) return launch_expanded_tc(a, st);
   const long long blocks = (long long)batch * max_q;
   if (blocks > 0x7fffffffLL / num_heads) return KVP_ERR_INVALID_ARG;
   const unsigned grid = (unsigned)(blocks * num_heads);

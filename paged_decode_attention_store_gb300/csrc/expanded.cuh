@@ -41,4 +41,8 @@ __device__ __forceinline__ ExpandedRequest expanded_request(const ExpandedCall& 
   return r;
 }
 
+// The tcgen05 kernel (expanded_tc.cu): whether it takes a call, and its launch.
+bool expanded_tc_eligible(const ExpandedCall& c, int dtype);
+int launch_expanded_tc(const ExpandedCall& c, cudaStream_t stream);
+
 }  // namespace kvp

@@ -1,0 +1,532 @@
+// Causal attention of ragged prompts in expanded form on the fifth-generation
+// tensor cores: bf16, nope_dim 128, rope_dim 64, v_dim 128.
+//
+// Mathematics (expanded.cu): s = scale (<q_nope, k> + <q_rope, r>), o = sum
+// softmax(s) v per head; the rotated part r of a key is one row for all heads, so
+// S = Q K^T over 192 entries takes k from the head's rows and r from the shared
+// ones, as a third 64-entry chunk of the same operand.
+//
+// What bounds it: the tensor cores. A tile is 128 query rows of one (request,
+// head); a block of 128 keys is 12 MMAs (M 128 N 128 K 16, 33 ns each) for S and 8
+// for O, 0.65 us, on 80 KB of K and V that the tiles of the same request and
+// head share through L2.
+//  * TMEM: two S buffers of 128 columns, O (128), two P buffers (64 columns, two
+//    bf16 keys each). S(i + 1) and O += P(i) V(i) run while the softmax works:
+//    four threads a row, 32 keys each, online softmax in log2 units, O rescaled
+//    only when a row's maximum grows by more than 8 (P <= 256).
+//  * Operands by TMA under the 128-byte swizzle: 64-entry chunks of 128 rows (16
+//    KB): Q 3, K 3 a stage (two of k, one of r), V 2 a stage, two stages each.
+//    Rows past the request's last key are another request's: their scores are
+//    masked, their V rows zeroed in shared memory (0 times what they hold must
+//    be 0).
+//  * One CTA an SM keeps running: it takes the next tile off the grid by
+//    cluster launch control (a waiting block's launch is cancelled and its index
+//    taken over), so that the next tile's Q and first K and V load while this
+//    one's last block and epilogue run, and the SMs stay balanced over prompts
+//    of any lengths. Tiles of a request and head are adjacent, the longest first.
+//
+// Warps: 0 takes tiles and loads Q and K, 1 issues S, 2 issues O, 3 loads V, 4..19
+// run the softmax and the epilogue (TMEM lane quadrant = warp % 4).
+#include "expanded.cuh"
+#include "tcgen05.cuh"
+
+namespace kvp {
+
+namespace {
+
+constexpr int kTile = 128, kKeys = 128;
+constexpr int kDn = 128, kDr = 64, kDv = 128;
+constexpr uint32_t kChunk = 16384;  // 128 rows x 128 B
+constexpr int kQChunks = (kDn + kDr) / 64, kVChunks = kDv / 64;
+constexpr int kKS = 2, kVS = 2;
+constexpr int kThreads = 640;
+constexpr int kSoft0 = 4, kSoftWarps = 16, kParts = 4;
+constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr size_t kSmem = (kQChunks + kKS * kQChunks + kVS * kVChunks) * kChunk;
+
+struct ExpArgs {
+  CUtensorMap qmap;   // (d, head, token), box (64, 1, 128); likewise the others
+  CUtensorMap kmap;
+  CUtensorMap pemap;  // (d, token), box (64, 128)
+  CUtensorMap vmap;
+  ExpandedCall c;
+  int tiles;          // of max_q
+  float scale_log2;
+};
+
+struct ExpBars {
+  uint64_t q_full, q_free;
+  uint64_t k_full[kKS], k_empty[kKS];
+  uint64_t v_full[kVS], v_empty[kVS];
+  uint64_t s_full[2], s_free[2], p_full[2], pv_done[2];
+  uint64_t o_free, drain, vtail;
+  uint64_t xbar[4];
+  uint64_t next_full[2], next_free[2];
+  uint32_t taddr;
+  int abort, late;
+  alignas(16) uint32_t next[2][4];  // cluster launch control's answers
+  float xch[2][kParts][kTile];
+};
+
+__device__ __forceinline__ bool ewait(uint64_t* bar, int k, volatile int* abort_flag, int32_t* err) {
+  return mbar_wait_bounded(bar, (uint32_t)(k & 1), abort_flag, err, kWaitNs);
+}
+
+__device__ __forceinline__ void tma_2d(void* dst, const void* tmap, int c0, int c1, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          smem_u32(dst)),
+      "l"(tmap), "r"(c0), "r"(c1), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// Ask for the index of a block that has not started; 16 bytes into ``dst``, counted on ``bar``.
+__device__ __forceinline__ void take_next(uint32_t* dst, uint64_t* bar) {
+  mbar_arrive_expect_tx(bar, 16);
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                   smem_u32(dst)),
+               "r"(smem_u32(bar))
+               : "memory");
+}
+// The index taken, or -1 when no block was waiting.
+__device__ __forceinline__ long long taken(const uint32_t* src) {
+  uint32_t ok, x;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\tld.shared.b128 r, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\tselp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, _, _, _}, r;\n\t}"
+      : "=r"(ok), "=r"(x)
+      : "r"(smem_u32(src))
+      : "memory");
+  return ok ? (long long)x : -1;
+}
+
+struct Tile {
+  int h, j0, jn;      // head, first query row of the request, query rows in the tile (0: nothing)
+  int q0, k0, kl;     // the request's first rows, its keys
+  int shift;          // query j sits at position shift + j
+  int nblk;
+};
+__device__ __forceinline__ Tile tile_of(const ExpArgs& a, long long idx) {
+  Tile t;
+  const long long bh = idx / a.tiles;
+  const int tile = a.tiles - 1 - (int)(idx - bh * a.tiles);
+  const int b = (int)(bh / a.c.H);
+  t.h = (int)(bh - (long long)b * a.c.H);
+  const ExpandedRequest r = expanded_request(a.c, b);
+  t.j0 = tile * kTile;
+  t.jn = r.ok ? max(0, min(kTile, r.ql - t.j0)) : 0;
+  t.q0 = r.q0;
+  t.k0 = r.k0;
+  t.kl = r.kl;
+  t.shift = r.kl - r.ql;
+  t.nblk = t.jn ? (t.shift + t.j0 + t.jn + kKeys - 1) / kKeys : 0;
+  if (!r.ok && t.h == 0 && tile == 0 && threadIdx.x == 0) set_error(a.c.err, KVP_ERR_BAD_INDEX);
+  return t;
+}
+
+__global__ void __launch_bounds__(kThreads, 1) expanded_tc_kernel(const __grid_constant__ ExpArgs a) {
+  extern __shared__ __align__(1024) unsigned char exp_raw[];
+  __shared__ ExpBars sb;
+  unsigned char* sQ = exp_raw;
+  unsigned char* sK = sQ + kQChunks * kChunk;
+  unsigned char* sV = sK + kKS * kQChunks * kChunk;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  volatile int* abort_flag = &sb.abort;
+  int32_t* err = a.c.err;
+
+  if (tid == 0) {
+    mbar_init(&sb.q_full, 1);
+    mbar_init(&sb.q_free, 1);
+    for (int s = 0; s < kKS; ++s) {
+      mbar_init(&sb.k_full[s], 1);
+      mbar_init(&sb.k_empty[s], 1);
+    }
+    for (int s = 0; s < kVS; ++s) {
+      mbar_init(&sb.v_full[s], 1);
+      mbar_init(&sb.v_empty[s], 1);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&sb.s_full[x], 1);
+      mbar_init(&sb.s_free[x], kSoftWarps);
+      mbar_init(&sb.p_full[x], kSoftWarps);
+      mbar_init(&sb.pv_done[x], 1);
+      mbar_init(&sb.next_full[x], 1);
+      mbar_init(&sb.next_free[x], 3 + kSoftWarps);
+    }
+    for (int q = 0; q < 4; ++q) mbar_init(&sb.xbar[q], kParts);
+    mbar_init(&sb.o_free, kSoftWarps);
+    mbar_init(&sb.drain, 2);
+    mbar_init(&sb.vtail, 1);
+    sb.abort = sb.late = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0) tc5::alloc512(&sb.taddr);
+  tc5::fence_before();
+  __syncthreads();
+  tc5::fence_after();
+  // TMEM: S buffers at columns 0 and 128, O at 256, P buffers at 384 and 448
+  const uint32_t tbase = sb.taddr;
+  const uint32_t tO = tbase + 256u;
+
+  // The index of this CTA's k-th tile (every role asks in order; the answer to
+  // the k-th request is in slot (k - 1) % 2); -1: none, or a wait gave up.
+  auto tile_index = [&](int k) -> long long {
+    if (k == 0) return (long long)blockIdx.x;
+    const int s = (k - 1) & 1;
+    if (!__all_sync(0xffffffffu, ewait(&sb.next_full[s], (k - 1) >> 1, abort_flag, err))) return -1;
+    const long long x = taken(sb.next[s]);
+    fence_proxy_async_smem();  // the slot's next answer comes through the async proxy
+    __syncwarp();
+    if (warp != 0 && lane == 0) mbar_arrive(&sb.next_free[s]);
+    return x;
+  };
+
+  if (warp == 0) {
+    // ======================= tiles, Q and K ===================================
+    int n = 0, nq = 0, asked = 0;
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      const long long idx = tile_index(k);
+      if (idx < 0) break;
+      // ask for the next one: slot k % 2, whose previous answer (tile k - 1's) every role has read
+      if (k >= 2) ok = __all_sync(0xffffffffu, ewait(&sb.next_free[k & 1], (k >> 1) - 1, abort_flag, err));
+      if (!ok) break;
+      if (lane == 0) take_next(sb.next[k & 1], &sb.next_full[k & 1]);
+      ++asked;
+      __syncwarp();
+      const Tile t = tile_of(a, idx);
+      if (!t.nblk) continue;
+      if (nq > 0) ok = __all_sync(0xffffffffu, ewait(&sb.q_free, nq - 1, abort_flag, err));
+      if (!ok) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&sb.q_full, kQChunks * kChunk);
+        for (int c = 0; c < kQChunks; ++c) tc5::tma_3d(sQ + c * kChunk, &a.qmap, 64 * c, t.h, t.q0 + t.j0, &sb.q_full);
+      }
+      ++nq;
+      __syncwarp();
+      for (int i = 0; i < t.nblk; ++i, ++n) {
+        const int st = n % kKS;
+        if (n >= kKS) ok = __all_sync(0xffffffffu, ewait(&sb.k_empty[st], n / kKS - 1, abort_flag, err));
+        if (!ok) break;
+        if (lane == 0) {
+          unsigned char* dst = sK + st * kQChunks * kChunk;
+          mbar_arrive_expect_tx(&sb.k_full[st], kQChunks * kChunk);
+          tc5::tma_3d(dst, &a.kmap, 0, t.h, t.k0 + i * kKeys, &sb.k_full[st]);
+          tc5::tma_3d(dst + kChunk, &a.kmap, 64, t.h, t.k0 + i * kKeys, &sb.k_full[st]);
+          tma_2d(dst + 2 * kChunk, &a.pemap, 0, t.k0 + i * kKeys, &sb.k_full[st]);
+        }
+        __syncwarp();
+      }
+    }
+    // what was issued has landed (bounded) before the shared memory goes away
+    if (nq > 0) ewait(&sb.q_full, nq - 1, &sb.late, err);
+    for (int s = 0; s < kKS; ++s) {
+      const int cnt = (n + kKS - 1 - s) / kKS;
+      if (cnt > 0) ewait(&sb.k_full[s], cnt - 1, &sb.late, err);
+    }
+    for (int s = 0; s < 2; ++s) {
+      const int cnt = (asked + 1 - s) / 2;
+      if (cnt > 0) ewait(&sb.next_full[s], cnt - 1, &sb.late, err);
+    }
+    __syncwarp();
+  } else if (warp == 3) {
+    // ======================= V ================================================
+    int n = 0, ntail = 0;
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      const long long idx = tile_index(k);
+      if (idx < 0) break;
+      const Tile t = tile_of(a, idx);
+      for (int i = 0; i < t.nblk; ++i, ++n) {
+        const int st = n % kVS;
+        if (n >= kVS) ok = __all_sync(0xffffffffu, ewait(&sb.v_empty[st], n / kVS - 1, abort_flag, err));
+        if (!ok) break;
+        unsigned char* dst = sV + st * kVChunks * kChunk;
+        const int rows = t.kl - i * kKeys;  // of this request
+        uint64_t* bar = rows < kKeys ? &sb.vtail : &sb.v_full[st];
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar, kVChunks * kChunk);
+          for (int c = 0; c < kVChunks; ++c) tc5::tma_3d(dst + c * kChunk, &a.vmap, 64 * c, t.h, t.k0 + i * kKeys, bar);
+        }
+        __syncwarp();
+        if (rows < kKeys) {
+          ok = __all_sync(0xffffffffu, ewait(&sb.vtail, ntail, abort_flag, err));
+          ++ntail;
+          if (!ok) break;
+          for (int x = rows * 8 + lane; x < kKeys * 8; x += 32)
+            for (int c = 0; c < kVChunks; ++c)
+              *reinterpret_cast<uint4*>(dst + c * kChunk + x * 16) = make_uint4(0u, 0u, 0u, 0u);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sb.v_full[st]);
+          __syncwarp();
+        }
+      }
+    }
+    if (ntail > 0) ewait(&sb.vtail, ntail - 1, &sb.late, err);
+    for (int s = 0; ok && s < kVS; ++s) {
+      const int cnt = (n + kVS - 1 - s) / kVS;
+      if (cnt > 0) ewait(&sb.v_full[s], cnt - 1, &sb.late, err);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ======================= S issuer =========================================
+    int n = 0, nq = 0;
+    bool ok = true;
+    constexpr uint32_t id = tc5::idesc(kTile, kKeys, 0, 0);
+    const uint64_t dq = tc5::desc(smem_u32(sQ), 16, 1024);
+    for (int k = 0; ok; ++k) {
+      const long long idx = tile_index(k);
+      if (idx < 0) break;
+      const Tile t = tile_of(a, idx);
+      if (!t.nblk) continue;
+      ok = __all_sync(0xffffffffu, ewait(&sb.q_full, nq, abort_flag, err));
+      ++nq;
+      for (int i = 0; ok && i < t.nblk; ++i, ++n) {
+        const int st = n % kKS, buf = n & 1;
+        ok = __all_sync(0xffffffffu, ewait(&sb.k_full[st], n / kKS, abort_flag, err));
+        if (ok && n >= 2) ok = __all_sync(0xffffffffu, ewait(&sb.s_free[buf], (n >> 1) - 1, abort_flag, err));
+        if (!ok) break;
+        tc5::fence_after();
+        const uint64_t dk = tc5::desc(smem_u32(sK) + st * kQChunks * kChunk, 16, 1024);
+        if (tc5::elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < 4 * kQChunks; ++kk) {
+            const uint64_t off = (uint64_t)(((kk >> 2) * kChunk + (kk & 3) * 32) >> 4);
+            tc5::mma_ss(tbase + 128u * (uint32_t)buf, dq + off, dk + off, id, kk > 0);
+          }
+          tc5::commit(&sb.s_full[buf]);
+          tc5::commit(&sb.k_empty[st]);
+          if (i + 1 == t.nblk) tc5::commit(&sb.q_free);
+        }
+        __syncwarp();
+      }
+    }
+    if (tc5::elect_one()) tc5::commit(&sb.drain);
+    __syncwarp();
+  } else if (warp == 2) {
+    // ======================= O issuer =========================================
+    int n = 0, np = 0;
+    bool ok = true;
+    constexpr uint32_t id = tc5::idesc(kTile, kDv, 0, 1);
+    for (int k = 0; ok; ++k) {
+      const long long idx = tile_index(k);
+      if (idx < 0) break;
+      const Tile t = tile_of(a, idx);
+      if (!t.nblk) continue;
+      if (np > 0) ok = __all_sync(0xffffffffu, ewait(&sb.o_free, np - 1, abort_flag, err));
+      ++np;
+      for (int i = 0; ok && i < t.nblk; ++i, ++n) {
+        const int st = n % kVS, buf = n & 1;
+        ok = __all_sync(0xffffffffu, ewait(&sb.v_full[st], n / kVS, abort_flag, err));
+        if (ok) ok = __all_sync(0xffffffffu, ewait(&sb.p_full[buf], n >> 1, abort_flag, err));
+        if (!ok) break;
+        tc5::fence_after();
+        const uint64_t dv = tc5::desc(smem_u32(sV) + st * kVChunks * kChunk, kChunk, 1024);
+        const uint32_t tP = tbase + 384u + 64u * (uint32_t)buf;
+        const bool first = i == 0;
+        if (tc5::elect_one()) {
+#pragma unroll
+          for (int m = 0; m < kKeys / 16; ++m)
+            tc5::mma_ts(tO, tP + (uint32_t)m * 8u, dv + (uint64_t)((m * 2048) >> 4), id, (first && m == 0) ? 0u : 1u);
+          tc5::commit(&sb.pv_done[buf]);
+          tc5::commit(&sb.v_empty[st]);
+        }
+        __syncwarp();
+      }
+    }
+    if (tc5::elect_one()) tc5::commit(&sb.drain);
+    __syncwarp();
+  } else {
+    // ======================= softmax ==========================================
+    const int quad = warp & 3, part = (warp - kSoft0) >> 2;
+    const int row = 32 * quad + lane;
+    const uint32_t lanes = (uint32_t)(32 * quad) << 16;
+    const uint32_t tOp = tO + lanes + 32u * (uint32_t)part;
+    const float sl2 = a.scale_log2;
+    int n = 0, nx = 0;
+    bool ok = true;
+    // the row's four parts: maxima or sums, through shared memory
+    auto exchange = [&](float v, bool use_max, float& res) -> bool {
+      volatile float* xc = &sb.xch[nx & 1][0][0];
+      xc[part * kTile + row] = v;
+      __threadfence_block();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sb.xbar[quad]);
+      const bool done = __all_sync(0xffffffffu, ewait(&sb.xbar[quad], nx, abort_flag, err));
+      ++nx;
+      if (!done) return false;
+      const float v0 = xc[row], v1 = xc[kTile + row], v2 = xc[2 * kTile + row], v3 = xc[3 * kTile + row];
+      res = use_max ? fmaxf(fmaxf(v0, v1), fmaxf(v2, v3)) : (v0 + v1) + (v2 + v3);
+      return true;
+    };
+    for (int k = 0; ok; ++k) {
+      const long long idx = tile_index(k);
+      if (idx < 0) break;
+      const Tile t = tile_of(a, idx);
+      if (!t.nblk) continue;
+      const int p = row < t.jn ? t.shift + t.j0 + row : -1;  // last key the row attends
+      float m = -INFINITY, lsum = 0.f;
+      for (int i = 0; i < t.nblk; ++i, ++n) {
+        const int buf = n & 1;
+        ok = __all_sync(0xffffffffu, ewait(&sb.s_full[buf], n >> 1, abort_flag, err));
+        if (!ok) break;
+        tc5::fence_after();
+        float sv[32];
+        const uint32_t ts = tbase + 128u * (uint32_t)buf + lanes + 32u * (uint32_t)part;
+        tc5::ld16(ts, sv);
+        tc5::ld16(ts + 16, sv + 16);
+        tc5::wait_ld();
+        tc5::fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sb.s_free[buf]);
+        const int we = p - (i * kKeys + 32 * part);  // the last of this thread's keys that the row attends
+        if (!__all_sync(0xffffffffu, we >= 31)) {
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            if (c > we) sv[c] = -INFINITY;
+        }
+        float mt[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          mt[q] = tc5::max3(tc5::max3(sv[8 * q], sv[8 * q + 1], sv[8 * q + 2]),
+                            tc5::max3(sv[8 * q + 3], sv[8 * q + 4], sv[8 * q + 5]), fmaxf(sv[8 * q + 6], sv[8 * q + 7]));
+        float mx;
+        if (!(ok = exchange(fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3])) * sl2, true, mx))) break;  // scale > 0
+        const bool grow = mx > m + 8.f;
+        const float f = grow && m > -INFINITY ? exp2f(m - mx) : 1.f;
+        if (grow) m = mx;
+        const float msub = m == -INFINITY ? 0.f : m;
+        uint32_t w[16];
+        float ps0 = 0.f, ps1 = 0.f;
+#pragma unroll
+        for (int x = 0; x < 16; ++x) {
+          float y0, y1;
+          tc5::fma2(y0, y1, sv[2 * x], sv[2 * x + 1], sl2, -msub);
+          const float p0 = tc5::ex2(y0), p1 = tc5::ex2(y1);
+          w[x] = pack_bf16(p0, p1);
+          tc5::add2(ps0, ps1, p0, p1);
+        }
+        if (n >= 2) {  // P buffer buf is free once O += P V of the block two before is done
+          ok = __all_sync(0xffffffffu, ewait(&sb.pv_done[buf], (n >> 1) - 1, abort_flag, err));
+          if (!ok) break;
+          tc5::fence_after();
+        }
+        tc5::st16(tbase + 384u + 64u * (uint32_t)buf + lanes + 16u * (uint32_t)part, w);
+        lsum = lsum * f + (ps0 + ps1);
+        if (__any_sync(0xffffffffu, f != 1.f)) {  // O holds this tile's blocks before i: scale them once they are in
+          ok = __all_sync(0xffffffffu, ewait(&sb.pv_done[buf ^ 1], (n - 1) >> 1, abort_flag, err));
+          if (!ok) break;
+          tc5::fence_after();
+#pragma unroll
+          for (int x = 0; x < 32; x += 16) {
+            float ov[16];
+            tc5::ld16(tOp + x, ov);
+            tc5::wait_ld();
+#pragma unroll
+            for (int c = 0; c < 16; ++c) ov[c] *= f;
+            tc5::st16(tOp + x, ov);
+          }
+        }
+        tc5::wait_st();
+        tc5::fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sb.p_full[buf]);
+      }
+      if (!ok) break;
+      // ---- epilogue: O / l to the output
+      ok = __all_sync(0xffffffffu, ewait(&sb.pv_done[(n - 1) & 1], (n - 1) >> 1, abort_flag, err));
+      if (!ok) break;
+      float tot;
+      if (!(ok = exchange(lsum, false, tot))) break;
+      tc5::fence_after();
+      float ov[32];
+      tc5::ld16(tOp, ov);
+      tc5::ld16(tOp + 16, ov + 16);
+      tc5::wait_ld();
+      tc5::fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sb.o_free);
+      // a NaN sum is the answer of a NaN score
+      const float inv = tot == 0.f ? 0.f : 1.f / tot;
+      if (row < t.jn) {
+        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.c.out) + ((size_t)(t.q0 + t.j0 + row) * a.c.H + t.h) * kDv + 32 * part;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *reinterpret_cast<uint4*>(o + 8 * q) =
+              make_uint4(pack_bf16(ov[8 * q] * inv, ov[8 * q + 1] * inv), pack_bf16(ov[8 * q + 2] * inv, ov[8 * q + 3] * inv),
+                         pack_bf16(ov[8 * q + 4] * inv, ov[8 * q + 5] * inv),
+                         pack_bf16(ov[8 * q + 6] * inv, ov[8 * q + 7] * inv));
+      }
+    }
+  }
+  // everything issued is done (bounded) before TMEM goes back
+  {
+    const uint64_t t0 = global_timer_ns();
+    while (!mbar_try_wait(&sb.drain, 0u))
+      if (global_timer_ns() - t0 > 2 * kWaitNs) {
+        set_error(err, KVP_ERR_TIMEOUT);
+        break;
+      }
+  }
+  tc5::fence_before();
+  __syncthreads();
+  if (warp == 0) tc5::dealloc512(tbase);
+}
+
+// A map (d, head, token) of a strided bf16 tensor, boxes of 64 entries of 128 tokens of a head.
+bool encode_heads(CUtensorMap* m, const void* p, int width, int heads, int tokens, long long stride, long long head_stride) {
+  const auto encode = tensor_map_encoder();
+  if (!encode) return false;
+  const cuuint64_t d[3] = {(cuuint64_t)width, (cuuint64_t)heads, (cuuint64_t)tokens};
+  const cuuint64_t s[2] = {(cuuint64_t)head_stride * 2, (cuuint64_t)stride * 2};
+  const cuuint32_t b[3] = {64, 1, 128}, one[3] = {1, 1, 1};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), d, s, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// A tensor map's address is a multiple of 16 bytes, its strides are too, positive and below 2^40.
+bool mappable(const void* p, long long stride, long long head_stride) {
+  const long long lim = 1ll << 38;
+  return !(reinterpret_cast<uintptr_t>(p) & 15) && stride > 0 && head_stride > 0 && !(stride & 7) && !(head_stride & 7) &&
+         stride < lim && head_stride < lim;
+}
+
+}  // namespace
+
+bool expanded_tc_eligible(const ExpandedCall& c, int dtype) {
+  return dtype == KVP_BF16 && c.dn == kDn && c.dr == kDr && c.dv == kDv && c.scale > 0.f &&
+         !(reinterpret_cast<uintptr_t>(c.out) & 15) && mappable(c.q, c.q_stride, c.q_head_stride) &&
+         mappable(c.k, c.k_stride, c.k_head_stride) && mappable(c.v, c.v_stride, c.v_head_stride) &&
+         mappable(c.k_pe, c.k_pe_stride, 8) && c.total_k > 0;
+}
+
+int launch_expanded_tc(const ExpandedCall& c, cudaStream_t stream) {
+  ExpArgs a;
+  a.c = c;
+  a.tiles = (c.max_q + kTile - 1) / kTile;
+  a.scale_log2 = c.scale * 1.4426950408889634f;
+  const long long grid = (long long)a.tiles * c.B * c.H;
+  if (grid > 0x7fffffffLL) return KVP_ERR_INVALID_ARG;
+  const auto encode = tensor_map_encoder();
+  if (!encode) return KVP_ERR_CUDA;
+  const cuuint64_t d[2] = {kDr, (cuuint64_t)c.total_k};
+  const cuuint64_t s[1] = {(cuuint64_t)c.k_pe_stride * 2};
+  const cuuint32_t b[2] = {64, 128}, one[2] = {1, 1};
+  if (!encode_heads(&a.qmap, c.q, kDn + kDr, c.H, c.total_q, c.q_stride, c.q_head_stride) ||
+      !encode_heads(&a.kmap, c.k, kDn, c.H, c.total_k, c.k_stride, c.k_head_stride) ||
+      !encode_heads(&a.vmap, c.v, kDv, c.H, c.total_k, c.v_stride, c.v_head_stride) ||
+      encode(&a.pemap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(c.k_pe), d, s, b, one,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return KVP_ERR_CUDA;
+  // set at every call: it belongs to the current context
+  if (cudaFuncSetAttribute(expanded_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem) != cudaSuccess)
+    return KVP_ERR_CUDA;
+  expanded_tc_kernel<<<(unsigned)grid, kThreads, kSmem, stream>>>(a);
+  return cudaGetLastError() == cudaSuccess ? KVP_OK : KVP_ERR_CUDA;
+}
+
+}  // namespace kvp
