@@ -6,10 +6,12 @@
 // S = Q K^T over 192 entries takes k from the head's rows and r from the shared
 // ones, as a third 64-entry chunk of the same operand.
 //
-// What bounds it: the tensor cores. A tile is 128 query rows of one (request,
-// head); a block of 128 keys is 12 MMAs (M 128 N 128 K 16, 33 ns each) for S and 8
-// for O, 0.65 us, on 80 KB of K and V that the tiles of the same request and
-// head share through L2.
+// What bounds it: the tensor cores, and the loads that feed them. A tile is 128
+// query rows of one (request, head); a block of 128 keys is 12 MMAs (M 128 N 128 K
+// 16, 33 ns each) for S and 8 for O, 0.65 us, on 80 KB of K and V. Measured: 1.02 us
+// a block (0.75 us from S to P, and S(i + 2) waits about 1 us for its K once S(i) has
+// freed the stage), 2.5 us a tile besides; 1082 TFLOP/s on 512-token chunks of 16
+// requests with 32 heads.
 //  * TMEM: two S buffers of 128 columns, O (128), two P buffers (64 columns, two
 //    bf16 keys each). S(i + 1) and O += P(i) V(i) run while the softmax works:
 //    four threads a row, 32 keys each, online softmax in log2 units, O rescaled
@@ -21,11 +23,19 @@
 //    be 0).
 //  * One CTA an SM keeps running: it takes the next tile off the grid by
 //    cluster launch control (a waiting block's launch is cancelled and its index
-//    taken over), so that the next tile's Q and first K and V load while this
-//    one's last block and epilogue run, and the SMs stay balanced over prompts
-//    of any lengths. Tiles of a request and head are adjacent, the longest first.
+//    taken over), so that the next tile's K, Q and V load while this one's last
+//    block and epilogue run, and the SMs stay balanced over prompts of any
+//    lengths. The loader alone decodes indices, skips tiles without rows and hands
+//    the others on through shared memory: code that runs once a tile comes from
+//    the instruction cache's slow levels (decoded by every warp: 182 us where this
+//    takes 177). Tiles of a request and head are adjacent, the longest first.
+//  * Slower on the same chunk: two tiles a CTA sharing K and V (half the loads, but
+//    no second S buffer; 229 us), Q in TMEM with P over S (S(i + 2) waits for O += P
+//    V(i); 221), most of Q in TMEM with one P buffer (192), K's barriers per chunk
+//    with an epilogue by warps of its own (203), softmax warps in two groups that
+//    take blocks in turn (258 and 273).
 //
-// Warps: 0 takes tiles and loads Q and K, 1 issues S, 2 issues O, 3 loads V, 4..19
+// Warps: 0 takes tiles and loads K and Q, 1 issues S, 2 issues O, 3 loads V, 4..19
 // run the softmax and the epilogue (TMEM lane quadrant = warp % 4).
 #include "expanded.cuh"
 #include "tcgen05.cuh"
@@ -54,6 +64,14 @@ struct ExpArgs {
   float scale_log2;
 };
 
+// A tile's rows as the loader hands them on; nblk 0: no more tiles.
+struct Tile {
+  int h, jn;          // head, query rows
+  int q0, k0, kl;     // first query row (of the tensor), first key row, the request's keys
+  int shift;          // query row j of the tile sits at position shift + j
+  int nblk;
+};
+
 struct ExpBars {
   uint64_t q_full, q_free;
   uint64_t k_full[kKS], k_empty[kKS];
@@ -61,10 +79,12 @@ struct ExpBars {
   uint64_t s_full[2], s_free[2], p_full[2], pv_done[2];
   uint64_t o_free, drain, vtail;
   uint64_t xbar[4];
-  uint64_t next_full[2], next_free[2];
+  uint64_t answer;                  // cluster launch control -> loader
+  uint64_t tile_full[2], tile_free[2];
   uint32_t taddr;
   int abort, late;
-  alignas(16) uint32_t next[2][4];  // cluster launch control's answers
+  alignas(16) uint32_t next[4];     // cluster launch control's answer
+  Tile tile[2];
   float xch[2][kParts][kTile];
 };
 
@@ -101,26 +121,20 @@ __device__ __forceinline__ long long taken(const uint32_t* src) {
   return ok ? (long long)x : -1;
 }
 
-struct Tile {
-  int h, j0, jn;      // head, first query row of the request, query rows in the tile (0: nothing)
-  int q0, k0, kl;     // the request's first rows, its keys
-  int shift;          // query j sits at position shift + j
-  int nblk;
-};
-__device__ __forceinline__ Tile tile_of(const ExpArgs& a, long long idx) {
+__device__ __forceinline__ Tile tile_of(const ExpArgs& a, uint32_t idx) {
   Tile t;
-  const long long bh = idx / a.tiles;
-  const int tile = a.tiles - 1 - (int)(idx - bh * a.tiles);
-  const int b = (int)(bh / a.c.H);
-  t.h = (int)(bh - (long long)b * a.c.H);
-  const ExpandedRequest r = expanded_request(a.c, b);
-  t.j0 = tile * kTile;
-  t.jn = r.ok ? max(0, min(kTile, r.ql - t.j0)) : 0;
-  t.q0 = r.q0;
+  const uint32_t bh = idx / (uint32_t)a.tiles;
+  const int tile = a.tiles - 1 - (int)(idx - bh * (uint32_t)a.tiles);
+  const uint32_t b = bh / (uint32_t)a.c.H;
+  t.h = (int)(bh - b * (uint32_t)a.c.H);
+  const ExpandedRequest r = expanded_request(a.c, (int)b);
+  const int j0 = tile * kTile;
+  t.jn = r.ok ? max(0, min(kTile, r.ql - j0)) : 0;
+  t.q0 = r.q0 + j0;
   t.k0 = r.k0;
   t.kl = r.kl;
-  t.shift = r.kl - r.ql;
-  t.nblk = t.jn ? (t.shift + t.j0 + t.jn + kKeys - 1) / kKeys : 0;
+  t.shift = r.kl - r.ql + j0;
+  t.nblk = t.jn ? (t.shift + t.jn + kKeys - 1) / kKeys : 0;
   if (!r.ok && t.h == 0 && tile == 0 && threadIdx.x == 0) set_error(a.c.err, KVP_ERR_BAD_INDEX);
   return t;
 }
@@ -151,10 +165,11 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_tc_kernel(const __grid_c
       mbar_init(&sb.s_free[x], kSoftWarps);
       mbar_init(&sb.p_full[x], kSoftWarps);
       mbar_init(&sb.pv_done[x], 1);
-      mbar_init(&sb.next_full[x], 1);
-      mbar_init(&sb.next_free[x], 3 + kSoftWarps);
+      mbar_init(&sb.tile_full[x], 1);
+      mbar_init(&sb.tile_free[x], 3 + kSoftWarps);
     }
     for (int q = 0; q < 4; ++q) mbar_init(&sb.xbar[q], kParts);
+    mbar_init(&sb.answer, 1);
     mbar_init(&sb.o_free, kSoftWarps);
     mbar_init(&sb.drain, 2);
     mbar_init(&sb.vtail, 1);
@@ -169,43 +184,62 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_tc_kernel(const __grid_c
   const uint32_t tbase = sb.taddr;
   const uint32_t tO = tbase + 256u;
 
-  // The index of this CTA's k-th tile (every role asks in order; the answer to
-  // the k-th request is in slot (k - 1) % 2); -1: none, or a wait gave up.
-  auto tile_index = [&](int k) -> long long {
-    if (k == 0) return (long long)blockIdx.x;
-    const int s = (k - 1) & 1;
-    if (!__all_sync(0xffffffffu, ewait(&sb.next_full[s], (k - 1) >> 1, abort_flag, err))) return -1;
-    const long long x = taken(sb.next[s]);
-    fence_proxy_async_smem();  // the slot's next answer comes through the async proxy
+  // This CTA's k-th tile, from slot k % 2; false: none, or a wait gave up.
+  auto get_tile = [&](int k, Tile& t) -> bool {
+    if (!__all_sync(0xffffffffu, ewait(&sb.tile_full[k & 1], k >> 1, abort_flag, err))) return false;
+    t = sb.tile[k & 1];
     __syncwarp();
-    if (warp != 0 && lane == 0) mbar_arrive(&sb.next_free[s]);
-    return x;
+    if (lane == 0) mbar_arrive(&sb.tile_free[k & 1]);
+    return t.nblk > 0;
   };
 
   if (warp == 0) {
     // ======================= tiles, Q and K ===================================
     int n = 0, nq = 0, asked = 0;
     bool ok = true;
-    for (int k = 0; ok; ++k) {
-      const long long idx = tile_index(k);
-      if (idx < 0) break;
-      // ask for the next one: slot k % 2, whose previous answer (tile k - 1's) every role has read
-      if (k >= 2) ok = __all_sync(0xffffffffu, ewait(&sb.next_free[k & 1], (k >> 1) - 1, abort_flag, err));
-      if (!ok) break;
-      if (lane == 0) take_next(sb.next[k & 1], &sb.next_full[k & 1]);
+    auto ask = [&]() {
+      if (lane == 0) take_next(sb.next, &sb.answer);
       ++asked;
       __syncwarp();
-      const Tile t = tile_of(a, idx);
-      if (!t.nblk) continue;
-      if (nq > 0) ok = __all_sync(0xffffffffu, ewait(&sb.q_free, nq - 1, abort_flag, err));
-      if (!ok) break;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&sb.q_full, kQChunks * kChunk);
-        for (int c = 0; c < kQChunks; ++c) tc5::tma_3d(sQ + c * kChunk, &a.qmap, 64 * c, t.h, t.q0 + t.j0, &sb.q_full);
+    };
+    // The next tile with rows off the grid (nblk 0: none left), after an ask().
+    auto answer = [&]() -> Tile {
+      Tile t;
+      t.nblk = 0;
+      while (ok) {
+        ok = __all_sync(0xffffffffu, ewait(&sb.answer, asked - 1, abort_flag, err));
+        if (!ok) break;
+        const long long idx = taken(sb.next);
+        fence_proxy_async_smem();  // the next answer comes through the async proxy
+        __syncwarp();
+        if (idx < 0) break;
+        t = tile_of(a, (uint32_t)idx);
+        if (t.nblk) break;
+        ask();
       }
-      ++nq;
+      if (!ok) t.nblk = 0;
+      return t;
+    };
+    auto publish = [&](int k, const Tile& t) {
+      if (k >= 2) ok = ok && __all_sync(0xffffffffu, ewait(&sb.tile_free[k & 1], (k >> 1) - 1, abort_flag, err));
+      if (!ok) return;
+      if (lane == 0) {
+        sb.tile[k & 1] = t;
+        mbar_arrive(&sb.tile_full[k & 1]);  // release: the tile is seen by who waits
+      }
       __syncwarp();
-      for (int i = 0; i < t.nblk; ++i, ++n) {
+    };
+    Tile t = tile_of(a, blockIdx.x);
+    if (!t.nblk) {
+      ask();
+      t = answer();
+    }
+    publish(0, t);
+    for (int k = 0; ok && t.nblk; ++k) {
+      Tile nx;
+      nx.nblk = 0;
+      ask();
+      for (int i = 0; ok && i < t.nblk; ++i, ++n) {
         const int st = n % kKS;
         if (n >= kKS) ok = __all_sync(0xffffffffu, ewait(&sb.k_empty[st], n / kKS - 1, abort_flag, err));
         if (!ok) break;
@@ -217,7 +251,23 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_tc_kernel(const __grid_c
           tma_2d(dst + 2 * kChunk, &a.pemap, 0, t.k0 + i * kKeys, &sb.k_full[st]);
         }
         __syncwarp();
+        if (i == 0) {  // behind the first block's K, which need not wait for the tile before
+          if (nq > 0) ok = __all_sync(0xffffffffu, ewait(&sb.q_free, nq - 1, abort_flag, err));
+          if (!ok) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&sb.q_full, kQChunks * kChunk);
+            for (int c = 0; c < kQChunks; ++c) tc5::tma_3d(sQ + c * kChunk, &a.qmap, 64 * c, t.h, t.q0, &sb.q_full);
+          }
+          ++nq;
+          __syncwarp();
+        }
+        // with the stages full, the next tile is decoded and handed on
+        if (i == min(kKS, t.nblk) - 1) {
+          nx = answer();
+          publish(k + 1, nx);
+        }
       }
+      t = nx;
     }
     // what was issued has landed (bounded) before the shared memory goes away
     if (nq > 0) ewait(&sb.q_full, nq - 1, &sb.late, err);
@@ -225,19 +275,14 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_tc_kernel(const __grid_c
       const int cnt = (n + kKS - 1 - s) / kKS;
       if (cnt > 0) ewait(&sb.k_full[s], cnt - 1, &sb.late, err);
     }
-    for (int s = 0; s < 2; ++s) {
-      const int cnt = (asked + 1 - s) / 2;
-      if (cnt > 0) ewait(&sb.next_full[s], cnt - 1, &sb.late, err);
-    }
+    if (asked > 0) ewait(&sb.answer, asked - 1, &sb.late, err);
     __syncwarp();
   } else if (warp == 3) {
     // ======================= V ================================================
     int n = 0, ntail = 0;
     bool ok = true;
-    for (int k = 0; ok; ++k) {
-      const long long idx = tile_index(k);
-      if (idx < 0) break;
-      const Tile t = tile_of(a, idx);
+    Tile t;
+    for (int k = 0; ok && get_tile(k, t); ++k) {
       for (int i = 0; i < t.nblk; ++i, ++n) {
         const int st = n % kVS;
         if (n >= kVS) ok = __all_sync(0xffffffffu, ewait(&sb.v_empty[st], n / kVS - 1, abort_flag, err));
@@ -272,17 +317,13 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_tc_kernel(const __grid_c
     __syncwarp();
   } else if (warp == 1) {
     // ======================= S issuer =========================================
-    int n = 0, nq = 0;
+    int n = 0;
     bool ok = true;
     constexpr uint32_t id = tc5::idesc(kTile, kKeys, 0, 0);
     const uint64_t dq = tc5::desc(smem_u32(sQ), 16, 1024);
-    for (int k = 0; ok; ++k) {
-      const long long idx = tile_index(k);
-      if (idx < 0) break;
-      const Tile t = tile_of(a, idx);
-      if (!t.nblk) continue;
-      ok = __all_sync(0xffffffffu, ewait(&sb.q_full, nq, abort_flag, err));
-      ++nq;
+    Tile t;
+    for (int k = 0; ok && get_tile(k, t); ++k) {
+      ok = __all_sync(0xffffffffu, ewait(&sb.q_full, k, abort_flag, err));
       for (int i = 0; ok && i < t.nblk; ++i, ++n) {
         const int st = n % kKS, buf = n & 1;
         ok = __all_sync(0xffffffffu, ewait(&sb.k_full[st], n / kKS, abort_flag, err));
@@ -307,16 +348,12 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_tc_kernel(const __grid_c
     __syncwarp();
   } else if (warp == 2) {
     // ======================= O issuer =========================================
-    int n = 0, np = 0;
+    int n = 0;
     bool ok = true;
     constexpr uint32_t id = tc5::idesc(kTile, kDv, 0, 1);
-    for (int k = 0; ok; ++k) {
-      const long long idx = tile_index(k);
-      if (idx < 0) break;
-      const Tile t = tile_of(a, idx);
-      if (!t.nblk) continue;
-      if (np > 0) ok = __all_sync(0xffffffffu, ewait(&sb.o_free, np - 1, abort_flag, err));
-      ++np;
+    Tile t;
+    for (int k = 0; ok && get_tile(k, t); ++k) {
+      if (k > 0) ok = __all_sync(0xffffffffu, ewait(&sb.o_free, k - 1, abort_flag, err));
       for (int i = 0; ok && i < t.nblk; ++i, ++n) {
         const int st = n % kVS, buf = n & 1;
         ok = __all_sync(0xffffffffu, ewait(&sb.v_full[st], n / kVS, abort_flag, err));
@@ -361,12 +398,9 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_tc_kernel(const __grid_c
       res = use_max ? fmaxf(fmaxf(v0, v1), fmaxf(v2, v3)) : (v0 + v1) + (v2 + v3);
       return true;
     };
-    for (int k = 0; ok; ++k) {
-      const long long idx = tile_index(k);
-      if (idx < 0) break;
-      const Tile t = tile_of(a, idx);
-      if (!t.nblk) continue;
-      const int p = row < t.jn ? t.shift + t.j0 + row : -1;  // last key the row attends
+    Tile t;
+    for (int k = 0; ok && get_tile(k, t); ++k) {
+      const int p = row < t.jn ? t.shift + row : -1;  // last key the row attends
       float m = -INFINITY, lsum = 0.f;
       for (int i = 0; i < t.nblk; ++i, ++n) {
         const int buf = n & 1;
@@ -451,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_tc_kernel(const __grid_c
       // a NaN sum is the answer of a NaN score
       const float inv = tot == 0.f ? 0.f : 1.f / tot;
       if (row < t.jn) {
-        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.c.out) + ((size_t)(t.q0 + t.j0 + row) * a.c.H + t.h) * kDv + 32 * part;
+        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.c.out) + ((size_t)(t.q0 + row) * a.c.H + t.h) * kDv + 32 * part;
 #pragma unroll
         for (int q = 0; q < 4; ++q)
           *reinterpret_cast<uint4*>(o + 8 * q) =

@@ -118,7 +118,7 @@ __device__ __forceinline__ void tma_3d(void* dst, const void* tmap, int c0, int 
       : "memory");
 }
 
-// Prefetch of a box of a 4-D map to L2.
+// Prefetch of a box to L2.
 __device__ __forceinline__ void tma_prefetch_4d(const void* tmap, int c0, int c1, int c2, int c3) {
   asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(tmap), "r"(c0), "r"(c1),
                "r"(c2), "r"(c3)
