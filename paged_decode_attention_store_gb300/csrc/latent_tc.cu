@@ -57,9 +57,11 @@ constexpr int kKeys = 64;                          // keys per block
 constexpr uint32_t kGroup = 8 * kW * 2;            // 8 keys
 constexpr uint32_t kStage = kKeys / 8 * kGroup;    // 73,728
 constexpr int kStages = 2;
-constexpr int kThreads = 384;
+constexpr int kThreads = 512;
+constexpr int kCopiers = 4;  // warps 12..15
 constexpr int kAhead = 2;  // blocks prefetched to L2 beyond the stages
 constexpr int kSoft0 = 4, kSoftWarps = 8;
+constexpr int kCopy0 = 12;
 constexpr int kMaxR = 64;
 constexpr int kMaxGs = 8;
 constexpr uint64_t kWaitNs = 2000000000ull;
@@ -206,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
     mbar_init(&sb.q_free, 1);
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&sb.job[s], 1);
-      mbar_init(&sb.full[s], 2);
+      mbar_init(&sb.full[s], 1 + kCopiers);
       mbar_init(&sb.empty[s], 1);
     }
     for (int x = 0; x < 2; ++x) {
@@ -357,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
         const int s8 = __shfl_sync(0xffffffffu, w.s0, (4 * lane) & 31);  // lane gi < 8: group gi's first slot
         if (lane == 0) {
           mbar_arrive_expect_tx(&sb.full[st], (uint32_t)__popc(w.boxes) * kGroup);
-          if (w.boxes == 0xFFu) mbar_arrive(&sb.full[st]);  // nothing for the copier
+          if (w.boxes == 0xFFu) mbar_arrive_n(&sb.full[st], kCopiers);  // nothing for the copiers
         }
         __syncwarp();
         if (lane < 8 && ((w.boxes >> lane) & 1))
@@ -396,7 +398,10 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
     }
     __syncwarp();
   } else if (warp == 3) {
-    // ======================= copier of scattered rows ==========================
+    // idle: the softmax warps start on a multiple of four
+  } else if (warp >= kCopy0) {
+    // ======================= copiers of scattered rows =========================
+    // Each takes two groups of a block.
     // A block's copies are one group. The block before is handed on once its
     // copies are in: before waiting for the next job, or, when that is there
     // already, after issuing its copies. Blocks of boxes alone need nothing.
@@ -416,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
       if (copy) {
         // a copy is 4 rows x 128 bytes a warp: lane = 8 row + 16-byte piece
         const int piece = lane & 7;
-        for (int h = 0; h < 16; ++h) {
+        for (int h = 4 * (warp - kCopy0); h < 4 * (warp - kCopy0) + 4; ++h) {
           if ((boxes >> (h >> 1)) & 1) continue;
           const int key = 4 * h + (lane >> 3), r = key & 7;
           const int s = *(volatile int*)&sb.slots[st][key];

@@ -14,13 +14,13 @@
 // both double arithmetic and a table of angles.
 //
 // What bounds it: bytes. Each token is read and written once (q, k, v) and
-// there are 3 flops per byte at most. A block takes ``tokens`` tokens: its
-// threads compute the tokens' rotary_dim / 2 (cos, sin) pairs into shared
-// memory once for all heads, then thread (unit, head) moves 16-byte chunks: a
-// unit is the two chunks of eight pairs in the half layout, one chunk of four
-// in the interleaved one, so that a thread keeps its cosines in registers over
-// the heads. Several tokens per block amortise the barrier when there are many
-// tokens; with few, one token per block spreads a step over the SMs.
+// there are 3 flops per byte at most. A block takes 1 to 4 tokens: its threads
+// compute the tokens' rotary_dim / 2 (cos, sin) pairs into shared memory once for
+// all heads, then move 16-byte chunks: a unit is the two chunks of eight pairs in
+// the half layout, one chunk of four in the interleaved one; a group of threads
+// takes one head of one token, the groups stride over the tokens' heads. Loads run
+// ahead of what they wait for: v and the first heads are on their way while
+// positions, slots and sines are found, later heads two at a time.
 #include "common.cuh"
 
 #include <cmath>
@@ -29,8 +29,9 @@ namespace kvp {
 
 namespace {
 
-constexpr int kRotThreads = 256;
+constexpr int kRotThreads = 128;
 constexpr int kRotMaxPairs = 512;  // (cos, sin) pairs a block holds: tokens * rotary_dim / 2
+constexpr int kRotMaxTokens = 4;
 
 struct RotArgs {
   const char* q;
@@ -91,86 +92,133 @@ struct Vec<__nv_bfloat16> {
   }
 };
 
+// One unit of one head of one token: the chunks, where they go, the pairs' turns.
+template <typename T, bool HALF>
+struct RotUnit {
+  uint4 w0, w1;
+  char* dst;  // nullptr: nothing to do (past the last head, or a key without a slot)
+  const float2* f;
+};
+
 // 16-byte chunks: every row, stride and half of a pair block starts on 16 bytes.
 template <typename T, bool HALF>
 __global__ void __launch_bounds__(kRotThreads) rotary_store_kernel(const RotArgs a) {
   constexpr int N = Vec<T>::N;
+  constexpr int kV = 2;  // chunks of v a thread loads ahead
   __shared__ float2 cs[kRotMaxPairs];
+  __shared__ int slots[kRotMaxTokens];
   const int tid = threadIdx.x;
   const int pairs = a.rot / 2;
   const int t0 = blockIdx.x * a.tokens;
   const int nt = min(a.tokens, a.n - t0);
+  // units of a head: rotated ones first (HALF: chunk u and chunk u + rot / 2 N), then the rest of the head, one chunk each
+  const int rot_units = HALF ? a.rot / (2 * N) : a.rot / N;
+  const int units = rot_units + (a.d - a.rot) / N;
+  const int upar = min(units, kRotThreads);
+  const int groups = kRotThreads / upar;
+  const int g = tid / upar, u0 = tid - g * upar;
+  const int heads = a.hq + a.hk;
+  const int jobs = g < groups ? nt * heads : 0;  // (token, head)
+  const int v_chunks = a.k ? a.v_elems / N : 0, v_jobs = nt * v_chunks;
+
+  // Loads the unit u of job j; its slot is looked up in store().
+  auto load = [&](int j, int u, RotUnit<T, HALF>& x, int& key_of) {
+    x.dst = nullptr;
+    key_of = -1;
+    if (j >= jobs) return;
+    const int t = j / heads, h = j - t * heads;
+    const size_t tok = (size_t)(t0 + t);
+    const bool is_q = h < a.hq, turn = u < rot_units;
+    const int e0 = HALF ? (turn ? u * N : a.rot + (u - rot_units) * N) : u * N;
+    const char* src = is_q ? a.q + tok * a.q_tok + (size_t)h * a.q_head
+                           : a.k + tok * a.k_tok + (size_t)(h - a.hq) * a.d * sizeof(T);
+    // plain loads: q_out may be q itself
+    x.w0 = *reinterpret_cast<const uint4*>(src + (size_t)e0 * sizeof(T));
+    if (HALF && turn) x.w1 = *reinterpret_cast<const uint4*>(src + (size_t)(e0 + pairs) * sizeof(T));
+    x.f = cs + t * pairs + (HALF ? e0 : e0 / 2);
+    if (is_q) {
+      x.dst = a.q_out + tok * a.qo_tok + (size_t)h * a.qo_head + (size_t)e0 * sizeof(T);
+    } else {
+      x.dst = a.k_dst + ((size_t)(h - a.hq) * a.d + e0) * sizeof(T);
+      key_of = t;
+    }
+  };
+  auto store = [&](const RotUnit<T, HALF>& x, int u, int key_of) {
+    if (!x.dst) return;
+    char* dst = x.dst;
+    if (key_of >= 0) {
+      const int slot = slots[key_of];
+      if (slot < 0) return;
+      dst += (size_t)slot * a.row_bytes;
+    }
+    if (u >= rot_units) {
+      *reinterpret_cast<uint4*>(dst) = x.w0;
+      return;
+    }
+    float v[N];
+    Vec<T>::get(x.w0, v);
+    if (HALF) {
+      float y[N], r0[N], r1[N];
+      Vec<T>::get(x.w1, y);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float2 f = x.f[i];
+        r0[i] = v[i] * f.x - y[i] * f.y;
+        r1[i] = y[i] * f.x + v[i] * f.y;
+      }
+      *reinterpret_cast<uint4*>(dst) = Vec<T>::put(r0);
+      *reinterpret_cast<uint4*>(dst + (size_t)pairs * sizeof(T)) = Vec<T>::put(r1);
+    } else {
+      float r[N];
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) {
+        const float2 f = x.f[i];
+        r[2 * i] = v[2 * i] * f.x - v[2 * i + 1] * f.y;
+        r[2 * i + 1] = v[2 * i + 1] * f.x + v[2 * i] * f.y;
+      }
+      *reinterpret_cast<uint4*>(dst) = Vec<T>::put(r);
+    }
+  };
+  auto v_src = [&](int c) {
+    const int t = c / v_chunks;
+    return reinterpret_cast<const uint4*>(a.v + (size_t)(t0 + t) * a.v_tok) + (c - t * v_chunks);
+  };
+  auto v_put = [&](int c, const uint4& w) {
+    const int t = c / v_chunks, slot = slots[t];
+    if (slot >= 0) reinterpret_cast<uint4*>(a.v_dst + (size_t)slot * a.row_bytes)[c - t * v_chunks] = w;
+  };
+
+  uint4 vw[kV];
+#pragma unroll
+  for (int i = 0; i < kV; ++i)
+    if (tid + i * kRotThreads < v_jobs) vw[i] = __ldg(v_src(tid + i * kRotThreads));
+  RotUnit<T, HALF> x0, x1;
+  int k0, k1;
+  load(g, u0, x0, k0);
+  load(g + groups, u0, x1, k1);
+  if (a.k && tid < nt) {
+    const int slot = __ldg(a.out_loc + t0 + tid);
+    const bool good = (unsigned)slot < (unsigned)a.num_slots;
+    if (!good) set_error(a.err, KVP_ERR_BAD_INDEX);
+    slots[tid] = good ? slot : -1;
+  }
   for (int x = tid; x < nt * pairs; x += kRotThreads) {
     const int t = x / pairs, i = x - t * pairs;
     cs[x] = turn_of(__ldg(a.positions + t0 + t), __ldg(a.freqs + i), a.attn);
   }
   __syncthreads();
-  // units of a head: rotated ones first (HALF: chunk u and chunk u + rot / 2 N), then the rest of the head, one chunk each
-  const int rot_units = HALF ? a.rot / (2 * N) : a.rot / N;
-  const int units = rot_units + (a.d - a.rot) / N;
-  const int upar = min(units, kRotThreads);
-  const int heads_at_once = kRotThreads / upar;
-  const int h0 = tid / upar;
-  const int v_chunks = a.v_elems / N;
-  for (int t = 0; t < nt; ++t) {
-    const size_t tok = (size_t)(t0 + t);
-    char* krow = nullptr;
-    if (a.k) {
-      const int slot = __ldg(a.out_loc + tok);
-      if ((unsigned)slot < (unsigned)a.num_slots) {
-        krow = a.k_dst + (size_t)slot * a.row_bytes;
-        const uint4* src = reinterpret_cast<const uint4*>(a.v + tok * a.v_tok);
-        uint4* dst = reinterpret_cast<uint4*>(a.v_dst + (size_t)slot * a.row_bytes);
-        for (int c = tid; c < v_chunks; c += kRotThreads) dst[c] = __ldg(src + c);
-      } else if (tid == 0) {
-        set_error(a.err, KVP_ERR_BAD_INDEX);
-      }
-    }
-    const int heads = a.hq + (krow ? a.hk : 0);
-    if (h0 >= heads_at_once) continue;
-    for (int u = tid % upar; u < units; u += upar) {
-      const bool turn = u < rot_units;
-      const int e0 = HALF ? (turn ? u * N : a.rot + (u - rot_units) * N) : u * N;  // first element of the unit's first chunk
-      const size_t b0 = (size_t)e0 * sizeof(T), b1 = b0 + (size_t)pairs * sizeof(T);
-      float2 f[HALF ? N : N / 2];
-      if (turn) {
 #pragma unroll
-        for (int i = 0; i < (HALF ? N : N / 2); ++i) f[i] = cs[t * pairs + (HALF ? e0 : e0 / 2) + i];
+  for (int i = 0; i < kV; ++i)
+    if (tid + i * kRotThreads < v_jobs) v_put(tid + i * kRotThreads, vw[i]);
+  for (int c = tid + kV * kRotThreads; c < v_jobs; c += kRotThreads) v_put(c, __ldg(v_src(c)));
+  for (int u = u0; u < units; u += upar) {  // more than one round only for heads of more than 256 units
+    for (int j = g; j < jobs; j += 2 * groups) {
+      if (j != g || u != u0) {
+        load(j, u, x0, k0);
+        load(j + groups, u, x1, k1);
       }
-      for (int h = h0; h < heads; h += heads_at_once) {
-        const bool is_q = h < a.hq;
-        const char* src = is_q ? a.q + tok * a.q_tok + (size_t)h * a.q_head
-                               : a.k + tok * a.k_tok + (size_t)(h - a.hq) * a.d * sizeof(T);
-        char* dst = is_q ? a.q_out + tok * a.qo_tok + (size_t)h * a.qo_head : krow + (size_t)(h - a.hq) * a.d * sizeof(T);
-        // plain loads: q_out may be q itself
-        const uint4 w0 = *reinterpret_cast<const uint4*>(src + b0);
-        if (!turn) {
-          *reinterpret_cast<uint4*>(dst + b0) = w0;
-          continue;
-        }
-        float x[N];
-        Vec<T>::get(w0, x);
-        if (HALF) {
-          const uint4 w1 = *reinterpret_cast<const uint4*>(src + b1);
-          float y[N], r0[N], r1[N];
-          Vec<T>::get(w1, y);
-#pragma unroll
-          for (int i = 0; i < N; ++i) {
-            r0[i] = x[i] * f[i].x - y[i] * f[i].y;
-            r1[i] = y[i] * f[i].x + x[i] * f[i].y;
-          }
-          *reinterpret_cast<uint4*>(dst + b0) = Vec<T>::put(r0);
-          *reinterpret_cast<uint4*>(dst + b1) = Vec<T>::put(r1);
-        } else {
-          float r[N];
-#pragma unroll
-          for (int i = 0; i < N / 2; ++i) {
-            r[2 * i] = x[2 * i] * f[i].x - x[2 * i + 1] * f[i].y;
-            r[2 * i + 1] = x[2 * i + 1] * f[i].x + x[2 * i] * f[i].y;
-          }
-          *reinterpret_cast<uint4*>(dst + b0) = Vec<T>::put(r);
-        }
-      }
+      store(x0, u, k0);
+      store(x1, u, k1);
     }
   }
 }
@@ -239,7 +287,7 @@ int launch_rotary(const kvp_pool* pool, RotArgs& a, int layout, cudaStream_t st)
   // as many tokens a block as its shared memory's pairs allow, up to 4, once
   // that still leaves every SM eight blocks
   int tokens = 1;
-  while (tokens < 4 && 2 * tokens * (a.rot / 2) <= kRotMaxPairs && a.n / (2 * tokens) >= pool->num_sms * 8) tokens *= 2;
+  while (tokens < kRotMaxTokens && 2 * tokens * (a.rot / 2) <= kRotMaxPairs && a.n / (2 * tokens) >= pool->num_sms * 8) tokens *= 2;
   a.tokens = tokens;
   const unsigned grid = (unsigned)((a.n + tokens - 1) / tokens);
   if (es == 4) {
