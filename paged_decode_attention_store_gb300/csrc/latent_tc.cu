@@ -87,8 +87,8 @@ struct LatArgs {
 
 struct LatBars {
   uint64_t q_full, q_free;
-  uint64_t job[kStages];    // loader -> copier: slots and boxes of the stage's block are set
-  uint64_t full[kStages];   // loader (boxes' bytes) and copier -> issuers: the block is in
+  uint64_t job[2], job_free[2];  // loader -> copiers: a block with scattered rows; its slots have been read
+  uint64_t full[kStages];   // loader (boxes' bytes) and copiers -> issuers: the block is in
   uint64_t empty[kStages];  // O issuer (commit) -> loader
   uint64_t s_full[2], s_free[2];
   uint64_t p_full, pv_done, o_free, drain, xbar;
@@ -97,8 +97,8 @@ struct LatBars {
   int late;  // raised by a wait for copies in flight that ran out
   int b0;
   long long off0;
-  int slots[kStages][kKeys];
-  int boxes[kStages];  // groups that come as boxes; -1: no more blocks
+  int slots[2][kKeys];  // of a job
+  int2 job_of[2];       // {groups that come as boxes, stage}; x = -1: no more jobs
   float xch[2][2][kMaxR];
 };
 
@@ -208,6 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
     mbar_init(&sb.q_free, 1);
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&sb.job[s], 1);
+      mbar_init(&sb.job_free[s], kCopiers);
       mbar_init(&sb.full[s], 1 + kCopiers);
       mbar_init(&sb.empty[s], 1);
     }
@@ -296,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
       int s0, s1;
       unsigned boxes;
     } ring[2 + kAhead];
-    int named = 0;
+    int named = 0, jobs = 0;
     Pieces<R> pr = pc;
     bool more = pr.next();
     int ri = more ? pr.k0 : 0;
@@ -362,13 +363,20 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
           if (w.boxes == 0xFFu) mbar_arrive_n(&sb.full[st], kCopiers);  // nothing for the copiers
         }
         __syncwarp();
+        if (w.boxes != 0xFFu) {
+          const int js = jobs & 1;
+          if (jobs >= 2) ok = __all_sync(0xffffffffu, lwait(&sb.job_free[js], (jobs >> 1) - 1, abort_flag, a.err));
+          if (!ok) break;
+          sb.slots[js][2 * lane] = w.s0;
+          sb.slots[js][2 * lane + 1] = w.s1;
+          if (lane == 0) sb.job_of[js] = make_int2((int)w.boxes, st);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sb.job[js]);
+          ++jobs;
+        }
         if (lane < 8 && ((w.boxes >> lane) & 1))
           tma_load_4d(sX + st * kStage + lane * kGroup, &a.box, 0, s8, 0, a.layer, &sb.full[st]);
-        sb.slots[st][2 * lane] = w.s0;
-        sb.slots[st][2 * lane + 1] = w.s1;
-        if (lane == 0) sb.boxes[st] = (int)w.boxes;
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sb.job[st]);
         // name the blocks ahead: the next one only while the first is on its way
         while (more && named < n + 2 + (n ? kAhead : 0)) {
           Named v;
@@ -392,55 +400,56 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
       if (cnt > 0) lwait(&sb.full[s], cnt - 1, &sb.late, a.err);
     }
     __syncwarp();
-    if (lane < kStages) {  // the copiers have read their last slots
-      sb.boxes[lane] = -1;
-      mbar_arrive(&sb.job[lane]);
+    if (jobs >= 2) lwait(&sb.job_free[jobs & 1], (jobs >> 1) - 1, &sb.late, a.err);
+    if (lane == 0) {
+      sb.job_of[jobs & 1] = make_int2(-1, 0);
+      mbar_arrive(&sb.job[jobs & 1]);
     }
     __syncwarp();
   } else if (warp == 3) {
     // idle: the softmax warps start on a multiple of four
   } else if (warp >= kCopy0) {
     // ======================= copiers of scattered rows =========================
-    // Each takes two groups of a block.
-    // A block's copies are one group. The block before is handed on once its
-    // copies are in: before waiting for the next job, or, when that is there
-    // already, after issuing its copies. Blocks of boxes alone need nothing.
+    // Each takes two groups of a block. Copies still on their way when the next
+    // job is there are handed on after that one's are issued, else at once.
     int before = -1;  // the stage whose copies are on their way
     for (int k = 0;; ++k) {
-      const int st = k % kStages;
-      if (before >= 0 && !__all_sync(0xffffffffu, mbar_test_wait(&sb.job[st], (uint32_t)(k / kStages) & 1))) {
+      const int js = k & 1;
+      if (before >= 0 && !__all_sync(0xffffffffu, mbar_test_wait(&sb.job[js], (uint32_t)(k >> 1) & 1))) {
         cp_async_wait<0>();
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sb.full[before]);
         before = -1;
       }
-      if (!__all_sync(0xffffffffu, lwait(&sb.job[st], k / kStages, abort_flag, a.err))) break;
-      const int boxes = *(volatile int*)&sb.boxes[st];
-      const bool copy = boxes >= 0 && boxes != 0xFF;
-      if (copy) {
+      if (!__all_sync(0xffffffffu, lwait(&sb.job[js], k >> 1, abort_flag, a.err))) break;
+      volatile int2* job = &sb.job_of[js];
+      const int boxes = job->x, st = job->y;
+      if (boxes >= 0) {
         // a copy is 4 rows x 128 bytes a warp: lane = 8 row + 16-byte piece
         const int piece = lane & 7;
         for (int h = 4 * (warp - kCopy0); h < 4 * (warp - kCopy0) + 4; ++h) {
           if ((boxes >> (h >> 1)) & 1) continue;
           const int key = 4 * h + (lane >> 3), r = key & 7;
-          const int s = *(volatile int*)&sb.slots[st][key];
+          const int s = *(volatile int*)&sb.slots[js][key];
           const char* src = a.rows + (size_t)max(s, 0) * (kW * 2) + piece * 16;
           const uint32_t dst = smem_u32(sX) + st * kStage + (uint32_t)(key >> 3) * kGroup + r * 128 + ((piece ^ r) << 4);
 #pragma unroll
           for (int c = 0; c < kChunks; ++c) tc5::cp_async16(dst + c * 1024, src + c * 128, s < 0 ? 0 : 16);
         }
         cp_async_commit();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sb.job_free[js]);
       }
       if (before >= 0) {
-        if (copy) cp_async_wait<1>();
+        if (boxes >= 0) cp_async_wait<1>();
         else cp_async_wait<0>();
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sb.full[before]);
       }
-      before = copy ? st : -1;
       if (boxes < 0) break;
+      before = st;
     }
     cp_async_wait<0>();
     __syncwarp();
