@@ -72,6 +72,7 @@ struct LatArgs {
   TableRef T;
   int layer;
   const char* rows;  // the layer's slot 0
+  int page_shift;    // log2 of the page size, -1: no power of two
   __nv_bfloat16* out;
   const int32_t* context_lens;
   const int32_t* table_rows;
@@ -127,7 +128,7 @@ struct LatItem {
 template <int R>
 __device__ __forceinline__ LatItem item_of(const LatArgs& a, const LatReq& r, int tg) {
   const int rows = r.ql * a.H, per = a.Gs * R;
-  const int j0 = tg * per / a.H, j1 = (min((tg + 1) * per, rows) - 1) / a.H;
+  const int j0 = a.C == 1 ? 0 : tg * per / a.H, j1 = a.C == 1 ? 0 : (min((tg + 1) * per, rows) - 1) / a.H;
   const int p0 = r.L - r.ql + j0, p1 = r.L - r.ql + j1;
   LatItem it;
   it.u = attend_span(p1 + 1, a.window > 0 ? a.window + (p1 - p0) : 0, a.sinks);
@@ -138,7 +139,7 @@ __device__ __forceinline__ LatItem item_of(const LatArgs& a, const LatReq& r, in
 template <int R>
 __device__ __forceinline__ int groups_of(const LatArgs& a, int ql) {
   const int per = a.Gs * R;
-  return (ql * a.H + per - 1) / per;
+  return ql * a.H <= per ? (ql > 0) : (ql * a.H + per - 1) / per;
 }
 
 // Walks the pieces of this CTA's range; every role walks the same ones.
@@ -184,6 +185,17 @@ struct Pieces {
   }
 };
 
+// resolve_slot with the page size's shift where it is a power of two.
+__device__ __forceinline__ int slot_of(const LatArgs& a, int row, int t) {
+  if (a.T.raw || a.page_shift < 0) return resolve_slot(a.T, row, t, a.err);
+  const int page = __ldg(a.T.table + (size_t)row * a.T.cols + (t >> a.page_shift));
+  if ((unsigned)page >= (unsigned)a.T.num_pages) {
+    set_error(a.err, KVP_ERR_BAD_INDEX);
+    return -1;
+  }
+  return (page << a.page_shift) + (t & (a.T.page_size - 1));
+}
+
 __device__ __forceinline__ long long range_start(long long total, int g, int NG) { return NG ? total * g / NG : 0; }
 
 template <int R>
@@ -203,6 +215,10 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
   const int cta = blockIdx.x, g = cta / a.Gs, t = cta % a.Gs;
 
   // before the wait for the stream's previous kernel: nothing here touches global memory
+  if (tid == 32) {
+    tc5::prefetch_map(&a.qmap);
+    tc5::prefetch_map(&a.box);
+  }
   if (tid == 0) {
     mbar_init(&sb.q_full, 1);
     mbar_init(&sb.q_free, 1);
@@ -282,6 +298,10 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
   // TMEM: O^T at columns 0 .. 4 R - 1 (block j of 128 entries at j R), S buffers at 256 and 320
   const uint32_t tbase = sb.taddr;
   Pieces<R> pc(a, t, sb.b0, sb.off0, r1 - r0);
+  // Rows leave L2 first: a step streams more of them than it holds, and would
+  // put out the kernels' own code, which then comes from memory again, a line at a
+  // time (64 requests of 2304 rows, 32 heads: 52.5 us without, 47.1 with).
+  const uint64_t once = policy_evict_first();
 
   if (warp == 0) {
     // ======================= loader ===========================================
@@ -310,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
         int s = -1;
         if (lane < 8 && og + 7 < nk && (og >= u.se || og + 7 < u.se)) {
           const int p = span_pos(u, og);
-          if ((p & 7) == 0) s = resolve_slot(a.T, pr.r.row, p, a.err);
+          if ((p & 7) == 0) s = slot_of(a, pr.r.row, p);
         }
         w.boxes = __ballot_sync(0xffffffffu, s >= 0) & 0xFFu;
         w.s0 = __shfl_sync(0xffffffffu, s, lane >> 2) + 2 * (lane & 3);
@@ -321,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const int o = o0 + 2 * lane + k;
-          sl[k] = o < nk ? resolve_slot(a.T, pr.r.row, span_pos(u, o), a.err) : -1;
+          sl[k] = o < nk ? slot_of(a, pr.r.row, span_pos(u, o)) : -1;
         }
         w.s0 = sl[0];
         w.s1 = sl[1];
@@ -337,6 +357,10 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
         ri = more ? pr.k0 : 0;
       }
     };
+    if (more) {  // the first block's rows before all else
+      name_next(ring[0]);
+      named = 1;
+    }
     while (ok && pc.next()) {
       if (np > 0) ok = __all_sync(0xffffffffu, lwait(&sb.q_free, np - 1, abort_flag, a.err));
       if (!ok) break;
@@ -348,10 +372,6 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
       __syncwarp();
       for (int i = pc.k0; i < pc.k1; ++i, ++n) {
         const int st = n % kStages;
-        if (named == n) {  // the first block; later ones are named in the loop below
-          name_next(ring[0]);
-          ++named;
-        }
         const Named w = ring[0];
 #pragma unroll
         for (int x = 0; x < 1 + kAhead; ++x) ring[x] = ring[x + 1];
@@ -375,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
           ++jobs;
         }
         if (lane < 8 && ((w.boxes >> lane) & 1))
-          tma_load_4d(sX + st * kStage + lane * kGroup, &a.box, 0, s8, 0, a.layer, &sb.full[st]);
+          tc5::tma_4d(sX + st * kStage + lane * kGroup, &a.box, 0, s8, 0, a.layer, &sb.full[st], once);
         __syncwarp();
         // name the blocks ahead: the next one only while the first is on its way
         while (more && named < n + 2 + (n ? kAhead : 0)) {
@@ -387,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
           // one CTA of a group prefetches the boxes (scattered rows gained nothing: 2.8 us a block without, 3.1 with)
           if (named >= kStages && t == 0 && v.boxes == 0xFFu) {
             const int p8 = __shfl_sync(0xffffffffu, v.s0, (4 * lane) & 31);
-            if (lane < 8) tc5::tma_prefetch_4d(&a.box, 0, p8, 0, a.layer);
+            if (lane < 8) tc5::tma_prefetch_4d(&a.box, 0, p8, 0, a.layer, once);
           }
           ++named;
         }
@@ -435,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
           const char* src = a.rows + (size_t)max(s, 0) * (kW * 2) + piece * 16;
           const uint32_t dst = smem_u32(sX) + st * kStage + (uint32_t)(key >> 3) * kGroup + r * 128 + ((piece ^ r) << 4);
 #pragma unroll
-          for (int c = 0; c < kChunks; ++c) tc5::cp_async16(dst + c * 1024, src + c * 128, s < 0 ? 0 : 16);
+          for (int c = 0; c < kChunks; ++c) tc5::cp_async16(dst + c * 1024, src + c * 128, s < 0 ? 0 : 16, once);
         }
         cp_async_commit();
         __syncwarp();
@@ -545,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
     while (ok && pc.next()) {
       const int rr = pc.tile * R + row;
       const bool rv = rr < pc.r.ql * a.H;
-      const int p = pc.r.L - pc.r.ql + rr / a.H;
+      const int p = pc.r.L - pc.r.ql + (a.C == 1 ? 0 : rr / a.H);
       const Span u = pc.it.u, sr0 = attend_span(p + 1, a.window, a.sinks);
       // the row attends key offsets [0, se) and [wb, we] of the item's span
       const int se = rv ? sr0.se : 0;
@@ -719,45 +739,55 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
   if (warp == 0) tc5::dealloc512(tbase);
 }
 
-// Joins the partials of the items that a range boundary cut. Block (x, y) takes
-// the x-th cut item of the records. With SPLIT (few items, many pieces each) it
-// takes row y, its eight warps every eighth piece, joined through shared
-// memory; else rows 8 y .. 8 y + 7, a warp each. A lane holds 16 of a row's 512
-// entries.
+// Joins the partials of the items that a range boundary cut. With SPLIT (few
+// items, many pieces each) block (x, y) takes row y of the x-th cut item, its eight
+// warps every eighth piece, joined through shared memory; else rows 8 y .. 8 y + 7
+// of the item that CTA x cut, a warp each. A lane holds 16 of a row's 512 entries.
 constexpr int kCombWarps = 8;
 template <int R, bool SPLIT>
 __global__ void __launch_bounds__(32 * kCombWarps) latent_combine_kernel(const LatArgs a) {
-  __shared__ int counts[kCombWarps];
+  __shared__ int counts[SPLIT ? kCombWarps : 1];
   __shared__ int4 rec;
   __shared__ int rec_cta;
   __shared__ float sm[SPLIT ? kCombWarps : 1], sl[SPLIT ? kCombWarps : 1];
   __shared__ float4 so[SPLIT ? kCombWarps : 1][SPLIT ? kDc / 4 : 1];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   griddep_wait();
-  const int ctas = a.NG * a.Gs;
-  int seen = 0;
-  if (tid == 0) rec_cta = -1;
-  for (int c0 = 0; c0 < ctas; c0 += 32 * kCombWarps) {
-    const int c = c0 + tid;
-    const int4 mg = c < ctas ? a.merge[c] : make_int4(-1, 0, 0, 0);
-    const unsigned has = __ballot_sync(0xffffffffu, mg.x >= 0);
-    __syncthreads();
-    if (lane == 0) counts[warp] = __popc(has);
-    __syncthreads();
-    int before = seen;
-    for (int w = 0; w < kCombWarps; ++w) {
-      if (w < warp) before += counts[w];
-      seen += counts[w];
+  // the stream's next kernel may set itself up; it waits for this one before it touches memory
+  griddep_launch_dependents();
+  int4 mg;  // {first output row, rows, last group, slot of the first piece}
+  int from;
+  if (SPLIT) {
+    const int ctas = a.NG * a.Gs;
+    int seen = 0;
+    if (tid == 0) rec_cta = -1;
+    for (int c0 = 0; c0 < ctas; c0 += 32 * kCombWarps) {
+      const int c = c0 + tid;
+      const int4 m = c < ctas ? a.merge[c] : make_int4(-1, 0, 0, 0);
+      const unsigned has = __ballot_sync(0xffffffffu, m.x >= 0);
+      __syncthreads();
+      if (lane == 0) counts[warp] = __popc(has);
+      __syncthreads();
+      int before = seen;
+      for (int w = 0; w < kCombWarps; ++w) {
+        if (w < warp) before += counts[w];
+        seen += counts[w];
+      }
+      if (m.x >= 0 && before + __popc(has & ((1u << lane) - 1)) == (int)blockIdx.x) {
+        rec = m;
+        rec_cta = c;
+      }
     }
-    if (mg.x >= 0 && before + __popc(has & ((1u << lane) - 1)) == (int)blockIdx.x) {
-      rec = mg;
-      rec_cta = c;
-    }
+    __syncthreads();
+    from = rec_cta;
+    mg = rec;
+    if (from < 0) return;
+  } else {
+    from = blockIdx.x;
+    mg = a.merge[from];
+    if (mg.x < 0) return;
   }
-  __syncthreads();
-  if (rec_cta < 0) return;
-  const int4 mg = rec;  // {first output row, rows, last group, slot of the first piece}
-  const int t = rec_cta % a.Gs, g = rec_cta / a.Gs, n = mg.z - g + 1;
+  const int t = from % a.Gs, g = from / a.Gs, n = mg.z - g + 1;
   const int r = SPLIT ? (int)blockIdx.y : kCombWarps * (int)blockIdx.y + warp;
   if (r >= mg.y) return;  // SPLIT: the whole block
   auto at = [&](int k) { return (size_t)(2 * ((g + k) * a.Gs + t) + (k ? 0 : mg.w)) * R + r; };
@@ -786,7 +816,7 @@ __global__ void __launch_bounds__(32 * kCombWarps) latent_combine_kernel(const L
     for (int sh = 16; sh > 0; sh >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, sh);
     l += ls;
     const int nk = min(32, mine - k0);
-#pragma unroll 2
+#pragma unroll 4
     for (int k = 0; k < nk; ++k) {
       const float fk = __shfl_sync(0xffffffffu, f, k);
       const float4* x = reinterpret_cast<const float4*>(a.part_o + at(first + step * (k0 + k)) * kDc) + lane;
@@ -901,7 +931,7 @@ cudaError_t launch_lat(const LatArgs& a, int ctas, cudaStream_t stream) {
     c.gridDim = dim3(cut, R);
     return cudaLaunchKernelEx(&c, latent_combine_kernel<R, true>, a);
   }
-  c.gridDim = dim3(cut, R / kCombWarps);
+  c.gridDim = dim3((unsigned)ctas, R / kCombWarps);
   return cudaLaunchKernelEx(&c, latent_combine_kernel<R, false>, a);
 }
 
@@ -961,6 +991,10 @@ int launch_latent_tc(const LatentCall& c, cudaStream_t stream) {
   a.T = c.T;
   a.layer = c.layer;
   a.rows = c.pool->buf + (size_t)c.layer * c.pool->layer_bytes;
+  a.page_shift = -1;
+  if (!(c.T.page_size & (c.T.page_size - 1)))
+    for (a.page_shift = 0; (1 << a.page_shift) < c.T.page_size; ++a.page_shift) {
+    }
   a.out = static_cast<__nv_bfloat16*>(c.out);
   a.context_lens = c.context_lens;
   a.table_rows = c.table_rows;
