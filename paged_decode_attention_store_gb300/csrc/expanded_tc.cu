@@ -49,8 +49,9 @@ constexpr int kDn = 128, kDr = 64, kDv = 128;
 constexpr uint32_t kChunk = 16384;  // 128 rows x 128 B
 constexpr int kQChunks = (kDn + kDr) / 64, kVChunks = kDv / 64;
 constexpr int kKS = 2, kVS = 2;
-constexpr int kThreads = 640;
+constexpr int kThreads = 768;
 constexpr int kSoft0 = 4, kSoftWarps = 16, kParts = 4;
+constexpr int kEpi0 = 20, kEpiWarps = 4;
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr size_t kSmem = (kQChunks + kKS * kQChunks + kVS * kVChunks) * kChunk;
 
@@ -77,6 +78,7 @@ struct ExpBars {
   uint64_t k_full[kKS], k_empty[kKS];
   uint64_t v_full[kVS], v_empty[kVS];
   uint64_t s_full[2], s_free[2], p_full[2], pv_done[2];
+  uint64_t l_full[2], l_free[2];    // a tile's row sums are in ``sums``; read
   uint64_t o_free, drain, vtail;
   uint64_t xbar[4];
   uint64_t answer;                  // cluster launch control -> loader
@@ -86,6 +88,7 @@ struct ExpBars {
   alignas(16) uint32_t next[4];     // cluster launch control's answer
   Tile tile[2];
   float xch[2][kParts][kTile];
+  float sums[2][kParts][kTile];
 };
 
 __device__ __forceinline__ bool ewait(uint64_t* bar, int k, volatile int* abort_flag, int32_t* err) {
@@ -166,11 +169,13 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_tc_kernel(const __grid_c
       mbar_init(&sb.p_full[x], kSoftWarps);
       mbar_init(&sb.pv_done[x], 1);
       mbar_init(&sb.tile_full[x], 1);
-      mbar_init(&sb.tile_free[x], 3 + kSoftWarps);
+      mbar_init(&sb.tile_free[x], 3 + kSoftWarps + kEpiWarps);
+      mbar_init(&sb.l_full[x], kSoftWarps);
+      mbar_init(&sb.l_free[x], kEpiWarps);
     }
     for (int q = 0; q < 4; ++q) mbar_init(&sb.xbar[q], kParts);
     mbar_init(&sb.answer, 1);
-    mbar_init(&sb.o_free, kSoftWarps);
+    mbar_init(&sb.o_free, kEpiWarps);
     mbar_init(&sb.drain, 2);
     mbar_init(&sb.vtail, 1);
     sb.abort = sb.late = 0;
@@ -375,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_tc_kernel(const __grid_c
     }
     if (tc5::elect_one()) tc5::commit(&sb.drain);
     __syncwarp();
-  } else {
+  } else if (warp < kEpi0) {
     // ======================= softmax ==========================================
     const int quad = warp & 3, part = (warp - kSoft0) >> 2;
     const int row = 32 * quad + lane;
@@ -384,8 +389,8 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_tc_kernel(const __grid_c
     const float sl2 = a.scale_log2;
     int n = 0, nx = 0;
     bool ok = true;
-    // the row's four parts: maxima or sums, through shared memory
-    auto exchange = [&](float v, bool use_max, float& res) -> bool {
+    // the maximum of the row's four parts, through shared memory
+    auto exchange = [&](float v, float& res) -> bool {
       volatile float* xc = &sb.xch[nx & 1][0][0];
       xc[part * kTile + row] = v;
       __threadfence_block();
@@ -395,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_tc_kernel(const __grid_c
       ++nx;
       if (!done) return false;
       const float v0 = xc[row], v1 = xc[kTile + row], v2 = xc[2 * kTile + row], v3 = xc[3 * kTile + row];
-      res = use_max ? fmaxf(fmaxf(v0, v1), fmaxf(v2, v3)) : (v0 + v1) + (v2 + v3);
+      res = fmaxf(fmaxf(v0, v1), fmaxf(v2, v3));
       return true;
     };
     Tile t;
@@ -427,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_tc_kernel(const __grid_c
           mt[q] = tc5::max3(tc5::max3(sv[8 * q], sv[8 * q + 1], sv[8 * q + 2]),
                             tc5::max3(sv[8 * q + 3], sv[8 * q + 4], sv[8 * q + 5]), fmaxf(sv[8 * q + 6], sv[8 * q + 7]));
         float mx;
-        if (!(ok = exchange(fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3])) * sl2, true, mx))) break;  // scale > 0
+        if (!(ok = exchange(fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3])) * sl2, mx))) break;  // scale > 0
         const bool grow = mx > m + 8.f;
         const float f = grow && m > -INFINITY ? exp2f(m - mx) : 1.f;
         if (grow) m = mx;
@@ -469,29 +474,53 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_tc_kernel(const __grid_c
         if (lane == 0) mbar_arrive(&sb.p_full[buf]);
       }
       if (!ok) break;
-      // ---- epilogue: O / l to the output
-      ok = __all_sync(0xffffffffu, ewait(&sb.pv_done[(n - 1) & 1], (n - 1) >> 1, abort_flag, err));
+      // ---- the row sum's part goes to the epilogue
+      if (k >= 2) ok = __all_sync(0xffffffffu, ewait(&sb.l_free[k & 1], (k >> 1) - 1, abort_flag, err));
       if (!ok) break;
-      float tot;
-      if (!(ok = exchange(lsum, false, tot))) break;
-      tc5::fence_after();
-      float ov[32];
-      tc5::ld16(tOp, ov);
-      tc5::ld16(tOp + 16, ov + 16);
-      tc5::wait_ld();
-      tc5::fence_before();
+      sb.sums[k & 1][part][row] = lsum;
+      __threadfence_block();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sb.o_free);
+      if (lane == 0) mbar_arrive(&sb.l_full[k & 1]);
+    }
+  } else {
+    // ======================= epilogue: O / l to the output =====================
+    const int quad = warp & 3, row = 32 * quad + lane;
+    const uint32_t lanes = (uint32_t)(32 * quad) << 16;
+    int n = 0;
+    bool ok = true;
+    Tile t;
+    for (int k = 0; ok && get_tile(k, t); ++k) {
+      n += t.nblk;
+      // The sums come after the softmax has seen all products but the last two of
+      // the tile, so the parity of the last one's phase is unambiguous from then on.
+      ok = __all_sync(0xffffffffu, ewait(&sb.l_full[k & 1], k >> 1, abort_flag, err));
+      if (ok) ok = __all_sync(0xffffffffu, ewait(&sb.pv_done[(n - 1) & 1], (n - 1) >> 1, abort_flag, err));
+      if (!ok) break;
+      tc5::fence_after();
+      volatile float* sm = &sb.sums[k & 1][0][0];
+      const float tot = (sm[row] + sm[kTile + row]) + (sm[2 * kTile + row] + sm[3 * kTile + row]);
       // a NaN sum is the answer of a NaN score
       const float inv = tot == 0.f ? 0.f : 1.f / tot;
-      if (row < t.jn) {
-        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.c.out) + ((size_t)(t.q0 + row) * a.c.H + t.h) * kDv + 32 * part;
+      // all of O to registers, packed, before the stores: the next tile's first product waits for it
+      uint32_t w[kDv / 2];
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          *reinterpret_cast<uint4*>(o + 8 * q) =
-              make_uint4(pack_bf16(ov[8 * q] * inv, ov[8 * q + 1] * inv), pack_bf16(ov[8 * q + 2] * inv, ov[8 * q + 3] * inv),
-                         pack_bf16(ov[8 * q + 4] * inv, ov[8 * q + 5] * inv),
-                         pack_bf16(ov[8 * q + 6] * inv, ov[8 * q + 7] * inv));
+      for (int c = 0; c < kDv; c += 16) {
+        float ov[16];
+        tc5::ld16(tO + lanes + c, ov);
+        tc5::wait_ld();
+#pragma unroll
+        for (int q = 0; q < 8; ++q) w[c / 2 + q] = pack_bf16(ov[2 * q] * inv, ov[2 * q + 1] * inv);
+      }
+      tc5::fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&sb.o_free);
+        mbar_arrive(&sb.l_free[k & 1]);
+      }
+      if (row < t.jn) {
+        uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.c.out) + ((size_t)(t.q0 + row) * a.c.H + t.h) * kDv);
+#pragma unroll
+        for (int q = 0; q < kDv / 8; ++q) o[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
       }
     }
   }

@@ -97,7 +97,7 @@ template <typename T, bool HALF>
 struct RotUnit {
   uint4 w0, w1;
   char* dst;  // nullptr: nothing to do (past the last head, or a key without a slot)
-  const float2* f;
+  const float4* f;  // two pairs' turns, the next two ``rot_units`` further
 };
 
 // 16-byte chunks: every row, stride and half of a pair block starts on 16 bytes.
@@ -105,7 +105,11 @@ template <typename T, bool HALF>
 __global__ void __launch_bounds__(kRotThreads) rotary_store_kernel(const RotArgs a) {
   constexpr int N = Vec<T>::N;
   constexpr int kV = 2;  // chunks of v a thread loads ahead
-  __shared__ float2 cs[kRotMaxPairs];
+  constexpr int PU = HALF ? N : N / 2;  // pairs of a unit
+  // A token's turns lie two pairs by two, unit after unit: the threads of a head
+  // read 16 bytes each side by side (pair after pair they met in the same banks
+  // eight at a time, which cost more than the memory did).
+  __shared__ float4 cs[kRotMaxPairs / 2];
   __shared__ int slots[kRotMaxTokens];
   const int tid = threadIdx.x;
   const int pairs = a.rot / 2;
@@ -135,7 +139,7 @@ __global__ void __launch_bounds__(kRotThreads) rotary_store_kernel(const RotArgs
     // plain loads: q_out may be q itself
     x.w0 = *reinterpret_cast<const uint4*>(src + (size_t)e0 * sizeof(T));
     if (HALF && turn) x.w1 = *reinterpret_cast<const uint4*>(src + (size_t)(e0 + pairs) * sizeof(T));
-    x.f = cs + t * pairs + (HALF ? e0 : e0 / 2);
+    x.f = cs + t * (pairs / 2) + (turn ? u : 0);
     if (is_q) {
       x.dst = a.q_out + tok * a.qo_tok + (size_t)h * a.qo_head + (size_t)e0 * sizeof(T);
     } else {
@@ -161,20 +165,24 @@ __global__ void __launch_bounds__(kRotThreads) rotary_store_kernel(const RotArgs
       float y[N], r0[N], r1[N];
       Vec<T>::get(x.w1, y);
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const float2 f = x.f[i];
+      for (int i = 0; i < N; i += 2) {
+        const float4 f = x.f[i / 2 * rot_units];
         r0[i] = v[i] * f.x - y[i] * f.y;
         r1[i] = y[i] * f.x + v[i] * f.y;
+        r0[i + 1] = v[i + 1] * f.z - y[i + 1] * f.w;
+        r1[i + 1] = y[i + 1] * f.z + v[i + 1] * f.w;
       }
       *reinterpret_cast<uint4*>(dst) = Vec<T>::put(r0);
       *reinterpret_cast<uint4*>(dst + (size_t)pairs * sizeof(T)) = Vec<T>::put(r1);
     } else {
       float r[N];
 #pragma unroll
-      for (int i = 0; i < N / 2; ++i) {
-        const float2 f = x.f[i];
+      for (int i = 0; i < N / 2; i += 2) {
+        const float4 f = x.f[i / 2 * rot_units];
         r[2 * i] = v[2 * i] * f.x - v[2 * i + 1] * f.y;
         r[2 * i + 1] = v[2 * i + 1] * f.x + v[2 * i] * f.y;
+        r[2 * i + 2] = v[2 * i + 2] * f.z - v[2 * i + 3] * f.w;
+        r[2 * i + 3] = v[2 * i + 3] * f.z + v[2 * i + 2] * f.w;
       }
       *reinterpret_cast<uint4*>(dst) = Vec<T>::put(r);
     }
@@ -204,7 +212,9 @@ __global__ void __launch_bounds__(kRotThreads) rotary_store_kernel(const RotArgs
   }
   for (int x = tid; x < nt * pairs; x += kRotThreads) {
     const int t = x / pairs, i = x - t * pairs;
-    cs[x] = turn_of(__ldg(a.positions + t0 + t), __ldg(a.freqs + i), a.attn);
+    const int u = i / PU, r = i % PU;
+    reinterpret_cast<float2*>(cs)[t * pairs + 2 * (r / 2 * rot_units + u) + (r & 1)] =
+        turn_of(__ldg(a.positions + t0 + t), __ldg(a.freqs + i), a.attn);
   }
   __syncthreads();
 #pragma unroll
