@@ -60,7 +60,7 @@ constexpr int kStages = 2;
 constexpr int kThreads = 512;
 constexpr int kCopiers = 4;  // warps 12..15
 constexpr int kAhead = 2;  // blocks prefetched to L2 beyond the stages
-constexpr int kSoft0 = 4, kSoftWarps = 8;
+constexpr int kSoft0 = 4, kScale0 = 8, kScaleWarps = 4;  // softmax: R / 16 of 4 warps
 constexpr int kCopy0 = 12;
 constexpr int kMaxR = 64;
 constexpr int kMaxGs = 8;
@@ -92,7 +92,8 @@ struct LatBars {
   uint64_t full[kStages];   // loader (boxes' bytes) and copiers -> issuers: the block is in
   uint64_t empty[kStages];  // O issuer (commit) -> loader
   uint64_t s_full[2], s_free[2];
-  uint64_t p_full, pv_done, o_free, drain, xbar;
+  uint64_t f_full[2];       // softmax -> scaling warps: the block's factors are in ``factor``
+  uint64_t p_full, pv_done, o_free, drain, sums;
   uint32_t taddr;
   int abort;
   int late;  // raised by a wait for copies in flight that ran out
@@ -100,7 +101,8 @@ struct LatBars {
   long long off0;
   int slots[2][kKeys];  // of a job
   int2 job_of[2];       // {groups that come as boxes, stage}; x = -1: no more jobs
-  float xch[2][2][kMaxR];
+  float factor[2][kMaxR];   // of a block: what O's rows have to be scaled by before it
+  float row_m[kMaxR], row_l[kMaxR];  // of a piece
 };
 
 __device__ __forceinline__ bool lwait(uint64_t* bar, int k, volatile int* abort_flag, int32_t* err) {
@@ -230,13 +232,14 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&sb.s_full[x], 1);
-      mbar_init(&sb.s_free[x], kSoftWarps);
+      mbar_init(&sb.s_free[x], R / 16);
+      mbar_init(&sb.f_full[x], R / 16);
     }
-    mbar_init(&sb.p_full, kSoftWarps);
+    mbar_init(&sb.p_full, R / 16 + kScaleWarps);
     mbar_init(&sb.pv_done, 1);
-    mbar_init(&sb.o_free, kSoftWarps);
+    mbar_init(&sb.o_free, 4 + kScaleWarps);
     mbar_init(&sb.drain, 2);
-    mbar_init(&sb.xbar, kSoftWarps);
+    mbar_init(&sb.sums, R / 16);
     sb.abort = sb.late = 0;
     fence_mbar_init();
   }
@@ -536,142 +539,158 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
     if (tc5::elect_one()) tc5::commit(&sb.drain);
     __syncwarp();
   } else {
-    // ======================= softmax ==========================================
-    // Thread (quadrant, lane < 16, part): query row 16 quadrant + lane, keys
-    // 32 part .. 32 part + 31 of each block. The running maxima of rows lane and
-    // lane + 32 are kept by every warp alike (m0, m1), since all eight rescale O.
+    // ======================= softmax, and the scaling of O ====================
+    // A softmax warp has 16 query rows: lane l rows row0 = 16 quadrant + l / 4 and
+    // row0 + 8, of every eight keys the two from 2 (l % 4) on (the 16-lane form of
+    // tcgen05.ld), so that no lane idles and a row lies in four lanes of one warp.
+    // The scaling warps hold back P until O has been scaled, when a maximum grew.
     const int quad = warp & 3, part = (warp - kSoft0) >> 2;
-    const int row = 16 * quad + (lane & 15);
-    const bool mine = row < R;                 // warp-uniform: R is a multiple of 16
-    const bool active = mine && lane < 16;
+    const bool softmax = warp < kScale0 && quad < R / 16;
     const uint32_t lanes = (uint32_t)(32 * quad) << 16;
+    const int row0 = 16 * quad + (lane >> 2);
     const float sl2 = a.scale_log2;
-    int n = 0, nx = 0;  // blocks, exchanges
+    int n = 0, np = 0;  // blocks, pieces
     int4 merge = make_int4(-1, 0, 0, 0);
     bool ok = true;
-    auto exchange = [&](float v, float& x00, float& x01, float& x10, float& x11) -> bool {
-      volatile float* xc = &sb.xch[nx & 1][0][0];
-      if (active) xc[part * kMaxR + row] = v;
-      __threadfence_block();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sb.xbar);
-      const bool done = __all_sync(0xffffffffu, lwait(&sb.xbar, nx, abort_flag, a.err));
-      ++nx;
-      if (!done) return false;
-      x00 = xc[lane], x10 = xc[kMaxR + lane];
-      if (R > 32) x01 = xc[lane + 32], x11 = xc[kMaxR + lane + 32];
-      return true;
-    };
     while (ok && pc.next()) {
-      const int rr = pc.tile * R + row;
-      const bool rv = rr < pc.r.ql * a.H;
-      const int p = pc.r.L - pc.r.ql + (a.C == 1 ? 0 : rr / a.H);
-      const Span u = pc.it.u, sr0 = attend_span(p + 1, a.window, a.sinks);
-      // the row attends key offsets [0, se) and [wb, we] of the item's span
-      const int se = rv ? sr0.se : 0;
-      const int wb0 = rv ? u.se + (sr0.lo - u.lo) : 1 << 30, we0 = rv ? u.se + (p - u.lo) : -1;
-      float m0 = -INFINITY, m1 = -INFINITY, lsum = 0.f;
-      for (int i = pc.k0; i < pc.k1; ++i, ++n) {
-        const int buf = n & 1;
-        ok = __all_sync(0xffffffffu, lwait(&sb.s_full[buf], n >> 1, abort_flag, a.err));
-        if (!ok) break;
-        float sv[32];
-        float mx = -INFINITY;
-        if (mine) {
+      if (softmax) {
+        // row x attends key offsets [0, se) and [wb, we] of the item's span
+        int se[2], wb0[2], we0[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int rr = pc.tile * R + row0 + 8 * x;
+          const bool rv = rr < pc.r.ql * a.H;
+          const int p = pc.r.L - pc.r.ql + (a.C == 1 ? 0 : rr / a.H);
+          const Span u = pc.it.u, sr = attend_span(p + 1, a.window, a.sinks);
+          se[x] = rv ? sr.se : 0;
+          wb0[x] = rv ? u.se + (sr.lo - u.lo) : 1 << 30;
+          we0[x] = rv ? u.se + (p - u.lo) : -1;
+        }
+        float m[2] = {-INFINITY, -INFINITY}, lsum[2] = {0.f, 0.f};
+        for (int i = pc.k0; i < pc.k1; ++i, ++n) {
+          const int buf = n & 1;
+          ok = __all_sync(0xffffffffu, lwait(&sb.s_full[buf], n >> 1, abort_flag, a.err));
+          if (!ok) break;
           tc5::fence_after();
-          const uint32_t ts = tbase + 256u + 64u * (uint32_t)buf + lanes + 32u * (uint32_t)part;
-          tc5::ld16(ts, sv);
-          tc5::ld16(ts + 16, sv + 16);
+          float sv[2][16];  // [row][key 8 (c / 2) + 2 (l % 4) + c % 2]
+          tc5::ld_rows16(tbase + 256u + 64u * (uint32_t)buf + lanes, sv[0], sv[1]);
           tc5::wait_ld();
           tc5::fence_before();
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sb.s_free[buf]);
-        if (mine) {
-          const int o0 = i * kKeys + 32 * part;
-          const int ea = se - o0, wb = wb0 - o0, we = we0 - o0;
-          if (!__all_sync(0xffffffffu, wb <= 0 && we >= 31)) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sb.s_free[buf]);
+          const int o0 = i * kKeys;
+          if (!__all_sync(0xffffffffu, max(wb0[0], wb0[1]) <= o0 && min(we0[0], we0[1]) >= o0 + kKeys - 1)) {
 #pragma unroll
-            for (int c = 0; c < 32; ++c)
-              if (!(c < ea || (c >= wb && c <= we))) sv[c] = -INFINITY;
-          }
-          float mt[4];
+            for (int x = 0; x < 2; ++x) {
+              const int oc = o0 + 2 * (lane & 3);
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            mt[q] = tc5::max3(tc5::max3(sv[8 * q], sv[8 * q + 1], sv[8 * q + 2]),
-                              tc5::max3(sv[8 * q + 3], sv[8 * q + 4], sv[8 * q + 5]), fmaxf(sv[8 * q + 6], sv[8 * q + 7]));
-          mx = fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3])) * sl2;  // scale > 0
-        }
-        float a0 = -INFINITY, a1 = -INFINITY, b0 = -INFINITY, b1 = -INFINITY;
-        if (!(ok = exchange(mx, a0, a1, b0, b1))) break;
-        // rows lane and lane + 32: a new maximum once it is 8 above the old (P <= 256 fits bf16's exponent with ease)
-        float f0 = 1.f, f1 = 1.f;
-        const float x0 = fmaxf(a0, b0), x1 = R > 32 ? fmaxf(a1, b1) : -INFINITY;
-        if ((R >= 32 || lane < R) && x0 > m0 + 8.f) {
-          if (m0 > -INFINITY) f0 = exp2f(m0 - x0);
-          m0 = x0;
-        }
-        if (R > 32 && x1 > m1 + 8.f) {
-          if (m1 > -INFINITY) f1 = exp2f(m1 - x1);
-          m1 = x1;
-        }
-        const bool rescale = __any_sync(0xffffffffu, f0 != 1.f || f1 != 1.f);
-        uint4 w[4];
-        if (mine) {
-          const float mlo = __shfl_sync(0xffffffffu, m0, row & 31), mhi = R > 32 ? __shfl_sync(0xffffffffu, m1, row & 31) : 0.f;
-          const float flo = __shfl_sync(0xffffffffu, f0, row & 31), fhi = R > 32 ? __shfl_sync(0xffffffffu, f1, row & 31) : 1.f;
-          const float m = row < 32 ? mlo : mhi, f = row < 32 ? flo : fhi;
-          const float msub = m == -INFINITY ? 0.f : m;  // nothing kept yet: 2^-inf = 0
-          float ps0 = 0.f, ps1 = 0.f;
-          uint32_t* wp = reinterpret_cast<uint32_t*>(w);
-#pragma unroll
-          for (int x = 0; x < 16; ++x) {
-            float y0, y1;
-            tc5::fma2(y0, y1, sv[2 * x], sv[2 * x + 1], sl2, -msub);
-            const float p0 = tc5::ex2(y0), p1 = tc5::ex2(y1);
-            wp[x] = pack_bf16(p0, p1);
-            tc5::add2(ps0, ps1, p0, p1);
-          }
-          lsum = lsum * f + (ps0 + ps1);
-        }
-        if (n > 0) {  // O += P X of the block before is done: P's buffer is free and O may be scaled
-          ok = __all_sync(0xffffffffu, lwait(&sb.pv_done, n - 1, abort_flag, a.err));
-          if (!ok) break;
-        }
-        if (active) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            *reinterpret_cast<uint4*>(sP + row * 128 + (((4 * part + q) ^ (row & 7)) << 4)) = w[q];
-        }
-        if (rescale) {  // only rows with a maximum before, so O holds blocks of this piece
-          tc5::fence_after();
-#pragma unroll
-          for (int jj = 0; jj < 2; ++jj)
-#pragma unroll
-            for (int c0 = 0; c0 < R; c0 += 16) {
-              const uint32_t to = tbase + lanes + (uint32_t)((2 * part + jj) * R + c0);
-              float ov[16];
-              tc5::ld16(to, ov);
-              tc5::wait_ld();
-#pragma unroll
-              for (int c = 0; c < 16; ++c) ov[c] *= __shfl_sync(0xffffffffu, c0 + c < 32 ? f0 : f1, (c0 + c) & 31);
-              tc5::st16(to, ov);
+              for (int c = 0; c < 16; ++c) {
+                const int o = oc + 8 * (c / 2) + c % 2;
+                if (!(o < se[x] || (o >= wb0[x] && o <= we0[x]))) sv[x][c] = -INFINITY;
+              }
             }
-          tc5::wait_st();
+          }
+          float f[2];
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float* v = sv[x];
+            float mx = tc5::max3(tc5::max3(tc5::max3(v[0], v[1], v[2]), tc5::max3(v[3], v[4], v[5]), v[15]),
+                                 tc5::max3(v[6], v[7], v[8]),
+                                 tc5::max3(tc5::max3(v[9], v[10], v[11]), tc5::max3(v[12], v[13], v[14]), -INFINITY));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2)) * sl2;  // scale > 0
+            // a new maximum once it is 8 above the old (P <= 256 fits bf16's exponent with ease)
+            f[x] = 1.f;
+            if (mx > m[x] + 8.f) {
+              if (m[x] > -INFINITY) f[x] = exp2f(m[x] - mx);
+              m[x] = mx;
+            }
+            if ((lane & 3) == 0) sb.factor[buf][row0 + 8 * x] = f[x];
+          }
+          __threadfence_block();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sb.f_full[buf]);
+          uint32_t w[2][8];
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float msub = m[x] == -INFINITY ? 0.f : m[x];  // nothing kept yet: 2^-inf = 0
+            float ps0 = 0.f, ps1 = 0.f;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              float y0, y1;
+              tc5::fma2(y0, y1, sv[x][2 * q], sv[x][2 * q + 1], sl2, -msub);
+              const float p0 = tc5::ex2(y0), p1 = tc5::ex2(y1);
+              w[x][q] = pack_bf16(p0, p1);
+              tc5::add2(ps0, ps1, p0, p1);
+            }
+            lsum[x] = lsum[x] * f[x] + (ps0 + ps1);
+          }
+          if (n > 0) {  // O += P X of the block before is done: P's buffer is free
+            ok = __all_sync(0xffffffffu, lwait(&sb.pv_done, n - 1, abort_flag, a.err));
+            if (!ok) break;
+          }
+          {
+            const int rw = 16 * quad + (lane & 15);
+            const uint32_t dst = smem_u32(sP) + rw * 128;
+#pragma unroll
+            for (int q = 0; q < 8; q += 2)
+              tc5::store_8x8x4(dst + (((q + (lane >> 4)) ^ (rw & 7)) << 4), w[0][q], w[1][q], w[0][q + 1], w[1][q + 1]);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sb.p_full);
         }
-        fence_proxy_async_smem();
+        if (!ok) break;
+        ok = __all_sync(0xffffffffu, lwait(&sb.pv_done, n - 1, abort_flag, a.err));
+        if (!ok) break;
+        tc5::fence_after();
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          lsum[x] += __shfl_xor_sync(0xffffffffu, lsum[x], 1);
+          lsum[x] += __shfl_xor_sync(0xffffffffu, lsum[x], 2);
+          if ((lane & 3) == 0) sb.row_m[row0 + 8 * x] = m[x], sb.row_l[row0 + 8 * x] = lsum[x];
+        }
+        __threadfence_block();
         tc5::fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sb.p_full);
+        if (lane == 0) mbar_arrive(&sb.sums);
+      } else if (warp >= kScale0) {
+        for (int i = pc.k0; i < pc.k1; ++i, ++n) {
+          const int buf = n & 1;
+          ok = __all_sync(0xffffffffu, lwait(&sb.f_full[buf], n >> 1, abort_flag, a.err));
+          if (!ok) break;
+          volatile float* fac = sb.factor[buf];
+          const float f0 = lane < R ? fac[lane] : 1.f, f1 = R > 32 ? fac[lane + 32] : 1.f;
+          if (__any_sync(0xffffffffu, f0 != 1.f || f1 != 1.f)) {
+            // Only rows with a maximum before, so O holds blocks of this piece. P(n - 1) has been
+            // written, so the product before that is done and the parity is unambiguous.
+            ok = __all_sync(0xffffffffu, lwait(&sb.pv_done, n - 1, abort_flag, a.err));
+            if (!ok) break;
+            tc5::fence_after();
+#pragma unroll
+            for (int c0 = 0; c0 < 4 * R; c0 += 16) {
+              float ov[16];
+              tc5::ld16(tbase + lanes + (uint32_t)c0, ov);
+              tc5::wait_ld();
+#pragma unroll
+              for (int c = 0; c < 16; ++c) ov[c] *= fac[c0 % R + c];
+              tc5::st16(tbase + lanes + (uint32_t)c0, ov);
+            }
+            tc5::wait_st();
+            tc5::fence_before();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sb.p_full);
+        }
+        if (!ok) break;
       }
+      // ---- the piece's end, once its last product is done: O / l to the output, or (m, l, O) to a partial
+      ok = __all_sync(0xffffffffu, lwait(&sb.sums, np, abort_flag, a.err));
       if (!ok) break;
-      // ---- the piece's end: O / l to the output, or (m, l, O) to a partial
-      ok = __all_sync(0xffffffffu, lwait(&sb.pv_done, n - 1, abort_flag, a.err));
-      if (!ok) break;
+      ++np;
       tc5::fence_after();
-      float a0 = 0.f, a1 = 0.f, b0 = 0.f, b1 = 0.f;
-      if (!(ok = exchange(lsum, a0, a1, b0, b1))) break;
-      const float l0 = a0 + b0, l1 = a1 + b1;
+      volatile float *rm = sb.row_m, *rl = sb.row_l;
+      const float l0 = lane < R ? rl[lane] : 0.f, l1 = R > 32 ? rl[lane + 32] : 0.f;
       const bool whole = pc.k0 == 0 && pc.k1 == pc.it.nblk;
       const int rows = min(R, pc.r.ql * a.H - pc.tile * R);
       // a NaN sum is the answer of a NaN score; a sum of zero belongs to a row that attends nothing here
@@ -680,8 +699,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
       const int slot = pc.left + (pc.k1 - pc.k0) == r1 - r0 ? 0 : 1;
       const size_t pbase = (size_t)(2 * cta + slot) * R;
       if (!whole && warp == kSoft0) {
-        if (lane < R) a.part_ml[pbase + lane] = make_float2(m0, l0);
-        if (R > 32) a.part_ml[pbase + lane + 32] = make_float2(m1, l1);
+        if (lane < R) a.part_ml[pbase + lane] = make_float2(rm[lane], l0);
+        if (R > 32) a.part_ml[pbase + lane + 32] = make_float2(rm[lane + 32], l1);
         if (pc.k0 == 0) {
           // this group starts the item: the last group is the first whose range reaches the item's end
           const long long e = r1 - pc.left - (pc.k1 - pc.k0) + pc.it.nblk;
