@@ -58,10 +58,9 @@ constexpr uint32_t kGroup = 8 * kW * 2;            // 8 keys
 constexpr uint32_t kStage = kKeys / 8 * kGroup;    // 73,728
 constexpr int kStages = 2;
 constexpr int kThreads = 512;
-constexpr int kCopiers = 4;  // warps 12..15
-constexpr int kAhead = 2;  // blocks prefetched to L2 beyond the stages
+constexpr int kCopiers = 4, kCopy0 = 12;
+constexpr int kNamed = 4;   // blocks named ahead of their loads; those beyond the stages are on their way to L2
 constexpr int kSoft0 = 4, kScale0 = 8, kScaleWarps = 4;  // softmax: R / 16 of 4 warps
-constexpr int kCopy0 = 12;
 constexpr int kMaxR = 64;
 constexpr int kMaxGs = 8;
 constexpr uint64_t kWaitNs = 2000000000ull;
@@ -88,9 +87,9 @@ struct LatArgs {
 
 struct LatBars {
   uint64_t q_full, q_free;
-  uint64_t job[2], job_free[2];  // loader -> copiers: a block with scattered rows; its slots have been read
-  uint64_t full[kStages];   // loader (boxes' bytes) and copiers -> issuers: the block is in
-  uint64_t empty[kStages];  // O issuer (commit) -> loader
+  uint64_t named[kNamed], named_free[kNamed];  // namer -> loaders: a block's slots; they have been read
+  uint64_t full[kStages];   // loaders (boxes' bytes, and each when its rows are in) -> issuers: the block is in
+  uint64_t empty[kStages];  // O issuer (commit) -> loaders
   uint64_t s_full[2], s_free[2];
   uint64_t f_full[2];       // softmax -> scaling warps: the block's factors are in ``factor``
   uint64_t p_full, pv_done, o_free, drain, sums;
@@ -99,8 +98,8 @@ struct LatBars {
   int late;  // raised by a wait for copies in flight that ran out
   int b0;
   long long off0;
-  int slots[2][kKeys];  // of a job
-  int2 job_of[2];       // {groups that come as boxes, stage}; x = -1: no more jobs
+  int slots[kNamed][kKeys];  // -1: nothing to read
+  int boxes[kNamed];         // mask of groups that come as boxes; -1: no more blocks
   float factor[2][kMaxR];   // of a block: what O's rows have to be scaled by before it
   float row_m[kMaxR], row_l[kMaxR];  // of a piece
 };
@@ -198,6 +197,11 @@ __device__ __forceinline__ int slot_of(const LatArgs& a, int row, int t) {
   return (page << a.page_shift) + (t & (a.T.page_size - 1));
 }
 
+// ``bytes`` from ``src`` on, both multiples of 16, on their way to L2.
+__device__ __forceinline__ void bulk_prefetch(const void* src, uint32_t bytes, uint64_t policy) {
+  asm volatile("cp.async.bulk.prefetch.L2.global.L2::cache_hint [%0], %1, %2;" ::"l"(src), "r"(bytes), "l"(policy) : "memory");
+}
+
 __device__ __forceinline__ long long range_start(long long total, int g, int NG) { return NG ? total * g / NG : 0; }
 
 template <int R>
@@ -225,10 +229,12 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
     mbar_init(&sb.q_full, 1);
     mbar_init(&sb.q_free, 1);
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&sb.job[s], 1);
-      mbar_init(&sb.job_free[s], kCopiers);
-      mbar_init(&sb.full[s], 1 + kCopiers);
+      mbar_init(&sb.full[s], 2 * kCopiers);
       mbar_init(&sb.empty[s], 1);
+    }
+    for (int x = 0; x < kNamed; ++x) {
+      mbar_init(&sb.named[x], 1);
+      mbar_init(&sb.named_free[x], kCopiers);
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&sb.s_full[x], 1);
@@ -307,63 +313,71 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
   const uint64_t once = policy_evict_first();
 
   if (warp == 0) {
-    // ======================= loader ===========================================
-    int n = 0, np = 0;  // blocks and pieces issued
+    // ======================= namer ============================================
+    // Finds each block's rows. Lane l has the slots of keys 2 l and 2 l + 1 (group gi
+    // is lanes 4 gi .. 4 gi + 3).
+    int n = 0;
     bool ok = true;
     // Eight consecutive positions of a block table whose pages hold a multiple
     // of eight, from a multiple of eight on, lie in one page: one table read.
     const bool paged8 = !a.T.raw && (a.T.page_size & 7) == 0;
-    // Blocks are resolved up to 1 + kAhead before they are loaded. Lane l holds
-    // the slots of keys 2 l and 2 l + 1 (group gi is lanes 4 gi .. 4 gi + 3; -1:
-    // nothing to read) and the mask of groups that are eight consecutive slots.
-    struct Named {
-      int s0, s1;
-      unsigned boxes;
-    } ring[2 + kAhead];
-    int named = 0, jobs = 0;
-    Pieces<R> pr = pc;
-    bool more = pr.next();
-    int ri = more ? pr.k0 : 0;
-    auto name_next = [&](Named& w) {
-      const Span u = pr.it.u;
-      const int o0 = ri * kKeys, nk = pr.it.n_keys;
-      w.boxes = 0;
-      if (paged8) {
-        const int og = o0 + 8 * lane;
-        int s = -1;
-        if (lane < 8 && og + 7 < nk && (og >= u.se || og + 7 < u.se)) {
-          const int p = span_pos(u, og);
-          if ((p & 7) == 0) s = slot_of(a, pr.r.row, p);
+    while (ok && pc.next()) {
+      const Span u = pc.it.u;
+      const int nk = pc.it.n_keys;
+      for (int i = pc.k0; i < pc.k1; ++i, ++n) {
+        const int o0 = i * kKeys, x = n % kNamed;
+        int s0 = -1, s1 = -1;
+        unsigned boxes = 0;
+        if (paged8) {
+          const int og = o0 + 8 * lane;
+          int s = -1;
+          if (lane < 8 && og + 7 < nk && (og >= u.se || og + 7 < u.se)) {
+            const int p = span_pos(u, og);
+            if ((p & 7) == 0) s = slot_of(a, pc.r.row, p);
+          }
+          boxes = __ballot_sync(0xffffffffu, s >= 0) & 0xFFu;
+          s0 = __shfl_sync(0xffffffffu, s, lane >> 2) + 2 * (lane & 3);
+          s1 = s0 + 1;
         }
-        w.boxes = __ballot_sync(0xffffffffu, s >= 0) & 0xFFu;
-        w.s0 = __shfl_sync(0xffffffffu, s, lane >> 2) + 2 * (lane & 3);
-        w.s1 = w.s0 + 1;
-      }
-      if (w.boxes != 0xFFu) {
-        int sl[2];
+        if (boxes != 0xFFu) {
+          int sl[2];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int o = o0 + 2 * lane + k;
-          sl[k] = o < nk ? slot_of(a, pr.r.row, span_pos(u, o)) : -1;
+          for (int k = 0; k < 2; ++k) {
+            const int o = o0 + 2 * lane + k;
+            sl[k] = o < nk ? slot_of(a, pc.r.row, span_pos(u, o)) : -1;
+          }
+          s0 = sl[0];
+          s1 = sl[1];
+          const int g0 = __shfl_sync(0xffffffffu, sl[0], lane & ~3);
+          const unsigned run = __ballot_sync(0xffffffffu, sl[0] >= 0 && sl[1] == sl[0] + 1 && sl[0] == g0 + 2 * (lane & 3));
+          boxes = 0;
+#pragma unroll
+          for (int gi = 0; gi < 8; ++gi)
+            if (((run >> (4 * gi)) & 0xFu) == 0xFu) boxes |= 1u << gi;
         }
-        w.s0 = sl[0];
-        w.s1 = sl[1];
-        const int g0 = __shfl_sync(0xffffffffu, sl[0], lane & ~3);
-        const unsigned run = __ballot_sync(0xffffffffu, sl[0] >= 0 && sl[1] == sl[0] + 1 && sl[0] == g0 + 2 * (lane & 3));
-        w.boxes = 0;
-#pragma unroll
-        for (int gi = 0; gi < 8; ++gi)
-          if (((run >> (4 * gi)) & 0xFu) == 0xFu) w.boxes |= 1u << gi;
+        if (n >= kNamed) ok = __all_sync(0xffffffffu, lwait(&sb.named_free[x], n / kNamed - 1, abort_flag, a.err));
+        if (!ok) break;
+        sb.slots[x][2 * lane] = s0;
+        sb.slots[x][2 * lane + 1] = s1;
+        if (lane == 0) sb.boxes[x] = (int)boxes;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sb.named[x]);
+        // one CTA of a group prefetches the boxes (scattered rows gained nothing: 2.8 us a block without, 3.1 with)
+        if (n >= kStages && t == 0 && boxes == 0xFFu && (lane & 3) == 0)
+          bulk_prefetch(a.rows + (size_t)s0 * (kW * 2), kGroup, once);
+        __syncwarp();
       }
-      if (++ri == pr.k1) {
-        more = pr.next();
-        ri = more ? pr.k0 : 0;
-      }
-    };
-    if (more) {  // the first block's rows before all else
-      name_next(ring[0]);
-      named = 1;
     }
+    if (ok && n >= kNamed) ok = __all_sync(0xffffffffu, lwait(&sb.named_free[n % kNamed], n / kNamed - 1, abort_flag, a.err));
+    if (lane == 0) {
+      sb.boxes[n % kNamed] = -1;
+      mbar_arrive(&sb.named[n % kNamed]);
+    }
+    __syncwarp();
+  } else if (warp == 3) {
+    // ======================= Q ================================================
+    int np = 0;
+    bool ok = true;
     while (ok && pc.next()) {
       if (np > 0) ok = __all_sync(0xffffffffu, lwait(&sb.q_free, np - 1, abort_flag, a.err));
       if (!ok) break;
@@ -373,108 +387,78 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
       }
       ++np;
       __syncwarp();
-      for (int i = pc.k0; i < pc.k1; ++i, ++n) {
-        const int st = n % kStages;
-        const Named w = ring[0];
-#pragma unroll
-        for (int x = 0; x < 1 + kAhead; ++x) ring[x] = ring[x + 1];
-        if (n >= kStages) ok = __all_sync(0xffffffffu, lwait(&sb.empty[st], n / kStages - 1, abort_flag, a.err));
-        if (!ok) break;
-        const int s8 = __shfl_sync(0xffffffffu, w.s0, (4 * lane) & 31);  // lane gi < 8: group gi's first slot
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&sb.full[st], (uint32_t)__popc(w.boxes) * kGroup);
-          if (w.boxes == 0xFFu) mbar_arrive_n(&sb.full[st], kCopiers);  // nothing for the copiers
-        }
-        __syncwarp();
-        if (w.boxes != 0xFFu) {
-          const int js = jobs & 1;
-          if (jobs >= 2) ok = __all_sync(0xffffffffu, lwait(&sb.job_free[js], (jobs >> 1) - 1, abort_flag, a.err));
-          if (!ok) break;
-          sb.slots[js][2 * lane] = w.s0;
-          sb.slots[js][2 * lane + 1] = w.s1;
-          if (lane == 0) sb.job_of[js] = make_int2((int)w.boxes, st);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sb.job[js]);
-          ++jobs;
-        }
-        if (lane < 8 && ((w.boxes >> lane) & 1))
-          tc5::tma_4d(sX + st * kStage + lane * kGroup, &a.box, 0, s8, 0, a.layer, &sb.full[st], once);
-        __syncwarp();
-        // name the blocks ahead: the next one only while the first is on its way
-        while (more && named < n + 2 + (n ? kAhead : 0)) {
-          Named v;
-          name_next(v);
-#pragma unroll
-          for (int x = 0; x < 1 + kAhead; ++x)
-            if (x == named - n - 1) ring[x] = v;
-          // one CTA of a group prefetches the boxes (scattered rows gained nothing: 2.8 us a block without, 3.1 with)
-          if (named >= kStages && t == 0 && v.boxes == 0xFFu) {
-            const int p8 = __shfl_sync(0xffffffffu, v.s0, (4 * lane) & 31);
-            if (lane < 8) tc5::tma_prefetch_4d(&a.box, 0, p8, 0, a.layer, once);
-          }
-          ++named;
-        }
-      }
     }
     // what was issued has landed (bounded) before the shared memory goes away
     if (np > 0) lwait(&sb.q_full, np - 1, &sb.late, a.err);
-    for (int s = 0; s < kStages; ++s) {
-      const int cnt = (n + kStages - 1 - s) / kStages;
-      if (cnt > 0) lwait(&sb.full[s], cnt - 1, &sb.late, a.err);
-    }
     __syncwarp();
-    if (jobs >= 2) lwait(&sb.job_free[jobs & 1], (jobs >> 1) - 1, &sb.late, a.err);
-    if (lane == 0) {
-      sb.job_of[jobs & 1] = make_int2(-1, 0);
-      mbar_arrive(&sb.job[jobs & 1]);
-    }
-    __syncwarp();
-  } else if (warp == 3) {
-    // idle: the softmax warps start on a multiple of four
   } else if (warp >= kCopy0) {
-    // ======================= copiers of scattered rows =========================
-    // Each takes two groups of a block. Copies still on their way when the next
-    // job is there are handed on after that one's are issued, else at once.
+    // ======================= loaders ==========================================
+    // Each loads two groups of a block: as boxes, or row by row. Copies still on
+    // their way when the next block can be loaded are handed on after that one's are
+    // issued, else at once.
+    const int w = warp - kCopy0;
+    int n = 0;
+    bool ok = true;
     int before = -1;  // the stage whose copies are on their way
-    for (int k = 0;; ++k) {
-      const int js = k & 1;
-      if (before >= 0 && !__all_sync(0xffffffffu, mbar_test_wait(&sb.job[js], (uint32_t)(k >> 1) & 1))) {
+    auto hand_on = [&]() {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sb.full[before]);
+      before = -1;
+    };
+    for (;; ++n) {
+      const int x = n % kNamed, st = n % kStages;
+      if (before >= 0 &&
+          !__all_sync(0xffffffffu, mbar_test_wait(&sb.named[x], (uint32_t)(n / kNamed) & 1) &&
+                                       (n < kStages || mbar_test_wait(&sb.empty[st], (uint32_t)(n / kStages - 1) & 1)))) {
         cp_async_wait<0>();
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sb.full[before]);
-        before = -1;
+        hand_on();
       }
-      if (!__all_sync(0xffffffffu, lwait(&sb.job[js], k >> 1, abort_flag, a.err))) break;
-      volatile int2* job = &sb.job_of[js];
-      const int boxes = job->x, st = job->y;
-      if (boxes >= 0) {
+      ok = __all_sync(0xffffffffu, lwait(&sb.named[x], n / kNamed, abort_flag, a.err));
+      if (!ok) break;
+      int boxes = *(volatile int*)&sb.boxes[x];
+      if (boxes < 0) break;
+      boxes = (boxes >> (2 * w)) & 3;
+      const int s8 = *(volatile int*)&sb.slots[x][16 * w + 8 * (lane & 1)];  // lane < 2: the group's first slot
+      if (n >= kStages) ok = __all_sync(0xffffffffu, lwait(&sb.empty[st], n / kStages - 1, abort_flag, a.err));
+      if (!ok) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&sb.full[st], (uint32_t)__popc(boxes) * kGroup);
+        if (boxes == 3) mbar_arrive(&sb.full[st]);
+      }
+      __syncwarp();
+      if (lane < 2 && ((boxes >> lane) & 1))
+        tc5::tma_4d(sX + st * kStage + (2 * w + lane) * kGroup, &a.box, 0, s8, 0, a.layer, &sb.full[st], once);
+      if (boxes != 3) {
         // a copy is 4 rows x 128 bytes a warp: lane = 8 row + 16-byte piece
         const int piece = lane & 7;
-        for (int h = 4 * (warp - kCopy0); h < 4 * (warp - kCopy0) + 4; ++h) {
-          if ((boxes >> (h >> 1)) & 1) continue;
+        for (int h = 4 * w; h < 4 * w + 4; ++h) {
+          if ((boxes >> ((h >> 1) & 1)) & 1) continue;
           const int key = 4 * h + (lane >> 3), r = key & 7;
-          const int s = *(volatile int*)&sb.slots[js][key];
+          const int s = *(volatile int*)&sb.slots[x][key];
           const char* src = a.rows + (size_t)max(s, 0) * (kW * 2) + piece * 16;
           const uint32_t dst = smem_u32(sX) + st * kStage + (uint32_t)(key >> 3) * kGroup + r * 128 + ((piece ^ r) << 4);
 #pragma unroll
           for (int c = 0; c < kChunks; ++c) tc5::cp_async16(dst + c * 1024, src + c * 128, s < 0 ? 0 : 16, once);
         }
         cp_async_commit();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sb.job_free[js]);
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sb.named_free[x]);
       if (before >= 0) {
-        if (boxes >= 0) cp_async_wait<1>();
+        if (boxes != 3) cp_async_wait<1>();
         else cp_async_wait<0>();
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sb.full[before]);
+        hand_on();
       }
-      if (boxes < 0) break;
-      before = st;
+      if (boxes != 3) before = st;
     }
     cp_async_wait<0>();
+    if (before >= 0) hand_on();
+    // the boxes too have landed (bounded) before the shared memory goes away
+    for (int s = 0; s < kStages; ++s) {
+      const int cnt = (n + kStages - 1 - s) / kStages;
+      if (cnt > 0) lwait(&sb.full[s], cnt - 1, &sb.late, a.err);
+    }
     __syncwarp();
   } else if (warp == 1) {
     // ======================= S issuer =========================================
@@ -530,8 +514,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
             for (int j = 0; j < 4; ++j)
               tc5::mma_ss(tbase + (uint32_t)(j * R), dx + (uint64_t)((2 * j * 1024 + ks * 2 * kGroup) >> 4),
                           dp + (uint64_t)((ks * 32) >> 4), id, (first && ks == 0) ? 0u : 1u);
-          tc5::commit(&sb.pv_done);
           tc5::commit(&sb.empty[st]);
+          tc5::commit(&sb.pv_done);
         }
         __syncwarp();
       }
