@@ -478,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
         const uint64_t dx = tc5::desc(smem_u32(sX) + st * kStage, 16, kGroup);
         const uint32_t ts = tbase + 256u + 64u * (uint32_t)buf;
         if (tc5::elect_one()) {
-#pragma unroll
+#pragma unroll 4
           for (int kk = 0; kk < kW / 16; ++kk)
             tc5::mma_ss(ts, dq + (uint64_t)(((kk >> 2) * R * 128 + (kk & 3) * 32) >> 4),
                         dx + (uint64_t)(((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), id, kk > 0);
@@ -508,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
         const uint64_t dx = tc5::desc(smem_u32(sX) + st * kStage, 1024, kGroup);
         const uint32_t first = i == pc.k0;
         if (tc5::elect_one()) {
-#pragma unroll
+#pragma unroll 1
           for (int ks = 0; ks < kKeys / 16; ++ks)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -651,7 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
             ok = __all_sync(0xffffffffu, lwait(&sb.pv_done, n - 1, abort_flag, a.err));
             if (!ok) break;
             tc5::fence_after();
-#pragma unroll
+#pragma unroll 1
             for (int c0 = 0; c0 < 4 * R; c0 += 16) {
               float ov[16];
               tc5::ld16(tbase + lanes + (uint32_t)c0, ov);
@@ -695,10 +695,10 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
       }
       __nv_bfloat16* orow = a.out + ((size_t)pc.b * a.C * a.H + (size_t)pc.tile * R) * kDc;
       float* prow = a.part_o + pbase * kDc;
-#pragma unroll
+#pragma unroll 1
       for (int jj = 0; jj < 2; ++jj) {
         const int d = 128 * (2 * part + jj) + 32 * quad + lane;
-#pragma unroll
+#pragma unroll 1
         for (int c0 = 0; c0 < R; c0 += 16) {
           float ov[16];
           tc5::ld16(tbase + lanes + (uint32_t)((2 * part + jj) * R + c0), ov);
