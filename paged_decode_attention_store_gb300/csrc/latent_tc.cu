@@ -59,6 +59,7 @@ constexpr uint32_t kStage = kKeys / 8 * kGroup;    // 73,728
 constexpr int kStages = 2;
 constexpr int kThreads = 512;
 constexpr int kCopiers = 4, kCopy0 = 12;
+constexpr int kPieces = 4;  // pieces published ahead
 constexpr int kNamed = 4;   // blocks named ahead of their loads; those beyond the stages are on their way to L2
 constexpr int kSoft0 = 4, kScale0 = 8, kScaleWarps = 4;  // softmax: R / 16 of 4 warps
 constexpr int kMaxR = 64;
@@ -85,7 +86,17 @@ struct LatArgs {
   int32_t* err;
 };
 
+// A piece of the range as the namer hands it on: key blocks k0 .. k1 - 1 of a tile; k1 0: no more.
+struct Piece {
+  int k0, k1;
+  int out_row, rows;    // first row of q and out, rows
+  int r0, p0;           // the tile's first row in its request; the request's first query position
+  Span u;
+  int slot, last;       // -1: the whole item; else the partial's slot and, if the item starts here, its last group
+};
+
 struct LatBars {
+  uint64_t piece_full[kPieces], piece_free[kPieces];
   uint64_t q_full, q_free;
   uint64_t named[kNamed], named_free[kNamed];  // namer -> loaders: a block's slots; they have been read
   uint64_t full[kStages];   // loaders (boxes' bytes, and each when its rows are in) -> issuers: the block is in
@@ -100,6 +111,7 @@ struct LatBars {
   long long off0;
   int slots[kNamed][kKeys];  // -1: nothing to read
   int boxes[kNamed];         // mask of groups that come as boxes; -1: no more blocks
+  Piece piece[kPieces];
   float factor[2][kMaxR];   // of a block: what O's rows have to be scaled by before it
   float row_m[kMaxR], row_l[kMaxR];  // of a piece
 };
@@ -143,7 +155,7 @@ __device__ __forceinline__ int groups_of(const LatArgs& a, int ql) {
   return ql * a.H <= per ? (ql > 0) : (ql * a.H + per - 1) / per;
 }
 
-// Walks the pieces of this CTA's range; every role walks the same ones.
+// Walks the pieces of this CTA's range.
 template <int R>
 struct Pieces {
   const LatArgs& a;
@@ -232,6 +244,10 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
       mbar_init(&sb.full[s], 2 * kCopiers);
       mbar_init(&sb.empty[s], 1);
     }
+    for (int x = 0; x < kPieces; ++x) {
+      mbar_init(&sb.piece_full[x], 1);
+      mbar_init(&sb.piece_free[x], kCopy0 - 1);  // warps 1 .. 11
+    }
     for (int x = 0; x < kNamed; ++x) {
       mbar_init(&sb.named[x], 1);
       mbar_init(&sb.named_free[x], kCopiers);
@@ -306,7 +322,15 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
   }
   // TMEM: O^T at columns 0 .. 4 R - 1 (block j of 128 entries at j R), S buffers at 256 and 320
   const uint32_t tbase = sb.taddr;
-  Pieces<R> pc(a, t, sb.b0, sb.off0, r1 - r0);
+  // This CTA's k-th piece; false: none, or a wait gave up.
+  auto get_piece = [&](int k, Piece& pc) -> bool {
+    const int x = k % kPieces;
+    if (!__all_sync(0xffffffffu, lwait(&sb.piece_full[x], k / kPieces, abort_flag, a.err))) return false;
+    pc = sb.piece[x];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sb.piece_free[x]);
+    return pc.k1 > 0;
+  };
   // Rows leave L2 first: a step streams more of them than it holds, and would
   // put out the kernels' own code, which then comes from memory again, a line at a
   // time (64 requests of 2304 rows, 32 heads: 52.5 us without, 47.1 with).
@@ -316,14 +340,49 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
     // ======================= namer ============================================
     // Finds each block's rows. Lane l has the slots of keys 2 l and 2 l + 1 (group gi
     // is lanes 4 gi .. 4 gi + 3).
-    int n = 0;
+    int n = 0, np = 0;
     bool ok = true;
+    Pieces<R> pc(a, t, sb.b0, sb.off0, r1 - r0);
+    auto publish = [&](const Piece& v) {
+      const int x = np % kPieces;
+      if (np >= kPieces) ok = __all_sync(0xffffffffu, lwait(&sb.piece_free[x], np / kPieces - 1, abort_flag, a.err));
+      if (!ok) return;
+      if (lane == 0) {
+        sb.piece[x] = v;
+        mbar_arrive(&sb.piece_full[x]);  // release: the piece is seen by who waits
+      }
+      ++np;
+      __syncwarp();
+    };
     // Eight consecutive positions of a block table whose pages hold a multiple
     // of eight, from a multiple of eight on, lie in one page: one table read.
     const bool paged8 = !a.T.raw && (a.T.page_size & 7) == 0;
     while (ok && pc.next()) {
       const Span u = pc.it.u;
       const int nk = pc.it.n_keys;
+      auto describe = [&]() {
+        Piece v;
+        v.k0 = pc.k0;
+        v.k1 = pc.k1;
+        v.out_row = pc.b * a.C * a.H + pc.tile * R;
+        v.rows = min(R, pc.r.ql * a.H - pc.tile * R);
+        v.r0 = pc.tile * R;
+        v.p0 = pc.r.L - pc.r.ql;
+        v.u = u;
+        v.slot = v.last = -1;
+        if (pc.k0 > 0 || pc.k1 < pc.it.nblk) {
+          // the range's first piece is the one that starts where the range does
+          v.slot = pc.left + (pc.k1 - pc.k0) == r1 - r0 ? 0 : 1;
+          if (pc.k0 == 0) {
+            // this group starts the item: the last group is the first whose range reaches the item's end
+            const long long e = r1 - pc.left - (pc.k1 - pc.k0) + pc.it.nblk;
+            v.last = g;
+            while (range_start(total, v.last + 1, ng_used) < e) ++v.last;
+          }
+        }
+        publish(v);
+      };
+      if (n) describe();
       for (int i = pc.k0; i < pc.k1; ++i, ++n) {
         const int o0 = i * kKeys, x = n % kNamed;
         int s0 = -1, s1 = -1;
@@ -366,6 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
         if (n >= kStages && t == 0 && boxes == 0xFFu && (lane & 3) == 0)
           bulk_prefetch(a.rows + (size_t)s0 * (kW * 2), kGroup, once);
         __syncwarp();
+        if (n == 0) describe();  // behind the first block, whose rows are what takes longest
       }
     }
     if (ok && n >= kNamed) ok = __all_sync(0xffffffffu, lwait(&sb.named_free[n % kNamed], n / kNamed - 1, abort_flag, a.err));
@@ -374,16 +434,20 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
       mbar_arrive(&sb.named[n % kNamed]);
     }
     __syncwarp();
+    Piece none;
+    none.k1 = 0;
+    if (ok) publish(none);
   } else if (warp == 3) {
     // ======================= Q ================================================
     int np = 0;
     bool ok = true;
-    while (ok && pc.next()) {
+    Piece pc;
+    while (ok && get_piece(np, pc)) {
       if (np > 0) ok = __all_sync(0xffffffffu, lwait(&sb.q_free, np - 1, abort_flag, a.err));
       if (!ok) break;
       if (lane == 0) {
         mbar_arrive_expect_tx(&sb.q_full, (uint32_t)R * kW * 2);
-        tc5::tma_3d(sQ, &a.qmap, 0, pc.b * a.C * a.H + pc.tile * R, 0, &sb.q_full);
+        tc5::tma_3d(sQ, &a.qmap, 0, pc.out_row, 0, &sb.q_full);
       }
       ++np;
       __syncwarp();
@@ -466,7 +530,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
     bool ok = true;
     constexpr uint32_t id = tc5::idesc(64, kKeys, 0, 0);
     const uint64_t dq = tc5::desc(smem_u32(sQ), 16, 1024);
-    while (ok && pc.next()) {
+    Piece pc;
+    while (ok && get_piece(np, pc)) {
       ok = __all_sync(0xffffffffu, lwait(&sb.q_full, np, abort_flag, a.err));
       ++np;
       for (int i = pc.k0; ok && i < pc.k1; ++i, ++n) {
@@ -496,7 +561,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
     bool ok = true;
     constexpr uint32_t id = tc5::idesc(128, R, 1, 0);
     const uint64_t dp = tc5::desc(smem_u32(sP), 16, 1024);
-    while (ok && pc.next()) {
+    Piece pc;
+    while (ok && get_piece(np, pc)) {
       if (np > 0) ok = __all_sync(0xffffffffu, lwait(&sb.o_free, np - 1, abort_flag, a.err));
       ++np;
       for (int i = pc.k0; ok && i < pc.k1; ++i, ++n) {
@@ -536,16 +602,17 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
     int n = 0, np = 0;  // blocks, pieces
     int4 merge = make_int4(-1, 0, 0, 0);
     bool ok = true;
-    while (ok && pc.next()) {
+    Piece pc;
+    while (ok && get_piece(np, pc)) {
       if (softmax) {
         // row x attends key offsets [0, se) and [wb, we] of the item's span
         int se[2], wb0[2], we0[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const int rr = pc.tile * R + row0 + 8 * x;
-          const bool rv = rr < pc.r.ql * a.H;
-          const int p = pc.r.L - pc.r.ql + (a.C == 1 ? 0 : rr / a.H);
-          const Span u = pc.it.u, sr = attend_span(p + 1, a.window, a.sinks);
+          const int rr = row0 + 8 * x;
+          const bool rv = rr < pc.rows;
+          const int p = pc.p0 + (a.C == 1 ? 0 : (pc.r0 + rr) / a.H);
+          const Span u = pc.u, sr = attend_span(p + 1, a.window, a.sinks);
           se[x] = rv ? sr.se : 0;
           wb0[x] = rv ? u.se + (sr.lo - u.lo) : 1 << 30;
           we0[x] = rv ? u.se + (p - u.lo) : -1;
@@ -675,25 +742,17 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
       tc5::fence_after();
       volatile float *rm = sb.row_m, *rl = sb.row_l;
       const float l0 = lane < R ? rl[lane] : 0.f, l1 = R > 32 ? rl[lane + 32] : 0.f;
-      const bool whole = pc.k0 == 0 && pc.k1 == pc.it.nblk;
-      const int rows = min(R, pc.r.ql * a.H - pc.tile * R);
+      const bool whole = pc.slot < 0;
+      const int rows = pc.rows;
       // a NaN sum is the answer of a NaN score; a sum of zero belongs to a row that attends nothing here
       const float i0 = !whole ? 1.f : l0 == 0.f ? 0.f : 1.f / l0, i1 = !whole ? 1.f : l1 == 0.f ? 0.f : 1.f / l1;
-      // the range's first piece is the one that starts where the range does
-      const int slot = pc.left + (pc.k1 - pc.k0) == r1 - r0 ? 0 : 1;
-      const size_t pbase = (size_t)(2 * cta + slot) * R;
+      const size_t pbase = (size_t)(2 * cta + max(pc.slot, 0)) * R;
       if (!whole && warp == kSoft0) {
         if (lane < R) a.part_ml[pbase + lane] = make_float2(rm[lane], l0);
         if (R > 32) a.part_ml[pbase + lane + 32] = make_float2(rm[lane + 32], l1);
-        if (pc.k0 == 0) {
-          // this group starts the item: the last group is the first whose range reaches the item's end
-          const long long e = r1 - pc.left - (pc.k1 - pc.k0) + pc.it.nblk;
-          int gl = g;
-          while (range_start(total, gl + 1, ng_used) < e) ++gl;
-          merge = make_int4(pc.b * a.C * a.H + pc.tile * R, rows, gl, slot);
-        }
+        if (pc.last >= 0) merge = make_int4(pc.out_row, rows, pc.last, pc.slot);
       }
-      __nv_bfloat16* orow = a.out + ((size_t)pc.b * a.C * a.H + (size_t)pc.tile * R) * kDc;
+      __nv_bfloat16* orow = a.out + (size_t)pc.out_row * kDc;
       float* prow = a.part_o + pbase * kDc;
 #pragma unroll 1
       for (int jj = 0; jj < 2; ++jj) {
