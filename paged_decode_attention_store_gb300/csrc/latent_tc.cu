@@ -60,7 +60,7 @@ constexpr int kStages = 2;
 constexpr int kThreads = 512;
 constexpr int kCopiers = 4, kCopy0 = 12;
 constexpr int kPieces = 4;  // pieces published ahead
-constexpr int kNamed = 4;   // blocks named ahead of their loads; those beyond the stages are on their way to L2
+constexpr int kNamed = 4;   // blocks named ahead of their loads
 constexpr int kSoft0 = 4, kScale0 = 8, kScaleWarps = 4;  // softmax: R / 16 of 4 warps
 constexpr int kMaxR = 64;
 constexpr int kMaxGs = 8;
@@ -207,11 +207,6 @@ __device__ __forceinline__ int slot_of(const LatArgs& a, int row, int t) {
     return -1;
   }
   return (page << a.page_shift) + (t & (a.T.page_size - 1));
-}
-
-// ``bytes`` from ``src`` on, both multiples of 16, on their way to L2.
-__device__ __forceinline__ void bulk_prefetch(const void* src, uint32_t bytes, uint64_t policy) {
-  asm volatile("cp.async.bulk.prefetch.L2.global.L2::cache_hint [%0], %1, %2;" ::"l"(src), "r"(bytes), "l"(policy) : "memory");
 }
 
 __device__ __forceinline__ long long range_start(long long total, int g, int NG) { return NG ? total * g / NG : 0; }
@@ -421,10 +416,6 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
         if (lane == 0) sb.boxes[x] = (int)boxes;
         __syncwarp();
         if (lane == 0) mbar_arrive(&sb.named[x]);
-        // one CTA of a group prefetches the boxes (scattered rows gained nothing: 2.8 us a block without, 3.1 with)
-        if (n >= kStages && t == 0 && boxes == 0xFFu && (lane & 3) == 0)
-          bulk_prefetch(a.rows + (size_t)s0 * (kW * 2), kGroup, once);
-        __syncwarp();
         if (n == 0) describe();  // behind the first block, whose rows are what takes longest
       }
     }
