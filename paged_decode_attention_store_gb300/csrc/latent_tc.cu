@@ -113,7 +113,7 @@ struct LatBars {
   int boxes[kNamed];         // mask of groups that come as boxes; -1: no more blocks
   Piece piece[kPieces];
   float factor[2][kMaxR];   // of a block: what O's rows have to be scaled by before it
-  float row_m[kMaxR], row_l[kMaxR];  // of a piece
+  float row_m[kMaxR], row_l[kMaxR], row_i[kMaxR];  // of a piece: maximum, sum, what O is multiplied by
 };
 
 __device__ __forceinline__ bool lwait(uint64_t* bar, int k, volatile int* abort_flag, int32_t* err) {
@@ -690,7 +690,12 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
         for (int x = 0; x < 2; ++x) {
           lsum[x] += __shfl_xor_sync(0xffffffffu, lsum[x], 1);
           lsum[x] += __shfl_xor_sync(0xffffffffu, lsum[x], 2);
-          if ((lane & 3) == 0) sb.row_m[row0 + 8 * x] = m[x], sb.row_l[row0 + 8 * x] = lsum[x];
+          if ((lane & 3) == 0) {
+            sb.row_m[row0 + 8 * x] = m[x];
+            sb.row_l[row0 + 8 * x] = lsum[x];
+            // a NaN sum is the answer of a NaN score; a sum of zero belongs to a row that attends nothing here
+            sb.row_i[row0 + 8 * x] = lsum[x] == 0.f ? 0.f : 1.f / lsum[x];
+          }
         }
         __threadfence_block();
         tc5::fence_before();
@@ -731,16 +736,12 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
       if (!ok) break;
       ++np;
       tc5::fence_after();
-      volatile float *rm = sb.row_m, *rl = sb.row_l;
-      const float l0 = lane < R ? rl[lane] : 0.f, l1 = R > 32 ? rl[lane + 32] : 0.f;
       const bool whole = pc.slot < 0;
       const int rows = pc.rows;
-      // a NaN sum is the answer of a NaN score; a sum of zero belongs to a row that attends nothing here
-      const float i0 = !whole ? 1.f : l0 == 0.f ? 0.f : 1.f / l0, i1 = !whole ? 1.f : l1 == 0.f ? 0.f : 1.f / l1;
       const size_t pbase = (size_t)(2 * cta + max(pc.slot, 0)) * R;
       if (!whole && warp == kSoft0) {
-        if (lane < R) a.part_ml[pbase + lane] = make_float2(rm[lane], l0);
-        if (R > 32) a.part_ml[pbase + lane + 32] = make_float2(rm[lane + 32], l1);
+        for (int r = lane; r < R; r += 32)
+          a.part_ml[pbase + r] = make_float2(*(volatile float*)&sb.row_m[r], *(volatile float*)&sb.row_l[r]);
         if (pc.last >= 0) merge = make_int4(pc.out_row, rows, pc.last, pc.slot);
       }
       __nv_bfloat16* orow = a.out + (size_t)pc.out_row * kDc;
@@ -755,7 +756,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
           tc5::wait_ld();
           if (whole) {
 #pragma unroll
-            for (int c = 0; c < 16; ++c) ov[c] *= __shfl_sync(0xffffffffu, c0 + c < 32 ? i0 : i1, (c0 + c) & 31);
+            for (int c = 0; c < 16; ++c) ov[c] *= *(volatile float*)&sb.row_i[c0 + c];
             // lanes 2 i and 2 i + 1 trade columns, so that each stores two entries of one row
 #pragma unroll
             for (int c = 0; c < 16; c += 2) {
