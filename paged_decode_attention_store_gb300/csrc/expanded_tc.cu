@@ -49,11 +49,11 @@ constexpr int kDn = 128, kDr = 64, kDv = 128;
 constexpr uint32_t kChunk = 16384;  // 128 rows x 128 B
 constexpr int kQChunks = (kDn + kDr) / 64, kVChunks = kDv / 64;
 constexpr int kKS = 2, kVS = 2;
-constexpr int kThreads = 768;
-constexpr int kSoft0 = 4, kSoftWarps = 16, kParts = 4;
-constexpr int kEpi0 = 20, kEpiWarps = 4;
+constexpr int kThreads = 512;
+constexpr int kSoft0 = 4, kSoftWarps = 8;
+constexpr int kEpi0 = 12, kEpiWarps = 4;
 constexpr uint64_t kWaitNs = 2000000000ull;
-constexpr size_t kSmem = (kQChunks + kKS * kQChunks + kVS * kVChunks) * kChunk;
+constexpr size_t kSmem = (kQChunks + kKS * kQChunks + kVS * kVChunks + 1) * kChunk;
 
 struct ExpArgs {
   CUtensorMap qmap;   // (d, head, token), box (64, 1, 128); likewise the others
@@ -80,15 +80,13 @@ struct ExpBars {
   uint64_t s_full[2], s_free[2], p_full[2], pv_done[2];
   uint64_t l_full[2], l_free[2];    // a tile's row sums are in ``sums``; read
   uint64_t o_free, drain, vtail;
-  uint64_t xbar[4];
   uint64_t answer;                  // cluster launch control -> loader
   uint64_t tile_full[2], tile_free[2];
   uint32_t taddr;
   int abort, late;
   alignas(16) uint32_t next[4];     // cluster launch control's answer
   Tile tile[2];
-  float xch[2][kParts][kTile];
-  float sums[2][kParts][kTile];
+  float sums[2][kTile];
 };
 
 __device__ __forceinline__ bool ewait(uint64_t* bar, int k, volatile int* abort_flag, int32_t* err) {
@@ -148,6 +146,7 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_tc_kernel(const __grid_c
   unsigned char* sQ = exp_raw;
   unsigned char* sK = sQ + kQChunks * kChunk;
   unsigned char* sV = sK + kKS * kQChunks * kChunk;
+  unsigned char* sO = sV + kVS * kVChunks * kChunk;  // 64 entries of the tile's rows of O
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   volatile int* abort_flag = &sb.abort;
   int32_t* err = a.c.err;
@@ -173,7 +172,6 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_tc_kernel(const __grid_c
       mbar_init(&sb.l_full[x], kSoftWarps);
       mbar_init(&sb.l_free[x], kEpiWarps);
     }
-    for (int q = 0; q < 4; ++q) mbar_init(&sb.xbar[q], kParts);
     mbar_init(&sb.answer, 1);
     mbar_init(&sb.o_free, kEpiWarps);
     mbar_init(&sb.drain, 2);
@@ -382,90 +380,89 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_tc_kernel(const __grid_c
     __syncwarp();
   } else if (warp < kEpi0) {
     // ======================= softmax ==========================================
-    const int quad = warp & 3, part = (warp - kSoft0) >> 2;
-    const int row = 32 * quad + lane;
-    const uint32_t lanes = (uint32_t)(32 * quad) << 16;
-    const uint32_t tOp = tO + lanes + 32u * (uint32_t)part;
+    // A warp has 16 query rows: lane l the rows row0 = l / 4 and row0 + 8 of its 16, of
+    // every eight keys the two from 2 (l % 4) on, so that a row lies in four lanes.
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3) + 16 * ((warp - kSoft0) >> 2)) << 16;
+    const int row0 = (int)(lanes >> 16) + (lane >> 2);
     const float sl2 = a.scale_log2;
-    int n = 0, nx = 0;
+    int n = 0;
     bool ok = true;
-    // the maximum of the row's four parts, through shared memory
-    auto exchange = [&](float v, float& res) -> bool {
-      volatile float* xc = &sb.xch[nx & 1][0][0];
-      xc[part * kTile + row] = v;
-      __threadfence_block();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sb.xbar[quad]);
-      const bool done = __all_sync(0xffffffffu, ewait(&sb.xbar[quad], nx, abort_flag, err));
-      ++nx;
-      if (!done) return false;
-      const float v0 = xc[row], v1 = xc[kTile + row], v2 = xc[2 * kTile + row], v3 = xc[3 * kTile + row];
-      res = fmaxf(fmaxf(v0, v1), fmaxf(v2, v3));
-      return true;
-    };
     Tile t;
     for (int k = 0; ok && get_tile(k, t); ++k) {
-      const int p = row < t.jn ? t.shift + row : -1;  // last key the row attends
-      float m = -INFINITY, lsum = 0.f;
+      // last key a row attends
+      const int p0 = row0 < t.jn ? t.shift + row0 : -1, p1 = row0 + 8 < t.jn ? t.shift + row0 + 8 : -1;
+      float m[2] = {-INFINITY, -INFINITY}, lsum[2] = {0.f, 0.f};
       for (int i = 0; i < t.nblk; ++i, ++n) {
         const int buf = n & 1;
         ok = __all_sync(0xffffffffu, ewait(&sb.s_full[buf], n >> 1, abort_flag, err));
         if (!ok) break;
         tc5::fence_after();
-        float sv[32];
-        const uint32_t ts = tbase + 128u * (uint32_t)buf + lanes + 32u * (uint32_t)part;
-        tc5::ld16(ts, sv);
-        tc5::ld16(ts + 16, sv + 16);
+        float sv[2][32];
+        const uint32_t ts = tbase + 128u * (uint32_t)buf + lanes;
+        tc5::ld_rows16(ts, sv[0], sv[1]);
+        tc5::ld_rows16(ts + 64, sv[0] + 16, sv[1] + 16);
         tc5::wait_ld();
         tc5::fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sb.s_free[buf]);
-        const int we = p - (i * kKeys + 32 * part);  // the last of this thread's keys that the row attends
-        if (!__all_sync(0xffffffffu, we >= 31)) {
+        const int kb = i * kKeys + 2 * (lane & 3);
+        if (!__all_sync(0xffffffffu, min(p0, p1) >= i * kKeys + kKeys - 1)) {
 #pragma unroll
-          for (int c = 0; c < 32; ++c)
-            if (c > we) sv[c] = -INFINITY;
+          for (int c = 0; c < 32; ++c) {
+            const int key = kb + 8 * (c / 2) + c % 2;
+            if (key > p0) sv[0][c] = -INFINITY;
+            if (key > p1) sv[1][c] = -INFINITY;
+          }
         }
-        float mt[4];
+        float f[2], msub[2];
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          mt[q] = tc5::max3(tc5::max3(sv[8 * q], sv[8 * q + 1], sv[8 * q + 2]),
-                            tc5::max3(sv[8 * q + 3], sv[8 * q + 4], sv[8 * q + 5]), fmaxf(sv[8 * q + 6], sv[8 * q + 7]));
-        float mx;
-        if (!(ok = exchange(fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3])) * sl2, mx))) break;  // scale > 0
-        const bool grow = mx > m + 8.f;
-        const float f = grow && m > -INFINITY ? exp2f(m - mx) : 1.f;
-        if (grow) m = mx;
-        const float msub = m == -INFINITY ? 0.f : m;
-        uint32_t w[16];
-        float ps0 = 0.f, ps1 = 0.f;
+        for (int x = 0; x < 2; ++x) {
+          float mt[4];
 #pragma unroll
-        for (int x = 0; x < 16; ++x) {
-          float y0, y1;
-          tc5::fma2(y0, y1, sv[2 * x], sv[2 * x + 1], sl2, -msub);
-          const float p0 = tc5::ex2(y0), p1 = tc5::ex2(y1);
-          w[x] = pack_bf16(p0, p1);
-          tc5::add2(ps0, ps1, p0, p1);
+          for (int q = 0; q < 4; ++q) {
+            const float* v = sv[x] + 8 * q;
+            mt[q] = tc5::max3(tc5::max3(v[0], v[1], v[2]), tc5::max3(v[3], v[4], v[5]), fmaxf(v[6], v[7]));
+          }
+          float mx = fmaxf(tc5::max3(mt[0], mt[1], mt[2]), mt[3]);
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2)) * sl2;  // scale > 0
+          const bool grow = mx > m[x] + 8.f;
+          f[x] = grow && m[x] > -INFINITY ? exp2f(m[x] - mx) : 1.f;
+          if (grow) m[x] = mx;
+          msub[x] = m[x] == -INFINITY ? 0.f : m[x];
+        }
+        uint32_t w[32];  // as the 16-lane store takes them: row row0, row row0 + 8 of every eight keys
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          float ps0 = 0.f, ps1 = 0.f;
+#pragma unroll
+          for (int q = 0; q < 16; ++q) {
+            float y0, y1;
+            tc5::fma2(y0, y1, sv[x][2 * q], sv[x][2 * q + 1], sl2, -msub[x]);
+            const float e0 = tc5::ex2(y0), e1 = tc5::ex2(y1);
+            w[2 * q + x] = pack_bf16(e0, e1);
+            tc5::add2(ps0, ps1, e0, e1);
+          }
+          lsum[x] = lsum[x] * f[x] + (ps0 + ps1);
         }
         if (n >= 2) {  // P buffer buf is free once O += P V of the block two before is done
           ok = __all_sync(0xffffffffu, ewait(&sb.pv_done[buf], (n >> 1) - 1, abort_flag, err));
           if (!ok) break;
           tc5::fence_after();
         }
-        tc5::st16(tbase + 384u + 64u * (uint32_t)buf + lanes + 16u * (uint32_t)part, w);
-        lsum = lsum * f + (ps0 + ps1);
-        if (__any_sync(0xffffffffu, f != 1.f)) {  // O holds this tile's blocks before i: scale them once they are in
+        tc5::st_pairs16(tbase + 384u + 64u * (uint32_t)buf + lanes, w);
+        if (__any_sync(0xffffffffu, f[0] != 1.f || f[1] != 1.f)) {  // O holds this tile's blocks before i: scale them once they are in
           ok = __all_sync(0xffffffffu, ewait(&sb.pv_done[buf ^ 1], (n - 1) >> 1, abort_flag, err));
           if (!ok) break;
           tc5::fence_after();
-#pragma unroll
-          for (int x = 0; x < 32; x += 16) {
-            float ov[16];
-            tc5::ld16(tOp + x, ov);
+#pragma unroll 1
+          for (int c0 = 0; c0 < kDv; c0 += 64) {
+            float o0[16], o1[16];
+            tc5::ld_rows16(tO + lanes + (uint32_t)c0, o0, o1);
             tc5::wait_ld();
 #pragma unroll
-            for (int c = 0; c < 16; ++c) ov[c] *= f;
-            tc5::st16(tOp + x, ov);
+            for (int c = 0; c < 16; ++c) o0[c] *= f[0], o1[c] *= f[1];
+            tc5::st_rows16(tO + lanes + (uint32_t)c0, o0, o1);
           }
         }
         tc5::wait_st();
@@ -474,10 +471,15 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_tc_kernel(const __grid_c
         if (lane == 0) mbar_arrive(&sb.p_full[buf]);
       }
       if (!ok) break;
-      // ---- the row sum's part goes to the epilogue
+      // ---- the row sums go to the epilogue
       if (k >= 2) ok = __all_sync(0xffffffffu, ewait(&sb.l_free[k & 1], (k >> 1) - 1, abort_flag, err));
       if (!ok) break;
-      sb.sums[k & 1][part][row] = lsum;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        lsum[x] += __shfl_xor_sync(0xffffffffu, lsum[x], 1);
+        lsum[x] += __shfl_xor_sync(0xffffffffu, lsum[x], 2);
+        if ((lane & 3) == 0) sb.sums[k & 1][row0 + 8 * x] = lsum[x];
+      }
       __threadfence_block();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sb.l_full[k & 1]);
@@ -497,8 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_tc_kernel(const __grid_c
       if (ok) ok = __all_sync(0xffffffffu, ewait(&sb.pv_done[(n - 1) & 1], (n - 1) >> 1, abort_flag, err));
       if (!ok) break;
       tc5::fence_after();
-      volatile float* sm = &sb.sums[k & 1][0][0];
-      const float tot = (sm[row] + sm[kTile + row]) + (sm[2 * kTile + row] + sm[3 * kTile + row]);
+      const float tot = *(volatile float*)&sb.sums[k & 1][row];
       // a NaN sum is the answer of a NaN score
       const float inv = tot == 0.f ? 0.f : 1.f / tot;
       // all of O to registers, packed, before the stores: the next tile's first product waits for it
@@ -517,10 +518,27 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_tc_kernel(const __grid_c
         mbar_arrive(&sb.o_free);
         mbar_arrive(&sb.l_free[k & 1]);
       }
-      if (row < t.jn) {
-        uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.c.out) + ((size_t)(t.q0 + row) * a.c.H + t.h) * kDv);
+      // To rows of 16-byte pieces side by side through shared memory, 64 entries at a
+      // time: stored row by row from here, 32 lines an instruction, they held up the
+      // softmax warps' accesses for 1.3 us a tile.
+      unsigned char* so = sO + quad * 32 * 128;
 #pragma unroll
-        for (int q = 0; q < kDv / 8; ++q) o[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+      for (int c = 0; c < 2; ++c) {
+        __syncwarp();
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const int x = 32 * c + 4 * q;
+          *reinterpret_cast<uint4*>(so + lane * 128 + ((q ^ (lane & 7)) << 4)) = make_uint4(w[x], w[x + 1], w[x + 2], w[x + 3]);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int y = 0; y < 8; ++y) {
+          const int r = 4 * y + (lane >> 3), q = lane & 7;
+          const uint4 v = *reinterpret_cast<const uint4*>(so + r * 128 + ((q ^ (r & 7)) << 4));
+          if (32 * quad + r < t.jn)
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.c.out) +
+                                      ((size_t)(t.q0 + 32 * quad + r) * a.c.H + t.h) * kDv + 64 * c + 8 * q) = v;
+        }
       }
     }
   }

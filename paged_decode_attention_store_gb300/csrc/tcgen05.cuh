@@ -110,6 +110,39 @@ __device__ __forceinline__ void ld_rows16(uint32_t taddr, float* a, float* b) {
   }
 }
 
+// The converse of ld_rows16.
+__device__ __forceinline__ void st_rows16(uint32_t taddr, const float* a, const float* b) {
+  uint32_t r[32];
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    r[4 * q] = __float_as_uint(a[2 * q]);
+    r[4 * q + 1] = __float_as_uint(a[2 * q + 1]);
+    r[4 * q + 2] = __float_as_uint(b[2 * q]);
+    r[4 * q + 3] = __float_as_uint(b[2 * q + 1]);
+  }
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+
+// 64 columns of 16 lanes, each two 16-bit entries: thread l has column l % 4 of
+// every four, of lane l / 4 (even words) and l / 4 + 8 (odd words).
+__device__ __forceinline__ void st_pairs16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+
 // Four 8 x 8 tiles of 16-bit entries to shared memory: lane l names the address of
 // row l % 8 of tile l / 8 and holds entries 2 (l % 4), + 1 of row l / 4 of each tile.
 __device__ __forceinline__ void store_8x8x4(uint32_t dst, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
