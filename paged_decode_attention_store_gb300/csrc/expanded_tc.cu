@@ -8,14 +8,15 @@
 //
 // What bounds it: the tensor cores, and the loads that feed them. A tile is 128
 // query rows of one (request, head); a block of 128 keys is 12 MMAs (M 128 N 128 K
-// 16, 33 ns each) for S and 8 for O, 0.65 us, on 80 KB of K and V. Measured: 1.02 us
-// a block (0.75 us from S to P, and S(i + 2) waits about 1 us for its K once S(i) has
-// freed the stage), 2.5 us a tile besides; 1082 TFLOP/s on 512-token chunks of 16
-// requests with 32 heads.
+// 16, 33 ns each) for S and 8 for O, 0.65 us, on 80 KB of K and V. Measured: 0.9 us a
+// block (48 KB of K take 1.0 us to come in and S 0.5 us on two stages; the softmax
+// takes 0.75 us), 1.5 us more a tile (its Q waits for the tile before); 164 us,
+// 1167 TFLOP/s on 512-token chunks of 16 requests with 32 heads.
 //  * TMEM: two S buffers of 128 columns, O (128), two P buffers (64 columns, two
 //    bf16 keys each). S(i + 1) and O += P(i) V(i) run while the softmax works:
-//    four threads a row, 32 keys each, online softmax in log2 units, O rescaled
-//    only when a row's maximum grows by more than 8 (P <= 256).
+//    four threads a row in one warp, 32 keys each (the 16-lane forms of the TMEM
+//    load and store), online softmax in log2 units, O rescaled only when a row's
+//    maximum grows by more than 8 (P <= 256).
 //  * Operands by TMA under the 128-byte swizzle: 64-entry chunks of 128 rows (16
 //    KB): Q 3, K 3 a stage (two of k, one of r), V 2 a stage, two stages each.
 //    Rows past the request's last key are another request's: their scores are
@@ -27,16 +28,20 @@
 //    block and epilogue run, and the SMs stay balanced over prompts of any
 //    lengths. The loader alone decodes indices, skips tiles without rows and hands
 //    the others on through shared memory: code that runs once a tile comes from
-//    the instruction cache's slow levels (decoded by every warp: 182 us where this
-//    takes 177). Tiles of a request and head are adjacent, the longest first.
+//    the instruction cache's slow levels. Tiles of a request and head are adjacent,
+//    the longest first.
+//  * The epilogue has warps of its own and turns its rows around in shared memory:
+//    stores of 32 rows an instruction held up the softmax for 1.3 us a tile (173 us
+//    where this takes 164).
 //  * Slower on the same chunk: two tiles a CTA sharing K and V (half the loads, but
-//    no second S buffer; 229 us), Q in TMEM with P over S (S(i + 2) waits for O += P
-//    V(i); 221), most of Q in TMEM with one P buffer (192), K's barriers per chunk
-//    with an epilogue by warps of its own (203), softmax warps in two groups that
-//    take blocks in turn (258 and 273).
+//    no second S buffer), Q in TMEM with P over S (S(i + 2) waits for O += P V(i)),
+//    most of Q in TMEM with one P buffer, a barrier per chunk of K (176 us), softmax
+//    warps in two groups that take blocks in turn, a part of the exponentials as a
+//    polynomial (172 us before the epilogue's change, 171 without).
 //
-// Warps: 0 takes tiles and loads K and Q, 1 issues S, 2 issues O, 3 loads V, 4..19
-// run the softmax and the epilogue (TMEM lane quadrant = warp % 4).
+// Warps: 0 takes tiles and loads K and Q, 1 issues S, 2 issues O, 3 loads V, 4..11
+// run the softmax (16 rows each: quadrant warp % 4, its lower or upper half), 12..15
+// the epilogue.
 #include "expanded.cuh"
 #include "tcgen05.cuh"
 

@@ -19,17 +19,26 @@
 //    rows on the lanes would take all 512 columns at M 64) and a small R costs
 //    little. X's block in shared memory serves both products: K-major for S,
 //    MN-major for O^T. 16 MMAs of 20-25 ns, 0.32-0.40 us a block.
-//  * Together at most 0.98 us of tensor time per block, against 1.65 us that one
-//    SM's share of the memory rate takes for the block's 72 KB: one CTA an SM
-//    with two block stages keeps the memory busy.
+//  * What an SM does in a block at R = 64: 1.0 us of tensor time; 316 KB through
+//    shared memory (the two products' operands and the block's arrival), 1.3 us at
+//    128 bytes a clock; 1.65 us as its share of the memory rate when no other CTA
+//    reads the same rows. Measured: 1.65 us a block in either case. Two block stages
+//    are all that fits beside Q (227 KB), so a block's way (load 1.0 us, S 0.75,
+//    softmax 0.5, O 0.5, two at a time) shows; finer stages of 32 keys or of a third
+//    of the entries gave nothing back (more, smaller boxes and products).
 //  * Layout of a block: groups of 8 keys, 9 KB each: 9 chunks of 64 entries, 8
 //    rows of 128 bytes (128-byte swizzle). Eight consecutive slots are one TMA
-//    box; any other rows are copied by a warp with 16-byte asynchronous
-//    copies (TMA row gathers of 4 x 128 bytes took 41 ns each, 6 us a block),
-//    rows past the span and behind holes as zeros: whatever lies in their place
-//    must not meet a weight of 0.
-//  * The loader names the rows of two blocks beyond those in shared memory and
-//    prefetches them to L2, which so serves as the deeper part of the ring.
+//    box; any other rows are copied with 16-byte asynchronous copies (TMA row
+//    gathers of 4 x 128 bytes took 41 ns each, 6 us a block), rows past the span
+//    and behind holes as zeros: whatever lies in their place must not meet a
+//    weight of 0.
+//  * One warp finds the rows of up to four blocks ahead, four warps load them, two
+//    groups of a block each: one warp for both was 6 % slower on a long context.
+//    Prefetches to L2 beyond the two stages only got in the way of other CTAs' loads
+//    (64 requests of about 2300 rows, 32 heads: 49.4 us with, 45.7 without).
+//  * Code that runs once a block or a piece comes from the instruction cache's slow
+//    levels: the walk over pieces lives in one warp, which hands them on, and the
+//    issue and epilogue loops stay rolled (10 % at the smallest calls).
 //
 // Work split. A request's tiles are taken ``Gs`` at a time; such an item's key
 // blocks, the union over its tiles, laid end to end over all items, are divided
@@ -38,9 +47,15 @@
 // all but one). A cut item leaves fp32 partials (slot 0: the group's first
 // piece, slot 1: its last), which latent_combine_kernel joins in block order.
 //
-// Warps: 0 loads, 1 issues S, 2 issues O, 3 copies scattered rows, 4..11 run the
-// softmax (quadrant = warp % 4, two warps a quadrant, 32 keys of a block each)
-// and the epilogue.
+// Warps: 0 walks the pieces and names the blocks' rows, 1 issues S, 2 issues O, 3
+// loads Q, 4..7 run the softmax (16 query rows each, TMEM quadrant = warp % 4),
+// 8..11 scale O when a row's maximum grew, 4..11 together the epilogue, 12..15 load
+// the blocks.
+// Measured (bf16, the whole call with its combine): one request of 777 rows, 16
+// heads: 11.8 us (two launches); 64 requests of 512 .. 4096 rows, 32 heads: 45.7 us,
+// 4.1 TB/s (7 us until the first block is in, 5 us of combine); 32 requests of 8192 ..
+// 32768 scattered rows, 128 heads: 237 us, 727 TFLOP/s; four tokens of 64 heads on 64
+// requests: 130 us, 655 TFLOP/s.
 // Every wait is bounded (2 s), as in the other kernels.
 #include <cstring>
 
