@@ -41,21 +41,22 @@
 //    issue and epilogue loops stay rolled (10 % at the smallest calls).
 //
 // Work split. A request's tiles are taken ``Gs`` at a time; such an item's key
-// blocks, the union over its tiles, laid end to end over all items, are divided
-// evenly over NG = SMs / Gs groups of Gs CTAs: CTA (g, t) walks group g's range
-// for tile t, the CTAs of a group read the same rows at the same time (L2 serves
-// all but one). A cut item leaves fp32 partials (slot 0: the group's first
-// piece, slot 1: its last), which latent_combine_kernel joins in block order.
+// blocks, the union over its tiles, laid end to end over all items (with a block or
+// two more for an item's start and end), are divided evenly over NG = SMs / Gs
+// groups of Gs CTAs: CTA (g, t) walks group g's range for tile t, the CTAs of a
+// group read the same rows at the same time (L2 serves all but one). A cut item
+// leaves fp32 partials (slot 0: the group's first piece, slot 1: its last), which
+// latent_combine_kernel joins in block order.
 //
 // Warps: 0 walks the pieces and names the blocks' rows, 1 issues S, 2 issues O, 3
 // loads Q, 4..7 run the softmax (16 query rows each, TMEM quadrant = warp % 4),
 // 8..11 scale O when a row's maximum grew, 4..11 together the epilogue, 12..15 load
 // the blocks.
 // Measured (bf16, the whole call with its combine): one request of 777 rows, 16
-// heads: 11.8 us (two launches); 64 requests of 512 .. 4096 rows, 32 heads: 45.7 us,
+// heads: 12 us (two launches); 64 requests of 512 .. 4096 rows, 32 heads: 45.3 us,
 // 4.1 TB/s (7 us until the first block is in, 5 us of combine); 32 requests of 8192 ..
-// 32768 scattered rows, 128 heads: 237 us, 727 TFLOP/s; four tokens of 64 heads on 64
-// requests: 130 us, 655 TFLOP/s.
+// 32768 scattered rows, 128 heads: 238 us, 724 TFLOP/s; four tokens of 64 heads on 64
+// requests: 128 us, 666 TFLOP/s.
 // Every wait is bounded (2 s), as in the other kernels.
 #include <cstring>
 
@@ -79,6 +80,11 @@ constexpr int kNamed = 4;   // blocks named ahead of their loads
 constexpr int kSoft0 = 4, kScale0 = 8, kScaleWarps = 4;  // softmax: R / 16 of 4 warps
 constexpr int kMaxR = 64;
 constexpr int kMaxGs = 8;
+// Blocks of time that an item's start and end cost: without them ranges of many
+// items end last (four-token verify: 131 us at 0, 128 at 2; 32 heads: 45.7 at 0,
+// 45.2 at 1, 46.1 at 2).
+template <int R>
+constexpr int kOver = R > 32 ? 2 : 1;
 constexpr uint64_t kWaitNs = 2000000000ull;
 
 struct LatArgs {
@@ -175,13 +181,15 @@ template <int R>
 struct Pieces {
   const LatArgs& a;
   int b, tg, ng, t;
-  long long off, left;
+  long long off, left, all;
   LatReq r;
   // the current piece
   LatItem it;
-  int k0, k1, tile;
+  int k0, k1, tile, slot;
+  long long end;  // of its item, from the range's start
+  bool first = true;
   __device__ Pieces(const LatArgs& args, int t_, int b0, long long off0, long long n)
-      : a(args), b(b0), tg(0), t(t_), off(off0), left(n) {
+      : a(args), b(b0), tg(0), t(t_), off(off0), left(n), all(n) {
     r = request(a, b);
     ng = groups_of<R>(a, r.ql);
   }
@@ -195,18 +203,23 @@ struct Pieces {
         tg = 0;
       }
       it = item_of<R>(a, r, tg);
-      if (off >= it.nblk) {  // only before the first piece: the range starts in a later item of the request
-        off -= it.nblk;
+      const int cost = it.nblk + kOver<R>;
+      if (off >= cost) {  // only before the first piece: the range starts in a later item of the request
+        off -= cost;
         ++tg;
         continue;
       }
-      k0 = (int)off;
-      const long long end = off + left;
-      k1 = end < it.nblk ? (int)end : it.nblk;
-      left -= k1 - k0;
+      const long long to = off + left < cost ? off + left : cost;
+      k0 = off > kOver<R> ? (int)off - kOver<R> : 0;
+      k1 = to > kOver<R> ? (int)to - kOver<R> : 0;
+      end = all - left - off + cost;
+      left -= to - off;
       off = 0;
+      slot = first ? 0 : 1;
+      first = false;
       tile = tg * a.Gs + t;
       ++tg;
+      if (k0 == k1) continue;  // only the item's overhead
       if (tile * R < r.ql * a.H) return true;
     }
     return false;
@@ -293,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
     if (b < a.B) {
       const LatReq r = request(a, b);
       const int ng = groups_of<R>(a, r.ql);
-      for (int tg = 0; tg < ng; ++tg) n += item_of<R>(a, r, tg).nblk;
+      for (int tg = 0; tg < ng; ++tg) n += item_of<R>(a, r, tg).nblk + kOver<R>;
     }
     return n;
   };
@@ -304,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
     block_exclusive_scan(blocks_of(c0 + tid), &sum);
     total += sum;
   }
-  // no more groups than blocks: the groups in use are the first ones, none of them empty
+  // no more groups than blocks: the groups in use are the first ones
   const int ng_used = a.NG < total ? a.NG : (int)total;
   const long long r0 = range_start(total, g, ng_used), r1 = range_start(total, g + 1, ng_used);
   const bool busy = g < ng_used;
@@ -381,13 +394,11 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
         v.u = u;
         v.slot = v.last = -1;
         if (pc.k0 > 0 || pc.k1 < pc.it.nblk) {
-          // the range's first piece is the one that starts where the range does
-          v.slot = pc.left + (pc.k1 - pc.k0) == r1 - r0 ? 0 : 1;
+          v.slot = pc.slot;
           if (pc.k0 == 0) {
             // this group starts the item: the last group is the first whose range reaches the item's end
-            const long long e = r1 - pc.left - (pc.k1 - pc.k0) + pc.it.nblk;
             v.last = g;
-            while (range_start(total, v.last + 1, ng_used) < e) ++v.last;
+            while (range_start(total, v.last + 1, ng_used) < r0 + pc.end) ++v.last;
           }
         }
         publish(v);
