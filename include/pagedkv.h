@@ -369,9 +369,9 @@ int rotary_store_latent(const kvp_pool* pool, int layer, const void* q_pe,
  * length, q_lens entry or table row is invalid are zero-filled; an attended
  * table entry that is a hole or out of range is skipped (nothing is read
  * through it) and that request's output is otherwise unspecified. The pool's
- * device must be current. The rows that any of a request's queries attends
- * must be finite for the others; rows past the context and in other pages may
- * hold anything.
+ * device must be current. Rows past the context, out of a query's
+ * window and in other pages may hold anything; a row that is not finite makes
+ * the queries that attend it NaN, and no others.
  * ---------------------------------------------------------------------- */
 int paged_latent_attention_workspace_size(const kvp_pool* pool, int batch,
                                           int chunk, int num_q_heads,

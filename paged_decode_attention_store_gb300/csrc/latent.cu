@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(32 * kLatWarps) latent_general_kernel(const La
     for (int sh = 16; sh > 0; sh >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, sh);
     const float s = dot * a.scale_log2;
     const float mn = fmaxf(m, s);
-    if (mn == -INFINITY) continue;
+    if (s == -INFINITY && m == -INFINITY) continue;  // a NaN goes on
     const float alpha = exp2f(m - mn), p = exp2f(s - mn);
     l = l * alpha + p;
     m = mn;

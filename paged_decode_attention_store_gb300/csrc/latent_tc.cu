@@ -237,6 +237,17 @@ __device__ __forceinline__ int slot_of(const LatArgs& a, int row, int t) {
   return (page << a.page_shift) + (t & (a.T.page_size - 1));
 }
 
+// Zeros in place of a block's rows that hold an infinity or a NaN (a warp; 9 x 128 bytes a row).
+__device__ __noinline__ void clear_not_finite(unsigned char* block, int lane) {
+  for (int key = lane; key < kKeys; key += 32) {
+    unsigned char* row = block + (key >> 3) * kGroup + (key & 7) * 128;
+    uint32_t bad = 0;
+    for (int x = 0; x < kChunks * 32; ++x)
+      bad |= tc5::not_finite2(*reinterpret_cast<const uint32_t*>(row + (x >> 5) * 1024 + (x & 31) * 4));
+    for (int x = 0; bad && x < kChunks * 32; ++x) *reinterpret_cast<uint32_t*>(row + (x >> 5) * 1024 + (x & 31) * 4) = 0u;
+  }
+}
+
 __device__ __forceinline__ long long range_start(long long total, int g, int NG) { return NG ? total * g / NG : 0; }
 
 template <int R>
@@ -648,14 +659,24 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
           if (lane == 0) mbar_arrive(&sb.s_free[buf]);
           const int o0 = i * kKeys;
           if (!__all_sync(0xffffffffu, max(wb0[0], wb0[1]) <= o0 && min(we0[0], we0[1]) >= o0 + kKeys - 1)) {
+            // A weight of 0 would not keep an infinity or a NaN in the latent out of O: where a score is
+            // no number, such rows of the block become zeros. Who attends one has its score already.
+            float odd = 0.f;
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
               const int oc = o0 + 2 * (lane & 3);
 #pragma unroll
               for (int c = 0; c < 16; ++c) {
                 const int o = oc + 8 * (c / 2) + c % 2;
+                odd = fmaf(sv[x][c], 0.f, odd);
                 if (!(o < se[x] || (o >= wb0[x] && o <= we0[x]))) sv[x][c] = -INFINITY;
               }
+            }
+            if (__any_sync(0xffffffffu, odd != odd)) {
+              const int st = n % kStages;
+              ok = __all_sync(0xffffffffu, lwait(&sb.full[st], n / kStages, abort_flag, a.err));
+              if (!ok) break;
+              clear_not_finite(sX + st * kStage, lane);
             }
           }
           float f[2];

@@ -143,6 +143,12 @@ __device__ __forceinline__ void st_pairs16(uint32_t taddr, const uint32_t* r) {
       : "memory");
 }
 
+// Non-zero if one of two bf16 values is an infinity or a NaN (its exponent is all ones).
+__device__ __forceinline__ uint32_t not_finite2(uint32_t w) {
+  const uint32_t e = w & 0x7f807f80u;
+  return (uint32_t)((e & 0xffffu) == 0x7f80u) | (uint32_t)((e >> 16) == 0x7f80u);
+}
+
 // Four 8 x 8 tiles of 16-bit entries to shared memory: lane l names the address of
 // row l % 8 of tile l / 8 and holds entries 2 (l % 4), + 1 of row l / 4 of each tile.
 __device__ __forceinline__ void store_8x8x4(uint32_t dst, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {

@@ -169,6 +169,43 @@ def test_large_scores_and_late_maximum(kb):
     c.verify()
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("window,sinks,at", [(0, 0, -3), (64, 0, -68), (64, 3, -68), (64, 3, -65), (64, 0, -2)])
+@pytest.mark.parametrize("dtype,C,H,dc,dr,part", [("bf16", 5, 40, 512, 64, 7), ("bf16", 5, 8, 512, 64, 575),
+                                                  ("bf16", 20, 64, 512, 64, 511), ("f32", 5, 4, 64, 16, 3)])
+def test_a_row_that_is_not_finite_reaches_only_who_attends_it(kb, bad, window, sinks, at, dtype, C, H, dc, dr, part):
+    """One entry of a row that some queries attend and others do not (later, or out of the window)."""
+    c = Case(kb, dtype, [300, 90, 129], C, H, dc, dr, 16, seed=13)
+    for b, L in enumerate(c.lens):
+        c.buf[0].view(-1, c.W)[c.slots[b][L + at], part] = bad
+    c.run(window, sinks)
+    assert kb.kvp_sync_error(c.pool) == 0
+    seen = [0, 0]
+    for b, L in enumerate(c.lens):
+        for j in range(C):
+            attends = L + at in R.span(L - C + j, window, sinks)
+            seen[attends] += 1
+            if attends:
+                assert not math.isnan(bad) or bool(c.out[b, j].isnan().all())
+            else:
+                R.check(c.out[b, j], *c.want(b, j, C, window, sinks), f"request {b} query {j}")
+    assert seen[0] and (seen[1] or at == -68)  # with 3 sinks and 5 queries that row has left all windows
+
+
+def test_a_query_that_is_not_finite_stays_alone(kb):
+    for bad in (float("nan"), float("inf")):
+        c = Case(kb, "bf16", [300, 90, 6], 5, 40, 512, 64, 16, seed=14)
+        c.q[0, 2, 7, 5] = c.q[1, 4, 39, 575] = c.q[2, 0, 0, 0] = bad
+        c.run()
+        out = c.out.cpu()
+        for b in range(3):
+            for j in range(5):
+                w, bound = c.want(b, j, 5)
+                ok = w.isfinite().all(-1)
+                R.check(out[b, j][ok], w[ok], bound[ok], f"request {b} query {j}")
+                assert int(ok.sum()) == 40 - (j == (2, 4, 0)[b])
+
+
 def test_bad_requests_and_pages(kb):
     """An invalid length or table row zero-fills its request, a hole is skipped, and the others are untouched by it."""
     for dc, dr, H in ((512, 64, 16), (128, 32, 4)):
