@@ -91,6 +91,12 @@ struct ExpBars {
   int abort, late;
   alignas(16) uint32_t next[4];     // cluster launch control's answer
   Tile tile[2];
+  // Values that are not finite (see the epilogue). Rings of four tiles: the V loader is two
+  // blocks ahead of the products, at most three tiles ahead of the epilogue.
+  int careful;                      // such values have been met: V's masked blocks are looked through
+  int looked[4], poison[4];         // per tile: they were; the first key cleared
+  int again, again_bits, epilogues; // tiles to do once more; by their index mod 32; warps' tiles done
+  Tile redo[8];
   float sums[2][kTile];
 };
 
@@ -104,6 +110,21 @@ __device__ __forceinline__ void tma_2d(void* dst, const void* tmap, int c0, int 
           smem_u32(dst)),
       "l"(tmap), "r"(c0), "r"(c1), "r"(smem_u32(bar))
       : "memory");
+}
+
+// Zeros in place of a V stage's rows r0 .. r1 - 1 that hold an infinity or a NaN (a warp);
+// the first of them, or kKeys.
+__device__ __noinline__ int clear_not_finite(unsigned char* stage, int r0, int r1, int lane) {
+  int first = kKeys;
+  for (int r = max(r0, 0) + lane; r < r1; r += 32) {
+    uint32_t bad = 0;
+    for (int x = 0; x < kVChunks * 32; ++x)
+      bad |= tc5::not_finite2(*reinterpret_cast<const uint32_t*>(stage + (x >> 5) * kChunk + r * 128 + (x & 31) * 4));
+    if (!bad) continue;
+    first = min(first, r);
+    for (int x = 0; x < kVChunks * 32; ++x) *reinterpret_cast<uint32_t*>(stage + (x >> 5) * kChunk + r * 128 + (x & 31) * 4) = 0u;
+  }
+  return __reduce_min_sync(0xffffffffu, first);
 }
 
 // Ask for the index of a block that has not started; 16 bytes into ``dst``, counted on ``bar``.
@@ -174,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_tc_kernel(const __grid_c
       mbar_init(&sb.pv_done[x], 1);
       mbar_init(&sb.tile_full[x], 1);
       mbar_init(&sb.tile_free[x], 3 + kSoftWarps + kEpiWarps);
-      mbar_init(&sb.l_full[x], kSoftWarps);
+      mbar_init(&sb.l_full[x], kSoftWarps + 1);
       mbar_init(&sb.l_free[x], kEpiWarps);
     }
     mbar_init(&sb.answer, 1);
@@ -182,6 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_tc_kernel(const __grid_c
     mbar_init(&sb.drain, 2);
     mbar_init(&sb.vtail, 1);
     sb.abort = sb.late = 0;
+    sb.careful = sb.again = sb.again_bits = sb.epilogues = 0;
     fence_mbar_init();
   }
   if (warp == 0) tc5::alloc512(&sb.taddr);
@@ -242,11 +264,29 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_tc_kernel(const __grid_c
       ask();
       t = answer();
     }
-    publish(0, t);
-    for (int k = 0; ok && t.nblk; ++k) {
+    if (t.nblk) publish(0, t);
+    int redo = -1;  // >= 0: the grid is done
+    for (int k = 0; ok; ++k) {
       Tile nx;
       nx.nblk = 0;
-      ask();
+      if (!t.nblk) {
+        if (redo < 0) {  // the tiles that have to be done again are known once all epilogues are through
+          const uint64_t t0 = global_timer_ns();
+          while (*(volatile int*)&sb.epilogues < k * kEpiWarps && !*abort_flag) {
+            if (global_timer_ns() - t0 > kWaitNs) {
+              set_error(err, KVP_ERR_TIMEOUT);
+              sb.abort = 1;
+            }
+            __nanosleep(64);
+          }
+          __syncwarp();
+          redo = 0;
+        }
+        if (redo < min(*(volatile int*)&sb.again, 8)) t = sb.redo[redo++];
+        publish(k, t);
+        if (!t.nblk) break;
+      }
+      if (redo < 0) ask();
       for (int i = 0; ok && i < t.nblk; ++i, ++n) {
         const int st = n % kKS;
         if (n >= kKS) ok = __all_sync(0xffffffffu, ewait(&sb.k_empty[st], n / kKS - 1, abort_flag, err));
@@ -271,8 +311,8 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_tc_kernel(const __grid_c
         }
         // with the stages full, the next tile is decoded and handed on
         if (i == min(kKS, t.nblk) - 1) {
-          nx = answer();
-          publish(k + 1, nx);
+          if (redo < 0) nx = answer();
+          if (nx.nblk) publish(k + 1, nx);
         }
       }
       t = nx;
@@ -291,25 +331,36 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_tc_kernel(const __grid_c
     bool ok = true;
     Tile t;
     for (int k = 0; ok && get_tile(k, t); ++k) {
+      const bool careful = *(volatile int*)&sb.careful;
+      if (lane == 0) {
+        sb.looked[k & 3] = careful;
+        sb.poison[k & 3] = 0x7fffffff;
+      }
+      __syncwarp();
       for (int i = 0; i < t.nblk; ++i, ++n) {
         const int st = n % kVS;
         if (n >= kVS) ok = __all_sync(0xffffffffu, ewait(&sb.v_empty[st], n / kVS - 1, abort_flag, err));
         if (!ok) break;
         unsigned char* dst = sV + st * kVChunks * kChunk;
         const int rows = t.kl - i * kKeys;  // of this request
-        uint64_t* bar = rows < kKeys ? &sb.vtail : &sb.v_full[st];
+        const bool look = careful && min(t.kl, (i + 1) * kKeys) - 1 > t.shift;  // the tile's first row does not attend all
+        uint64_t* bar = rows < kKeys || look ? &sb.vtail : &sb.v_full[st];
         if (lane == 0) {
           mbar_arrive_expect_tx(bar, kVChunks * kChunk);
           for (int c = 0; c < kVChunks; ++c) tc5::tma_3d(dst + c * kChunk, &a.vmap, 64 * c, t.h, t.k0 + i * kKeys, bar);
         }
         __syncwarp();
-        if (rows < kKeys) {
+        if (rows < kKeys || look) {
           ok = __all_sync(0xffffffffu, ewait(&sb.vtail, ntail, abort_flag, err));
           ++ntail;
           if (!ok) break;
           for (int x = rows * 8 + lane; x < kKeys * 8; x += 32)
             for (int c = 0; c < kVChunks; ++c)
               *reinterpret_cast<uint4*>(dst + c * kChunk + x * 16) = make_uint4(0u, 0u, 0u, 0u);
+          if (look) {
+            const int first = clear_not_finite(dst, t.shift + 1 - i * kKeys, min(rows, kKeys), lane);
+            if (lane == 0 && first < kKeys) sb.poison[k & 3] = min(sb.poison[k & 3], i * kKeys + first);
+          }
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(&sb.v_full[st]);
@@ -377,6 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_tc_kernel(const __grid_c
             tc5::mma_ts(tO, tP + (uint32_t)m * 8u, dv + (uint64_t)((m * 2048) >> 4), id, (first && m == 0) ? 0u : 1u);
           tc5::commit(&sb.pv_done[buf]);
           tc5::commit(&sb.v_empty[st]);
+          if (i + 1 == t.nblk) mbar_arrive(&sb.l_full[k & 1]);  // the V loader's word on the tile is in
         }
         __syncwarp();
       }
@@ -506,7 +558,9 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_tc_kernel(const __grid_c
       tc5::fence_after();
       const float tot = *(volatile float*)&sb.sums[k & 1][row];
       // a NaN sum is the answer of a NaN score
-      const float inv = tot == 0.f ? 0.f : 1.f / tot;
+      const bool none = t.shift + row >= *(volatile int*)&sb.poison[k & 3];
+      const float inv = none ? __int_as_float(0x7fffffff) : tot == 0.f ? 0.f : 1.f / tot;
+      float odd = 0.f;  // NaN once an entry of O is not finite
       // all of O to registers, packed, before the stores: the next tile's first product waits for it
       uint32_t w[kDv / 2];
 #pragma unroll
@@ -516,6 +570,21 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_tc_kernel(const __grid_c
         tc5::wait_ld();
 #pragma unroll
         for (int q = 0; q < 8; ++q) w[c / 2 + q] = pack_bf16(ov[2 * q] * inv, ov[2 * q + 1] * inv);
+#pragma unroll
+        for (int q = 0; q < 16; ++q) odd = fmaf(ov[q], 0.f, odd);
+      }
+      // A weight of 0 does not keep an infinity or a NaN of V out of O. It is rare enough
+      // that a look through V's masked blocks, 1.4 us each, waits until an O that is no
+      // number shows up under a sum that is one: from then on such values that some row
+      // does not attend become zeros (rows that do attend one become NaN here), and the
+      // tiles that were already under way are done again.
+      if (__any_sync(0xffffffffu, odd != odd && tot == tot && row < t.jn && !*(volatile int*)&sb.looked[k & 3]) && lane == 0) {
+        sb.careful = 1;
+        if (!(atomicOr(&sb.again_bits, 1 << (k & 31)) >> (k & 31) & 1)) {
+          const int x = atomicAdd(&sb.again, 1);
+          if (x < 8) sb.redo[x] = t;  // four at most: see above
+        }
+        __threadfence_block();
       }
       tc5::fence_before();
       __syncwarp();
@@ -545,6 +614,9 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_tc_kernel(const __grid_c
                                       ((size_t)(t.q0 + 32 * quad + r) * a.c.H + t.h) * kDv + 64 * c + 8 * q) = v;
         }
       }
+      __threadfence_block();
+      __syncwarp();
+      if (lane == 0) atomicAdd(&sb.epilogues, 1);
     }
   }
   // everything issued is done (bounded) before TMEM goes back

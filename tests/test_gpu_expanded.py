@@ -94,6 +94,55 @@ def test_expanded_attention_is_the_formula(kb, dtype, ql, kl, H, dn, dr, dv, ext
     assert torch.equal(first, c.out) and int(c.err) == 0
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("where", ["v", "k", "pe", "q"])
+@pytest.mark.parametrize("dtype,dn,dr,dv", [("bf16", 128, 64, 128), ("bf16", 64, 32, 64), ("f32", 128, 64, 128)])
+def test_what_is_not_finite_reaches_only_who_attends_it(kb, bad, where, dtype, dn, dr, dv):
+    c = Case(kb, dtype, [150, 70, 260, 1, 3], [300, 70, 260, 200, 3], 3, dn, dr, dv, seed=4)
+    t = [280, 20, 130, 199, 1]  # a key row, or the query row that sits at it
+    for b, x in enumerate(t):
+        if where == "q":
+            c.q[c.q0[b] + x - (c.kl[b] - c.ql[b]), 1, 5] = bad
+        elif where == "pe":
+            c.pe[c.k0[b] + x, 3] = bad
+        else:
+            getattr(c, where)[c.k0[b] + x, 1, 9] = bad
+    c.run()
+    assert int(c.err) == 0
+    out, q, v = c.out.cpu(), c.q.double().cpu(), c.v.double().cpu()
+    key = torch.cat((c.k.double().cpu(), c.pe.double().cpu()[:, None].expand(-1, 3, -1)), -1)
+    for b, x in enumerate(t):
+        first = c.kl[b] - c.ql[b]
+        for p in sorted({first, x - 2, x - 1, x, x + 1, c.kl[b] - 1} & set(range(first, c.kl[b]))):
+            keys = slice(c.k0[b], c.k0[b] + p + 1)
+            w, bound = R.attend(q[c.q0[b] + p - first], key[keys], v[keys], c.scale, c.dt)
+            got = out[c.q0[b] + p - first]
+            hit = torch.tensor([h == 1 or where == "pe" for h in range(3)]) & (p == x if where == "q" else p >= x)
+            R.check(got[~hit], w[~hit], bound[~hit], f"request {b} position {p}")
+            if math.isnan(bad):
+                assert bool(got[hit].isnan().any(-1).all())
+
+
+def test_values_that_are_not_finite_in_every_tile(kb):
+    """More such tiles than SMs, several to each: rows before the value are right, rows from it on are not finite."""
+    c = Case(kb, "bf16", [130] * 20, [130] * 20, 64, 128, 64, 128, seed=6)
+    at = [(29 * b + 40) % 127 + 1 for b in range(20)]
+    for b in range(20):
+        c.v[c.k0[b] + at[b], :, 3 * b] = float("nan") if b % 2 else float("inf")
+    c.run()
+    c.run()
+    assert int(c.err) == 0
+    out, q, v = c.out.cpu(), c.q.double().cpu(), c.v.double().cpu()
+    key = torch.cat((c.k.double().cpu(), c.pe.double().cpu()[:, None].expand(-1, 64, -1)), -1)
+    for b in range(20):
+        rows = out[c.q0[b]:c.q0[b + 1]]
+        assert bool(rows[:at[b]].isfinite().all()) and not bool(rows[at[b]:].isfinite().all(-1).any())
+        for j in {0, at[b] - 1}:
+            keys = slice(c.k0[b], c.k0[b] + j + 1)
+            w, bound = R.attend(q[c.q0[b] + j], key[keys], v[keys], c.scale, c.dt)
+            R.check(rows[j], w, bound, f"request {b} query {j}")
+
+
 def test_strides(kb):
     """Heads before tokens, odd token strides, and rows that do not start on 16 bytes."""
     a = Case(kb, "bf16", [70, 130], [100, 130], 4, 128, 64, 128, seed=2)
