@@ -371,7 +371,8 @@ class PagedLatentCache(PagedKVCache):
     rows and rotates the queries' key part (:meth:`store`) and attends in the
     latent space (:meth:`attend`: decode, multi-token verify and chunks). Long
     prompts are cheaper in expanded form: project :meth:`rows` up and call
-    :func:`binding.latent_prefill_attention`."""
+    :func:`binding.latent_prefill_attention`. Calls of one shape share a
+    workspace: those of one cache run one after another on the GPU."""
 
     def __init__(self, num_pages, page_size, latent_dim, rope_dim, num_layers, dtype="bf16", max_requests=256,
                  table_mode="block", max_seq_len=None, free_stack=None, device="cuda", zero=True):
@@ -386,9 +387,10 @@ class PagedLatentCache(PagedKVCache):
 
     def store(self, layer, q_pe, latent, k_pe, positions, out_loc, rope, q):
         """Write the tokens' rows and the rotated ``q_pe`` into the tail of the
-        absorbed queries ``q`` [n, Hq, latent_dim + rope_dim], in one launch."""
+        absorbed queries ``q`` [n, Hq, latent_dim + rope_dim], in one launch.
+        ``q_pe`` and ``q`` None: only the store (the rows of a prompt)."""
         kb.rotary_store_latent(self.pool, layer, q_pe, latent, k_pe, positions, out_loc, rope,
-                               q[..., self.latent_dim:])
+                               None if q is None else q[..., self.latent_dim:])
 
     def workspace(self, batch, num_q_heads, chunk=1):
         key = (batch, num_q_heads, chunk)
@@ -414,6 +416,8 @@ class PagedLatentCache(PagedKVCache):
         afterwards. Asynchronous on the current stream."""
         B, C, Hq, W = q[0].shape
         r = np.ascontiguousarray(rids, dtype=np.int32)
+        if len(r) != B or len(np.unique(r)) != B:
+            raise ValueError(f"step takes {B} distinct requests, got {list(map(int, r))}")
         before = self.lengths[r].copy()
         out_loc = self.append(np.repeat(r, C))
         flat = np.concatenate((before + C, r, (before[:, None] + np.arange(C)).ravel()))
@@ -430,7 +434,8 @@ class PagedLatentCache(PagedKVCache):
     def rows(self, layer, rids):
         """The stored rows of requests ``rids`` in logical order, [total,
         latent_dim + rope_dim], and their offsets int32 [len(rids) + 1]: what
-        the projections of the expanded form take."""
+        the projections of the expanded form take. A request that a window
+        has taken pages from has no such rows left (ValueError)."""
         r = np.ascontiguousarray(rids, dtype=np.int32)
         lens = self.lengths[r]
         d = self._to_device(np.concatenate((lens, r, [0], np.cumsum(lens))))
@@ -438,7 +443,11 @@ class PagedLatentCache(PagedKVCache):
         slots = torch.empty((n, max(1, int(lens.max(initial=0)))), dtype=torch.int32, device=self.dev)
         kb.gather_indices(self.pool, self.table, self.table_mode, d[:n], 0, slots, table_rows=d[n:2 * n])
         live = torch.arange(slots.shape[1], device=self.dev)[None, :] < d[:n, None]
-        return self.kv[layer].view(-1, self.D)[slots[live].long()], d[2 * n:]
+        slots = slots[live].long()
+        if bool((slots < 0).any()):
+            kb.kvp_sync_error(self.pool)  # what the gather recorded of it
+            raise ValueError("a request's first pages are released")
+        return self.kv[layer].view(-1, self.D)[slots], d[2 * n:]
 
     def _unsupported(self, what):
         raise TypeError(f"{what} reads separate K and V: a latent cache uses store, attend and step")

@@ -331,3 +331,16 @@ def test_latent_cache_steps(kb):
     for what in ("decode_step", "verify_step", "prefill_step"):
         with pytest.raises(TypeError):
             getattr(cache, what)([0], [torch.empty((1, 1, H, W), device=DEV)], None, None, None, 0, 1.0)
+    lengths = cache.lengths.copy()
+    for rids in ([1, 1], [1]):  # a request twice, and fewer requests than queries
+        with pytest.raises(ValueError):
+            cache.step(rids, [torch.empty((2, 1, H, W), device=DEV)], None, None, None, rope, None, 0, scale)
+    with pytest.raises(ValueError):
+        cache.rows(0, [1])  # the window's steps have released its first pages
+    assert kb.kvp_sync_error(cache.pool) == 0 and (cache.lengths == lengths).all()
+    cache.new(4)
+    slots = cache.append([4] * 20)  # the rows of a prompt, without queries
+    lat, pe = torch.randn((20, dc), generator=g).bfloat16().to(DEV), torch.zeros((20, dr)).bfloat16().to(DEV)
+    cache.store(1, None, lat, pe, torch.arange(20, dtype=torch.int32, device=DEV), slots, rope, None)
+    rows, start = cache.rows(1, [4])
+    assert torch.equal(rows, torch.cat((lat, pe), -1)) and start.tolist() == [0, 20]
