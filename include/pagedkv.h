@@ -332,7 +332,8 @@ int rotary_store_cache(const kvp_pool* pool, int layer, const void* q,
  *   latent    device, latent_dim contiguous entries at latent + i * stride.
  *   k_pe      device, rope_dim contiguous entries at k_pe + i * stride.
  *             latent and k_pe both NULL: only q_pe.
- * rotary_dim is even, 0 .. rope_dim. Everything else as rotary_store_cache.
+ * rotary_dim is even, 0 .. rope_dim. A pool without rope_dim takes only the
+ * latents (q_pe and k_pe are not read). Everything else as rotary_store_cache.
  * ---------------------------------------------------------------------- */
 int rotary_store_latent(const kvp_pool* pool, int layer, const void* q_pe,
                         long long q_stride, long long q_head_stride,

@@ -259,7 +259,9 @@ class RotaryPlan:
         if layout not in _LAYOUTS:
             raise ValueError(f"layout must be one of {sorted(_LAYOUTS)}, got {layout!r}")
         self.rotary_dim, self.layout, self.attn_factor = int(rotary_dim), _LAYOUTS[layout], float(attn_factor)
-        f = rotary_frequencies(rotary_dim, base, scaling, factor, original_len, low_turns, high_turns)
+        f = []  # 0: nothing turns
+        if self.rotary_dim:
+            f = rotary_frequencies(rotary_dim, base, scaling, factor, original_len, low_turns, high_turns)
         signed = [x - (1 << 64) if x >= 1 << 63 else x for x in f]
         self.freqs = torch.tensor(signed, dtype=torch.int64).to(device)
 

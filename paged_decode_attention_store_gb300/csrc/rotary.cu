@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kRotThreads) rotary_store_kernel(const RotArgs
   // units of a head: rotated ones first (HALF: chunk u and chunk u + rot / 2 N), then the rest of the head, one chunk each
   const int rot_units = HALF ? a.rot / (2 * N) : a.rot / N;
   const int units = rot_units + (a.d - a.rot) / N;
-  const int upar = min(units, kRotThreads);
+  const int upar = max(1, min(units, kRotThreads));  // no units: rows without a rotated part
   const int groups = kRotThreads / upar;
   const int g = tid / upar, u0 = tid - g * upar;
   const int heads = a.hq + a.hk;
@@ -429,6 +429,12 @@ extern "C" int rotary_store_latent(const kvp_pool* pool, int layer, const void* 
                                    long long q_out_stride, long long q_out_head_stride, void* stream) {
   if (!pool || !pool->latent_dim) return KVP_ERR_INVALID_ARG;
   const int dc = pool->latent_dim, dr = pool->head_dim - dc;
+  if (dr == 0) {  // rows without a rotated part: no queries, and k_pe may have no address
+    q_pe = nullptr;
+    k_pe = latent;
+    k_pe_stride = latent_stride;
+    if (!latent) return n == 0 ? KVP_OK : KVP_ERR_INVALID_ARG;
+  }
   if (!kvp::rotary_args_ok(pool, layer, q_pe, q_stride, q_head_stride, num_q_heads, dr, k_pe, k_pe_stride, latent,
                            latent_stride, positions, out_loc, n, freqs, rotary_dim, layout, attn_factor, q_pe_out,
                            q_out_stride, q_out_head_stride))
@@ -455,7 +461,7 @@ extern "C" int rotary_store_latent(const kvp_pool* pool, int layer, const void* 
   a.freqs = freqs;
   a.n = n;
   a.hq = q_pe ? num_q_heads : 0;
-  a.hk = k_pe ? 1 : 0;
+  a.hk = k_pe && dr > 0 ? 1 : 0;
   a.d = dr;
   a.rot = rotary_dim;
   a.v_elems = dc;

@@ -231,6 +231,27 @@ def test_latent_store_is_the_formula(kb, dtype, n, Hq, dc, dr, P, layout):
     assert kb.kvp_sync_error(pool) == 0
 
 
+@pytest.mark.parametrize("dtype,dc", [("bf16", 512), ("bf16", 8), ("f32", 20), ("bf16", 1024)])
+def test_latent_rows_without_a_rotated_part(kb, dtype, dc):
+    """rope_dim 0: only the latents are stored, queries and key parts have no entries."""
+    g = torch.Generator().manual_seed(dc)
+    buf = torch.full((2, 40, 4, dc), 7.0, dtype=DT[dtype], device=DEV)
+    pool = kb.LatentPool(buf, dc, kb.KVP_BF16 if dtype == "bf16" else kb.KVP_F32)
+    n, none = 33, torch.empty((33, 0), dtype=DT[dtype], device=DEV)
+    lat = torch.randn((n, 2 * dc), generator=g).to(DT[dtype]).to(DEV)[:, :dc]
+    loc = torch.randperm(160, generator=g)[:n].to(torch.int32)
+    pos = torch.arange(n, dtype=torch.int32, device=DEV)
+    rope = kb.RotaryPlan(0, device=DEV)
+    kb.rotary_store_latent(pool, 1, None, lat, none, pos, loc.to(DEV), rope, None)
+    kb.rotary_store_latent(pool, 0, none[:, None].expand(n, 3, 0), lat, none, pos, loc.to(DEV), rope,
+                           torch.empty((n, 3, 0), dtype=DT[dtype], device=DEV))
+    want = torch.full((160, dc), 7.0, dtype=DT[dtype])
+    want[loc.long()] = lat.cpu()
+    for layer in range(2):
+        assert torch.equal(buf[layer].view(160, dc).cpu(), want)
+    assert kb.kvp_sync_error(pool) == 0
+
+
 def test_refusals(kb):
     pool, kv, loc, qkv = make(kb, "bf16", 8, 4, 2, 64, 4, seed=1)
     rope = kb.RotaryPlan(64, device=DEV)
