@@ -157,7 +157,9 @@ extern "C" int paged_latent_attention(const kvp_pool* pool, int layer, const voi
   if (table_mode != KVP_BLOCK_TABLE && table_mode != KVP_RAW_LOCATIONS) return KVP_ERR_INVALID_ARG;
   if (!(scale - scale == 0.f)) return KVP_ERR_INVALID_ARG;
   if (sinks < 0 || (window > 0 && sinks >= window)) return KVP_ERR_INVALID_ARG;
-  if (window <= 0) window = sinks = 0;
+  // a window that holds every context the table can hold is none
+  if (window <= 0 || window >= (long long)table_cols * (table_mode == KVP_RAW_LOCATIONS ? 1 : pool->page_size))
+    window = sinks = 0;
   if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) & 15) return KVP_ERR_INVALID_ARG;
   if ((long long)batch * chunk > 0x7fffffffLL / num_q_heads) return KVP_ERR_INVALID_ARG;
   size_t need = 0;

@@ -206,6 +206,19 @@ def test_a_query_that_is_not_finite_stays_alone(kb):
                 assert int(ok.sum()) == 40 - (j == (2, 4, 0)[b])
 
 
+def test_the_widest_windows(kb):
+    """Windows at and past what the table can hold, to the end of int32."""
+    for dc, dr, H in ((512, 64, 40), (64, 16, 3)):
+        c = Case(kb, "bf16", [300, 90, 7], 5, H, dc, dr, 16, seed=15)
+        full = c.run().clone()
+        cap = c.table.shape[1] * 16
+        for window, sinks in ((cap, 0), (cap + 1, 3), (2 ** 31 - 1, 0), (2 ** 31 - 1, 2 ** 31 - 2)):
+            c.out.fill_(5.0)
+            assert torch.equal(c.run(window, sinks), full)
+        c.run(cap - 1, 0)
+        c.verify(cap - 1, 0)
+
+
 def test_bad_requests_and_pages(kb):
     """An invalid length or table row zero-fills its request, a hole is skipped, and the others are untouched by it."""
     for dc, dr, H in ((512, 64, 16), (128, 32, 4)):
