@@ -129,6 +129,12 @@ extern "C" int latent_prefill_attention(const void* q, long long q_stride, long 
   if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v) |
        reinterpret_cast<uintptr_t>(k_pe) | reinterpret_cast<uintptr_t>(out)) & em)
     return KVP_ERR_INVALID_ARG;
+  for (const void* p : {q, k, v, static_cast<const void*>(out)}) {  // another device's memory
+    cudaPointerAttributes at;
+    int dev = -1;
+    if (cudaPointerGetAttributes(&at, p) != cudaSuccess || cudaGetDevice(&dev) != cudaSuccess) return KVP_ERR_CUDA;
+    if (at.type == cudaMemoryTypeDevice && at.device != dev) return KVP_ERR_INVALID_ARG;
+  }
   if (max_q > total_q) max_q = total_q;
   ExpandedCall a;
   a.q = q;
