@@ -55,8 +55,8 @@
 // Measured (bf16, the whole call with its combine): one request of 777 rows, 16
 // heads: 12 us (two launches); 64 requests of 512 .. 4096 rows, 32 heads: 45.3 us,
 // 4.1 TB/s (7 us until the first block is in, 5 us of combine); 32 requests of 8192 ..
-// 32768 scattered rows, 128 heads: 238 us, 724 TFLOP/s; four tokens of 64 heads on 64
-// requests: 128 us, 666 TFLOP/s.
+// 32768 scattered rows, 128 heads: 235 us, 733 TFLOP/s; four tokens of 64 heads on 64
+// requests: 127 us, 669 TFLOP/s.
 // Every wait is bounded (2 s), as in the other kernels.
 #include <cstring>
 

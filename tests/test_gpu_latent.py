@@ -206,6 +206,31 @@ def test_a_query_that_is_not_finite_stays_alone(kb):
                 assert int(ok.sum()) == 40 - (j == (2, 4, 0)[b])
 
 
+@pytest.mark.parametrize("P", [16, 1])
+def test_rows_past_four_gigabytes(kb, P):
+    """Stored by rotary_store_latent and attended at offsets that 32 bits do not hold, in the second layer."""
+    dc, dr, H, slots = 512, 64, 16, 2_000_000
+    W, g = dc + dr, torch.Generator().manual_seed(P)
+    buf = torch.empty((2, slots // P, P, W), dtype=torch.bfloat16, device=DEV)
+    assert 2 * slots * W > 2 ** 31
+    pool = kb.LatentPool(buf, dc, kb.KVP_BF16)
+    L = 150
+    pages = slots // P - 1 - torch.randperm(-(-L // P) + 5, generator=g)[:-(-L // P)]
+    sl = torch.tensor([int(pages[t // P]) * P + t % P for t in range(L)], dtype=torch.int32, device=DEV)
+    rows = torch.randn((L, W), generator=g).bfloat16().to(DEV)
+    kb.rotary_store_latent(pool, 1, None, rows[:, :dc], rows[:, dc:], torch.zeros(L, dtype=torch.int32, device=DEV), sl,
+                           kb.RotaryPlan(dr, device=DEV), None)
+    assert torch.equal(buf[1].view(slots, W)[sl.long()], rows)  # position 0 turns nothing
+    q = torch.randn((1, 1, H, W), generator=g).bfloat16().to(DEV)
+    out = torch.empty((1, 1, H, dc), dtype=torch.bfloat16, device=DEV)
+    kb.paged_latent_attention(pool, 1, q, pages.to(torch.int32)[None].to(DEV), kb.KVP_BLOCK_TABLE,
+                              torch.tensor([L], dtype=torch.int32, device=DEV), 0, W ** -0.5, out,
+                              kb.alloc_latent_workspace(pool, 1, 1, H, device=DEV))
+    x = rows.double().cpu()
+    R.check(out[0, 0], *R.attend(q[0, 0].double().cpu(), x, x[:, :dc], W ** -0.5, torch.bfloat16))
+    assert kb.kvp_sync_error(pool) == 0
+
+
 def test_the_widest_windows(kb):
     """Windows at and past what the table can hold, to the end of int32."""
     for dc, dr, H in ((512, 64, 40), (64, 16, 3)):

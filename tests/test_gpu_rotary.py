@@ -252,6 +252,20 @@ def test_latent_rows_without_a_rotated_part(kb, dtype, dc):
     assert kb.kvp_sync_error(pool) == 0
 
 
+def test_slots_past_four_gigabytes(kb):
+    Hkv, D, P, slots, n = 8, 128, 16, 2_200_000, 40
+    kv = torch.empty((2, 1, slots // P, P, Hkv, D), dtype=torch.bfloat16, device=DEV)
+    pool = kb.Pool(kv, P, kb.KVP_BF16)
+    g = torch.Generator().manual_seed(3)
+    k, v = (torch.randn((n, Hkv, D), generator=g).bfloat16().to(DEV) for _ in range(2))
+    loc = (slots - 1 - torch.randperm(500, generator=g)[:n]).to(torch.int32).to(DEV)
+    kb.rotary_store_cache(pool, 0, None, k, v, torch.zeros(n, dtype=torch.int32, device=DEV), loc,
+                          kb.RotaryPlan(D, device=DEV), None)
+    for plane, want in ((kv[0, 0], k), (kv[1, 0], v)):
+        assert torch.equal(plane.view(slots, Hkv, D)[loc.long()], want)
+    assert kb.kvp_sync_error(pool) == 0
+
+
 def test_refusals(kb):
     pool, kv, loc, qkv = make(kb, "bf16", 8, 4, 2, 64, 4, seed=1)
     rope = kb.RotaryPlan(64, device=DEV)
