@@ -12,7 +12,7 @@
 // heads, else 64) of one request in one CTA; keys come in blocks of 64.
 //  * S (64 x 64) = Q X^T: 36 M 64 N 64 K 16 MMAs (16 ns each, 0.59 us a block).
 //    Query rows lie on TMEM lanes (16 a warp quadrant), so a row's maximum and
-//    sum stay within two threads. When R < 64 the A tile reads past Q into the
+//    sum stay within four lanes of a warp. When R < 64 the A tile reads past Q into the
 //    next bytes of shared memory: those rows of S are never read.
 //  * O^T (512 x R) += X_c^T P^T: latent entries on the M axis, four M 128 blocks
 //    of N = R, so that O takes 4 R <= 256 TMEM columns on all 128 lanes (O with
