@@ -19,11 +19,9 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-// Whether the phase with the given parity is complete, without waiting.
 }  // namespace tc5
-__device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
-  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n) : "memory");
-}
+
+// Whether the phase with the given parity is complete, without waiting.
 __device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -35,7 +33,9 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
+
 namespace tc5 {
+
 
 // Shared-memory matrix descriptor, 128-byte swizzle (8-row atoms of 1 KB).
 // K-major: ``sbo`` bytes between 8-row groups, ``lbo`` unused. MN-major: ``lbo``
