@@ -124,7 +124,8 @@ struct LatBars {
   uint64_t empty[kStages];  // O issuer (commit) -> loaders
   uint64_t s_full[2], s_free[2];
   uint64_t f_full[2];       // softmax -> scaling warps: the block's factors are in ``factor``
-  uint64_t p_full, pv_done, o_free, drain, sums;
+  uint64_t p_full[2];       // by blocks in turn: a scaling warp with nothing to do may be a block ahead of the slowest
+  uint64_t pv_done, o_free, drain, sums;
   uint32_t taddr;
   int abort;
   int late;  // raised by a wait for copies in flight that ran out
@@ -290,8 +291,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
       mbar_init(&sb.s_full[x], 1);
       mbar_init(&sb.s_free[x], R / 16);
       mbar_init(&sb.f_full[x], R / 16);
+      mbar_init(&sb.p_full[x], R / 16 + kScaleWarps);
     }
-    mbar_init(&sb.p_full, R / 16 + kScaleWarps);
     mbar_init(&sb.pv_done, 1);
     mbar_init(&sb.o_free, 4 + kScaleWarps);
     mbar_init(&sb.drain, 2);
@@ -596,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
       for (int i = pc.k0; ok && i < pc.k1; ++i, ++n) {
         const int st = n % kStages;
         ok = __all_sync(0xffffffffu, lwait(&sb.full[st], n / kStages, abort_flag, a.err));
-        if (ok) ok = __all_sync(0xffffffffu, lwait(&sb.p_full, n, abort_flag, a.err));
+        if (ok) ok = __all_sync(0xffffffffu, lwait(&sb.p_full[n & 1], n >> 1, abort_flag, a.err));
         if (!ok) break;
         tc5::fence_after();
         const uint64_t dx = tc5::desc(smem_u32(sX) + st * kStage, 1024, kGroup);
@@ -727,7 +728,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sb.p_full);
+          if (lane == 0) mbar_arrive(&sb.p_full[buf]);
         }
         if (!ok) break;
         ok = __all_sync(0xffffffffu, lwait(&sb.pv_done, n - 1, abort_flag, a.err));
@@ -774,7 +775,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
             tc5::fence_before();
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sb.p_full);
+          if (lane == 0) mbar_arrive(&sb.p_full[buf]);
         }
         if (!ok) break;
       }

@@ -342,3 +342,25 @@ def test_negative_and_zero_scale(kb):
         c.scale = scale
         c.run()
         c.verify()
+
+
+@pytest.mark.parametrize("C,H,L", [(1, 16, 3000), (1, 32, 1500), (4, 64, 900), (20, 64, 640)])
+def test_a_maximum_that_grows_in_some_rows_of_every_block(kb, C, H, L):
+    """O is scaled in each block, for other rows each time, so that the warps that scale it and those that do not are
+    never in step: the formula, and the same bits every time."""
+    c = Case(kb, "bf16", [L, L // 2], C, H, 512, 64, 16, seed=16)
+    flat = c.buf[0].view(-1, c.W)
+    for b, n in enumerate(c.lens):
+        sl = torch.tensor(c.slots[b], device=DEV)
+        # block i grows with the query of head i mod H, by 9 and more in log2 units of that head's scores
+        which = (torch.arange(n, device=DEV) // 64) % H
+        size = (1 + torch.arange(n, device=DEV) // 64)[:, None] * 8.0 / (c.scale * c.W)
+        flat[sl] = (c.q[b, 0, which].float() * size + 0.1 * flat[sl].float()).to(c.dt)
+    c.run()
+    c.verify()
+    first = c.out.clone()
+    for _ in range(30):
+        c.out.fill_(5.0)
+        c.run()
+        assert torch.equal(c.out, first)
+    assert kb.kvp_sync_error(c.pool) == 0
