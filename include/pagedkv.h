@@ -371,8 +371,9 @@ int rotary_store_latent(const kvp_pool* pool, int layer, const void* q_pe,
  * table entry that is a hole or out of range is skipped (nothing is read
  * through it) and that request's output is otherwise unspecified. The pool's
  * device must be current. Rows past the context, out of a query's
- * window and in other pages may hold anything; a row that is not finite makes
- * the queries that attend it NaN, and no others.
+ * window and in other pages may hold anything; a row that holds an infinity or
+ * a NaN makes the queries that attend it NaN, whatever their scores, and no
+ * others. A score that overflows to minus infinity weighs nothing.
  * ---------------------------------------------------------------------- */
 int paged_latent_attention_workspace_size(const kvp_pool* pool, int batch,
                                           int chunk, int num_q_heads,

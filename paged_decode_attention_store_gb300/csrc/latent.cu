@@ -78,14 +78,20 @@ __global__ void __launch_bounds__(32 * kLatWarps) latent_general_kernel(const La
     if (slot < 0) continue;
     const T* x = reinterpret_cast<const T*>(a.layer) + (size_t)slot * a.width;
     float xr[PER];
-    float dot = 0.f;
+    float dot = 0.f, odd = 0.f;  // odd: NaN once an entry is not finite, whatever it meets in q
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const int d = lane + 32 * i;
       xr[i] = d < a.dc ? lat_f(x[d]) : 0.f;
       if (d < a.dc) dot = fmaf(qs[d], xr[i], dot);
+      odd = fmaf(xr[i], 0.f, odd);
     }
-    for (int d = a.dc + lane; d < a.width; d += 32) dot = fmaf(qs[d], lat_f(x[d]), dot);
+    for (int d = a.dc + lane; d < a.width; d += 32) {
+      const float y = lat_f(x[d]);
+      dot = fmaf(qs[d], y, dot);
+      odd = fmaf(y, 0.f, odd);
+    }
+    dot += odd;
 #pragma unroll
     for (int sh = 16; sh > 0; sh >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, sh);
     const float s = dot * a.scale_log2;

@@ -50,8 +50,8 @@
 //
 // Warps: 0 walks the pieces and names the blocks' rows, 1 issues S, 2 issues O, 3
 // loads Q, 4..7 run the softmax (16 query rows each, TMEM quadrant = warp % 4),
-// 8..11 scale O when a row's maximum grew, 4..11 together the epilogue, 12..15 load
-// the blocks.
+// 8..11 look for rows that are not finite and scale O when a row's maximum grew, 4..11
+// together the epilogue, 12..15 load the blocks.
 // Measured (bf16, the whole call with its combine): one request of 777 rows, 16
 // heads: 12 us (two launches); 64 requests of 512 .. 4096 rows, 32 heads: 45.3 us,
 // 4.1 TB/s (7 us until the first block is in, 5 us of combine); 32 requests of 8192 ..
@@ -134,6 +134,7 @@ struct LatBars {
   int slots[kNamed][kKeys];  // -1: nothing to read
   int boxes[kNamed];         // mask of groups that come as boxes; -1: no more blocks
   Piece piece[kPieces];
+  uint32_t row_bad[2];      // of a piece: its rows that attend a key that is not finite
   float factor[2][kMaxR];   // of a block: what O's rows have to be scaled by before it
   float row_m[kMaxR], row_l[kMaxR], row_i[kMaxR];  // of a piece: maximum, sum, what O is multiplied by
 };
@@ -238,15 +239,38 @@ __device__ __forceinline__ int slot_of(const LatArgs& a, int row, int t) {
   return (page << a.page_shift) + (t & (a.T.page_size - 1));
 }
 
-// Zeros in place of a block's rows that hold an infinity or a NaN (a warp; 9 x 128 bytes a row).
-__device__ __noinline__ void clear_not_finite(unsigned char* block, int lane) {
-  for (int key = lane; key < kKeys; key += 32) {
-    unsigned char* row = block + (key >> 3) * kGroup + (key & 7) * 128;
-    uint32_t bad = 0;
-    for (int x = 0; x < kChunks * 32; ++x)
-      bad |= tc5::not_finite2(*reinterpret_cast<const uint32_t*>(row + (x >> 5) * 1024 + (x & 31) * 4));
-    for (int x = 0; bad && x < kChunks * 32; ++x) *reinterpret_cast<uint32_t*>(row + (x >> 5) * 1024 + (x & 31) * 4) = 0u;
+// Row rr of a tile attends key offsets [0, se) and [wb, we] of its item's span; rows past the tile's end: none.
+struct RowSpan {
+  int se, wb, we;
+  __device__ __forceinline__ RowSpan(const LatArgs& a, const Piece& pc, int rr) {
+    const bool rv = rr < pc.rows;
+    const int p = pc.p0 + (a.C == 1 ? 0 : (pc.r0 + rr) / a.H);
+    const Span u = pc.u, sr = attend_span(p + 1, a.window, a.sinks);
+    se = rv ? sr.se : 0;
+    wb = rv ? u.se + (sr.lo - u.lo) : 1 << 30;
+    we = rv ? u.se + (p - u.lo) : -1;
   }
+  __device__ __forceinline__ bool attends(int o) const { return o < se || (o >= wb && o <= we); }
+};
+
+// Zeros in place of those of a block's rows key0 .. key0 + n - 1 that hold an infinity or a NaN (a warp; 9 x 128
+// bytes a row); who of the tile attends one goes into ``row_bad``. ``o0``: offset of the block's first key.
+template <int R>
+__device__ __noinline__ void clear_not_finite(const LatArgs& a, const Piece& pc, unsigned char* block, uint32_t* row_bad,
+                                              int key0, int n, int o0) {
+  const int lane = threadIdx.x & 31;
+  for (int key = key0; key < key0 + n; ++key) {
+    unsigned char* row = block + (key >> 3) * kGroup + (key & 7) * 128 + lane * 4;
+    uint32_t odd = 0;
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) odd |= tc5::not_finite2(*reinterpret_cast<const uint32_t*>(row + c * 1024));
+    if (!__any_sync(0xffffffffu, odd)) continue;
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) *reinterpret_cast<uint32_t*>(row + c * 1024) = 0u;
+    for (int rr = lane; rr < R; rr += 32)
+      if (RowSpan(a, pc, rr).attends(o0 + key)) atomicOr(&row_bad[rr >> 5], 1u << (rr & 31));
+  }
+  fence_proxy_async_smem();  // before the product reads them
 }
 
 __device__ __forceinline__ long long range_start(long long total, int g, int NG) { return NG ? total * g / NG : 0; }
@@ -289,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&sb.s_full[x], 1);
-      mbar_init(&sb.s_free[x], R / 16);
+      mbar_init(&sb.s_free[x], 2 * (R / 16));  // softmax warps and the scaling warps that look at their rows
       mbar_init(&sb.f_full[x], R / 16);
       mbar_init(&sb.p_full[x], R / 16 + kScaleWarps);
     }
@@ -298,6 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
     mbar_init(&sb.drain, 2);
     mbar_init(&sb.sums, R / 16);
     sb.abort = sb.late = 0;
+    sb.row_bad[0] = sb.row_bad[1] = 0;
     fence_mbar_init();
   }
   if (warp == 0) tc5::alloc512(&sb.taddr);
@@ -634,18 +659,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
     Piece pc;
     while (ok && get_piece(np, pc)) {
       if (softmax) {
-        // row x attends key offsets [0, se) and [wb, we] of the item's span
-        int se[2], wb0[2], we0[2];
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int rr = row0 + 8 * x;
-          const bool rv = rr < pc.rows;
-          const int p = pc.p0 + (a.C == 1 ? 0 : (pc.r0 + rr) / a.H);
-          const Span u = pc.u, sr = attend_span(p + 1, a.window, a.sinks);
-          se[x] = rv ? sr.se : 0;
-          wb0[x] = rv ? u.se + (sr.lo - u.lo) : 1 << 30;
-          we0[x] = rv ? u.se + (p - u.lo) : -1;
-        }
+        const RowSpan sp[2] = {RowSpan(a, pc, row0), RowSpan(a, pc, row0 + 8)};
         float m[2] = {-INFINITY, -INFINITY}, lsum[2] = {0.f, 0.f};
         for (int i = pc.k0; i < pc.k1; ++i, ++n) {
           const int buf = n & 1;
@@ -659,26 +673,12 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
           __syncwarp();
           if (lane == 0) mbar_arrive(&sb.s_free[buf]);
           const int o0 = i * kKeys;
-          if (!__all_sync(0xffffffffu, max(wb0[0], wb0[1]) <= o0 && min(we0[0], we0[1]) >= o0 + kKeys - 1)) {
-            // A weight of 0 would not keep an infinity or a NaN in the latent out of O: where a score is
-            // no number, such rows of the block become zeros. Who attends one has its score already.
-            float odd = 0.f;
+          if (!__all_sync(0xffffffffu, max(sp[0].wb, sp[1].wb) <= o0 && min(sp[0].we, sp[1].we) >= o0 + kKeys - 1)) {
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const int oc = o0 + 2 * (lane & 3);
+            for (int x = 0; x < 2; ++x)
 #pragma unroll
-              for (int c = 0; c < 16; ++c) {
-                const int o = oc + 8 * (c / 2) + c % 2;
-                odd = fmaf(sv[x][c], 0.f, odd);
-                if (!(o < se[x] || (o >= wb0[x] && o <= we0[x]))) sv[x][c] = -INFINITY;
-              }
-            }
-            if (__any_sync(0xffffffffu, odd != odd)) {
-              const int st = n % kStages;
-              ok = __all_sync(0xffffffffu, lwait(&sb.full[st], n / kStages, abort_flag, a.err));
-              if (!ok) break;
-              clear_not_finite(sX + st * kStage, lane);
-            }
+              for (int c = 0; c < 16; ++c)
+                if (!sp[x].attends(o0 + 8 * (c / 2) + 2 * (lane & 3) + c % 2)) sv[x][c] = -INFINITY;
           }
           float f[2];
 #pragma unroll
@@ -738,6 +738,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
         for (int x = 0; x < 2; ++x) {
           lsum[x] += __shfl_xor_sync(0xffffffffu, lsum[x], 1);
           lsum[x] += __shfl_xor_sync(0xffffffffu, lsum[x], 2);
+          if ((*(volatile uint32_t*)&sb.row_bad[(row0 + 8 * x) >> 5] >> ((row0 + 8 * x) & 31)) & 1) lsum[x] = __int_as_float(0x7fffffff);
           if ((lane & 3) == 0) {
             sb.row_m[row0 + 8 * x] = m[x];
             sb.row_l[row0 + 8 * x] = lsum[x];
@@ -745,6 +746,9 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
             sb.row_i[row0 + 8 * x] = lsum[x] == 0.f ? 0.f : 1.f / lsum[x];
           }
         }
+        __syncwarp();
+        // read above by all lanes; nobody sets it again before this piece's epilogue
+        if (lane == 0) atomicAnd(&sb.row_bad[quad >> 1], quad & 1 ? 0x0000ffffu : 0xffff0000u);
         __threadfence_block();
         tc5::fence_before();
         __syncwarp();
@@ -754,6 +758,38 @@ __global__ void __launch_bounds__(kThreads, 1) latent_tc_kernel(const __grid_con
           const int buf = n & 1;
           ok = __all_sync(0xffffffffu, lwait(&sb.f_full[buf], n >> 1, abort_flag, a.err));
           if (!ok) break;
+          if (quad < R / 16) {
+            // A row of the cache that holds an infinity or a NaN makes NaN who attends it, whatever their scores
+            // (minus infinity would weigh 0), and nobody else (a weight of 0 would not keep it out of O). Its score
+            // with any query at all is not finite: this warp looks at its share of the block's keys, each with one
+            // query row, while the softmax takes its exponentials. (Every score, and in the softmax's own chain,
+            // cost 4 .. 8 %.) A query that is not finite only makes it look in vain.
+            constexpr int kOwn = kKeys / (R / 16);
+            float sv[kOwn / 4], z0 = 0.f, z1 = 0.f;
+            tc5::fence_after();
+            const uint32_t ts = tbase + 256u + 64u * (uint32_t)buf + lanes + (uint32_t)(quad * kOwn);
+            if constexpr (kOwn == 16) {
+              tc5::ld_rows8x16(ts, sv);
+            } else if constexpr (kOwn == 32) {
+              tc5::ld_rows8x32(ts, sv);
+            } else {
+              float other[16];
+              tc5::ld_rows16(ts, sv, other);
+            }
+            tc5::wait_ld();
+#pragma unroll
+            for (int q = 0; q < kOwn / 8; ++q) tc5::fma2_acc(z0, z1, sv[2 * q], sv[2 * q + 1], 0.f);
+            if (__any_sync(0xffffffffu, z0 + z1 != 0.f)) {  // NaN
+              ok = __all_sync(0xffffffffu, lwait(&sb.full[n % kStages], n / kStages, abort_flag, a.err));
+              if (!ok) break;
+              const Piece copy = pc;  // pc itself stays in registers
+              clear_not_finite<R>(a, copy, sX + (n % kStages) * kStage, sb.row_bad, quad * kOwn, kOwn, i * kKeys);
+              __syncwarp();
+            }
+            tc5::fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sb.s_free[buf]);
+          }
           volatile float* fac = sb.factor[buf];
           const float f0 = lane < R ? fac[lane] : 1.f, f1 = R > 32 ? fac[lane + 32] : 1.f;
           if (__any_sync(0xffffffffu, f0 != 1.f || f1 != 1.f)) {

@@ -110,6 +110,26 @@ __device__ __forceinline__ void ld_rows16(uint32_t taddr, float* a, float* b) {
   }
 }
 
+// The first half of ld_rows16 (``a`` alone) over 32 and over 16 columns.
+__device__ __forceinline__ void ld_rows8x32(uint32_t taddr, float* a) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+#pragma unroll
+  for (int q = 0; q < 4; ++q) a[2 * q] = __uint_as_float(r[4 * q]), a[2 * q + 1] = __uint_as_float(r[4 * q + 1]);
+}
+__device__ __forceinline__ void ld_rows8x16(uint32_t taddr, float* a) {
+  uint32_t r[8];
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+#pragma unroll
+  for (int q = 0; q < 2; ++q) a[2 * q] = __uint_as_float(r[4 * q]), a[2 * q + 1] = __uint_as_float(r[4 * q + 1]);
+}
+
 // The converse of ld_rows16.
 __device__ __forceinline__ void st_rows16(uint32_t taddr, const float* a, const float* b) {
   uint32_t r[32];
@@ -220,6 +240,13 @@ __device__ __forceinline__ void add2(float& d0, float& d1, float a0, float a1) {
       "add.rn.f32x2 rd, rd, ra;\n\tmov.b64 {%0, %1}, rd;\n\t}"
       : "+f"(d0), "+f"(d1)
       : "f"(a0), "f"(a1));
+}
+// (d0, d1) += (a0, a1) * (b, b).
+__device__ __forceinline__ void fma2_acc(float& d0, float& d1, float a0, float a1, float b) {
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %4};\n\tmov.b64 rd, {%0, %1};\n\t"
+      "fma.rn.f32x2 rd, ra, rb, rd;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "+f"(d0), "+f"(d1)
+      : "f"(a0), "f"(a1), "f"(b));
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;

@@ -364,3 +364,59 @@ def test_a_maximum_that_grows_in_some_rows_of_every_block(kb, C, H, L):
         c.run()
         assert torch.equal(c.out, first)
     assert kb.kvp_sync_error(c.pool) == 0
+
+
+NOT_FINITE = [
+    # dtype, lens, C, H, dc, dr, P, window, sinks, position of the row from the end
+    ("bf16", [300, 90, 131], 1, 64, 512, 64, 16, 0, 0, -1),     # in the last block of 64 keys
+    ("bf16", [300, 90, 131], 1, 64, 512, 64, 16, 0, 0, -80),    # in a block that every query attends
+    ("bf16", [300, 91, 131], 1, 16, 512, 64, 1, 0, 0, -80),
+    ("bf16", [300, 90, 131], 5, 40, 512, 64, 16, 0, 0, -80),
+    ("bf16", [300, 90, 131], 5, 40, 512, 64, 16, 0, 0, -3),     # newer than some queries
+    ("bf16", [300, 90, 131], 20, 64, 512, 64, 16, 0, 0, -12),
+    ("bf16", [300, 90, 131], 3, 32, 512, 64, 16, 70, 2, -70),   # at the window's edge
+    ("bf16", [5000], 1, 16, 512, 64, 16, 0, 0, -2000),          # a split request
+    ("bf16", [5000], 4, 16, 512, 64, 16, 0, 0, -3),
+    ("bf16", [70, 33], 3, 4, 128, 32, 4, 0, 0, -2),             # the general kernel
+    ("f32", [70, 33], 3, 4, 64, 16, 4, 0, 0, -20),
+    ("f32", [70, 33], 3, 4, 64, 16, 4, 9, 2, -10),
+]
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("rope", [False, True])
+@pytest.mark.parametrize("dtype,lens,C,H,dc,dr,P,window,sinks,at", NOT_FINITE)
+def test_who_attends_a_row_that_is_not_finite_is_nan(kb, bad, rope, dtype, lens, C, H, dc, dr, P, window, sinks, at):
+    """Wherever the row lies and whatever its score: heads that meet an infinity with the other sign score minus
+    infinity, a weight of zero, and are NaN all the same."""
+    c = Case(kb, dtype, lens, C, H, dc, dr, P, seed=21)
+    part = dc + 3 if rope else dc // 2 + 1
+    for b, L in enumerate(lens):
+        c.buf[0].view(-1, c.W)[c.slots[b][L + at], part] = bad
+    c.run(window, sinks)
+    assert kb.kvp_sync_error(c.pool) == 0
+    for b, L in enumerate(lens):
+        for j in range(C):
+            if L + at in R.span(L - C + j, window, sinks):
+                assert bool(c.out[b, j].isnan().all()), f"request {b} query {j}"
+            else:
+                R.check(c.out[b, j], *c.want(b, j, C, window, sinks), f"request {b} query {j}")
+
+
+@pytest.mark.parametrize("dtype,C,H,dc,dr", [("bf16", 1, 16, 512, 64), ("bf16", 5, 40, 512, 64), ("f32", 2, 4, 64, 16)])
+def test_a_score_past_fp32_of_a_finite_row_weighs_nothing(kb, dtype, C, H, dc, dr):
+    """A finite row whose score overflows to minus infinity counts as the formula has it: not at all."""
+    c = Case(kb, dtype, [200, 67], C, H, dc, dr, 16, seed=22)
+    c.q[..., 3] = -100.0
+    rows = c.buf[0].view(-1, c.W)
+    for b, L in enumerate(c.lens):
+        rows[torch.tensor(c.slots[b], device=DEV), 3] = 0
+        for t in (5, L - C):  # one that all rows' blocks attend, one in the last block
+            rows[c.slots[b][t], 3] = 3e38
+    c.run()
+    for b, L in enumerate(c.lens):
+        for j in range(C):
+            sl = torch.tensor([c.slots[b][t] for t in range(L - C + j + 1) if t not in (5, L - C)], device=DEV)
+            x = rows[sl].double().cpu()
+            w, bound = R.attend(c.q[b, j].double().cpu(), x, x[:, :dc], c.scale, c.dt)
+            R.check(c.out[b, j], w, bound, f"request {b} query {j}")
