@@ -282,7 +282,10 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_tc_kernel(const __grid_c
           __syncwarp();
           redo = 0;
         }
-        if (redo < min(*(volatile int*)&sb.again, 8)) t = sb.redo[redo++];
+        // one lane's reading for all; after a wait that gave up the list may be half written
+        const int again = __shfl_sync(0xffffffffu, *(volatile int*)&sb.again, 0);
+        ok = ok && __all_sync(0xffffffffu, !*abort_flag);
+        if (ok && redo < min(again, 8)) t = sb.redo[redo++];
         publish(k, t);
         if (!t.nblk) break;
       }
@@ -331,7 +334,8 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_tc_kernel(const __grid_c
     bool ok = true;
     Tile t;
     for (int k = 0; ok && get_tile(k, t); ++k) {
-      const bool careful = *(volatile int*)&sb.careful;
+      // one lane's reading for all: an epilogue warp may set it at this moment
+      const bool careful = __shfl_sync(0xffffffffu, *(volatile int*)&sb.careful, 0);
       if (lane == 0) {
         sb.looked[k & 3] = careful;
         sb.poison[k & 3] = 0x7fffffff;

@@ -344,3 +344,19 @@ def test_latent_cache_steps(kb):
     cache.store(1, None, lat, pe, torch.arange(20, dtype=torch.int32, device=DEV), slots, rope, None)
     rows, start = cache.rows(1, [4])
     assert torch.equal(rows, torch.cat((lat, pe), -1)) and start.tolist() == [0, 20]
+
+
+def test_values_that_are_not_finite_give_the_same_bits(kb):
+    """Whichever SM takes a tile, and whether it has met such values before: tiles with and without them, several to
+    each SM, come out the same in every call."""
+    c = Case(kb, "bf16", [700, 130, 260, 40] * 5, [900, 130, 515, 40] * 5, 24, 128, 64, 128, seed=11)
+    for b in range(0, 20, 3):
+        for t in range(b % 7, c.kl[b], 97):
+            c.v[c.k0[b] + t, (b + t) % 24, t % 128] = float("nan") if t % 2 else float("inf")
+    c.run()
+    first = c.out.clone()
+    assert int(c.err) == 0 and not bool(first.isfinite().all())
+    for _ in range(15):
+        c.out.fill_(5.0)
+        c.run()
+        assert int(c.err) == 0 and torch.equal(first.view(torch.int16), c.out.view(torch.int16))
