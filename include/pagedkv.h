@@ -408,9 +408,11 @@ int paged_latent_attention(const kvp_pool* pool, int layer, const void* q,
  *   max_q the longest request's query rows (an upper bound is fine).
  *   nope_dim, rope_dim, v_dim  up to 512 each (rope_dim may be 0).
  *   out   device [total_q, num_heads, v_dim], contiguous.
- * An infinity or a NaN in a key or value reaches the queries that attend it
- * (a value among the newest keys may make all their entries of that head NaN),
- * and no others.
+ * An infinity or a NaN in a value makes that entry of that head not finite (NaN
+ * or an infinity) for the queries that attend it, and no other entry. In a key
+ * it reaches the queries that attend it by their scores, and no others: minus
+ * infinity weighs nothing, the others make the head's output NaN. A query all
+ * of whose scores are minus infinity gets zeros.
  * A request without queries is fine; rows of out that no request owns are not
  * written. A request whose offsets are out of order or out of range, or that
  * has more query rows than max_q or than key rows, sets KVP_ERR_BAD_INDEX in

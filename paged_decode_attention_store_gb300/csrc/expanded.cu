@@ -64,8 +64,8 @@ __global__ void __launch_bounds__(32 * kExpWarps) expanded_general_kernel(const 
     for (int sh = 16; sh > 0; sh >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, sh);
     const float s = dot * sl2;
     const float mn = fmaxf(m, s);
-    if (s == -INFINITY && m == -INFINITY) continue;  // a NaN goes on
-    const float alpha = exp2f(m - mn), p = exp2f(s - mn);
+    const bool none = s == -INFINITY && m == -INFINITY;  // nothing yet: its value still meets a weight of 0
+    const float alpha = none ? 1.f : exp2f(m - mn), p = none ? 0.f : exp2f(s - mn);
     l = l * alpha + p;
     m = mn;
 #pragma unroll

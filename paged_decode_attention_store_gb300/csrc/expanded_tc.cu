@@ -94,7 +94,8 @@ struct ExpBars {
   // Values that are not finite (see the epilogue). Rings of four tiles: the V loader is two
   // blocks ahead of the products, at most three tiles ahead of the epilogue.
   int careful;                      // such values have been met: V's masked blocks are looked through
-  int looked[4], poison[4];         // per tile: they were; the first key cleared
+  int looked[4], cleared[4];        // per tile: they were; such values were found
+  uint32_t first[4][kDv / 4];       // per tile: of an entry (a byte), the first key cleared, from the first row's own on; 255: none
   int again, again_bits, epilogues; // tiles to do once more; by their index mod 32; warps' tiles done
   Tile redo[8];
   float sums[2][kTile];
@@ -112,19 +113,27 @@ __device__ __forceinline__ void tma_2d(void* dst, const void* tmap, int c0, int 
       : "memory");
 }
 
-// Zeros in place of a V stage's rows r0 .. r1 - 1 that hold an infinity or a NaN (a warp);
-// the first of them, or kKeys.
-__device__ __noinline__ int clear_not_finite(unsigned char* stage, int r0, int r1, int lane) {
-  int first = kKeys;
-  for (int r = max(r0, 0) + lane; r < r1; r += 32) {
-    uint32_t bad = 0;
-    for (int x = 0; x < kVChunks * 32; ++x)
-      bad |= tc5::not_finite2(*reinterpret_cast<const uint32_t*>(stage + (x >> 5) * kChunk + r * 128 + (x & 31) * 4));
-    if (!bad) continue;
-    first = min(first, r);
-    for (int x = 0; x < kVChunks * 32; ++x) *reinterpret_cast<uint32_t*>(stage + (x >> 5) * kChunk + r * 128 + (x & 31) * 4) = 0u;
+// Zeros in place of the infinities and NaNs in a V stage's rows r0 .. r1 - 1 (a warp: a lane has four entries).
+// ``first``: per entry (a byte) the smallest r - r0 + base with one, 255: none. Returns whether there are any.
+__device__ __noinline__ bool clear_not_finite(unsigned char* stage, int r0, int r1, int base, uint32_t* first, int lane) {
+  uint32_t any = 0, mine = first[lane];
+  for (int r = r0; r < r1; ++r) {
+    uint32_t* at = reinterpret_cast<uint32_t*>(stage + (lane >> 4) * kChunk + r * 128 + ((((lane & 15) >> 1) ^ (r & 7)) << 4) + (lane & 1) * 8);
+    uint32_t cleared = 0;  // a byte for each of the four entries
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const uint32_t w = at[x];
+      const bool lo = (w & 0x7f80u) == 0x7f80u, hi = (w & 0x7f800000u) == 0x7f800000u;
+      if (lo || hi) at[x] = w & (lo ? 0xffff0000u : 0xffffffffu) & (hi ? 0x0000ffffu : 0xffffffffu);
+      cleared |= (lo ? 0xffu : 0u) << (16 * x) | (hi ? 0xff00u : 0u) << (16 * x);
+    }
+    if (cleared) {
+      any = 1;
+      mine = __vminu4(mine, (~cleared) | (uint32_t)(r - r0 + base) * 0x01010101u);
+    }
   }
-  return __reduce_min_sync(0xffffffffu, first);
+  first[lane] = mine;
+  return __any_sync(0xffffffffu, any);
 }
 
 // Ask for the index of a block that has not started; 16 bytes into ``dst``, counted on ``bar``.
@@ -338,8 +347,9 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_tc_kernel(const __grid_c
       const bool careful = __shfl_sync(0xffffffffu, *(volatile int*)&sb.careful, 0);
       if (lane == 0) {
         sb.looked[k & 3] = careful;
-        sb.poison[k & 3] = 0x7fffffff;
+        sb.cleared[k & 3] = 0;
       }
+      sb.first[k & 3][lane] = 0xffffffffu;
       __syncwarp();
       for (int i = 0; i < t.nblk; ++i, ++n) {
         const int st = n % kVS;
@@ -362,8 +372,10 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_tc_kernel(const __grid_c
             for (int c = 0; c < kVChunks; ++c)
               *reinterpret_cast<uint4*>(dst + c * kChunk + x * 16) = make_uint4(0u, 0u, 0u, 0u);
           if (look) {
-            const int first = clear_not_finite(dst, t.shift + 1 - i * kKeys, min(rows, kKeys), lane);
-            if (lane == 0 && first < kKeys) sb.poison[k & 3] = min(sb.poison[k & 3], i * kKeys + first);
+            // the keys after the tile's first row's own: fewer than a tile has rows, over at most two blocks
+            const int r0 = t.shift + 1 - i * kKeys;
+            if (clear_not_finite(dst, max(r0, 0), min(rows, kKeys), max(r0, 0) - r0, sb.first[k & 3], lane) && lane == 0)
+              sb.cleared[k & 3] = 1;
           }
           fence_proxy_async_smem();
           __syncwarp();
@@ -561,9 +573,9 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_tc_kernel(const __grid_c
       if (!ok) break;
       tc5::fence_after();
       const float tot = *(volatile float*)&sb.sums[k & 1][row];
+      const bool met = *(volatile int*)&sb.cleared[k & 3];
       // a NaN sum is the answer of a NaN score
-      const bool none = t.shift + row >= *(volatile int*)&sb.poison[k & 3];
-      const float inv = none ? __int_as_float(0x7fffffff) : tot == 0.f ? 0.f : 1.f / tot;
+      const float inv = tot == 0.f ? 0.f : 1.f / tot;
       float odd = 0.f;  // NaN once an entry of O is not finite
       // all of O to registers, packed, before the stores: the next tile's first product waits for it
       uint32_t w[kDv / 2];
@@ -577,11 +589,19 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_tc_kernel(const __grid_c
 #pragma unroll
         for (int q = 0; q < 16; ++q) odd = fmaf(ov[q], 0.f, odd);
       }
+      if (met) {  // NaN where an entry met a value that was cleared, one of a key up to the row's own
+#pragma unroll
+        for (int q = 0; q < kDv / 4; ++q) {
+          const uint32_t hit = __vcmpltu4(*(volatile uint32_t*)&sb.first[k & 3][q], (uint32_t)row * 0x01010101u);
+          w[2 * q] |= __byte_perm(hit, 0, 0x1100) & 0x7fff7fffu;
+          w[2 * q + 1] |= __byte_perm(hit, 0, 0x3322) & 0x7fff7fffu;
+        }
+      }
       // A weight of 0 does not keep an infinity or a NaN of V out of O. It is rare enough
       // that a look through V's masked blocks, 1.4 us each, waits until an O that is no
       // number shows up under a sum that is one: from then on such values that some row
-      // does not attend become zeros (rows that do attend one become NaN here), and the
-      // tiles that were already under way are done again.
+      // does not attend become zeros (that entry of the rows that do becomes NaN here), and
+      // the tiles that were already under way are done again.
       if (__any_sync(0xffffffffu, odd != odd && tot == tot && row < t.jn && !*(volatile int*)&sb.looked[k & 3]) && lane == 0) {
         sb.careful = 1;
         if (!(atomicOr(&sb.again_bits, 1 << (k & 31)) >> (k & 31) & 1)) {

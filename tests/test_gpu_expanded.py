@@ -360,3 +360,51 @@ def test_values_that_are_not_finite_give_the_same_bits(kb):
         c.out.fill_(5.0)
         c.run()
         assert int(c.err) == 0 and torch.equal(first.view(torch.int16), c.out.view(torch.int16))
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("dtype,dn,dr,dv", [("bf16", 128, 64, 128), ("bf16", 64, 32, 64), ("f32", 128, 64, 128)])
+def test_a_value_that_is_not_finite_reaches_its_entry_alone(kb, bad, dtype, dn, dr, dv):
+    """Of the head it is in, for the queries that attend it, wherever in their keys it lies; all else is the formula's."""
+    H = 3
+    c = Case(kb, dtype, [150, 70, 260, 1, 3], [300, 70, 260, 200, 3], H, dn, dr, dv, seed=8)
+    entries = {}  # (request, head) -> (key, entry) that are not finite
+    for b, keys in enumerate([(40, 160, 280), (20, 61), (0, 127, 128, 130, 255), (3, 199), (1,)]):
+        for i, t in enumerate(keys):
+            h, d = i % 2, (37 * i + 9) % dv
+            c.v[c.k0[b] + t, h, d] = bad
+            entries.setdefault((b, h), []).append((t, d))
+    for _ in range(2):
+        c.out.fill_(5.0)
+        c.run()
+        assert int(c.err) == 0
+        out, q, v = c.out.cpu(), c.q.double().cpu(), c.v.double().cpu()
+        v[~v.isfinite()] = 0.0
+        key = torch.cat((c.k.double().cpu(), c.pe.double().cpu()[:, None].expand(-1, H, -1)), -1)
+        for b in range(len(c.ql)):
+            first = c.kl[b] - c.ql[b]
+            near = {t + x for h in range(H) for t, _ in entries.get((b, h), []) for x in (-1, 0, 1)}
+            for p in sorted((near | {first, c.kl[b] - 1}) & set(range(first, c.kl[b]))):
+                keys = slice(c.k0[b], c.k0[b] + p + 1)
+                w, bound = R.attend(q[c.q0[b] + p - first], key[keys], v[keys], c.scale, c.dt)
+                hit = torch.zeros((H, dv), dtype=torch.bool)
+                for h in range(H):
+                    for t, d in entries.get((b, h), []):
+                        hit[h, d] |= t <= p
+                got = out[c.q0[b] + p - first]
+                assert not bool(got[hit].isfinite().any()), f"request {b} position {p}"
+                R.check(got[~hit], w[~hit], bound[~hit], f"request {b} position {p}")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_value_that_is_not_finite_under_a_score_of_minus_infinity(kb, dtype):
+    """A weight of zero does not keep it from its entry, as the formula has it, in whatever order the keys come."""
+    for t in (0, 5, 140, 149):
+        c = Case(kb, dtype, [150], [150], 2, 128, 64, 128, seed=9)
+        c.q[:, 1, 4] = 1.0
+        c.k[t, 1, 4] = -float("inf")
+        c.v[t, 1, 7] = float("inf")
+        c.run()
+        hit = torch.zeros((150, 2, 128), dtype=torch.bool)
+        hit[t:, 1, 7] = True
+        assert not bool(c.out.cpu()[hit].isfinite().any()) and bool(c.out.cpu()[~hit].isfinite().all())
