@@ -159,6 +159,24 @@ def _dev(t, dtype=None, name="tensor"):
     return t
 
 
+def _elsewhere(t, index, name):
+    """The refusal of what is no tensor on the CUDA device of that index."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    raise ValueError(f"{name} must be on device {index}, got {t.device}")
+
+
+def _on(t, index, dtype, name):
+    """_dev, on the CUDA device of that index."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != index:
+        _elsewhere(t, index, name)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    return t
+
+
 def _stream(stream):
     if stream is None:
         stream = torch.cuda.current_stream()
@@ -180,6 +198,7 @@ class Pool:
         _, self.num_layers, self.num_pages, self.page_size, self.kv_heads, self.head_dim = kv_buffer.shape
         self.dtype = dtype
         self.kv_buffer = kv_buffer
+        self.device_index = kv_buffer.get_device()
         self.error_word = (torch.zeros(1, dtype=torch.int32, device=kv_buffer.device)
                            if error_word is None else _dev(error_word, torch.int32, "error_word"))
         h = ctypes.c_void_p()
@@ -216,8 +235,9 @@ class LatentPool:
         self.latent_dim, self.rope_dim, self.kv_heads, self.head_dim = latent_dim, width - latent_dim, 1, width
         self.dtype = dtype
         self.kv_buffer = buffer
+        self.device_index = buffer.get_device()
         self.error_word = (torch.zeros(1, dtype=torch.int32, device=buffer.device)
-                           if error_word is None else _dev(error_word, torch.int32, "error_word"))
+                           if error_word is None else _on(error_word, self.device_index, torch.int32, "error_word"))
         h = ctypes.c_void_p()
         with torch.cuda.device(buffer.device):
             _check(lib().kv_latent_pool_create(self.num_pages, self.page_size, latent_dim, self.rope_dim, dtype,
@@ -277,10 +297,11 @@ def _raw_stream(stream):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _heads_view(t, dt, name, heads, width):
-    """(address, stride of a token, stride of a head, heads) of a [n, heads, width] view whose last axis is contiguous."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
+def _heads_view(t, index, dt, name, heads, width):
+    """(address, stride of a token, stride of a head, heads) of a [n, heads, width] view on device ``index`` whose last
+    axis is contiguous."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != index:
+        _elsewhere(t, index, name)
     if t.dtype != dt:
         raise TypeError(f"{name} must be {dt}, got {t.dtype}")
     shape = t.shape
@@ -297,10 +318,11 @@ def _heads_view(t, dt, name, heads, width):
     return t.data_ptr(), st, sh, h
 
 
-def _rows_view(t, dt, name, n, heads, width):
-    """(address, stride of a token) of [n, heads, width] (or, for one head, [n, width]) with each token's row contiguous."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
+def _rows_view(t, index, dt, name, n, heads, width):
+    """(address, stride of a token) of [n, heads, width] (or, for one head, [n, width]) on device ``index`` with each
+    token's row contiguous."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != index:
+        _elsewhere(t, index, name)
     if t.dtype != dt:
         raise TypeError(f"{name} must be {dt}, got {t.dtype}")
     shape, stride = t.shape, t.stride()
@@ -316,8 +338,10 @@ def _rows_view(t, dt, name, n, heads, width):
 def _rotary_call(fn, what, pool, layer, q, first, second, positions, out_loc, rope, q_out, width, stream):
     """Marshals rotary_store_cache and rotary_store_latent: ``first`` and ``second`` are the two row inputs in the
     order of the C call, each (tensor, name, heads, width)."""
-    dt = _TORCH_DTYPE[pool.dtype]
-    n = _dev(positions, torch.int32, "positions").numel()
+    dt, dev = _TORCH_DTYPE[pool.dtype], pool.device_index
+    n = _on(positions, dev, torch.int32, "positions").numel()
+    if rope.rotary_dim and rope.freqs.get_device() != dev:
+        _elsewhere(rope.freqs, dev, "the plan's frequencies")
     k, v = first[0], second[0]
     if (k is None) != (v is None):
         raise ValueError(f"{first[1]} and {second[1]} come together")
@@ -325,16 +349,16 @@ def _rotary_call(fn, what, pool, layer, q, first, second, positions, out_loc, ro
         raise ValueError(f"the plan turns {rope.rotary_dim} entries of {width}")
     qp = qt = qh = heads = op = ot = oh = kp = kt = vp = vt = loc = 0
     if q is not None:
-        qp, qt, qh, heads = _heads_view(q, dt, "q", None, width)
-        op, ot, oh, _ = _heads_view(q_out, dt, "q_out", heads, width)
+        qp, qt, qh, heads = _heads_view(q, dev, dt, "q", None, width)
+        op, ot, oh, _ = _heads_view(q_out, dev, dt, "q_out", heads, width)
         if q.shape[0] != n or q_out.shape[0] != n:
             raise ValueError("the queries and their output must hold one row per position")
     elif k is None:
         raise ValueError("neither queries nor keys")
     if k is not None:
-        kp, kt = _rows_view(k, dt, first[1], n, first[2], first[3])
-        vp, vt = _rows_view(v, dt, second[1], n, second[2], second[3])
-        if _dev(out_loc, torch.int32, "out_loc").numel() != n:
+        kp, kt = _rows_view(k, dev, dt, first[1], n, first[2], first[3])
+        vp, vt = _rows_view(v, dev, dt, second[1], n, second[2], second[3])
+        if _on(out_loc, dev, torch.int32, "out_loc").numel() != n:
             raise ValueError("out_loc and positions must have the same length")
         loc = out_loc.data_ptr()
     _check(fn(pool.handle, layer, qp, qt, qh, heads, kp, kt, vp, vt, positions.data_ptr(), loc, n, rope.freqs.data_ptr(),
@@ -380,11 +404,11 @@ def paged_latent_attention(pool, layer, q, table, table_mode, context_lens, wind
     context_lens[b] - q_lens[b] + j (q_lens None: C) and attends causally
     (decode: C = 1). Rows j >= q_lens[b] are not written. See
     include/pagedkv.h."""
-    dt = _TORCH_DTYPE[pool.dtype]
-    _dev(q, dt, "q")
-    _dev(out, dt, "out")
-    _dev(table, torch.int32, "table")
-    _dev(context_lens, torch.int32, "context_lens")
+    dt, dev = _TORCH_DTYPE[pool.dtype], pool.device_index
+    _on(q, dev, dt, "q")
+    _on(out, dev, dt, "out")
+    _on(table, dev, torch.int32, "table")
+    _on(context_lens, dev, torch.int32, "context_lens")
     shape = q.shape
     if len(shape) != 4 or shape[3] != pool.head_dim or out.shape != (*shape[:3], pool.latent_dim):
         raise ValueError("q must be [B, C, Hq, latent_dim + rope_dim] and out [B, C, Hq, latent_dim]")
@@ -392,13 +416,13 @@ def paged_latent_attention(pool, layer, q, table, table_mode, context_lens, wind
     per = [0, 0]
     for i, (t, nm) in enumerate(((q_lens, "q_lens"), (table_rows, "table_rows"))):
         if t is not None:
-            if _dev(t, torch.int32, nm).numel() != B:
+            if _on(t, dev, torch.int32, nm).numel() != B:
                 raise ValueError(f"{nm} must be [B]")
             per[i] = t.data_ptr()
     if context_lens.numel() != B:
         raise ValueError("context_lens must be [B]")
     rows, cols = table.shape
-    ws_ptr, ws_bytes = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
+    ws_ptr, ws_bytes = (0, 0) if workspace is None else (_on(workspace, dev, None, "workspace").data_ptr(), workspace.nbytes)
     _check(lib().paged_latent_attention(pool.handle, layer, q.data_ptr(), B, C, Hq, per[0], table.data_ptr(), rows, cols,
                                         table_mode, per[1], context_lens.data_ptr(), int(window or 0), int(sinks),
                                         float(scale), out.data_ptr(), ws_ptr, ws_bytes, _raw_stream(stream)),
@@ -414,6 +438,9 @@ def latent_prefill_attention(q, k, k_pe, v, q_start, k_start, max_q, scale, out,
     dt = q.dtype
     if dt not in (torch.float32, torch.bfloat16):
         raise TypeError(f"q must be float32 or bfloat16, got {dt}")
+    dev = q.get_device()
+    if dev < 0:
+        _elsewhere(q, dev, "q")
     if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
         raise ValueError("q, k and v must be [tokens, heads, entries]")
     tq, H, width = q.shape
@@ -422,19 +449,19 @@ def latent_prefill_attention(q, k, k_pe, v, q_start, k_start, max_q, scale, out,
     dr = width - dn
     if dr < 0 or (dr > 0) != (k_pe is not None):
         raise ValueError("q must be as wide as k and k_pe together")
-    qa = _heads_view(q, dt, "q", None, width)[:3]
-    ka = _heads_view(k, dt, "k", H, dn)[:3]
-    va = _heads_view(v, dt, "v", H, dv)[:3]
-    pa = (0, 0) if k_pe is None else _rows_view(k_pe, dt, "k_pe", tk, 1, dr)
-    _dev(out, dt, "out")
-    _dev(q_start, torch.int32, "q_start")
-    _dev(k_start, torch.int32, "k_start")
+    qa = _heads_view(q, dev, dt, "q", None, width)[:3]
+    ka = _heads_view(k, dev, dt, "k", H, dn)[:3]
+    va = _heads_view(v, dev, dt, "v", H, dv)[:3]
+    pa = (0, 0) if k_pe is None else _rows_view(k_pe, dev, dt, "k_pe", tk, 1, dr)
+    _on(out, dev, dt, "out")
+    _on(q_start, dev, torch.int32, "q_start")
+    _on(k_start, dev, torch.int32, "k_start")
     B = q_start.numel() - 1
     if v.shape[0] != tk or out.shape != (tq, H, dv) or B < 0 or k_start.numel() != B + 1:
         raise ValueError("v must hold k's tokens, out be [total_q, H, dv], q_start and k_start [B + 1]")
     if B == 0:
         return
-    err = 0 if error_word is None else _dev(error_word, torch.int32, "error_word").data_ptr()
+    err = 0 if error_word is None else _on(error_word, dev, torch.int32, "error_word").data_ptr()
     _check(lib().latent_prefill_attention(*qa, *ka, *pa, *va, q_start.data_ptr(), k_start.data_ptr(), B, H, int(max_q), tq,
                                           tk, dn, dr, dv, KVP_F32 if dt == torch.float32 else KVP_BF16, float(scale),
                                           out.data_ptr(), err, _raw_stream(stream)), "latent_prefill_attention")

@@ -129,10 +129,13 @@ extern "C" int latent_prefill_attention(const void* q, long long q_stride, long 
   if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v) |
        reinterpret_cast<uintptr_t>(k_pe) | reinterpret_cast<uintptr_t>(out)) & em)
     return KVP_ERR_INVALID_ARG;
-  for (const void* p : {q, k, v, static_cast<const void*>(out)}) {  // another device's memory
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return KVP_ERR_CUDA;
+  for (const void* p : {q, k, k_pe, v, static_cast<const void*>(out), static_cast<const void*>(q_start),
+                        static_cast<const void*>(k_start), static_cast<const void*>(error_word)}) {  // another device's memory
     cudaPointerAttributes at;
-    int dev = -1;
-    if (cudaPointerGetAttributes(&at, p) != cudaSuccess || cudaGetDevice(&dev) != cudaSuccess) return KVP_ERR_CUDA;
+    if (!p) continue;
+    if (cudaPointerGetAttributes(&at, p) != cudaSuccess) return KVP_ERR_CUDA;
     if (at.type == cudaMemoryTypeDevice && at.device != dev) return KVP_ERR_INVALID_ARG;
   }
   if (max_q > total_q) max_q = total_q;
