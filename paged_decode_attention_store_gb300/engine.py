@@ -371,8 +371,10 @@ class PagedLatentCache(PagedKVCache):
     rows and rotates the queries' key part (:meth:`store`) and attends in the
     latent space (:meth:`attend`: decode, multi-token verify and chunks). Long
     prompts are cheaper in expanded form: project :meth:`rows` up and call
-    :func:`binding.latent_prefill_attention`. Calls of one shape share a
-    workspace: those of one cache run one after another on the GPU."""
+    :func:`binding.latent_prefill_attention`. All calls of a cache share a
+    workspace: they, and replays of graphs that hold them, run one after another
+    on the GPU (calls that overlap take their own:
+    :func:`binding.paged_latent_attention`)."""
 
     def __init__(self, num_pages, page_size, latent_dim, rope_dim, num_layers, dtype="bf16", max_requests=256,
                  table_mode="block", max_seq_len=None, free_stack=None, device="cuda", zero=True):
@@ -380,6 +382,7 @@ class PagedLatentCache(PagedKVCache):
         super().__init__(num_pages, page_size, 1, latent_dim + rope_dim, num_layers, dtype=dtype,
                          max_requests=max_requests, table_mode=table_mode, max_seq_len=max_seq_len,
                          free_stack=free_stack, device=device, zero=zero)
+        self._need, self._largest = {}, 0
 
     def _make_pool(self, alloc, pages, kdt):
         self.kv = alloc((self.layers, pages, self.P, self.D), dtype=self.tdt, device=self.dev)
@@ -393,10 +396,16 @@ class PagedLatentCache(PagedKVCache):
                                None if q is None else q[..., self.latent_dim:])
 
     def workspace(self, batch, num_q_heads, chunk=1):
+        """The cache's workspace, for calls of this shape among others: one that grows. Outgrown ones are kept, as a
+        captured graph may hold them: a pool has half a dozen sizes, 10 to 40 MB, whatever the batches and chunks."""
         key = (batch, num_q_heads, chunk)
-        if key not in self._ws:
-            self._ws[key] = kb.alloc_latent_workspace(self.pool, batch, chunk, num_q_heads, device=self.dev)
-        return self._ws[key]
+        need = self._need.get(key)
+        if need is None:
+            need = self._need[key] = kb.paged_latent_attention_workspace_size(self.pool, batch, chunk, num_q_heads)
+        if need > self._largest:
+            self._ws[need] = torch.empty(need, dtype=torch.uint8, device=self.dev)
+            self._largest = need
+        return self._ws[self._largest]
 
     def attend(self, layer, q, context_lens, window, scale, out, q_lens=None, table_rows=None, sinks=0):
         """Absorbed attention: q [B, C, Hq, latent_dim + rope_dim], out [B, C,

@@ -420,3 +420,52 @@ def test_a_score_past_fp32_of_a_finite_row_weighs_nothing(kb, dtype, C, H, dc, d
             x = rows[sl].double().cpu()
             w, bound = R.attend(c.q[b, j].double().cpu(), x, x[:, :dc], c.scale, c.dt)
             R.check(c.out[b, j], w, bound, f"request {b} query {j}")
+
+
+def test_the_cache_has_one_workspace_for_all_shapes(kb):
+    """Many batches and chunk lengths take no more memory than the largest few, and a graph captured on a smaller
+    workspace replays after larger calls have come."""
+    from paged_decode_attention_store_gb300.engine import PagedLatentCache
+
+    dc, dr, H = 512, 64, 8
+    cache = PagedLatentCache(64, 16, dc, dr, 1, max_requests=8)
+    g = torch.Generator().manual_seed(1)
+    rnd = lambda *s: torch.randn(s, generator=g).bfloat16().to(DEV)  # noqa: E731
+    rope = kb.RotaryPlan(dr, device=DEV)
+    cache.new(0)
+    L = 200
+    slots = cache.append([0] * L)
+    cache.store(0, None, rnd(L, dc), rnd(L, dr), torch.arange(L, dtype=torch.int32, device=DEV), slots, rope, None)
+    lens = torch.tensor([L], dtype=torch.int32, device=DEV)
+    scale = (dc + dr) ** -0.5
+    x = cache.rows(0, [0])[0].double().cpu()
+
+    def right(q, out):
+        C = q.shape[1]
+        for j in {0, C - 1}:
+            keys = x[:L - C + j + 1]
+            R.check(out[0, j], *R.attend(q[0, j].double().cpu(), keys, keys[:, :dc], scale, torch.bfloat16))
+
+    q1, out1 = rnd(1, 1, H, dc + dr), torch.empty((1, 1, H, dc), dtype=torch.bfloat16, device=DEV)
+    cache.attend(0, q1, lens, 0, scale, out1)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cache.attend(0, q1, lens, 0, scale, out1)
+    held = torch.cuda.memory_allocated()
+    sizes = set()
+    for B in range(1, 33):
+        for C in (1, 2, 3, 5, 8, 33, 64):
+            need = kb.paged_latent_attention_workspace_size(cache.pool, B, C, H)
+            assert cache.workspace(B, H, C).nbytes >= need
+            sizes.add(need)
+    assert len({t.data_ptr() for t in cache._ws.values()}) <= len(sizes) <= 6
+    assert torch.cuda.memory_allocated() - held <= sum(sizes) + 512 * len(sizes)
+    for C in (1, 3, 64, 150, 2):
+        q, out = rnd(1, C, H, dc + dr), torch.empty((1, C, H, dc), dtype=torch.bfloat16, device=DEV)
+        cache.attend(0, q, lens, 0, scale, out)
+        right(q, out)
+    out1.fill_(5.0)
+    graph.replay()
+    torch.cuda.synchronize()
+    right(q1, out1)
+    cache.check()
