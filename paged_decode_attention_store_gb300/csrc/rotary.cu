@@ -8,10 +8,14 @@
 // the interleaved one. The angle p theta_i reaches 10^6 radians and more, where
 // 32-bit floats are off by 0.03 rad and more, so it is kept as turns in 64-bit
 // fixed point: f_i = theta_i / 2 pi mod 1 scaled by 2^64, p * f_i mod 2^64 is
-// the exact fraction of a turn (the product wraps as turns do), and
-// sincospif() of the fraction rounded to float is good to 2^-24 of a turn for
-// every int32 position, negative ones too. One 64-bit multiplication replaces
-// both double arithmetic and a table of angles.
+// the exact fraction of a turn (the product wraps as turns do), for every int32
+// position, negative ones too. The nearest quarter turn is taken off it in
+// integers and put back by exchanging sine and cosine and their signs; what is
+// left, pi / 4 at most, is rounded to float once, relative to itself, so that
+// sines and cosines are good to two units in the last place near their zeros too
+// (the whole fraction rounded to float was off by 2^-25 of half a turn: 1.3 times
+// the fp32 store's error). One 64-bit multiplication replaces both double
+// arithmetic and a table of angles.
 //
 // What bounds it: bytes. Each token is read and written once (q, k, v) and
 // there are 3 flops per byte at most. A block takes 1 to 4 tokens: its threads
@@ -59,10 +63,15 @@ struct RotArgs {
 // (cos, sin) * attn of position p and the pair's frequency f (turns * 2^64).
 __device__ __forceinline__ float2 turn_of(int p, uint64_t f, float attn) {
   const uint64_t t = (uint64_t)(int64_t)p * f;
-  const float half_turns = (float)(int32_t)(uint32_t)(t >> 32) * 0x1p-31f;  // [-1, 1): angle / pi
+  const uint32_t quarters = ((uint32_t)(t >> 32) + (1u << 29)) >> 30;
+  // [-1/4, 1/4]: the rest's angle / pi, its bits down to 2^-34 of a turn (bits 30 to 61 with bit 61 as the sign: it is
+  // the one that rounded ``quarters`` up)
+  const float half_turns = (float)(int32_t)(uint32_t)(t >> 30) * 0x1p-33f;
   float s, c;
   sincospif(half_turns, &s, &c);
-  return make_float2(c * attn, s * attn);
+  const bool odd = quarters & 1;  // (c, s) -> (-s, c) a quarter
+  const float x = odd ? s : c, y = odd ? c : s;
+  return make_float2(((quarters + 1) & 2 ? -x : x) * attn, (quarters & 2 ? -y : y) * attn);
 }
 
 template <typename T>
@@ -104,9 +113,10 @@ struct RotUnit {
   const float4* f;  // two pairs' turns, the next two ``rot_units`` further
 };
 
-// 16-byte chunks: every row, stride and half of a pair block starts on 16 bytes.
+// 16-byte chunks: every row, stride and half of a pair block starts on 16 bytes. The fp32 interleaved form is held to
+// 48 registers, ten blocks an SM (the 56 it takes by itself: 9.1 us for 8.1 at 3,001 tokens); bounds cost the others.
 template <typename T, bool HALF>
-__global__ void __launch_bounds__(kRotThreads) rotary_store_kernel(const RotArgs a) {
+__global__ void __launch_bounds__(kRotThreads, !HALF && sizeof(T) == 4 ? 10 : 0) rotary_store_kernel(const RotArgs a) {
   constexpr int N = Vec<T>::N;
   constexpr int kV = 2;  // chunks of v a thread loads ahead
   constexpr int PU = HALF ? N : N / 2;  // pairs of a unit
@@ -225,7 +235,7 @@ __global__ void __launch_bounds__(kRotThreads) rotary_store_kernel(const RotArgs
   for (int i = 0; i < kV; ++i)
     if (tid + i * kRotThreads < v_jobs) v_put(tid + i * kRotThreads, vw[i]);
   for (int c = tid + kV * kRotThreads; c < v_jobs; c += kRotThreads) v_put(c, __ldg(v_src(c)));
-  for (int u = u0; u < units; u += upar) {  // more than one round only for heads of more than 256 units
+  for (int u = u0; u < units; u += upar) {  // more than one round only for heads of more than 128 units
     for (int j = g; j < jobs; j += 2 * groups) {
       if (j != g || u != u0) {
         load(j, u, x0, k0);

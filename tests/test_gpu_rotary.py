@@ -311,3 +311,35 @@ def test_refusals(kb):
     call(pool, 0, q[:0], k[:0], v[:0], pos[:0], loc[:0], rope, out[:0])  # nothing to do
     torch.cuda.synchronize()
     assert kb.kvp_sync_error(pool) == 0
+
+
+@pytest.mark.parametrize("layout,D", [("half", 64), ("interleaved", 64), ("half", 12)])
+def test_sines_and_cosines_keep_their_bits(kb, layout, D):
+    """The turned pair (1, 0) is (cos, sin). With a turn's quadrant taken off exactly, what is left of the angle, t with
+    |t| <= pi / 4, is rounded to fp32 once (U32 |t|; the bits below 2^-34 of a turn, 0.006 U32, are cut), and sincospif is
+    within one unit in the last place (2 U32 of the value). With |t| <= 1.12 |sin t| the sine of it is off by (3.12 |sin t|
+    + 0.007) U32, the cosine by (0.57 + 2 |cos t|) U32 <= 2.9 |cos t| U32. 355, 710 and the like lie next to multiples of pi."""
+    import math
+    from fractions import Fraction
+
+    pos = [0, 1, 2, 3, 11, 22, 33, 44, 88, 355, 710, 1065, 51819, 52174, 103993, 104348, 1000003, 2 ** 31 - 1, -355, -2 ** 31]
+    n, rot = len(pos), D
+    buf = torch.zeros((2, 1, 8, 4, 1, D), device=DEV)
+    pool = kb.Pool(buf, 4, kb.KVP_F32)
+    rope = kb.RotaryPlan(rot, layout=layout, device=DEV)
+    first = slice(0, rot // 2) if layout == "half" else slice(0, rot, 2)
+    second = slice(rot // 2, rot) if layout == "half" else slice(1, rot, 2)
+    q = torch.zeros((n, 1, D), device=DEV)
+    q[..., first] = 1.0
+    out = torch.empty_like(q)
+    kb.rotary_store_cache(pool, 0, q, None, None, torch.tensor(pos, dtype=torch.int32, device=DEV), None, rope, out)
+    want_c, want_s = torch.empty((n, rot // 2), dtype=torch.float64), torch.empty((n, rot // 2), dtype=torch.float64)
+    for x, p in enumerate(pos):
+        for i, f in enumerate(kb.rotary_frequencies(rot)):
+            t = p * f % (1 << 64)
+            k = (t + (1 << 61)) >> 62  # the nearest quarter turn
+            a = 2 * math.pi * float(Fraction(t - (k << 62), 1 << 64))
+            c, s = math.cos(a), math.sin(a)
+            want_c[x, i], want_s[x, i] = ((c, s), (-s, c), (-c, -s), (s, -c))[k % 4]
+    for got, want in ((out[:, 0, first], want_c), (out[:, 0, second], want_s)):
+        R.check(got, want, R.U32 * (3.2 * want.abs() + 0.01), layout)
