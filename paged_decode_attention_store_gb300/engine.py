@@ -422,20 +422,26 @@ class PagedLatentCache(PagedKVCache):
         filled from ``q_pe`` [B, C, Hq, rope_dim] rotated), ``latent`` [B * C,
         latent_dim], ``k_pe`` [B * C, rope_dim] (request-major), ``out`` [B, C,
         Hq, latent_dim]. With a window, the pages it leaves are released
-        afterwards. Asynchronous on the current stream."""
+        afterwards. A step that is refused leaves the lengths and pages as they
+        were. Asynchronous on the current stream."""
         B, C, Hq, W = q[0].shape
         r = np.ascontiguousarray(rids, dtype=np.int32)
         if len(r) != B or len(np.unique(r)) != B:
             raise ValueError(f"step takes {B} distinct requests, got {list(map(int, r))}")
         before = self.lengths[r].copy()
         out_loc = self.append(np.repeat(r, C))
-        flat = np.concatenate((before + C, r, (before[:, None] + np.arange(C)).ravel()))
-        d = self._to_device(flat)
-        lens, rows, positions = d[:B], d[B:2 * B], d[2 * B:]
-        for layer in range(self.layers):
-            self.store(layer, q_pe[layer].view(B * C, Hq, self.rope_dim), latent[layer], k_pe[layer], positions,
-                       out_loc, rope, q[layer].view(B * C, Hq, W))
-            self.attend(layer, q[layer], lens, window, scale, out[layer], table_rows=rows, sinks=sinks)
+        try:
+            flat = np.concatenate((before + C, r, (before[:, None] + np.arange(C)).ravel()))
+            d = self._to_device(flat)
+            lens, rows, positions = d[:B], d[B:2 * B], d[2 * B:]
+            for layer in range(self.layers):
+                self.store(layer, q_pe[layer].view(B * C, Hq, self.rope_dim), latent[layer], k_pe[layer], positions,
+                           out_loc, rope, q[layer].view(B * C, Hq, W))
+                self.attend(layer, q[layer], lens, window, scale, out[layer], table_rows=rows, sinks=sinks)
+        except Exception:
+            for rid in r[::-1]:  # the last page taken goes back first
+                self.rewind(int(rid), C)
+            raise
         if window and window > 0:
             for i, rid in enumerate(r):
                 self.trim(int(rid), max(0, int(before[i]) + C + 1 - (window - sinks)), sinks=sinks)

@@ -140,3 +140,32 @@ def test_windowed_steps_put_queries_at_their_positions(kb):
             off = R.u(s.dt) * (q[0][0, j, :, 512:].double().cpu().abs() @ keys[:, 512:].abs().T).amax(-1) * s.scale
             weights = torch.softmax(q[0][0, j].double().cpu() @ keys.T * s.scale, -1)
             R.check(out[0][0, j], w, bound + (2 * torch.expm1(off))[:, None] * (weights @ keys[:, :512].abs()), f"query {j}")
+
+
+def test_a_step_that_is_refused_leaves_the_cache_as_it_was(kb):
+    s = Steps(kb, "bf16", 512, 64, 8, 16, "block", "half", "none")
+    s.cache.new(0)
+    s.cache.new(1)
+    s.step([0, 1], 30)
+    before, free = s.cache.lengths.copy(), s.cache.host.free_list()
+    table = s.cache.table.clone()
+    B, C, H, dc, dr = 2, 5, s.H, s.dc, s.dr
+    good = dict(q=s.rnd(B, C, H, dc + dr), q_pe=s.rnd(B, C, H, dr), latent=s.rnd(B * C, dc), k_pe=s.rnd(B * C, dr),
+                out=torch.empty((B, C, H, dc), dtype=s.dt, device=DEV), window=0, sinks=0, scale=s.scale, plan=s.plan)
+
+    def call(**kw):
+        a = {**good, **kw}
+        s.cache.step([0, 1], *([a[x]] * 2 for x in ("q", "q_pe", "latent", "k_pe")), a["plan"], [a["out"]] * 2, a["window"],
+                     a["scale"], sinks=a["sinks"])
+
+    for kw in (dict(latent=s.rnd(B * C - 1, dc)), dict(k_pe=s.rnd(B * C, dr + 8)), dict(latent=good["latent"].float()),
+               dict(out=good["out"][..., :8]), dict(window=4, sinks=4), dict(scale=float("nan")),
+               dict(plan=kb.RotaryPlan(2 * dr, device=DEV)), dict(plan=kb.RotaryPlan(dr, device="cpu"))):
+        with pytest.raises((ValueError, TypeError, kb.KvpError)):
+            call(**kw)
+        assert (s.cache.lengths == before).all() and s.cache.host.free_list() == free
+        assert [s.cache.host.length(r)[0] for r in (0, 1)] == [30, 30]
+    torch.cuda.synchronize()
+    assert torch.equal(s.cache.table, table)
+    s.step([0, 1], C)
+    s.step([1, 0], 1)
