@@ -450,19 +450,24 @@ class PagedLatentCache(PagedKVCache):
         """The stored rows of requests ``rids`` in logical order, [total,
         latent_dim + rope_dim], and their offsets int32 [len(rids) + 1]: what
         the projections of the expanded form take. A request that a window
-        has taken pages from has no such rows left (ValueError)."""
+        has taken pages from has no such rows left (ValueError). Waits for the
+        GPU, to see that; not for capture into a graph."""
         r = np.ascontiguousarray(rids, dtype=np.int32)
         lens = self.lengths[r]
-        d = self._to_device(np.concatenate((lens, r, [0], np.cumsum(lens))))
-        n = len(r)
-        slots = torch.empty((n, max(1, int(lens.max(initial=0)))), dtype=torch.int32, device=self.dev)
+        some = lens > 0
+        n = int(some.sum())
+        d = self._to_device(np.concatenate((lens[some], r[some], [0], np.cumsum(lens))))
+        start = d[2 * n:]
+        if n == 0:
+            return self.kv[layer].view(-1, self.D)[:0], start
+        slots = torch.empty((n, int(lens.max())), dtype=torch.int32, device=self.dev)
         kb.gather_indices(self.pool, self.table, self.table_mode, d[:n], 0, slots, table_rows=d[n:2 * n])
         live = torch.arange(slots.shape[1], device=self.dev)[None, :] < d[:n, None]
         slots = slots[live].long()
         if bool((slots < 0).any()):
             kb.kvp_sync_error(self.pool)  # what the gather recorded of it
             raise ValueError("a request's first pages are released")
-        return self.kv[layer].view(-1, self.D)[slots], d[2 * n:]
+        return self.kv[layer].view(-1, self.D)[slots], start
 
     def _unsupported(self, what):
         raise TypeError(f"{what} reads separate K and V: a latent cache uses store, attend and step")

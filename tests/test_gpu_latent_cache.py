@@ -169,3 +169,18 @@ def test_a_step_that_is_refused_leaves_the_cache_as_it_was(kb):
     assert torch.equal(s.cache.table, table)
     s.step([0, 1], C)
     s.step([1, 0], 1)
+
+
+def test_rows_of_requests_without_tokens(kb):
+    """They have none, alone or among others, and leave no error behind."""
+    s = Steps(kb, "bf16", 512, 64, 8, 16, "block", "half", "none")
+    for r in range(4):
+        s.cache.new(r)
+    for rids in ([], [0], [0, 3]):
+        rows, start = s.cache.rows(0, rids)
+        assert rows.shape == (0, 576) and rows.dtype == s.dt and start.tolist() == [0] * (len(rids) + 1)
+    s.step([1, 3], 20)
+    rows, start = s.cache.rows(1, [0, 3, 2, 1])
+    assert start.tolist() == [0, 0, 20, 20, 40]
+    assert torch.equal(rows, torch.cat((s.rows(1, 3), s.rows(1, 1))))
+    s.cache.check()
