@@ -313,7 +313,7 @@ int launch_rotary(const kvp_pool* pool, RotArgs& a, int layout, cudaStream_t st)
   int tokens = 1;
   while (tokens < kRotMaxTokens && 2 * tokens * (a.rot / 2) <= kRotMaxPairs && a.n / (2 * tokens) >= pool->num_sms * 8) tokens *= 2;
   a.tokens = tokens;
-  const unsigned grid = (unsigned)((a.n + tokens - 1) / tokens);
+  const unsigned grid = (unsigned)(((long long)a.n + tokens - 1) / tokens);
   if (es == 4) {
     if (half) rotary_store_kernel<float, true><<<grid, kRotThreads, 0, st>>>(a);
     else rotary_store_kernel<float, false><<<grid, kRotThreads, 0, st>>>(a);

@@ -343,3 +343,24 @@ def test_sines_and_cosines_keep_their_bits(kb, layout, D):
             want_c[x, i], want_s[x, i] = ((c, s), (-s, c), (-c, -s), (s, -c))[k % 4]
     for got, want in ((out[:, 0, first], want_c), (out[:, 0, second], want_s)):
         R.check(got, want, R.U32 * (3.2 * want.abs() + 0.01), layout)
+
+
+def test_as_many_tokens_as_int32_counts(kb):
+    """Queries alone, in place: 2^31 - 1 tokens of one head of 8 entries (34 GB), all at the same position but the ends."""
+    n, D = 2 ** 31 - 1, 8
+    if torch.cuda.mem_get_info()[0] < 80 << 30:
+        pytest.skip("needs 80 GB of free memory")
+    pool = kb.Pool(torch.zeros((2, 1, 2, 4, 1, D), dtype=torch.bfloat16, device=DEV), 4, kb.KVP_BF16)
+    q = torch.ones((n, 1, D), dtype=torch.bfloat16, device=DEV)
+    pos = torch.zeros(n, dtype=torch.int32, device=DEV)
+    ends = torch.tensor([0, 1, 2, n // 2, n - 3, n - 2, n - 1], device=DEV)
+    pos[ends] = torch.arange(1, 8, dtype=torch.int32, device=DEV) * 1000
+    kb.rotary_store_cache(pool, 0, q, None, None, pos, None, kb.RotaryPlan(D, layout="interleaved", device=DEV), q)
+    want, bound = R.rotate(torch.ones((7, 1, D)), pos[ends].cpu(), R.thetas(D), "interleaved")
+    R.check(q[ends], want, bound + R.u(torch.bfloat16) * (want.abs() + bound), "ends")
+    assert int((pos != 0).sum()) == 7
+    for at in range(3, n - 3, 1 << 28):  # the rest stays: position 0 turns nothing
+        part = q[at:min(at + (1 << 28), n - 3)]
+        moved = int((part != 1).any(-1).sum())
+        assert moved == (1 if at <= n // 2 < at + (1 << 28) else 0)
+    assert kb.kvp_sync_error(pool) == 0
