@@ -11,12 +11,15 @@
 // 16, 33 ns each) for S and 8 for O, 0.65 us, on 80 KB of K and V. Measured: 0.9 us a
 // block (48 KB of K take 1.0 us to come in and S 0.5 us on two stages; the softmax
 // takes 0.75 us), 1.5 us more a tile (its Q waits for the tile before); 164 us,
-// 1167 TFLOP/s on 512-token chunks of 16 requests with 32 heads.
+// 1170 TFLOP/s on 512-token chunks of 16 requests with 32 heads (GPU time in a short
+// CUDA graph; 183 us under the power limit of a longer run).
 //  * TMEM: two S buffers of 128 columns, O (128), two P buffers (64 columns, two
 //    bf16 keys each). S(i + 1) and O += P(i) V(i) run while the softmax works:
 //    four threads a row in one warp, 32 keys each (the 16-lane forms of the TMEM
 //    load and store), online softmax in log2 units, O rescaled only when a row's
-//    maximum grows by more than 8 (P <= 256).
+//    maximum grows by more than 8 (P <= 256). P is rounded to bf16 once (half a step,
+//    2^-8, at most), as an operand has to be; the row sums keep it in fp32. Against 64
+//    bits the output is off by 1.2 to 1.4 times what its own last rounding costs.
 //  * Operands by TMA under the 128-byte swizzle: 64-entry chunks of 128 rows (16
 //    KB): Q 3, K 3 a stage (two of k, one of r), V 2 a stage, two stages each.
 //    Rows past the request's last key are another request's: their scores are
@@ -598,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_tc_kernel(const __grid_c
         }
       }
       // A weight of 0 does not keep an infinity or a NaN of V out of O. It is rare enough
-      // that a look through V's masked blocks, 1.4 us each, waits until an O that is no
+      // that a look through V's masked blocks, which cost 14 %, waits until an O that is no
       // number shows up under a sum that is one: from then on such values that some row
       // does not attend become zeros (that entry of the rows that do becomes NaN here), and
       // the tiles that were already under way are done again.

@@ -22,10 +22,16 @@
 //  * What an SM does in a block at R = 64: 1.0 us of tensor time; 316 KB through
 //    shared memory (the two products' operands and the block's arrival), 1.3 us at
 //    128 bytes a clock; 1.65 us as its share of the memory rate when no other CTA
-//    reads the same rows. Measured: 1.65 us a block in either case. Two block stages
-//    are all that fits beside Q (227 KB), so a block's way (load 1.0 us, S 0.75,
-//    softmax 0.5, O 0.5, two at a time) shows; finer stages of 32 keys or of a third
-//    of the entries gave nothing back (more, smaller boxes and products).
+//    reads the same rows. Measured: 1.65 us a block in either case, with the tensor
+//    pipe 45 % and shared memory about 65 % busy over the call: neither is what holds
+//    a tile that shares its rows. Two block stages are all that fits beside Q (227
+//    KB), so a block's way (load 1.0 us, S 0.75, softmax 0.5, O 0.5, two at a time)
+//    shows; finer stages of 32 keys or of a third of the entries gave nothing back
+//    (more, smaller boxes and products).
+//  * The softmax weights are rounded to bf16 once, half a step (2^-8) each at most,
+//    as the operand of the second product has to be; their sum keeps them in fp32.
+//    Against 64 bits the output is off by 1.1 to 1.3 times what its own last
+//    rounding costs.
 //  * Layout of a block: groups of 8 keys, 9 KB each: 9 chunks of 64 entries, 8
 //    rows of 128 bytes (128-byte swizzle). Eight consecutive slots are one TMA
 //    box; any other rows are copied with 16-byte asynchronous copies (TMA row
@@ -52,11 +58,11 @@
 // loads Q, 4..7 run the softmax (16 query rows each, TMEM quadrant = warp % 4),
 // 8..11 look for rows that are not finite and scale O when a row's maximum grew, 4..11
 // together the epilogue, 12..15 load the blocks.
-// Measured (bf16, the whole call with its combine): one request of 777 rows, 16
-// heads: 12 us (two launches); 64 requests of 512 .. 4096 rows, 32 heads: 45.3 us,
-// 4.1 TB/s (7 us until the first block is in, 5 us of combine); 32 requests of 8192 ..
-// 32768 scattered rows, 128 heads: 235 us, 733 TFLOP/s; four tokens of 64 heads on 64
-// requests: 127 us, 669 TFLOP/s.
+// Measured (bf16, GPU time of the whole call with its combine in a CUDA graph): one
+// request of 777 rows, 16 heads: 12.5 us (two launches); 64 requests of 512 .. 4096
+// rows, 32 heads: 45.6 us, 4.1 TB/s (6 us until the first block is in, 4 us of
+// combine); 32 requests of 8192 .. 32768 scattered rows, 128 heads: 234 us, 735
+// TFLOP/s; four tokens of 64 heads on 64 requests: 128 us, 666 TFLOP/s.
 // Every wait is bounded (2 s), as in the other kernels.
 #include <cstring>
 

@@ -25,10 +25,10 @@
 // takes one head of one token, the groups stride over the tokens' heads. Loads run
 // ahead of what they wait for: v and the first heads are on their way while
 // positions, slots and sines are found, later heads two at a time.
-// Measured (bf16 unless said, 8 key heads): 64 tokens of 32 heads 3.5 us; 8,192 of
-// them 33.9 us (5.9 TB/s, 0.88 of a copy's rate); 65,537 of 64 heads, half of
-// each turned, 428 us (6.3 TB/s, 0.92); 3,001 fp32 tokens of 16 heads 8.8 us; 16,461
-// latent rows with 32 heads' rotated parts 31.8 us (5.4 TB/s, 0.80).
+// Measured (GPU time in a CUDA graph, bf16 unless said, 8 key heads): 64 tokens of 32
+// heads 3.6 us; 8,192 of them 34.0 us (5.9 TB/s, 0.87 of a copy's rate); 65,537 of 64
+// heads, half of each turned, 410 us (6.6 TB/s, 0.97); 3,001 fp32 tokens of 16 heads 8.1
+// us; 16,461 latent rows with 32 heads' rotated parts 32.2 us (5.4 TB/s, 0.79).
 #include "common.cuh"
 
 #include <cmath>

@@ -36,7 +36,6 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
 
 namespace tc5 {
 
-
 // Shared-memory matrix descriptor, 128-byte swizzle (8-row atoms of 1 KB).
 // K-major: ``sbo`` bytes between 8-row groups, ``lbo`` unused. MN-major: ``lbo``
 // bytes between blocks of 64 MN entries, ``sbo`` between groups of 8 K rows.
@@ -213,7 +212,7 @@ __device__ __forceinline__ void prefetch_map(const void* tmap) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(tmap) : "memory");
 }
 
-// A box of a 4-D map with an L2 policy (createpolicy): into shared memory, or to L2 alone.
+// A box of a 4-D map into shared memory with an L2 policy (createpolicy).
 __device__ __forceinline__ void tma_4d(void* dst, const void* tmap, int c0, int c1, int c2, int c3, uint64_t* bar,
                                        uint64_t policy) {
   asm volatile(
