@@ -405,7 +405,9 @@ int paged_latent_attention(const kvp_pool* pool, int layer, const void* q,
  *   k, v  device, [total_k] rows, nope_dim / v_dim entries per head.
  *   k_pe  device, [total_k] rows of rope_dim entries (NULL when rope_dim is 0).
  *   q_start, k_start  device int32 [batch + 1], ascending.
- *   max_q the longest request's query rows (an upper bound is fine).
+ *   max_q the longest request's query rows (an upper bound is fine). batch *
+ *         num_heads * ceil(max_q / 128) is below 2^31, for fp32, other widths and
+ *         strides that are no multiples of 16 bytes batch * num_heads * max_q.
  *   nope_dim, rope_dim, v_dim  up to 512 each (rope_dim may be 0).
  *   out   device [total_q, num_heads, v_dim], contiguous.
  * An infinity or a NaN in a value makes that entry of that head not finite (NaN

@@ -61,6 +61,9 @@ constexpr int kThreads = 512;
 constexpr int kSoft0 = 4, kSoftWarps = 8;
 constexpr int kEpi0 = 12, kEpiWarps = 4;
 constexpr uint64_t kWaitNs = 2000000000ull;
+// For the loader's next tile: it may come by 2^31 tiles without rows before (a long prompt among many requests), 0.5 us
+// each and CTA, 7 s in all. What the loader itself waits for is bounded as above and ends these waits too.
+constexpr uint64_t kTileWaitNs = 20000000000ull;
 constexpr size_t kSmem = (kQChunks + kKS * kQChunks + kVS * kVChunks + 1) * kChunk;
 
 struct ExpArgs {
@@ -228,7 +231,8 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_tc_kernel(const __grid_c
 
   // This CTA's k-th tile, from slot k % 2; false: none, or a wait gave up.
   auto get_tile = [&](int k, Tile& t) -> bool {
-    if (!__all_sync(0xffffffffu, ewait(&sb.tile_full[k & 1], k >> 1, abort_flag, err))) return false;
+    if (!__all_sync(0xffffffffu, mbar_wait_bounded(&sb.tile_full[k & 1], (uint32_t)((k >> 1) & 1), abort_flag, err, kTileWaitNs)))
+      return false;
     t = sb.tile[k & 1];
     __syncwarp();
     if (lane == 0) mbar_arrive(&sb.tile_free[k & 1]);
@@ -244,24 +248,6 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_tc_kernel(const __grid_c
       ++asked;
       __syncwarp();
     };
-    // The next tile with rows off the grid (nblk 0: none left), after an ask().
-    auto answer = [&]() -> Tile {
-      Tile t;
-      t.nblk = 0;
-      while (ok) {
-        ok = __all_sync(0xffffffffu, ewait(&sb.answer, asked - 1, abort_flag, err));
-        if (!ok) break;
-        const long long idx = taken(sb.next);
-        fence_proxy_async_smem();  // the next answer comes through the async proxy
-        __syncwarp();
-        if (idx < 0) break;
-        t = tile_of(a, (uint32_t)idx);
-        if (t.nblk) break;
-        ask();
-      }
-      if (!ok) t.nblk = 0;
-      return t;
-    };
     auto publish = [&](int k, const Tile& t) {
       if (k >= 2) ok = ok && __all_sync(0xffffffffu, ewait(&sb.tile_free[k & 1], (k >> 1) - 1, abort_flag, err));
       if (!ok) return;
@@ -271,17 +257,14 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_tc_kernel(const __grid_c
       }
       __syncwarp();
     };
-    Tile t = tile_of(a, blockIdx.x);
-    if (!t.nblk) {
-      ask();
-      t = answer();
-    }
-    if (t.nblk) publish(0, t);
-    int redo = -1;  // >= 0: the grid is done
-    for (int k = 0; ok; ++k) {
+    Tile t;
+    t.nblk = 0;
+    bool looking = true;  // for the next tile: at first this block's own, then what is asked for
+    int redo = -1;        // >= 0: the grid is done
+    for (int k = -1; ok; ++k) {
       Tile nx;
       nx.nblk = 0;
-      if (!t.nblk) {
+      if (k >= 0 && !t.nblk) {
         if (redo < 0) {  // the tiles that have to be done again are known once all epilogues are through
           const uint64_t t0 = global_timer_ns();
           while (*(volatile int*)&sb.epilogues < k * kEpiWarps && !*abort_flag) {
@@ -301,34 +284,53 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_tc_kernel(const __grid_c
         publish(k, t);
         if (!t.nblk) break;
       }
-      if (redo < 0) ask();
-      for (int i = 0; ok && i < t.nblk; ++i, ++n) {
-        const int st = n % kKS;
-        if (n >= kKS) ok = __all_sync(0xffffffffu, ewait(&sb.k_empty[st], n / kKS - 1, abort_flag, err));
-        if (!ok) break;
-        if (lane == 0) {
-          unsigned char* dst = sK + st * kQChunks * kChunk;
-          mbar_arrive_expect_tx(&sb.k_full[st], kQChunks * kChunk);
-          tc5::tma_3d(dst, &a.kmap, 0, t.h, t.k0 + i * kKeys, &sb.k_full[st]);
-          tc5::tma_3d(dst + kChunk, &a.kmap, 64, t.h, t.k0 + i * kKeys, &sb.k_full[st]);
-          tma_2d(dst + 2 * kChunk, &a.pemap, 0, t.k0 + i * kKeys, &sb.k_full[st]);
-        }
-        __syncwarp();
-        if (i == 0) {  // behind the first block's K, which need not wait for the tile before
-          if (nq > 0) ok = __all_sync(0xffffffffu, ewait(&sb.q_free, nq - 1, abort_flag, err));
+      if (k >= 0 && redo < 0) {
+        ask();
+        looking = true;
+      }
+      for (int i = 0; i < t.nblk || looking;) {
+        if (i < t.nblk) {
+          const int st = n % kKS;
+          if (n >= kKS) ok = __all_sync(0xffffffffu, ewait(&sb.k_empty[st], n / kKS - 1, abort_flag, err));
           if (!ok) break;
           if (lane == 0) {
-            mbar_arrive_expect_tx(&sb.q_full, kQChunks * kChunk);
-            for (int c = 0; c < kQChunks; ++c) tc5::tma_3d(sQ + c * kChunk, &a.qmap, 64 * c, t.h, t.q0, &sb.q_full);
+            unsigned char* dst = sK + st * kQChunks * kChunk;
+            mbar_arrive_expect_tx(&sb.k_full[st], kQChunks * kChunk);
+            tc5::tma_3d(dst, &a.kmap, 0, t.h, t.k0 + i * kKeys, &sb.k_full[st]);
+            tc5::tma_3d(dst + kChunk, &a.kmap, 64, t.h, t.k0 + i * kKeys, &sb.k_full[st]);
+            tma_2d(dst + 2 * kChunk, &a.pemap, 0, t.k0 + i * kKeys, &sb.k_full[st]);
           }
-          ++nq;
+          __syncwarp();
+          if (i == 0) {  // behind the first block's K, which need not wait for the tile before
+            if (nq > 0) ok = __all_sync(0xffffffffu, ewait(&sb.q_free, nq - 1, abort_flag, err));
+            if (!ok) break;
+            if (lane == 0) {
+              mbar_arrive_expect_tx(&sb.q_full, kQChunks * kChunk);
+              for (int c = 0; c < kQChunks; ++c) tc5::tma_3d(sQ + c * kChunk, &a.qmap, 64 * c, t.h, t.q0, &sb.q_full);
+            }
+            ++nq;
+            __syncwarp();
+          }
+          ++i;
+          ++n;
+        }
+        // With the stages full, the next tile is decoded and handed on; where it has no rows, the look for another one
+        // does not hold up this one's blocks: a long prompt may have millions of tiles without rows behind it.
+        if (!looking || i < min(kKS, t.nblk)) continue;
+        long long idx = blockIdx.x;
+        if (k >= 0 || asked > 0) {
+          if (i == kKS || i == t.nblk) ok = __all_sync(0xffffffffu, ewait(&sb.answer, asked - 1, abort_flag, err));
+          else if (!__all_sync(0xffffffffu, mbar_test_wait(&sb.answer, (uint32_t)((asked - 1) & 1)))) continue;
+          if (!ok) break;
+          idx = taken(sb.next);
+          fence_proxy_async_smem();  // the next answer comes through the async proxy
           __syncwarp();
         }
-        // with the stages full, the next tile is decoded and handed on
-        if (i == min(kKS, t.nblk) - 1) {
-          if (redo < 0) nx = answer();
-          if (nx.nblk) publish(k + 1, nx);
-        }
+        if (idx >= 0) nx = tile_of(a, (uint32_t)idx);
+        looking = idx >= 0 && !nx.nblk;
+        if (looking) ask();
+        if (nx.nblk) publish(k + 1, nx);
+        if (!ok) break;
       }
       t = nx;
     }

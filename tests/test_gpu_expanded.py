@@ -408,3 +408,31 @@ def test_a_value_that_is_not_finite_under_a_score_of_minus_infinity(kb, dtype):
         hit = torch.zeros((150, 2, 128), dtype=torch.bool)
         hit[t:, 1, 7] = True
         assert not bool(c.out.cpu()[hit].isfinite().any()) and bool(c.out.cpu()[~hit].isfinite().all())
+
+
+def test_a_long_prompt_among_very_many_requests(kb):
+    """1.05e9 tiles of queries of which 128 times 65 have rows: the others take 3 s to come by, longer than any wait but
+    the one for the next tile may be."""
+    B, H, L, T = 2 ** 17, 128, 8192, 8192 + 7
+    g = torch.Generator(device=DEV).manual_seed(3)
+
+    def heads(width):  # overlapping heads, eight entries apart: small inputs
+        flat = torch.randn(T * (8 * H + width) + width, generator=g, device=DEV).bfloat16()
+        return flat.as_strided((T, H, width), (8 * H + width, 8, 1))
+
+    q, k, v = heads(192), heads(128), heads(128)
+    pe = torch.randn((T, 64), generator=g, device=DEV).bfloat16()
+    out = torch.full((T, H, 128), 5.0, dtype=torch.bfloat16, device=DEV)
+    start = torch.zeros(B + 1, dtype=torch.int32)
+    start[B // 3 + 1:] = L
+    start[B:] = T
+    start, err = start.to(DEV), torch.zeros(1, dtype=torch.int32, device=DEV)
+    kb.latent_prefill_attention(q, k, pe, v, start, start, L, 192 ** -0.5, out, error_word=err)
+    assert int(err) == 0
+    for first, n in ((0, L), (L, 7)):
+        for j in {0, n // 2, n - 1}:
+            keys = slice(first, first + j + 1)
+            key = torch.cat((k[keys].double().cpu(), pe[keys].double().cpu()[:, None].expand(-1, H, -1)), -1)[:, ::37]
+            w, bound = R.attend(q[first + j, ::37].double().cpu(), key, v[keys, ::37].double().cpu(), 192 ** -0.5,
+                                torch.bfloat16)
+            R.check(out[first + j, ::37], w, bound, f"query {first + j}")
