@@ -436,3 +436,41 @@ def test_a_long_prompt_among_very_many_requests(kb):
             w, bound = R.attend(q[first + j, ::37].double().cpu(), key, v[keys, ::37].double().cpu(), 192 ** -0.5,
                                 torch.bfloat16)
             R.check(out[first + j, ::37], w, bound, f"query {first + j}")
+
+
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf")])
+@pytest.mark.parametrize("where", ["k", "pe"])
+@pytest.mark.parametrize("dtype,dn,dr,dv", [("bf16", 128, 64, 128), ("bf16", 64, 32, 64), ("f32", 128, 64, 128)])
+def test_an_infinite_key_counts_by_its_score(kb, bad, where, dtype, dn, dr, dv):
+    """Minus infinity weighs nothing, plus infinity makes the head's output NaN; a query with that key alone gets zeros."""
+    H = 3
+    c = Case(kb, dtype, [150, 200, 1], [300, 200, 1], H, dn, dr, dv, seed=12)
+    t = [200, 64, 0]
+    q, v = c.q.double().cpu(), c.v.double().cpu()
+    for b, x in enumerate(t):
+        if where == "k":
+            c.k[c.k0[b] + x, 1, 5] = bad
+        else:
+            c.pe[c.k0[b] + x, 5] = bad
+    c.run()
+    assert int(c.err) == 0
+    out = c.out.cpu()
+    key = torch.cat((c.k.double().cpu(), c.pe.double().cpu()[:, None].expand(-1, H, -1)), -1)
+    seen = set()
+    for b, x in enumerate(t):
+        first = c.kl[b] - c.ql[b]
+        for p in range(max(first, x), min(x + 40, c.kl[b])):
+            for h in range(H) if where == "pe" else (1,):
+                met = q[c.q0[b] + p - first, h, 5 if where == "k" else dn + 5] * bad
+                got = out[c.q0[b] + p - first, h]
+                seen.add((float(met), p == 0))
+                if met > 0:
+                    assert bool(got.isnan().all())
+                    continue
+                keep = [c.k0[b] + i for i in range(p + 1) if i != x]
+                if not keep:
+                    assert bool((got == 0).all())
+                    continue
+                w, bound = R.attend(q[c.q0[b] + p - first, h:h + 1], key[keep][:, h:h + 1], v[keep][:, h:h + 1], c.scale, c.dt)
+                R.check(got[None], w, bound, f"request {b} position {p} head {h}")
+    assert {s for s, _ in seen} == {float("inf"), -float("inf")}
