@@ -70,6 +70,8 @@ enum kvp_rotary_scaling { /* of the frequencies theta_i = base^(-2 i / rotary_di
   KVP_ROTARY_BY_PARTS = 3  /* slow pairs / factor, fast ones kept, see below   */
 };
 
+#define KVP_ROTARY_MAX_AXES 8 /* axes of a position (time, height, width, ...) */
+
 typedef struct kvp_pool kvp_pool;
 
 /* ------------------------------------------------------------------------
@@ -114,6 +116,33 @@ int kv_pool_destroy(kvp_pool* pool);
 int kv_latent_pool_create(int num_pages, int page_size, int latent_dim,
                           int rope_dim, int dtype, int num_layers, void* buffer,
                           int32_t* error_word, kvp_pool** out);
+
+/* ------------------------------------------------------------------------
+ * kv_fp4_pool_create: describe a caller-owned cache of K and V in four bits. A
+ * block is 16 consecutive entries of one head's K or V of one token; an entry
+ * stands for code * scale * g: code e2m1 (bit 3 the sign, then 0, 0.5, 1, 1.5,
+ * 2, 3, 4, 6), scale e4m3 of the block, g a power of two per layer and plane.
+ *   codes   device bytes (num_layers, num_pages, page_size, kv_heads, 2,
+ *           head_dim / 2): K, then V; entry 2 i is the low half of byte i.
+ *   scales  device bytes (num_layers, ceil(num_pages * page_size / 16),
+ *           kv_heads, 16, 2, head_dim / 16): slot s is row s % 16 of group
+ *           s / 16. Both C-contiguous, 16-byte aligned.
+ *   k_scales, v_scales  host arrays [num_layers] of g, powers of two in
+ *           2^-64 .. 2^64; NULL: 1. Copied. A block reaches 2688 g; below
+ *           g * 2^-8 its scale loses bits, as e4m3 does.
+ *   dtype   of what is stored, read back and attended (kvp_dtype).
+ * head_dim is a multiple of 16, 256 at most; kv_heads * head_dim a multiple of 128.
+ * The descriptor is a kvp_pool with pages, slots and tables as any other:
+ * page_table_write, copy_pages(_device_count), gather_indices, kvp_sync_error,
+ * kvp_host_* and kvp_dev_* take it or serve it; rotary_store_fp4,
+ * load_cache_fp4 and paged_fp4_attention take only such pools, and the calls of
+ * K/V and latent pools refuse them with KVP_ERR_INVALID_ARG. Destroyed by
+ * kv_pool_destroy. Errors as kv_pool_create.
+ * ---------------------------------------------------------------------- */
+int kv_fp4_pool_create(int num_pages, int page_size, int kv_heads, int head_dim,
+                       int dtype, int num_layers, void* codes, void* scales,
+                       const float* k_scales, const float* v_scales,
+                       int32_t* error_word, kvp_pool** out);
 
 /* ------------------------------------------------------------------------
  * store_cache: K[layer][out_loc[i]] = k[i], V[layer][out_loc[i]] = v[i] for
@@ -344,6 +373,113 @@ int rotary_store_latent(const kvp_pool* pool, int layer, const void* q_pe,
                         int rotary_dim, int layout, float attn_factor,
                         void* q_pe_out, long long q_out_stride,
                         long long q_out_head_stride, void* stream);
+
+/* ------------------------------------------------------------------------
+ * rotary_store_cache_axes, rotary_store_latent_axes: the same with positions of
+ * several axes (time, height and width of images and video): pair i of token t
+ * turns by positions[pair_axis[i] * position_stride + t] * theta_i. Text has the
+ * same position on every axis.
+ *   positions  device int32, axis x of token t at x * position_stride + t;
+ *              position_stride >= n.
+ *   pair_axis  device uint8 [rotary_dim / 2], each below num_axes (another one
+ *              sets KVP_ERR_BAD_INDEX and counts as axis 0).
+ *   num_axes   1 .. KVP_ROTARY_MAX_AXES; with 1, pair_axis is not read and the
+ *              call is rotary_store_cache or rotary_store_latent.
+ * Everything else as those.
+ * ---------------------------------------------------------------------- */
+int rotary_store_cache_axes(const kvp_pool* pool, int layer, const void* q,
+                            long long q_stride, long long q_head_stride,
+                            int num_q_heads, const void* k, long long k_stride,
+                            const void* v, long long v_stride,
+                            const int32_t* positions, long long position_stride,
+                            const int32_t* out_loc, int n, const uint64_t* freqs,
+                            const uint8_t* pair_axis, int num_axes,
+                            int rotary_dim, int layout, float attn_factor,
+                            void* q_out, long long q_out_stride,
+                            long long q_out_head_stride, void* stream);
+int rotary_store_latent_axes(const kvp_pool* pool, int layer, const void* q_pe,
+                             long long q_stride, long long q_head_stride,
+                             int num_q_heads, const void* latent,
+                             long long latent_stride, const void* k_pe,
+                             long long k_pe_stride, const int32_t* positions,
+                             long long position_stride, const int32_t* out_loc,
+                             int n, const uint64_t* freqs,
+                             const uint8_t* pair_axis, int num_axes,
+                             int rotary_dim, int layout, float attn_factor,
+                             void* q_pe_out, long long q_out_stride,
+                             long long q_out_head_stride, void* stream);
+
+/* ------------------------------------------------------------------------
+ * rotary_store_fp4: rotary_store_cache_axes into a four-bit pool (q, k, v and
+ * q_out of the pool's dtype). A block x of rotated K or of V, not rounded in
+ * between, becomes
+ *     scale = e4m3(max |x| / (6 g)),  code = e2m1(x / (scale g)),
+ * each to the nearest value, ties to the even code, at most 448 and 6; a scale
+ * that rounds to zero makes the block zero. The codes and scales are those of
+ * the formula with sines, cosines, products and sums in 64 bits. A block with an
+ * infinity or a NaN gets the scale NaN (0x7f) and reads as NaN throughout.
+ * With q NULL and rotary_dim 0, positions and freqs may be NULL: the store
+ * alone, of k and v as they are.
+ * ---------------------------------------------------------------------- */
+int rotary_store_fp4(const kvp_pool* pool, int layer, const void* q,
+                     long long q_stride, long long q_head_stride,
+                     int num_q_heads, const void* k, long long k_stride,
+                     const void* v, long long v_stride,
+                     const int32_t* positions, long long position_stride,
+                     const int32_t* out_loc, int n, const uint64_t* freqs,
+                     const uint8_t* pair_axis, int num_axes, int rotary_dim,
+                     int layout, float attn_factor, void* q_out,
+                     long long q_out_stride, long long q_out_head_stride,
+                     void* stream);
+
+/* ------------------------------------------------------------------------
+ * load_cache_fp4: the rows of a four-bit pool: k[i], v[i] = K, V of slot
+ * slots[i], as the values they stand for (exact in both dtypes).
+ *   slots  device int32 [n], any order, repeated ones too (gather_indices
+ *          names a context's). A slot outside the pool sets KVP_ERR_BAD_INDEX
+ *          and gives zeros. n == 0 launches nothing.
+ *   k, v   device [n, kv_heads, head_dim], pool dtype, 16-byte aligned.
+ * The pool's device must be current.
+ * ---------------------------------------------------------------------- */
+int load_cache_fp4(const kvp_pool* pool, int layer, const int32_t* slots, int n,
+                   void* k, void* v, void* stream);
+
+/* ------------------------------------------------------------------------
+ * paged_fp4_attention: attention over a four-bit pool, for decode (chunk 1),
+ * multi-token verify and chunks: request b's q_lens[b] newest tokens (NULL: chunk
+ * each; their rows already stored, L = context_lens[b] counts them) are queries
+ * at once, query j at position L - q_lens[b] + j, and attends what a one-token
+ * step with that context attends (causal; window and sinks as
+ * paged_decode_attention).
+ *   q    device [batch, chunk, num_q_heads, head_dim], pool dtype, contiguous,
+ *        16-byte aligned.
+ *   out  device, likewise; rows j >= q_lens[b] are not written.
+ *   q_lens  device int32 [batch], 1 <= q_lens[b] <= min(chunk, L), or NULL.
+ *   max_context  a bound of context_lens that the host knows (an upper bound is
+ *        fine); chunks need a workspace for as many rows a request.
+ *   workspace  device, >= paged_fp4_attention_workspace_size() bytes, 256-byte
+ *        aligned; contents need no initialisation and are clobbered; calls that
+ *        may overlap on the GPU (captured graphs among them) need separate ones.
+ * Device-detected errors set KVP_ERR_BAD_INDEX: the rows of a request whose
+ * length (0, above max_context or the table's columns), q_lens entry or table
+ * row is invalid are zero-filled; an attended table entry that is a hole or out
+ * of range is skipped (nothing is read through it) and that request's output is
+ * otherwise unspecified. Rows past the context, out of a query's window and in
+ * other pages may hold anything. A block that reads as NaN reaches the queries
+ * that attend it and no others: one of K makes that head's output NaN, one of V
+ * its 16 entries. The pool's device must be current.
+ * ---------------------------------------------------------------------- */
+int paged_fp4_attention_workspace_size(const kvp_pool* pool, int batch, int chunk,
+                                       int num_q_heads, int max_context,
+                                       size_t* bytes);
+int paged_fp4_attention(const kvp_pool* pool, int layer, const void* q, int batch,
+                        int chunk, int num_q_heads, const int32_t* q_lens,
+                        const int32_t* table, int table_rows_total,
+                        int table_cols, int table_mode,
+                        const int32_t* table_rows, const int32_t* context_lens,
+                        int max_context, int window, int sinks, float scale,
+                        void* out, void* workspace, size_t workspace_bytes,
+                        void* stream);
 
 /* ------------------------------------------------------------------------
  * paged_latent_attention: attention over a latent pool in absorbed form, for

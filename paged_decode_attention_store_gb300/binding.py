@@ -26,6 +26,7 @@ KVP_ERR_TIMEOUT = -5
 KVP_F32, KVP_BF16 = 0, 1
 KVP_BLOCK_TABLE, KVP_RAW_LOCATIONS = 0, 1
 KVP_ROTARY_HALF, KVP_ROTARY_INTERLEAVED = 0, 1
+KVP_ROTARY_MAX_AXES = 8
 KVP_ROTARY_PLAIN, KVP_ROTARY_LINEAR, KVP_ROTARY_NTK, KVP_ROTARY_BY_PARTS = 0, 1, 2, 3
 
 _ERR_NAMES = {
@@ -61,6 +62,16 @@ SIGNATURES = {
                            _vp],
     "rotary_store_latent": [_vp, _i, _vp, _ll, _ll, _i, _vp, _ll, _vp, _ll, _vp, _vp, _i, _vp, _i, _i, _f, _vp, _ll, _ll,
                             _vp],
+    "kv_fp4_pool_create": [_i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, ctypes.POINTER(_vp)],
+    "rotary_store_cache_axes": [_vp, _i, _vp, _ll, _ll, _i, _vp, _ll, _vp, _ll, _vp, _ll, _vp, _i, _vp, _vp, _i, _i, _i, _f,
+                                _vp, _ll, _ll, _vp],
+    "rotary_store_latent_axes": [_vp, _i, _vp, _ll, _ll, _i, _vp, _ll, _vp, _ll, _vp, _ll, _vp, _i, _vp, _vp, _i, _i, _i, _f,
+                                 _vp, _ll, _ll, _vp],
+    "rotary_store_fp4": [_vp, _i, _vp, _ll, _ll, _i, _vp, _ll, _vp, _ll, _vp, _ll, _vp, _i, _vp, _vp, _i, _i, _i, _f, _vp, _ll,
+                         _ll, _vp],
+    "load_cache_fp4": [_vp, _i, _vp, _i, _vp, _vp, _vp],
+    "paged_fp4_attention_workspace_size": [_vp, _i, _i, _i, _i, _szp],
+    "paged_fp4_attention": [_vp, _i, _vp, _i, _i, _i, _vp, _vp, _i, _i, _i, _vp, _vp, _i, _i, _i, _f, _vp, _vp, _sz, _vp],
     "paged_latent_attention_workspace_size": [_vp, _i, _i, _i, _szp],
     "paged_latent_attention": [_vp, _i, _vp, _i, _i, _i, _vp, _vp, _i, _i, _i, _vp, _vp, _i, _i, _f, _vp, _vp, _sz, _vp],
     "latent_prefill_attention": [_vp, _ll, _ll, _vp, _ll, _ll, _vp, _ll, _vp, _ll, _ll, _vp, _vp, _i, _i, _i, _i, _i, _i,
@@ -252,6 +263,61 @@ class LatentPool:
             self.handle = None
 
 
+class Fp4Pool:
+    """A kvp_pool over caller-owned codes and block scales (kept alive here), K
+    and V in four bits: codes uint8 (layers, num_pages, page_size, kv_heads, 2,
+    head_dim / 2), scales uint8 (layers, ceil(slots / 16), kv_heads, 16, 2,
+    head_dim / 16); see include/pagedkv.h, kv_fp4_pool_create. ``dtype`` is that
+    of what is stored, read and attended; ``k_scale`` and ``v_scale``: powers of
+    two, one or one a layer."""
+
+    def __init__(self, codes, scales, dtype, k_scale=1.0, v_scale=1.0, error_word=None):
+        _dev(codes, torch.uint8, "codes")
+        if codes.dim() != 6 or codes.shape[4] != 2:
+            raise ValueError("codes must be (layers, num_pages, page_size, kv_heads, 2, head_dim / 2)")
+        self.num_layers, self.num_pages, self.page_size, self.kv_heads, _, half = codes.shape
+        self.head_dim = 2 * half
+        self.device_index = codes.get_device()
+        _on(scales, self.device_index, torch.uint8, "scales")
+        groups = -(-self.num_pages * self.page_size // 16)
+        if scales.shape != (self.num_layers, groups, self.kv_heads, 16, 2, self.head_dim // 16):
+            raise ValueError(f"scales must be {(self.num_layers, groups, self.kv_heads, 16, 2, self.head_dim // 16)}, got "
+                             f"{tuple(scales.shape)}")
+        if dtype not in _TORCH_DTYPE:
+            raise ValueError(f"dtype must be KVP_F32 or KVP_BF16, got {dtype!r}")
+        self.dtype, self.codes, self.scales = dtype, codes, scales
+        self.error_word = (torch.zeros(1, dtype=torch.int32, device=codes.device)
+                           if error_word is None else _on(error_word, self.device_index, torch.int32, "error_word"))
+        each = []
+        for g, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            g = [float(g)] * self.num_layers if isinstance(g, (int, float)) else [float(x) for x in g]
+            if len(g) != self.num_layers:
+                raise ValueError(f"{name} must be one number or one a layer")
+            each.append((ctypes.c_float * self.num_layers)(*g))
+        h = ctypes.c_void_p()
+        with torch.cuda.device(codes.device):
+            _check(lib().kv_fp4_pool_create(self.num_pages, self.page_size, self.kv_heads, self.head_dim, dtype,
+                                            self.num_layers, _ptr(codes), _ptr(scales), *each, _ptr(self.error_word),
+                                            ctypes.byref(h)), "kv_fp4_pool_create")
+        self.handle = h
+
+    def __del__(self):
+        h = getattr(self, "handle", None)
+        if h is not None and _lib is not None:
+            _lib.kv_pool_destroy(h)
+            self.handle = None
+
+
+def kv_fp4_pool_create(num_pages, page_size, kv_heads, head_dim, dtype, num_layers, k_scale=1.0, v_scale=1.0, device="cuda",
+                       zero=False):
+    """Describe a four-bit K/V cache, its codes and scales allocated with torch."""
+    alloc = torch.zeros if zero else torch.empty
+    codes = alloc((num_layers, num_pages, page_size, kv_heads, 2, head_dim // 2), dtype=torch.uint8, device=device)
+    scales = alloc((num_layers, -(-num_pages * page_size // 16), kv_heads, 16, 2, head_dim // 16), dtype=torch.uint8,
+                   device=device)
+    return Fp4Pool(codes, scales, dtype, k_scale, v_scale)
+
+
 _SCALINGS = {"none": KVP_ROTARY_PLAIN, "linear": KVP_ROTARY_LINEAR, "ntk": KVP_ROTARY_NTK, "by_parts": KVP_ROTARY_BY_PARTS}
 _LAYOUTS = {"half": KVP_ROTARY_HALF, "interleaved": KVP_ROTARY_INTERLEAVED}
 
@@ -268,22 +334,59 @@ def rotary_frequencies(rotary_dim, base=10000.0, scaling="none", factor=1.0, ori
     return list(out)
 
 
+def pair_axes(sections, interleave=False):
+    """The axis of each pair: sections[a] pairs for axis a, axis after axis or dealt in turn."""
+    left = [int(x) for x in sections]
+    if not 1 <= len(left) <= KVP_ROTARY_MAX_AXES or min(left) < 0:
+        raise ValueError(f"sections must be 1 to {KVP_ROTARY_MAX_AXES} counts, got {sections!r}")
+    if not interleave:
+        return [a for a, n in enumerate(left) for _ in range(n)]
+    out = []
+    while any(left):
+        for a in range(len(left)):
+            if left[a]:
+                out.append(a)
+                left[a] -= 1
+    return out
+
+
 class RotaryPlan:
     """Frequencies on the device, layout and factor of rotary_store_cache and
     rotary_store_latent. ``layout``: "half" or "interleaved"; ``scaling``:
     "none", "linear", "ntk" or "by_parts" (see include/pagedkv.h,
-    kvp_rotary_frequencies); ``attn_factor`` multiplies what is rotated."""
+    kvp_rotary_frequencies); ``attn_factor`` multiplies what is rotated.
+
+    ``sections``: positions of several axes (time, height, width), then int32
+    [axes, n] in the calls: how many of the rotary_dim / 2 pairs turn by each
+    axis, one axis after another, or dealt to them in turn (``interleave``)
+    until each has its share. Pair i's frequency is that of pair i of one axis,
+    or (``per_axis``) each axis' pairs have the frequencies of a rotary_dim of
+    their own, twice their number."""
+
+    axes, pair_axis = 1, None
 
     def __init__(self, rotary_dim, base=10000.0, layout="half", scaling="none", factor=1.0, original_len=4096,
-                 low_turns=1.0, high_turns=32.0, attn_factor=1.0, device="cuda"):
+                 low_turns=1.0, high_turns=32.0, attn_factor=1.0, device="cuda", sections=None, interleave=False,
+                 per_axis=False):
         if layout not in _LAYOUTS:
             raise ValueError(f"layout must be one of {sorted(_LAYOUTS)}, got {layout!r}")
         self.rotary_dim, self.layout, self.attn_factor = int(rotary_dim), _LAYOUTS[layout], float(attn_factor)
+        freq = lambda dim: rotary_frequencies(dim, base, scaling, factor, original_len, low_turns, high_turns)  # noqa: E731
+        pairs = self.rotary_dim // 2
+        of_pair = pair_axes(sections, interleave) if sections is not None else [0] * pairs
+        if len(of_pair) != pairs:
+            raise ValueError(f"the sections must add up to {pairs} pairs, got {list(sections)}")
         f = []  # 0: nothing turns
-        if self.rotary_dim:
-            f = rotary_frequencies(rotary_dim, base, scaling, factor, original_len, low_turns, high_turns)
+        if self.rotary_dim and per_axis:
+            own = {a: iter(freq(2 * of_pair.count(a))) for a in set(of_pair)}
+            f = [next(own[a]) for a in of_pair]
+        elif self.rotary_dim:
+            f = freq(self.rotary_dim)
         signed = [x - (1 << 64) if x >= 1 << 63 else x for x in f]
         self.freqs = torch.tensor(signed, dtype=torch.int64).to(device)
+        if sections is not None and len(sections) > 1:
+            self.axes = len(sections)
+            self.pair_axis = torch.tensor(of_pair, dtype=torch.uint8).to(device)
 
 
 def _current_stream():
@@ -335,18 +438,50 @@ def _rows_view(t, index, dt, name, n, heads, width):
     return t.data_ptr(), stride[0] if n > 1 else heads * width
 
 
-def _rotary_call(fn, what, pool, layer, q, first, second, positions, out_loc, rope, q_out, width, stream):
-    """Marshals rotary_store_cache and rotary_store_latent: ``first`` and ``second`` are the two row inputs in the
-    order of the C call, each (tensor, name, heads, width)."""
+def _positions_of(t, index, axes):
+    """(address, tokens, distance of two axes) of int32 positions: [n], or [axes, n] for a plan of several axes, whose
+    rows may lie apart."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != index:
+        _elsewhere(t, index, "positions")
+    if axes == 1:
+        return _on(t, index, torch.int32, "positions").data_ptr(), t.numel(), 0
+    if t.dtype != torch.int32:
+        raise TypeError(f"positions must be {torch.int32}, got {t.dtype}")
+    if t.dim() != 2 or t.shape[0] != axes:
+        raise ValueError(f"positions must be [{axes}, n] for a plan of {axes} axes, got {tuple(t.shape)}")
+    n = t.shape[1]
+    if n > 1 and t.stride(1) != 1:
+        raise ValueError("positions' last axis must be contiguous")
+    stride = t.stride(0) if n else 0
+    if stride < n:
+        raise ValueError("positions' axes must not overlap")
+    return t.data_ptr(), n, stride
+
+
+def _rotary_call(what, pool, layer, q, first, second, positions, out_loc, rope, q_out, width, stream, always_axes=False):
+    """Marshals the rotary stores: ``first`` and ``second`` are the two row inputs in the order of the C call, each
+    (tensor, name, heads, width). With a plan of several axes the call is what + "_axes" (``always_axes``: the call takes
+    axes under its own name, and may come without a plan)."""
     dt, dev = _TORCH_DTYPE[pool.dtype], pool.device_index
-    n = _on(positions, dev, torch.int32, "positions").numel()
-    if rope.rotary_dim and rope.freqs.get_device() != dev:
-        _elsewhere(rope.freqs, dev, "the plan's frequencies")
+    axes = 1 if rope is None else getattr(rope, "axes", 1)
     k, v = first[0], second[0]
     if (k is None) != (v is None):
         raise ValueError(f"{first[1]} and {second[1]} come together")
-    if rope.rotary_dim > width:
-        raise ValueError(f"the plan turns {rope.rotary_dim} entries of {width}")
+    freqs = of_pair = rot = layout = pos = apart = 0
+    factor = 1.0
+    if rope is None:  # rows as they are
+        if positions is not None or q is not None:
+            raise ValueError("positions and queries need a plan")
+        n = _on(out_loc, dev, torch.int32, "out_loc").numel()
+    else:
+        pos, n, apart = _positions_of(positions, dev, axes)
+        if rope.rotary_dim and rope.freqs.get_device() != dev:
+            _elsewhere(rope.freqs, dev, "the plan's frequencies")
+        freqs, rot, layout, factor = rope.freqs.data_ptr(), rope.rotary_dim, rope.layout, rope.attn_factor
+        if axes > 1:
+            of_pair = rope.pair_axis.data_ptr()
+    if rot > width:
+        raise ValueError(f"the plan turns {rot} entries of {width}")
     qp = qt = qh = heads = op = ot = oh = kp = kt = vp = vt = loc = 0
     if q is not None:
         qp, qt, qh, heads = _heads_view(q, dev, dt, "q", None, width)
@@ -361,19 +496,25 @@ def _rotary_call(fn, what, pool, layer, q, first, second, positions, out_loc, ro
         if _on(out_loc, dev, torch.int32, "out_loc").numel() != n:
             raise ValueError("out_loc and positions must have the same length")
         loc = out_loc.data_ptr()
-    _check(fn(pool.handle, layer, qp, qt, qh, heads, kp, kt, vp, vt, positions.data_ptr(), loc, n, rope.freqs.data_ptr(),
-              rope.rotary_dim, rope.layout, rope.attn_factor, op, ot, oh, _raw_stream(stream)), what)
+    if axes > 1 or always_axes:
+        what = what if always_axes else what + "_axes"
+        _check(getattr(lib(), what)(pool.handle, layer, qp, qt, qh, heads, kp, kt, vp, vt, pos, apart, loc, n, freqs, of_pair,
+                                    axes, rot, layout, factor, op, ot, oh, _raw_stream(stream)), what)
+    else:
+        _check(getattr(lib(), what)(pool.handle, layer, qp, qt, qh, heads, kp, kt, vp, vt, pos, loc, n, freqs, rot, layout,
+                                    factor, op, ot, oh, _raw_stream(stream)), what)
 
 
 def rotary_store_cache(pool, layer, q, k, v, positions, out_loc, rope, q_out, stream=None):
     """Rotary positions of a step's q and k, and the store of the rotated k and
     of v, in one launch. q, q_out [n, Hq, D] (any token and head strides;
     q_out may be q), k, v [n, kv_heads, D] (any token stride), positions and
-    out_loc int32 [n], ``rope`` a RotaryPlan. q and q_out None: only the store;
-    k, v and out_loc None: only q. See include/pagedkv.h."""
+    out_loc int32 [n], ``rope`` a RotaryPlan (of several axes: positions int32
+    [axes, n]). q and q_out None: only the store; k, v and out_loc None: only
+    q. See include/pagedkv.h."""
     h, d = pool.kv_heads, pool.head_dim
-    _rotary_call(lib().rotary_store_cache, "rotary_store_cache", pool, layer, q, (k, "k", h, d), (v, "v", h, d), positions,
-                 out_loc, rope, q_out, d, stream)
+    _rotary_call("rotary_store_cache", pool, layer, q, (k, "k", h, d), (v, "v", h, d), positions, out_loc, rope, q_out, d,
+                 stream)
 
 
 def rotary_store_latent(pool, layer, q_pe, latent, k_pe, positions, out_loc, rope, q_pe_out, stream=None):
@@ -381,8 +522,86 @@ def rotary_store_latent(pool, layer, q_pe, latent, k_pe, positions, out_loc, rop
     (q_pe_out usually the tail of the absorbed queries), latent [n,
     latent_dim] and k_pe [n, rope_dim] with any token stride. q_pe and
     q_pe_out None: only the store; latent, k_pe and out_loc None: only q_pe."""
-    _rotary_call(lib().rotary_store_latent, "rotary_store_latent", pool, layer, q_pe, (latent, "latent", 1, pool.latent_dim),
+    _rotary_call("rotary_store_latent", pool, layer, q_pe, (latent, "latent", 1, pool.latent_dim),
                  (k_pe, "k_pe", 1, pool.rope_dim), positions, out_loc, rope, q_pe_out, pool.rope_dim, stream)
+
+
+def rotary_store_fp4(pool, layer, q, k, v, positions, out_loc, rope, q_out, stream=None):
+    """rotary_store_cache into a Fp4Pool: the rotated k and v are rounded to four
+    bits as they are stored (the rotated k is not rounded before). See
+    include/pagedkv.h."""
+    if rope is None:
+        raise ValueError("rotary_store_fp4 needs a plan (rows as they are: store_cache_fp4)")
+    h, d = pool.kv_heads, pool.head_dim
+    _rotary_call("rotary_store_fp4", pool, layer, q, (k, "k", h, d), (v, "v", h, d), positions, out_loc, rope, q_out, d, stream,
+                 always_axes=True)
+
+
+def store_cache_fp4(pool, layer, k, v, out_loc, stream=None):
+    """store_cache of a Fp4Pool: k, v [n, kv_heads, D] as they are (any token
+    stride), rounded to four bits, to the slots out_loc int32 [n]."""
+    h, d = pool.kv_heads, pool.head_dim
+    if k is None:
+        raise ValueError("store_cache_fp4 needs k and v")
+    _rotary_call("rotary_store_fp4", pool, layer, None, (k, "k", h, d), (v, "v", h, d), None, out_loc, None, None, d, stream,
+                 always_axes=True)
+
+
+def load_cache_fp4(pool, layer, slots, k_out, v_out, stream=None):
+    """The rows of a Fp4Pool at ``slots`` (int32 [n], any order) as the values
+    they stand for: k_out, v_out [n, kv_heads, D] contiguous, pool dtype."""
+    dt, dev = _TORCH_DTYPE[pool.dtype], pool.device_index
+    n = _on(slots, dev, torch.int32, "slots").numel()
+    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
+        if _on(t, dev, dt, name).numel() != n * pool.kv_heads * pool.head_dim:
+            raise ValueError(f"{name} must be [{n}, {pool.kv_heads}, {pool.head_dim}], got {tuple(t.shape)}")
+    _check(lib().load_cache_fp4(pool.handle, layer, slots.data_ptr(), n, k_out.data_ptr(), v_out.data_ptr(),
+                                _raw_stream(stream)), "load_cache_fp4")
+
+
+def paged_fp4_attention_workspace_size(pool, batch, chunk, num_q_heads, max_context):
+    n = ctypes.c_size_t()
+    _check(lib().paged_fp4_attention_workspace_size(pool.handle, batch, chunk, num_q_heads, max_context, ctypes.byref(n)),
+           "paged_fp4_attention_workspace_size")
+    return n.value
+
+
+def alloc_fp4_workspace(pool, batch, chunk, num_q_heads, max_context, device="cuda"):
+    nbytes = paged_fp4_attention_workspace_size(pool, batch, chunk, num_q_heads, max_context)
+    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def paged_fp4_attention(pool, layer, q, table, table_mode, context_lens, window, scale, out, workspace, q_lens=None,
+                        table_rows=None, stream=None, sinks=0, max_context=None):
+    """Attention over a Fp4Pool: q, out [B, C, Hq, D]; query j of request b sits
+    at position context_lens[b] - q_lens[b] + j (q_lens None: C) and attends
+    causally (decode: C = 1). Rows j >= q_lens[b] are not written.
+    ``max_context``: a bound of context_lens (None: what the table holds), the
+    one the workspace was made for. See include/pagedkv.h."""
+    dt, dev = _TORCH_DTYPE[pool.dtype], pool.device_index
+    _on(q, dev, dt, "q")
+    _on(out, dev, dt, "out")
+    _on(table, dev, torch.int32, "table")
+    _on(context_lens, dev, torch.int32, "context_lens")
+    shape = q.shape
+    if len(shape) != 4 or shape[3] != pool.head_dim or out.shape != shape:
+        raise ValueError("q and out must be [B, C, Hq, D]")
+    B, C, Hq, _ = shape
+    per = [0, 0]
+    for i, (t, nm) in enumerate(((q_lens, "q_lens"), (table_rows, "table_rows"))):
+        if t is not None:
+            if _on(t, dev, torch.int32, nm).numel() != B:
+                raise ValueError(f"{nm} must be [B]")
+            per[i] = t.data_ptr()
+    if context_lens.numel() != B or table.dim() != 2:
+        raise ValueError("context_lens must be [B], table [rows, columns]")
+    rows, cols = table.shape
+    if max_context is None:
+        max_context = min(cols if table_mode == KVP_RAW_LOCATIONS else cols * pool.page_size, (1 << 31) - 1)
+    _check(lib().paged_fp4_attention(pool.handle, layer, q.data_ptr(), B, C, Hq, per[0], table.data_ptr(), rows, cols,
+                                     table_mode, per[1], context_lens.data_ptr(), int(max_context), int(window or 0),
+                                     int(sinks), float(scale), out.data_ptr(), _on(workspace, dev, None, "workspace").data_ptr(),
+                                     workspace.nbytes, _raw_stream(stream)), "paged_fp4_attention")
 
 
 def paged_latent_attention_workspace_size(pool, batch, chunk, num_q_heads):

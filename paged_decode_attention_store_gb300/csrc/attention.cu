@@ -206,14 +206,14 @@ using namespace kvp;
 
 extern "C" int paged_decode_attention_workspace_size(const kvp_pool* pool, int batch, int num_q_heads,
                                                      size_t* bytes) {
-  if (!pool || pool->latent_dim || !bytes || batch <= 0 || num_q_heads <= 0) return KVP_ERR_INVALID_ARG;
+  if (!pool || !pool->kv_rows() || !bytes || batch <= 0 || num_q_heads <= 0) return KVP_ERR_INVALID_ARG;
   *bytes = workspace_bytes_for(pool, batch, 1, num_q_heads);
   return KVP_OK;
 }
 
 extern "C" int paged_verify_attention_workspace_size(const kvp_pool* pool, int batch, int num_q_tokens,
                                                      int num_q_heads, size_t* bytes) {
-  if (!pool || pool->latent_dim || !bytes || batch <= 0 || num_q_heads <= 0 || num_q_tokens < 1) return KVP_ERR_INVALID_ARG;
+  if (!pool || !pool->kv_rows() || !bytes || batch <= 0 || num_q_heads <= 0 || num_q_tokens < 1) return KVP_ERR_INVALID_ARG;
   *bytes = workspace_bytes_for(pool, batch, num_q_tokens, num_q_heads);
   return KVP_OK;
 }
@@ -236,7 +236,7 @@ int attention_impl(const kvp_pool* pool, int layer, const void* q, int batch, in
                    const int32_t* table, int table_rows_total, int table_cols, int table_mode,
                    const int32_t* table_rows, const int32_t* context_lens, int window, int sinks, float scale,
                    void* out, void* workspace, size_t workspace_bytes, void* stream, const FuseIn* fz) {
-  if (!pool || pool->latent_dim || !q || !table || !context_lens || !out) return KVP_ERR_INVALID_ARG;
+  if (!pool || !pool->kv_rows() || !q || !table || !context_lens || !out) return KVP_ERR_INVALID_ARG;
   if (M < 1 || M > 32 || (fz && M != 1)) return KVP_ERR_INVALID_ARG;
   if (layer < 0 || layer >= pool->num_layers || batch <= 0 || num_q_heads <= 0) return KVP_ERR_INVALID_ARG;
   if (num_q_heads % pool->kv_heads) return KVP_ERR_INVALID_ARG;
@@ -413,7 +413,7 @@ extern "C" int paged_prefill_attention(const kvp_pool* pool, int layer, const vo
                                        int table_rows_total, int table_cols, int table_mode,
                                        const int32_t* table_rows, const int32_t* context_lens, int window, int sinks,
                                        float scale, void* out, void* stream) {
-  if (!pool || pool->latent_dim || !q || !table || !context_lens || !out) return KVP_ERR_INVALID_ARG;
+  if (!pool || !pool->kv_rows() || !q || !table || !context_lens || !out) return KVP_ERR_INVALID_ARG;
   if (layer < 0 || layer >= pool->num_layers || batch <= 0 || chunk <= 0 || num_q_heads <= 0) return KVP_ERR_INVALID_ARG;
   if (num_q_heads % pool->kv_heads) return KVP_ERR_INVALID_ARG;
   if (table_rows_total <= 0 || table_cols <= 0) return KVP_ERR_INVALID_ARG;

@@ -160,6 +160,7 @@ cudaError_t launch_tc(const TcArgs& a, const CombineArgs& c, cudaStream_t stream
 // ---------------------------------------------------------------------------
 // Latent pools (latent.cu, latent_tc.cu) and expanded prompts (expanded.cu).
 // ---------------------------------------------------------------------------
+constexpr int kFp4MaxDim = 256;  // head_dim of four-bit pools: the general kernel's registers hold 8 entries a lane
 constexpr int kLatentMaxDim = 1024;  // the general kernel's registers hold 32 floats a lane
 
 TableRef make_table(const kvp_pool* pool, const int32_t* table, int rows_total, int cols, int mode);
@@ -187,4 +188,23 @@ void latent_encode_map(kvp_pool* pool);
 bool latent_tc_eligible(const kvp_pool* pool, int C, int H);
 size_t latent_tc_workspace(const kvp_pool* pool, int C, int H);
 int launch_latent_tc(const LatentCall& c, cudaStream_t stream);
+
+// ---------------------------------------------------------------------------
+// Four-bit pools (fp4.cu, fp4_tc.cu).
+// ---------------------------------------------------------------------------
+// One call of paged_fp4_attention.
+struct Fp4Call {
+  const kvp_pool* pool;
+  int layer;
+  const void* q;  // [B, C, H, head_dim]
+  void* out;      // likewise
+  int B, C, H;
+  const int32_t* q_lens;
+  TableRef T;
+  const int32_t* table_rows;
+  const int32_t* context_lens;
+  int window, sinks, max_context;
+  float scale;
+  void* workspace;
+};
 }  // namespace kvp

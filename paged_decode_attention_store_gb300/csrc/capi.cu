@@ -1,4 +1,5 @@
 // Pool descriptor and device error word of libpagedkv.
+#include <cmath>
 #include <new>
 
 #include "attention.cuh"
@@ -47,6 +48,11 @@ int pool_create(int num_pages, int page_size, int kv_heads, int head_dim, int la
   p->tmap_hg = 0;
   p->tmap1_state = 0;
   p->lat_map_ok = 0;
+  p->fp4 = 0;
+  p->fp4_scales = nullptr;
+  p->fp4_scale_layer_bytes = 0;
+  p->fp4_globals = nullptr;
+  p->fp4_map_hg = 0;
   *out = p;
   return KVP_OK;
 }
@@ -68,7 +74,43 @@ extern "C" int kv_latent_pool_create(int num_pages, int page_size, int latent_di
   return rc;
 }
 
+extern "C" int kv_fp4_pool_create(int num_pages, int page_size, int kv_heads, int head_dim, int dtype, int num_layers,
+                                  void* codes, void* scales, const float* k_scales, const float* v_scales,
+                                  int32_t* error_word, kvp_pool** out) {
+  if (!out || !scales || (reinterpret_cast<uintptr_t>(scales) & 15) || kv_heads <= 0 || num_layers <= 0) return KVP_ERR_INVALID_ARG;
+  if (head_dim <= 0 || head_dim % 16 || head_dim > kvp::kFp4MaxDim || (long long)kv_heads * head_dim % 128)
+    return KVP_ERR_INVALID_ARG;
+  for (const float* g : {k_scales, v_scales})
+    for (int l = 0; g && l < num_layers; ++l) {
+      int e;
+      if (std::frexp(g[l], &e) != 0.5f || e < -63 || e > 65) return KVP_ERR_INVALID_ARG;  // a power of two in 2^-64 .. 2^64
+    }
+  float* globals = new (std::nothrow) float[2 * (size_t)num_layers];
+  if (!globals) return KVP_ERR_INVALID_ARG;
+  kvp_pool* p = nullptr;
+  const int rc = pool_create(num_pages, page_size, kv_heads, head_dim, 0, dtype, num_layers, codes, error_word, &p);
+  if (rc != KVP_OK) {
+    delete[] globals;
+    return rc;
+  }
+  for (int l = 0; l < num_layers; ++l) {
+    globals[l] = k_scales ? k_scales[l] : 1.f;
+    globals[num_layers + l] = v_scales ? v_scales[l] : 1.f;
+  }
+  p->fp4 = 1;
+  p->planes = 1;
+  p->row_bytes = (size_t)kv_heads * head_dim;
+  p->layer_bytes = (size_t)p->num_slots * p->row_bytes;
+  p->kv_bytes = 0;
+  p->fp4_scales = static_cast<char*>(scales);
+  p->fp4_scale_layer_bytes = ((size_t)p->num_slots + 15) / 16 * 16 * kv_heads * (head_dim / 8);
+  p->fp4_globals = globals;
+  *out = p;
+  return KVP_OK;
+}
+
 extern "C" int kv_pool_destroy(kvp_pool* pool) {
+  if (pool) delete[] pool->fp4_globals;
   delete pool;
   return KVP_OK;
 }

@@ -14,8 +14,9 @@ struct kvp_pool {
   int kv_heads;
   int head_dim;     // latent pools: latent_dim + rope_dim, with kv_heads 1
   int latent_dim;   // 0: K and V planes; else one plane of rows [latent | shared key part]
-  int planes;       // buffers of num_layers layers: 2 (K, V), or 1 (latent)
-  int dtype;        // kvp_dtype
+  int planes;       // buffers of num_layers layers: 2 (K, V), or 1 (latent rows, or a four-bit pool's codes)
+  int fp4;          // 1: a four-bit pool (fp4.cuh): buf holds the codes, fp4_scales the block scales
+  int dtype;        // kvp_dtype (four-bit pools: of what is stored, read and attended)
   int num_layers;
   int elem;         // bytes per element
   int num_slots;    // num_pages * page_size
@@ -35,6 +36,14 @@ struct kvp_pool {
   int tmap1_state;   // 0: not encoded yet, 1: both encoded, -1: refused
   CUtensorMap lat_box;  // latent pools: (d % 64, slot, d / 64, layer), box (64, 8, width / 64, 1)
   int lat_map_ok;       // 1: encoded (at creation), 0: the pool's shape does not take it
+  char* fp4_scales;     // four-bit pools: block scales, (layers, ceil(slots / 16), kv_heads, 16, 2, head_dim / 16)
+  size_t fp4_scale_layer_bytes;
+  float* fp4_globals;   // host [2 * num_layers]: layer l's K scale at l, its V scale at num_layers + l (powers of two)
+  CUtensorMap fp4_map;  // the codes as (byte of a head, slot, head, layer), box (128, 16, HG, 1)
+  int fp4_map_hg;       // heads per box it was encoded for (0: none yet, -HG: refused for HG)
+
+  // K and V planes of full elements: what the calls that are not for latent or four-bit pools take.
+  bool kv_rows() const { return !latent_dim && !fp4; }
 };
 
 namespace kvp {

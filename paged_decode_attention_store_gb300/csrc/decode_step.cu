@@ -29,7 +29,7 @@ extern "C" int kvp_decode_step(kvp_host* h, const kvp_pool* pool, int32_t* table
                                const void* const* v, void* const* out, void* const* layer_ready,
                                void* const* layer_done, int32_t* host_meta, int32_t* dev_meta, int meta_cap,
                                void* workspace, size_t workspace_bytes, void* stream, kvp_step_info* info) {
-  if (!h || !pool || pool->latent_dim || !table || !rids || n <= 0 || !q || !k || !v || !out || !host_meta || !dev_meta || !info)
+  if (!h || !pool || !pool->kv_rows() || !table || !rids || n <= 0 || !q || !k || !v || !out || !host_meta || !dev_meta || !info)
     return KVP_ERR_INVALID_ARG;
   if (table_mode != KVP_BLOCK_TABLE && table_mode != KVP_RAW_LOCATIONS) return KVP_ERR_INVALID_ARG;
   if (sinks < 0 || (window > 0 && sinks >= window)) return KVP_ERR_INVALID_ARG;
@@ -146,7 +146,7 @@ extern "C" int kvp_decode_step_device(kvp_dev_pages* d, const kvp_pool* pool, in
                                       const void* const* k, const void* const* v, void* const* out,
                                       void* const* layer_ready, void* const* layer_done, int32_t* scratch,
                                       int may_share, void* workspace, size_t workspace_bytes, void* stream) {
-  if (!d || !pool || pool->latent_dim || !table || !rids || n <= 0 || !q || !k || !v || !out || !scratch) return KVP_ERR_INVALID_ARG;
+  if (!d || !pool || !pool->kv_rows() || !table || !rids || n <= 0 || !q || !k || !v || !out || !scratch) return KVP_ERR_INVALID_ARG;
   if (sinks < 0 || (window > 0 && sinks >= window)) return KVP_ERR_INVALID_ARG;
   if (window <= 0) sinks = 0;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -193,7 +193,7 @@ extern "C" int kvp_decode_step_device_io(kvp_dev_pages* d, const kvp_pool* pool,
                                          void* const* k_dev, void* const* v_dev, void* const* out_dev,
                                          int32_t* scratch, int may_share, void* workspace, size_t workspace_bytes,
                                          void* stream) {
-  if (!d || !pool || pool->latent_dim || !q_host || !k_host || !v_host || !out_host || !q_dev || !k_dev || !v_dev || !out_dev ||
+  if (!d || !pool || !pool->kv_rows() || !q_host || !k_host || !v_host || !out_host || !q_dev || !k_dev || !v_dev || !out_dev ||
       n <= 0 || num_q_heads <= 0)
     return KVP_ERR_INVALID_ARG;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -256,7 +256,7 @@ extern "C" int kvp_verify_step_device_io(kvp_dev_pages* d, const kvp_pool* pool,
                                          void* const* v_dev, void* const* out_dev, int32_t* scratch, int may_share,
                                          void* workspace, size_t workspace_bytes, void* stream) {
   const int M = num_q_tokens;
-  if (!d || !pool || pool->latent_dim || !table || !rids || n <= 0 || M < 1 || num_q_heads <= 0 || !q_host || !k_host || !v_host ||
+  if (!d || !pool || !pool->kv_rows() || !table || !rids || n <= 0 || M < 1 || num_q_heads <= 0 || !q_host || !k_host || !v_host ||
       !n_back_host || !out_host || !q_dev || !k_dev || !v_dev || !out_dev || !scratch)
     return KVP_ERR_INVALID_ARG;
   if (sinks < 0 || (window > 0 && sinks >= window)) return KVP_ERR_INVALID_ARG;

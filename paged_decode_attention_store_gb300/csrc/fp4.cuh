@@ -1,0 +1,165 @@
+// Four-bit pools: layout and rounding.
+//
+// A block is 16 consecutive entries of one head's K or V of one token: 16
+// codes of 4 bits (e2m1: sign, then 0, 0.5, 1, 1.5, 2, 3, 4, 6) and one scale
+// (e4m3, never negative). An entry stands for code * scale * g, g a power of two
+// per layer and plane, so every value has six significant bits at most: exact in
+// bf16 and, without g, in fp16.
+//
+// Codes: a token's row is kv_heads * head_dim bytes, per head head_dim / 2 bytes
+// of K and head_dim / 2 of V (entry 2 i in the low half of byte i), so one row is
+// one contiguous copy whatever page or slot it lies in. Scales lie 16 slots
+// together, head by head: (slot / 16, head, slot % 16, K or V, block). A group of
+// 16 slots is then one contiguous copy that lands head-major, where the lanes of
+// a warp, one token each, read their scales from different banks; token-major rows
+// of 128 bytes would put all of them in one.
+#pragma once
+
+#include "common.cuh"
+
+namespace kvp {
+
+constexpr int kFp4Block = 16;
+
+// Byte offset of the scales of slot s, head h: head_dim / 16 of K, then of V.
+__host__ __device__ __forceinline__ size_t fp4_scale_offset(int s, int h, int kv_heads, int head_dim) {
+  return (((size_t)(s >> 4) * kv_heads + h) * 16 + (s & 15)) * (size_t)(head_dim / 8);
+}
+
+// The value of an e2m1 code without its sign bit, and of an e4m3 code below 0x7f.
+template <typename F>
+__device__ __forceinline__ F e2m1_value(uint32_t c) {
+  return c < 2 ? F(0.5) * F(c) : F(2 + (c & 1)) * F(1u << (c >> 1)) * F(0.25);
+}
+__device__ __forceinline__ float e4m3_value(uint32_t c) {
+  // exponent and mantissa at fp32's places: the value times 2^-120, its subnormals too
+  return __uint_as_float(c << 20) * 0x1p120f;
+}
+
+// Two floats to e2m1 (a in the low 4 bits), one to e4m3: nearest, ties to even, the largest value at most.
+__device__ __forceinline__ uint32_t e2m1x2(float a, float b) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 x;\n\tcvt.rn.satfinite.e2m1x2.f32 x, %2, %1;\n\tcvt.u32.u8 %0, x;\n\t}" : "=r"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3_code(float a) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(r) : "f"(a), "f"(0.f));
+  return r & 0xffu;
+}
+
+// The code of the scale for a block whose largest entry is m >= 0 (m / 6 g, nearest, ties to even), exact when m is and
+// F holds 7 bits more than the midpoints of two scales: products of small integers and powers of two.
+template <typename F>
+__device__ __forceinline__ uint32_t fp4_scale_exact(F m, F g) {
+  uint32_t c = e4m3_code((float)(m / g) * (1.f / 6.f));
+  // the midpoint of scales c and c + 1, times 6 g
+  auto border = [&](uint32_t k) { return (F(e4m3_value(k)) + F(e4m3_value(k + 1))) * F(3) * g; };
+  if (c < 0x7e && (m > border(c) || (m == border(c) && (c & 1)))) return c + 1;
+  if (c > 0 && (m < border(c - 1) || (m == border(c - 1) && (c & 1)))) return c - 1;
+  return c;
+}
+// The code (without sign) of |x| under the scale sg = scale * g > 0, likewise.
+template <typename F>
+__device__ __forceinline__ uint32_t fp4_code_exact(F ax, F sg) {
+  uint32_t c = e2m1x2((float)(ax / sg), 0.f) & 7u;
+  auto border = [&](uint32_t k) { return (e2m1_value<F>(k) + e2m1_value<F>(k + 1)) * F(0.5) * sg; };
+  if (c < 7 && (ax > border(c) || (ax == border(c) && (c & 1)))) return c + 1;
+  if (c > 0 && (ax < border(c - 1) || (ax == border(c - 1) && (c & 1)))) return c - 1;
+  return c;
+}
+
+// Whether a float is an infinity or NaN, by its bits without the sign.
+__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+constexpr uint32_t kInfBits = 0x7f800000u;
+constexpr uint32_t kFp4NanScale = 0x7fu;
+
+// N of a block's 16 entries in each of 16 / N neighbouring lanes (``mask``: those lanes). x is off by ex at most (0:
+// exact). Gives the lane's codes and the block's scale and returns false, or returns true, to all of the block's lanes,
+// when a rounding lies within the error of a border and x has to be found more exactly. A block with an entry that is
+// not finite has the scale NaN.
+template <int N>
+__device__ __forceinline__ bool fp4_block(const float (&x)[N], const float (&ex)[N], float g, float inv_g, unsigned mask,
+                                          uint32_t& codes, uint32_t& scale) {
+  constexpr int kLanes = kFp4Block / N;
+  uint32_t mb = 0;
+  float em = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    mb = max(mb, abs_bits(x[i]));
+    em = fmaxf(em, ex[i]);
+  }
+#pragma unroll
+  for (int d = 1; d < kLanes; d <<= 1) {
+    mb = max(mb, __shfl_xor_sync(mask, mb, d));
+    em = fmaxf(em, __shfl_xor_sync(mask, em, d));
+  }
+  codes = 0;
+  scale = kFp4NanScale;
+  if (mb >= kInfBits) return false;
+  const float m = __uint_as_float(mb);
+  const float q = m * inv_g * (1.f / 6.f), eq = em * inv_g * (1.f / 6.f) + q * 0x1p-22f;
+  const uint32_t lo = e4m3_code(fmaxf(q - eq, 0.f)), hi = e4m3_code(q + eq);
+  scale = lo;
+  if (lo != hi) {
+    if (em > 0.f) return true;
+    scale = fp4_scale_exact<float>(m, g);
+  }
+  if (scale == 0) return false;
+  const float sg = e4m3_value(scale) * g, inv = __frcp_rn(sg);
+  uint32_t other = 0;
+  float el = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    const float r0 = x[i] * inv, r1 = x[i + 1] * inv;
+    const float e0 = ex[i] * inv + fabsf(r0) * 0x1p-22f, e1 = ex[i + 1] * inv + fabsf(r1) * 0x1p-22f;
+    codes |= e2m1x2(r0 - e0, r1 - e1) << (4 * i);
+    other |= e2m1x2(r0 + e0, r1 + e1) << (4 * i);
+    el = fmaxf(el, fmaxf(ex[i], ex[i + 1]));
+  }
+  bool near = false;
+  if (codes != other) {
+    near = el > 0.f;
+    if (!near) {
+      codes = 0;
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        codes |= (fp4_code_exact<float>(fabsf(x[i]), sg) | (__float_as_uint(x[i]) >> 28 & 8u)) << (4 * i);
+    }
+  }
+#pragma unroll
+  for (int d = 1; d < kLanes; d <<= 1) near |= (bool)__shfl_xor_sync(mask, (int)near, d);
+  return near;
+}
+
+// The same of entries known to 53 bits (finite ones).
+template <int N>
+__device__ __forceinline__ void fp4_block_exact(const double (&x)[N], double g, unsigned mask, uint32_t& codes,
+                                                uint32_t& scale) {
+  double m = 0.0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) m = fmax(m, fabs(x[i]));
+#pragma unroll
+  for (int d = 1; d < kFp4Block / N; d <<= 1) m = fmax(m, __shfl_xor_sync(mask, m, d));
+  codes = 0;
+  scale = fp4_scale_exact<double>(m, g);
+  if (scale == 0) return;
+  const double sg = (double)e4m3_value(scale) * g;
+#pragma unroll
+  for (int i = 0; i < N; ++i) codes |= (fp4_code_exact<double>(fabs(x[i]), sg) | (x[i] < 0.0 ? 8u : 0u)) << (4 * i);
+}
+
+// Eight codes to four pairs of fp16, and two scales to a pair: exact.
+__device__ __forceinline__ void e2m1x8_to_half(uint32_t w, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\tcvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\tcvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+}
+__device__ __forceinline__ uint32_t e4m3x2_to_half(uint32_t two) {
+  uint32_t h;
+  asm("{\n\t.reg .b16 a;\n\tcvt.u16.u32 a, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t}" : "=r"(h) : "r"(two));
+  return h;
+}
+
+}  // namespace kvp

@@ -29,7 +29,7 @@
 // heads 3.6 us; 8,192 of them 34.0 us (5.9 TB/s, 0.87 of a copy's rate); 65,537 of 64
 // heads, half of each turned, 410 us (6.6 TB/s, 0.97); 3,001 fp32 tokens of 16 heads 8.1
 // us; 16,461 latent rows with 32 heads' rotated parts 32.2 us (5.4 TB/s, 0.79).
-#include "common.cuh"
+#include "fp4.cuh"
 
 #include <cmath>
 
@@ -58,7 +58,24 @@ struct RotArgs {
   int n, tokens, hq, hk, d, rot, v_elems, num_slots;
   float attn;
   int32_t* err;
+  const uint8_t* pair_axis;  // positions of several axes: pair i's axis; axis x of token t at positions[x * pos_axis + t]
+  long long pos_axis;
+  int axes;
+  char* scales;  // four-bit pools: the layer's block scales; k_dst and v_dst are codes
+  float gk, gv;
 };
+
+// The position by which pair i of token tok turns.
+template <bool AXES>
+__device__ __forceinline__ int position_of(const RotArgs& a, size_t tok, int i) {
+  if (!AXES) return __ldg(a.positions + tok);
+  int x = __ldg(a.pair_axis + i);
+  if (x >= a.axes) {
+    set_error(a.err, KVP_ERR_BAD_INDEX);
+    x = 0;
+  }
+  return __ldg(a.positions + x * a.pos_axis + tok);
+}
 
 // (cos, sin) * attn of position p and the pair's frequency f (turns * 2^64).
 __device__ __forceinline__ float2 turn_of(int p, uint64_t f, float attn) {
@@ -72,6 +89,33 @@ __device__ __forceinline__ float2 turn_of(int p, uint64_t f, float attn) {
   const bool odd = quarters & 1;  // (c, s) -> (-s, c) a quarter
   const float x = odd ? s : c, y = odd ? c : s;
   return make_float2(((quarters + 1) & 2 ? -x : x) * attn, (quarters & 2 ? -y : y) * attn);
+}
+
+__device__ __forceinline__ double exact_value(float x) { return x; }
+__device__ __forceinline__ double exact_value(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+// Entry e of a head at src, turned, in 64 bits: what decides a rounding to four bits when 32 leave it open.
+template <typename T, bool AXES>
+__device__ double exact_entry(const RotArgs& a, const T* src, size_t tok, int e, bool half) {
+  if (e >= a.rot) return exact_value(src[e]);
+  const int pairs = a.rot / 2, i = half ? (e < pairs ? e : e - pairs) : e / 2;
+  const bool first = half ? e < pairs : !(e & 1);
+  const double x = exact_value(src[half ? i : 2 * i]), y = exact_value(src[half ? i + pairs : 2 * i + 1]);
+  const uint64_t t = (uint64_t)(int64_t)position_of<AXES>(a, tok, i) * __ldg(a.freqs + i);
+  double s, c;
+  sincospi((double)(int64_t)t * 0x1p-63, &s, &c);
+  return (first ? x * c - y * s : y * c + x * s) * (double)a.attn;
+}
+
+// N consecutive entries from e0 of key head h, in 64 bits, to their codes and the block's scale.
+template <typename T, bool AXES, int N>
+__device__ __noinline__ void exact_codes(const RotArgs& a, size_t tok, int h, int e0, bool half, unsigned mask,
+                                         uint32_t* codes, uint32_t* scale) {
+  const T* src = reinterpret_cast<const T*>(a.k + tok * a.k_tok) + (size_t)h * a.d;
+  double x[N];
+#pragma unroll 1
+  for (int i = 0; i < N; ++i) x[i] = exact_entry<T, AXES>(a, src, tok, e0 + i, half);
+  fp4_block_exact<N>(x, (double)a.gk, mask, *codes, *scale);
 }
 
 template <typename T>
@@ -111,12 +155,19 @@ struct RotUnit {
   uint4 w0, w1;
   char* dst;  // nullptr: nothing to do (past the last head, or a key without a slot)
   const float4* f;  // two pairs' turns, the next two ``rot_units`` further
+  int head;  // of keys into a four-bit pool
 };
 
 // 16-byte chunks: every row, stride and half of a pair block starts on 16 bytes. The fp32 interleaved form is held to
 // 48 registers, ten blocks an SM (the 56 it takes by itself: 9.1 us for 8.1 at 3,001 tokens); bounds cost the others.
-template <typename T, bool HALF>
-__global__ void __launch_bounds__(kRotThreads, !HALF && sizeof(T) == 4 ? 10 : 0) rotary_store_kernel(const RotArgs a) {
+//
+// FP4: keys and values go to a four-bit pool. A block of 16 entries lies in 16 / N neighbouring threads, which agree on
+// its largest entry by shuffles. The rotation's error (2^-21 of a pair's size; 2^-20 is reckoned with) leaves one
+// rounding in some ten thousand open: those blocks are done again in 64 bits, so that codes and scales are those of the
+// 64-bit formula.
+template <typename T, bool HALF, bool AXES, bool FP4>
+__global__ void __launch_bounds__(kRotThreads, !HALF && sizeof(T) == 4 && !AXES && !FP4 ? 10 : 0)
+    rotary_store_kernel(const __grid_constant__ RotArgs a) {
   constexpr int N = Vec<T>::N;
   constexpr int kV = 2;  // chunks of v a thread loads ahead
   constexpr int PU = HALF ? N : N / 2;  // pairs of a unit
@@ -157,24 +208,47 @@ __global__ void __launch_bounds__(kRotThreads, !HALF && sizeof(T) == 4 ? 10 : 0)
     if (is_q) {
       x.dst = a.q_out + tok * a.qo_tok + (size_t)h * a.qo_head + (size_t)e0 * sizeof(T);
     } else {
-      x.dst = a.k_dst + ((size_t)(h - a.hq) * a.d + e0) * sizeof(T);
+      x.head = h - a.hq;
+      x.dst = FP4 ? a.k_dst + (size_t)x.head * a.d + e0 / 2 : a.k_dst + ((size_t)x.head * a.d + e0) * sizeof(T);
       key_of = t;
     }
+  };
+  // N entries of a block to their place in a four-bit pool: entries e0 .. of plane ``part`` of a head; ``scale`` is the block's.
+  const unsigned block_mask = ((1u << (kFp4Block / N)) - 1u) << (tid & 31 & ~(kFp4Block / N - 1));
+  auto put_codes = [&](char* dst, uint32_t codes, uint32_t scale, int slot, int head, int part, int e0) {
+    if (N == 8) *reinterpret_cast<uint32_t*>(dst) = codes;
+    else *reinterpret_cast<uint16_t*>(dst) = (uint16_t)codes;
+    if (e0 % kFp4Block == 0)
+      a.scales[fp4_scale_offset(slot, head, a.v_elems / a.d, a.d) + part * (a.d / 16) + e0 / 16] = (char)scale;
+  };
+  auto put_block = [&](const float (&r)[N], const float (&er)[N], char* dst, int t, int slot, int head, int e0) {
+    uint32_t codes, scale;
+    if (fp4_block<N>(r, er, a.gk, 1.f / a.gk, block_mask, codes, scale))
+      exact_codes<T, AXES, N>(a, (size_t)(t0 + t), head, e0, HALF, block_mask, &codes, &scale);
+    put_codes(dst, codes, scale, slot, head, 0, e0);
   };
   auto store = [&](const RotUnit<T, HALF>& x, int u, int key_of) {
     if (!x.dst) return;
     char* dst = x.dst;
+    int slot = -1;
     if (key_of >= 0) {
-      const int slot = slots[key_of];
+      slot = slots[key_of];
       if (slot < 0) return;
       dst += (size_t)slot * a.row_bytes;
     }
     if (u >= rot_units) {
+      if (FP4 && key_of >= 0) {
+        float v[N], exact[N] = {};
+        Vec<T>::get(x.w0, v);
+        put_block(v, exact, dst, key_of, slot, x.head, HALF ? a.rot + (u - rot_units) * N : u * N);
+        return;
+      }
       *reinterpret_cast<uint4*>(dst) = x.w0;
       return;
     }
     float v[N];
     Vec<T>::get(x.w0, v);
+    const float off = fabsf(a.attn) * 0x1p-20f;
     if (HALF) {
       float y[N], r0[N], r1[N];
       Vec<T>::get(x.w1, y);
@@ -185,6 +259,14 @@ __global__ void __launch_bounds__(kRotThreads, !HALF && sizeof(T) == 4 ? 10 : 0)
         r1[i] = y[i] * f.x + v[i] * f.y;
         r0[i + 1] = v[i + 1] * f.z - y[i + 1] * f.w;
         r1[i + 1] = y[i + 1] * f.z + v[i + 1] * f.w;
+      }
+      if (FP4 && key_of >= 0) {
+        float er[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) er[i] = (fabsf(v[i]) + fabsf(y[i])) * off;
+        put_block(r0, er, dst, key_of, slot, x.head, u * N);
+        put_block(r1, er, dst + pairs / 2, key_of, slot, x.head, u * N + pairs);
+        return;
       }
       *reinterpret_cast<uint4*>(dst) = Vec<T>::put(r0);
       *reinterpret_cast<uint4*>(dst + (size_t)pairs * sizeof(T)) = Vec<T>::put(r1);
@@ -198,6 +280,13 @@ __global__ void __launch_bounds__(kRotThreads, !HALF && sizeof(T) == 4 ? 10 : 0)
         r[2 * i + 2] = v[2 * i + 2] * f.z - v[2 * i + 3] * f.w;
         r[2 * i + 3] = v[2 * i + 3] * f.z + v[2 * i + 2] * f.w;
       }
+      if (FP4 && key_of >= 0) {
+        float er[N];
+#pragma unroll
+        for (int i = 0; i < N; i += 2) er[i] = er[i + 1] = (fabsf(v[i]) + fabsf(v[i + 1])) * off;
+        put_block(r, er, dst, key_of, slot, x.head, u * N);
+        return;
+      }
       *reinterpret_cast<uint4*>(dst) = Vec<T>::put(r);
     }
   };
@@ -207,6 +296,16 @@ __global__ void __launch_bounds__(kRotThreads, !HALF && sizeof(T) == 4 ? 10 : 0)
   };
   auto v_put = [&](int c, const uint4& w) {
     const int t = c / v_chunks, slot = slots[t];
+    if (FP4) {
+      if (slot < 0) return;
+      const int e = (c - t * v_chunks) * N, head = e / a.d, e0 = e - head * a.d;
+      float x[N], exact[N] = {};
+      Vec<T>::get(w, x);
+      uint32_t codes, scale;
+      fp4_block<N>(x, exact, a.gv, 1.f / a.gv, block_mask, codes, scale);
+      put_codes(a.v_dst + (size_t)slot * a.row_bytes + (size_t)head * a.d + e0 / 2, codes, scale, slot, head, 1, e0);
+      return;
+    }
     if (slot >= 0) reinterpret_cast<uint4*>(a.v_dst + (size_t)slot * a.row_bytes)[c - t * v_chunks] = w;
   };
 
@@ -228,7 +327,7 @@ __global__ void __launch_bounds__(kRotThreads, !HALF && sizeof(T) == 4 ? 10 : 0)
     const int t = x / pairs, i = x - t * pairs;
     const int u = i / PU, r = i % PU;
     reinterpret_cast<float2*>(cs)[t * pairs + 2 * (r / 2 * rot_units + u) + (r & 1)] =
-        turn_of(__ldg(a.positions + t0 + t), __ldg(a.freqs + i), a.attn);
+        turn_of(AXES ? position_of<AXES>(a, (size_t)(t0 + t), i) : __ldg(a.positions + t0 + t), __ldg(a.freqs + i), a.attn);
   }
   __syncthreads();
 #pragma unroll
@@ -254,11 +353,11 @@ __device__ __forceinline__ void st1(__nv_bfloat16* p, float x) { *p = __float2bf
 
 // Any alignment and any even rotary_dim: one block per token, element by
 // element (a thread owns a whole pair, so q_out may be q itself).
-template <typename T>
+template <typename T, bool AXES>
 __global__ void __launch_bounds__(kRotThreads) rotary_store_elem_kernel(const RotArgs a, int half) {
   const size_t tok = blockIdx.x;
   const int tid = threadIdx.x, pairs = a.rot / 2, per = pairs + (a.d - a.rot);
-  const int p = __ldg(a.positions + tok);
+  const int p = AXES ? 0 : __ldg(a.positions + tok);
   char* krow = nullptr;
   if (a.k) {
     const int slot = __ldg(a.out_loc + tok);
@@ -283,7 +382,7 @@ __global__ void __launch_bounds__(kRotThreads) rotary_store_elem_kernel(const Ro
       dst[a.rot + i - pairs] = src[a.rot + i - pairs];
       continue;
     }
-    const float2 f = turn_of(p, __ldg(a.freqs + i), a.attn);
+    const float2 f = turn_of(AXES ? position_of<AXES>(a, tok, i) : p, __ldg(a.freqs + i), a.attn);
     const int e0 = half ? i : 2 * i, e1 = half ? i + pairs : 2 * i + 1;
     const float x0 = ld1(src + e0), x1 = ld1(src + e1);
     st1(dst + e0, x0 * f.x - x1 * f.y);
@@ -291,21 +390,105 @@ __global__ void __launch_bounds__(kRotThreads) rotary_store_elem_kernel(const Ro
   }
 }
 
+// Keys and values into a four-bit pool, any alignment and any even rotary_dim: a thread makes one block, in 64 bits.
+template <typename T, bool AXES>
+__global__ void __launch_bounds__(kRotThreads) fp4_store_elem_kernel(const __grid_constant__ RotArgs a, int half) {
+  const int blocks = a.d / kFp4Block, per = 2 * a.hk * blocks;
+  const long long stride = (long long)gridDim.x * kRotThreads;
+  for (long long id = (long long)blockIdx.x * kRotThreads + threadIdx.x; id < (long long)a.n * per; id += stride) {
+    const size_t tok = (size_t)(id / per);
+    const int x = (int)(id % per), part = x / (a.hk * blocks), h = x / blocks % a.hk, e0 = x % blocks * kFp4Block;
+    const int slot = __ldg(a.out_loc + tok);
+    if ((unsigned)slot >= (unsigned)a.num_slots) {
+      if (x == 0) set_error(a.err, KVP_ERR_BAD_INDEX);
+      continue;
+    }
+    const T* src = reinterpret_cast<const T*>(part ? a.v + tok * a.v_tok : a.k + tok * a.k_tok) + (size_t)h * a.d;
+    double v[kFp4Block];
+    bool finite = true;
+  #pragma unroll 1
+    for (int i = 0; i < kFp4Block; ++i) {
+      v[i] = part ? exact_value(src[e0 + i]) : exact_entry<T, AXES>(a, src, tok, e0 + i, half);
+      finite = finite && fabs(v[i]) <= 0x1.fffffep127;  // as the 32-bit formula's
+    }
+    uint32_t scale = kFp4NanScale, lo = 0, hi = 0;
+    if (finite) {
+      const double g = part ? a.gv : a.gk;
+      double m = 0.0;
+  #pragma unroll 1
+      for (int i = 0; i < kFp4Block; ++i) m = fmax(m, fabs(v[i]));
+      scale = fp4_scale_exact<double>(m, g);
+      const double sg = (double)e4m3_value(scale) * g;
+  #pragma unroll 1
+      for (int i = 0; scale && i < kFp4Block; ++i) {
+        const uint32_t c = (fp4_code_exact<double>(fabs(v[i]), sg) | (v[i] < 0.0 ? 8u : 0u)) << (4 * (i & 7));
+        if (i < 8) lo |= c;
+        else hi |= c;
+      }
+    }
+    char* dst = a.k_dst + (size_t)slot * a.row_bytes + (size_t)h * a.d + part * (a.d / 2) + e0 / 2;
+    reinterpret_cast<uint32_t*>(dst)[0] = lo;
+    reinterpret_cast<uint32_t*>(dst)[1] = hi;
+    a.scales[fp4_scale_offset(slot, h, a.hk, a.d) + part * blocks + e0 / 16] = (char)scale;
+  }
+}
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+template <typename T, bool HALF, bool FP4>
+void launch_vec(const RotArgs& a, unsigned grid, cudaStream_t st) {
+  if (a.pair_axis) rotary_store_kernel<T, HALF, true, FP4><<<grid, kRotThreads, 0, st>>>(a);
+  else rotary_store_kernel<T, HALF, false, FP4><<<grid, kRotThreads, 0, st>>>(a);
+}
+template <typename T, bool FP4>
+void launch_layout(const RotArgs& a, bool half, unsigned grid, cudaStream_t st) {
+  if (half) launch_vec<T, true, FP4>(a, grid, st);
+  else launch_vec<T, false, FP4>(a, grid, st);
+}
+template <typename T>
+void launch_elem(const RotArgs& a, bool half, cudaStream_t st) {
+  if (a.pair_axis) rotary_store_elem_kernel<T, true><<<a.n, kRotThreads, 0, st>>>(a, half);
+  else rotary_store_elem_kernel<T, false><<<a.n, kRotThreads, 0, st>>>(a, half);
+}
+template <typename T>
+void launch_fp4_elem(const RotArgs& a, bool half, cudaStream_t st) {
+  const long long blocks = ((long long)a.n * 2 * a.hk * (a.d / kFp4Block) + kRotThreads - 1) / kRotThreads;
+  const unsigned grid = (unsigned)(blocks < 1 << 20 ? blocks : 1 << 20);
+  if (a.pair_axis) fp4_store_elem_kernel<T, true><<<grid, kRotThreads, 0, st>>>(a, half);
+  else fp4_store_elem_kernel<T, false><<<grid, kRotThreads, 0, st>>>(a, half);
+}
 
 int launch_rotary(const kvp_pool* pool, RotArgs& a, int layout, cudaStream_t st) {
   const int es = pool->elem, N = 16 / es;
-  const bool half = layout == KVP_ROTARY_HALF;
+  const bool half = layout == KVP_ROTARY_HALF, fp4 = pool->fp4 && a.k;
   const int span = half ? a.rot / 2 : a.rot;  // contiguous elements of a rotated block
-  bool vec = a.d % N == 0 && span % N == 0 && a.rot / 2 <= kRotMaxPairs;
-  if (a.q)
-    vec = vec && aligned16(a.q) && aligned16(a.q_out) && !((a.q_tok | a.q_head | a.qo_tok | a.qo_head) & 15);
+  // four bits: threads that share a block of 16 all turn it or all do not
+  bool vec = a.d % N == 0 && span % (fp4 ? kFp4Block : N) == 0 && a.rot / 2 <= kRotMaxPairs;
+  bool vec_q = true;
+  if (a.q) vec_q = aligned16(a.q) && aligned16(a.q_out) && !((a.q_tok | a.q_head | a.qo_tok | a.qo_head) & 15);
+  bool vec_k = true;
   if (a.k)
-    vec = vec && aligned16(a.k) && aligned16(a.v) && !((a.k_tok | a.v_tok) & 15) && a.v_elems % N == 0 &&
-          aligned16(a.k_dst) && aligned16(a.v_dst) && a.row_bytes % 16 == 0;
+    vec_k = aligned16(a.k) && aligned16(a.v) && !((a.k_tok | a.v_tok) & 15) && a.v_elems % N == 0 &&
+            (fp4 || (aligned16(a.k_dst) && aligned16(a.v_dst))) && a.row_bytes % 16 == 0;
+  if (fp4 && a.q && !(vec && vec_q && vec_k)) {  // the queries by themselves, then keys and values
+    RotArgs q = a;
+    q.k = q.v = nullptr;
+    q.hk = 0;
+    const int rc = launch_rotary(pool, q, layout, st);
+    if (rc != KVP_OK) return rc;
+    a.q = nullptr;
+    a.hq = 0;
+    vec_q = true;
+  }
+  vec = vec && vec_q && vec_k;
   if (!vec) {
-    if (es == 4) rotary_store_elem_kernel<float><<<a.n, kRotThreads, 0, st>>>(a, half);
-    else rotary_store_elem_kernel<__nv_bfloat16><<<a.n, kRotThreads, 0, st>>>(a, half);
+    if (fp4) {
+      if (es == 4) launch_fp4_elem<float>(a, half, st);
+      else launch_fp4_elem<__nv_bfloat16>(a, half, st);
+    } else {
+      if (es == 4) launch_elem<float>(a, half, st);
+      else launch_elem<__nv_bfloat16>(a, half, st);
+    }
     return cudaGetLastError() == cudaSuccess ? KVP_OK : KVP_ERR_CUDA;
   }
   // as many tokens a block as its shared memory's pairs allow, up to 4, once
@@ -315,27 +498,39 @@ int launch_rotary(const kvp_pool* pool, RotArgs& a, int layout, cudaStream_t st)
   a.tokens = tokens;
   const unsigned grid = (unsigned)(((long long)a.n + tokens - 1) / tokens);
   if (es == 4) {
-    if (half) rotary_store_kernel<float, true><<<grid, kRotThreads, 0, st>>>(a);
-    else rotary_store_kernel<float, false><<<grid, kRotThreads, 0, st>>>(a);
+    if (fp4) launch_layout<float, true>(a, half, grid, st);
+    else launch_layout<float, false>(a, half, grid, st);
   } else {
-    if (half) rotary_store_kernel<__nv_bfloat16, true><<<grid, kRotThreads, 0, st>>>(a);
-    else rotary_store_kernel<__nv_bfloat16, false><<<grid, kRotThreads, 0, st>>>(a);
+    if (fp4) launch_layout<__nv_bfloat16, true>(a, half, grid, st);
+    else launch_layout<__nv_bfloat16, false>(a, half, grid, st);
   }
   return cudaGetLastError() == cudaSuccess ? KVP_OK : KVP_ERR_CUDA;
 }
 
-// The checks both entry points share. ``width``: entries of a query head.
+// Positions of several axes: their number, the axis of each pair (device; not read for one axis), the distance of two
+// axes' positions in entries.
+struct Axes {
+  int count;
+  const uint8_t* of_pair;
+  long long stride;
+};
+constexpr Axes kOneAxis = {1, nullptr, 0};
+
+// The checks the entry points share. ``width``: entries of a query head.
 bool rotary_args_ok(const kvp_pool* pool, int layer, const void* q, long long q_stride, long long q_head_stride, int hq,
                     int width, const void* k, long long k_stride, const void* v, long long v_stride,
                     const int32_t* positions, const int32_t* out_loc, int n, const uint64_t* freqs,
                     int rotary_dim, int layout, float attn, const void* q_out, long long qo_stride,
-                    long long qo_head_stride) {
+                    long long qo_head_stride, const Axes& ax) {
   if (layer < 0 || layer >= pool->num_layers || n < 0) return false;
   if (layout != KVP_ROTARY_HALF && layout != KVP_ROTARY_INTERLEAVED) return false;
   if (rotary_dim < 0 || rotary_dim % 2 || rotary_dim > width || !(attn == attn)) return false;
+  if (ax.count < 1 || ax.count > KVP_ROTARY_MAX_AXES) return false;
   if (n == 0) return true;  // empty tensors may have no address
   if ((k == nullptr) != (v == nullptr) || (!q && !k)) return false;
-  if (!positions || (rotary_dim > 0 && !freqs)) return false;
+  if ((!positions && (q || rotary_dim > 0)) || (rotary_dim > 0 && !freqs)) return false;
+  if (ax.count != 1 && (rotary_dim > 0 && !ax.of_pair)) return false;
+  if (ax.count > 1 && ax.stride < n) return false;
   if (k && (!out_loc || k_stride < 0 || v_stride < 0)) return false;
   if (q) {
     if (!q_out || hq <= 0 || q_stride < 0 || q_head_stride < 0) return false;
@@ -388,47 +583,158 @@ extern "C" int kvp_rotary_frequencies(int rotary_dim, double base, int scaling, 
   return KVP_OK;
 }
 
+namespace kvp {
+namespace {
+
+// Every entry point's arguments; two rows a token: K and V, or the shared key part and the latent.
+struct RotaryCall {
+  const void* q;
+  long long q_stride, q_head_stride;
+  int num_q_heads;
+  const void* k;
+  long long k_stride;
+  const void* v;
+  long long v_stride;
+  const int32_t* positions;
+  const int32_t* out_loc;
+  int n;
+  const uint64_t* freqs;
+  int rotary_dim, layout;
+  float attn_factor;
+  void* q_out;
+  long long q_out_stride, q_out_head_stride;
+  Axes axes;
+};
+
+bool call_ok(const kvp_pool* pool, int layer, const RotaryCall& c, int width) {
+  return rotary_args_ok(pool, layer, c.q, c.q_stride, c.q_head_stride, c.num_q_heads, width, c.k, c.k_stride, c.v,
+                        c.v_stride, c.positions, c.out_loc, c.n, c.freqs, c.rotary_dim, c.layout, c.attn_factor, c.q_out,
+                        c.q_out_stride, c.q_out_head_stride, c.axes);
+}
+
+// What does not depend on the pool's kind.
+RotArgs common_args(const kvp_pool* pool, const RotaryCall& c) {
+  const long long es = pool->elem;
+  RotArgs a = {};
+  a.q = static_cast<const char*>(c.q);
+  a.q_out = static_cast<char*>(c.q_out);
+  a.q_tok = c.q_stride * es;
+  a.q_head = c.q_head_stride * es;
+  a.qo_tok = c.q_out_stride * es;
+  a.qo_head = c.q_out_head_stride * es;
+  a.k = static_cast<const char*>(c.k);
+  a.k_tok = c.k_stride * es;
+  a.v = static_cast<const char*>(c.v);
+  a.v_tok = c.v_stride * es;
+  a.row_bytes = pool->row_bytes;
+  a.positions = c.positions;
+  a.out_loc = c.out_loc;
+  a.freqs = c.freqs;
+  a.n = c.n;
+  a.hq = c.q ? c.num_q_heads : 0;
+  a.rot = c.rotary_dim;
+  a.num_slots = pool->num_slots;
+  a.attn = c.attn_factor;
+  a.err = pool->err;
+  if (c.axes.count > 1) {
+    a.pair_axis = c.axes.of_pair;
+    a.pos_axis = c.axes.stride;
+    a.axes = c.axes.count;
+  }
+  return a;
+}
+
+int store_planes(const kvp_pool* pool, int layer, const RotaryCall& c, void* stream) {
+  if (!pool || !pool->kv_rows()) return KVP_ERR_INVALID_ARG;
+  if (!call_ok(pool, layer, c, pool->head_dim)) return KVP_ERR_INVALID_ARG;
+  if (c.n == 0) return KVP_OK;
+  if (!pool_device_current(pool)) return KVP_ERR_INVALID_ARG;
+  RotArgs a = common_args(pool, c);
+  a.k_dst = pool->buf + (size_t)layer * pool->layer_bytes;
+  a.v_dst = a.k_dst + pool->kv_bytes;
+  a.hk = c.k ? pool->kv_heads : 0;
+  a.d = pool->head_dim;
+  a.v_elems = pool->kv_heads * pool->head_dim;
+  return launch_rotary(pool, a, c.layout, static_cast<cudaStream_t>(stream));
+}
+
+int store_fp4(const kvp_pool* pool, int layer, const RotaryCall& c, void* stream) {
+  if (!pool || !pool->fp4) return KVP_ERR_INVALID_ARG;
+  if (!call_ok(pool, layer, c, pool->head_dim)) return KVP_ERR_INVALID_ARG;
+  if (c.n == 0) return KVP_OK;
+  if (!pool_device_current(pool)) return KVP_ERR_INVALID_ARG;
+  RotArgs a = common_args(pool, c);
+  a.k_dst = pool->buf + (size_t)layer * pool->layer_bytes;
+  a.v_dst = a.k_dst + pool->head_dim / 2;
+  a.scales = pool->fp4_scales + (size_t)layer * pool->fp4_scale_layer_bytes;
+  a.gk = pool->fp4_globals[layer];
+  a.gv = pool->fp4_globals[pool->num_layers + layer];
+  a.hk = c.k ? pool->kv_heads : 0;
+  a.d = pool->head_dim;
+  a.v_elems = pool->kv_heads * pool->head_dim;
+  return launch_rotary(pool, a, c.layout, static_cast<cudaStream_t>(stream));
+}
+
+int store_latent(const kvp_pool* pool, int layer, RotaryCall c, void* stream) {
+  if (!pool || !pool->latent_dim) return KVP_ERR_INVALID_ARG;
+  const int dc = pool->latent_dim, dr = pool->head_dim - dc;
+  if (dr == 0) {  // rows without a rotated part: no queries, and k_pe may have no address
+    c.q = nullptr;
+    c.k = c.v;
+    c.k_stride = c.v_stride;
+    if (!c.v) return c.n == 0 ? KVP_OK : KVP_ERR_INVALID_ARG;
+  }
+  if (!call_ok(pool, layer, c, dr)) return KVP_ERR_INVALID_ARG;
+  if (c.n == 0) return KVP_OK;
+  if (!pool_device_current(pool)) return KVP_ERR_INVALID_ARG;
+  RotArgs a = common_args(pool, c);
+  a.v_dst = pool->buf + (size_t)layer * pool->layer_bytes;
+  a.k_dst = a.v_dst + (size_t)dc * pool->elem;
+  a.hk = c.k && dr > 0 ? 1 : 0;
+  a.d = dr;
+  a.v_elems = dc;
+  return launch_rotary(pool, a, c.layout, static_cast<cudaStream_t>(stream));
+}
+
+}  // namespace
+}  // namespace kvp
+
 extern "C" int rotary_store_cache(const kvp_pool* pool, int layer, const void* q, long long q_stride,
                                   long long q_head_stride, int num_q_heads, const void* k, long long k_stride,
                                   const void* v, long long v_stride, const int32_t* positions, const int32_t* out_loc,
                                   int n, const uint64_t* freqs, int rotary_dim, int layout, float attn_factor,
                                   void* q_out, long long q_out_stride, long long q_out_head_stride, void* stream) {
-  if (!pool || pool->latent_dim) return KVP_ERR_INVALID_ARG;
-  const int row = pool->kv_heads * pool->head_dim;
-  if (!kvp::rotary_args_ok(pool, layer, q, q_stride, q_head_stride, num_q_heads, pool->head_dim, k, k_stride, v, v_stride,
-                           positions, out_loc, n, freqs, rotary_dim, layout, attn_factor, q_out,
-                           q_out_stride, q_out_head_stride))
-    return KVP_ERR_INVALID_ARG;
-  if (n == 0) return KVP_OK;
-  if (!kvp::pool_device_current(pool)) return KVP_ERR_INVALID_ARG;
-  const long long es = pool->elem;
-  kvp::RotArgs a = {};
-  a.q = static_cast<const char*>(q);
-  a.q_out = static_cast<char*>(q_out);
-  a.q_tok = q_stride * es;
-  a.q_head = q_head_stride * es;
-  a.qo_tok = q_out_stride * es;
-  a.qo_head = q_out_head_stride * es;
-  a.k = static_cast<const char*>(k);
-  a.k_tok = k_stride * es;
-  a.v = static_cast<const char*>(v);
-  a.v_tok = v_stride * es;
-  a.k_dst = pool->buf + (size_t)layer * pool->layer_bytes;
-  a.v_dst = a.k_dst + pool->kv_bytes;
-  a.row_bytes = pool->row_bytes;
-  a.positions = positions;
-  a.out_loc = out_loc;
-  a.freqs = freqs;
-  a.n = n;
-  a.hq = q ? num_q_heads : 0;
-  a.hk = k ? pool->kv_heads : 0;
-  a.d = pool->head_dim;
-  a.rot = rotary_dim;
-  a.v_elems = row;
-  a.num_slots = pool->num_slots;
-  a.attn = attn_factor;
-  a.err = pool->err;
-  return kvp::launch_rotary(pool, a, layout, static_cast<cudaStream_t>(stream));
+  return kvp::store_planes(pool, layer,
+                           {q, q_stride, q_head_stride, num_q_heads, k, k_stride, v, v_stride, positions, out_loc, n, freqs,
+                            rotary_dim, layout, attn_factor, q_out, q_out_stride, q_out_head_stride, kvp::kOneAxis},
+                           stream);
+}
+
+extern "C" int rotary_store_cache_axes(const kvp_pool* pool, int layer, const void* q, long long q_stride,
+                                       long long q_head_stride, int num_q_heads, const void* k, long long k_stride,
+                                       const void* v, long long v_stride, const int32_t* positions,
+                                       long long position_stride, const int32_t* out_loc, int n, const uint64_t* freqs,
+                                       const uint8_t* pair_axis, int num_axes, int rotary_dim, int layout,
+                                       float attn_factor, void* q_out, long long q_out_stride,
+                                       long long q_out_head_stride, void* stream) {
+  return kvp::store_planes(pool, layer,
+                           {q, q_stride, q_head_stride, num_q_heads, k, k_stride, v, v_stride, positions, out_loc, n, freqs,
+                            rotary_dim, layout, attn_factor, q_out, q_out_stride, q_out_head_stride,
+                            {num_axes, pair_axis, position_stride}},
+                           stream);
+}
+
+extern "C" int rotary_store_fp4(const kvp_pool* pool, int layer, const void* q, long long q_stride,
+                                long long q_head_stride, int num_q_heads, const void* k, long long k_stride,
+                                const void* v, long long v_stride, const int32_t* positions, long long position_stride,
+                                const int32_t* out_loc, int n, const uint64_t* freqs, const uint8_t* pair_axis,
+                                int num_axes, int rotary_dim, int layout, float attn_factor, void* q_out,
+                                long long q_out_stride, long long q_out_head_stride, void* stream) {
+  return kvp::store_fp4(pool, layer,
+                        {q, q_stride, q_head_stride, num_q_heads, k, k_stride, v, v_stride, positions, out_loc, n, freqs,
+                         rotary_dim, layout, attn_factor, q_out, q_out_stride, q_out_head_stride,
+                         {num_axes, pair_axis, position_stride}},
+                        stream);
 }
 
 extern "C" int rotary_store_latent(const kvp_pool* pool, int layer, const void* q_pe, long long q_stride,
@@ -437,46 +743,23 @@ extern "C" int rotary_store_latent(const kvp_pool* pool, int layer, const void* 
                                    const int32_t* positions, const int32_t* out_loc, int n, const uint64_t* freqs,
                                    int rotary_dim, int layout, float attn_factor, void* q_pe_out,
                                    long long q_out_stride, long long q_out_head_stride, void* stream) {
-  if (!pool || !pool->latent_dim) return KVP_ERR_INVALID_ARG;
-  const int dc = pool->latent_dim, dr = pool->head_dim - dc;
-  if (dr == 0) {  // rows without a rotated part: no queries, and k_pe may have no address
-    q_pe = nullptr;
-    k_pe = latent;
-    k_pe_stride = latent_stride;
-    if (!latent) return n == 0 ? KVP_OK : KVP_ERR_INVALID_ARG;
-  }
-  if (!kvp::rotary_args_ok(pool, layer, q_pe, q_stride, q_head_stride, num_q_heads, dr, k_pe, k_pe_stride, latent,
-                           latent_stride, positions, out_loc, n, freqs, rotary_dim, layout, attn_factor, q_pe_out,
-                           q_out_stride, q_out_head_stride))
-    return KVP_ERR_INVALID_ARG;
-  if (n == 0) return KVP_OK;
-  if (!kvp::pool_device_current(pool)) return KVP_ERR_INVALID_ARG;
-  const long long es = pool->elem;
-  kvp::RotArgs a = {};
-  a.q = static_cast<const char*>(q_pe);
-  a.q_out = static_cast<char*>(q_pe_out);
-  a.q_tok = q_stride * es;
-  a.q_head = q_head_stride * es;
-  a.qo_tok = q_out_stride * es;
-  a.qo_head = q_out_head_stride * es;
-  a.k = static_cast<const char*>(k_pe);
-  a.k_tok = k_pe_stride * es;
-  a.v = static_cast<const char*>(latent);
-  a.v_tok = latent_stride * es;
-  a.v_dst = pool->buf + (size_t)layer * pool->layer_bytes;
-  a.k_dst = a.v_dst + (size_t)dc * pool->elem;
-  a.row_bytes = pool->row_bytes;
-  a.positions = positions;
-  a.out_loc = out_loc;
-  a.freqs = freqs;
-  a.n = n;
-  a.hq = q_pe ? num_q_heads : 0;
-  a.hk = k_pe && dr > 0 ? 1 : 0;
-  a.d = dr;
-  a.rot = rotary_dim;
-  a.v_elems = dc;
-  a.num_slots = pool->num_slots;
-  a.attn = attn_factor;
-  a.err = pool->err;
-  return kvp::launch_rotary(pool, a, layout, static_cast<cudaStream_t>(stream));
+  return kvp::store_latent(pool, layer,
+                           {q_pe, q_stride, q_head_stride, num_q_heads, k_pe, k_pe_stride, latent, latent_stride, positions,
+                            out_loc, n, freqs, rotary_dim, layout, attn_factor, q_pe_out, q_out_stride, q_out_head_stride,
+                            kvp::kOneAxis},
+                           stream);
+}
+
+extern "C" int rotary_store_latent_axes(const kvp_pool* pool, int layer, const void* q_pe, long long q_stride,
+                                        long long q_head_stride, int num_q_heads, const void* latent,
+                                        long long latent_stride, const void* k_pe, long long k_pe_stride,
+                                        const int32_t* positions, long long position_stride, const int32_t* out_loc, int n,
+                                        const uint64_t* freqs, const uint8_t* pair_axis, int num_axes, int rotary_dim,
+                                        int layout, float attn_factor, void* q_pe_out, long long q_out_stride,
+                                        long long q_out_head_stride, void* stream) {
+  return kvp::store_latent(pool, layer,
+                           {q_pe, q_stride, q_head_stride, num_q_heads, k_pe, k_pe_stride, latent, latent_stride, positions,
+                            out_loc, n, freqs, rotary_dim, layout, attn_factor, q_pe_out, q_out_stride, q_out_head_stride,
+                            {num_axes, pair_axis, position_stride}},
+                           stream);
 }

@@ -4,7 +4,7 @@
 // (copy-on-write of whole pages). All three are bandwidth- or latency-bound
 // byte moves: 16-byte vector accesses, consecutive threads on consecutive
 // bytes of one row, a grid sized in multiples of the SM count.
-#include "common.cuh"
+#include "fp4.cuh"
 
 namespace kvp {
 
@@ -78,6 +78,33 @@ __global__ void page_table_write_kernel(int32_t* __restrict__ table, int rows_to
   }
 }
 
+// The same for a four-bit pool's block scales: unit u of pair p, layer l, offset o in the page is one head's scales of
+// one slot, ``bytes`` long (a multiple of two); slots lie 16 together, head by head (fp4.cuh).
+__global__ void copy_page_scales_kernel(char* __restrict__ scales, size_t layer_bytes, int layers, int kv_heads,
+                                        int head_dim, const int32_t* __restrict__ src, const int32_t* __restrict__ dst,
+                                        int n, const int32_t* __restrict__ n_dev, int page_size, int num_pages) {
+  if (n_dev) n = min(n, max(0, __ldg(n_dev)));
+  const int bytes = head_dim / 8;
+  const long long total = (long long)n * layers * kv_heads * page_size;
+  for (long long u = blockIdx.x * (long long)blockDim.x + threadIdx.x; u < total;
+       u += (long long)gridDim.x * blockDim.x) {
+    const int o = (int)(u % page_size);
+    long long rest = u / page_size;
+    const int h = (int)(rest % kv_heads);
+    rest /= kv_heads;
+    const int l = (int)(rest % layers), p = (int)(rest / layers);
+    const int s = __ldg(src + p), d = __ldg(dst + p);
+    if ((unsigned)s >= (unsigned)num_pages || (unsigned)d >= (unsigned)num_pages) continue;  // the codes' copy records it
+    const char* from = scales + l * layer_bytes + fp4_scale_offset(s * page_size + o, h, kv_heads, head_dim);
+    char* to = scales + l * layer_bytes + fp4_scale_offset(d * page_size + o, h, kv_heads, head_dim);
+    if (bytes == 16) {
+      *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(from);
+    } else {
+      for (int i = 0; i < bytes; i += 2) *reinterpret_cast<uint16_t*>(to + i) = *reinterpret_cast<const uint16_t*>(from + i);
+    }
+  }
+}
+
 static int grid_for(long long work, int threads, int num_sms) {
   long long blocks = (work + threads - 1) / threads;
   long long cap = (long long)num_sms * 8;  // 8 resident 256-thread blocks per SM
@@ -96,7 +123,7 @@ static int sm_count_current() {
 
 extern "C" int store_cache(const kvp_pool* pool, int layer, const void* k, const void* v, const int32_t* out_loc,
                            int n, void* stream) {
-  if (!pool || pool->latent_dim || n < 0 || layer < 0 || layer >= pool->num_layers) return KVP_ERR_INVALID_ARG;
+  if (!pool || !pool->kv_rows() || n < 0 || layer < 0 || layer >= pool->num_layers) return KVP_ERR_INVALID_ARG;
   if (n == 0) return KVP_OK;
   if (!k || !v || !out_loc) return KVP_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 15) return KVP_ERR_INVALID_ARG;
@@ -109,29 +136,35 @@ extern "C" int store_cache(const kvp_pool* pool, int layer, const void* k, const
   return cudaGetLastError() == cudaSuccess ? KVP_OK : KVP_ERR_CUDA;
 }
 
+// n pairs, or as many as *n_dev says, n at most.
+static int copy_pages_impl(const kvp_pool* pool, const int32_t* src, const int32_t* dst, const int32_t* n_dev, int n,
+                           cudaStream_t st) {
+  const int page_chunks = (int)(pool->row_bytes * pool->page_size / 16);
+  const long long work = (long long)n * pool->num_layers * pool->planes * page_chunks;
+  const int threads = 256;
+  kvp::copy_pages_kernel<<<kvp::grid_for(work, threads, pool->num_sms), threads, 0, st>>>(
+      pool->buf, pool->layer_bytes, pool->num_layers * pool->planes, src, dst, n, n_dev, page_chunks, pool->num_pages, pool->err);
+  if (pool->fp4) {
+    const long long units = (long long)n * pool->num_layers * pool->kv_heads * pool->page_size;
+    kvp::copy_page_scales_kernel<<<kvp::grid_for(units, threads, pool->num_sms), threads, 0, st>>>(
+        pool->fp4_scales, pool->fp4_scale_layer_bytes, pool->num_layers, pool->kv_heads, pool->head_dim, src, dst, n, n_dev,
+        pool->page_size, pool->num_pages);
+  }
+  return cudaGetLastError() == cudaSuccess ? KVP_OK : KVP_ERR_CUDA;
+}
+
 extern "C" int copy_pages(const kvp_pool* pool, const int32_t* src, const int32_t* dst, int n, void* stream) {
   if (!pool || n < 0) return KVP_ERR_INVALID_ARG;
   if (n == 0) return KVP_OK;
   if (!src || !dst) return KVP_ERR_INVALID_ARG;
-  const int page_chunks = (int)(pool->row_bytes * pool->page_size / 16);
-  const long long work = (long long)n * pool->num_layers * pool->planes * page_chunks;
-  const int threads = 256;
-  kvp::copy_pages_kernel<<<kvp::grid_for(work, threads, pool->num_sms), threads, 0, (cudaStream_t)stream>>>(
-      pool->buf, pool->layer_bytes, pool->num_layers * pool->planes, src, dst, n, nullptr, page_chunks, pool->num_pages, pool->err);
-  return cudaGetLastError() == cudaSuccess ? KVP_OK : KVP_ERR_CUDA;
+  return copy_pages_impl(pool, src, dst, nullptr, n, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" int copy_pages_device_count(const kvp_pool* pool, const int32_t* src, const int32_t* dst,
                                        const int32_t* n_dev, int max_n, void* stream) {
   if (!pool || max_n < 0 || (max_n > 0 && (!src || !dst || !n_dev))) return KVP_ERR_INVALID_ARG;
   if (max_n == 0) return KVP_OK;
-  const int page_chunks = (int)(pool->row_bytes * pool->page_size / 16);
-  const long long work = (long long)max_n * pool->num_layers * pool->planes * page_chunks;
-  const int threads = 256;
-  kvp::copy_pages_kernel<<<kvp::grid_for(work, threads, pool->num_sms), threads, 0, (cudaStream_t)stream>>>(
-      pool->buf, pool->layer_bytes, pool->num_layers * pool->planes, src, dst, max_n, n_dev, page_chunks, pool->num_pages,
-      pool->err);
-  return cudaGetLastError() == cudaSuccess ? KVP_OK : KVP_ERR_CUDA;
+  return copy_pages_impl(pool, src, dst, n_dev, max_n, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" int page_table_write(int32_t* table, int table_rows_total, int table_cols, const int32_t* rows,
