@@ -207,4 +207,8 @@ struct Fp4Call {
   float scale;
   void* workspace;
 };
+// The tensor-core kernel for few query tokens (fp4_tc.cu): whether it takes a call's shape, its scratch, its launch.
+bool fp4_tc_eligible(const kvp_pool* pool, int C, int H);
+size_t fp4_tc_workspace(const kvp_pool* pool, int C, int H);
+int launch_fp4_tc(const Fp4Call& c, cudaStream_t stream);
 }  // namespace kvp

@@ -261,7 +261,8 @@ extern "C" int load_cache_fp4(const kvp_pool* pool, int layer, const int32_t* sl
 extern "C" int paged_fp4_attention_workspace_size(const kvp_pool* pool, int batch, int chunk, int num_q_heads,
                                                   int max_context, size_t* bytes) {
   if (!bytes || !shape_ok(pool, batch, chunk, num_q_heads, max_context)) return KVP_ERR_INVALID_ARG;
-  *bytes = 256;
+  const size_t need = fp4_tc_workspace(pool, chunk, num_q_heads);
+  *bytes = need ? need : 256;  // the general kernel needs none
   return KVP_OK;
 }
 
@@ -300,5 +301,6 @@ extern "C" int paged_fp4_attention(const kvp_pool* pool, int layer, const void* 
   c.max_context = cap < max_context ? (int)cap : max_context;
   c.scale = scale;
   c.workspace = workspace;
-  return launch_general(c, static_cast<cudaStream_t>(stream));
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return fp4_tc_eligible(pool, chunk, num_q_heads) ? launch_fp4_tc(c, st) : launch_general(c, st);
 }
