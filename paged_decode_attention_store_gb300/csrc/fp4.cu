@@ -1,13 +1,24 @@
-// Four-bit pools (fp4.cuh): the rows of given slots, the general attention
-// kernel, and the entry points of paged_fp4_attention.
+// Four-bit pools (fp4.cuh): rows turned back into full entries, the general
+// attention kernel, chunks, and the entry points of paged_fp4_attention.
 //
 // Mathematics: as attention.cu, over K and V entries code * scale * g. The
 // general kernel takes every type and width: one block per query token and
 // head, its warps take 32 positions in turn; a lane scores one position (its
-// K row is its own 8-byte loads), then the lanes take V's entries and the
-// positions' weights come by shuffles; the warps' running maxima, sums and
-// outputs are joined at the end. It is bound by instructions: a row is read
-// again for every query head.
+// K row is its own loads), then the lanes take V's entries and the positions'
+// weights come by shuffles; the warps' running maxima, sums and outputs are
+// joined at the end. It is bound by instructions: a row is read again for every
+// query head.
+//
+// Chunks (many query tokens a request) are bound by the matrix rate, and every
+// key is met by many query tiles: turning it back once a tile would cost more
+// than once a call. So a call turns the attended rows into bf16 (exactly) in its
+// workspace, request b's as the one page b of a pool whose pages are as long as
+// the longest context, and runs the chunk kernel of bf16 pools (prefill_tc.cu)
+// over them. Bytes: 1.1 KB read and 4 KB written a token of eight heads, and
+// read again by the chunk kernel, mostly from L2. That kernel multiplies V by
+// weights of zero where a query does not attend, so a block that reads as NaN
+// would reach more queries than it should: a request with one in its span is
+// noticed on the way and done again by the general kernel.
 #include <cstring>
 
 #include "attention.cuh"
@@ -18,6 +29,7 @@ namespace kvp {
 namespace {
 
 constexpr int kLoadThreads = 256;
+constexpr int kChunkColumns = 64;
 
 __device__ __forceinline__ float2 half2_floats(uint32_t h) {
   float2 f;
@@ -49,32 +61,101 @@ __device__ __forceinline__ void put8(__nv_bfloat16* dst, const float (&x)[8]) {
       make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
 }
 
-// Rows of slots: a thread turns four code bytes into eight entries; a warp reads the 128 bytes of a head of 128 and
-// writes 256 bytes of K and of V. Bytes bound it: 9 / 16 read, 2 written (bf16) an entry.
-template <typename T>
-__global__ void __launch_bounds__(kLoadThreads) load_fp4_kernel(const char* __restrict__ codes,
-                                                                 const char* __restrict__ scales, int heads, int d,
-                                                                 const int32_t* __restrict__ slots, int n, int num_slots,
-                                                                 float gk, float gv, T* __restrict__ k, T* __restrict__ v,
-                                                                 int32_t* err) {
-  const int per_head = d / 4;  // words of four code bytes: half of them K's
-  const long long total = (long long)n * heads * per_head;
-  for (long long u = blockIdx.x * (long long)kLoadThreads + threadIdx.x; u < total; u += (long long)gridDim.x * kLoadThreads) {
-    const int w = (int)(u % per_head);
-    const long long rest = u / per_head;
-    const int h = (int)(rest % heads);
-    const long long i = rest / heads;
-    const int part = w >= per_head / 2, e0 = (w - part * (per_head / 2)) * 8;
-    const int slot = __ldg(slots + i);
-    float x[8] = {};
-    if ((unsigned)slot < (unsigned)num_slots) {
-      const uint32_t c = __ldg(reinterpret_cast<const uint32_t*>(codes + (size_t)slot * heads * d + (size_t)h * d) + w);
-      const uint8_t* s = reinterpret_cast<const uint8_t*>(scales) + fp4_scale_offset(slot, h, heads, d);
-      fp4_entries(c, __ldg(s + part * (d / 16) + e0 / 16), part ? gv : gk, x);
-    } else if (w == 0 && h == 0) {
-      set_error(err, KVP_ERR_BAD_INDEX);
+constexpr int kUnpackRows = 32;  // rows a block
+
+// Chunks: where a request's rows come from, and what the launches after this one read.
+struct Chunk {
+  TableRef T;
+  const int32_t* context_lens;
+  const int32_t* q_lens;
+  const int32_t* table_rows;
+  int C, window, sinks, max_context;
+  int blocks;      // of kUnpackRows positions, max_context in all
+  long long page;  // rows of a request's page in the workspace
+  int32_t* lens;   // [B] context lengths, 0 for invalid requests
+  int32_t* table;  // [B] page b
+  int32_t* nan;    // [B][blocks] whether a row of the block has a scale NaN; written up to the context's end
+};
+
+struct Unpack {
+  const char* codes;
+  const char* scales;
+  int heads, d;
+  float gk, gv;
+  void* k;
+  void* v;
+  int32_t* err;
+  const int32_t* slots;  // rows of these slots ...
+  int n, num_slots;
+  Chunk ch;              // ... or of the requests' spans
+};
+
+__device__ __forceinline__ bool request_ok(int L, int ql, int row, int C, int max_context, int rows_total) {
+  return ql >= 1 && ql <= C && L >= ql && L <= max_context && row >= 0 && row < rows_total;
+}
+
+// Rows back to full entries: a block takes 32 rows (slots first, all at once), a thread turns four code bytes into eight
+// entries at a time; a warp reads the 128 bytes of a head of 128 and writes 256 bytes of K and of V. Bytes bound it: 9 / 16
+// read and 2 written (bf16) an entry.
+template <typename T, bool CHUNK>
+__global__ void __launch_bounds__(kLoadThreads) unpack_kernel(const __grid_constant__ Unpack a) {
+  __shared__ int slots[kUnpackRows];
+  const int tid = threadIdx.x;
+  const size_t row_entries = (size_t)a.heads * a.d;
+  size_t out0;  // row of slots[0] in k and v
+  int rows;
+  if (CHUNK) {
+    const Chunk& s = a.ch;
+    const int b = blockIdx.y, t0 = blockIdx.x * kUnpackRows;
+    const int L = __ldg(s.context_lens + b), ql = s.q_lens ? __ldg(s.q_lens + b) : s.C;
+    const int row = s.table_rows ? __ldg(s.table_rows + b) : b;
+    const bool ok = request_ok(L, ql, row, s.C, s.max_context, s.T.rows_total);
+    if (blockIdx.x == 0 && tid == 0) {
+      s.lens[b] = ok ? L : 0;
+      s.table[b] = b;
     }
-    put8((part ? v : k) + ((size_t)i * heads + h) * d + e0, x);
+    if (!ok || t0 >= L) return;
+    const int wide = s.window > 0 && ql - 1 < 0x7fffffff - s.window ? s.window + ql - 1 : 0;
+    const Span u = attend_span(L, wide, s.sinks);
+    if (tid < kUnpackRows) {
+      const int t = t0 + tid;
+      slots[tid] = t < L && (t >= u.lo || t < u.se) ? resolve_slot(s.T, row, t, a.err) : -1;
+    }
+    rows = min(kUnpackRows, L - t0);
+    out0 = (size_t)b * s.page + t0;
+  } else {
+    const long long i0 = (long long)blockIdx.x * kUnpackRows;
+    rows = (int)min((long long)kUnpackRows, a.n - i0);
+    if (tid < rows) {
+      const int slot = __ldg(a.slots + i0 + tid);
+      const bool good = (unsigned)slot < (unsigned)a.num_slots;
+      if (!good) set_error(a.err, KVP_ERR_BAD_INDEX);
+      slots[tid] = good ? slot : -1;
+    }
+    out0 = (size_t)i0;
+  }
+  __syncthreads();
+  const int words = a.d / 4, total = rows * a.heads * words;  // words of four code bytes, K's first in a head
+  bool nan = false;
+#pragma unroll 4
+  for (int u = tid; u < total; u += kLoadThreads) {
+    const int r = u / (a.heads * words), hw = u - r * (a.heads * words), h = hw / words, w = hw - h * words;
+    const int part = w >= words / 2, e0 = (w - part * (words / 2)) * 8, slot = slots[r];
+    float x[8] = {};
+    if (slot >= 0) {
+      const uint32_t c = __ldg(reinterpret_cast<const uint32_t*>(a.codes + (size_t)slot * row_entries) + hw);
+      const uint32_t s = __ldg(reinterpret_cast<const uint8_t*>(a.scales) + fp4_scale_offset(slot, h, a.heads, a.d) +
+                               part * (a.d / 16) + e0 / 16);
+      nan |= s == kFp4NanScale;
+      fp4_entries(c, s, part ? a.gv : a.gk, x);
+    } else if (CHUNK) {
+      continue;  // not attended, or a hole: nothing reads it, or what is read is unspecified
+    }
+    put8(static_cast<T*>(part ? a.v : a.k) + (out0 + r) * row_entries + (size_t)h * a.d + e0, x);
+  }
+  if (CHUNK) {
+    const int any = __syncthreads_or(nan);
+    if (tid == 0) a.ch.nan[(size_t)blockIdx.y * a.ch.blocks + blockIdx.x] = any;
   }
 }
 
@@ -99,17 +180,18 @@ __device__ __forceinline__ float as_float(__nv_bfloat16 x) { return __bfloat162f
 __device__ __forceinline__ void put1(float* p, float x) { *p = x; }
 __device__ __forceinline__ void put1(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
+// Query head ``item`` (of all requests' tokens' heads) by one block.
 template <typename T>
-__global__ void __launch_bounds__(32 * kGenWarps) fp4_general_kernel(const GenArgs a) {
+__device__ void general_item(const GenArgs& a, int item) {
   __shared__ float qs[kFp4MaxDim];
   __shared__ float part_o[kGenWarps][kFp4MaxDim], part_m[kGenWarps], part_l[kGenWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int h = blockIdx.x % a.Hq, bj = blockIdx.x / a.Hq, b = bj / a.C, j = bj % a.C;
+  const int h = item % a.Hq, bj = item / a.Hq, b = bj / a.C, j = bj % a.C;
   const int kvh = h / (a.Hq / a.Hkv), D = a.D;
-  T* out = static_cast<T*>(a.out) + (size_t)blockIdx.x * D;
-  const T* q = static_cast<const T*>(a.q) + (size_t)blockIdx.x * D;
+  T* out = static_cast<T*>(a.out) + (size_t)item * D;
+  const T* q = static_cast<const T*>(a.q) + (size_t)item * D;
   const int Lr = a.context_lens[b], row = a.table_rows ? a.table_rows[b] : b, ql = a.q_lens ? a.q_lens[b] : a.C;
-  if (ql < 1 || ql > a.C || Lr < ql || Lr > a.max_context || row < 0 || row >= a.T.rows_total) {
+  if (!request_ok(Lr, ql, row, a.C, a.max_context, a.T.rows_total)) {
     if (threadIdx.x == 0 && h == 0 && j == 0) set_error(a.err, KVP_ERR_BAD_INDEX);
     for (int d = threadIdx.x; d < D; d += blockDim.x) put1(out + d, 0.f);
     return;
@@ -198,7 +280,28 @@ __global__ void __launch_bounds__(32 * kGenWarps) fp4_general_kernel(const GenAr
   }
 }
 
-int launch_general(const Fp4Call& c, cudaStream_t st) {
+template <typename T>
+__global__ void __launch_bounds__(32 * kGenWarps) fp4_general_kernel(const __grid_constant__ GenArgs a) {
+  general_item<T>(a, blockIdx.x);
+}
+
+// Chunks: the requests with a scale NaN in their spans, all their query heads again.
+__global__ void __launch_bounds__(32 * kGenWarps)
+    fp4_again_kernel(const __grid_constant__ GenArgs a, int B, const int32_t* lens, const int32_t* nan, int blocks) {
+  for (int b = 0; b < B; ++b) {
+    const int n = (lens[b] + kUnpackRows - 1) / kUnpackRows;
+    int hit = 0;
+    for (int i = threadIdx.x; i < n; i += blockDim.x) hit |= nan[(size_t)b * blocks + i];
+    if (!__syncthreads_or(hit)) continue;
+    const int per = a.C * a.Hq;
+    for (int i = blockIdx.x; i < per; i += gridDim.x) {
+      general_item<__nv_bfloat16>(a, b * per + i);
+      __syncthreads();  // its shared memory is the next one's
+    }
+  }
+}
+
+GenArgs general_args(const Fp4Call& c) {
   GenArgs g;
   g.T = c.T;
   g.codes = c.pool->buf + (size_t)c.layer * c.pool->layer_bytes;
@@ -218,9 +321,92 @@ int launch_general(const Fp4Call& c, cudaStream_t st) {
   g.scale_log2 = c.scale * c.pool->fp4_globals[c.layer] * 1.4426950408889634f;
   g.gv = c.pool->fp4_globals[c.pool->num_layers + c.layer];
   g.err = c.pool->err;
+  return g;
+}
+
+int launch_general(const Fp4Call& c, cudaStream_t st) {
+  const GenArgs g = general_args(c);
   const unsigned grid = (unsigned)((long long)c.B * c.C * c.H);
   if (c.pool->dtype == KVP_F32) fp4_general_kernel<float><<<grid, 32 * kGenWarps, 0, st>>>(g);
   else fp4_general_kernel<__nv_bfloat16><<<grid, 32 * kGenWarps, 0, st>>>(g);
+  return cudaGetLastError() == cudaSuccess ? KVP_OK : KVP_ERR_CUDA;
+}
+
+Unpack unpack_args(const kvp_pool* pool, int layer, void* k, void* v) {
+  Unpack u = {};
+  u.codes = pool->buf + (size_t)layer * pool->layer_bytes;
+  u.scales = pool->fp4_scales + (size_t)layer * pool->fp4_scale_layer_bytes;
+  u.heads = pool->kv_heads;
+  u.d = pool->head_dim;
+  u.gk = pool->fp4_globals[layer];
+  u.gv = pool->fp4_globals[pool->num_layers + layer];
+  u.k = k;
+  u.v = v;
+  u.err = pool->err;
+  u.num_slots = pool->num_slots;
+  return u;
+}
+
+// A chunk's workspace for B requests of up to ``longest`` rows.
+struct ChunkLayout {
+  long long page;  // rows of a request
+  int blocks;
+  size_t lens, table, nan, kv, plane, total;
+};
+ChunkLayout chunk_layout(const kvp_pool* pool, int B, int longest) {
+  ChunkLayout l;
+  l.page = ((long long)longest + 15) / 16 * 16;
+  l.blocks = (longest - 1) / kUnpackRows + 1;
+  l.lens = 0;
+  l.table = align256(sizeof(int32_t) * (size_t)B);
+  l.nan = align256(l.table + sizeof(int32_t) * (size_t)B);
+  l.kv = align256(l.nan + sizeof(int32_t) * (size_t)B * l.blocks);
+  l.plane = (size_t)B * l.page * pool->kv_heads * pool->head_dim * 2;
+  l.total = l.kv + 2 * l.plane;
+  return l;
+}
+
+// The pool that a chunk's rows become: request b's are its page b.
+kvp_pool chunk_pool(const kvp_pool* pool, int B, const ChunkLayout& l, char* ws) {
+  kvp_pool p = *pool;
+  p.fp4 = 0;
+  p.planes = 2;
+  p.num_layers = 1;
+  p.num_pages = B;
+  p.page_size = (int)l.page;
+  p.num_slots = (int)(B * l.page);
+  p.row_bytes = (size_t)p.kv_heads * p.head_dim * 2;
+  p.layer_bytes = p.kv_bytes = l.plane;
+  p.buf = ws + l.kv;
+  p.tmap1_state = 0;  // its maps are made for this call
+  p.ev_before = p.ev_after = nullptr;
+  return p;
+}
+
+// Whether a call goes through the chunk kernel of bf16 pools. Few (token, head) columns a KV head are the decode kernel's.
+bool chunk_eligible(const kvp_pool* pool, int B, int C, int H, int longest, float scale) {
+  if ((long long)C * (H / pool->kv_heads) <= kChunkColumns && fp4_tc_eligible(pool, C, H)) return false;
+  return pool->dtype == KVP_BF16 && (long long)B * (((long long)longest + 15) / 16 * 16) <= 0x7fffffffLL && B <= 65535 &&
+         prefill_tc_eligible(pool, H, C, scale);
+}
+
+int launch_chunk(const Fp4Call& c, int longest, cudaStream_t st) {
+  const kvp_pool* pool = c.pool;
+  char* ws = static_cast<char*>(c.workspace);
+  const ChunkLayout l = chunk_layout(pool, c.B, longest);
+  kvp_pool rows = chunk_pool(pool, c.B, l, ws);
+  int32_t* lens = reinterpret_cast<int32_t*>(ws + l.lens);
+  int32_t* table = reinterpret_cast<int32_t*>(ws + l.table);
+  int32_t* nan = reinterpret_cast<int32_t*>(ws + l.nan);
+  Unpack u = unpack_args(pool, c.layer, ws + l.kv, ws + l.kv + l.plane);
+  u.ch = {c.T, c.context_lens, c.q_lens, c.table_rows, c.C, c.window, c.sinks, c.max_context, l.blocks, l.page, lens, table,
+          nan};
+  unpack_kernel<__nv_bfloat16, true><<<dim3(l.blocks, c.B), kLoadThreads, 0, st>>>(u);
+  if (cudaGetLastError() != cudaSuccess) return KVP_ERR_CUDA;
+  const int rc = launch_prefill_tc(&rows, 0, c.q, c.B, c.C, c.H, c.q_lens, make_table(&rows, table, c.B, 1, KVP_BLOCK_TABLE),
+                                   nullptr, lens, c.window, c.sinks, c.scale, c.out, st);
+  if (rc != KVP_OK) return rc;
+  fp4_again_kernel<<<2 * pool->num_sms, 32 * kGenWarps, 0, st>>>(general_args(c), c.B, lens, nan, l.blocks);
   return cudaGetLastError() == cudaSuccess ? KVP_OK : KVP_ERR_CUDA;
 }
 
@@ -241,27 +427,25 @@ extern "C" int load_cache_fp4(const kvp_pool* pool, int layer, const int32_t* sl
   if (!slots || !k || !v || ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 15))
     return KVP_ERR_INVALID_ARG;
   if (!pool_device_current(pool)) return KVP_ERR_INVALID_ARG;
-  const char* codes = pool->buf + (size_t)layer * pool->layer_bytes;
-  const char* scales = pool->fp4_scales + (size_t)layer * pool->fp4_scale_layer_bytes;
-  const float gk = pool->fp4_globals[layer], gv = pool->fp4_globals[pool->num_layers + layer];
-  const long long blocks = ((long long)n * pool->kv_heads * (pool->head_dim / 4) + kLoadThreads - 1) / kLoadThreads;
-  const unsigned grid = (unsigned)(blocks < 1 << 22 ? blocks : 1 << 22);
+  Unpack u = unpack_args(pool, layer, k, v);
+  u.slots = slots;
+  u.n = n;
+  const unsigned grid = (unsigned)(((long long)n + kUnpackRows - 1) / kUnpackRows);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (pool->dtype == KVP_F32)
-    load_fp4_kernel<float><<<grid, kLoadThreads, 0, st>>>(codes, scales, pool->kv_heads, pool->head_dim, slots, n,
-                                                          pool->num_slots, gk, gv, static_cast<float*>(k),
-                                                          static_cast<float*>(v), pool->err);
-  else
-    load_fp4_kernel<__nv_bfloat16><<<grid, kLoadThreads, 0, st>>>(codes, scales, pool->kv_heads, pool->head_dim, slots, n,
-                                                                  pool->num_slots, gk, gv, static_cast<__nv_bfloat16*>(k),
-                                                                  static_cast<__nv_bfloat16*>(v), pool->err);
+  if (pool->dtype == KVP_F32) unpack_kernel<float, false><<<grid, kLoadThreads, 0, st>>>(u);
+  else unpack_kernel<__nv_bfloat16, false><<<grid, kLoadThreads, 0, st>>>(u);
   return cudaGetLastError() == cudaSuccess ? KVP_OK : KVP_ERR_CUDA;
 }
 
 extern "C" int paged_fp4_attention_workspace_size(const kvp_pool* pool, int batch, int chunk, int num_q_heads,
                                                   int max_context, size_t* bytes) {
   if (!bytes || !shape_ok(pool, batch, chunk, num_q_heads, max_context)) return KVP_ERR_INVALID_ARG;
-  const size_t need = fp4_tc_workspace(pool, chunk, num_q_heads);
+  // whatever the scale's sign, which decides between chunk kernel and the others
+  size_t need = fp4_tc_workspace(pool, chunk, num_q_heads);
+  if (chunk_eligible(pool, batch, chunk, num_q_heads, max_context, 1.f)) {
+    const size_t rows = chunk_layout(pool, batch, max_context).total;
+    if (rows > need) need = rows;
+  }
   *bytes = need ? need : 256;  // the general kernel needs none
   return KVP_OK;
 }
@@ -302,5 +486,6 @@ extern "C" int paged_fp4_attention(const kvp_pool* pool, int layer, const void* 
   c.scale = scale;
   c.workspace = workspace;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (chunk_eligible(pool, batch, chunk, num_q_heads, max_context, scale)) return launch_chunk(c, max_context, st);
   return fp4_tc_eligible(pool, chunk, num_q_heads) ? launch_fp4_tc(c, st) : launch_general(c, st);
 }

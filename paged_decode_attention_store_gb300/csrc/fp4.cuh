@@ -27,9 +27,8 @@ __host__ __device__ __forceinline__ size_t fp4_scale_offset(int s, int h, int kv
 }
 
 // The value of an e2m1 code without its sign bit, and of an e4m3 code below 0x7f.
-template <typename F>
-__device__ __forceinline__ F e2m1_value(uint32_t c) {
-  return c < 2 ? F(0.5) * F(c) : F(2 + (c & 1)) * F(1u << (c >> 1)) * F(0.25);
+__device__ __forceinline__ float e2m1_value(uint32_t c) {
+  return c < 2 ? 0.5f * (float)c : (float)(2 + (c & 1)) * (float)(1u << (c >> 1)) * 0.25f;
 }
 __device__ __forceinline__ float e4m3_value(uint32_t c) {
   // exponent and mantissa at fp32's places: the value times 2^-120, its subnormals too
@@ -48,22 +47,20 @@ __device__ __forceinline__ uint32_t e4m3_code(float a) {
   return r & 0xffu;
 }
 
-// The code of the scale for a block whose largest entry is m >= 0 (m / 6 g, nearest, ties to even), exact when m is and
-// F holds 7 bits more than the midpoints of two scales: products of small integers and powers of two.
-template <typename F>
-__device__ __forceinline__ uint32_t fp4_scale_exact(F m, F g) {
+// The code of the scale for a block whose largest entry is m >= 0 (m / 6 g, nearest, ties to even): a first guess, put
+// right by comparing with the borders, which are small integers times powers of two.
+__device__ __forceinline__ uint32_t fp4_scale_exact(double m, double g) {
   uint32_t c = e4m3_code((float)(m / g) * (1.f / 6.f));
   // the midpoint of scales c and c + 1, times 6 g
-  auto border = [&](uint32_t k) { return (F(e4m3_value(k)) + F(e4m3_value(k + 1))) * F(3) * g; };
+  auto border = [&](uint32_t k) { return ((double)e4m3_value(k) + (double)e4m3_value(k + 1)) * 3.0 * g; };
   if (c < 0x7e && (m > border(c) || (m == border(c) && (c & 1)))) return c + 1;
   if (c > 0 && (m < border(c - 1) || (m == border(c - 1) && (c & 1)))) return c - 1;
   return c;
 }
 // The code (without sign) of |x| under the scale sg = scale * g > 0, likewise.
-template <typename F>
-__device__ __forceinline__ uint32_t fp4_code_exact(F ax, F sg) {
+__device__ __forceinline__ uint32_t fp4_code_exact(double ax, double sg) {
   uint32_t c = e2m1x2((float)(ax / sg), 0.f) & 7u;
-  auto border = [&](uint32_t k) { return (e2m1_value<F>(k) + e2m1_value<F>(k + 1)) * F(0.5) * sg; };
+  auto border = [&](uint32_t k) { return (double)(e2m1_value(k) + e2m1_value(k + 1)) * 0.5 * sg; };
   if (c < 7 && (ax > border(c) || (ax == border(c) && (c & 1)))) return c + 1;
   if (c > 0 && (ax < border(c - 1) || (ax == border(c - 1) && (c & 1)))) return c - 1;
   return c;
@@ -74,59 +71,70 @@ __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x
 constexpr uint32_t kInfBits = 0x7f800000u;
 constexpr uint32_t kFp4NanScale = 0x7fu;
 
-// N of a block's 16 entries in each of 16 / N neighbouring lanes (``mask``: those lanes). x is off by ex at most (0:
-// exact). Gives the lane's codes and the block's scale and returns false, or returns true, to all of the block's lanes,
-// when a rounding lies within the error of a border and x has to be found more exactly. A block with an entry that is
-// not finite has the scale NaN.
+// The largest of a block's entries by its bits, over the 16 / N neighbouring lanes (``mask``) that hold N each.
 template <int N>
-__device__ __forceinline__ bool fp4_block(const float (&x)[N], const float (&ex)[N], float g, float inv_g, unsigned mask,
-                                          uint32_t& codes, uint32_t& scale) {
-  constexpr int kLanes = kFp4Block / N;
+__device__ __forceinline__ uint32_t fp4_block_max(const float (&x)[N], unsigned mask) {
   uint32_t mb = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) mb = max(mb, abs_bits(x[i]));
+#pragma unroll
+  for (int d = 1; d < kFp4Block / N; d <<= 1) mb = max(mb, __shfl_xor_sync(mask, mb, d));
+  return mb;
+}
+
+// x / y by y's reciprocal, corrected once by the residual (which one fma gives exactly): off by a 2^-45th before its
+// rounding. Where the quotient is a border of two codes, four bits, it is that border; an x beside it, a 2^-24th away at
+// least, is not. Far quotients saturate whatever the correction, which would be no number where r overflows.
+__device__ __forceinline__ float quotient(float x, float y, float inv) {
+  const float r = x * inv;
+  return fabsf(r) < 1024.f ? fmaf(fmaf(-r, y, x), inv, r) : r;
+}
+
+// A block's codes and scale from exact entries, N of them in each of 16 / N neighbouring lanes. A block with an entry
+// that is not finite has the scale NaN.
+template <int N>
+__device__ __forceinline__ void fp4_block(const float (&x)[N], float g, float inv_g, unsigned mask, uint32_t& codes,
+                                          uint32_t& scale) {
+  const uint32_t mb = fp4_block_max<N>(x, mask);
+  codes = 0;
+  scale = kFp4NanScale;
+  if (mb >= kInfBits) return;
+  scale = e4m3_code(quotient(__uint_as_float(mb) * inv_g, 6.f, 1.f / 6.f));
+  if (scale == 0) return;
+  const float sg = e4m3_value(scale) * g, inv = __frcp_rn(sg);
+#pragma unroll
+  for (int i = 0; i < N; i += 2) codes |= e2m1x2(quotient(x[i], sg, inv), quotient(x[i + 1], sg, inv)) << (4 * i);
+}
+
+// The same from entries that are off by ex at most. Returns true, to all of the block's lanes, when a rounding lies within
+// the error of a border and the entries have to be found more exactly.
+template <int N>
+__device__ __forceinline__ bool fp4_block_within(const float (&x)[N], const float (&ex)[N], float g, float inv_g,
+                                                 unsigned mask, uint32_t& codes, uint32_t& scale) {
+  constexpr int kLanes = kFp4Block / N;
+  const uint32_t mb = fp4_block_max<N>(x, mask);
   float em = 0.f;
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    mb = max(mb, abs_bits(x[i]));
-    em = fmaxf(em, ex[i]);
-  }
+  for (int i = 0; i < N; ++i) em = fmaxf(em, ex[i]);
 #pragma unroll
-  for (int d = 1; d < kLanes; d <<= 1) {
-    mb = max(mb, __shfl_xor_sync(mask, mb, d));
-    em = fmaxf(em, __shfl_xor_sync(mask, em, d));
-  }
+  for (int d = 1; d < kLanes; d <<= 1) em = fmaxf(em, __shfl_xor_sync(mask, em, d));
   codes = 0;
   scale = kFp4NanScale;
   if (mb >= kInfBits) return false;
-  const float m = __uint_as_float(mb);
-  const float q = m * inv_g * (1.f / 6.f), eq = em * inv_g * (1.f / 6.f) + q * 0x1p-22f;
-  const uint32_t lo = e4m3_code(fmaxf(q - eq, 0.f)), hi = e4m3_code(q + eq);
-  scale = lo;
-  if (lo != hi) {
-    if (em > 0.f) return true;
-    scale = fp4_scale_exact<float>(m, g);
-  }
+  const float q = __uint_as_float(mb) * inv_g * (1.f / 6.f), eq = em * inv_g * (1.f / 6.f) + q * 0x1p-22f;
+  scale = e4m3_code(fmaxf(q - eq, 0.f));
+  if (scale != e4m3_code(q + eq)) return true;
   if (scale == 0) return false;
-  const float sg = e4m3_value(scale) * g, inv = __frcp_rn(sg);
+  const float inv = __frcp_rn(e4m3_value(scale) * g);
   uint32_t other = 0;
-  float el = 0.f;
 #pragma unroll
   for (int i = 0; i < N; i += 2) {
     const float r0 = x[i] * inv, r1 = x[i + 1] * inv;
-    const float e0 = ex[i] * inv + fabsf(r0) * 0x1p-22f, e1 = ex[i + 1] * inv + fabsf(r1) * 0x1p-22f;
+    const float e0 = fmaf(ex[i], inv, fabsf(r0) * 0x1p-22f), e1 = fmaf(ex[i + 1], inv, fabsf(r1) * 0x1p-22f);
     codes |= e2m1x2(r0 - e0, r1 - e1) << (4 * i);
     other |= e2m1x2(r0 + e0, r1 + e1) << (4 * i);
-    el = fmaxf(el, fmaxf(ex[i], ex[i + 1]));
   }
-  bool near = false;
-  if (codes != other) {
-    near = el > 0.f;
-    if (!near) {
-      codes = 0;
-#pragma unroll
-      for (int i = 0; i < N; ++i)
-        codes |= (fp4_code_exact<float>(fabsf(x[i]), sg) | (__float_as_uint(x[i]) >> 28 & 8u)) << (4 * i);
-    }
-  }
+  bool near = codes != other;
 #pragma unroll
   for (int d = 1; d < kLanes; d <<= 1) near |= (bool)__shfl_xor_sync(mask, (int)near, d);
   return near;
@@ -142,11 +150,11 @@ __device__ __forceinline__ void fp4_block_exact(const double (&x)[N], double g, 
 #pragma unroll
   for (int d = 1; d < kFp4Block / N; d <<= 1) m = fmax(m, __shfl_xor_sync(mask, m, d));
   codes = 0;
-  scale = fp4_scale_exact<double>(m, g);
+  scale = fp4_scale_exact(m, g);
   if (scale == 0) return;
   const double sg = (double)e4m3_value(scale) * g;
 #pragma unroll
-  for (int i = 0; i < N; ++i) codes |= (fp4_code_exact<double>(fabs(x[i]), sg) | (x[i] < 0.0 ? 8u : 0u)) << (4 * i);
+  for (int i = 0; i < N; ++i) codes |= (fp4_code_exact(fabs(x[i]), sg) | (x[i] < 0.0 ? 8u : 0u)) << (4 * i);
 }
 
 // Eight codes to four pairs of fp16, and two scales to a pair: exact.

@@ -221,9 +221,10 @@ __global__ void __launch_bounds__(kRotThreads, !HALF && sizeof(T) == 4 && !AXES 
     if (e0 % kFp4Block == 0)
       a.scales[fp4_scale_offset(slot, head, a.v_elems / a.d, a.d) + part * (a.d / 16) + e0 / 16] = (char)scale;
   };
+  const float inv_gk = FP4 ? 1.f / a.gk : 0.f, inv_gv = FP4 ? 1.f / a.gv : 0.f;
   auto put_block = [&](const float (&r)[N], const float (&er)[N], char* dst, int t, int slot, int head, int e0) {
     uint32_t codes, scale;
-    if (fp4_block<N>(r, er, a.gk, 1.f / a.gk, block_mask, codes, scale))
+    if (fp4_block_within<N>(r, er, a.gk, inv_gk, block_mask, codes, scale))
       exact_codes<T, AXES, N>(a, (size_t)(t0 + t), head, e0, HALF, block_mask, &codes, &scale);
     put_codes(dst, codes, scale, slot, head, 0, e0);
   };
@@ -238,9 +239,11 @@ __global__ void __launch_bounds__(kRotThreads, !HALF && sizeof(T) == 4 && !AXES 
     }
     if (u >= rot_units) {
       if (FP4 && key_of >= 0) {
-        float v[N], exact[N] = {};
+        float v[N];
+        uint32_t codes, scale;
         Vec<T>::get(x.w0, v);
-        put_block(v, exact, dst, key_of, slot, x.head, HALF ? a.rot + (u - rot_units) * N : u * N);
+        fp4_block<N>(v, a.gk, inv_gk, block_mask, codes, scale);
+        put_codes(dst, codes, scale, slot, x.head, 0, HALF ? a.rot + (u - rot_units) * N : u * N);
         return;
       }
       *reinterpret_cast<uint4*>(dst) = x.w0;
@@ -299,10 +302,10 @@ __global__ void __launch_bounds__(kRotThreads, !HALF && sizeof(T) == 4 && !AXES 
     if (FP4) {
       if (slot < 0) return;
       const int e = (c - t * v_chunks) * N, head = e / a.d, e0 = e - head * a.d;
-      float x[N], exact[N] = {};
+      float x[N];
       Vec<T>::get(w, x);
       uint32_t codes, scale;
-      fp4_block<N>(x, exact, a.gv, 1.f / a.gv, block_mask, codes, scale);
+      fp4_block<N>(x, a.gv, inv_gv, block_mask, codes, scale);
       put_codes(a.v_dst + (size_t)slot * a.row_bytes + (size_t)head * a.d + e0 / 2, codes, scale, slot, head, 1, e0);
       return;
     }
@@ -417,11 +420,11 @@ __global__ void __launch_bounds__(kRotThreads) fp4_store_elem_kernel(const __gri
       double m = 0.0;
   #pragma unroll 1
       for (int i = 0; i < kFp4Block; ++i) m = fmax(m, fabs(v[i]));
-      scale = fp4_scale_exact<double>(m, g);
+      scale = fp4_scale_exact(m, g);
       const double sg = (double)e4m3_value(scale) * g;
   #pragma unroll 1
       for (int i = 0; scale && i < kFp4Block; ++i) {
-        const uint32_t c = (fp4_code_exact<double>(fabs(v[i]), sg) | (v[i] < 0.0 ? 8u : 0u)) << (4 * (i & 7));
+        const uint32_t c = (fp4_code_exact(fabs(v[i]), sg) | (v[i] < 0.0 ? 8u : 0u)) << (4 * (i & 7));
         if (i < 8) lo |= c;
         else hi |= c;
       }

@@ -63,8 +63,9 @@ def rotate_axes(x, positions, theta, of_pair, layout, attn=1.0):
     return y, bound
 
 
-def attend(q, keys, vals, scale, dtype):
+def attend(q, keys, vals, scale, dtype, weights=torch.float16):
     """q [H, W], keys, vals [n, W] float64 -> (out [H, W], bound): operator_reference.attend with fp16 operands.
+    ``weights``: what bf16 pools' softmax weights are rounded to; the chunk kernel's are bf16, as those of a bf16 pool.
 
     Beyond the fp32 sums and exponentials: a query is scaled by a power of two to at most 1 and held in fp16, exact but
     below 2^-14, where it is off by 2^-25 at most: that times the keys' sizes moves a score. A weight is rounded once to
@@ -79,6 +80,6 @@ def attend(q, keys, vals, scale, dtype):
     wabs = torch.einsum("hn,nd->hd", w, vals.abs())
     n = keys.shape[0]
     half = dtype == torch.bfloat16
-    rel = 2 * torch.expm1(e) + 2 * (n + 16) * R.U32 + (2 * 2.0 ** -11 if half else 0.0)
+    rel = 2 * torch.expm1(e) + 2 * (n + 16) * R.U32 + (2 * R.u(weights) if half else 0.0)
     tiny = 2.0 ** -25 * n * vals.abs().amax() if half else 0.0
     return out, rel[:, None] * wabs + R.u(dtype) * out.abs() + tiny + 1e-30

@@ -147,6 +147,22 @@ def test_borders_and_extremes(kb, dtype, aligned):
     assert bool(ko[5:7, :, :32].isnan().any(-1).all()) and bool(ko[7].isnan().all()) and not bool(ko[8:].isnan().any())
 
 
+@pytest.mark.parametrize("e", [-64, 64])
+def test_global_scales_at_their_ends(kb, e):
+    """g = 2^-64 and 2^64: the codes of the values over g; far values saturate, with their signs."""
+    g = torch.Generator().manual_seed(11)
+    n, hkv, D = 20, 2, 64
+    x = torch.randn((n, 2 * hkv, D), generator=g).to(torch.bfloat16).double() * 2.0 ** e
+    x[3] *= 2.0 ** 30
+    x[4, :, ::2] = -3e38 if e < 0 else 2.0 ** 100
+    pool = make_pool(kb, 4, 16, hkv, D, "bf16", ks=2.0 ** e, vs=2.0 ** e)
+    loc = slots_of(n, 64, g)
+    d = x.to(torch.bfloat16).to(DEV)
+    kb.store_cache_fp4(pool, 0, d[:, :hkv], d[:, hkv:], loc.to(DEV))
+    x = d.double().cpu()
+    check_rows(pool, loc, x[:, :hkv], x[:, hkv:], 2.0 ** e, 2.0 ** e)
+
+
 def test_rows_as_they_are_at_position_zero(kb):
     """Nothing turns at position zero: borders are met exactly, where only 64 bits decide."""
     g = torch.Generator().manual_seed(6)
