@@ -54,10 +54,8 @@ constexpr int kD = 128;
 constexpr int kHeadBytes = kD;       // codes of one token and head: K, then V
 constexpr int kScaleBytes = kD / 8;  // scales of one token and head
 constexpr int kMaxStages = 6;
-constexpr int kAhead = 2;     // stages whose table entries are fetched ahead of their copies
-constexpr int kQueue = 4;     // > kAhead
 constexpr int kMaxConsumers = 8;
-constexpr int kThreads = 32 * (kMaxConsumers + 1);
+constexpr int kThreads = 32 * (kMaxConsumers + kMaxConsumers / 2);
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr size_t kSmemPerSm = 227 * 1024;  // what the CTAs of an SM share, 1 KB of each one's is the system's
 
@@ -73,30 +71,28 @@ struct Args {
   const int32_t* q_lens;
   const int32_t* context_lens;
   const int32_t* table_rows;
-  int B, C, Hq, Hkv, G, HG, n_groups, tiles, CW, stages, num_ctas;
+  int B, C, Hq, Hkv, G, HG, n_groups, tiles, CW, PW, stages, num_ctas;
+  int by_request;  // records are numbered by request and group (there are at most num_ctas), else by CTA
   int window, sinks, max_context;
   float scale_log2, gv;
-  int4* merge;    // [num_ctas] the cut request whose last piece is here: request and group, first CTA, its slot, last CTA
+  int4* merge;    // records of cut requests: request and group (-1: none), CTA and slot of the first piece, last CTA
   float* part_ml; // [2 * num_ctas][HG * C * G][2]
   float* part_o;  // [2 * num_ctas][HG * C * G][128]
   int32_t* err;
 };
 
 struct __align__(16) Hdr {
-  int live;
-  int t0;      // first position of the stage
-  int valid;   // bit j: position t0 + j is in the span and its row is here
   int flags;   // 1 first stage of the piece, 2 last, 4 masks needed, 8 and 16: the groups' rows lie token by token
-  int b, group, part, L;
-  int ql, pad0, pad1, pad2;
+  int valid;   // bit j: position t0 + j is in the span and its row is here
+  int t0;      // first position of the stage
+  int b, group, part, L, ql;
 };
 
 struct Smem {
   int code_group, scale_group, stage, pitch;
   unsigned char* stages;
-  Hdr* queue;    // [kQueue]
-  int* entries;  // [kQueue][kTok]
-  Hdr* hdr;      // [stages]
+  unsigned char* queries;  // [warp][nt][4][lane] 16 bytes: each warp's queries as operand B, two k steps of it a word
+  Hdr* hdr;  // [stages]
   uint64_t* full;
   uint64_t* empty;
   volatile int* abort_flag;
@@ -107,22 +103,21 @@ __host__ __device__ __forceinline__ int code_group_bytes(int HG) { return (16 * 
 __host__ __device__ __forceinline__ int stage_bytes(int HG) {
   return (2 * (code_group_bytes(HG) + HG * 16 * kScaleBytes) + 1023) & ~1023;
 }
-__host__ __forceinline__ size_t smem_bytes(int HG, int S) {
-  return 1024 + (size_t)S * stage_bytes(HG) + (kQueue + S) * sizeof(Hdr) + kQueue * kTok * sizeof(int) +
-         2 * S * sizeof(uint64_t) + 16;
+constexpr int kQueryBytes = 2048;  // of a warp's eight columns
+__host__ __forceinline__ size_t smem_bytes(int HG, int S, int CW, int NT) {
+  return 1024 + (size_t)S * (stage_bytes(HG) + sizeof(Hdr) + 2 * sizeof(uint64_t)) + (size_t)CW * NT * kQueryBytes + 16;
 }
 
-__device__ __forceinline__ Smem map_smem(unsigned char* raw, int HG, int S) {
+__device__ __forceinline__ Smem map_smem(unsigned char* raw, int HG, int S, int CW, int NT) {
   Smem s;
   s.code_group = code_group_bytes(HG);
   s.scale_group = HG * 16 * kScaleBytes;
   s.stage = stage_bytes(HG);
   s.pitch = HG * kHeadBytes + 16;
   s.stages = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-  s.queue = reinterpret_cast<Hdr*>(s.stages + (size_t)S * s.stage);
-  s.hdr = s.queue + kQueue;
-  s.entries = reinterpret_cast<int*>(s.hdr + S);
-  s.full = reinterpret_cast<uint64_t*>(s.entries + kQueue * kTok);
+  s.queries = s.stages + (size_t)S * s.stage;
+  s.hdr = reinterpret_cast<Hdr*>(s.queries + CW * NT * kQueryBytes);
+  s.full = reinterpret_cast<uint64_t*>(s.hdr + S);
   s.empty = s.full + S;
   s.abort_flag = reinterpret_cast<volatile int*>(s.empty + S);
   return s;
@@ -139,10 +134,28 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// The same without a sum to begin with.
+__device__ __forceinline__ void mma_f16_new(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+// movmatrix_trans that the compiler may move.
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+// (a & mask) | (b & ~mask)
+template <uint32_t MASK>
+__device__ __forceinline__ uint32_t select_bits(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xb8;" : "=r"(r) : "r"(b), "r"(MASK), "r"(a));
+  return r;
 }
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   uint32_t r;
@@ -205,7 +218,8 @@ __device__ __forceinline__ Request request_of(const Args& a, int b) {
 // This CTA's share of the batch's stages, found by the whole CTA.
 struct Plan {
   long long R0, R1, Sv;  // the share, and where its first request and group begin
-  int active, b, g;
+  int active, b, g, ql;
+  int4 cut;  // the record of that one if its last piece is here and it began before
 };
 
 __device__ void make_plan(const Args& a, Plan* pl, bool* any_bad) {
@@ -222,13 +236,14 @@ __device__ void make_plan(const Args& a, Plan* pl, bool* any_bad) {
   long long total;
   long long at = block_exclusive_scan(mine, &total);
   const long long T = total * a.n_groups, Ne = min((long long)a.num_ctas, T), k = blockIdx.x;
-  if (threadIdx.x == 0) a.merge[k] = make_int4(-1, 0, 0, 0);
+  if (threadIdx.x == 0 && !a.by_request) a.merge[k] = make_int4(-1, 0, 0, 0);
   __syncthreads();
   if (k < Ne) {
     const long long R0 = k * T / Ne, R1 = (k + 1) * T / Ne;
     if (at * a.n_groups <= R0 && R0 < (at + mine) * a.n_groups) {  // the first request is one of this thread's
       for (int b = b0; b < b1; ++b) {
-        const int n = request_of(a, b).n;
+        const Request r = request_of(a, b);
+        const int n = r.n;
         const long long first = at * a.n_groups;
         if (R0 < first + (long long)n * a.n_groups) {
           const int g = (int)((R0 - first) / n);
@@ -239,9 +254,12 @@ __device__ void make_plan(const Args& a, Plan* pl, bool* any_bad) {
           pl->b = b;
           pl->g = g;
           pl->active = 1;
+          pl->ql = r.ql;
+          pl->cut = make_int4(-1, 0, 0, 0);
           if (Sv < R0 && Sv + n <= R1) {  // cut, and its last piece is here
             const long long ka = ((Sv + 1) * Ne + T - 1) / T - 1;  // the CTA of its first piece
-            a.merge[k] = make_int4(b * a.n_groups + g, (int)ka, (int)(ka * T / Ne == Sv ? 2 * ka : 2 * ka + 1), (int)k);
+            pl->cut = make_int4(b * a.n_groups + g, (int)ka, (int)(ka * T / Ne == Sv ? 2 * ka : 2 * ka + 1), (int)k);
+            if (!a.by_request) a.merge[k] = pl->cut;
           }
           break;
         }
@@ -253,140 +271,236 @@ __device__ void make_plan(const Args& a, Plan* pl, bool* any_bad) {
 }
 
 // ---------------------------------------------------------------------------
-// The producer warp: table entries kAhead stages ahead, then the copies.
+// The producer warp. It takes the share's stages 32 at a time, a lane each: every lane finds its stage's request and group
+// (from 32 requests' sizes and their sums), and in a block table whose pages are whole groups also the two slots that its
+// copies start at, all while the 32 stages before are on their way. Issuing such a stage is then one lane's work: two
+// tensor copies and two of scales. Of other tables each lane fetches one position's entry, a stage ahead, and copies that
+// row where the group does not lie together. (A stage at a time with the whole warp took 800 instructions, and set the
+// pace: 55 us for 64 requests.)
 // ---------------------------------------------------------------------------
-__device__ void produce(const Args& a, const Smem& s, const Plan& pl, int lane) {
-  const int HG = a.HG, S = a.stages;
-  const uint32_t row_copy = (uint32_t)(HG * kHeadBytes);
-  long long x = pl.R0, Sv = pl.Sv;  // stream position of the next stage to queue, and of its request and group
-  int b = pl.b, g = pl.g;
-  bool done = !pl.active, fresh = true;
+struct Lane {   // a stage, in one lane's registers
+  Hdr h;
+  int row;      // of the table
+  int e0, e1;   // table entries of its two groups (block tables of whole groups)
+};
+
+// Stages x0 .. x0 + 31 of the stream, lane by lane; (b, g, Sv) is the request and group of x0 or an earlier one, and
+// becomes that of stage x0 + 31 or the last. ``n``: the share's stages from x0 on.
+__device__ __forceinline__ void prepare(const Args& a, const Plan& pl, long long x0, int n, int& b, int& g, long long& Sv,
+                                        bool paged, int shift, int lane, Lane& o) {
+  const int want = min(lane, n - 1);  // lanes past the end repeat the last stage
+  bool found = false;
+  int fb = 0, fg = 0;
+  long long fS = 0;
   Request r;
-  if (!done) r = request_of(a, b);
-  int queued = 0;
-  auto queue_next = [&]() {
-    Hdr* h = s.queue + queued % kQueue;
-    if (!done) {
-      const int i = (int)(x - Sv);
-      const bool sink = i < r.n_sink;
-      const int t0 = (sink ? i : r.lo / kTok + i - r.n_sink) * kTok;
-      const int first = sink ? 0 : r.lo, end = sink ? r.se : r.L;
-      const int t = t0 + lane;
-      const bool in = t >= first && t < end;
-      if (in)
-        cp_async4(&s.entries[queued % kQueue * kTok + lane],
-                  a.T.table + (size_t)r.row * a.T.cols + (a.T.raw ? t : t / a.T.page_size));
-      const bool last_of_request = x + 1 == Sv + r.n, last = last_of_request || x + 1 == pl.R1;
-      const unsigned inside = __ballot_sync(0xffffffffu, in);
-      if (lane == 0) {
-        h->live = 1;
-        h->t0 = t0;
-        h->valid = (int)inside;
-        // every query attends the whole stage: it ends before the first query's position, and lies in the last one's
-        // window or in the first one's sinks
-        const int p0 = r.L - r.ql;
-        const Span sl = attend_span(r.L, a.window, a.sinks), sf = attend_span(p0 + 1, a.window, a.sinks);
-        const bool whole = inside == 0xffffffffu && t0 + kTok - 1 <= p0 && (t0 >= sl.lo || t0 + kTok <= sf.se);
-        h->flags = (fresh ? 1 : 0) | (last ? 2 : 0) | (whole ? 0 : 4);
-        h->b = b;
-        h->group = g;
-        const bool cut = Sv < pl.R0 || Sv + r.n > pl.R1;
-        h->part = cut ? (Sv <= pl.R0 ? 2 * (int)blockIdx.x : 2 * (int)blockIdx.x + 1) : -1;
-        h->L = r.L;
-        h->ql = r.ql;
+  for (;;) {
+    // requests b .. b + 31: their stages over all groups (of b, those from group g on), and the sums before them
+    r = request_of(a, min(b + lane, a.B - 1));
+    long long size = b + lane < a.B ? (long long)r.n * (lane ? a.n_groups : a.n_groups - g) : 0, sum = size;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, sum, d);
+      if (lane >= d) sum += y;
+    }
+    const long long target = x0 + want - Sv;  // from the first one's start
+    int i = 0;
+    for (; i < 32; ++i) {
+      const long long end = __shfl_sync(0xffffffffu, sum, i);
+      if (!found && target < end) {
+        found = true;
+        fb = b + i;
+        fS = Sv + end;  // its end, for now
       }
-      fresh = last;
-      if (++x >= pl.R1) {
-        done = true;
-      } else if (last_of_request) {
-        Sv = x;
-        if (++g == a.n_groups) {
-          g = 0;
-          do r = request_of(a, ++b);  // the share ends within a valid request
-          while (r.n == 0 && b + 1 < a.B);
-        }
-      }
-    } else if (lane == 0) {
-      h->live = 0;
+      if (__all_sync(0xffffffffu, found)) break;
     }
-    cp_async_commit();
-    ++queued;
-  };
-  for (int k = 0; k < kAhead; ++k) queue_next();
-  int k = 0;
-  bool ok = true;
-  for (;; ++k) {
-    queue_next();
-    cp_async_wait<kAhead>();
-    __syncwarp();
-    const Hdr h = s.queue[k % kQueue];
-    const int st = k % S;
-    if (k >= S) {
-      ok = __all_sync(0xffffffffu, mbar_wait_bounded(&s.empty[st], (uint32_t)((k / S - 1) & 1), s.abort_flag, a.err, kWaitNs));
-      if (!ok) break;
+    if (__all_sync(0xffffffffu, found)) break;
+    const long long all = __shfl_sync(0xffffffffu, sum, 31);
+    Sv += all;
+    b += 32;
+    g = 0;
+    if (b >= a.B) break;  // cannot happen within the share
+  }
+  r = request_of(a, fb);
+  const long long x = x0 + want;
+  const int back = (int)((fS - x - 1) / max(r.n, 1));  // groups after this stage's: fS is the end of all
+  fg = a.n_groups - 1 - back;
+  fS -= (long long)(back + 1) * r.n;                   // this group's first stage
+  const int i = (int)(x - fS);
+  const bool sink = i < r.n_sink;
+  const int t0 = (sink ? i : r.lo / kTok + i - r.n_sink) * kTok;
+  const int first = max((sink ? 0 : r.lo) - t0, 0), end = min((sink ? r.se : r.L) - t0, kTok);  // positions t0 + first ..
+  const unsigned inside = !found ? 0u : (end >= 32 ? 0xffffffffu : (1u << end) - 1u) & ~((1u << first) - 1u);
+  // every query attends the whole stage: it ends before the first query's position, and lies in the last one's window or
+  // in the first one's sinks
+  const int p0 = r.L - r.ql;
+  const Span sl = attend_span(r.L, a.window, a.sinks), sf = attend_span(p0 + 1, a.window, a.sinks);
+  const bool whole = inside == 0xffffffffu && t0 + kTok - 1 <= p0 && (t0 >= sl.lo || t0 + kTok <= sf.se);
+  const bool cut = fS < pl.R0 || fS + r.n > pl.R1;
+  o.h.flags = (x == max(fS, pl.R0) ? 1 : 0) | (x + 1 == min(fS + r.n, pl.R1) ? 2 : 0) | (whole ? 0 : 4);
+  o.h.valid = (int)inside;
+  o.h.t0 = t0;
+  o.h.b = fb;
+  o.h.group = fg;
+  o.h.part = cut ? (fS <= pl.R0 ? 2 * (int)blockIdx.x : 2 * (int)blockIdx.x + 1) : -1;
+  o.h.L = r.L;
+  o.h.ql = r.ql;
+  o.row = r.row;
+  if (a.by_request && found && lane < n && x + 1 == fS + r.n)  // the request's last stage: its record is this CTA's to write
+    a.merge[fb * a.n_groups + fg] = fS < pl.R0 ? pl.cut : make_int4(-1, 0, 0, 0);
+  o.e0 = o.e1 = -1;
+  if (paged) {
+    const int32_t* row = a.T.table + (size_t)r.row * a.T.cols;
+    if (inside & 0xffffu) o.e0 = __ldg(row + (shift >= 0 ? t0 >> shift : t0 / a.T.page_size));
+    if (inside >> 16) o.e1 = __ldg(row + (shift >= 0 ? (t0 + 16) >> shift : (t0 + 16) / a.T.page_size));
+  }
+  b = __shfl_sync(0xffffffffu, fb, 31);
+  g = __shfl_sync(0xffffffffu, fg, 31);
+  Sv = __shfl_sync(0xffffffffu, fS, 31);
+}
+
+// A stage's copies by the whole warp, rows that lie together by groups, others one by one; ``e``: the lane's table entry.
+__device__ __forceinline__ void load_rows(const Args& a, const Smem& s, Hdr h, int e, int st, int shift, int lane) {
+  const int HG = a.HG, P = a.T.page_size;
+  const uint32_t row_copy = (uint32_t)(HG * kHeadBytes);
+  const int t = h.t0 + lane, grp = lane >> 4, j = lane & 15;
+  int slot = -1;
+  if (h.valid >> lane & 1) {
+    const bool good = a.T.raw ? (unsigned)e < (unsigned)a.T.num_slots : (unsigned)e < (unsigned)a.T.num_pages;
+    if (good) slot = a.T.raw ? e : e * P + (shift >= 0 ? t & (P - 1) : t % P);
+    else set_error(a.err, KVP_ERR_BAD_INDEX);
+  }
+  const unsigned here = __ballot_sync(0xffffffffu, slot >= 0);
+  const unsigned mine = here >> (16 * grp) & 0xffffu;
+  const int lead = mine ? __ffs(mine) - 1 : 0;
+  const int base = __shfl_sync(0xffffffffu, slot, 16 * grp + lead) - lead;
+  const unsigned off = __ballot_sync(0xffffffffu, slot >= 0 && slot - j != base);
+  const bool together = a.use_map && mine && (base & 15) == 0 && base >= 0 && (off >> (16 * grp) & 0xffffu) == 0;
+  const unsigned tg = __ballot_sync(0xffffffffu, together), lin = __ballot_sync(0xffffffffu, mine && !together);
+  unsigned char* sbuf = s.stages + (size_t)st * s.stage;
+  unsigned char* scb = sbuf + 2 * s.code_group;
+  uint64_t* full = &s.full[st];
+  if (lane == 0) {
+    h.valid = (int)here;
+    h.flags |= (lin & 1 ? 8 : 0) | (lin >> 16 & 1 ? 16 : 0) | (here != 0xffffffffu ? 4 : 0);
+    s.hdr[st] = h;
+    mbar_arrive_expect_tx(full, ((tg & 1) + (tg >> 16 & 1)) * (uint32_t)(HG * 16 * (kHeadBytes + kScaleBytes)) +
+                                    (uint32_t)__popc(here & lin) * row_copy);
+  }
+  __syncwarp();
+  if (together && j == 0) {  // lanes 0 and 16
+    tma_load_4d(sbuf + grp * s.code_group, &a.map, 0, base, h.group * HG, a.layer, full);
+    bulk_g2s(scb + grp * s.scale_group, a.scales + fp4_scale_offset(base, h.group * HG, a.Hkv, kD), (uint32_t)s.scale_group,
+             full);
+  }
+  if (lin) {
+    if ((lin >> lane & 1) && slot >= 0) {
+      bulk_g2s(sbuf + grp * s.code_group + j * s.pitch, a.codes + (size_t)slot * a.row_bytes + (size_t)h.group * row_copy,
+               row_copy, full);
+      const char* src = a.scales + fp4_scale_offset(slot, h.group * HG, a.Hkv, kD);
+      unsigned char* dst = scb + grp * s.scale_group + j * kScaleBytes;
+      for (int hh = 0; hh < HG; ++hh) cp_async16(dst + hh * 16 * kScaleBytes, src + hh * 16 * kScaleBytes);
     }
-    if (!h.live) {
-      if (lane == 0) {
-        s.hdr[st].live = 0;
-        mbar_arrive_n(&s.full[st], 33);
-      }
-      break;
-    }
-    const int t = h.t0 + lane, grp = lane >> 4, j = lane & 15;
-    int slot = -1;
-    if (h.valid >> lane & 1) {
-      const int e = s.entries[k % kQueue * kTok + lane];
-      const bool good = a.T.raw ? (unsigned)e < (unsigned)a.T.num_slots : (unsigned)e < (unsigned)a.T.num_pages;
-      if (good) slot = a.T.raw ? e : e * a.T.page_size + t % a.T.page_size;
-      else set_error(a.err, KVP_ERR_BAD_INDEX);
-    }
-    const unsigned here = __ballot_sync(0xffffffffu, slot >= 0);
-    const unsigned mine = here >> (16 * grp) & 0xffffu;
-    const int lead = mine ? __ffs(mine) - 1 : 0;
-    const int base = __shfl_sync(0xffffffffu, slot, 16 * grp + lead) - lead;
-    const unsigned off = __ballot_sync(0xffffffffu, slot >= 0 && slot - j != base);
-    const bool together = a.use_map && mine && (base & 15) == 0 && base >= 0 && (off >> (16 * grp) & 0xffffu) == 0;
-    const unsigned tg = __ballot_sync(0xffffffffu, together), lin = __ballot_sync(0xffffffffu, mine && !together);
-    const bool t0g = tg & 1, t1g = tg >> 16 & 1, l0 = lin & 1, l1 = lin >> 16 & 1;
-    unsigned char* sbuf = s.stages + (size_t)st * s.stage;
-    unsigned char* scb = sbuf + 2 * s.code_group;
-    if (lane == 0) {
-      Hdr o = h;
-      o.valid = (int)here;
-      o.flags = h.flags | (l0 ? 8 : 0) | (l1 ? 16 : 0) | (here != 0xffffffffu ? 4 : 0);
-      s.hdr[st] = o;
-      const uint32_t tx = (uint32_t)((int)t0g + (int)t1g) * (uint32_t)(HG * 16 * (kHeadBytes + kScaleBytes)) +
-                          (uint32_t)__popc(here & ((l0 ? 0xffffu : 0u) | (l1 ? 0xffff0000u : 0u))) * row_copy;
-      mbar_arrive_expect_tx(&s.full[st], tx);
-    }
-    __syncwarp();
-    if (together && j == 0) {  // lanes 0 and 16
-      tma_load_4d(sbuf + grp * s.code_group, &a.map, 0, base, h.group * HG, a.layer, &s.full[st]);
-      bulk_g2s(scb + grp * s.scale_group, a.scales + fp4_scale_offset(base, h.group * HG, a.Hkv, kD),
-               (uint32_t)s.scale_group, &s.full[st]);
-    }
-    if (l0 || l1) {
-      if ((grp ? l1 : l0) && slot >= 0)
-        bulk_g2s(sbuf + grp * s.code_group + j * s.pitch, a.codes + (size_t)slot * a.row_bytes + (size_t)h.group * row_copy,
-                 row_copy, &s.full[st]);
-      for (int u = lane; u < kTok * HG; u += 32) {  // (token, head): two heads' lines of 16 tokens at a time
-        const int tk = u & 31, hh = u >> 5;
-        const int sl = __shfl_sync(0xffffffffu, slot, tk);
-        if ((tk < 16 ? l0 : l1) && sl >= 0)
-          cp_async16(scb + (tk >> 4) * s.scale_group + (hh * 16 + (tk & 15)) * kScaleBytes,
-                     a.scales + fp4_scale_offset(sl, h.group * HG + hh, a.Hkv, kD));
-      }
-      cp_async_arrive(&s.full[st]);
-    } else if (lane == 0) {
-      mbar_arrive_n(&s.full[st], 32);
+    cp_async_arrive(full);
+  } else if (lane == 0) {
+    mbar_arrive_n(full, 32);
+  }
+}
+
+// The copies of a stage of whole groups, by one lane.
+__device__ __forceinline__ void load_groups(const Args& a, const Smem& s, Lane& o, int st, int shift) {
+  const int HG = a.HG, P = a.T.page_size;
+  const uint32_t codes = (uint32_t)(HG * 16 * kHeadBytes);
+  int base[2] = {-1, -1};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int e = i ? o.e1 : o.e0, t = o.h.t0 + 16 * i;
+    if (!(o.h.valid >> (16 * i) & 0xffff)) continue;
+    if ((unsigned)e < (unsigned)a.T.num_pages) {
+      base[i] = e * P + (shift >= 0 ? t & (P - 1) : t % P);
+    } else {
+      set_error(a.err, KVP_ERR_BAD_INDEX);
+      o.h.valid &= i ? 0xffff : (int)0xffff0000u;
+      o.h.flags |= 4;
     }
   }
-  cp_async_wait<0>();
+  uint64_t* full = &s.full[st];
+  s.hdr[st] = o.h;
+  mbar_arrive_expect_tx(full, ((base[0] >= 0) + (base[1] >= 0)) * (codes + (uint32_t)s.scale_group));
+  unsigned char* sbuf = s.stages + (size_t)st * s.stage;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (base[i] >= 0) {
+      tma_load_4d(sbuf + i * s.code_group, &a.map, 0, base[i], o.h.group * HG, a.layer, full);
+      bulk_g2s(sbuf + 2 * s.code_group + i * s.scale_group, a.scales + fp4_scale_offset(base[i], o.h.group * HG, a.Hkv, kD),
+               (uint32_t)s.scale_group, full);
+    }
+  mbar_arrive_n(full, 32);
+}
+
+__device__ __forceinline__ Hdr from_lane(const Hdr& h, int j) {
+  Hdr o;
+  o.flags = __shfl_sync(0xffffffffu, h.flags, j);
+  o.valid = __shfl_sync(0xffffffffu, h.valid, j);
+  o.t0 = __shfl_sync(0xffffffffu, h.t0, j);
+  o.b = __shfl_sync(0xffffffffu, h.b, j);
+  o.group = __shfl_sync(0xffffffffu, h.group, j);
+  o.part = __shfl_sync(0xffffffffu, h.part, j);
+  o.L = __shfl_sync(0xffffffffu, h.L, j);
+  o.ql = __shfl_sync(0xffffffffu, h.ql, j);
+  return o;
+}
+
+__device__ void produce(const Args& a, const Smem& s, const Plan& pl, int me, int lane) {
+  const int S = a.stages, P = a.T.page_size;
+  const int shift = (P & (P - 1)) == 0 ? __ffs(P) - 1 : -1;
+  const bool paged = a.use_map && !a.T.raw && (P & 15) == 0;
+  if (paged && me) return;
+  const int PW = paged ? 1 : a.PW;  // each has every PW-th stage
+  int b = pl.b, g = pl.g;
+  long long Sv = pl.Sv, x = pl.R0;
+  Lane cur, nxt;
+  prepare(a, pl, x, (int)min(pl.R1 - x, (long long)32), b, g, Sv, paged, shift, lane, cur);
+  bool ok = true;
+  int st = me % S, phase = 1 ^ (me / S & 1), k = me;  // stage k goes to buffer st; a buffer's first wait passes at once
+  int e = 0;
+  auto fetch = [&](const Hdr& h, int row) {  // the lane's table entry of a stage
+    if (!(h.valid >> lane & 1)) return 0;
+    const int t = h.t0 + lane;
+    return __ldg(a.T.table + (size_t)row * a.T.cols + (a.T.raw ? t : shift >= 0 ? t >> shift : t / P));
+  };
+  if (!paged && me < pl.R1 - pl.R0) e = fetch(from_lane(cur.h, me), __shfl_sync(0xffffffffu, cur.row, me));
+  while (ok) {
+    const int n = (int)min(pl.R1 - x, (long long)32);
+    const bool more = pl.R1 - x > 32;
+    if (more) prepare(a, pl, x + 32, (int)min(pl.R1 - x - 32, (long long)32), b, g, Sv, paged, shift, lane, nxt);
+    for (int j = me; j < n && ok; j += PW) {  // PW divides 32
+      if (paged) {
+        if (lane == j) {
+          ok = mbar_wait_bounded(&s.empty[st], (uint32_t)phase, s.abort_flag, a.err, kWaitNs);
+          if (ok) load_groups(a, s, cur, st, shift);
+        }
+        ok = __all_sync(0xffffffffu, ok);
+      } else {
+        const Hdr h = from_lane(cur.h, j);
+        const int mine = e;
+        if (j + PW < n) e = fetch(from_lane(cur.h, j + PW), __shfl_sync(0xffffffffu, cur.row, j + PW));
+        else if (more && me < pl.R1 - x - 32) e = fetch(from_lane(nxt.h, me), __shfl_sync(0xffffffffu, nxt.row, me));
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&s.empty[st], (uint32_t)phase, s.abort_flag, a.err, kWaitNs));
+        if (ok) load_rows(a, s, h, mine, st, shift, lane);
+      }
+      if (!ok) break;
+      k += PW;
+      for (st += PW; st >= S; st -= S) phase ^= 1;
+    }
+    x += 32;
+    if (!more) break;
+    cur = nxt;
+  }
   if (!ok) {  // let the copies land before the CTA ends
     *s.abort_flag = 1;
-    for (int k2 = k - 1; k2 >= 0 && k2 >= k - S; --k2) {
+    for (int k2 = k - PW; k2 >= 0 && k2 >= k - PW - S; k2 -= PW) {
       const uint64_t t_start = global_timer_ns();
-      while (!mbar_try_wait(&s.full[k2 % S], (uint32_t)((k2 / S) & 1)))
+      while (!mbar_try_wait(&s.full[k2 % S], (uint32_t)(k2 / S & 1)))
         if (global_timer_ns() - t_start > 100000000ull) break;
     }
   }
@@ -395,289 +509,406 @@ __device__ void produce(const Args& a, const Smem& s, const Plan& pl, int lane) 
 // ---------------------------------------------------------------------------
 // Consumer warps: one KV head and 8 NT (token, head) columns each.
 // ---------------------------------------------------------------------------
+
+// Whether the query token of column ``col`` attends position t (the stage's masks allow for rows that are not there).
+struct Column {
+  int p, lo, se;
+};
+__device__ __forceinline__ Column column_of(const Args& a, const Hdr* h, int col) {
+  Column q;
+  q.p = h->L - h->ql + min(col, a.C * a.G - 1) / a.G;
+  const Span sp = attend_span(q.p + 1, a.window, a.sinks);
+  q.lo = sp.lo;
+  q.se = sp.se;
+  return q;
+}
+__device__ __forceinline__ bool attends(const Column& q, int t) { return t <= q.p && (t >= q.lo || t < q.se); }
+
+// What a warp keeps from stage to stage.
 template <int NT>
-__device__ void consume(const Args& a, const Smem& s, int w, int lane) {
-  const int G = a.G, HG = a.HG, h = w / a.tiles, col0 = (w % a.tiles) * 8 * NT, C = a.C * G;
-  const int g = lane >> 2, c = lane & 3;
-  const int ktok = g & 1 ? g ^ 4 : g;            // the token of row g; row g + 8: 8 further
-  const int vt0 = 2 * c, vt1 = (2 * c + 1) ^ 4;  // the tokens of k 2 c and 2 c + 1, and 8 further
-  // offsets in a group: rows of 128 bytes, head-major and swizzled (chunk ^ token % 8), or token by token
-  auto swz = [&](int tok, int chunk) { return (uint32_t)((h * 16 + tok) * 128 + ((chunk ^ (tok & 7)) << 4)); };
-  auto linr = [&](int tok, int chunk) { return (uint32_t)(tok * s.pitch + h * kHeadBytes + chunk * 16); };
-  const int vchunk = 4 + (g >> 1), vin = (g & 1) * 8;
-  const uint32_t ks = swz(ktok, c), kl = linr(ktok, c), v0s = swz(vt0, vchunk) + vin, v0l = linr(vt0, vchunk) + vin,
-                 v1s = swz(vt1, vchunk) + vin, v1l = linr(vt1, vchunk) + vin;
-  const uint32_t ksc = (uint32_t)((h * 16 + ktok) * kScaleBytes + 2 * c),
-                 v0sc = (uint32_t)((h * 16 + vt0) * kScaleBytes + 8 + g), v1sc = (uint32_t)((h * 16 + vt1) * kScaleBytes + 8 + g);
-  const uint32_t stages = smem_u32(s.stages);
+struct State {
+  float o[8][NT][4];                  // O^T
+  float m[NT][2], l[NT][2], f[NT][2]; // of its columns: running maximum (log2), this lane's part of the sum, score's factor
+};
 
-  uint32_t qf[8][NT][2];
-  float o[8][NT][4], m[NT][2], l[NT][2], f[NT][2];
-  int qp[NT][2];  // positions of the columns' tokens
+// Where a lane's K and V of the first tile lie: rows of 128 bytes, head-major and swizzled (chunk ^ token % 8), or token by
+// token. A tile's tokens 8 to 15 lie ``eight`` further.
+struct Place {
+  uint32_t k, v0, v1, eight;
+};
+
+// What a lane knows of its part in every stage.
+struct Part {
+  Place swz, lin;
+  uint32_t ksc, vsc;       // its scales in a group's
+  uint32_t queries;        // its operand words
+  int col, ktok, vt0, vt1; // its first column, its row's token, its tokens of k 2 c and 2 c + 1
+};
+
+// A stage that is being worked on.
+struct Stage {
+  const Hdr* hd;
+  uint32_t flags, valid, sb;
+  int t0;
+};
+
+// The phases of a stage. LIN: 0 both groups swizzled, 1 both token by token, 2 as the flags say; MASKED: the flags' masks
+// count.
+template <int NT, int LIN>
+__device__ __forceinline__ void scores(const Smem& s, const Stage& g, const Part& p, float (&x)[2][NT][4]) {
+  // S^T = K Q^T, two tiles of 16 tokens
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    m[nt][0] = m[nt][1] = -INFINITY;
-    l[nt][0] = l[nt][1] = f[nt][0] = f[nt][1] = 0.f;
-    qp[nt][0] = qp[nt][1] = 0;
+  for (int tile = 0; tile < 2; ++tile) {
+    const bool by_row = LIN == 1 || (LIN == 2 && (g.flags & (8 << tile)));
+    const uint32_t ab = g.sb + tile * s.code_group + (by_row ? p.lin.k : p.swz.k);
+    const uint32_t scb = g.sb + 2 * s.code_group + tile * s.scale_group + p.ksc;
+    const uint4 r0 = lds16(ab), r1 = lds16(ab + (by_row ? p.lin.eight : 1024));
+    const uint32_t s0 = e4m3x2_to_half(lds_u16(scb)), s1 = e4m3x2_to_half(lds_u16(scb + 8 * kScaleBytes));
+    const uint32_t w0[4] = {r0.x, r0.y, r0.z, r0.w}, w1[4] = {r1.x, r1.y, r1.z, r1.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t d0 = __byte_perm(s0, s0, i < 2 ? 0x1010 : 0x3232), d1 = __byte_perm(s1, s1, i < 2 ? 0x1010 : 0x3232);
+      uint32_t h0[4], h1[4];
+      e2m1x8_to_half(w0[i], h0);
+      e2m1x8_to_half(w1[i], h1);
+      // read again for every tile: sixteen registers less, and no spills at 96
+      uint4 q[NT];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) q[nt] = lds16(p.queries + nt * kQueryBytes + i * 512);
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const uint32_t af[4] = {hmul2(h0[2 * y], d0), hmul2(h1[2 * y], d1), hmul2(h0[2 * y + 1], d0), hmul2(h1[2 * y + 1], d1)};
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          if (i == 0 && y == 0) mma_f16_new(x[tile][nt], af, q[nt].x, q[nt].y);
+          else mma_f16(x[tile][nt], af, y ? q[nt].z : q[nt].x, y ? q[nt].w : q[nt].y);
+        }
+      }
+    }
   }
+}
 
-  for (int it = 0, st = 0, phase = 0;; ++it) {
-    if (!__all_sync(0xffffffffu, mbar_wait_bounded(&s.full[st], (uint32_t)phase, s.abort_flag, a.err, kWaitNs))) return;
-    const volatile Hdr* hd = &s.hdr[st];
-    if (!hd->live) return;
-    const int flags = hd->flags;
-    const uint32_t sb = stages + (uint32_t)st * (uint32_t)s.stage;
-
-    if (flags & 1) {  // a new piece: its queries in fp16, scaled by powers of two; state
-      const int b = hd->b, ql = hd->ql, L = hd->L, grp = hd->group;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const int col = col0 + nt * 8 + g, cj = col / G;
-        uint4 x[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (col < C && cj < ql) {
-          const uint4* src = reinterpret_cast<const uint4*>(
-              a.q + (((size_t)b * a.C + cj) * a.Hq + (size_t)(grp * HG + h) * G + col % G) * kD + 32 * c);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) x[i] = __ldg(src + i);
-        }
-        uint32_t mx = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          for (const uint32_t v : {x[i].x, x[i].y, x[i].z, x[i].w}) mx = max(mx, max(v << 16 & 0x7fff0000u, v & 0x7fff0000u));
-        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        // 2^e <= the largest < 2^(e + 1); zeros and subnormal rows: the smallest normal exponent; not finite: as it is
-        const int e = mx >= kInfBits ? 0 : max((int)(mx >> 23), 1) - 127;
-        const float down = e == 127 ? 0x1p-127f : __uint_as_float((uint32_t)(127 - e) << 23);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-          for (int y = 0; y < 4; ++y) qf[2 * i + (y >> 1)][nt][y & 1] = pack_half(bf16_lo(v[y]) * down, bf16_hi(v[y]) * down);
-        }
-#pragma unroll
-        for (int x2 = 0; x2 < 2; ++x2) {
-          const int ec = __shfl_sync(0xffffffffu, e, (2 * c + x2) * 4);
-          const float up = ec == -126 ? 0x1p-126f : __uint_as_float((uint32_t)(127 + ec) << 23);
-          f[nt][x2] = fminf(fmaxf(a.scale_log2 * up, -3.0e38f), 3.0e38f);
-          qp[nt][x2] = L - ql + min(col0 + nt * 8 + 2 * c + x2, C - 1) / G;
-          m[nt][x2] = -INFINITY;
-          l[nt][x2] = 0.f;
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.f;
-      }
-    }
-
-    // S^T = K Q^T, two tiles of 16 tokens
-    float x[2][NT][4];
-#pragma unroll
-    for (int tile = 0; tile < 2; ++tile) {
-      const bool lin = flags & (8 << tile);
-      const uint32_t cb = sb + tile * s.code_group, ab = cb + (lin ? kl : ks);
-      const uint32_t scb = sb + 2 * s.code_group + tile * s.scale_group + ksc;
-      const uint4 r0 = lds16(ab), r1 = lds16(ab + (lin ? 8 * s.pitch : 1024));
-      const uint32_t s0 = e4m3x2_to_half(lds_u16(scb)), s1 = e4m3x2_to_half(lds_u16(scb + 8 * kScaleBytes));
-      const uint32_t w0[4] = {r0.x, r0.y, r0.z, r0.w}, w1[4] = {r1.x, r1.y, r1.z, r1.w};
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) x[tile][nt][0] = x[tile][nt][1] = x[tile][nt][2] = x[tile][nt][3] = 0.f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t d0 = __byte_perm(s0, s0, i < 2 ? 0x1010 : 0x3232), d1 = __byte_perm(s1, s1, i < 2 ? 0x1010 : 0x3232);
-        uint32_t h0[4], h1[4];
-        e2m1x8_to_half(w0[i], h0);
-        e2m1x8_to_half(w1[i], h1);
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          const uint32_t af[4] = {hmul2(h0[2 * y], d0), hmul2(h1[2 * y], d1), hmul2(h0[2 * y + 1], d0), hmul2(h1[2 * y + 1], d1)};
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma_f16(x[tile][nt], af, qf[2 * i + y][nt][0], qf[2 * i + y][nt][1]);
-        }
-      }
-    }
-
-    // softmax over the 32 tokens: rows g and g + 8 of each tile
-    const unsigned valid = (unsigned)hd->valid;
-    const int t0 = hd->t0;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-      for (int tile = 0; tile < 2; ++tile)
-#pragma unroll
-        for (int y = 0; y < 4; ++y) x[tile][nt][y] *= f[nt][y & 1];
-      if (flags & 4) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const Span sp = attend_span(qp[nt][e] + 1, a.window, a.sinks);
-#pragma unroll
-          for (int tile = 0; tile < 2; ++tile)
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const int jt = tile * 16 + y * 8 + ktok, t = t0 + jt;
-              const bool in = (valid >> jt & 1) && t <= qp[nt][e] && (t >= sp.lo || t < sp.se);
-              if (!in) x[tile][nt][2 * y + e] = -INFINITY;
-            }
-        }
-      }
-    }
-    float mx[NT][2];
-    bool grow = false;
+template <int NT, bool MASKED>
+__device__ __forceinline__ void weights(const Args& a, const Stage& g, const Part& p, float (&x)[2][NT][4],
+                                        uint32_t (&pb)[2][NT][2], State<NT>& z) {
+  // softmax over the 32 tokens: rows g and g + 8 of each tile
+  if (MASKED) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float v = fmaxf(fmaxf(x[0][nt][e], x[0][nt][2 + e]), fmaxf(x[1][nt][e], x[1][nt][2 + e]));
+        const Column q = column_of(a, g.hd, p.col + nt * 8 + e);
 #pragma unroll
-        for (int sh = 4; sh < 32; sh <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, sh));
-        mx[nt][e] = v;
-        grow |= v > m[nt][e] + 8.f;
-      }
-    if (__any_sync(0xffffffffu, grow)) {
+        for (int tile = 0; tile < 2; ++tile)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float mn = fmaxf(m[nt][e], mx[nt][e]);
-          const float al = m[nt][e] == -INFINITY ? 0.f : ex2(m[nt][e] - mn);
-          m[nt][e] = mn;
-          l[nt][e] *= al;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            o[i][nt][e] *= al;
-            o[i][nt][2 + e] *= al;
+          for (int y = 0; y < 2; ++y) {
+            const int jt = tile * 16 + y * 8 + p.ktok;
+            if (!((g.valid >> jt & 1) && attends(q, g.t0 + jt))) x[tile][nt][2 * y + e] = -INFINITY;
           }
-        }
-    }
-    uint32_t pb[2][NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
-#pragma unroll
-      for (int tile = 0; tile < 2; ++tile) {
-        const float p0 = ex2(x[tile][nt][0] - m0), p1 = ex2(x[tile][nt][1] - m1), p2 = ex2(x[tile][nt][2] - m0),
-                    p3 = ex2(x[tile][nt][3] - m1);
-        l[nt][0] += p0 + p2;
-        l[nt][1] += p1 + p3;
-        pb[tile][nt][0] = movmatrix_trans(pack_half(p0, p1));
-        pb[tile][nt][1] = movmatrix_trans(pack_half(p2, p3));
       }
+  }
+  float mx[NT][2];
+  bool grow = false;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float v = fmaxf(fmaxf(x[0][nt][e], x[0][nt][2 + e]), fmaxf(x[1][nt][e], x[1][nt][2 + e]));
+#pragma unroll
+      for (int sh = 4; sh < 32; sh <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, sh));
+      mx[nt][e] = fminf(__fmul_rn(v, z.f[nt][e]), 3.0e38f);  // finite: a product beyond it gives an infinite weight, and a NaN
+      grow |= mx[nt][e] > z.m[nt][e] + 8.f;
     }
-
-    // O^T += V^T P^T
+  if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float mn = fmaxf(z.m[nt][e], mx[nt][e]);
+        const float al = z.m[nt][e] == -INFINITY ? 0.f : ex2(z.m[nt][e] - mn);
+        z.m[nt][e] = mn;
+        z.l[nt][e] *= al;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          z.o[i][nt][e] *= al;
+          z.o[i][nt][2 + e] *= al;
+        }
+      }
+  }
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    // the product rounded before the difference, as in the maximum: one rounding of both would leave 2^-24 of a score,
+    // more than all of an exponent where scores are large
+    const float m0 = fmaxf(z.m[nt][0], -3.0e38f), m1 = fmaxf(z.m[nt][1], -3.0e38f);  // nothing attended: 2^-inf, not NaN
 #pragma unroll
     for (int tile = 0; tile < 2; ++tile) {
-      const bool lin = flags & (8 << tile);
-      const uint32_t cb = sb + tile * s.code_group, eight = lin ? 8 * s.pitch : 1024;
-      const uint32_t a0 = cb + (lin ? v0l : v0s), a1 = cb + (lin ? v1l : v1s);
-      const uint32_t scb = sb + 2 * s.code_group + tile * s.scale_group;
-      const uint2 r[4] = {lds8(a0), lds8(a1), lds8(a0 + eight), lds8(a1 + eight)};
-      uint32_t sc[4] = {lds_u8(scb + v0sc), lds_u8(scb + v1sc), lds_u8(scb + v0sc + 8 * kScaleBytes),
-                        lds_u8(scb + v1sc + 8 * kScaleBytes)};
-      if (flags & 4) {  // rows that are not there count zero times
-        const unsigned vm = valid >> (16 * tile);
-        if (!(vm >> vt0 & 1)) sc[0] = 0;
-        if (!(vm >> vt1 & 1)) sc[1] = 0;
-        if (!(vm >> (vt0 + 8) & 1)) sc[2] = 0;
-        if (!(vm >> (vt1 + 8) & 1)) sc[3] = 0;
-        const bool nan = sc[0] == kFp4NanScale || sc[1] == kFp4NanScale || sc[2] == kFp4NanScale || sc[3] == kFp4NanScale;
-        if (__any_sync(0xffffffffu, nan)) {
-          // the tokens whose block g is NaN, for the columns that attend them; their scale is zero from here on
-          uint32_t who = 0;
+      const float p0 = ex2(__fmul_rn(x[tile][nt][0], z.f[nt][0]) - m0), p1 = ex2(__fmul_rn(x[tile][nt][1], z.f[nt][1]) - m1),
+                  p2 = ex2(__fmul_rn(x[tile][nt][2], z.f[nt][0]) - m0), p3 = ex2(__fmul_rn(x[tile][nt][3], z.f[nt][1]) - m1);
+      z.l[nt][0] += p0 + p2;
+      z.l[nt][1] += p1 + p3;
+      pb[tile][nt][0] = transposed(pack_half(p0, p1));
+      pb[tile][nt][1] = transposed(pack_half(p2, p3));
+    }
+  }
+}
+
+template <int NT, int LIN, bool MASKED>
+__device__ __forceinline__ void values(const Args& a, const Smem& s, const Stage& g, const Part& p,
+                                       const uint32_t (&pb)[2][NT][2], State<NT>& z) {
+  // O^T += V^T P^T. Codes of two tokens are put side by side in a byte, so that a conversion gives the pair that a fragment
+  // holds.
 #pragma unroll
-          for (int y = 0; y < 4; ++y)
-            if (sc[y] == kFp4NanScale) {
-              who |= 1u << ((y & 1 ? vt1 : vt0) + (y & 2 ? 8 : 0));
-              sc[y] = 0;
-            }
-          who |= __shfl_xor_sync(0xffffffffu, who, 1);
-          who |= __shfl_xor_sync(0xffffffffu, who, 2);
+  for (int tile = 0; tile < 2; ++tile) {
+    const bool by_row = LIN == 1 || (LIN == 2 && (g.flags & (8 << tile)));
+    const uint32_t cb = g.sb + tile * s.code_group, eight = by_row ? p.lin.eight : 1024;
+    const uint32_t a0 = cb + (by_row ? p.lin.v0 : p.swz.v0), a1 = cb + (by_row ? p.lin.v1 : p.swz.v1);
+    const uint32_t scb = g.sb + 2 * s.code_group + tile * s.scale_group + p.vsc, one = (uint32_t)((p.vt1 - p.vt0) * kScaleBytes);
+    const uint2 r[4] = {lds8(a0), lds8(a1), lds8(a0 + eight), lds8(a1 + eight)};
+    uint32_t sc0 = lds_u8(scb) + 256u * lds_u8(scb + one),
+             sc1 = lds_u8(scb + 8 * kScaleBytes) + 256u * lds_u8(scb + one + 8 * kScaleBytes);
+    if (MASKED) {  // rows that are not there count zero times
+      const unsigned vm = g.valid >> (16 * tile);
+      if (!(vm >> p.vt0 & 1)) sc0 &= 0xff00u;
+      if (!(vm >> p.vt1 & 1)) sc0 &= 0xffu;
+      if (!(vm >> (p.vt0 + 8) & 1)) sc1 &= 0xff00u;
+      if (!(vm >> (p.vt1 + 8) & 1)) sc1 &= 0xffu;
+      const uint32_t two = sc0 | sc1 << 16;
+      uint32_t who = 0;  // tokens whose block g is NaN; their scale is zero from here on
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const Span sp = attend_span(qp[nt][e] + 1, a.window, a.sinks);
-              bool hit = false;
-              for (int jt = 0; jt < 16; ++jt) {
-                const int t = t0 + 16 * tile + jt;
-                hit |= (who >> jt & 1) && t <= qp[nt][e] && (t >= sp.lo || t < sp.se);
-              }
-              if (hit)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) o[i][nt][e] = o[i][nt][2 + e] = __int_as_float(0x7fffffff);
-            }
+      for (int y = 0; y < 4; ++y)
+        if ((two >> (8 * y) & 0xff) == kFp4NanScale) {
+          who |= 1u << ((y & 1 ? p.vt1 : p.vt0) + (y & 2 ? 8 : 0));
+          if (y < 2) sc0 &= y ? 0xffu : 0xff00u;
+          else sc1 &= y & 1 ? 0xffu : 0xff00u;
         }
-      }
-      uint32_t d[4];
+      if (__any_sync(0xffffffffu, who != 0)) {
+        who |= __shfl_xor_sync(0xffffffffu, who, 1);
+        who |= __shfl_xor_sync(0xffffffffu, who, 2);
 #pragma unroll
-      for (int y = 0; y < 4; ++y) d[y] = e4m3x2_to_half(sc[y] * 0x101u);
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        uint32_t hv[4][4];
+          for (int e = 0; e < 2; ++e) {
+            const Column q = column_of(a, g.hd, p.col + nt * 8 + e);
+            bool hit = false;
+            for (int jt = 0; jt < 16; ++jt) hit |= (who >> jt & 1) && attends(q, g.t0 + 16 * tile + jt);
+            if (hit)
 #pragma unroll
-        for (int y = 0; y < 4; ++y) e2m1x8_to_half(i ? r[y].y : r[y].x, hv[y]);
-#pragma unroll
-        for (int z = 0; z < 4; ++z) {
-          const uint32_t y0 = hmul2(hv[0][z], d[0]), y1 = hmul2(hv[1][z], d[1]), y2 = hmul2(hv[2][z], d[2]),
-                         y3 = hmul2(hv[3][z], d[3]);
-          const uint32_t af[4] = {__byte_perm(y0, y1, 0x5410), __byte_perm(y0, y1, 0x7632), __byte_perm(y2, y3, 0x5410),
-                                  __byte_perm(y2, y3, 0x7632)};
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma_f16(o[4 * i + z][nt], af, pb[tile][nt][0], pb[tile][nt][1]);
-        }
+              for (int i = 0; i < 8; ++i) z.o[i][nt][e] = z.o[i][nt][2 + e] = __int_as_float(0x7fffffff);
+          }
       }
     }
-    const int b = hd->b, grp = hd->group, part = hd->part, ql = hd->ql;
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&s.empty[st]);
+    const uint32_t d0 = e4m3x2_to_half(sc0), d1 = e4m3x2_to_half(sc1);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t y0 = i ? r[0].y : r[0].x, y1 = i ? r[1].y : r[1].x, y2 = i ? r[2].y : r[2].x, y3 = i ? r[3].y : r[3].x;
+      constexpr uint32_t kLow = 0x0f0f0f0fu;
+      uint32_t e0[4], o0[4], e1[4], o1[4];  // even and odd entries of tokens 2 c, 2 c + 1 and of 2 c + 8, 2 c + 9
+      e2m1x8_to_half(select_bits<kLow>(y0, y1 << 4), e0);
+      e2m1x8_to_half(select_bits<kLow>(y0 >> 4, y1), o0);
+      e2m1x8_to_half(select_bits<kLow>(y2, y3 << 4), e1);
+      e2m1x8_to_half(select_bits<kLow>(y2 >> 4, y3), o1);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const uint32_t af[4] = {hmul2(e0[u], d0), hmul2(o0[u], d0), hmul2(e1[u], d1), hmul2(o1[u], d1)};
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma_f16(z.o[4 * i + u][nt], af, pb[tile][nt][0], pb[tile][nt][1]);
+      }
+    }
+  }
+}
+
+// A new piece: its queries in fp16, scaled by powers of two; nothing attended yet.
+template <int NT>
+__device__ __forceinline__ void begin(const Args& a, int b, int grp, int ql, unsigned char* queries, int h, int col0, int lane,
+                                      State<NT>& z) {
+  const int g = lane >> 2, c = lane & 3, C = a.C * a.G;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int col = col0 + nt * 8 + g, cj = col / a.G;
+    uint4 x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (col < C && cj < ql) {
+      const uint4* src = reinterpret_cast<const uint4*>(
+          a.q + (((size_t)b * a.C + cj) * a.Hq + (size_t)(grp * a.HG + h) * a.G + col % a.G) * kD + 32 * c);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = __ldg(src + i);
+    }
+    uint32_t mx = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      for (const uint32_t v : {x[i].x, x[i].y, x[i].z, x[i].w}) mx = max(mx, max(v << 16 & 0x7fff0000u, v & 0x7fff0000u));
+    mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+    mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+    // 2^e <= the largest < 2^(e + 1); zeros and subnormal rows: the smallest normal exponent; not finite: as it is
+    const int e = mx >= kInfBits ? 0 : max((int)(mx >> 23), 1) - 127;
+    // the sign of the scale goes to the queries: f is positive, and the largest score has the largest product
+    const float down = (e == 127 ? 0x1p-127f : __uint_as_float((uint32_t)(127 - e) << 23)) * (a.scale_log2 < 0.f ? -1.f : 1.f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+      uint32_t y[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) y[u] = pack_half(bf16_lo(v[u]) * down, bf16_hi(v[u]) * down);
+      reinterpret_cast<uint4*>(queries + nt * kQueryBytes)[i * 32 + lane] = make_uint4(y[0], y[1], y[2], y[3]);  // its own lane's
+    }
+#pragma unroll
+    for (int x2 = 0; x2 < 2; ++x2) {
+      const int ec = __shfl_sync(0xffffffffu, e, (2 * c + x2) * 4);
+      const float up = ec == -126 ? 0x1p-126f : __uint_as_float((uint32_t)(127 + ec) << 23);
+      // not zero, as masked products are -inf, and finite
+      z.f[nt][x2] = fminf(fmaxf(fabsf(a.scale_log2) * up, 1e-37f), 3.0e38f);
+      z.m[nt][x2] = -INFINITY;
+      z.l[nt][x2] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z.o[i][nt][0] = z.o[i][nt][1] = z.o[i][nt][2] = z.o[i][nt][3] = 0.f;
+  }
+}
+
+// The piece's end: entries 16 g .. 16 g + 15 of columns 2 c and 2 c + 1, the result or a partial one.
+template <int NT>
+__device__ __forceinline__ void finish(const Args& a, const Hdr* hd, int h, int col0, int lane, const State<NT>& z) {
+  const int g = lane >> 2, c = lane & 3, C = a.C * a.G, part = hd->part, ql = hd->ql;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float ls = z.l[nt][e];
+#pragma unroll
+      for (int sh = 4; sh < 32; sh <<= 1) ls += __shfl_xor_sync(0xffffffffu, ls, sh);
+      const int col = col0 + nt * 8 + 2 * c + e, cj = col / a.G;
+      if (col >= C || cj >= ql) continue;
+      float v[16];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        v[2 * i] = z.o[i][nt][e];
+        v[2 * i + 1] = z.o[i][nt][2 + e];
+      }
+      if (part < 0) {
+        const float inv = ls == 0.f ? 0.f : a.gv / ls;
+        uint4* dst = reinterpret_cast<uint4*>(
+            a.out + (((size_t)hd->b * a.C + cj) * a.Hq + (size_t)(hd->group * a.HG + h) * a.G + col % a.G) * kD + 16 * g);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          dst[i] = make_uint4(pack_bf16(v[8 * i] * inv, v[8 * i + 1] * inv), pack_bf16(v[8 * i + 2] * inv, v[8 * i + 3] * inv),
+                              pack_bf16(v[8 * i + 4] * inv, v[8 * i + 5] * inv),
+                              pack_bf16(v[8 * i + 6] * inv, v[8 * i + 7] * inv));
+      } else {
+        const size_t at = (size_t)part * a.HG * C + (size_t)h * C + col;
+        float4* dst = reinterpret_cast<float4*>(a.part_o + at * kD + 16 * g);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        if (g == 0) *reinterpret_cast<float2*>(a.part_ml + at * 2) = make_float2(z.m[nt][e], ls);
+      }
+    }
+}
+
+template <int NT>
+__device__ void consume(const Args& a, const Smem& s, const Plan& pl, int w, int lane) {
+  const int h = w / a.tiles, col0 = (w % a.tiles) * 8 * NT;
+  const int g = lane >> 2, c = lane & 3;
+  const int vchunk = 4 + (g >> 1), vin = (g & 1) * 8;
+  auto swz = [&](int tok, int chunk) { return (uint32_t)((h * 16 + tok) * 128 + ((chunk ^ (tok & 7)) << 4)); };
+  auto row = [&](int tok, int chunk) { return (uint32_t)(tok * s.pitch + h * kHeadBytes + chunk * 16); };
+  unsigned char* queries = s.queries + (size_t)w * NT * kQueryBytes;
+  Part p;
+  p.col = col0 + 2 * c;
+  p.ktok = g & 1 ? g ^ 4 : g;     // the token of row g; row g + 8: 8 further
+  p.vt0 = 2 * c;                  // the tokens of k 2 c and 2 c + 1, and 8 further
+  p.vt1 = (2 * c + 1) ^ 4;
+  p.swz = {swz(p.ktok, c), swz(p.vt0, vchunk) + vin, swz(p.vt1, vchunk) + vin, 1024u};
+  p.lin = {row(p.ktok, c), row(p.vt0, vchunk) + vin, row(p.vt1, vchunk) + vin, 8u * s.pitch};
+  p.ksc = (uint32_t)((h * 16 + p.ktok) * kScaleBytes + 2 * c);
+  p.vsc = (uint32_t)((h * 16 + p.vt0) * kScaleBytes + 8 + g);
+  p.queries = smem_u32(queries) + 16 * lane;
+  const uint32_t stages = smem_u32(s.stages);
+  State<NT> z;
+  begin<NT>(a, pl.b, pl.g, pl.ql, queries, h, col0, lane, z);  // the first piece's, while its rows are on their way
+
+  int st = 0, phase = 0;  // the buffer of the next stage to wait for, and that wait's parity
+  auto next = [&](Stage& o) {
+    if (!__all_sync(0xffffffffu, mbar_wait_bounded(&s.full[st], (uint32_t)phase, s.abort_flag, a.err, kWaitNs))) return false;
+    o.hd = &s.hdr[st];
+    const uint4 head = lds16(smem_u32(o.hd));  // flags, valid, t0, request
+    o.flags = head.x;
+    o.valid = head.y;
+    o.t0 = (int)head.z;
+    o.sb = stages + (uint32_t)st * (uint32_t)s.stage;
     if (++st == a.stages) {
       st = 0;
       phase ^= 1;
     }
-
-    if (flags & 2) {  // the piece's end: entries 16 g .. 16 g + 15 of columns 2 c and 2 c + 1
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float ls = l[nt][e];
-#pragma unroll
-          for (int sh = 4; sh < 32; sh <<= 1) ls += __shfl_xor_sync(0xffffffffu, ls, sh);
-          const int col = col0 + nt * 8 + 2 * c + e, cj = col / G;
-          if (col >= C || cj >= ql) continue;
-          float v[16];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            v[2 * i] = o[i][nt][e];
-            v[2 * i + 1] = o[i][nt][2 + e];
-          }
-          if (part < 0) {
-            const float inv = ls == 0.f ? 0.f : a.gv / ls;
-            uint4* dst = reinterpret_cast<uint4*>(
-                a.out + (((size_t)b * a.C + cj) * a.Hq + (size_t)(grp * HG + h) * G + col % G) * kD + 16 * g);
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-              dst[i] = make_uint4(pack_bf16(v[8 * i] * inv, v[8 * i + 1] * inv), pack_bf16(v[8 * i + 2] * inv, v[8 * i + 3] * inv),
-                                  pack_bf16(v[8 * i + 4] * inv, v[8 * i + 5] * inv),
-                                  pack_bf16(v[8 * i + 6] * inv, v[8 * i + 7] * inv));
-          } else {
-            const size_t at = (size_t)part * HG * C + (size_t)h * C + col;
-            float4* dst = reinterpret_cast<float4*>(a.part_o + at * kD + 16 * g);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-            if (g == 0) *reinterpret_cast<float2*>(a.part_ml + at * 2) = make_float2(m[nt][e], ls);
-          }
-        }
+    return true;
+  };
+  auto release = [&](const Stage& o) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&s.empty[(int)(o.hd - s.hdr)]);
+  };
+  long long left = pl.R1 - pl.R0;
+  Stage cur;
+  if (!next(cur)) return;
+  bool fresh = false;
+  for (;;) {
+    // plain stages of a piece, all swizzled or all token by token: the next one's scores beside this one's values, two
+    // streams of instructions that wait for each other only through the weights
+    float x[2][NT][4];
+    uint32_t pb[2][NT][2];
+    if (fresh && (cur.flags & 1)) begin<NT>(a, cur.hd->b, cur.hd->group, cur.hd->ql, queries, h, col0, lane, z);
+    fresh = true;
+    const uint32_t kind = cur.flags & 28;
+    Stage ahead;
+    if (kind == 0) {
+      scores<NT, 0>(s, cur, p, x);
+      for (;;) {
+        weights<NT, false>(a, cur, p, x, pb, z);
+        if (cur.flags & 2) break;
+        if (!next(ahead)) return;
+        if (ahead.flags & 28) break;
+        scores<NT, 0>(s, ahead, p, x);
+        values<NT, 0, false>(a, s, cur, p, pb, z);
+        release(cur);
+        cur = ahead;
+        --left;
+      }
+      values<NT, 0, false>(a, s, cur, p, pb, z);
+    } else if (kind == 24) {
+      scores<NT, 1>(s, cur, p, x);
+      for (;;) {
+        weights<NT, false>(a, cur, p, x, pb, z);
+        if (cur.flags & 2) break;
+        if (!next(ahead)) return;
+        if ((ahead.flags & 28) != 24) break;
+        scores<NT, 1>(s, ahead, p, x);
+        values<NT, 1, false>(a, s, cur, p, pb, z);
+        release(cur);
+        cur = ahead;
+        --left;
+      }
+      values<NT, 1, false>(a, s, cur, p, pb, z);
+    } else {
+      scores<NT, 2>(s, cur, p, x);
+      weights<NT, true>(a, cur, p, x, pb, z);
+      values<NT, 2, true>(a, s, cur, p, pb, z);
+      if (!(cur.flags & 2) && !next(ahead)) return;
+    }
+    const bool last = cur.flags & 2;
+    if (last) finish<NT>(a, cur.hd, h, col0, lane, z);
+    release(cur);
+    if (--left == 0) return;
+    if (last) {
+      if (!next(cur)) return;
+    } else {
+      cur = ahead;
     }
   }
 }
 
 template <int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fp4_decode_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kThreads, 1) fp4_decode_kernel(const __grid_constant__ Args a) {
   extern __shared__ __align__(128) unsigned char raw[];
   __shared__ Plan pl;
-  const Smem s = map_smem(raw, a.HG, a.stages);
+  const Smem s = map_smem(raw, a.HG, a.stages, a.CW, NT);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < a.stages; ++i) {
@@ -695,54 +926,78 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) fp4_decode_kernel(c
     for (int b = blockIdx.x; b < a.B; b += a.num_ctas) {
       if (request_of(a, b).n) continue;
       if (threadIdx.x == 0) set_error(a.err, KVP_ERR_BAD_INDEX);
+      if (a.by_request)
+        for (int i = threadIdx.x; i < a.n_groups; i += blockDim.x) a.merge[b * a.n_groups + i] = make_int4(-1, 0, 0, 0);
       uint4* o = reinterpret_cast<uint4*>(a.out + (size_t)b * a.C * a.Hq * kD);
       for (int i = threadIdx.x; i < a.C * a.Hq * (kD / 8); i += blockDim.x) o[i] = make_uint4(0u, 0u, 0u, 0u);
     }
   }
   if (!pl.active) return;
-  if (warp == a.CW) produce(a, s, pl, lane);
-  else consume<NT>(a, s, warp, lane);
+  if (warp >= a.CW) produce(a, s, pl, warp - a.CW, lane);
+  else consume<NT>(a, s, pl, warp, lane);
 }
 
-// Joins the pieces of the request that CTA blockIdx.x recorded, in CTA order: one warp a column.
-__global__ void __launch_bounds__(128) fp4_combine_kernel(const __grid_constant__ Args a) {
+// Joins the pieces of the request that CTA blockIdx.x recorded, in CTA order: four warps a column, a quarter of the
+// pieces each (in order, eight loads on their way at a time), then the quarters in order.
+constexpr int kJoinColumns = 4;  // columns a block of 16 warps
+__global__ void __launch_bounds__(128 * kJoinColumns) fp4_combine_kernel(const __grid_constant__ Args a) {
+  __shared__ float4 sum[kJoinColumns][4][32];
+  __shared__ float weight[kJoinColumns][4];
   griddep_wait();
   const int4 mg = a.merge[blockIdx.x];
   if (mg.x < 0) return;
   const int b = mg.x / a.n_groups, grp = mg.x % a.n_groups, C = a.C * a.G, lane = threadIdx.x & 31;
-  const int ql = a.q_lens ? __ldg(a.q_lens + b) : a.C;
-  for (int u = blockIdx.y * 4 + (threadIdx.x >> 5); u < a.HG * C; u += 4 * gridDim.y) {
-    const int h = u / C, col = u % C, cj = col / a.G;
-    if (cj >= ql) continue;
-    const int pieces = 1 + mg.w - mg.y;
-    auto at = [&](int i) { return (size_t)(i ? 2 * (mg.y + i) : mg.z) * a.HG * C + u; };
-    float M = -INFINITY;
-    for (int i = lane; i < pieces; i += 32) M = fmaxf(M, __ldcg(a.part_ml + at(i) * 2));
-#pragma unroll
-    for (int sh = 16; sh > 0; sh >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, sh));
-    const float base = M == -INFINITY ? 0.f : M;
+  const int ql = a.q_lens ? __ldg(a.q_lens + b) : a.C, pieces = 1 + mg.w - mg.y;
+  const int quarter = threadIdx.x >> 5 & 3, sub = threadIdx.x >> 7;
+  const int per = (pieces + 3) / 4, i0 = min(pieces, quarter * per), i1 = min(pieces, i0 + per);
+  for (int u0 = blockIdx.y * kJoinColumns; u0 < a.HG * C; u0 += gridDim.y * kJoinColumns) {
+    const int u = u0 + sub, h = u / C, col = u % C, cj = col / a.G;
+    const bool on = u < a.HG * C && cj < ql;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float L = 0.f;
-    for (int i = 0; i < pieces; ++i) {
-      const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml + at(i) * 2));
-      const float wgt = ex2(ml.x - base);
-      L += wgt * ml.y;
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_o + at(i) * kD) + lane);
-      acc.x += wgt * v.x;
-      acc.y += wgt * v.y;
-      acc.z += wgt * v.z;
-      acc.w += wgt * v.w;
+    if (on) {
+      auto at = [&](int i) { return (size_t)(i ? 2 * (mg.y + i) : mg.z) * a.HG * C + u; };
+      float M = -INFINITY;
+      for (int i = lane; i < pieces; i += 32) M = fmaxf(M, __ldcg(a.part_ml + at(i) * 2));
+#pragma unroll
+      for (int sh = 16; sh > 0; sh >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, sh));
+      const float base = fmaxf(M, -3.0e38f);
+#pragma unroll 8
+      for (int i = i0; i < i1; ++i) {
+        const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml + at(i) * 2));
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_o + at(i) * kD) + lane);
+        const float wgt = ex2(ml.x - base);
+        L += wgt * ml.y;
+        acc.x += wgt * v.x;
+        acc.y += wgt * v.y;
+        acc.z += wgt * v.z;
+        acc.w += wgt * v.w;
+      }
     }
-    const float inv = L == 0.f ? 0.f : a.gv / L;
-    uint2* dst = reinterpret_cast<uint2*>(
-        a.out + (((size_t)b * a.C + cj) * a.Hq + (size_t)(grp * a.HG + h) * a.G + col % a.G) * kD) + lane;
-    *dst = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+    sum[sub][quarter][lane] = acc;
+    if (lane == 0) weight[sub][quarter] = L;
+    __syncthreads();
+    if (on && quarter == 0) {
+      for (int i = 1; i < 4; ++i) {
+        const float4 v = sum[sub][i][lane];
+        L += weight[sub][i];
+        acc.x += v.x;
+        acc.y += v.y;
+        acc.z += v.z;
+        acc.w += v.w;
+      }
+      const float inv = L == 0.f ? 0.f : a.gv / L;
+      uint2* dst = reinterpret_cast<uint2*>(
+          a.out + (((size_t)b * a.C + cj) * a.Hq + (size_t)(grp * a.HG + h) * a.G + col % a.G) * kD) + lane;
+      *dst = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+    }
+    __syncthreads();
   }
 }
 
 // How the columns of a KV head go to warps, and the CTAs to an SM.
 struct Shape {
-  int NT, tiles, HG, CW, ctas_per_sm, stages;
+  int NT, tiles, HG, CW, PW, ctas_per_sm, stages;
 };
 
 bool shape_for(const kvp_pool* pool, int C, int H, Shape* o) {
@@ -754,11 +1009,10 @@ bool shape_for(const kvp_pool* pool, int C, int H, Shape* o) {
   o->HG = kMaxConsumers / o->tiles;
   while (pool->kv_heads % o->HG) --o->HG;
   o->CW = o->HG * o->tiles;
-  // 18 warps an SM at 112 registers a thread, 9 at twice as many columns
-  o->ctas_per_sm = (o->NT == 1 ? 18 : 9) / (o->CW + 1);
-  if (o->ctas_per_sm > 8) o->ctas_per_sm = 8;
+  o->PW = o->CW > 4 ? 4 : o->CW > 2 ? 2 : 1;
+  o->ctas_per_sm = kThreads / 32 / (o->CW + o->PW);  // twelve warps an SM, 168 registers a thread
   o->stages = kMaxStages;
-  while (o->stages > 2 && smem_bytes(o->HG, o->stages) + 2048 > kSmemPerSm / o->ctas_per_sm) --o->stages;
+  while (o->stages > 2 && smem_bytes(o->HG, o->stages, o->CW, o->NT) + 2048 > kSmemPerSm / o->ctas_per_sm) --o->stages;
   return true;
 }
 
@@ -833,8 +1087,10 @@ int launch_fp4_tc(const Fp4Call& c, cudaStream_t stream) {
   a.n_groups = pool->kv_heads / sh.HG;
   a.tiles = sh.tiles;
   a.CW = sh.CW;
+  a.PW = sh.PW;
   a.stages = sh.stages;
   a.num_ctas = pool->num_sms * sh.ctas_per_sm;
+  a.by_request = (long long)c.B * a.n_groups <= a.num_ctas;
   a.window = c.window;
   a.sinks = c.sinks;
   a.max_context = c.max_context;
@@ -845,7 +1101,7 @@ int launch_fp4_tc(const Fp4Call& c, cudaStream_t stream) {
   a.part_o = reinterpret_cast<float*>(ws + lay.o);
   a.err = pool->err;
   auto kernel = sh.NT == 1 ? fp4_decode_kernel<1> : fp4_decode_kernel<2>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes(sh.HG, sh.stages)) !=
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes(sh.HG, sh.stages, sh.CW, sh.NT)) !=
       cudaSuccess)
     return KVP_ERR_CUDA;
   cudaLaunchAttribute attr[1];
@@ -853,14 +1109,17 @@ int launch_fp4_tc(const Fp4Call& c, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.num_ctas);
-  cfg.blockDim = dim3(32 * (sh.CW + 1));
-  cfg.dynamicSmemBytes = smem_bytes(sh.HG, sh.stages);
+  cfg.blockDim = dim3(32 * (sh.CW + sh.PW));
+  cfg.dynamicSmemBytes = smem_bytes(sh.HG, sh.stages, sh.CW, sh.NT);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, kernel, a) != cudaSuccess) return KVP_ERR_CUDA;
-  cfg.gridDim = dim3(a.num_ctas, (sh.HG * a.C * a.G + 3) / 4);
-  cfg.blockDim = dim3(128);
+  // a block a record at least; about as many as run at once, where there are columns for them
+  const int records = a.by_request ? c.B * a.n_groups : a.num_ctas;
+  const int columns = (sh.HG * a.C * a.G + kJoinColumns - 1) / kJoinColumns, most = 4 * pool->num_sms / records;
+  cfg.gridDim = dim3(records, most < 1 ? 1 : most < columns ? most : columns);
+  cfg.blockDim = dim3(128 * kJoinColumns);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, fp4_combine_kernel, a) == cudaSuccess ? KVP_OK : KVP_ERR_CUDA;
 }
