@@ -717,27 +717,39 @@ __device__ __forceinline__ void values(const Args& a, const Smem& s, const Stage
   }
 }
 
-// A new piece: its queries in fp16, scaled by powers of two; nothing attended yet.
+// A new piece's queries, on their way: entries 32 c .. 32 c + 31 of column g of each eight.
 template <int NT>
-__device__ __forceinline__ void begin(const Args& a, int b, int grp, int ql, unsigned char* queries, int h, int col0, int lane,
-                                      State<NT>& z) {
-  const int g = lane >> 2, c = lane & 3, C = a.C * a.G;
+struct Queries {
+  uint4 x[NT][4];
+};
+template <int NT>
+__device__ __forceinline__ void fetch_queries(const Args& a, int b, int grp, int ql, int h, int col0, int lane, Queries<NT>& q) {
+  const int g = lane >> 2, c = lane & 3;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const int col = col0 + nt * 8 + g, cj = col / a.G;
-    uint4 x[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (col < C && cj < ql) {
+    for (int i = 0; i < 4; ++i) q.x[nt][i] = make_uint4(0u, 0u, 0u, 0u);
+    if (col < a.C * a.G && cj < ql) {
       const uint4* src = reinterpret_cast<const uint4*>(
           a.q + (((size_t)b * a.C + cj) * a.Hq + (size_t)(grp * a.HG + h) * a.G + col % a.G) * kD + 32 * c);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = __ldg(src + i);
+      for (int i = 0; i < 4; ++i) q.x[nt][i] = __ldg(src + i);
     }
+  }
+}
+
+// They turn to fp16, scaled by powers of two; nothing is attended yet.
+template <int NT>
+__device__ __forceinline__ void begin(const Args& a, const Queries<NT>& q, unsigned char* queries, int lane, State<NT>& z) {
+  const int c = lane & 3;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
     uint32_t mx = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      for (const uint32_t v : {x[i].x, x[i].y, x[i].z, x[i].w}) mx = max(mx, max(v << 16 & 0x7fff0000u, v & 0x7fff0000u));
+      for (const uint32_t v : {q.x[nt][i].x, q.x[nt][i].y, q.x[nt][i].z, q.x[nt][i].w})
+        mx = max(mx, max(v << 16 & 0x7fff0000u, v & 0x7fff0000u));
     mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
     mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
     // 2^e <= the largest < 2^(e + 1); zeros and subnormal rows: the smallest normal exponent; not finite: as it is
@@ -746,7 +758,7 @@ __device__ __forceinline__ void begin(const Args& a, int b, int grp, int ql, uns
     const float down = (e == 127 ? 0x1p-127f : __uint_as_float((uint32_t)(127 - e) << 23)) * (a.scale_log2 < 0.f ? -1.f : 1.f);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+      const uint32_t v[4] = {q.x[nt][i].x, q.x[nt][i].y, q.x[nt][i].z, q.x[nt][i].w};
       uint32_t y[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) y[u] = pack_half(bf16_lo(v[u]) * down, bf16_hi(v[u]) * down);
@@ -824,7 +836,9 @@ __device__ void consume(const Args& a, const Smem& s, const Plan& pl, int w, int
   p.queries = smem_u32(queries) + 16 * lane;
   const uint32_t stages = smem_u32(s.stages);
   State<NT> z;
-  begin<NT>(a, pl.b, pl.g, pl.ql, queries, h, col0, lane, z);  // the first piece's, while its rows are on their way
+  Queries<NT> q;
+  fetch_queries<NT>(a, pl.b, pl.g, pl.ql, h, col0, lane, q);  // the first piece's, while its rows are on their way
+  begin<NT>(a, q, queries, lane, z);
 
   int st = 0, phase = 0;  // the buffer of the next stage to wait for, and that wait's parity
   auto next = [&](Stage& o) {
@@ -848,59 +862,59 @@ __device__ void consume(const Args& a, const Smem& s, const Plan& pl, int w, int
   long long left = pl.R1 - pl.R0;
   Stage cur;
   if (!next(cur)) return;
-  bool fresh = false;
   for (;;) {
     // plain stages of a piece, all swizzled or all token by token: the next one's scores beside this one's values, two
     // streams of instructions that wait for each other only through the weights
     float x[2][NT][4];
     uint32_t pb[2][NT][2];
-    if (fresh && (cur.flags & 1)) begin<NT>(a, cur.hd->b, cur.hd->group, cur.hd->ql, queries, h, col0, lane, z);
-    fresh = true;
     const uint32_t kind = cur.flags & 28;
     Stage ahead;
     if (kind == 0) {
       scores<NT, 0>(s, cur, p, x);
       for (;;) {
         weights<NT, false>(a, cur, p, x, pb, z);
-        if (cur.flags & 2) break;
+        if ((cur.flags & 2) && left == 1) break;
         if (!next(ahead)) return;
-        if (ahead.flags & 28) break;
+        if ((cur.flags & 2) || (ahead.flags & 28)) break;
         scores<NT, 0>(s, ahead, p, x);
         values<NT, 0, false>(a, s, cur, p, pb, z);
         release(cur);
         cur = ahead;
         --left;
       }
+      if (NT == 1 && (ahead.flags & 1) && left > 1) fetch_queries<NT>(a, ahead.hd->b, ahead.hd->group, ahead.hd->ql, h, col0, lane, q);
       values<NT, 0, false>(a, s, cur, p, pb, z);
     } else if (kind == 24) {
       scores<NT, 1>(s, cur, p, x);
       for (;;) {
         weights<NT, false>(a, cur, p, x, pb, z);
-        if (cur.flags & 2) break;
+        if ((cur.flags & 2) && left == 1) break;
         if (!next(ahead)) return;
-        if ((ahead.flags & 28) != 24) break;
+        if ((cur.flags & 2) || (ahead.flags & 28) != 24) break;
         scores<NT, 1>(s, ahead, p, x);
         values<NT, 1, false>(a, s, cur, p, pb, z);
         release(cur);
         cur = ahead;
         --left;
       }
+      if (NT == 1 && (ahead.flags & 1) && left > 1) fetch_queries<NT>(a, ahead.hd->b, ahead.hd->group, ahead.hd->ql, h, col0, lane, q);
       values<NT, 1, false>(a, s, cur, p, pb, z);
     } else {
       scores<NT, 2>(s, cur, p, x);
       weights<NT, true>(a, cur, p, x, pb, z);
+      if (left > 1 && !next(ahead)) return;
+      if (NT == 1 && (ahead.flags & 1) && left > 1) fetch_queries<NT>(a, ahead.hd->b, ahead.hd->group, ahead.hd->ql, h, col0, lane, q);
       values<NT, 2, true>(a, s, cur, p, pb, z);
-      if (!(cur.flags & 2) && !next(ahead)) return;
     }
     const bool last = cur.flags & 2;
     if (last) finish<NT>(a, cur.hd, h, col0, lane, z);
     release(cur);
     if (--left == 0) return;
     if (last) {
-      if (!next(cur)) return;
-    } else {
-      cur = ahead;
+      if (NT > 1) fetch_queries<NT>(a, ahead.hd->b, ahead.hd->group, ahead.hd->ql, h, col0, lane, q);
+      begin<NT>(a, q, queries, lane, z);
     }
+    cur = ahead;
   }
 }
 
@@ -937,54 +951,73 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_decode_kernel(const __grid_co
   else consume<NT>(a, s, pl, warp, lane);
 }
 
-// Joins the pieces of the request that CTA blockIdx.x recorded, in CTA order: four warps a column, a quarter of the
-// pieces each (in order, eight loads on their way at a time), then the quarters in order.
-constexpr int kJoinColumns = 4;  // columns a block of 16 warps
-__global__ void __launch_bounds__(128 * kJoinColumns) fp4_combine_kernel(const __grid_constant__ Args a) {
-  __shared__ float4 sum[kJoinColumns][4][32];
-  __shared__ float weight[kJoinColumns][4];
+// Joins the pieces of a cut request, in CTA order: a block a column at a time, its four warps a quarter of the pieces each,
+// in order and six loads on their way at a time, then the quarters in order.
+constexpr int kJoin = 6;
+__global__ void __launch_bounds__(128, 8) fp4_combine_kernel(const __grid_constant__ Args a) {
+  __shared__ float4 sum[4][32];
+  __shared__ float2 weight[4];  // a quarter's maximum and sum
   griddep_wait();
   const int4 mg = a.merge[blockIdx.x];
   if (mg.x < 0) return;
-  const int b = mg.x / a.n_groups, grp = mg.x % a.n_groups, C = a.C * a.G, lane = threadIdx.x & 31;
+  const int b = mg.x / a.n_groups, grp = mg.x % a.n_groups, C = a.C * a.G, cols = a.HG * C;
+  const int lane = threadIdx.x & 31, quarter = threadIdx.x >> 5;
   const int ql = a.q_lens ? __ldg(a.q_lens + b) : a.C, pieces = 1 + mg.w - mg.y;
-  const int quarter = threadIdx.x >> 5 & 3, sub = threadIdx.x >> 7;
   const int per = (pieces + 3) / 4, i0 = min(pieces, quarter * per), i1 = min(pieces, i0 + per);
-  for (int u0 = blockIdx.y * kJoinColumns; u0 < a.HG * C; u0 += gridDim.y * kJoinColumns) {
-    const int u = u0 + sub, h = u / C, col = u % C, cj = col / a.G;
-    const bool on = u < a.HG * C && cj < ql;
+  for (int u = blockIdx.y; u < cols; u += gridDim.y) {
+    const int h = u / C, col = u % C, cj = col / a.G;
+    if (cj >= ql) continue;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float L = 0.f;
-    if (on) {
-      auto at = [&](int i) { return (size_t)(i ? 2 * (mg.y + i) : mg.z) * a.HG * C + u; };
-      float M = -INFINITY;
-      for (int i = lane; i < pieces; i += 32) M = fmaxf(M, __ldcg(a.part_ml + at(i) * 2));
+    float L = 0.f, M = -3.0e38f;
+    for (int i = i0; i < i1; i += kJoin) {
+      float2 ml[kJoin];
+      float4 v[kJoin];
 #pragma unroll
-      for (int sh = 16; sh > 0; sh >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, sh));
-      const float base = fmaxf(M, -3.0e38f);
-#pragma unroll 8
-      for (int i = i0; i < i1; ++i) {
-        const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml + at(i) * 2));
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_o + at(i) * kD) + lane);
-        const float wgt = ex2(ml.x - base);
-        L += wgt * ml.y;
+      for (int y = 0; y < kJoin; ++y) {
+        ml[y] = make_float2(-INFINITY, 0.f);
+        v[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i + y < i1) {
+          const size_t at = (size_t)(i + y ? 2 * (mg.y + i + y) : mg.z) * cols + u;
+          ml[y] = __ldcg(reinterpret_cast<const float2*>(a.part_ml + at * 2));
+          v[y] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * kD) + lane);
+        }
+      }
+      float mn = M;
+#pragma unroll
+      for (int y = 0; y < kJoin; ++y) mn = fmaxf(mn, ml[y].x);
+      const float al = ex2(M - mn);
+      M = mn;
+      L *= al;
+      acc = make_float4(acc.x * al, acc.y * al, acc.z * al, acc.w * al);
+#pragma unroll
+      for (int y = 0; y < kJoin; ++y) {
+        const float wgt = ex2(ml[y].x - M);
+        L += wgt * ml[y].y;
+        acc.x += wgt * v[y].x;
+        acc.y += wgt * v[y].y;
+        acc.z += wgt * v[y].z;
+        acc.w += wgt * v[y].w;
+      }
+    }
+    sum[quarter][lane] = acc;
+    if (lane == 0) weight[quarter] = make_float2(M, L);
+    __syncthreads();
+    if (quarter == 0) {
+      float mn = M;
+#pragma unroll
+      for (int i = 1; i < 4; ++i) mn = fmaxf(mn, weight[i].x);
+      const float al = ex2(M - mn);
+      L *= al;
+      acc = make_float4(acc.x * al, acc.y * al, acc.z * al, acc.w * al);
+#pragma unroll
+      for (int i = 1; i < 4; ++i) {
+        const float wgt = ex2(weight[i].x - mn);
+        const float4 v = sum[i][lane];
+        L += wgt * weight[i].y;
         acc.x += wgt * v.x;
         acc.y += wgt * v.y;
         acc.z += wgt * v.z;
         acc.w += wgt * v.w;
-      }
-    }
-    sum[sub][quarter][lane] = acc;
-    if (lane == 0) weight[sub][quarter] = L;
-    __syncthreads();
-    if (on && quarter == 0) {
-      for (int i = 1; i < 4; ++i) {
-        const float4 v = sum[sub][i][lane];
-        L += weight[sub][i];
-        acc.x += v.x;
-        acc.y += v.y;
-        acc.z += v.z;
-        acc.w += v.w;
       }
       const float inv = L == 0.f ? 0.f : a.gv / L;
       uint2* dst = reinterpret_cast<uint2*>(
@@ -1115,11 +1148,11 @@ int launch_fp4_tc(const Fp4Call& c, cudaStream_t stream) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, kernel, a) != cudaSuccess) return KVP_ERR_CUDA;
-  // a block a record at least; about as many as run at once, where there are columns for them
+  // a block a column, no more than run at once
   const int records = a.by_request ? c.B * a.n_groups : a.num_ctas;
-  const int columns = (sh.HG * a.C * a.G + kJoinColumns - 1) / kJoinColumns, most = 4 * pool->num_sms / records;
+  const int columns = sh.HG * a.C * a.G, most = 16 * pool->num_sms / records;
   cfg.gridDim = dim3(records, most < 1 ? 1 : most < columns ? most : columns);
-  cfg.blockDim = dim3(128 * kJoinColumns);
+  cfg.blockDim = dim3(128);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, fp4_combine_kernel, a) == cudaSuccess ? KVP_OK : KVP_ERR_CUDA;
 }
