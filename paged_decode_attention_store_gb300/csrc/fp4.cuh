@@ -47,20 +47,20 @@ __device__ __forceinline__ uint32_t e4m3_code(float a) {
   return r & 0xffu;
 }
 
-// The code of the scale for a block whose largest entry is m >= 0 (m / 6 g, nearest, ties to even): a first guess, put
-// right by comparing with the borders, which are small integers times powers of two.
-__device__ __forceinline__ uint32_t fp4_scale_exact(double m, double g) {
-  uint32_t c = e4m3_code((float)(m / g) * (1.f / 6.f));
+// The code of the scale for a block whose largest entry is m >= 0 (m / 6 g, nearest, ties to even; inv_g = 1 / g): a first
+// guess, put right by comparing with the borders, which are small integers times powers of two.
+__device__ __forceinline__ uint32_t fp4_scale_exact(double m, double g, double inv_g) {
+  const uint32_t c = e4m3_code((float)(m * inv_g) * (1.f / 6.f));
   // the midpoint of scales c and c + 1, times 6 g
-  auto border = [&](uint32_t k) { return ((double)e4m3_value(k) + (double)e4m3_value(k + 1)) * 3.0 * g; };
+  auto border = [&](uint32_t k) { return (double)((e4m3_value(k) + e4m3_value(k + 1)) * 3.f) * g; };
   if (c < 0x7e && (m > border(c) || (m == border(c) && (c & 1)))) return c + 1;
   if (c > 0 && (m < border(c - 1) || (m == border(c - 1) && (c & 1)))) return c - 1;
   return c;
 }
 // The code (without sign) of |x| under the scale sg = scale * g > 0, likewise.
-__device__ __forceinline__ uint32_t fp4_code_exact(double ax, double sg) {
-  uint32_t c = e2m1x2((float)(ax / sg), 0.f) & 7u;
-  auto border = [&](uint32_t k) { return (double)(e2m1_value(k) + e2m1_value(k + 1)) * 0.5 * sg; };
+__device__ __forceinline__ uint32_t fp4_code_exact(double ax, float sg) {
+  const uint32_t c = e2m1x2(__fdividef((float)ax, sg), 0.f) & 7u;
+  auto border = [&](uint32_t k) { return (double)((e2m1_value(k) + e2m1_value(k + 1)) * 0.5f) * (double)sg; };
   if (c < 7 && (ax > border(c) || (ax == border(c) && (c & 1)))) return c + 1;
   if (c > 0 && (ax < border(c - 1) || (ax == border(c - 1) && (c & 1)))) return c - 1;
   return c;
@@ -84,11 +84,23 @@ __device__ __forceinline__ uint32_t fp4_block_max(const float (&x)[N], unsigned 
 
 // x / y by y's reciprocal, corrected once by the residual (which one fma gives exactly): off by a 2^-45th before its
 // rounding. Where the quotient is a border of two codes, four bits, it is that border; an x beside it, a 2^-24th away at
-// least, is not. Far quotients saturate whatever the correction, which would be no number where r overflows.
+// least, is not. FAR: quotients beyond 1024 may come; they saturate whatever the correction, which would be no number where
+// r overflows.
+template <bool FAR>
 __device__ __forceinline__ float quotient(float x, float y, float inv) {
   const float r = x * inv;
-  return fabsf(r) < 1024.f ? fmaf(fmaf(-r, y, x), inv, r) : r;
+  return !FAR || fabsf(r) < 1024.f ? fmaf(fmaf(-r, y, x), inv, r) : r;
 }
+
+// N exact entries to codes under the scale of that code; entries are within 7 scales of zero but for the largest scale.
+template <int N, bool FAR>
+__device__ __forceinline__ uint32_t fp4_codes(const float* x, float sg, float inv) {
+  uint32_t codes = 0;
+#pragma unroll
+  for (int i = 0; i < N; i += 2) codes |= e2m1x2(quotient<FAR>(x[i], sg, inv), quotient<FAR>(x[i + 1], sg, inv)) << (4 * i);
+  return codes;
+}
+constexpr uint32_t kFp4MostScale = 0x7eu;  // 448
 
 // A block's codes and scale from exact entries, N of them in each of 16 / N neighbouring lanes. A block with an entry
 // that is not finite has the scale NaN.
@@ -99,62 +111,75 @@ __device__ __forceinline__ void fp4_block(const float (&x)[N], float g, float in
   codes = 0;
   scale = kFp4NanScale;
   if (mb >= kInfBits) return;
-  scale = e4m3_code(quotient(__uint_as_float(mb) * inv_g, 6.f, 1.f / 6.f));
+  scale = e4m3_code(quotient<true>(__uint_as_float(mb) * inv_g, 6.f, 1.f / 6.f));
   if (scale == 0) return;
   const float sg = e4m3_value(scale) * g, inv = __frcp_rn(sg);
-#pragma unroll
-  for (int i = 0; i < N; i += 2) codes |= e2m1x2(quotient(x[i], sg, inv), quotient(x[i + 1], sg, inv)) << (4 * i);
+  codes = scale == kFp4MostScale ? fp4_codes<N, true>(x, sg, inv) : fp4_codes<N, false>(x, sg, inv);
 }
 
-// The same from entries that are off by ex at most. Returns true, to all of the block's lanes, when a rounding lies within
-// the error of a border and the entries have to be found more exactly.
-template <int N>
-__device__ __forceinline__ bool fp4_block_within(const float (&x)[N], const float (&ex)[N], float g, float inv_g,
-                                                 unsigned mask, uint32_t& codes, uint32_t& scale) {
+// A whole block in one thread.
+__device__ __forceinline__ void fp4_block16(const float (&x)[16], float g, float inv_g, uint32_t& lo, uint32_t& hi,
+                                            uint32_t& scale) {
+  uint32_t mb = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) mb = max(mb, abs_bits(x[i]));
+  lo = hi = 0;
+  scale = kFp4NanScale;
+  if (mb >= kInfBits) return;
+  scale = e4m3_code(quotient<true>(__uint_as_float(mb) * inv_g, 6.f, 1.f / 6.f));
+  if (scale == 0) return;
+  const float sg = e4m3_value(scale) * g, inv = __frcp_rn(sg);
+  if (scale == kFp4MostScale) {
+    lo = fp4_codes<8, true>(x, sg, inv);
+    hi = fp4_codes<8, true>(x + 8, sg, inv);
+  } else {
+    lo = fp4_codes<8, false>(x, sg, inv);
+    hi = fp4_codes<8, false>(x + 8, sg, inv);
+  }
+}
+
+// The same from a lane's N entries that are off by ex at most; exact(i) gives its entry i to 52 bits. It is asked for where a
+// rounding lies within the error of a border: for the entries that may be the largest when it is the scale's, for the one
+// entry when it is a code's.
+template <int N, typename Exact>
+__device__ __forceinline__ void fp4_block_within(const float (&x)[N], float ex, float g, float inv_g, unsigned mask,
+                                                 const Exact& exact, uint32_t& codes, uint32_t& scale) {
   constexpr int kLanes = kFp4Block / N;
   const uint32_t mb = fp4_block_max<N>(x, mask);
-  float em = 0.f;
 #pragma unroll
-  for (int i = 0; i < N; ++i) em = fmaxf(em, ex[i]);
-#pragma unroll
-  for (int d = 1; d < kLanes; d <<= 1) em = fmaxf(em, __shfl_xor_sync(mask, em, d));
+  for (int d = 1; d < kLanes; d <<= 1) ex = fmaxf(ex, __shfl_xor_sync(mask, ex, d));
   codes = 0;
   scale = kFp4NanScale;
-  if (mb >= kInfBits) return false;
-  const float q = __uint_as_float(mb) * inv_g * (1.f / 6.f), eq = em * inv_g * (1.f / 6.f) + q * 0x1p-22f;
+  if (mb >= kInfBits) return;
+  const float m = __uint_as_float(mb), q = m * inv_g * (1.f / 6.f), eq = ex * inv_g * (1.f / 6.f) + q * 0x1p-22f;
   scale = e4m3_code(fmaxf(q - eq, 0.f));
-  if (scale != e4m3_code(q + eq)) return true;
-  if (scale == 0) return false;
-  const float inv = __frcp_rn(e4m3_value(scale) * g);
+  if (scale != e4m3_code(q + eq)) {
+    uint32_t largest = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) largest |= fabsf(x[i]) + ex >= m - ex ? 1u << i : 0u;
+    double md = 0.0;
+    for (; largest; largest &= largest - 1) md = fmax(md, fabs(exact(__ffs(largest) - 1)));
+#pragma unroll
+    for (int d = 1; d < kLanes; d <<= 1) md = fmax(md, __shfl_xor_sync(mask, md, d));
+    scale = fp4_scale_exact(md, g, inv_g);
+  }
+  if (scale == 0) return;
+  // an entry's quotient is off by the rotation's error and by 2^-23 of itself, which is 7 at most or saturates
+  const float sg = e4m3_value(scale) * g, inv = __frcp_rn(sg), e = ex * inv + 0x1p-20f;
   uint32_t other = 0;
 #pragma unroll
   for (int i = 0; i < N; i += 2) {
     const float r0 = x[i] * inv, r1 = x[i + 1] * inv;
-    const float e0 = fmaf(ex[i], inv, fabsf(r0) * 0x1p-22f), e1 = fmaf(ex[i + 1], inv, fabsf(r1) * 0x1p-22f);
-    codes |= e2m1x2(r0 - e0, r1 - e1) << (4 * i);
-    other |= e2m1x2(r0 + e0, r1 + e1) << (4 * i);
+    codes |= e2m1x2(r0 - e, r1 - e) << (4 * i);
+    other |= e2m1x2(r0 + e, r1 + e) << (4 * i);
   }
-  bool near = codes != other;
-#pragma unroll
-  for (int d = 1; d < kLanes; d <<= 1) near |= (bool)__shfl_xor_sync(mask, (int)near, d);
-  return near;
-}
-
-// The same of entries known to 53 bits (finite ones).
-template <int N>
-__device__ __forceinline__ void fp4_block_exact(const double (&x)[N], double g, unsigned mask, uint32_t& codes,
-                                                uint32_t& scale) {
-  double m = 0.0;
-#pragma unroll
-  for (int i = 0; i < N; ++i) m = fmax(m, fabs(x[i]));
-#pragma unroll
-  for (int d = 1; d < kFp4Block / N; d <<= 1) m = fmax(m, __shfl_xor_sync(mask, m, d));
-  codes = 0;
-  scale = fp4_scale_exact(m, g);
-  if (scale == 0) return;
-  const double sg = (double)e4m3_value(scale) * g;
-#pragma unroll
-  for (int i = 0; i < N; ++i) codes |= (fp4_code_exact(fabs(x[i]), sg) | (x[i] < 0.0 ? 8u : 0u)) << (4 * i);
+  for (uint32_t open = codes ^ other; open;) {
+    const int i = (__ffs(open) - 1) >> 2;
+    const double v = exact(i);
+    const uint32_t c = fp4_code_exact(fabs(v), sg) | (v < 0.0 ? 8u : 0u);
+    codes = (codes & ~(15u << (4 * i))) | c << (4 * i);
+    open &= ~(15u << (4 * i));
+  }
 }
 
 // Eight codes to four pairs of fp16, and two scales to a pair: exact.

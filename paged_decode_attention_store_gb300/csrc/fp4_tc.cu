@@ -215,6 +215,13 @@ __device__ __forceinline__ Request request_of(const Args& a, int b) {
   return r;
 }
 
+// a / b of numbers that are not negative: in 32 bits where they fit, as they nearly always do (64 take a hundred
+// instructions, and four of them lie one after another at every CTA's start).
+__device__ __forceinline__ long long quotient_of(long long a, long long b) {
+  if (((unsigned long long)(a | b) >> 32) == 0) return (unsigned)a / (unsigned)b;
+  return a / b;
+}
+
 // This CTA's share of the batch's stages, found by the whole CTA.
 struct Plan {
   long long R0, R1, Sv;  // the share, and where its first request and group begin
@@ -239,14 +246,14 @@ __device__ void make_plan(const Args& a, Plan* pl, bool* any_bad) {
   if (threadIdx.x == 0 && !a.by_request) a.merge[k] = make_int4(-1, 0, 0, 0);
   __syncthreads();
   if (k < Ne) {
-    const long long R0 = k * T / Ne, R1 = (k + 1) * T / Ne;
+    const long long R0 = quotient_of(k * T, Ne), R1 = quotient_of((k + 1) * T, Ne);
     if (at * a.n_groups <= R0 && R0 < (at + mine) * a.n_groups) {  // the first request is one of this thread's
       for (int b = b0; b < b1; ++b) {
         const Request r = request_of(a, b);
         const int n = r.n;
         const long long first = at * a.n_groups;
         if (R0 < first + (long long)n * a.n_groups) {
-          const int g = (int)((R0 - first) / n);
+          const int g = a.n_groups == 1 ? 0 : (int)quotient_of(R0 - first, n);
           const long long Sv = first + (long long)g * n;
           pl->R0 = R0;
           pl->R1 = R1;
@@ -257,8 +264,8 @@ __device__ void make_plan(const Args& a, Plan* pl, bool* any_bad) {
           pl->ql = r.ql;
           pl->cut = make_int4(-1, 0, 0, 0);
           if (Sv < R0 && Sv + n <= R1) {  // cut, and its last piece is here
-            const long long ka = ((Sv + 1) * Ne + T - 1) / T - 1;  // the CTA of its first piece
-            pl->cut = make_int4(b * a.n_groups + g, (int)ka, (int)(ka * T / Ne == Sv ? 2 * ka : 2 * ka + 1), (int)k);
+            const long long ka = quotient_of((Sv + 1) * Ne + T - 1, T) - 1;  // the CTA of its first piece
+            pl->cut = make_int4(b * a.n_groups + g, (int)ka, (int)(quotient_of(ka * T, Ne) == Sv ? 2 * ka : 2 * ka + 1), (int)k);
             if (!a.by_request) a.merge[k] = pl->cut;
           }
           break;
@@ -322,7 +329,7 @@ __device__ __forceinline__ void prepare(const Args& a, const Plan& pl, long long
   }
   r = request_of(a, fb);
   const long long x = x0 + want;
-  const int back = (int)((fS - x - 1) / max(r.n, 1));  // groups after this stage's: fS is the end of all
+  const int back = a.n_groups == 1 ? 0 : (int)quotient_of(max(fS - x - 1, 0ll), max(r.n, 1));  // groups after this stage's: fS is the end of all
   fg = a.n_groups - 1 - back;
   fS -= (long long)(back + 1) * r.n;                   // this group's first stage
   const int i = (int)(x - fS);
@@ -727,12 +734,12 @@ __device__ __forceinline__ void fetch_queries(const Args& a, int b, int grp, int
   const int g = lane >> 2, c = lane & 3;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    const int col = col0 + nt * 8 + g, cj = col / a.G;
+    const int col = col0 + nt * 8 + g, cj = a.C == 1 ? 0 : col / a.G;
 #pragma unroll
     for (int i = 0; i < 4; ++i) q.x[nt][i] = make_uint4(0u, 0u, 0u, 0u);
     if (col < a.C * a.G && cj < ql) {
       const uint4* src = reinterpret_cast<const uint4*>(
-          a.q + (((size_t)b * a.C + cj) * a.Hq + (size_t)(grp * a.HG + h) * a.G + col % a.G) * kD + 32 * c);
+          a.q + (((size_t)b * a.C + cj) * a.Hq + (size_t)(grp * a.HG + h) * a.G + col - cj * a.G) * kD + 32 * c);
 #pragma unroll
       for (int i = 0; i < 4; ++i) q.x[nt][i] = __ldg(src + i);
     }
@@ -789,7 +796,7 @@ __device__ __forceinline__ void finish(const Args& a, const Hdr* hd, int h, int 
       float ls = z.l[nt][e];
 #pragma unroll
       for (int sh = 4; sh < 32; sh <<= 1) ls += __shfl_xor_sync(0xffffffffu, ls, sh);
-      const int col = col0 + nt * 8 + 2 * c + e, cj = col / a.G;
+      const int col = col0 + nt * 8 + 2 * c + e, cj = a.C == 1 ? 0 : col / a.G;
       if (col >= C || cj >= ql) continue;
       float v[16];
 #pragma unroll
@@ -800,7 +807,7 @@ __device__ __forceinline__ void finish(const Args& a, const Hdr* hd, int h, int 
       if (part < 0) {
         const float inv = ls == 0.f ? 0.f : a.gv / ls;
         uint4* dst = reinterpret_cast<uint4*>(
-            a.out + (((size_t)hd->b * a.C + cj) * a.Hq + (size_t)(hd->group * a.HG + h) * a.G + col % a.G) * kD + 16 * g);
+            a.out + (((size_t)hd->b * a.C + cj) * a.Hq + (size_t)(hd->group * a.HG + h) * a.G + col - cj * a.G) * kD + 16 * g);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
           dst[i] = make_uint4(pack_bf16(v[8 * i] * inv, v[8 * i + 1] * inv), pack_bf16(v[8 * i + 2] * inv, v[8 * i + 3] * inv),
@@ -965,7 +972,7 @@ __global__ void __launch_bounds__(128, 8) fp4_combine_kernel(const __grid_consta
   const int ql = a.q_lens ? __ldg(a.q_lens + b) : a.C, pieces = 1 + mg.w - mg.y;
   const int per = (pieces + 3) / 4, i0 = min(pieces, quarter * per), i1 = min(pieces, i0 + per);
   for (int u = blockIdx.y; u < cols; u += gridDim.y) {
-    const int h = u / C, col = u % C, cj = col / a.G;
+    const int h = u / C, col = u % C, cj = a.C == 1 ? 0 : col / a.G;
     if (cj >= ql) continue;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float L = 0.f, M = -3.0e38f;
@@ -1021,7 +1028,7 @@ __global__ void __launch_bounds__(128, 8) fp4_combine_kernel(const __grid_consta
       }
       const float inv = L == 0.f ? 0.f : a.gv / L;
       uint2* dst = reinterpret_cast<uint2*>(
-          a.out + (((size_t)b * a.C + cj) * a.Hq + (size_t)(grp * a.HG + h) * a.G + col % a.G) * kD) + lane;
+          a.out + (((size_t)b * a.C + cj) * a.Hq + (size_t)(grp * a.HG + h) * a.G + col - cj * a.G) * kD) + lane;
       *dst = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
     }
     __syncthreads();

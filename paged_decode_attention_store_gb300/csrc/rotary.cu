@@ -63,6 +63,7 @@ struct RotArgs {
   int axes;
   char* scales;  // four-bit pools: the layer's block scales; k_dst and v_dst are codes
   float gk, gv;
+  int kv_tokens, kv_blocks;  // tokens a block of keys and values takes, and how many such blocks there are
 };
 
 // The position by which pair i of token tok turns.
@@ -94,28 +95,44 @@ __device__ __forceinline__ float2 turn_of(int p, uint64_t f, float attn) {
 __device__ __forceinline__ double exact_value(float x) { return x; }
 __device__ __forceinline__ double exact_value(__nv_bfloat16 x) { return __bfloat162float(x); }
 
-// Entry e of a head at src, turned, in 64 bits: what decides a rounding to four bits when 32 leave it open.
+// The cosine and sine of turn t (of 2^64) in 62-bit fixed point, good to 2^-57: the Taylor series of both on [-pi/4, pi/4]
+// around the nearest quarter turn. In integers, as they run at full rate here: 64-bit floats run at a 64th of it.
+__device__ __forceinline__ void turn_exact(uint64_t t, int64_t* cosine, int64_t* sine) {
+  // (-1)^k / (2 k)! and (-1)^k / (2 k + 1)!, times 2^62, k = 8 .. 0
+  constexpr int64_t kOne = 1ll << 62;
+  constexpr int64_t kCos[9] = {kOne / 20922789888000ll, -kOne / 87178291200ll, kOne / 479001600ll, -kOne / 3628800ll,
+                               kOne / 40320ll, -kOne / 720ll, kOne / 24ll, -kOne / 2ll, kOne};
+  constexpr int64_t kSin[9] = {kOne / 355687428096000ll, -kOne / 1307674368000ll, kOne / 6227020800ll, -kOne / 39916800ll,
+                               kOne / 362880ll, -kOne / 5040ll, kOne / 120ll, -kOne / 6ll, kOne};
+  const uint32_t quarters = ((uint32_t)(t >> 32) + (1u << 29)) >> 30;
+  const int64_t r = (int64_t)(t - ((uint64_t)quarters << 62));  // a quarter turn is 2^62
+  const int64_t angle = __mul64hi(r, 7244019458077122842ll) << 2;  // r * pi / 2^63, times 2^62: by pi * 2^61
+  const int64_t z = __mul64hi(angle, angle) << 2;
+  int64_t c = kCos[0], s = kSin[0];
+#pragma unroll
+  for (int k = 1; k < 9; ++k) {
+    c = kCos[k] + (__mul64hi(c, z) << 2);
+    s = kSin[k] + (__mul64hi(s, z) << 2);
+  }
+  s = __mul64hi(s, angle) << 2;
+  const bool odd = quarters & 1;  // (c, s) -> (-s, c) a quarter
+  const int64_t x = odd ? s : c, y = odd ? c : s;
+  *cosine = (quarters + 1) & 2 ? -x : x;
+  *sine = quarters & 2 ? -y : y;
+}
+
+// Entry e of a head at src, turned, to 52 bits: what decides a rounding to four bits when 32 leave it open.
 template <typename T, bool AXES>
-__device__ double exact_entry(const RotArgs& a, const T* src, size_t tok, int e, bool half) {
+__device__ __noinline__ double exact_entry(const RotArgs& a, const T* src, size_t tok, int e, bool half) {
   if (e >= a.rot) return exact_value(src[e]);
   const int pairs = a.rot / 2, i = half ? (e < pairs ? e : e - pairs) : e / 2;
   const bool first = half ? e < pairs : !(e & 1);
   const double x = exact_value(src[half ? i : 2 * i]), y = exact_value(src[half ? i + pairs : 2 * i + 1]);
   const uint64_t t = (uint64_t)(int64_t)position_of<AXES>(a, tok, i) * __ldg(a.freqs + i);
-  double s, c;
-  sincospi((double)(int64_t)t * 0x1p-63, &s, &c);
+  int64_t ci, si;
+  turn_exact(t, &ci, &si);
+  const double c = (double)ci * 0x1p-62, s = (double)si * 0x1p-62;
   return (first ? x * c - y * s : y * c + x * s) * (double)a.attn;
-}
-
-// N consecutive entries from e0 of key head h, in 64 bits, to their codes and the block's scale.
-template <typename T, bool AXES, int N>
-__device__ __noinline__ void exact_codes(const RotArgs& a, size_t tok, int h, int e0, bool half, unsigned mask,
-                                         uint32_t* codes, uint32_t* scale) {
-  const T* src = reinterpret_cast<const T*>(a.k + tok * a.k_tok) + (size_t)h * a.d;
-  double x[N];
-#pragma unroll 1
-  for (int i = 0; i < N; ++i) x[i] = exact_entry<T, AXES>(a, src, tok, e0 + i, half);
-  fp4_block_exact<N>(x, (double)a.gk, mask, *codes, *scale);
 }
 
 template <typename T>
@@ -155,19 +172,12 @@ struct RotUnit {
   uint4 w0, w1;
   char* dst;  // nullptr: nothing to do (past the last head, or a key without a slot)
   const float4* f;  // two pairs' turns, the next two ``rot_units`` further
-  int head;  // of keys into a four-bit pool
 };
 
 // 16-byte chunks: every row, stride and half of a pair block starts on 16 bytes. The fp32 interleaved form is held to
 // 48 registers, ten blocks an SM (the 56 it takes by itself: 9.1 us for 8.1 at 3,001 tokens); bounds cost the others.
-//
-// FP4: keys and values go to a four-bit pool. A block of 16 entries lies in 16 / N neighbouring threads, which agree on
-// its largest entry by shuffles. The rotation's error (2^-21 of a pair's size; 2^-20 is reckoned with) leaves one
-// rounding in some ten thousand open: those blocks are done again in 64 bits, so that codes and scales are those of the
-// 64-bit formula.
-template <typename T, bool HALF, bool AXES, bool FP4>
-__global__ void __launch_bounds__(kRotThreads, !HALF && sizeof(T) == 4 && !AXES && !FP4 ? 10 : 0)
-    rotary_store_kernel(const __grid_constant__ RotArgs a) {
+template <typename T, bool HALF, bool AXES, bool KEYS>
+__device__ __forceinline__ void rotary_body(const RotArgs& a, int block) {
   constexpr int N = Vec<T>::N;
   constexpr int kV = 2;  // chunks of v a thread loads ahead
   constexpr int PU = HALF ? N : N / 2;  // pairs of a unit
@@ -178,7 +188,7 @@ __global__ void __launch_bounds__(kRotThreads, !HALF && sizeof(T) == 4 && !AXES 
   __shared__ int slots[kRotMaxTokens];
   const int tid = threadIdx.x;
   const int pairs = a.rot / 2;
-  const int t0 = blockIdx.x * a.tokens;
+  const int t0 = block * a.tokens;
   const int nt = min(a.tokens, a.n - t0);
   // units of a head: rotated ones first (HALF: chunk u and chunk u + rot / 2 N), then the rest of the head, one chunk each
   const int rot_units = HALF ? a.rot / (2 * N) : a.rot / N;
@@ -186,9 +196,9 @@ __global__ void __launch_bounds__(kRotThreads, !HALF && sizeof(T) == 4 && !AXES 
   const int upar = max(1, min(units, kRotThreads));  // no units: rows without a rotated part
   const int groups = kRotThreads / upar;
   const int g = tid / upar, u0 = tid - g * upar;
-  const int heads = a.hq + a.hk;
+  const int heads = KEYS ? a.hq + a.hk : a.hq;
   const int jobs = g < groups ? nt * heads : 0;  // (token, head)
-  const int v_chunks = a.k ? a.v_elems / N : 0, v_jobs = nt * v_chunks;
+  const int v_chunks = KEYS && a.k ? a.v_elems / N : 0, v_jobs = nt * v_chunks;
 
   // Loads the unit u of job j; its slot is looked up in store().
   auto load = [&](int j, int u, RotUnit<T, HALF>& x, int& key_of) {
@@ -208,50 +218,24 @@ __global__ void __launch_bounds__(kRotThreads, !HALF && sizeof(T) == 4 && !AXES 
     if (is_q) {
       x.dst = a.q_out + tok * a.qo_tok + (size_t)h * a.qo_head + (size_t)e0 * sizeof(T);
     } else {
-      x.head = h - a.hq;
-      x.dst = FP4 ? a.k_dst + (size_t)x.head * a.d + e0 / 2 : a.k_dst + ((size_t)x.head * a.d + e0) * sizeof(T);
+      x.dst = a.k_dst + ((size_t)(h - a.hq) * a.d + e0) * sizeof(T);
       key_of = t;
     }
-  };
-  // N entries of a block to their place in a four-bit pool: entries e0 .. of plane ``part`` of a head; ``scale`` is the block's.
-  const unsigned block_mask = ((1u << (kFp4Block / N)) - 1u) << (tid & 31 & ~(kFp4Block / N - 1));
-  auto put_codes = [&](char* dst, uint32_t codes, uint32_t scale, int slot, int head, int part, int e0) {
-    if (N == 8) *reinterpret_cast<uint32_t*>(dst) = codes;
-    else *reinterpret_cast<uint16_t*>(dst) = (uint16_t)codes;
-    if (e0 % kFp4Block == 0)
-      a.scales[fp4_scale_offset(slot, head, a.v_elems / a.d, a.d) + part * (a.d / 16) + e0 / 16] = (char)scale;
-  };
-  const float inv_gk = FP4 ? 1.f / a.gk : 0.f, inv_gv = FP4 ? 1.f / a.gv : 0.f;
-  auto put_block = [&](const float (&r)[N], const float (&er)[N], char* dst, int t, int slot, int head, int e0) {
-    uint32_t codes, scale;
-    if (fp4_block_within<N>(r, er, a.gk, inv_gk, block_mask, codes, scale))
-      exact_codes<T, AXES, N>(a, (size_t)(t0 + t), head, e0, HALF, block_mask, &codes, &scale);
-    put_codes(dst, codes, scale, slot, head, 0, e0);
   };
   auto store = [&](const RotUnit<T, HALF>& x, int u, int key_of) {
     if (!x.dst) return;
     char* dst = x.dst;
-    int slot = -1;
-    if (key_of >= 0) {
-      slot = slots[key_of];
+    if (KEYS && key_of >= 0) {
+      const int slot = slots[key_of];
       if (slot < 0) return;
       dst += (size_t)slot * a.row_bytes;
     }
     if (u >= rot_units) {
-      if (FP4 && key_of >= 0) {
-        float v[N];
-        uint32_t codes, scale;
-        Vec<T>::get(x.w0, v);
-        fp4_block<N>(v, a.gk, inv_gk, block_mask, codes, scale);
-        put_codes(dst, codes, scale, slot, x.head, 0, HALF ? a.rot + (u - rot_units) * N : u * N);
-        return;
-      }
       *reinterpret_cast<uint4*>(dst) = x.w0;
       return;
     }
     float v[N];
     Vec<T>::get(x.w0, v);
-    const float off = fabsf(a.attn) * 0x1p-20f;
     if (HALF) {
       float y[N], r0[N], r1[N];
       Vec<T>::get(x.w1, y);
@@ -262,14 +246,6 @@ __global__ void __launch_bounds__(kRotThreads, !HALF && sizeof(T) == 4 && !AXES 
         r1[i] = y[i] * f.x + v[i] * f.y;
         r0[i + 1] = v[i + 1] * f.z - y[i + 1] * f.w;
         r1[i + 1] = y[i + 1] * f.z + v[i + 1] * f.w;
-      }
-      if (FP4 && key_of >= 0) {
-        float er[N];
-#pragma unroll
-        for (int i = 0; i < N; ++i) er[i] = (fabsf(v[i]) + fabsf(y[i])) * off;
-        put_block(r0, er, dst, key_of, slot, x.head, u * N);
-        put_block(r1, er, dst + pairs / 2, key_of, slot, x.head, u * N + pairs);
-        return;
       }
       *reinterpret_cast<uint4*>(dst) = Vec<T>::put(r0);
       *reinterpret_cast<uint4*>(dst + (size_t)pairs * sizeof(T)) = Vec<T>::put(r1);
@@ -283,32 +259,15 @@ __global__ void __launch_bounds__(kRotThreads, !HALF && sizeof(T) == 4 && !AXES 
         r[2 * i + 2] = v[2 * i + 2] * f.z - v[2 * i + 3] * f.w;
         r[2 * i + 3] = v[2 * i + 3] * f.z + v[2 * i + 2] * f.w;
       }
-      if (FP4 && key_of >= 0) {
-        float er[N];
-#pragma unroll
-        for (int i = 0; i < N; i += 2) er[i] = er[i + 1] = (fabsf(v[i]) + fabsf(v[i + 1])) * off;
-        put_block(r, er, dst, key_of, slot, x.head, u * N);
-        return;
-      }
       *reinterpret_cast<uint4*>(dst) = Vec<T>::put(r);
     }
   };
   auto v_src = [&](int c) {
-    const int t = c / v_chunks;
+    const int t = KEYS ? c / v_chunks : 0;
     return reinterpret_cast<const uint4*>(a.v + (size_t)(t0 + t) * a.v_tok) + (c - t * v_chunks);
   };
   auto v_put = [&](int c, const uint4& w) {
-    const int t = c / v_chunks, slot = slots[t];
-    if (FP4) {
-      if (slot < 0) return;
-      const int e = (c - t * v_chunks) * N, head = e / a.d, e0 = e - head * a.d;
-      float x[N];
-      Vec<T>::get(w, x);
-      uint32_t codes, scale;
-      fp4_block<N>(x, a.gv, inv_gv, block_mask, codes, scale);
-      put_codes(a.v_dst + (size_t)slot * a.row_bytes + (size_t)head * a.d + e0 / 2, codes, scale, slot, head, 1, e0);
-      return;
-    }
+    const int t = KEYS ? c / v_chunks : 0, slot = slots[t];
     if (slot >= 0) reinterpret_cast<uint4*>(a.v_dst + (size_t)slot * a.row_bytes)[c - t * v_chunks] = w;
   };
 
@@ -320,7 +279,7 @@ __global__ void __launch_bounds__(kRotThreads, !HALF && sizeof(T) == 4 && !AXES 
   int k0, k1;
   load(g, u0, x0, k0);
   load(g + groups, u0, x1, k1);
-  if (a.k && tid < nt) {
+  if (KEYS && a.k && tid < nt) {
     const int slot = __ldg(a.out_loc + t0 + tid);
     const bool good = (unsigned)slot < (unsigned)a.num_slots;
     if (!good) set_error(a.err, KVP_ERR_BAD_INDEX);
@@ -347,6 +306,151 @@ __global__ void __launch_bounds__(kRotThreads, !HALF && sizeof(T) == 4 && !AXES 
       store(x1, u, k1);
     }
   }
+}
+
+template <typename T, bool HALF, bool AXES>
+__global__ void __launch_bounds__(kRotThreads, !HALF && sizeof(T) == 4 && !AXES ? 10 : 0) rotary_store_kernel(const RotArgs a) {
+  rotary_body<T, HALF, AXES, true>(a, blockIdx.x);
+}
+
+// Keys and values into a four-bit pool (fp4.cuh): a block takes up to four tokens. A thread has one place in a token's row
+// for all of them, a whole block of V (16 entries) or what the rotated form calls a unit of K. K's blocks lie in 16 / N neighbouring threads, which agree on the largest entry by shuffles.
+// The rotation's error (2^-21 of a pair's size; 2^-20 is reckoned with) leaves one rounding in some ten thousand open:
+// those entries are turned again to 52 bits, so that codes and scales are those of the 64-bit formula.
+template <typename T, bool HALF, bool AXES>
+__device__ __forceinline__ void fp4_body(const RotArgs& a, int block) {
+  constexpr int N = Vec<T>::N;
+  constexpr int PU = HALF ? N : N / 2;   // pairs of a unit
+  constexpr int kChunks = kFp4Block / N;  // of a block of V; also the threads of a block of K
+  constexpr int kMost = kChunks > 2 ? kChunks : 2;
+  __shared__ float4 cs[kRotMaxPairs / 2];  // laid out as in rotary_body
+  __shared__ int slots[kRotMaxTokens];
+  const int tid = threadIdx.x, t0 = block * a.kv_tokens, nt = min(a.kv_tokens, a.n - t0);
+  const int pairs = a.rot / 2, rot_units = HALF ? a.rot / (2 * N) : a.rot / N, units = rot_units + (a.d - a.rot) / N;
+  const int v_units = a.hk * (a.d / kFp4Block), all = v_units + a.hk * units;
+  const unsigned mask = ((1u << kChunks) - 1u) << (tid & 31 & ~(kChunks - 1));
+  const float inv_gk = 1.f / a.gk, inv_gv = 1.f / a.gv, off = fabsf(a.attn) * 0x1p-20f;
+
+  uint4 w[kMost];
+  // where a unit lies: head, first entry, whether it turns
+  auto place = [&](int x, int& h, int& u, int& e0) {
+    if (x < v_units) {
+      h = x / (a.d / kFp4Block);
+      u = x - h * (a.d / kFp4Block);
+      e0 = u * kFp4Block;
+    } else {
+      h = (x - v_units) / units;
+      u = x - v_units - h * units;
+      e0 = HALF && u >= rot_units ? a.rot + (u - rot_units) * N : u * N;
+    }
+  };
+  auto load = [&](int x, int t) {
+    int h, u, e0;
+    place(x, h, u, e0);
+    const size_t tok = (size_t)(t0 + t);
+    if (x < v_units) {
+      const uint4* src = reinterpret_cast<const uint4*>(a.v + tok * a.v_tok + ((size_t)h * a.d + e0) * sizeof(T));
+#pragma unroll
+      for (int i = 0; i < kChunks; ++i) w[i] = __ldg(src + i);
+    } else {
+      const char* src = a.k + tok * a.k_tok + ((size_t)h * a.d + e0) * sizeof(T);
+      w[0] = __ldg(reinterpret_cast<const uint4*>(src));
+      if (HALF && u < rot_units) w[1] = __ldg(reinterpret_cast<const uint4*>(src + (size_t)pairs * sizeof(T)));
+    }
+  };
+  if (tid < all) load(tid, 0);
+  if (tid < nt) {
+    const int slot = __ldg(a.out_loc + t0 + tid);
+    const bool good = (unsigned)slot < (unsigned)a.num_slots;
+    if (!good) set_error(a.err, KVP_ERR_BAD_INDEX);
+    slots[tid] = good ? slot : -1;
+  }
+  for (int x = tid; x < nt * pairs; x += kRotThreads) {
+    const int t = x / pairs, i = x - t * pairs;
+    const int u = i / PU, r = i % PU;
+    reinterpret_cast<float2*>(cs)[t * pairs + 2 * (r / 2 * rot_units + u) + (r & 1)] =
+        turn_of(AXES ? position_of<AXES>(a, (size_t)(t0 + t), i) : __ldg(a.positions + t0 + t), __ldg(a.freqs + i), a.attn);
+  }
+  __syncthreads();
+  for (int x = tid; x < all; x += kRotThreads) {
+    int h, u, e0;
+    place(x, h, u, e0);
+    for (int t = 0; t < nt; ++t) {
+      if (x != tid || t) load(x, t);
+      const int slot = slots[t];
+      if (slot < 0) continue;
+      char* row = a.k_dst + (size_t)slot * a.row_bytes + (size_t)h * a.d;
+      char* scales = a.scales + fp4_scale_offset(slot, h, a.hk, a.d);
+      uint32_t codes, scale;
+      if (x < v_units) {
+        float v[kFp4Block];
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) Vec<T>::get(w[i], v + N * i);
+        uint32_t lo, hi;
+        fp4_block16(v, a.gv, inv_gv, lo, hi, scale);
+        *reinterpret_cast<uint2*>(row + a.d / 2 + e0 / 2) = make_uint2(lo, hi);
+        scales[a.d / 16 + u] = (char)scale;
+        continue;
+      }
+      auto put = [&](int e) {
+        if (N == 8) *reinterpret_cast<uint32_t*>(row + e / 2) = codes;
+        else *reinterpret_cast<uint16_t*>(row + e / 2) = (uint16_t)codes;
+        if (e % kFp4Block == 0) scales[e / kFp4Block] = (char)scale;
+      };
+      float v[N];
+      Vec<T>::get(w[0], v);
+      if (u >= rot_units) {
+        fp4_block<N>(v, a.gk, inv_gk, mask, codes, scale);
+        put(e0);
+        continue;
+      }
+      const T* src = reinterpret_cast<const T*>(a.k + (size_t)(t0 + t) * a.k_tok) + (size_t)h * a.d;
+      const float4* f = cs + t * (pairs / 2) + u;
+      auto entry = [&](int e) { return exact_entry<T, AXES>(a, src, (size_t)(t0 + t), e, HALF); };
+      float er = 0.f;  // what the rotation may be off by, in any of the unit's entries
+      if (HALF) {
+        float y[N], r0[N], r1[N];
+        Vec<T>::get(w[1], y);
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+          const float4 c = f[i / 2 * rot_units];
+          r0[i] = v[i] * c.x - y[i] * c.y;
+          r1[i] = y[i] * c.x + v[i] * c.y;
+          r0[i + 1] = v[i + 1] * c.z - y[i + 1] * c.w;
+          r1[i + 1] = y[i + 1] * c.z + v[i + 1] * c.w;
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) er = fmaxf(er, fabsf(v[i]) + fabsf(y[i]));
+        er *= off;
+        fp4_block_within<N>(r0, er, a.gk, inv_gk, mask, [&](int i) { return entry(e0 + i); }, codes, scale);
+        put(e0);
+        fp4_block_within<N>(r1, er, a.gk, inv_gk, mask, [&](int i) { return entry(e0 + pairs + i); }, codes, scale);
+        put(e0 + pairs);
+      } else {
+        float r[N];
+#pragma unroll
+        for (int i = 0; i < N / 2; i += 2) {
+          const float4 c = f[i / 2 * rot_units];
+          r[2 * i] = v[2 * i] * c.x - v[2 * i + 1] * c.y;
+          r[2 * i + 1] = v[2 * i + 1] * c.x + v[2 * i] * c.y;
+          r[2 * i + 2] = v[2 * i + 2] * c.z - v[2 * i + 3] * c.w;
+          r[2 * i + 3] = v[2 * i + 3] * c.z + v[2 * i + 2] * c.w;
+        }
+#pragma unroll
+        for (int i = 0; i < N; i += 2) er = fmaxf(er, fabsf(v[i]) + fabsf(v[i + 1]));
+        er *= off;
+        fp4_block_within<N>(r, er, a.gk, inv_gk, mask, [&](int i) { return entry(e0 + i); }, codes, scale);
+        put(e0);
+      }
+    }
+  }
+}
+
+// A step into a four-bit pool in one launch: the first a.kv_blocks blocks have keys and values, the others queries.
+template <typename T, bool HALF, bool AXES>
+__global__ void __launch_bounds__(kRotThreads, 10) fp4_store_kernel(const __grid_constant__ RotArgs a) {
+  if ((int)blockIdx.x < a.kv_blocks) fp4_body<T, HALF, AXES>(a, blockIdx.x);
+  else rotary_body<T, HALF, AXES, false>(a, blockIdx.x - a.kv_blocks);
 }
 
 __device__ __forceinline__ float ld1(const float* p) { return *p; }
@@ -420,7 +524,7 @@ __global__ void __launch_bounds__(kRotThreads) fp4_store_elem_kernel(const __gri
       double m = 0.0;
   #pragma unroll 1
       for (int i = 0; i < kFp4Block; ++i) m = fmax(m, fabs(v[i]));
-      scale = fp4_scale_exact(m, g);
+      scale = fp4_scale_exact(m, g, 1.0 / g);
       const double sg = (double)e4m3_value(scale) * g;
   #pragma unroll 1
       for (int i = 0; scale && i < kFp4Block; ++i) {
@@ -438,15 +542,20 @@ __global__ void __launch_bounds__(kRotThreads) fp4_store_elem_kernel(const __gri
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-template <typename T, bool HALF, bool FP4>
-void launch_vec(const RotArgs& a, unsigned grid, cudaStream_t st) {
-  if (a.pair_axis) rotary_store_kernel<T, HALF, true, FP4><<<grid, kRotThreads, 0, st>>>(a);
-  else rotary_store_kernel<T, HALF, false, FP4><<<grid, kRotThreads, 0, st>>>(a);
+template <typename T, bool HALF>
+void launch_vec(const RotArgs& a, bool fp4, unsigned grid, cudaStream_t st) {
+  if (fp4) {
+    if (a.pair_axis) fp4_store_kernel<T, HALF, true><<<grid, kRotThreads, 0, st>>>(a);
+    else fp4_store_kernel<T, HALF, false><<<grid, kRotThreads, 0, st>>>(a);
+  } else {
+    if (a.pair_axis) rotary_store_kernel<T, HALF, true><<<grid, kRotThreads, 0, st>>>(a);
+    else rotary_store_kernel<T, HALF, false><<<grid, kRotThreads, 0, st>>>(a);
+  }
 }
-template <typename T, bool FP4>
-void launch_layout(const RotArgs& a, bool half, unsigned grid, cudaStream_t st) {
-  if (half) launch_vec<T, true, FP4>(a, grid, st);
-  else launch_vec<T, false, FP4>(a, grid, st);
+template <typename T>
+void launch_layout(const RotArgs& a, bool half, bool fp4, unsigned grid, cudaStream_t st) {
+  if (half) launch_vec<T, true>(a, fp4, grid, st);
+  else launch_vec<T, false>(a, fp4, grid, st);
 }
 template <typename T>
 void launch_elem(const RotArgs& a, bool half, cudaStream_t st) {
@@ -499,14 +608,15 @@ int launch_rotary(const kvp_pool* pool, RotArgs& a, int layout, cudaStream_t st)
   int tokens = 1;
   while (tokens < kRotMaxTokens && 2 * tokens * (a.rot / 2) <= kRotMaxPairs && a.n / (2 * tokens) >= pool->num_sms * 8) tokens *= 2;
   a.tokens = tokens;
-  const unsigned grid = (unsigned)(((long long)a.n + tokens - 1) / tokens);
-  if (es == 4) {
-    if (fp4) launch_layout<float, true>(a, half, grid, st);
-    else launch_layout<float, false>(a, half, grid, st);
-  } else {
-    if (fp4) launch_layout<__nv_bfloat16, true>(a, half, grid, st);
-    else launch_layout<__nv_bfloat16, false>(a, half, grid, st);
+  long long grid = fp4 && !a.q ? 0 : ((long long)a.n + tokens - 1) / tokens;
+  if (fp4) {
+    a.kv_tokens = tokens;
+    a.kv_blocks = (int)(((long long)a.n + tokens - 1) / tokens);
+    grid += a.kv_blocks;
+    if (grid > 0x7fffffffLL) return KVP_ERR_INVALID_ARG;
   }
+  if (es == 4) launch_layout<float>(a, half, fp4, (unsigned)grid, st);
+  else launch_layout<__nv_bfloat16>(a, half, fp4, (unsigned)grid, st);
   return cudaGetLastError() == cudaSuccess ? KVP_OK : KVP_ERR_CUDA;
 }
 
