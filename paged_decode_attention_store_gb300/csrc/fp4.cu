@@ -61,7 +61,7 @@ __device__ __forceinline__ void put8(__nv_bfloat16* dst, const float (&x)[8]) {
       make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
 }
 
-constexpr int kUnpackRows = 32;  // rows a block
+constexpr int kUnpackRows = 32;  // rows a block at most
 
 // Chunks: where a request's rows come from, and what the launches after this one read.
 struct Chunk {
@@ -86,7 +86,7 @@ struct Unpack {
   void* v;
   int32_t* err;
   const int32_t* slots;  // rows of these slots ...
-  int n, num_slots;
+  int n, num_slots, rows;  // ``rows`` a block
   Chunk ch;              // ... or of the requests' spans
 };
 
@@ -94,9 +94,9 @@ __device__ __forceinline__ bool request_ok(int L, int ql, int row, int C, int ma
   return ql >= 1 && ql <= C && L >= ql && L <= max_context && row >= 0 && row < rows_total;
 }
 
-// Rows back to full entries: a block takes 32 rows (slots first, all at once), a thread turns four code bytes into eight
-// entries at a time; a warp reads the 128 bytes of a head of 128 and writes 256 bytes of K and of V. Bytes bound it: 9 / 16
-// read and 2 written (bf16) an entry.
+// Rows back to full entries: a block takes up to 32 rows (their slots first, all at once). A thread has one word of four
+// code bytes of a row, or of several side by side, and turns it into eight entries, row after row; a warp reads the 128
+// bytes of a head of 128 and writes 256 bytes of K and of V. Bytes bound it: 9 / 16 read and 2 written (bf16) an entry.
 template <typename T, bool CHUNK>
 __global__ void __launch_bounds__(kLoadThreads) unpack_kernel(const __grid_constant__ Unpack a) {
   __shared__ int slots[kUnpackRows];
@@ -124,8 +124,8 @@ __global__ void __launch_bounds__(kLoadThreads) unpack_kernel(const __grid_const
     rows = min(kUnpackRows, L - t0);
     out0 = (size_t)b * s.page + t0;
   } else {
-    const long long i0 = (long long)blockIdx.x * kUnpackRows;
-    rows = (int)min((long long)kUnpackRows, a.n - i0);
+    const long long i0 = (long long)blockIdx.x * a.rows;
+    rows = (int)min((long long)a.rows, a.n - i0);
     if (tid < rows) {
       const int slot = __ldg(a.slots + i0 + tid);
       const bool good = (unsigned)slot < (unsigned)a.num_slots;
@@ -135,24 +135,31 @@ __global__ void __launch_bounds__(kLoadThreads) unpack_kernel(const __grid_const
     out0 = (size_t)i0;
   }
   __syncthreads();
-  const int words = a.d / 4, total = rows * a.heads * words;  // words of four code bytes, K's first in a head
+  const int words = a.d / 4, width = a.heads * words;  // words of four code bytes, K's first in a head
+  const int beside = width < kLoadThreads ? kLoadThreads / width : 1;
+  const int r0 = width < kLoadThreads ? tid / width : 0;
   bool nan = false;
+  if (r0 < beside)
+    for (int hw = tid - r0 * width; hw < width; hw += kLoadThreads) {
+      const int h = hw / words, w = hw - h * words, part = w >= words / 2, e0 = (w - part * (words / 2)) * 8;
+      const float g = part ? a.gv : a.gk;
+      T* dst = static_cast<T*>(part ? a.v : a.k) + (size_t)h * a.d + e0;
+      const uint8_t* scales = reinterpret_cast<const uint8_t*>(a.scales) + part * (a.d / 16) + e0 / 16;
 #pragma unroll 4
-  for (int u = tid; u < total; u += kLoadThreads) {
-    const int r = u / (a.heads * words), hw = u - r * (a.heads * words), h = hw / words, w = hw - h * words;
-    const int part = w >= words / 2, e0 = (w - part * (words / 2)) * 8, slot = slots[r];
-    float x[8] = {};
-    if (slot >= 0) {
-      const uint32_t c = __ldg(reinterpret_cast<const uint32_t*>(a.codes + (size_t)slot * row_entries) + hw);
-      const uint32_t s = __ldg(reinterpret_cast<const uint8_t*>(a.scales) + fp4_scale_offset(slot, h, a.heads, a.d) +
-                               part * (a.d / 16) + e0 / 16);
-      nan |= s == kFp4NanScale;
-      fp4_entries(c, s, part ? a.gv : a.gk, x);
-    } else if (CHUNK) {
-      continue;  // not attended, or a hole: nothing reads it, or what is read is unspecified
+      for (int r = r0; r < rows; r += beside) {
+        const int slot = slots[r];
+        float x[8] = {};
+        if (slot >= 0) {
+          const uint32_t c = __ldg(reinterpret_cast<const uint32_t*>(a.codes + (size_t)slot * row_entries) + hw);
+          const uint32_t s = __ldg(scales + fp4_scale_offset(slot, h, a.heads, a.d));
+          nan |= s == kFp4NanScale;
+          fp4_entries(c, s, g, x);
+        } else if (CHUNK) {
+          continue;  // not attended, or a hole: nothing reads it, or what is read is unspecified
+        }
+        put8(dst + (out0 + r) * row_entries, x);
+      }
     }
-    put8(static_cast<T*>(part ? a.v : a.k) + (out0 + r) * row_entries + (size_t)h * a.d + e0, x);
-  }
   if (CHUNK) {
     const int any = __syncthreads_or(nan);
     if (tid == 0) a.ch.nan[(size_t)blockIdx.y * a.ch.blocks + blockIdx.x] = any;
@@ -288,6 +295,12 @@ __global__ void __launch_bounds__(32 * kGenWarps) fp4_general_kernel(const __gri
 // Chunks: the requests with a scale NaN in their spans, all their query heads again.
 __global__ void __launch_bounds__(32 * kGenWarps)
     fp4_again_kernel(const __grid_constant__ GenArgs a, int B, const int32_t* lens, const int32_t* nan, int blocks) {
+  int any = 0;
+  for (long long u = threadIdx.x; u < (long long)B * blocks; u += blockDim.x) {
+    const int b = (int)(u / blocks), i = (int)(u - (long long)b * blocks);
+    if (i * kUnpackRows < lens[b]) any |= nan[u];
+  }
+  if (!__syncthreads_or(any)) return;
   for (int b = 0; b < B; ++b) {
     const int n = (lens[b] + kUnpackRows - 1) / kUnpackRows;
     int hit = 0;
@@ -430,7 +443,10 @@ extern "C" int load_cache_fp4(const kvp_pool* pool, int layer, const int32_t* sl
   Unpack u = unpack_args(pool, layer, k, v);
   u.slots = slots;
   u.n = n;
-  const unsigned grid = (unsigned)(((long long)n + kUnpackRows - 1) / kUnpackRows);
+  // as many rows a block as leave every SM eight blocks (64 rows by 32 at a time are two blocks, and 12 us)
+  u.rows = 1;
+  while (u.rows < kUnpackRows && n / (2 * u.rows) >= 8 * pool->num_sms) u.rows *= 2;
+  const unsigned grid = (unsigned)(((long long)n + u.rows - 1) / u.rows);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (pool->dtype == KVP_F32) unpack_kernel<float, false><<<grid, kLoadThreads, 0, st>>>(u);
   else unpack_kernel<__nv_bfloat16, false><<<grid, kLoadThreads, 0, st>>>(u);
