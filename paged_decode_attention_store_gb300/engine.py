@@ -33,6 +33,11 @@ def _align32(n):
     return (n + 31) // 32 * 32
 
 
+def _on_axes(positions, rope):
+    """Positions [n] as a plan takes them: those of text, the same on every axis."""
+    return positions if rope.axes == 1 else positions.expand(rope.axes, -1).contiguous()
+
+
 class PagedKVCache:
     def __init__(self, num_pages, page_size, kv_heads, head_dim, num_layers, dtype="bf16", max_requests=256,
                  table_mode="block", max_seq_len=None, free_stack=None, device="cuda", zero=True):
@@ -252,6 +257,46 @@ class PagedKVCache:
         if e != 0:
             raise kb.KvpError(e, "device")
 
+    def _append_and(self, work, rids, B, C, window, sinks):
+        """A step of B distinct requests, C new tokens each: append, then ``work(lens, rows, positions, out_loc)`` (int32 on
+        the device: contexts and table rows [B], positions and slots [B * C]), then the pages that the window leaves are
+        released. A step that is refused leaves the lengths and pages as they were."""
+        r = np.ascontiguousarray(rids, dtype=np.int32)
+        if len(r) != B or len(np.unique(r)) != B:
+            raise ValueError(f"step takes {B} distinct requests, got {list(map(int, r))}")
+        before = self.lengths[r].copy()
+        out_loc = self.append(np.repeat(r, C))
+        try:
+            flat = np.concatenate((before + C, r, (before[:, None] + np.arange(C)).ravel()))
+            d = self._to_device(flat)
+            work(d[:B], d[B:2 * B], d[2 * B:], out_loc)
+        except Exception:
+            for rid in r[::-1]:  # the last page taken goes back first
+                self.rewind(int(rid), C)
+            raise
+        if window and window > 0:
+            for i, rid in enumerate(r):
+                self.trim(int(rid), max(0, int(before[i]) + C + 1 - (window - sinks)), sinks=sinks)
+
+    def _slots_in_order(self, rids):
+        """The slots of requests ``rids`` in logical order, int64 [total], and their offsets int32 [len(rids) + 1]. A
+        request that a window has taken pages from has no such rows left (ValueError). Waits for the GPU, to see that."""
+        r = np.ascontiguousarray(rids, dtype=np.int32)
+        lens = self.lengths[r]
+        some = lens > 0
+        n = int(some.sum())
+        d = self._to_device(np.concatenate((lens[some], r[some], [0], np.cumsum(lens))))
+        start = d[2 * n:]
+        if n == 0:
+            return torch.empty(0, dtype=torch.int64, device=self.dev), start
+        slots = torch.empty((n, int(lens.max())), dtype=torch.int32, device=self.dev)
+        kb.gather_indices(self.pool, self.table, self.table_mode, d[:n], 0, slots, table_rows=d[n:2 * n])
+        live = torch.arange(slots.shape[1], device=self.dev)[None, :] < d[:n, None]
+        slots = slots[live].long()
+        if bool((slots < 0).any()):
+            kb.kvp_sync_error(self.pool)  # what the gather recorded of it
+            raise ValueError("a request's first pages are released")
+        return slots, start
 
     # -- one decode step, host buffers in and out ----------------------------
     def decode_step(self, rids, q, k, v, out, window, scale, sinks=0):
@@ -425,26 +470,15 @@ class PagedLatentCache(PagedKVCache):
         afterwards. A step that is refused leaves the lengths and pages as they
         were. Asynchronous on the current stream."""
         B, C, Hq, W = q[0].shape
-        r = np.ascontiguousarray(rids, dtype=np.int32)
-        if len(r) != B or len(np.unique(r)) != B:
-            raise ValueError(f"step takes {B} distinct requests, got {list(map(int, r))}")
-        before = self.lengths[r].copy()
-        out_loc = self.append(np.repeat(r, C))
-        try:
-            flat = np.concatenate((before + C, r, (before[:, None] + np.arange(C)).ravel()))
-            d = self._to_device(flat)
-            lens, rows, positions = d[:B], d[B:2 * B], d[2 * B:]
+
+        def work(lens, rows, positions, out_loc):
+            positions = _on_axes(positions, rope)
             for layer in range(self.layers):
                 self.store(layer, q_pe[layer].view(B * C, Hq, self.rope_dim), latent[layer], k_pe[layer], positions,
                            out_loc, rope, q[layer].view(B * C, Hq, W))
                 self.attend(layer, q[layer], lens, window, scale, out[layer], table_rows=rows, sinks=sinks)
-        except Exception:
-            for rid in r[::-1]:  # the last page taken goes back first
-                self.rewind(int(rid), C)
-            raise
-        if window and window > 0:
-            for i, rid in enumerate(r):
-                self.trim(int(rid), max(0, int(before[i]) + C + 1 - (window - sinks)), sinks=sinks)
+
+        self._append_and(work, rids, B, C, window, sinks)
 
     def rows(self, layer, rids):
         """The stored rows of requests ``rids`` in logical order, [total,
@@ -452,21 +486,7 @@ class PagedLatentCache(PagedKVCache):
         the projections of the expanded form take. A request that a window
         has taken pages from has no such rows left (ValueError). Waits for the
         GPU, to see that; not for capture into a graph."""
-        r = np.ascontiguousarray(rids, dtype=np.int32)
-        lens = self.lengths[r]
-        some = lens > 0
-        n = int(some.sum())
-        d = self._to_device(np.concatenate((lens[some], r[some], [0], np.cumsum(lens))))
-        start = d[2 * n:]
-        if n == 0:
-            return self.kv[layer].view(-1, self.D)[:0], start
-        slots = torch.empty((n, int(lens.max())), dtype=torch.int32, device=self.dev)
-        kb.gather_indices(self.pool, self.table, self.table_mode, d[:n], 0, slots, table_rows=d[n:2 * n])
-        live = torch.arange(slots.shape[1], device=self.dev)[None, :] < d[:n, None]
-        slots = slots[live].long()
-        if bool((slots < 0).any()):
-            kb.kvp_sync_error(self.pool)  # what the gather recorded of it
-            raise ValueError("a request's first pages are released")
+        slots, start = self._slots_in_order(rids)
         return self.kv[layer].view(-1, self.D)[slots], start
 
     def _unsupported(self, what):
@@ -489,6 +509,122 @@ class PagedLatentCache(PagedKVCache):
 
     def decode_step(self, *args, **kwargs):
         self._unsupported("decode_step")
+
+
+class PagedFp4Cache(PagedKVCache):
+    """A paged cache of K and V in four bits (binding.Fp4Pool: a code of four
+    bits an entry, a scale for 16 of them), with the page bookkeeping of
+    :class:`PagedKVCache` (new, fork, append with copy-on-write, trim, rewind,
+    release). ``dtype`` is that of queries, keys, values and outputs;
+    ``k_scale`` and ``v_scale`` (powers of two, one or one a layer) place the
+    range of the scales.
+
+    :meth:`rotary_store` or :meth:`store` round a step's keys and values as they
+    are stored; :meth:`attend`, :meth:`verify` and :meth:`prefill` read them in
+    place; :meth:`step` is a whole step. All calls of a cache share a workspace:
+    they, and replays of graphs that hold them, run one after another on the GPU
+    (calls that overlap take their own: :func:`binding.paged_fp4_attention`)."""
+
+    def __init__(self, num_pages, page_size, kv_heads, head_dim, num_layers, dtype="bf16", max_requests=256,
+                 table_mode="block", max_seq_len=None, free_stack=None, device="cuda", zero=True, k_scale=1.0, v_scale=1.0):
+        self.k_scale, self.v_scale = k_scale, v_scale
+        super().__init__(num_pages, page_size, kv_heads, head_dim, num_layers, dtype=dtype, max_requests=max_requests,
+                         table_mode=table_mode, max_seq_len=max_seq_len, free_stack=free_stack, device=device, zero=zero)
+        self._need, self._largest = {}, 0
+
+    def _make_pool(self, alloc, pages, kdt):
+        self.pool = kb.kv_fp4_pool_create(pages, self.P, self.Hkv, self.D, kdt, self.layers, self.k_scale, self.v_scale,
+                                          device=self.dev, zero=alloc is torch.zeros)
+        self.codes, self.block_scales = self.pool.codes, self.pool.scales
+
+    def store(self, layer, k, v, out_loc):
+        """k, v [n, Hkv, D] as they are, rounded to four bits."""
+        kb.store_cache_fp4(self.pool, layer, k, v, out_loc)
+
+    def rotary_store(self, layer, q, k, v, positions, out_loc, rope, q_out=None):
+        """Rotary positions of q and k and the store of the rotated k and of v
+        in four bits, in one launch; returns the rotated q (``q_out``, or q
+        itself when it is None). As :meth:`PagedKVCache.rotary_store`."""
+        q_out = q if q_out is None else q_out
+        kb.rotary_store_fp4(self.pool, layer, q, k, v, positions, out_loc, rope, q_out)
+        return q_out
+
+    def workspace(self, batch, num_q_heads, chunk=1, max_context=1):
+        """The cache's workspace, for calls of this shape among others: one that grows, by powers of two. Outgrown ones are
+        kept, as a captured graph may hold them: all together they are no larger than the last."""
+        key = (batch, num_q_heads, chunk, max_context)
+        need = self._need.get(key)
+        if need is None:
+            if len(self._need) > 4096:
+                self._need.clear()
+            need = self._need[key] = kb.paged_fp4_attention_workspace_size(self.pool, batch, chunk, num_q_heads, max_context)
+        if need > self._largest:
+            self._largest = 1 << (need - 1).bit_length()
+            self._ws[self._largest] = torch.empty(self._largest, dtype=torch.uint8, device=self.dev)
+        return self._ws[self._largest]
+
+    def attend(self, layer, q, context_lens, window, scale, out, q_lens=None, table_rows=None, sinks=0, max_context=None):
+        """Attention over the stored rows: q, out [B, Hq, D] (one token a
+        request) or [B, C, Hq, D], query j of request b at position
+        context_lens[b] - q_lens[b] + j (q_lens None: C). ``max_context``: a
+        bound of context_lens; None: the longest request's length so far, in
+        steps of 256 (a graph that is replayed with longer contexts gives
+        theirs)."""
+        if q.dim() == 3:
+            q, out = q[:, None], out[:, None]
+        if max_context is None:
+            max_context = max(1, -(-int(self.lengths.max()) // 256)) * 256
+        ws = self.workspace(q.shape[0], q.shape[2], q.shape[1], max_context)
+        kb.paged_fp4_attention(self.pool, layer, q, self.table, self.table_mode, context_lens, window, scale, out, ws,
+                               q_lens=q_lens, table_rows=table_rows, sinks=sinks, max_context=max_context)
+
+    def verify(self, layer, q, context_lens, window, scale, out, table_rows=None, sinks=0):
+        self.attend(layer, q, context_lens, window, scale, out, table_rows=table_rows, sinks=sinks)
+
+    def prefill(self, layer, q, context_lens, window, scale, out, q_lens=None, table_rows=None, sinks=0):
+        self.attend(layer, q, context_lens, window, scale, out, q_lens=q_lens, table_rows=table_rows, sinks=sinks)
+
+    def step(self, rids, q, k, v, rope, out, window, scale, sinks=0, positions=None):
+        """One step for requests ``rids``, all layers, C new tokens each (C = 1:
+        decode): append, then per layer rotate, store and attend. Per-layer
+        device tensors: ``q`` (rotated in place) and ``out`` [B, C, Hq, D],
+        ``k``, ``v`` [B * C, Hkv, D] (request-major). ``positions``: int32 [B * C],
+        or [axes, B * C] for a plan of several axes; None: the tokens' places in
+        their requests, on every axis. ``rope`` None: q and k as they are. With a
+        window, the pages it leaves are released afterwards. A step that is
+        refused leaves the lengths and pages as they were. Asynchronous on the
+        current stream."""
+        B, C, Hq, D = q[0].shape
+
+        def work(lens, rows, places, out_loc):
+            pos = positions
+            if rope is not None and pos is None:
+                pos = _on_axes(places, rope)
+            for layer in range(self.layers):
+                if rope is None:
+                    self.store(layer, k[layer], v[layer], out_loc)
+                else:
+                    self.rotary_store(layer, q[layer].view(B * C, Hq, D), k[layer], v[layer], pos, out_loc, rope)
+                self.attend(layer, q[layer], lens, window, scale, out[layer], table_rows=rows, sinks=sinks)
+
+        self._append_and(work, rids, B, C, window, sinks)
+
+    def rows(self, layer, rids):
+        """K and V of requests ``rids`` in logical order, [total, Hkv, D] each,
+        as the values that the four bits stand for, and their offsets int32
+        [len(rids) + 1]. A request that a window has taken pages from has no
+        such rows left (ValueError). Waits for the GPU, to see that; not for
+        capture into a graph."""
+        slots, start = self._slots_in_order(rids)
+        k, v = (torch.empty((slots.numel(), self.Hkv, self.D), dtype=self.tdt, device=self.dev) for _ in range(2))
+        kb.load_cache_fp4(self.pool, layer, slots.to(torch.int32), k, v)
+        return k, v, start
+
+    def store_and_attend(self, *args, **kwargs):
+        raise TypeError("a four-bit cache stores, then attends: store or rotary_store, then attend, or step")
+
+    def decode_step(self, *args, **kwargs):
+        raise TypeError("a four-bit cache steps through step (or prefill_step and verify_step for host tensors)")
 
 
 class DevicePagedKVCache:
