@@ -396,9 +396,14 @@ kvp_pool chunk_pool(const kvp_pool* pool, int B, const ChunkLayout& l, char* ws)
   return p;
 }
 
-// Whether a call goes through the chunk kernel of bf16 pools. Few (token, head) columns a KV head are the decode kernel's.
+// Whether a call goes through the chunk kernel of bf16 pools. Up to 64 (token, head) columns a KV head are the decode
+// kernel's, which splits contexts over the SMs; it takes up to 128, and above 64 a CTA has one KV head alone. 64 requests of
+// 512-4096 rows, 8 KV heads, decode kernel against chunk kernel: 64 columns 229 and 348 us, 96 397 and 347. Where the chunk
+// kernel would have less than a CTA an SM, the decode kernel keeps them all: 4 requests, 128 columns 36 and 46 us.
 bool chunk_eligible(const kvp_pool* pool, int B, int C, int H, int longest, float scale) {
-  if ((long long)C * (H / pool->kv_heads) <= kChunkColumns && fp4_tc_eligible(pool, C, H)) return false;
+  const long long columns = (long long)C * (H / pool->kv_heads);
+  const bool few = columns <= kChunkColumns || (long long)B * pool->kv_heads < pool->num_sms;
+  if (few && fp4_tc_eligible(pool, C, H)) return false;
   return pool->dtype == KVP_BF16 && (long long)B * (((long long)longest + 15) / 16 * 16) <= 0x7fffffffLL && B <= 65535 &&
          prefill_tc_eligible(pool, H, C, scale);
 }
