@@ -70,7 +70,7 @@ struct Chunk {
   const int32_t* q_lens;
   const int32_t* table_rows;
   int C, window, sinks, max_context;
-  int blocks;      // of kUnpackRows positions, max_context in all
+  int blocks;      // of Unpack::rows positions, max_context in all
   long long page;  // rows of a request's page in the workspace
   int32_t* lens;   // [B] context lengths, 0 for invalid requests
   int32_t* table;  // [B] page b
@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(kLoadThreads) unpack_kernel(const __grid_const
   int rows;
   if (CHUNK) {
     const Chunk& s = a.ch;
-    const int b = blockIdx.y, t0 = blockIdx.x * kUnpackRows;
+    const int b = blockIdx.y, t0 = blockIdx.x * a.rows;
     const int L = __ldg(s.context_lens + b), ql = s.q_lens ? __ldg(s.q_lens + b) : s.C;
     const int row = s.table_rows ? __ldg(s.table_rows + b) : b;
     const bool ok = request_ok(L, ql, row, s.C, s.max_context, s.T.rows_total);
@@ -117,11 +117,11 @@ __global__ void __launch_bounds__(kLoadThreads) unpack_kernel(const __grid_const
     if (!ok || t0 >= L) return;
     const int wide = s.window > 0 && ql - 1 < 0x7fffffff - s.window ? s.window + ql - 1 : 0;
     const Span u = attend_span(L, wide, s.sinks);
-    if (tid < kUnpackRows) {
+    if (tid < a.rows) {
       const int t = t0 + tid;
       slots[tid] = t < L && (t >= u.lo || t < u.se) ? resolve_slot(s.T, row, t, a.err) : -1;
     }
-    rows = min(kUnpackRows, L - t0);
+    rows = min(a.rows, L - t0);
     out0 = (size_t)b * s.page + t0;
   } else {
     const long long i0 = (long long)blockIdx.x * a.rows;
@@ -294,15 +294,15 @@ __global__ void __launch_bounds__(32 * kGenWarps) fp4_general_kernel(const __gri
 
 // Chunks: the requests with a scale NaN in their spans, all their query heads again.
 __global__ void __launch_bounds__(32 * kGenWarps)
-    fp4_again_kernel(const __grid_constant__ GenArgs a, int B, const int32_t* lens, const int32_t* nan, int blocks) {
+    fp4_again_kernel(const __grid_constant__ GenArgs a, int B, const int32_t* lens, const int32_t* nan, int blocks, int rows) {
   int any = 0;
   for (long long u = threadIdx.x; u < (long long)B * blocks; u += blockDim.x) {
     const int b = (int)(u / blocks), i = (int)(u - (long long)b * blocks);
-    if (i * kUnpackRows < lens[b]) any |= nan[u];
+    if ((long long)i * rows < lens[b]) any |= nan[u];
   }
   if (!__syncthreads_or(any)) return;
   for (int b = 0; b < B; ++b) {
-    const int n = (lens[b] + kUnpackRows - 1) / kUnpackRows;
+    const int n = lens[b] == 0 ? 0 : (lens[b] - 1) / rows + 1;
     int hit = 0;
     for (int i = threadIdx.x; i < n; i += blockDim.x) hit |= nan[(size_t)b * blocks + i];
     if (!__syncthreads_or(hit)) continue;
@@ -363,17 +363,19 @@ Unpack unpack_args(const kvp_pool* pool, int layer, void* k, void* v) {
 // A chunk's workspace for B requests of up to ``longest`` rows.
 struct ChunkLayout {
   long long page;  // rows of a request
-  int blocks;
+  int rows, blocks;  // positions a block takes, blocks of a request
   size_t lens, table, nan, kv, plane, total;
 };
 ChunkLayout chunk_layout(const kvp_pool* pool, int B, int longest) {
   ChunkLayout l;
   l.page = ((long long)longest + 15) / 16 * 16;
-  l.blocks = (longest - 1) / kUnpackRows + 1;
+  l.rows = kUnpackRows;  // fewer where that would be less than eight blocks an SM (6,000 rows of 8 heads by 32 at a time: 21 us, by 4: 9)
+  while (l.rows > 2 && (long long)B * longest / l.rows < 8 * pool->num_sms) l.rows /= 2;
+  l.blocks = (longest - 1) / l.rows + 1;
   l.lens = 0;
   l.table = align256(sizeof(int32_t) * (size_t)B);
   l.nan = align256(l.table + sizeof(int32_t) * (size_t)B);
-  l.kv = align256(l.nan + sizeof(int32_t) * (size_t)B * l.blocks);
+  l.kv = align256(l.nan + sizeof(int32_t) * (size_t)B * (l.page / 2));  // for any ``rows``: larger calls' workspaces fit
   l.plane = (size_t)B * l.page * pool->kv_heads * pool->head_dim * 2;
   l.total = l.kv + 2 * l.plane;
   return l;
@@ -419,12 +421,13 @@ int launch_chunk(const Fp4Call& c, int longest, cudaStream_t st) {
   Unpack u = unpack_args(pool, c.layer, ws + l.kv, ws + l.kv + l.plane);
   u.ch = {c.T, c.context_lens, c.q_lens, c.table_rows, c.C, c.window, c.sinks, c.max_context, l.blocks, l.page, lens, table,
           nan};
+  u.rows = l.rows;
   unpack_kernel<__nv_bfloat16, true><<<dim3(l.blocks, c.B), kLoadThreads, 0, st>>>(u);
   if (cudaGetLastError() != cudaSuccess) return KVP_ERR_CUDA;
   const int rc = launch_prefill_tc(&rows, 0, c.q, c.B, c.C, c.H, c.q_lens, make_table(&rows, table, c.B, 1, KVP_BLOCK_TABLE),
                                    nullptr, lens, c.window, c.sinks, c.scale, c.out, st);
   if (rc != KVP_OK) return rc;
-  fp4_again_kernel<<<2 * pool->num_sms, 32 * kGenWarps, 0, st>>>(general_args(c), c.B, lens, nan, l.blocks);
+  fp4_again_kernel<<<2 * pool->num_sms, 32 * kGenWarps, 0, st>>>(general_args(c), c.B, lens, nan, l.blocks, l.rows);
   return cudaGetLastError() == cudaSuccess ? KVP_OK : KVP_ERR_CUDA;
 }
 

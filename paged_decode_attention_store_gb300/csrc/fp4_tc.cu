@@ -958,9 +958,27 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_decode_kernel(const __grid_co
   else consume<NT>(a, s, pl, warp, lane);
 }
 
-// Joins the pieces of a cut request, in CTA order: a block a column at a time, its four warps a quarter of the pieces each,
-// in order and six loads on their way at a time, then the quarters in order.
+// Joins the pieces of a cut request, in CTA order, six loads on their way at a time: a warp a column, or, of more pieces, a
+// block a column, its four warps a quarter of the pieces each, then the quarters in order.
 constexpr int kJoin = 6;
+struct Joined {
+  float4 o;
+  float m, l;
+};
+__device__ __forceinline__ void join(Joined& j, float m, float l, const float4& o) {
+  const float w = ex2(m - j.m);
+  j.l += w * l;
+  j.o.x += w * o.x;
+  j.o.y += w * o.y;
+  j.o.z += w * o.z;
+  j.o.w += w * o.w;
+}
+__device__ __forceinline__ void raise(Joined& j, float m) {
+  const float al = ex2(j.m - m);
+  j.m = m;
+  j.l *= al;
+  j.o = make_float4(j.o.x * al, j.o.y * al, j.o.z * al, j.o.w * al);
+}
 __global__ void __launch_bounds__(128, 8) fp4_combine_kernel(const __grid_constant__ Args a) {
   __shared__ float4 sum[4][32];
   __shared__ float2 weight[4];  // a quarter's maximum and sum
@@ -968,14 +986,17 @@ __global__ void __launch_bounds__(128, 8) fp4_combine_kernel(const __grid_consta
   const int4 mg = a.merge[blockIdx.x];
   if (mg.x < 0) return;
   const int b = mg.x / a.n_groups, grp = mg.x % a.n_groups, C = a.C * a.G, cols = a.HG * C;
-  const int lane = threadIdx.x & 31, quarter = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int ql = a.q_lens ? __ldg(a.q_lens + b) : a.C, pieces = 1 + mg.w - mg.y;
-  const int per = (pieces + 3) / 4, i0 = min(pieces, quarter * per), i1 = min(pieces, i0 + per);
-  for (int u = blockIdx.y; u < cols; u += gridDim.y) {
-    const int h = u / C, col = u % C, cj = a.C == 1 ? 0 : col / a.G;
+  const bool alone = pieces <= kJoin;  // a warp has a column's pieces
+  const int per = alone ? pieces : (pieces + 3) / 4;
+  const int i0 = alone ? 0 : min(pieces, warp * per), i1 = min(pieces, i0 + per), beside = alone ? 4 : 1;
+  for (int u0 = blockIdx.y * beside; u0 < cols; u0 += gridDim.y * beside) {
+    const int u = alone ? u0 + warp : u0;
+    if (u >= cols) break;
+    const int h = u / C, col = u - h * C, cj = a.C == 1 ? 0 : col / a.G;
     if (cj >= ql) continue;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float L = 0.f, M = -3.0e38f;
+    Joined j = {make_float4(0.f, 0.f, 0.f, 0.f), -3.0e38f, 0.f};
     for (int i = i0; i < i1; i += kJoin) {
       float2 ml[kJoin];
       float4 v[kJoin];
@@ -989,49 +1010,30 @@ __global__ void __launch_bounds__(128, 8) fp4_combine_kernel(const __grid_consta
           v[y] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * kD) + lane);
         }
       }
-      float mn = M;
+      float mn = j.m;
 #pragma unroll
       for (int y = 0; y < kJoin; ++y) mn = fmaxf(mn, ml[y].x);
-      const float al = ex2(M - mn);
-      M = mn;
-      L *= al;
-      acc = make_float4(acc.x * al, acc.y * al, acc.z * al, acc.w * al);
+      raise(j, mn);
 #pragma unroll
-      for (int y = 0; y < kJoin; ++y) {
-        const float wgt = ex2(ml[y].x - M);
-        L += wgt * ml[y].y;
-        acc.x += wgt * v[y].x;
-        acc.y += wgt * v[y].y;
-        acc.z += wgt * v[y].z;
-        acc.w += wgt * v[y].w;
-      }
+      for (int y = 0; y < kJoin; ++y) join(j, ml[y].x, ml[y].y, v[y]);
     }
-    sum[quarter][lane] = acc;
-    if (lane == 0) weight[quarter] = make_float2(M, L);
-    __syncthreads();
-    if (quarter == 0) {
-      float mn = M;
+    if (!alone) {
+      sum[warp][lane] = j.o;
+      if (lane == 0) weight[warp] = make_float2(j.m, j.l);
+      __syncthreads();
+      if (warp == 0) {
+        raise(j, fmaxf(fmaxf(j.m, weight[1].x), fmaxf(weight[2].x, weight[3].x)));
 #pragma unroll
-      for (int i = 1; i < 4; ++i) mn = fmaxf(mn, weight[i].x);
-      const float al = ex2(M - mn);
-      L *= al;
-      acc = make_float4(acc.x * al, acc.y * al, acc.z * al, acc.w * al);
-#pragma unroll
-      for (int i = 1; i < 4; ++i) {
-        const float wgt = ex2(weight[i].x - mn);
-        const float4 v = sum[i][lane];
-        L += wgt * weight[i].y;
-        acc.x += wgt * v.x;
-        acc.y += wgt * v.y;
-        acc.z += wgt * v.z;
-        acc.w += wgt * v.w;
+        for (int i = 1; i < 4; ++i) join(j, weight[i].x, weight[i].y, sum[i][lane]);
       }
-      const float inv = L == 0.f ? 0.f : a.gv / L;
+      __syncthreads();
+    }
+    if (alone || warp == 0) {
+      const float inv = j.l == 0.f ? 0.f : a.gv / j.l;
       uint2* dst = reinterpret_cast<uint2*>(
           a.out + (((size_t)b * a.C + cj) * a.Hq + (size_t)(grp * a.HG + h) * a.G + col - cj * a.G) * kD) + lane;
-      *dst = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+      *dst = make_uint2(pack_bf16(j.o.x * inv, j.o.y * inv), pack_bf16(j.o.z * inv, j.o.w * inv));
     }
-    __syncthreads();
   }
 }
 
