@@ -52,7 +52,8 @@ int pool_create(int num_pages, int page_size, int kv_heads, int head_dim, int la
   p->fp4_scales = nullptr;
   p->fp4_scale_layer_bytes = 0;
   p->fp4_globals = nullptr;
-  p->fp4_map_hg = 0;
+  memset(p->fp4_map, 0, sizeof(p->fp4_map));
+  memset(p->fp4_map_state, 0, sizeof(p->fp4_map_state));
   *out = p;
   return KVP_OK;
 }

@@ -39,8 +39,8 @@ struct kvp_pool {
   char* fp4_scales;     // four-bit pools: block scales, (layers, ceil(slots / 16), kv_heads, 16, 2, head_dim / 16)
   size_t fp4_scale_layer_bytes;
   float* fp4_globals;   // host [2 * num_layers]: layer l's K scale at l, its V scale at num_layers + l (powers of two)
-  CUtensorMap fp4_map;  // the codes as (byte of a head, slot, head, layer), box (128, 16, HG, 1)
-  int fp4_map_hg;       // heads per box it was encoded for (0: none yet, -HG: refused for HG)
+  CUtensorMap fp4_map[8];  // the codes as (byte of a head, slot, head, layer), box (128, 16, HG, 1), by HG - 1
+  int fp4_map_state[8];    // 0: not encoded yet, 1: encoded, -1: refused
 
   // K and V planes of full elements: what the calls that are not for latent or four-bit pools take.
   bool kv_rows() const { return !latent_dim && !fp4; }

@@ -40,7 +40,7 @@
 #include <cuda_fp16.h>
 #include <cudaTypedefs.h>
 
-#include <cstring>
+#include <mutex>
 
 #include "attention.cuh"
 #include "fp4.cuh"
@@ -57,7 +57,8 @@ constexpr int kMaxStages = 6;
 constexpr int kMaxConsumers = 8;
 constexpr int kThreads = 32 * (kMaxConsumers + kMaxConsumers / 2);
 constexpr uint64_t kWaitNs = 2000000000ull;
-constexpr size_t kSmemPerSm = 227 * 1024;  // what the CTAs of an SM share, 1 KB of each one's is the system's
+constexpr size_t kSmemPerSm = 227 * 1024;  // what the CTAs of an SM share
+constexpr size_t kSmemRest = 2048;         // of each: 1 KB is the system's, the rest the kernel's static part
 
 struct Args {
   CUtensorMap map;  // codes as (byte of a head, slot, head, layer), box (128, 16, HG, 1), 128-byte swizzle
@@ -1054,7 +1055,7 @@ bool shape_for(const kvp_pool* pool, int C, int H, Shape* o) {
   o->PW = o->CW > 4 ? 4 : o->CW > 2 ? 2 : 1;
   o->ctas_per_sm = kThreads / 32 / (o->CW + o->PW);  // twelve warps an SM, 168 registers a thread
   o->stages = kMaxStages;
-  while (o->stages > 2 && smem_bytes(o->HG, o->stages, o->CW, o->NT) + 2048 > kSmemPerSm / o->ctas_per_sm) --o->stages;
+  while (o->stages > 2 && smem_bytes(o->HG, o->stages, o->CW, o->NT) + kSmemRest > kSmemPerSm / o->ctas_per_sm) --o->stages;
   return true;
 }
 
@@ -1105,11 +1106,14 @@ int launch_fp4_tc(const Fp4Call& c, cudaStream_t stream) {
   const Layout lay = layout_for(pool, sh, c.C, c.H);
   char* ws = static_cast<char*>(c.workspace);
   Args a;
-  if (pool->fp4_map_hg != sh.HG && pool->fp4_map_hg != -sh.HG)
-    pool->fp4_map_hg = encode_map(pool, sh.HG, &pool->fp4_map) ? sh.HG : -sh.HG;
-  a.use_map = pool->fp4_map_hg == sh.HG;
-  if (a.use_map) a.map = pool->fp4_map;
-  else memset(&a.map, 0, sizeof(a.map));
+  {
+    static std::mutex encoding;  // host threads may call at once, with other shapes
+    std::lock_guard<std::mutex> lock(encoding);
+    int& state = pool->fp4_map_state[sh.HG - 1];
+    if (state == 0) state = encode_map(pool, sh.HG, &pool->fp4_map[sh.HG - 1]) ? 1 : -1;
+    a.use_map = state == 1;
+    a.map = pool->fp4_map[sh.HG - 1];
+  }
   a.layer = c.layer;
   a.T = c.T;
   a.codes = pool->buf + (size_t)c.layer * pool->layer_bytes;
@@ -1143,8 +1147,8 @@ int launch_fp4_tc(const Fp4Call& c, cudaStream_t stream) {
   a.part_o = reinterpret_cast<float*>(ws + lay.o);
   a.err = pool->err;
   auto kernel = sh.NT == 1 ? fp4_decode_kernel<1> : fp4_decode_kernel<2>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes(sh.HG, sh.stages, sh.CW, sh.NT)) !=
-      cudaSuccess)
+  // the most that a shape takes, whatever this one does: host threads may call at once, with other shapes
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(kSmemPerSm - kSmemRest)) != cudaSuccess)
     return KVP_ERR_CUDA;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
