@@ -211,4 +211,6 @@ struct Fp4Call {
 bool fp4_tc_eligible(const kvp_pool* pool, int C, int H);
 size_t fp4_tc_workspace(const kvp_pool* pool, int C, int H);
 int launch_fp4_tc(const Fp4Call& c, cudaStream_t stream);
+// Every other shape of a bf16 pool (fp4_tile.cu).
+int launch_fp4_tile(const Fp4Call& c, cudaStream_t stream);
 }  // namespace kvp

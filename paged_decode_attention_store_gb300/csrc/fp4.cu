@@ -287,9 +287,8 @@ __device__ void general_item(const GenArgs& a, int item) {
   }
 }
 
-template <typename T>
 __global__ void __launch_bounds__(32 * kGenWarps) fp4_general_kernel(const __grid_constant__ GenArgs a) {
-  general_item<T>(a, blockIdx.x);
+  general_item<float>(a, blockIdx.x);
 }
 
 // Chunks: the requests with a scale NaN in their spans, all their query heads again.
@@ -340,8 +339,7 @@ GenArgs general_args(const Fp4Call& c) {
 int launch_general(const Fp4Call& c, cudaStream_t st) {
   const GenArgs g = general_args(c);
   const unsigned grid = (unsigned)((long long)c.B * c.C * c.H);
-  if (c.pool->dtype == KVP_F32) fp4_general_kernel<float><<<grid, 32 * kGenWarps, 0, st>>>(g);
-  else fp4_general_kernel<__nv_bfloat16><<<grid, 32 * kGenWarps, 0, st>>>(g);
+  fp4_general_kernel<<<grid, 32 * kGenWarps, 0, st>>>(g);
   return cudaGetLastError() == cudaSuccess ? KVP_OK : KVP_ERR_CUDA;
 }
 
@@ -470,7 +468,7 @@ extern "C" int paged_fp4_attention_workspace_size(const kvp_pool* pool, int batc
     const size_t rows = chunk_layout(pool, batch, max_context).total;
     if (rows > need) need = rows;
   }
-  *bytes = need ? need : 256;  // the general kernel needs none
+  *bytes = need ? need : 256;  // the other kernels need none
   return KVP_OK;
 }
 
@@ -511,5 +509,6 @@ extern "C" int paged_fp4_attention(const kvp_pool* pool, int layer, const void* 
   c.workspace = workspace;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (chunk_eligible(pool, batch, chunk, num_q_heads, max_context, scale)) return launch_chunk(c, max_context, st);
-  return fp4_tc_eligible(pool, chunk, num_q_heads) ? launch_fp4_tc(c, st) : launch_general(c, st);
+  if (fp4_tc_eligible(pool, chunk, num_q_heads)) return launch_fp4_tc(c, st);
+  return pool->dtype == KVP_BF16 ? launch_fp4_tile(c, st) : launch_general(c, st);
 }
