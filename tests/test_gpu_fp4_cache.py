@@ -162,3 +162,20 @@ def test_a_refused_step_leaves_the_cache(kb):
         s.cache.decode_step([0], None, None, None, None, 0, 1.0)
     with pytest.raises(TypeError):
         s.cache.store_and_attend(0)
+
+
+def test_the_example_runs(kb):
+    """The example of a four-bit cache in README.md, as written."""
+    import os
+    import re
+
+    from libbuild import ROOT
+
+    text = open(os.path.join(ROOT, "README.md")).read()
+    code = [c for c in re.findall(r"```python\n(.*?)```", text, flags=re.S) if "PagedFp4Cache(" in c][0]
+    env = {"torch": torch, "RotaryPlan": kb.RotaryPlan}
+    exec(compile(code, "README.md", "exec"), env)
+    torch.cuda.synchronize()
+    assert bool(torch.isfinite(env["out"][0].float()).all()) and env["out"][0].shape == (1, 1, 32, 128)
+    assert env["keys"].shape == env["values"].shape == (271, 8, 128) and bool(torch.isfinite(env["keys"].float()).all())
+    env["cache"].check()

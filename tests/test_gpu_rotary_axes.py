@@ -109,3 +109,30 @@ def test_an_axis_that_is_none_is_recorded(kb):
     pos = torch.ones((2, 3), dtype=torch.int32, device=DEV)
     kb.rotary_store_cache(pool, 0, None, x, x, pos, torch.arange(3, dtype=torch.int32, device=DEV), plan, None)
     assert kb.kvp_sync_error(pool) == kb.KVP_ERR_BAD_INDEX
+
+
+@pytest.mark.parametrize("page_size", [1, 16])
+def test_steps_of_a_latent_cache_on_several_axes(kb, page_size):
+    """Text has the same position on every axis: a step with such a plan is the one of a single axis."""
+    from paged_decode_attention_store_gb300.engine import PagedLatentCache
+
+    dc, dr, H, C = 64, 32, 4, 3
+    g = torch.Generator().manual_seed(4)
+    rnd = lambda *s: torch.randn(s, generator=g).to(torch.bfloat16).to(DEV)  # noqa: E731
+    steps = [(rnd(2, C, H, dc + dr), rnd(2, C, H, dr), rnd(2 * C, dc), rnd(2 * C, dr)) for _ in range(3)]
+    outs = []
+    for sections in (None, (6, 5, 5)):
+        cache = PagedLatentCache(num_pages=64, page_size=page_size, latent_dim=dc, rope_dim=dr, num_layers=1, dtype="bf16",
+                                 max_requests=4, max_seq_len=64, device=DEV)
+        plan = kb.RotaryPlan(dr, device=DEV, sections=sections, interleave=True)
+        for rid in (0, 1):
+            cache.new(rid)
+        got = []
+        for q, q_pe, latent, k_pe in steps:
+            out = torch.empty(2, C, H, dc, dtype=torch.bfloat16, device=DEV)
+            cache.step([0, 1], [q.clone()], [q_pe], [latent], [k_pe], plan, [out], window=0, scale=0.1)
+            got.append(out)
+        torch.cuda.synchronize()
+        cache.check()
+        outs.append(torch.stack(got))
+    assert bool(torch.isfinite(outs[0].float()).all()) and torch.equal(outs[0], outs[1])
