@@ -13,7 +13,7 @@
 //
 // A row is turned back once for every 64 columns, not once a call as in the chunk path, so long chunks are bound by the
 // conversions and by mma's rate; few columns by the loads' latency, which other CTAs of the SM hide. 64 requests of 512-4096
-// rows, 32 query heads on 8: head_dim 64 99 us (13 at the memory's rate; a block a query head on CUDA cores 474), 256 314
+// rows, 32 query heads on 8: head_dim 64 98 us (13 at the memory's rate; a block a query head on CUDA cores 474), 256 307
 // (51; 1537). 16 chunks of 512 tokens on up to 2048 rows, head_dim 64: 532 us (29,107).
 //
 // A block of V that reads as NaN counts as zero; the columns that attend it get the NaN by hand.
@@ -350,26 +350,44 @@ __global__ void __launch_bounds__(kTileThreads, DT == 64 ? 4 : DT == 128 ? 3 : 2
         *reinterpret_cast<float2*>(po + (warp * 16 + r) * D + 8 * d + 2 * c) = make_float2(o[d][2 * y], o[d][2 * y + 1]);
   }
   cluster.sync();
-  for (int r = rank; r < 16 * CT; r += R) {
+  // a warp a column: lane k has part k's maximum and sum, then the parts' outputs come four at a time
+  for (int r = rank + R * warp; r < 16 * CT; r += 4 * R) {
     const int col = col0 + r;
-    if (col >= cols || col / a.G > j1) continue;
-    float M = -3.0e38f, sum = 0.f;
-    for (int k = 0; k < R; ++k)
-      for (int y = 0; y < kParts; ++y) M = fmaxf(M, cluster.map_shared_rank(&part_m[0][0], k)[(y * CT + r / 16) * 16 + r % 16]);
-    float2 acc = make_float2(0.f, 0.f);
-    for (int k = 0; k < R; ++k)
-      for (int y = 0; y < kParts; ++y) {
-        const int w = (y * CT + r / 16) * 16 + r % 16;
-        const float scale = exp2_of(cluster.map_shared_rank(&part_m[0][0], k)[w] - M);
-        sum += scale * cluster.map_shared_rank(&part_l[0][0], k)[w];
-        if (tid < D / 2) {
-          const float2 x = reinterpret_cast<const float2*>(cluster.map_shared_rank(po, k) + w * D)[tid];
-          acc.x += scale * x.x;
-          acc.y += scale * x.y;
+    if (col >= cols || col / a.G > j1) break;  // nor are later ones
+    const int parts = kParts * R, w0 = (r / 16) * 16 + r % 16;
+    auto at = [&](int k) { return k % kParts * CT * 16 + w0; };  // of a CTA's warps' columns
+    float mk = -3.0e38f, lk = 0.f;
+    if (lane < parts) {
+      mk = cluster.map_shared_rank(&part_m[0][0], lane / kParts)[at(lane)];
+      lk = cluster.map_shared_rank(&part_l[0][0], lane / kParts)[at(lane)];
+    }
+    float M = mk;
+#pragma unroll
+    for (int sh = 16; sh > 0; sh >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, sh));
+    const float wk = exp2_of(mk - M);
+    float sum = wk * lk;
+#pragma unroll
+    for (int sh = 16; sh > 0; sh >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, sh);
+    float2 acc[DT / 64];
+#pragma unroll
+    for (int i = 0; i < DT / 64; ++i) acc[i] = make_float2(0.f, 0.f);
+#pragma unroll 4
+    for (int k = 0; k < parts; ++k) {
+      const float scale = __shfl_sync(0xffffffffu, wk, k);
+      const float2* src = reinterpret_cast<const float2*>(cluster.map_shared_rank(po, k / kParts) + at(k) * D);
+#pragma unroll
+      for (int i = 0; i < DT / 64; ++i)
+        if (lane + 32 * i < D / 2) {
+          const float2 x = src[lane + 32 * i];
+          acc[i].x += scale * x.x;
+          acc[i].y += scale * x.y;
         }
-      }
+    }
     const float inv = a.gv / sum;
-    if (tid < D / 2) reinterpret_cast<uint32_t*>(column_out(col))[tid] = pack_bf16(acc.x * inv, acc.y * inv);
+    uint32_t* dst = reinterpret_cast<uint32_t*>(column_out(col));
+#pragma unroll
+    for (int i = 0; i < DT / 64; ++i)
+      if (lane + 32 * i < D / 2) dst[lane + 32 * i] = pack_bf16(acc[i].x * inv, acc[i].y * inv);
   }
   cluster.sync();  // the others have read this CTA's parts
 }
@@ -422,9 +440,11 @@ int launch_fp4_tile(const Fp4Call& c, cudaStream_t st) {
   const int CT = cols <= 16 ? 1 : 4;
   a.tiles = (int)((cols + 16 * CT - 1) / (16 * CT));
   const long long items = (long long)a.tiles * a.Hkv * c.B;
-  // CTAs share a tile while that leaves no SM more than four, and each a block at least
+  // CTAs share a tile while that leaves no SM more than four, and each a block at least, or four where they join 64 columns
+  // (head_dim 64: one request of 500 rows 8.9 us, with four each 13.3; a chunk of 256 tokens 20.8 us, with one each 24.4)
   int R = 1;
-  while (R < kMaxParts && 2 * R * items <= 4LL * pool->num_sms && 2 * R * kRows <= c.max_context) R *= 2;
+  const long long least = (CT == 1 ? 1 : 4) * kRows;
+  while (R < kMaxParts && 2 * R * items <= 4LL * pool->num_sms && 2 * R * least <= c.max_context) R *= 2;
   if (items * R > 0x7fffffffLL) return KVP_ERR_INVALID_ARG;
   const size_t smem = (size_t)(2 * kRows + 16 * CT) * (2 * a.D + 16);
   const unsigned grid = (unsigned)(items * R);
