@@ -172,8 +172,8 @@ struct GenArgs {
   TableRef T;
   const char* codes;
   const char* scales;
-  const void* q;
-  void* out;
+  const float* q;
+  float* out;
   const int32_t* context_lens;
   const int32_t* table_rows;
   const int32_t* q_lens;
@@ -182,30 +182,25 @@ struct GenArgs {
   int32_t* err;
 };
 
-__device__ __forceinline__ float as_float(float x) { return x; }
-__device__ __forceinline__ float as_float(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ void put1(float* p, float x) { *p = x; }
-__device__ __forceinline__ void put1(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
-
-// Query head ``item`` (of all requests' tokens' heads) by one block.
-template <typename T>
-__device__ void general_item(const GenArgs& a, int item) {
+// fp32 pools: a block has one query head of one token.
+__global__ void __launch_bounds__(32 * kGenWarps) fp4_general_kernel(const __grid_constant__ GenArgs a) {
+  const int item = blockIdx.x;
   __shared__ float qs[kFp4MaxDim];
   __shared__ float part_o[kGenWarps][kFp4MaxDim], part_m[kGenWarps], part_l[kGenWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int h = item % a.Hq, bj = item / a.Hq, b = bj / a.C, j = bj % a.C;
   const int kvh = h / (a.Hq / a.Hkv), D = a.D;
-  T* out = static_cast<T*>(a.out) + (size_t)item * D;
-  const T* q = static_cast<const T*>(a.q) + (size_t)item * D;
+  float* out = a.out + (size_t)item * D;
+  const float* q = a.q + (size_t)item * D;
   const int Lr = a.context_lens[b], row = a.table_rows ? a.table_rows[b] : b, ql = a.q_lens ? a.q_lens[b] : a.C;
   if (!request_ok(Lr, ql, row, a.C, a.max_context, a.T.rows_total)) {
     if (threadIdx.x == 0 && h == 0 && j == 0) set_error(a.err, KVP_ERR_BAD_INDEX);
-    for (int d = threadIdx.x; d < D; d += blockDim.x) put1(out + d, 0.f);
+    for (int d = threadIdx.x; d < D; d += blockDim.x) out[d] = 0.f;
     return;
   }
   if (j >= ql) return;
   const int L = Lr - ql + j + 1;  // the query token's own context
-  for (int d = threadIdx.x; d < D; d += blockDim.x) qs[d] = as_float(q[d]);
+  for (int d = threadIdx.x; d < D; d += blockDim.x) qs[d] = q[d];
   __syncthreads();
   const Span sp = attend_span(L, a.window, a.sinks);
   const int n = sp.se + L - sp.lo;
@@ -283,33 +278,7 @@ __device__ void general_item(const GenArgs& a, int item) {
   for (int d = threadIdx.x; d < D; d += blockDim.x) {
     float o = 0.f;
     for (int w = 0; w < kGenWarps; ++w) o += exp2f(part_m[w] - base) * part_o[w][d];
-    put1(out + d, o * inv);
-  }
-}
-
-__global__ void __launch_bounds__(32 * kGenWarps) fp4_general_kernel(const __grid_constant__ GenArgs a) {
-  general_item<float>(a, blockIdx.x);
-}
-
-// Chunks: the requests with a scale NaN in their spans, all their query heads again.
-__global__ void __launch_bounds__(32 * kGenWarps)
-    fp4_again_kernel(const __grid_constant__ GenArgs a, int B, const int32_t* lens, const int32_t* nan, int blocks, int rows) {
-  int any = 0;
-  for (long long u = threadIdx.x; u < (long long)B * blocks; u += blockDim.x) {
-    const int b = (int)(u / blocks), i = (int)(u - (long long)b * blocks);
-    if ((long long)i * rows < lens[b]) any |= nan[u];
-  }
-  if (!__syncthreads_or(any)) return;
-  for (int b = 0; b < B; ++b) {
-    const int n = lens[b] == 0 ? 0 : (lens[b] - 1) / rows + 1;
-    int hit = 0;
-    for (int i = threadIdx.x; i < n; i += blockDim.x) hit |= nan[(size_t)b * blocks + i];
-    if (!__syncthreads_or(hit)) continue;
-    const int per = a.C * a.Hq;
-    for (int i = blockIdx.x; i < per; i += gridDim.x) {
-      general_item<__nv_bfloat16>(a, b * per + i);
-      __syncthreads();  // its shared memory is the next one's
-    }
+    out[d] = o * inv;
   }
 }
 
@@ -318,8 +287,8 @@ GenArgs general_args(const Fp4Call& c) {
   g.T = c.T;
   g.codes = c.pool->buf + (size_t)c.layer * c.pool->layer_bytes;
   g.scales = c.pool->fp4_scales + (size_t)c.layer * c.pool->fp4_scale_layer_bytes;
-  g.q = c.q;
-  g.out = c.out;
+  g.q = static_cast<const float*>(c.q);
+  g.out = static_cast<float*>(c.out);
   g.context_lens = c.context_lens;
   g.table_rows = c.table_rows;
   g.q_lens = c.q_lens;
@@ -425,8 +394,7 @@ int launch_chunk(const Fp4Call& c, int longest, cudaStream_t st) {
   const int rc = launch_prefill_tc(&rows, 0, c.q, c.B, c.C, c.H, c.q_lens, make_table(&rows, table, c.B, 1, KVP_BLOCK_TABLE),
                                    nullptr, lens, c.window, c.sinks, c.scale, c.out, st);
   if (rc != KVP_OK) return rc;
-  fp4_again_kernel<<<2 * pool->num_sms, 32 * kGenWarps, 0, st>>>(general_args(c), c.B, lens, nan, l.blocks, l.rows);
-  return cudaGetLastError() == cudaSuccess ? KVP_OK : KVP_ERR_CUDA;
+  return launch_fp4_again(c, lens, nan, l.blocks, l.rows, st);
 }
 
 // What both calls about a shape check.

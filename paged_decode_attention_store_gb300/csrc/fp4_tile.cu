@@ -132,13 +132,11 @@ __device__ __forceinline__ uint32_t turn(const Row<DT>& r, int D, bool v, unsign
   return nan;
 }
 
-// DT: head_dim rounded up to 64, 128 or 256. CT: tiles of 16 columns a CTA, 1 or 4.
+// Tile ``item`` of the call's. DT: head_dim rounded up to 64, 128 or 256. CT: tiles of 16 columns a CTA, 1 or 4.
 template <int DT, int CT>
-__global__ void __launch_bounds__(kTileThreads, DT == 64 ? 4 : DT == 128 ? 3 : 2)
-    fp4_tile_kernel(const __grid_constant__ TileArgs a) {
+__device__ __forceinline__ void tile_item(const TileArgs& a, unsigned char* smem, long long item, cg::cluster_group cluster) {
   constexpr int kWarpRows = kRows * CT / 4;  // positions of a block that a warp has
   constexpr int kParts = 4 / CT;
-  extern __shared__ __align__(128) unsigned char smem[];
   __shared__ int pos[kRows];
   __shared__ uint32_t vnan[kRows];
   __shared__ float factor[16 * CT], part_m[4][16], part_l[4][16];
@@ -147,9 +145,7 @@ __global__ void __launch_bounds__(kTileThreads, DT == 64 ? 4 : DT == 128 ? 3 : 2
   unsigned char* sv = sk + kRows * pitch;
   unsigned char* sq = sv + kRows * pitch;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  cg::cluster_group cluster = cg::this_cluster();
   const int R = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
-  const long long item = (long long)blockIdx.x / R;
   const int tile = (int)(item % a.tiles), kvh = (int)(item / a.tiles % a.Hkv), b = (int)(item / a.tiles / a.Hkv);
   const int col0 = tile * 16 * CT, cols = a.C * a.G;
 
@@ -393,10 +389,45 @@ __global__ void __launch_bounds__(kTileThreads, DT == 64 ? 4 : DT == 128 ? 3 : 2
 }
 
 template <int DT, int CT>
+__global__ void __launch_bounds__(kTileThreads, DT == 64 ? 4 : DT == 128 ? 3 : 2)
+    fp4_tile_kernel(const __grid_constant__ TileArgs a) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  cg::cluster_group cluster = cg::this_cluster();
+  tile_item<DT, CT>(a, smem, blockIdx.x / cluster.num_blocks(), cluster);
+}
+
+// Chunks: the requests with a scale NaN in their spans, all their query heads again. The other calls' cost is one look
+// through the marks (4 us).
+__global__ void __launch_bounds__(kTileThreads, 3)
+    fp4_again_kernel(const __grid_constant__ TileArgs a, int B, const int32_t* lens, const int32_t* nan, int blocks, int rows) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  int any = 0;
+#pragma unroll 8
+  for (unsigned u = threadIdx.x; u < (unsigned)(B * blocks); u += kTileThreads) {  // 2^30 at most
+    const unsigned b = u / (unsigned)blocks, first = (u - b * blocks) * rows;
+    const int mark = nan[u];  // past the context's end whatever lay there
+    any |= first < (unsigned)lens[b] ? mark : 0;
+  }
+  if (!__syncthreads_or(any)) return;
+  const long long per = (long long)a.tiles * a.Hkv;
+  for (int b = 0; b < B; ++b) {
+    const int n = lens[b] == 0 ? 0 : (lens[b] - 1) / rows + 1;
+    int hit = 0;
+    for (int i = threadIdx.x; i < n; i += blockDim.x) hit |= nan[(size_t)b * blocks + i];
+    if (!__syncthreads_or(hit)) continue;
+    for (long long i = blockIdx.x; i < per; i += gridDim.x) {
+      tile_item<128, 4>(a, smem, b * per + i, cg::this_cluster());
+      __syncthreads();  // its shared memory is the next one's
+    }
+  }
+}
+
+size_t tile_smem(int D, int CT) { return (size_t)(2 * kRows + 16 * CT) * (2 * D + 16); }
+
+template <int DT, int CT>
 cudaError_t launch_one(const TileArgs& a, unsigned grid, int R, size_t smem, cudaStream_t st) {
   auto kernel = fp4_tile_kernel<DT, CT>;
-  const size_t most = (size_t)(2 * kRows + 16 * CT) * (2 * DT + 16);
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)tile_smem(DT, CT));
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -412,9 +443,8 @@ cudaError_t launch_one(const TileArgs& a, unsigned grid, int R, size_t smem, cud
   return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
-}  // namespace
-
-int launch_fp4_tile(const Fp4Call& c, cudaStream_t st) {
+// ``columns``: of a tile.
+TileArgs tile_args(const Fp4Call& c, int columns) {
   const kvp_pool* pool = c.pool;
   TileArgs a;
   a.T = c.T;
@@ -436,9 +466,16 @@ int launch_fp4_tile(const Fp4Call& c, cudaStream_t st) {
   a.scale_log2 = c.scale * pool->fp4_globals[c.layer] * 1.4426950408889634f;
   a.gv = pool->fp4_globals[pool->num_layers + c.layer];
   a.err = pool->err;
-  const long long cols = (long long)c.C * a.G;
-  const int CT = cols <= 16 ? 1 : 4;
-  a.tiles = (int)((cols + 16 * CT - 1) / (16 * CT));
+  a.tiles = (int)(((long long)c.C * a.G + columns - 1) / columns);
+  return a;
+}
+
+}  // namespace
+
+int launch_fp4_tile(const Fp4Call& c, cudaStream_t st) {
+  const kvp_pool* pool = c.pool;
+  const int CT = (long long)c.C * (c.H / pool->kv_heads) <= 16 ? 1 : 4;
+  const TileArgs a = tile_args(c, 16 * CT);
   const long long items = (long long)a.tiles * a.Hkv * c.B;
   // CTAs share a tile while that leaves no SM more than four, and each a block at least, or four where they join 64 columns
   // (head_dim 64: one request of 500 rows 8.9 us, with four each 13.3; a chunk of 256 tokens 20.8 us, with one each 24.4)
@@ -446,13 +483,22 @@ int launch_fp4_tile(const Fp4Call& c, cudaStream_t st) {
   const long long least = (CT == 1 ? 1 : 4) * kRows;
   while (R < kMaxParts && 2 * R * items <= 4LL * pool->num_sms && 2 * R * least <= c.max_context) R *= 2;
   if (items * R > 0x7fffffffLL) return KVP_ERR_INVALID_ARG;
-  const size_t smem = (size_t)(2 * kRows + 16 * CT) * (2 * a.D + 16);
+  const size_t smem = tile_smem(a.D, CT);
   const unsigned grid = (unsigned)(items * R);
   cudaError_t e;
   if (a.D <= 64) e = CT == 1 ? launch_one<64, 1>(a, grid, R, smem, st) : launch_one<64, 4>(a, grid, R, smem, st);
   else if (a.D <= 128) e = CT == 1 ? launch_one<128, 1>(a, grid, R, smem, st) : launch_one<128, 4>(a, grid, R, smem, st);
   else e = CT == 1 ? launch_one<256, 1>(a, grid, R, smem, st) : launch_one<256, 4>(a, grid, R, smem, st);
   return e == cudaSuccess ? KVP_OK : KVP_ERR_CUDA;
+}
+
+int launch_fp4_again(const Fp4Call& c, const int32_t* lens, const int32_t* nan, int blocks, int rows, cudaStream_t st) {
+  const TileArgs a = tile_args(c, 64);
+  const size_t smem = tile_smem(a.D, 4);
+  if (a.D != 128 || cudaFuncSetAttribute(fp4_again_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return KVP_ERR_CUDA;
+  fp4_again_kernel<<<3 * c.pool->num_sms, kTileThreads, smem, st>>>(a, c.B, lens, nan, blocks, rows);
+  return cudaGetLastError() == cudaSuccess ? KVP_OK : KVP_ERR_CUDA;
 }
 
 }  // namespace kvp
