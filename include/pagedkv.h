@@ -182,7 +182,7 @@ int page_table_write(int32_t* table, int table_rows_total, int table_cols,
 /* ------------------------------------------------------------------------
  * copy_pages: copy-on-write (chapter 15, section "The model": a shared tail
  * page is copied whole before a private write). For i < n, every layer, K
- * and V (or the latent rows): page dst[i] <- page src[i]. src/dst device int32 [n]; a page
+ * and V (or the latent rows, or codes and block scales): page dst[i] <- page src[i]. src/dst device int32 [n]; a page
  * outside [0, num_pages) sets KVP_ERR_BAD_INDEX and is skipped. Pairs must
  * not overlap (no page is both a source and a destination).
  * ---------------------------------------------------------------------- */
@@ -417,7 +417,8 @@ int rotary_store_latent_axes(const kvp_pool* pool, int layer, const void* q_pe,
  * each to the nearest value, ties to the even code, at most 448 and 6; a scale
  * that rounds to zero makes the block zero. The codes and scales are those of
  * the formula with sines, cosines, products and sums in 64 bits. A block with an
- * infinity or a NaN gets the scale NaN (0x7f) and reads as NaN throughout.
+ * infinity or a NaN gets the scale NaN (0x7f) and reads as NaN throughout. Of
+ * equal slots in one call any token's blocks may stay, block by block.
  * With q NULL and rotary_dim 0, positions and freqs may be NULL: the store
  * alone, of k and v as they are.
  * ---------------------------------------------------------------------- */

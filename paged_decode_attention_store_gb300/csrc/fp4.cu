@@ -1,24 +1,27 @@
-// Four-bit pools (fp4.cuh): rows turned back into full entries, the general
-// attention kernel, chunks, and the entry points of paged_fp4_attention.
+// Four-bit pools (fp4.cuh): rows turned back into full entries, chunks, the
+// general attention kernel of fp32 pools, and the entry points.
 //
 // Mathematics: as attention.cu, over K and V entries code * scale * g. The
-// general kernel takes every type and width: one block per query token and
-// head, its warps take 32 positions in turn; a lane scores one position (its
-// K row is its own loads), then the lanes take V's entries and the positions'
-// weights come by shuffles; the warps' running maxima, sums and outputs are
-// joined at the end. It is bound by instructions: a row is read again for every
-// query head.
+// general kernel takes every fp32 shape: one block per query token and head, its
+// warps take 32 positions in turn; a lane scores one position (its K row is its
+// own loads), then the lanes take V's entries and the positions' weights come by
+// shuffles; the warps' running maxima, sums and outputs are joined at the end.
+// It is bound by instructions: a row is read again for every query head (64
+// requests of 512-4096 rows, 32 heads on 8 of 128: 810 us).
 //
 // Chunks (many query tokens a request) are bound by the matrix rate, and every
-// key is met by many query tiles: turning it back once a tile would cost more
-// than once a call. So a call turns the attended rows into bf16 (exactly) in its
-// workspace, request b's as the one page b of a pool whose pages are as long as
-// the longest context, and runs the chunk kernel of bf16 pools (prefill_tc.cu)
-// over them. Bytes: 1.1 KB read and 4 KB written a token of eight heads, and
-// read again by the chunk kernel, mostly from L2. That kernel multiplies V by
-// weights of zero where a query does not attend, so a block that reads as NaN
-// would reach more queries than it should: a request with one in its span is
-// noticed on the way and done again by the general kernel.
+// key is met by many query tiles: turning it back once a tile costs more than
+// once a call (16 chunks of 512 tokens: 975 us by fp4_tile.cu, 258 so). So a call
+// turns the attended rows into bf16 (exactly) in its workspace, request b's as
+// the one page b of a pool whose pages are as long as the longest context, and
+// runs the chunk kernel of bf16 pools (prefill_tc.cu) over them. Bytes: 1.1 KB
+// read and 4 KB written a token of eight heads, and read again by the chunk
+// kernel, mostly from L2. Of the 258 us the unpacking takes 32, the chunk kernel
+// 221, the look for NaN 4; five prompts of 33-600 tokens 48 us (7, 38, 3).
+// That kernel multiplies V by weights of zero where a query does not attend, so a
+// block that reads as NaN would reach more queries than it should: a request with
+// one in its span is noticed on the way and done again (fp4_tile.cu; 383 us with
+// one of the 16).
 #include <cstring>
 
 #include "attention.cuh"
@@ -96,7 +99,8 @@ __device__ __forceinline__ bool request_ok(int L, int ql, int row, int C, int ma
 
 // Rows back to full entries: a block takes up to 32 rows (their slots first, all at once). A thread has one word of four
 // code bytes of a row, or of several side by side, and turns it into eight entries, row after row; a warp reads the 128
-// bytes of a head of 128 and writes 256 bytes of K and of V. Bytes bound it: 9 / 16 read and 2 written (bf16) an entry.
+// bytes of a head of 128 and writes 256 bytes of K and of V. Bytes bound it: 9 / 16 read and 2 written (bf16) an entry: 8,192
+// rows of 8 heads of 128 12.7 us (3.3 TB/s; 42 MB, of which the writes stay in L2), 30,011 scattered ones 36 us (4.3 TB/s).
 template <typename T, bool CHUNK>
 __global__ void __launch_bounds__(kLoadThreads) unpack_kernel(const __grid_constant__ Unpack a) {
   __shared__ int slots[kUnpackRows];

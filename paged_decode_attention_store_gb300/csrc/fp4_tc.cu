@@ -7,12 +7,12 @@
 // sums are). The weights are rounded once to fp16 (half a step, 2^-11; they are an operand of the second product), their
 // sum keeps them in fp32.
 //
-// What bounds it. A token and head is 144 bytes, K and V, and its 256 entries have to become fp16 pairs: 128
-// conversions, 128 multiplications by scales and 64 permutations that put two tokens' values side by side, a lane and
-// instruction each, beside the products. An SM streams 23 bytes a clock (45 GB/s of 6.8 TB/s), 98 clocks for 16 tokens of
-// a head; conversions and permutations issue at 64 lanes a clock and take 48 of those, everything together about 65 of
-// its issue slots. So bytes bound it as long as nothing waits, and what is laid out here is laid out to need few
-// instructions:
+// What bounds it. A token and head is 144 bytes, K and V, and its 256 entries have to become fp16 pairs. An SM streams 23
+// bytes a clock (45 GB/s of 6.8 TB/s): 32 positions of eight heads in 1,660 clocks, 0.80 us. For such a stage each of the
+// eight consumer warps, two on a scheduler, has 128 conversions, 128 multiplications by scales and 32 mma a lane; fp16
+// multiplications and mma share a port, and in a loop of nothing else two warps took 551 clocks each way. With the shared
+// loads, the permutations that put two tokens' values side by side and the softmax a stage takes 0.95 us: issue slots and
+// that port bound it (0.73 of the memory's rate over a long batch), and every choice here is for fewer instructions:
 // * K is operand A of S^T = K Q^T (mma m16n8k16, tokens x heads) straight from 16-byte shared loads: which entries of d a
 //   k step takes is free as long as Q agrees, so a lane's 16 bytes (32 entries, two blocks) are its part of all eight k
 //   steps of its token's row. No transposing loads.
@@ -25,11 +25,19 @@
 //
 // How. The work is the batch's blocks of 32 positions (aligned, of the union of the request's queries' spans) laid end to
 // end and divided evenly over the CTAs; a cut request leaves fp32 partials that a second launch joins in CTA order, so
-// results do not depend on timing. One producer warp fills a ring of such blocks: a group of 16 slots that lie together
-// and aligned comes by one tensor copy (all heads of the CTA, head-major, swizzled) and one copy of its scales, whole
-// even if only some of its rows are attended (they lie in the pool; masks drop the others); other rows come one by one
-// (a kilobyte of codes each, scales by 16-byte asynchronous copies). A consumer warp takes one KV head and up to 16
-// (token, head) columns.
+// results do not depend on timing. Twelve warps an SM at 168 registers: eight that compute, one KV head and up to 16 (token,
+// head) columns each, and up to four that fill a ring of five blocks or so. A group of 16 slots that lie together and aligned
+// comes by one tensor copy (all heads of the CTA, head-major, swizzled) and one copy of its scales, whole even if only some
+// of its rows are attended (they lie in the pool; masks drop the others): one warp issues all of these. Other rows come one
+// by one (a kilobyte of codes each, scales by 16-byte asynchronous copies), the blocks dealt to the four warps. A warp that
+// computes works on the next block's scores beside this one's values: two chains of instructions that hide each other's
+// latencies (139 us instead of 185 for 256 requests).
+//
+// Measured (8 KV heads of 128, pages of 16): 256 requests of 512-4096 rows, 32 query heads, 136 us (0.73 of a copy's rate);
+// 64 of them 46.8 us (0.57); with 4 tokens each 62 us; one of 777 rows 11 us, of which about 2 us are the work split, 1 the
+// table, 3 the first rows' way and 3.5 the join: chains of memory latencies, as in the other small calls. 32 requests of
+// 8,192-32,768 scattered rows, 64 query heads, 192 us (0.61): a row's scales, 16 bytes a head, cost a sector of 32
+// each (161 us with the scales left out).
 //
 // A block of V that reads as NaN may be attended by some of the columns only: 0 * NaN would reach the others, so when a
 // lane sees a NaN scale (a compare, and only with several query tokens) its scale counts as zero and the columns that
@@ -279,12 +287,12 @@ __device__ void make_plan(const Args& a, Plan* pl, bool* any_bad) {
 }
 
 // ---------------------------------------------------------------------------
-// The producer warp. It takes the share's stages 32 at a time, a lane each: every lane finds its stage's request and group
+// The producers. They take the share's stages 32 at a time, a lane each: every lane finds its stage's request and group
 // (from 32 requests' sizes and their sums), and in a block table whose pages are whole groups also the two slots that its
 // copies start at, all while the 32 stages before are on their way. Issuing such a stage is then one lane's work: two
 // tensor copies and two of scales. Of other tables each lane fetches one position's entry, a stage ahead, and copies that
-// row where the group does not lie together. (A stage at a time with the whole warp took 800 instructions, and set the
-// pace: 55 us for 64 requests.)
+// row where the group does not lie together. (Planning a stage at a time with the whole warp set the pace: 55 us for 64
+// requests that take 47 now.)
 // ---------------------------------------------------------------------------
 struct Lane {   // a stage, in one lane's registers
   Hdr h;
@@ -1038,7 +1046,7 @@ __global__ void __launch_bounds__(128, 8) fp4_combine_kernel(const __grid_consta
   }
 }
 
-// How the columns of a KV head go to warps, and the CTAs to an SM.
+// How the columns of a KV head go to warps, and the CTAs to an SM (one with eight heads; fewer heads make smaller CTAs).
 struct Shape {
   int NT, tiles, HG, CW, PW, ctas_per_sm, stages;
 };

