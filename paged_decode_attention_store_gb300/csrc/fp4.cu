@@ -97,10 +97,10 @@ __device__ __forceinline__ bool request_ok(int L, int ql, int row, int C, int ma
   return ql >= 1 && ql <= C && L >= ql && L <= max_context && row >= 0 && row < rows_total;
 }
 
-// Rows back to full entries: a block takes up to 32 rows (their slots first, all at once). A thread has one word of four
-// code bytes of a row, or of several side by side, and turns it into eight entries, row after row; a warp reads the 128
-// bytes of a head of 128 and writes 256 bytes of K and of V. Bytes bound it: 9 / 16 read and 2 written (bf16) an entry: 8,192
-// rows of 8 heads of 128 12.7 us (3.3 TB/s; 42 MB, of which the writes stay in L2), 30,011 scattered ones 36 us (4.3 TB/s).
+// Rows back to full entries: a block takes up to 32 rows (their slots first, all at once). A thread has 32 bytes of
+// a row's entries, or of several rows side by side, row after row; a bf16 warp reads 256 bytes of two heads of 128 and writes
+// 512 bytes of K and of V. Bytes bound it: 9 / 16 read and 2 written (bf16) an entry: 8,192
+// rows of 8 heads of 128 12 us (3.5 TB/s; 42 MB, of which the writes stay in L2), 30,011 scattered ones 32 us (4.9 TB/s).
 template <typename T, bool CHUNK>
 __global__ void __launch_bounds__(kLoadThreads) unpack_kernel(const __grid_constant__ Unpack a) {
   __shared__ int slots[kUnpackRows];
@@ -139,29 +139,40 @@ __global__ void __launch_bounds__(kLoadThreads) unpack_kernel(const __grid_const
     out0 = (size_t)i0;
   }
   __syncthreads();
-  const int words = a.d / 4, width = a.heads * words;  // words of four code bytes, K's first in a head
+  constexpr int kWords = sizeof(T) == 2 ? 2 : 1;  // words of four code bytes: 32 bytes of entries
+  const int units = a.d / 4 / kWords, width = a.heads * units;  // of a token's row, K's first in a head
   const int beside = width < kLoadThreads ? kLoadThreads / width : 1;
   const int r0 = width < kLoadThreads ? tid / width : 0;
   bool nan = false;
   if (r0 < beside)
-    for (int hw = tid - r0 * width; hw < width; hw += kLoadThreads) {
-      const int h = hw / words, w = hw - h * words, part = w >= words / 2, e0 = (w - part * (words / 2)) * 8;
+    for (int hu = tid - r0 * width; hu < width; hu += kLoadThreads) {
+      const int h = hu / units, u = hu - h * units, part = u >= units / 2, e0 = (u - part * (units / 2)) * 8 * kWords;
       const float g = part ? a.gv : a.gk;
       T* dst = static_cast<T*>(part ? a.v : a.k) + (size_t)h * a.d + e0;
       const uint8_t* scales = reinterpret_cast<const uint8_t*>(a.scales) + part * (a.d / 16) + e0 / 16;
 #pragma unroll 4
       for (int r = r0; r < rows; r += beside) {
         const int slot = slots[r];
-        float x[8] = {};
+        float x[kWords][8] = {};
         if (slot >= 0) {
-          const uint32_t c = __ldg(reinterpret_cast<const uint32_t*>(a.codes + (size_t)slot * row_entries) + hw);
+          const char* from = a.codes + (size_t)slot * row_entries + (size_t)hu * 4 * kWords;
+          uint32_t c[2];
+          if (kWords == 2) {
+            const uint2 w = __ldg(reinterpret_cast<const uint2*>(from));
+            c[0] = w.x;
+            c[1] = w.y;
+          } else {
+            c[0] = __ldg(reinterpret_cast<const uint32_t*>(from));
+          }
           const uint32_t s = __ldg(scales + fp4_scale_offset(slot, h, a.heads, a.d));
           nan |= s == kFp4NanScale;
-          fp4_entries(c, s, g, x);
+#pragma unroll
+          for (int i = 0; i < kWords; ++i) fp4_entries(c[i], s, g, x[i]);
         } else if (CHUNK) {
           continue;  // not attended, or a hole: nothing reads it, or what is read is unspecified
         }
-        put8(dst + (out0 + r) * row_entries, x);
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) put8(dst + (out0 + r) * row_entries + 8 * i, x[i]);
       }
     }
   if (CHUNK) {

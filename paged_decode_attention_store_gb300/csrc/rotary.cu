@@ -506,47 +506,57 @@ __global__ void __launch_bounds__(kRotThreads) rotary_store_elem_kernel(const Ro
   }
 }
 
-// Keys and values into a four-bit pool, any alignment and any even rotary_dim: a thread makes one block, in 64 bits, whose
-// rate bounds it (64 tokens of 8 heads of 128: 35 us, 8,192 tokens 763 us): the way of views that are not aligned, not a fast one.
+// Keys and values into a four-bit pool, any alignment and any even rotary_dim, entry by entry: two neighbouring threads make
+// one block, as in fp4_body, with a sine a pair and head (64 tokens of 8 heads of 128: 7.4 us, 8,192 tokens 49 us).
 template <typename T, bool AXES>
 __global__ void __launch_bounds__(kRotThreads) fp4_store_elem_kernel(const __grid_constant__ RotArgs a, int half) {
-  const int blocks = a.d / kFp4Block, per = 2 * a.hk * blocks;
+  constexpr int N = kFp4Block / 2;
+  const int blocks = a.d / kFp4Block, per = 2 * a.hk * blocks, pairs = a.rot / 2;
   const long long stride = (long long)gridDim.x * kRotThreads;
-  for (long long id = (long long)blockIdx.x * kRotThreads + threadIdx.x; id < (long long)a.n * per; id += stride) {
-    const size_t tok = (size_t)(id / per);
-    const int x = (int)(id % per), part = x / (a.hk * blocks), h = x / blocks % a.hk, e0 = x % blocks * kFp4Block;
+  const unsigned mask = 3u << (threadIdx.x & 30);
+  const float off = fabsf(a.attn) * 0x1p-20f;
+  for (long long id = (long long)blockIdx.x * kRotThreads + threadIdx.x; id < 2LL * a.n * per; id += stride) {
+    const size_t tok = (size_t)(id / (2 * per));
+    const int x = (int)(id / 2 % per), part = x / (a.hk * blocks), h = x / blocks % a.hk;
+    const int e0 = x % blocks * kFp4Block + (int)(id & 1) * N;
     const int slot = __ldg(a.out_loc + tok);
     if ((unsigned)slot >= (unsigned)a.num_slots) {
       if (x == 0) set_error(a.err, KVP_ERR_BAD_INDEX);
       continue;
     }
     const T* src = reinterpret_cast<const T*>(part ? a.v + tok * a.v_tok : a.k + tok * a.k_tok) + (size_t)h * a.d;
-    double v[kFp4Block];
-    bool finite = true;
-  #pragma unroll 1
-    for (int i = 0; i < kFp4Block; ++i) {
-      v[i] = part ? exact_value(src[e0 + i]) : exact_entry<T, AXES>(a, src, tok, e0 + i, half);
-      finite = finite && fabs(v[i]) <= 0x1.fffffep127;  // as the 32-bit formula's
+    const float g = part ? a.gv : a.gk, inv_g = 1.f / g;
+    float v[N];
+    uint32_t codes, scale;
+    if (part || e0 >= a.rot) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = ld1(src + e0 + i);
     }
-    uint32_t scale = kFp4NanScale, lo = 0, hi = 0;
-    if (finite) {
-      const double g = part ? a.gv : a.gk;
-      double m = 0.0;
-  #pragma unroll 1
-      for (int i = 0; i < kFp4Block; ++i) m = fmax(m, fabs(v[i]));
-      scale = fp4_scale_exact(m, g, 1.0 / g);
-      const double sg = (double)e4m3_value(scale) * g;
-  #pragma unroll 1
-      for (int i = 0; scale && i < kFp4Block; ++i) {
-        const uint32_t c = (fp4_code_exact(fabs(v[i]), sg) | (v[i] < 0.0 ? 8u : 0u)) << (4 * (i & 7));
-        if (i < 8) lo |= c;
-        else hi |= c;
+    // K's blocks that turn, or the halves of one, agree on the way they take
+    if (part || e0 - (int)(id & 1) * N >= a.rot) {
+      fp4_block<N>(v, g, inv_g, mask, codes, scale);
+    } else {
+      float er = 0.f;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int e = e0 + i;
+        if (e >= a.rot) {
+          v[i] = ld1(src + e);
+          continue;
+        }
+        const int pair = half ? (e < pairs ? e : e - pairs) : e / 2;
+        const bool first = half ? e < pairs : !(e & 1);
+        const float x0 = ld1(src + (half ? pair : 2 * pair)), x1 = ld1(src + (half ? pair + pairs : 2 * pair + 1));
+        const float2 f = turn_of(position_of<AXES>(a, tok, pair), __ldg(a.freqs + pair), a.attn);
+        v[i] = first ? x0 * f.x - x1 * f.y : x1 * f.x + x0 * f.y;
+        er = fmaxf(er, fabsf(x0) + fabsf(x1));
       }
+      fp4_block_within<N>(v, er * off, g, inv_g, mask, [&](int i) { return exact_entry<T, AXES>(a, src, tok, e0 + i, half); },
+                          codes, scale);
     }
     char* dst = a.k_dst + (size_t)slot * a.row_bytes + (size_t)h * a.d + part * (a.d / 2) + e0 / 2;
-    reinterpret_cast<uint32_t*>(dst)[0] = lo;
-    reinterpret_cast<uint32_t*>(dst)[1] = hi;
-    a.scales[fp4_scale_offset(slot, h, a.hk, a.d) + part * blocks + e0 / 16] = (char)scale;
+    *reinterpret_cast<uint32_t*>(dst) = codes;
+    if (!(id & 1)) a.scales[fp4_scale_offset(slot, h, a.hk, a.d) + part * blocks + e0 / 16] = (char)scale;
   }
 }
 
@@ -574,7 +584,7 @@ void launch_elem(const RotArgs& a, bool half, cudaStream_t st) {
 }
 template <typename T>
 void launch_fp4_elem(const RotArgs& a, bool half, cudaStream_t st) {
-  const long long blocks = ((long long)a.n * 2 * a.hk * (a.d / kFp4Block) + kRotThreads - 1) / kRotThreads;
+  const long long blocks = ((long long)a.n * 4 * a.hk * (a.d / kFp4Block) + kRotThreads - 1) / kRotThreads;
   const unsigned grid = (unsigned)(blocks < 1 << 20 ? blocks : 1 << 20);
   if (a.pair_axis) fp4_store_elem_kernel<T, true><<<grid, kRotThreads, 0, st>>>(a, half);
   else fp4_store_elem_kernel<T, false><<<grid, kRotThreads, 0, st>>>(a, half);
