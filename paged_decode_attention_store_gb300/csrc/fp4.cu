@@ -1,13 +1,7 @@
 // Four-bit pools (fp4.cuh): rows turned back into full entries, chunks, the
-// general attention kernel of fp32 pools, and the entry points.
+// attention kernel of fp32 pools, and the entry points.
 //
-// Mathematics: as attention.cu, over K and V entries code * scale * g. The
-// general kernel takes every fp32 shape: one block per query token and head, its
-// warps take 32 positions in turn; a lane scores one position (its K row is its
-// own loads), then the lanes take V's entries and the positions' weights come by
-// shuffles; the warps' running maxima, sums and outputs are joined at the end.
-// It is bound by instructions: a row is read again for every query head (64
-// requests of 512-4096 rows, 32 heads on 8 of 128: 810 us).
+// Mathematics: as attention.cu, over K and V entries code * scale * g.
 //
 // Chunks (many query tokens a request) are bound by the matrix rate, and every
 // key is met by many query tiles: turning it back once a tile costs more than
@@ -22,7 +16,9 @@
 // block that reads as NaN would reach more queries than it should: a request with
 // one in its span is noticed on the way and done again (fp4_tile.cu; 383 us with
 // one of the 16).
-#include <cstring>
+#include <cooperative_groups.h>
+
+#include <type_traits>
 
 #include "attention.cuh"
 #include "fp4.cuh"
@@ -181,9 +177,21 @@ __global__ void __launch_bounds__(kLoadThreads) unpack_kernel(const __grid_const
   }
 }
 
-constexpr int kGenWarps = 8;
+// ---------------------------------------------------------------------------
+// fp32 pools. A CTA of eight warps has up to 32 (token, head) columns of one KV head, four a warp. Blocks of 64 positions are
+// turned into fp32 rows in shared memory, the next block's codes fetched meanwhile. A lane scores a position for its warp's
+// four columns (its K row is its own loads, the queries' are broadcast), then has four entries of V and the columns' weights
+// of each position come as one word: 16 multiplications and additions a load either way, so fp32's rate bounds it where there
+// are columns enough. With fewer, all eight warps work all the same, on parts of a block's positions: 32, 16 or 8, of which a
+// lane then scores a half or a quarter. Where tiles are few a cluster shares
+// one, as in fp4_tile.cu. 64 requests of 512-4096 rows, 32 heads on 8 of 128: 380 us (a block a query head
+// 810), one of 500 rows 11; four prompts of up to 100 tokens on up to 300 73 us (233).
+// ---------------------------------------------------------------------------
+namespace cg = cooperative_groups;
 
-struct GenArgs {
+constexpr int kF32Rows = 64, kF32Warps = 8, kF32Parts = 8;
+
+struct F32Args {
   TableRef T;
   const char* codes;
   const char* scales;
@@ -192,139 +200,311 @@ struct GenArgs {
   const int32_t* context_lens;
   const int32_t* table_rows;
   const int32_t* q_lens;
-  int Hq, Hkv, D, C, window, sinks, max_context;
+  int Hq, Hkv, G, D, C, window, sinks, max_context, tiles;
   float scale_log2, gv;  // K's g is in the scale
   int32_t* err;
 };
 
-// fp32 pools: a block has one query head of one token.
-__global__ void __launch_bounds__(32 * kGenWarps) fp4_general_kernel(const __grid_constant__ GenArgs a) {
-  const int item = blockIdx.x;
-  __shared__ float qs[kFp4MaxDim];
-  __shared__ float part_o[kGenWarps][kFp4MaxDim], part_m[kGenWarps], part_l[kGenWarps];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int h = item % a.Hq, bj = item / a.Hq, b = bj / a.C, j = bj % a.C;
-  const int kvh = h / (a.Hq / a.Hkv), D = a.D;
-  float* out = a.out + (size_t)item * D;
-  const float* q = a.q + (size_t)item * D;
-  const int Lr = a.context_lens[b], row = a.table_rows ? a.table_rows[b] : b, ql = a.q_lens ? a.q_lens[b] : a.C;
-  if (!request_ok(Lr, ql, row, a.C, a.max_context, a.T.rows_total)) {
-    if (threadIdx.x == 0 && h == 0 && j == 0) set_error(a.err, KVP_ERR_BAD_INDEX);
-    for (int d = threadIdx.x; d < D; d += blockDim.x) out[d] = 0.f;
+// I: head_dim over 128, rounded up; CG: warps that have columns of their own.
+template <int I, int CG>
+__global__ void __launch_bounds__(32 * kF32Warps, I == 1 ? 2 : 1) fp4_f32_kernel(const __grid_constant__ F32Args a) {
+  constexpr int kParts = kF32Warps / CG;              // of a block's positions
+  constexpr int kPos = CG < 4 ? 8 * CG : 32;           // positions at once, 32 / kPos lanes each
+  constexpr int kSubs = kF32Rows / kParts / kPos;
+  constexpr int kLanes = 32 / kPos;
+  extern __shared__ __align__(16) float f32_smem[];
+  __shared__ int pos[kF32Rows];
+  __shared__ uint32_t vnan[2][kF32Rows];  // of a row's even and odd blocks
+  __shared__ float4 weights[kF32Warps][32];
+  __shared__ float part_m[kF32Warps][4], part_l[kF32Warps][4];
+  const int D = a.D, pitch = D + 4;
+  float* sk = f32_smem;
+  float* sv = sk + kF32Rows * pitch;
+  float* sq = sv + kF32Rows * pitch;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int R = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const long long item = (long long)blockIdx.x / R;
+  const int tile = (int)(item % a.tiles), kvh = (int)(item / a.tiles % a.Hkv), b = (int)(item / a.tiles / a.Hkv);
+  const int col0 = tile * 4 * CG, cols = a.C * a.G;
+  const int L = a.context_lens[b], ql = a.q_lens ? a.q_lens[b] : a.C, row = a.table_rows ? a.table_rows[b] : b;
+  auto column = [&](int col) {  // its row of q and out
+    const int cj = col / a.G;
+    return (((size_t)b * a.C + cj) * a.Hq + (size_t)kvh * a.G + (col - cj * a.G)) * D;
+  };
+  if (!request_ok(L, ql, row, a.C, a.max_context, a.T.rows_total)) {
+    if (rank) return;
+    if (tid == 0 && tile == 0 && kvh == 0) set_error(a.err, KVP_ERR_BAD_INDEX);
+    for (int i = tid; i < 4 * CG * D; i += 32 * kF32Warps)
+      if (col0 + i / D < cols) a.out[column(col0 + i / D) + i % D] = 0.f;
     return;
   }
-  if (j >= ql) return;
-  const int L = Lr - ql + j + 1;  // the query token's own context
-  for (int d = threadIdx.x; d < D; d += blockDim.x) qs[d] = q[d];
-  __syncthreads();
-  const Span sp = attend_span(L, a.window, a.sinks);
-  const int n = sp.se + L - sp.lo;
-  constexpr int kBytes = kFp4MaxDim / 64;  // bytes of V a lane takes
-  float acc[2 * kBytes] = {}, m = -INFINITY, l = 0.f;
-  for (int o0 = 32 * warp; o0 < n; o0 += 32 * kGenWarps) {
-    const int o = o0 + lane;
-    int slot = -1;
-    float s = -INFINITY;
-    if (o < n) {
-      slot = resolve_slot(a.T, row, span_pos(sp, o), a.err);
-      if (slot >= 0) {
-        const uint32_t* kr = reinterpret_cast<const uint32_t*>(a.codes + ((size_t)slot * a.Hkv + kvh) * D);
-        const uint8_t* ks = reinterpret_cast<const uint8_t*>(a.scales) + fp4_scale_offset(slot, kvh, a.Hkv, D);
-        float dot = 0.f;
-        for (int w = 0; w < D / 8; ++w) {
-          float x[8];
-          fp4_entries(__ldg(kr + w), __ldg(ks + w / 2), 1.f, x);
+  const int j0 = col0 / a.G, j1 = min((min(col0 + 4 * CG, cols) - 1) / a.G, ql - 1);
+  if (j0 > j1) return;
+  const int p0 = L - ql + j0, p1 = L - ql + j1;
+  const Span u = attend_span(p1 + 1, a.window > 0 && j1 - j0 < 0x7fffffff - a.window ? a.window + (j1 - j0) : 0, a.sinks);
+  const Span newest = attend_span(p1 + 1, a.window, a.sinks);
+  const int n = u.se + (p1 + 1) - u.lo, blocks = (n - 1) / kF32Rows + 1;
+
+  // a thread's part of a block: every other block of 16 entries of K or of V of one position
+  const int mine = tid & (kF32Rows - 1), odd = tid >> 6 & 1;
+  const bool is_v = tid >= 2 * kF32Rows;
+  uint2 codes[4 * I];
+  uint32_t scales[I];
+  int at = 0x7fffffff;
+  auto fetch = [&](int o) {
+    const int t = o < n ? span_pos(u, o) : 0;
+    const int slot = o < n ? resolve_slot(a.T, row, t, a.err) : -1;
+    at = slot < 0 ? 0x7fffffff : t;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) dot = fmaf(qs[8 * w + i], x[i], dot);
+    for (int i = 0; i < I; ++i) scales[i] = 0;
+#pragma unroll
+    for (int i = 0; i < 4 * I; ++i) {
+      codes[i] = make_uint2(0u, 0u);
+      const int x = 2 * i + odd;  // block of the row
+      if (slot < 0 || 16 * x >= D) continue;
+      codes[i] = __ldg(reinterpret_cast<const uint2*>(a.codes + ((size_t)slot * a.Hkv + kvh) * D + (is_v ? D / 2 : 0)) + x);
+      scales[i / 4] |= (uint32_t)__ldg(reinterpret_cast<const uint8_t*>(a.scales) + fp4_scale_offset(slot, kvh, a.Hkv, D) +
+                                       (is_v ? D / 16 : 0) + x)
+                       << (8 * (i & 3));
+    }
+  };
+  if (rank < blocks) fetch(rank * kF32Rows + mine);
+  for (int i = tid; i < 4 * CG * D; i += 32 * kF32Warps) {
+    const int c = i / D, col = col0 + c;
+    sq[c * pitch + i % D] = col < cols && col / a.G <= j1 ? __ldg(a.q + column(col) + i % D) : 0.f;
+  }
+
+  const int group = warp % CG, part = warp / CG;
+  float4 o[4][I];
+  float m[4], l[4];
+  int p[4], lo[4], se[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    m[c] = -3.0e38f;
+    l[c] = 0.f;
+    p[c] = L - ql + min((col0 + 4 * group + c) / a.G, j1);
+    const Span s = attend_span(p[c] + 1, a.window, a.sinks);
+    lo[c] = s.lo;
+    se[c] = s.se;
+#pragma unroll
+    for (int i = 0; i < I; ++i) o[c][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  const bool live = col0 + 4 * group < cols;
+  for (int blk = rank; blk < blocks; blk += R) {
+    __syncthreads();  // the block before is done with
+    uint32_t bad = 0;
+    float* dst = (is_v ? sv : sk) + mine * pitch;
+#pragma unroll
+    for (int i = 0; i < 4 * I; ++i) {
+      const int x = 2 * i + odd;
+      if (16 * x >= D) break;
+      uint32_t sc = scales[i / 4] >> (8 * (i & 3)) & 0xffu;
+      if (is_v && sc == kFp4NanScale) {
+        bad |= 1u << x;
+        sc = 0;
+      }
+      float y[8];
+      fp4_entries(codes[i].x, sc, 1.f, y);
+      put8(dst + 16 * x, y);
+      fp4_entries(codes[i].y, sc, 1.f, y);
+      put8(dst + 16 * x + 8, y);
+    }
+    if (is_v) vnan[odd][mine] = bad;
+    else if (!odd) pos[mine] = at;
+    // whether some column does not attend some position, or a V block is NaN
+    const int special = __syncthreads_or(bad != 0 || at > p0 || at < newest.lo);
+    if (blk + R < blocks) fetch((blk + R) * kF32Rows + mine);
+    if (!live) continue;
+#pragma unroll 1
+    for (int sub = 0; sub < kSubs; ++sub) {
+      const int first = kPos * (part * kSubs + sub);
+      float s[4] = {};
+      const float4* kr = reinterpret_cast<const float4*>(sk + (first + lane % kPos) * pitch);
+      const float* qr = sq + 4 * group * pitch;
+#pragma unroll 4
+      for (int w = lane / kPos; w < D / 4; w += kLanes) {
+        const float4 kv = kr[w];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float4 qv = reinterpret_cast<const float4*>(qr + c * pitch)[w];
+          s[c] = fmaf(qv.x, kv.x, fmaf(qv.y, kv.y, fmaf(qv.z, kv.z, fmaf(qv.w, kv.w, s[c]))));
         }
-        s = dot * a.scale_log2;
       }
-    }
-    float mx = s;
 #pragma unroll
-    for (int sh = 16; sh > 0; sh >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
-    const float mn = fmaxf(m, mx), base = mn == -INFINITY ? 0.f : mn;  // a NaN score passes by the maximum, not by p
-    const float alpha = exp2f(m - base), p = exp2f(s - base);
-    float ps = p;
+      for (int c = 0; c < 4; ++c)
 #pragma unroll
-    for (int sh = 16; sh > 0; sh >>= 1) ps += __shfl_xor_sync(0xffffffffu, ps, sh);
-    l = l * alpha + ps;
-    m = mn;
+        for (int sh = kPos; sh < 32; sh <<= 1) s[c] += __shfl_xor_sync(0xffffffffu, s[c], sh);
+      const int t = pos[first + lane % kPos];
+      float w4[4];
 #pragma unroll
-    for (int i = 0; i < 2 * kBytes; ++i) acc[i] *= alpha;
-    const int nt = min(32, n - o0);
-    for (int t = 0; t < nt; ++t) {
-      const float pt = __shfl_sync(0xffffffffu, p, t);
-      const int st = __shfl_sync(0xffffffffu, slot, t);
-      if (st < 0) continue;
-      const uint8_t* vr = reinterpret_cast<const uint8_t*>(a.codes) + ((size_t)st * a.Hkv + kvh) * D + D / 2;
-      const uint8_t* vs = reinterpret_cast<const uint8_t*>(a.scales) + fp4_scale_offset(st, kvh, a.Hkv, D) + D / 16;
+      for (int c = 0; c < 4; ++c) {
+        const float x = special && !(t <= p[c] && (t >= lo[c] || t < se[c])) ? -INFINITY : __fmul_rn(s[c], a.scale_log2);
+        float mx = x;
 #pragma unroll
-      for (int i = 0; i < kBytes; ++i) {
-        const int x = lane + 32 * i;
-        if (x >= D / 2) break;
-        uint32_t hh[4];
-        e2m1x8_to_half(__ldg(vr + x), hh);
-        const float2 f = half2_floats(hh[0]);
-        const float w = half2_floats(e4m3x2_to_half(__ldg(vs + x / 8))).x * pt;
-        acc[2 * i] = fmaf(f.x, w, acc[2 * i]);
-        acc[2 * i + 1] = fmaf(f.y, w, acc[2 * i + 1]);
+        for (int sh = kPos / 2; sh > 0; sh >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
+        mx = fminf(fmaxf(mx, m[c]), 3.0e38f);  // finite: a score beyond it becomes a NaN
+        const float al = exp2f(m[c] - mx);
+        m[c] = mx;
+        w4[c] = exp2f(x - mx);
+        l[c] = l[c] * al + (lane < kPos ? w4[c] : 0.f);
+        if (al != 1.f)
+#pragma unroll
+          for (int i = 0; i < I; ++i) {
+            o[c][i].x *= al;
+            o[c][i].y *= al;
+            o[c][i].z *= al;
+            o[c][i].w *= al;
+          }
       }
+      __syncwarp();
+      if (lane < kPos) weights[warp][lane] = make_float4(w4[0], w4[1], w4[2], w4[3]);
+      __syncwarp();
+#pragma unroll 4
+      for (int y = 0; y < kPos; ++y) {
+        const float4 wv = weights[warp][y];
+        const float wc[4] = {wv.x, wv.y, wv.z, wv.w};
+#pragma unroll
+        for (int i = 0; i < I; ++i) {
+          const int e = 4 * (lane + 32 * i);
+          if (e >= D) break;
+          const float4 v = *reinterpret_cast<const float4*>(sv + (first + y) * pitch + e);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            o[c][i].x = fmaf(wc[c], v.x, o[c][i].x);
+            o[c][i].y = fmaf(wc[c], v.y, o[c][i].y);
+            o[c][i].z = fmaf(wc[c], v.z, o[c][i].z);
+            o[c][i].w = fmaf(wc[c], v.w, o[c][i].w);
+          }
+        }
+      }
+      if (special)
+        for (int y = first; y < first + kPos; ++y) {
+          const uint32_t blocks_of = vnan[0][y] | vnan[1][y];
+          if (!blocks_of) continue;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int i = 0; i < I; ++i)
+              if ((blocks_of >> ((lane + 32 * i) / 4) & 1) && pos[y] <= p[c] && (pos[y] >= lo[c] || pos[y] < se[c])) {
+                const float none = __int_as_float(0x7fffffff);
+                o[c][i] = make_float4(none, none, none, none);
+              }
+        }
     }
-  }
-  if (lane == 0) {
-    part_m[warp] = m;
-    part_l[warp] = l;
   }
 #pragma unroll
-  for (int i = 0; i < kBytes; ++i) {
-    const int x = lane + 32 * i;
-    if (x < D / 2) {
-      part_o[warp][2 * x] = acc[2 * i];
-      part_o[warp][2 * x + 1] = acc[2 * i + 1];
-    }
-  }
+  for (int c = 0; c < 4; ++c)
+#pragma unroll
+    for (int sh = 16; sh > 0; sh >>= 1) l[c] += __shfl_xor_sync(0xffffffffu, l[c], sh);
+  // the parts' sums, maxima and outputs to shared memory, over K and V, and their join: a warp a column
   __syncthreads();
-  float M = -INFINITY, Ls = 0.f;
-  for (int w = 0; w < kGenWarps; ++w) M = fmaxf(M, part_m[w]);
-  const float base = M == -INFINITY ? 0.f : M;
-  for (int w = 0; w < kGenWarps; ++w) Ls += exp2f(part_m[w] - base) * part_l[w];
-  const float inv = Ls == 0.f ? 0.f : a.gv / Ls;  // no weight at all: zeros; a NaN stays one
-  for (int d = threadIdx.x; d < D; d += blockDim.x) {
-    float o = 0.f;
-    for (int w = 0; w < kGenWarps; ++w) o += exp2f(part_m[w] - base) * part_o[w][d];
-    out[d] = o * inv;
+  float* po = f32_smem;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    if (lane == 0) {
+      part_m[warp][c] = m[c];
+      part_l[warp][c] = l[c];
+    }
+#pragma unroll
+    for (int i = 0; i < I; ++i)
+      if (4 * (lane + 32 * i) < D) *reinterpret_cast<float4*>(po + (warp * 4 + c) * D + 4 * (lane + 32 * i)) = o[c][i];
   }
+  cluster.sync();
+  for (int r = rank + R * warp; r < 4 * CG; r += kF32Warps * R) {
+    const int col = col0 + r;
+    if (col >= cols || col / a.G > j1) break;  // nor are later ones
+    const int parts = kParts * R;
+    auto from = [&](int k) { return (k % kParts * CG) * 4 + r; };  // of a CTA's warps' columns
+    float M = -3.0e38f, sum = 0.f;
+    for (int k = lane; k < parts; k += 32) M = fmaxf(M, cluster.map_shared_rank(&part_m[0][0], k / kParts)[from(k)]);
+#pragma unroll
+    for (int sh = 16; sh > 0; sh >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, sh));
+    for (int k = lane; k < parts; k += 32)
+      sum += exp2f(cluster.map_shared_rank(&part_m[0][0], k / kParts)[from(k)] - M) *
+             cluster.map_shared_rank(&part_l[0][0], k / kParts)[from(k)];
+#pragma unroll
+    for (int sh = 16; sh > 0; sh >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, sh);
+    const float inv = a.gv / sum;
+    float* dst = a.out + column(col);
+    for (int e = 4 * lane; e < D; e += 128) {
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int k = 0; k < parts; ++k) {
+        const float w = exp2f(cluster.map_shared_rank(&part_m[0][0], k / kParts)[from(k)] - M);
+        const float4 x = *reinterpret_cast<const float4*>(cluster.map_shared_rank(po, k / kParts) + from(k) * D + e);
+        acc.x = fmaf(w, x.x, acc.x);
+        acc.y = fmaf(w, x.y, acc.y);
+        acc.z = fmaf(w, x.z, acc.z);
+        acc.w = fmaf(w, x.w, acc.w);
+      }
+      *reinterpret_cast<float4*>(dst + e) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    }
+  }
+  cluster.sync();  // the others have read this CTA's parts
 }
 
-GenArgs general_args(const Fp4Call& c) {
-  GenArgs g;
-  g.T = c.T;
-  g.codes = c.pool->buf + (size_t)c.layer * c.pool->layer_bytes;
-  g.scales = c.pool->fp4_scales + (size_t)c.layer * c.pool->fp4_scale_layer_bytes;
-  g.q = static_cast<const float*>(c.q);
-  g.out = static_cast<float*>(c.out);
-  g.context_lens = c.context_lens;
-  g.table_rows = c.table_rows;
-  g.q_lens = c.q_lens;
-  g.Hq = c.H;
-  g.Hkv = c.pool->kv_heads;
-  g.D = c.pool->head_dim;
-  g.C = c.C;
-  g.window = c.window;
-  g.sinks = c.sinks;
-  g.max_context = c.max_context;
-  g.scale_log2 = c.scale * c.pool->fp4_globals[c.layer] * 1.4426950408889634f;
-  g.gv = c.pool->fp4_globals[c.pool->num_layers + c.layer];
-  g.err = c.pool->err;
-  return g;
+template <int I, int CG>
+cudaError_t launch_f32_one(const F32Args& a, unsigned grid, int R, cudaStream_t st) {
+  auto kernel = fp4_f32_kernel<I, CG>;
+  auto bytes = [](int D) { return (size_t)(2 * kF32Rows + 4 * CG) * (D + 4) * sizeof(float); };
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes(128 * I));
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = R;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(32 * kF32Warps);
+  cfg.dynamicSmemBytes = bytes(a.D);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
-int launch_general(const Fp4Call& c, cudaStream_t st) {
-  const GenArgs g = general_args(c);
-  const unsigned grid = (unsigned)((long long)c.B * c.C * c.H);
-  fp4_general_kernel<<<grid, 32 * kGenWarps, 0, st>>>(g);
-  return cudaGetLastError() == cudaSuccess ? KVP_OK : KVP_ERR_CUDA;
+int launch_f32(const Fp4Call& c, cudaStream_t st) {
+  const kvp_pool* pool = c.pool;
+  F32Args a;
+  a.T = c.T;
+  a.codes = pool->buf + (size_t)c.layer * pool->layer_bytes;
+  a.scales = pool->fp4_scales + (size_t)c.layer * pool->fp4_scale_layer_bytes;
+  a.q = static_cast<const float*>(c.q);
+  a.out = static_cast<float*>(c.out);
+  a.context_lens = c.context_lens;
+  a.table_rows = c.table_rows;
+  a.q_lens = c.q_lens;
+  a.Hq = c.H;
+  a.Hkv = pool->kv_heads;
+  a.G = c.H / pool->kv_heads;
+  a.D = pool->head_dim;
+  a.C = c.C;
+  a.window = c.window;
+  a.sinks = c.sinks;
+  a.max_context = c.max_context;
+  a.scale_log2 = c.scale * pool->fp4_globals[c.layer] * 1.4426950408889634f;
+  a.gv = pool->fp4_globals[pool->num_layers + c.layer];
+  a.err = pool->err;
+  const long long cols = (long long)c.C * a.G;
+  const int CG = cols <= 4 ? 1 : cols <= 8 ? 2 : cols <= 16 ? 4 : 8;
+  a.tiles = (int)((cols + 4 * CG - 1) / (4 * CG));
+  const long long items = (long long)a.tiles * a.Hkv * c.B;
+  // CTAs share a tile while that leaves no SM more than two, and each a block at least
+  int R = 1;
+  while (R < kF32Parts && 2 * R * items <= 2LL * pool->num_sms && 2 * R * kF32Rows <= c.max_context) R *= 2;
+  if (items * R > 0x7fffffffLL) return KVP_ERR_INVALID_ARG;
+  const unsigned grid = (unsigned)(items * R);
+  cudaError_t e;
+  auto launch = [&](auto width) {
+    constexpr int I = decltype(width)::value;
+    return CG == 1   ? launch_f32_one<I, 1>(a, grid, R, st)
+           : CG == 2 ? launch_f32_one<I, 2>(a, grid, R, st)
+           : CG == 4 ? launch_f32_one<I, 4>(a, grid, R, st)
+                     : launch_f32_one<I, 8>(a, grid, R, st);
+  };
+  e = a.D <= 128 ? launch(std::integral_constant<int, 1>{}) : launch(std::integral_constant<int, 2>{});
+  return e == cudaSuccess ? KVP_OK : KVP_ERR_CUDA;
 }
 
 Unpack unpack_args(const kvp_pool* pool, int layer, void* k, void* v) {
@@ -493,5 +673,5 @@ extern "C" int paged_fp4_attention(const kvp_pool* pool, int layer, const void* 
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (chunk_eligible(pool, batch, chunk, num_q_heads, max_context, scale)) return launch_chunk(c, max_context, st);
   if (fp4_tc_eligible(pool, chunk, num_q_heads)) return launch_fp4_tc(c, st);
-  return pool->dtype == KVP_BF16 ? launch_fp4_tile(c, st) : launch_general(c, st);
+  return pool->dtype == KVP_BF16 ? launch_fp4_tile(c, st) : launch_f32(c, st);
 }

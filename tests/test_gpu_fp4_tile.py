@@ -1,5 +1,5 @@
 """paged_fp4_attention at the shapes of neither the decode kernel nor the chunk kernel: other widths, groups that do not
-divide 128, negative scales of many queries; and calls of several host threads."""
+divide 128, negative scales of many queries, fp32; and calls of several host threads."""
 
 import threading
 
@@ -44,6 +44,56 @@ def test_attention_is_the_formula(kb, lens, C, H, hkv, D, P, raw, window, sinks)
     c.run(window, sinks)
     c.verify(window, sinks)
     assert kb.kvp_sync_error(c.pool) == 0
+
+
+F32 = [
+    ([1], 1, 8, 8, 16, 16, False, 0, 0),
+    ([1, 31, 32, 33, 63, 64, 65, 129, 1000], 1, 32, 8, 128, 16, False, 0, 0),
+    ([33, 500], 1, 16, 16, 48, 16, False, 0, 0),
+    ([33, 500], 1, 14, 2, 192, 16, False, 0, 0),                    # seven columns
+    ([1, 33, 500], 1, 16, 1, 256, 16, False, 0, 0),                 # sixteen
+    ([33, 500], 1, 17, 1, 256, 1, True, 0, 0),                      # seventeen
+    ([4, 66, 700], 4, 32, 8, 128, 16, False, 0, 0),
+    ([8, 64, 169], 8, 8, 2, 64, 16, False, 0, 0),                   # thirty-two: one tile
+    ([9, 64, 169], 9, 8, 2, 64, 16, False, 0, 0),                   # thirty-six: two
+    ([130, 211], 130, 12, 4, 128, 16, False, 0, 0),
+    ([131], 131, 5, 1, 128, 3, True, 0, 0),
+    ([40, 64, 100, 1000], 1, 32, 8, 128, 16, False, 70, 40),
+    ([130, 211], 130, 16, 4, 64, 4, True, 33, 5),
+    ([30011], 1, 8, 2, 128, 16, False, 0, 0),
+]
+
+
+@pytest.mark.parametrize("lens,C,H,hkv,D,P,raw,window,sinks", F32)
+def test_attention_in_fp32(kb, lens, C, H, hkv, D, P, raw, window, sinks):  # noqa: F811
+    c = Case(kb, "f32", lens, C, H, hkv, D, P, raw, seed=C + H + D, gk=2.0, gv=0.25)
+    first = c.run(window, sinks).clone()
+    c.verify(window, sinks, few=True)
+    assert kb.kvp_sync_error(c.pool) == 0
+    c.run(window, sinks)
+    assert torch.equal(first, c.out)
+
+
+@pytest.mark.parametrize("C", [1, 70])
+def test_fp32_bad_requests_holes_and_queries(kb, C):  # noqa: F811
+    c = Case(kb, "f32", [200, 100, 220, 170, 250, 300], C, 32, 8, 128, 16, seed=6)
+    c.clens.copy_(torch.tensor([200, 0, 100000, 170, 250, 300]))
+    c.table[4, 3], c.table[4, 5] = -1, 1 << 30
+    c.q[5, 0, 9, 7], c.q[5, 0, 13, 7] = float("nan"), float("inf")
+    c.q[5, 0, 3] *= 2.0 ** 60
+    c.q[5, 0, 4] *= 2.0 ** -60
+    c.q[5, 0, 5] = 0
+    rows = torch.tensor([0, 1, 2, 77, 4, 5], dtype=torch.int32, device=DEV)
+    c.run(table_rows=rows)
+    assert kb.kvp_sync_error(c.pool) == kb.KVP_ERR_BAD_INDEX
+    assert bool((c.out[1:4] == 0).all())
+    c.verify(only=[0])
+    w, bound = c.want(5, 0, C)
+    bad = c.out[5, 0].cpu().isnan()
+    assert bool(bad[[9, 13]].all()) and int(bad.any(-1).sum()) == 2
+    keep = [h for h in range(32) if h not in (3, 9, 13)]
+    R.check(c.out[5, 0].cpu()[keep], w[keep], bound[keep])
+    R.check(c.out[5, 0, 3].cpu(), w[3], 2 * R.u(torch.float32) * w[3].abs() + 1e-30)  # one key has all the weight
 
 
 @pytest.mark.parametrize("D,H,hkv", [(64, 32, 8), (256, 8, 2), (128, 24, 8)])
@@ -97,10 +147,12 @@ def test_holes_are_skipped_and_recorded(kb, C):  # noqa: F811
     c.verify(only=[1])
 
 
-@pytest.mark.parametrize("C,H,hkv,D", [(1, 32, 8, 64), (4, 32, 8, 64), (140, 32, 8, 64), (30, 2, 1, 256), (50, 9, 3, 128)])
-def test_blocks_of_nan_reach_who_attends_them(kb, C, H, hkv, D):  # noqa: F811
+@pytest.mark.parametrize("C,H,hkv,D,dtype", [(1, 32, 8, 64, "bf16"), (4, 32, 8, 64, "bf16"), (140, 32, 8, 64, "bf16"),
+                                             (30, 2, 1, 256, "bf16"), (50, 9, 3, 128, "bf16"), (1, 32, 8, 128, "f32"),
+                                             (4, 32, 8, 64, "f32"), (50, 9, 3, 128, "f32"), (30, 2, 1, 256, "f32")])
+def test_blocks_of_nan_reach_who_attends_them(kb, C, H, hkv, D, dtype):  # noqa: F811
     lens = [180, 333]
-    c = Case(kb, "bf16", lens, C, H, hkv, D, 16, seed=7)
+    c = Case(kb, dtype, lens, C, H, hkv, D, 16, seed=7)
     cut, block = max(1, C // 2), D // 16 - 2
     kt, vt = c.lens[0] - cut, c.lens[1] - cut
     for slot, head, part, at in ((c.slots[0][kt], 0, 0, 2), (c.slots[1][vt], hkv - 1, 1, block)):
