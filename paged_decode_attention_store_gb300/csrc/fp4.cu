@@ -572,6 +572,15 @@ bool chunk_eligible(const kvp_pool* pool, int B, int C, int H, int longest, floa
          prefill_tc_eligible(pool, H, C, scale);
 }
 
+// Few query tokens of few short contexts: the tile kernel's one launch, whose clusters join their parts, before the decode
+// kernel's two. Columns up to 16, 8 KV heads: one request of 128 rows 6.9 and 8.7 us, 16 of them 8.6 and 10.4, 4 tokens of
+// two requests of 200 rows 11.6 and 13.2, one request of 300 rows 10.1 and 9.9; 64 of 50 rows, more tiles than SMs, 14.6 and
+// 11.8; 28 columns of 100 rows 18.6 and 13.5.
+bool short_eligible(const kvp_pool* pool, int B, int C, int H, int longest) {
+  return pool->dtype == KVP_BF16 && (long long)C * (H / pool->kv_heads) <= 16 && longest <= 256 &&
+         (long long)B * pool->kv_heads <= pool->num_sms;
+}
+
 int launch_chunk(const Fp4Call& c, int longest, cudaStream_t st) {
   const kvp_pool* pool = c.pool;
   char* ws = static_cast<char*>(c.workspace);
@@ -672,6 +681,7 @@ extern "C" int paged_fp4_attention(const kvp_pool* pool, int layer, const void* 
   c.workspace = workspace;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (chunk_eligible(pool, batch, chunk, num_q_heads, max_context, scale)) return launch_chunk(c, max_context, st);
-  if (fp4_tc_eligible(pool, chunk, num_q_heads)) return launch_fp4_tc(c, st);
+  if (fp4_tc_eligible(pool, chunk, num_q_heads) && !short_eligible(pool, batch, chunk, num_q_heads, max_context))
+    return launch_fp4_tc(c, st);
   return pool->dtype == KVP_BF16 ? launch_fp4_tile(c, st) : launch_f32(c, st);
 }

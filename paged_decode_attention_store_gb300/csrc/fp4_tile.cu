@@ -1,5 +1,5 @@
 // Attention over a four-bit pool, bf16, on the tensor cores for every head_dim, group size and number of query tokens: what
-// neither the decode kernel (fp4_tc.cu) nor the chunk kernel takes (they are for head_dim 128).
+// neither the decode kernel (fp4_tc.cu) nor the chunk kernel takes (they are for head_dim 128), and few short contexts.
 //
 // Mathematics: as fp4_tc.cu. K and V entries are code * block scale, exact in fp16; a query row is scaled by a power of two
 // and held in fp16; the weights, at most 256 (their sum stays in fp32), are rounded once to fp16.

@@ -126,6 +126,20 @@ def test_more_context_than_there_is(kb):  # noqa: F811
     c.verify()
 
 
+@pytest.mark.parametrize("most", [200, 256, 257, 5000])
+@pytest.mark.parametrize("C,H,hkv,raw", [(1, 32, 8, False), (4, 32, 8, False), (1, 16, 1, True), (16, 2, 2, False), (17, 2, 2, True)])
+def test_short_contexts_under_any_bound(kb, C, H, hkv, raw, most):  # noqa: F811
+    """The bound chooses the kernel, and with more of the same requests their number does."""
+    for window, sinks, times in ((0, 0, 1), (0, 0, 20), (40, 3, 1)):
+        lens = [L for L in (17, 31, 32, 33, 63, 64, 65, 200) if L >= C] * times
+        c = Case(kb, "bf16", lens if C > 1 else lens + [1, 2], C, H, hkv, 128, 1 if raw else 16, raw, seed=C + H)
+        c.most = most
+        c.ws = kb.alloc_fp4_workspace(c.pool, len(c.lens), C, H, most, device=DEV)
+        c.run(window, sinks)
+        c.verify(window, sinks, only=range(len(c.lens) - 7, len(c.lens)))
+        assert kb.kvp_sync_error(c.pool) == 0
+
+
 @pytest.mark.parametrize("C,H,hkv", [(1, 32, 8), (4, 32, 8), (140, 32, 8)])
 def test_bad_requests_are_zeros_and_recorded(kb, C, H, hkv):  # noqa: F811
     c = Case(kb, "bf16", [200, 1, 220, 170, 250], C, H, hkv, 64, 16, seed=6)
