@@ -3,7 +3,9 @@
 Same names as the C ABI in ``include/pagedkv.h``. Device arguments are torch
 CUDA tensors (PyTorch supplies device memory and streams); every step of the
 path runs in the library's kernels. A missing library or a non-zero status
-raises: there is no fallback.
+raises: there is no fallback. The calls that a step makes once a layer hand
+plain arguments to the library through _marshal.so (csrc/python/marshal.cpp),
+the others, and whatever is not plain, through ctypes.
 """
 
 from __future__ import annotations
@@ -122,6 +124,7 @@ class StepInfo(ctypes.Structure):
                 ("meta_ints", ctypes.c_int)]
 
 _lib = None
+_addresses = {}
 
 
 class KvpError(RuntimeError):
@@ -145,8 +148,35 @@ def lib():
             fn = getattr(L, name)
             fn.argtypes = args
             fn.restype = ctypes.c_int
+        _addresses.clear()
         _lib = L
     return _lib
+
+
+_marshal = None
+
+
+def _native():
+    """The argument marshalling in C++ (_marshal.so, built with the library), None where another library stands in for it."""
+    global _marshal
+    if lib() is not _lib:
+        return None
+    if _marshal is None:
+        try:
+            from . import _marshal as m
+        except ImportError as e:
+            raise RuntimeError(f"_marshal.so cannot be loaded ({e}): build it first (python -c 'import __graft_entry__ as g; "
+                               "g.build()')") from e
+        _marshal = m
+    return _marshal
+
+
+def _address(what):
+    """The address of a function of the library."""
+    a = _addresses.get(what)
+    if a is None:
+        a = _addresses[what] = ctypes.cast(getattr(lib(), what), ctypes.c_void_p).value
+    return a
 
 
 def _check(code, what):
@@ -465,6 +495,17 @@ def _rotary_call(what, pool, layer, q, first, second, positions, out_loc, rope, 
     dt, dev = _TORCH_DTYPE[pool.dtype], pool.device_index
     axes = 1 if rope is None else getattr(rope, "axes", 1)
     k, v = first[0], second[0]
+    native = _native()
+    if native is not None:
+        on_axes = axes > 1 or always_axes
+        name = what if always_axes or axes == 1 else what + "_axes"
+        of_plan = ((None, None, 1, 0, 0, 1.0) if rope is None else
+                   (rope.freqs, rope.pair_axis, axes, rope.rotary_dim, rope.layout, rope.attn_factor))
+        code = native.rotary(_address(name), 1 if on_axes else 0, pool.handle.value, pool.dtype, dev, layer, q, k, first[2],
+                             first[3], v, second[2], second[3], positions, out_loc, *of_plan, q_out, width,
+                             None if stream is None else _raw_stream(stream))
+        if code is not None:
+            return _check(code, name)
     if (k is None) != (v is None):
         raise ValueError(f"{first[1]} and {second[1]} come together")
     freqs = of_pair = rot = layout = pos = apart = 0
@@ -551,6 +592,12 @@ def load_cache_fp4(pool, layer, slots, k_out, v_out, stream=None):
     """The rows of a Fp4Pool at ``slots`` (int32 [n], any order) as the values
     they stand for: k_out, v_out [n, kv_heads, D] contiguous, pool dtype."""
     dt, dev = _TORCH_DTYPE[pool.dtype], pool.device_index
+    native = _native()
+    if native is not None:
+        code = native.load(_address("load_cache_fp4"), pool.handle.value, pool.dtype, dev, layer, slots, k_out, v_out,
+                           pool.kv_heads * pool.head_dim, None if stream is None else _raw_stream(stream))
+        if code is not None:
+            return _check(code, "load_cache_fp4")
     n = _on(slots, dev, torch.int32, "slots").numel()
     for t, name in ((k_out, "k_out"), (v_out, "v_out")):
         if _on(t, dev, dt, name).numel() != n * pool.kv_heads * pool.head_dim:
@@ -579,6 +626,13 @@ def paged_fp4_attention(pool, layer, q, table, table_mode, context_lens, window,
     ``max_context``: a bound of context_lens (None: what the table holds), the
     one the workspace was made for. See include/pagedkv.h."""
     dt, dev = _TORCH_DTYPE[pool.dtype], pool.device_index
+    native = _native()
+    if native is not None:
+        code = native.attend(_address("paged_fp4_attention"), pool.handle.value, pool.dtype, dev, pool.head_dim, pool.page_size,
+                             layer, q, q_lens, table, table_mode, table_rows, context_lens, max_context, window or 0, sinks, scale,
+                             out, workspace, None if stream is None else _raw_stream(stream))
+        if code is not None:
+            return _check(code, "paged_fp4_attention")
     _on(q, dev, dt, "q")
     _on(out, dev, dt, "out")
     _on(table, dev, torch.int32, "table")
@@ -597,9 +651,10 @@ def paged_fp4_attention(pool, layer, q, table, table_mode, context_lens, window,
         raise ValueError("context_lens must be [B], table [rows, columns]")
     rows, cols = table.shape
     if max_context is None:
-        max_context = min(cols if table_mode == KVP_RAW_LOCATIONS else cols * pool.page_size, (1 << 31) - 1)
+        max_context = cols if table_mode == KVP_RAW_LOCATIONS else cols * pool.page_size
+    max_context = min(int(max_context), (1 << 31) - 1)
     _check(lib().paged_fp4_attention(pool.handle, layer, q.data_ptr(), B, C, Hq, per[0], table.data_ptr(), rows, cols,
-                                     table_mode, per[1], context_lens.data_ptr(), int(max_context), int(window or 0),
+                                     table_mode, per[1], context_lens.data_ptr(), max_context, int(window or 0),
                                      int(sinks), float(scale), out.data_ptr(), _on(workspace, dev, None, "workspace").data_ptr(),
                                      workspace.nbytes, _raw_stream(stream)), "paged_fp4_attention")
 

@@ -1,7 +1,9 @@
 """Build libpagedkv.so in-tree (nvcc for sm_103a, g++ for the host bookkeeping).
 
 Objects go to ``_build/`` next to this file; the library to
-``libpagedkv.so`` next to this file. Translation units compile in parallel
+``libpagedkv.so`` next to this file, and the binding's argument marshalling
+(``csrc/python/marshal.cpp``, against Python's and torch's headers) to
+``_marshal.so``. Translation units compile in parallel
 and only when a source or header is newer than the library.
 ``build_traced()`` builds the tracing variant of the prefill kernel
 (``-DKVP_PREFILL_TRACE``) as ``libpagedkv_trace.so`` from objects in
@@ -24,6 +26,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libpagedkv.so")
 TRACE_LIB = os.path.join(HERE, "libpagedkv_trace.so")
+MARSHAL_SRC = os.path.join(CSRC, "python", "marshal.cpp")
+MARSHAL = os.path.join(HERE, "_marshal.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -57,11 +61,33 @@ def _run(cmd):
     return r.stdout + r.stderr
 
 
+def build_marshal(force: bool = False) -> str:
+    """Compile the binding's argument marshalling; returns its path."""
+    if not force and os.path.exists(MARSHAL) and os.path.getmtime(MARSHAL) > os.path.getmtime(MARSHAL_SRC):
+        return MARSHAL
+    import sysconfig
+
+    import torch
+
+    home = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    tmp = MARSHAL + ".tmp"
+    _run(["g++", "-O2", "-std=c++20", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"], "-I", os.path.join(home, "include"),
+          "-I", os.path.join(home, "include", "torch", "csrc", "api", "include"), "-I", os.path.join(cuda, "include"),
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", MARSHAL_SRC, "-o", tmp,
+          "-L", os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+          "-Wl,-rpath," + os.path.join(home, "lib")])
+    os.replace(tmp, MARSHAL)
+    return MARSHAL
+
+
 def build(force: bool = False, verbose: bool = False, lib: str = LIB, objdir: str = BUILD,
           defines: tuple = ()) -> str:
     """Compile every translation unit and link ``lib`` (libpagedkv.so by
-    default); returns its path."""
+    default, the argument marshalling beside it); returns its path."""
     if not force and not needs_build(lib):
+        if lib == LIB:
+            build_marshal()
         return lib
     os.makedirs(objdir, exist_ok=True)
     nvcc = _nvcc()
@@ -75,7 +101,10 @@ def build(force: bool = False, verbose: bool = False, lib: str = LIB, objdir: st
             cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-I", INCLUDE, "-c", src, "-o", obj]
         jobs.append((cmd, obj))
     with ThreadPoolExecutor(max_workers=min(8, len(jobs))) as ex:
+        marshal = ex.submit(build_marshal, force) if lib == LIB else None
         logs = list(ex.map(lambda j: _run(j[0]), jobs))
+        if marshal:
+            marshal.result()
     if verbose:
         for log in logs:
             sys.stdout.write(log)
