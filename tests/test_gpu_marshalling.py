@@ -44,13 +44,13 @@ def rnd(*shape, dtype=torch.bfloat16, seed=1):
     return torch.randn(shape, generator=torch.Generator().manual_seed(seed)).to(dtype).to(DEV)
 
 
-@pytest.mark.parametrize("kind", ["cache", "axes", "latent", "fp4", "as they are"])
+KINDS = [(kind, part) for kind in ("cache", "axes", "latent", "fp4") for part in ("all", "queries", "rows")] + [("as they are", "rows")]
+
+
+@pytest.mark.parametrize("kind,part", KINDS)
 @pytest.mark.parametrize("n", [0, 1, 5])
-@pytest.mark.parametrize("part", ["all", "queries", "rows"])
 @pytest.mark.parametrize("strided", [False, True])
 def test_rotary_stores(kb, monkeypatch, kind, n, part, strided):
-    if kind == "as they are" and part != "rows":
-        pytest.skip("rows only")
     D, H, hkv, dc = 64, 6, 2, 32
     sections = (10, 10, 12) if kind in ("axes", "fp4") else None
     plan = kb.RotaryPlan(D, sections=sections, attn_factor=1.5)
