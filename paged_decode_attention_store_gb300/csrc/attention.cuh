@@ -211,7 +211,7 @@ struct Fp4Call {
 bool fp4_tc_eligible(const kvp_pool* pool, int C, int H);
 size_t fp4_tc_workspace(const kvp_pool* pool, int C, int H);
 int launch_fp4_tc(const Fp4Call& c, cudaStream_t stream);
-// Every other shape of a bf16 pool (fp4_tile.cu).
+// The other shapes of a bf16 pool, and few short contexts (fp4_tile.cu).
 int launch_fp4_tile(const Fp4Call& c, cudaStream_t stream);
 // A chunk's requests of lengths ``lens`` (0: none) with a mark again, head_dim 128: nan [B][blocks], a mark for ``rows`` rows.
 int launch_fp4_again(const Fp4Call& c, const int32_t* lens, const int32_t* nan, int blocks, int rows, cudaStream_t stream);
