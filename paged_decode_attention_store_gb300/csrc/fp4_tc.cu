@@ -633,7 +633,7 @@ __device__ __forceinline__ void weights(const Args& a, const Stage& g, const Par
 #pragma unroll
       for (int sh = 4; sh < 32; sh <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, sh));
       mx[nt][e] = fminf(__fmul_rn(v, z.f[nt][e]), 3.0e38f);  // finite: a product beyond it gives an infinite weight, and a NaN
-      grow |= mx[nt][e] > z.m[nt][e] + 8.f;
+      grow |= mx[nt][e] - z.m[nt][e] > 8.f;  // the difference is exact where scores are large; a sum with 8 is not
     }
   if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll

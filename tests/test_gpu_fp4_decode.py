@@ -1,0 +1,69 @@
+"""The decode kernel of four-bit pools at its edges. Contexts are bounded above 256 rows, where short ones go to the tile
+kernel, unless a case is about both."""
+
+import math
+
+import pytest
+import torch
+
+import fp4_reference as F
+import operator_reference as R
+from test_gpu_fp4_attention import DEV, Case, kb  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+LOG2E = math.log2(math.e)
+FAR = 1000  # a bound of the lengths that keeps few short contexts with the decode kernel
+
+
+def bounded(c, most, fill=0x3C):
+    c.most = most
+    c.ws = c.kb.alloc_fp4_workspace(c.pool, len(c.lens), c.C, c.H, most, device=DEV)
+    c.ws.fill_(fill)
+    return c
+
+
+def rewrite(c, k, v):
+    """Every request's rows: the first of k, v [L, D], the same for every head."""
+    each = lambda x: x.to(c.dt).to(DEV)[:, None].expand(-1, c.hkv, -1).contiguous()  # noqa: E731
+    for sl in c.slots:
+        c.kb.store_cache_fp4(c.pool, c.layer, each(k[:len(sl)]), each(v[:len(sl)]), torch.tensor(sl, dtype=torch.int32, device=DEV))
+    c.read()
+
+
+def scale_for(factor):
+    """A scale whose product with log2(e) is ``factor`` (a power of two) in fp32."""
+    log2e = torch.tensor(LOG2E, dtype=torch.float32)
+    s = torch.tensor(factor / LOG2E, dtype=torch.float32)
+    for step in (0.0, math.inf, -math.inf):
+        x = s if step == 0.0 else torch.nextafter(s, torch.tensor(step))
+        if float(x * log2e) == factor:
+            return float(x)
+    raise AssertionError("no such scale")
+
+
+@pytest.mark.parametrize("C,raw", [(1, False), (4, False), (1, True)])
+def test_scores_a_step_of_fp32_apart(kb, C, raw):  # noqa: F811
+    """Scores about 2^27 in log2, where fp32's step is 16: the maximum rises by one step from a stage of 32 rows to the
+    next. A row 16 below the maximum weighs 2^-16."""
+    L = 320  # of so many requests that a piece of the work is several stages
+    c = bounded(Case(kb, "bf16", [L] * 200, C, 8, 8, 128, 1 if raw else 16, raw, seed=1), FAR)
+    k, v = torch.zeros(L, 128), torch.randn(L, 128, generator=torch.Generator().manual_seed(2))
+    k[:, 0] = k[:, 1] = 1024.0
+    k[:, 16] = 2.0 ** -4
+    k[:, 15], k[:, 31] = 6 * 256.0, 6 * 2.0 ** -3  # these only make the blocks' scales 256 and 2^-3
+    k[160:, 16] = 2.0 ** -3  # q . k is 2048 + 2^-12 in the first 160 rows, then 2048 + 2^-11
+    rewrite(c, k, v)
+    assert torch.equal(c.k[c.slots[0], 0], k.double())
+    c.q.zero_()
+    c.q[..., 0] = c.q[..., 1] = 1.0
+    c.q[..., 16] = 2.0 ** -8
+    c.scale = scale_for(2.0 ** 16)
+    c.run()
+    out, vals = c.out.double().cpu(), c.v[c.slots[0], 0]
+    for j in range(C):
+        s = torch.where(torch.arange(L) < 160, 0.0, 16.0)[:L - C + j + 1]
+        w = torch.exp2(s - 16)
+        want = (w[:, None] * vals[:len(w)]).sum(0) / w.sum()
+        # the weights are powers of two: what is left is the fp32 sums and the result's rounding
+        bound = R.u(torch.bfloat16) * want.abs() + 2 * (len(w) + 16) * R.U32 * vals.abs().amax(0)
+        R.check(out[:, j], want.expand(200, 8, -1), bound.expand(200, 8, -1), f"query {j}")
