@@ -4,8 +4,8 @@
 // scale. Such an entry has six significant bits at most and lies between 2^-10 and 2688: exact in fp16, so both products
 // run on fp16 operands with fp32 accumulators, K and V without any rounding. A query row is scaled by a power of two to
 // at most 2 and held in fp16 (its eight bits fit; entries below 2^-14 of the largest are off by 2^-25 of it, as the fp32
-// sums are). The weights are rounded once to fp16 (half a step, 2^-11; they are an operand of the second product), their
-// sum keeps them in fp32.
+// sums are). The weights are rounded once to fp16 (half a step, 2^-11, or 2^-32 of the largest if that is more; they are an
+// operand of the second product), their sum keeps them in fp32.
 //
 // What bounds it. A token and head is 144 bytes, K and V, and its 256 entries have to become fp16 pairs. An SM streams 23
 // bytes a clock (45 GB/s of 6.8 TB/s): 32 positions of eight heads in 1,660 clocks, 0.80 us. For such a stage each of the
@@ -20,8 +20,9 @@
 //   are the entries' even ones, so that a lane ends with 16 consecutive outputs.
 // * Which token is row r of a tile is free too: r for even r, r ^ 4 for odd ones, so that with the 128-byte swizzle both
 //   K's loads (two tokens at a time) and V's (four) touch different banks.
-// * Softmax over 32 tokens at once; the running maximum is raised only when it grows by more than 8 (in log2), as P <=
-//   256 fits fp16, so O is seldom rescaled.
+// * Softmax over 32 tokens at once; weights are taken against a reference, the maximum less 7 (in log2), that is raised only
+//   when a score is more than 15 above it, as 2^15 fits fp16: O is seldom rescaled, and a weight still counts down to 2^-32 of
+//   the largest (against the maximum itself, thousands of rows at 2^-26 of one were lost from O while the sum had them).
 //
 // How. The work is the batch's blocks of 32 positions (aligned, of the union of the request's queries' spans) laid end to
 // end and divided evenly over the CTAs; a cut request leaves fp32 partials that a second launch joins in CTA order, so
@@ -544,7 +545,9 @@ __device__ __forceinline__ bool attends(const Column& q, int t) { return t <= q.
 template <int NT>
 struct State {
   float o[8][NT][4];                  // O^T
-  float m[NT][2], l[NT][2], f[NT][2]; // of its columns: running maximum (log2), this lane's part of the sum, score's factor
+  // of its columns: the reference (log2: the running maximum less 7, 8 further behind at most), this lane's part of the sum
+  // of weights 2^(score - reference), the score's factor
+  float m[NT][2], l[NT][2], f[NT][2];
 };
 
 // Where a lane's K and V of the first tile lie: rows of 128 bytes, head-major and swizzled (chunk ^ token % 8), or token by
@@ -623,6 +626,7 @@ __device__ __forceinline__ void weights(const Args& a, const Stage& g, const Par
           }
       }
   }
+  constexpr float kBelow = 7.f, kMost = 15.f;
   float mx[NT][2];
   bool grow = false;
 #pragma unroll
@@ -633,14 +637,14 @@ __device__ __forceinline__ void weights(const Args& a, const Stage& g, const Par
 #pragma unroll
       for (int sh = 4; sh < 32; sh <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, sh));
       mx[nt][e] = fminf(__fmul_rn(v, z.f[nt][e]), 3.0e38f);  // finite: a product beyond it gives an infinite weight, and a NaN
-      grow |= mx[nt][e] - z.m[nt][e] > 8.f;  // the difference is exact where scores are large; a sum with 8 is not
+      grow |= mx[nt][e] - z.m[nt][e] > kMost;  // the difference is exact where scores are large; a sum is not
     }
   if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float mn = fmaxf(z.m[nt][e], mx[nt][e]);
+        const float mn = fmaxf(z.m[nt][e], mx[nt][e] - kBelow);
         const float al = z.m[nt][e] == -INFINITY ? 0.f : ex2(z.m[nt][e] - mn);
         z.m[nt][e] = mn;
         z.l[nt][e] *= al;

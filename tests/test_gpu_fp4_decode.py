@@ -67,3 +67,26 @@ def test_scores_a_step_of_fp32_apart(kb, C, raw):  # noqa: F811
         # the weights are powers of two: what is left is the fp32 sums and the result's rounding
         bound = R.u(torch.bfloat16) * want.abs() + 2 * (len(w) + 16) * R.U32 * vals.abs().amax(0)
         R.check(out[:, j], want.expand(200, 8, -1), bound.expand(200, 8, -1), f"query {j}")
+
+
+@pytest.mark.parametrize("C,at", [(1, 0), (1, 1500), (1, 2999), (4, 0), (4, 1500)])
+@pytest.mark.parametrize("gap", [26.5, 30.0])
+def test_many_rows_far_below_one(kb, C, at, gap):  # noqa: F811
+    """One row far above thousands that weigh 2^-gap each and alone have values: they are the result, whether the one
+    comes first, in the middle or last."""
+    L, B = 3000, 40
+    c = Case(kb, "bf16", [L] * B, C, 8, 2, 128, 16, seed=1)
+    k, v = torch.zeros(L, 128), torch.rand(L, 128, generator=torch.Generator().manual_seed(2)) + 0.5
+    k[:, 0], k[at, 0], v[at] = 1.0, 6.0, 0.0
+    rewrite(c, k, v)
+    c.q.zero_()
+    c.q[..., 0] = 1.0
+    c.scale = gap / 5 / LOG2E
+    c.run()
+    for j in range(C):
+        p = L - C + j
+        sl = torch.tensor(c.slots[0][:p + 1])
+        want, bound = F.attend(c.q[0, j, :1].double().cpu(), c.k[sl, 0], c.v[sl, 0], c.scale, c.dt)
+        # a weight is off by half a step of fp16, or, below 2^-14 of a largest one that is 2^7 at least, by 2^-32 of that
+        bound = bound + (2.0 ** -32 - 2.0 ** -25) * (p + 1) * c.v[sl, 0].abs().amax()
+        R.check(c.out[:, j].cpu(), want.expand(B, 8, -1), bound.expand(B, 8, -1), f"query {j}")
