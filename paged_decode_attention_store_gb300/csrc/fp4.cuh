@@ -140,7 +140,8 @@ __device__ __forceinline__ void fp4_block16(const float (&x)[16], float g, float
 
 // The same from a lane's N entries that are off by ex at most; exact(i) gives its entry i to 52 bits. It is asked for where a
 // rounding lies within the error of a border: for the entries that may be the largest when it is the scale's, for the one
-// entry when it is a code's.
+// entry when it is a code's. Where an entry is not finite in 32 bits, for all: a sum of two may pass their range and be finite,
+// and the block is NaN only if one is not.
 template <int N, typename Exact>
 __device__ __forceinline__ void fp4_block_within(const float (&x)[N], float ex, float g, float inv_g, unsigned mask,
                                                  const Exact& exact, uint32_t& codes, uint32_t& scale) {
@@ -149,18 +150,27 @@ __device__ __forceinline__ void fp4_block_within(const float (&x)[N], float ex, 
 #pragma unroll
   for (int d = 1; d < kLanes; d <<= 1) ex = fmaxf(ex, __shfl_xor_sync(mask, ex, d));
   codes = 0;
-  scale = kFp4NanScale;
-  if (mb >= kInfBits) return;
+  const bool far = mb >= kInfBits;
   const float m = __uint_as_float(mb), q = m * inv_g * (1.f / 6.f), eq = ex * inv_g * (1.f / 6.f) + q * 0x1p-22f;
   scale = e4m3_code(fmaxf(q - eq, 0.f));
-  if (scale != e4m3_code(q + eq)) {
-    uint32_t largest = 0;
+  if (far || scale != e4m3_code(q + eq)) {
+    uint32_t largest = far ? (1u << N) - 1u : 0u;
 #pragma unroll
     for (int i = 0; i < N; ++i) largest |= fabsf(x[i]) + ex >= m - ex ? 1u << i : 0u;
     double md = 0.0;
-    for (; largest; largest &= largest - 1) md = fmax(md, fabs(exact(__ffs(largest) - 1)));
+    for (; largest; largest &= largest - 1) {
+      const double v = fabs(exact(__ffs(largest) - 1));
+      md = v > md || v != v ? v : md;  // a NaN stays
+    }
 #pragma unroll
-    for (int d = 1; d < kLanes; d <<= 1) md = fmax(md, __shfl_xor_sync(mask, md, d));
+    for (int d = 1; d < kLanes; d <<= 1) {
+      const double v = __shfl_xor_sync(mask, md, d);
+      md = v > md || v != v ? v : md;
+    }
+    if (!(md < INFINITY)) {
+      scale = kFp4NanScale;
+      return;
+    }
     scale = fp4_scale_exact(md, g, inv_g);
   }
   if (scale == 0) return;
@@ -173,7 +183,7 @@ __device__ __forceinline__ void fp4_block_within(const float (&x)[N], float ex, 
     codes |= e2m1x2(r0 - e, r1 - e) << (4 * i);
     other |= e2m1x2(r0 + e, r1 + e) << (4 * i);
   }
-  for (uint32_t open = codes ^ other; open;) {
+  for (uint32_t open = far ? 0xffffffffu >> (32 - 4 * N) : codes ^ other; open;) {
     const int i = (__ffs(open) - 1) >> 2;
     const double v = exact(i);
     const uint32_t c = fp4_code_exact(fabs(v), sg) | (v < 0.0 ? 8u : 0u);
