@@ -661,7 +661,8 @@ bool rotary_args_ok(const kvp_pool* pool, int layer, const void* q, long long q_
   if (ax.count < 1 || ax.count > KVP_ROTARY_MAX_AXES) return false;
   if (n == 0) return true;  // empty tensors may have no address
   if ((k == nullptr) != (v == nullptr) || (!q && !k)) return false;
-  if ((!positions && (q || rotary_dim > 0)) || (rotary_dim > 0 && !freqs)) return false;
+  // rows as they are into a four-bit pool need no positions; the kernels of other pools read them whatever turns
+  if ((!positions && (!pool->fp4 || q || rotary_dim > 0)) || (rotary_dim > 0 && !freqs)) return false;
   if (ax.count != 1 && (rotary_dim > 0 && !ax.of_pair)) return false;
   if (ax.count > 1 && ax.stride < n) return false;
   if (k && (!out_loc || k_stride < 0 || v_stride < 0)) return false;
