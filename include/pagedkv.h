@@ -121,7 +121,8 @@ int kv_latent_pool_create(int num_pages, int page_size, int latent_dim,
  * kv_fp4_pool_create: describe a caller-owned cache of K and V in four bits. A
  * block is 16 consecutive entries of one head's K or V of one token; an entry
  * stands for code * scale * g: code e2m1 (bit 3 the sign, then 0, 0.5, 1, 1.5,
- * 2, 3, 4, 6), scale e4m3 of the block, g a power of two per layer and plane.
+ * 2, 3, 4, 6), scale e4m3 of the block (0x7f and 0xff: NaN), g a power of two per
+ * layer and plane.
  *   codes   device bytes (num_layers, num_pages, page_size, kv_heads, 2,
  *           head_dim / 2): K, then V; entry 2 i is the low half of byte i.
  *   scales  device bytes (num_layers, ceil(num_pages * page_size / 16),

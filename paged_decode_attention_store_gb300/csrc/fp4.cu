@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(kLoadThreads) unpack_kernel(const __grid_const
             c[0] = __ldg(reinterpret_cast<const uint32_t*>(from));
           }
           const uint32_t s = __ldg(scales + fp4_scale_offset(slot, h, a.heads, a.d));
-          nan |= s == kFp4NanScale;
+          nan |= fp4_is_nan(s);
 #pragma unroll
           for (int i = 0; i < kWords; ++i) fp4_entries(c[i], s, g, x[i]);
         } else if (CHUNK) {
@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(32 * kF32Warps, I == 1 ? 2 : 1) fp4_f32_kernel
       const int x = 2 * i + odd;
       if (16 * x >= D) break;
       uint32_t sc = scales[i / 4] >> (8 * (i & 3)) & 0xffu;
-      if (is_v && sc == kFp4NanScale) {
+      if (is_v && fp4_is_nan(sc)) {
         bad |= 1u << x;
         sc = 0;
       }

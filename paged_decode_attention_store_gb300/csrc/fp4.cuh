@@ -2,7 +2,7 @@
 //
 // A block is 16 consecutive entries of one head's K or V of one token: 16
 // codes of 4 bits (e2m1: sign, then 0, 0.5, 1, 1.5, 2, 3, 4, 6) and one scale
-// (e4m3, never negative). An entry stands for code * scale * g, g a power of two
+// (e4m3, stored without a sign). An entry stands for code * scale * g, g a power of two
 // per layer and plane, so every value has six significant bits at most: exact in
 // bf16 and, without g, in fp16.
 //
@@ -70,6 +70,8 @@ __device__ __forceinline__ uint32_t fp4_code_exact(double ax, float sg) {
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 constexpr uint32_t kInfBits = 0x7f800000u;
 constexpr uint32_t kFp4NanScale = 0x7fu;
+// Whether a scale in a pool, which others may have filled, is NaN, of either sign.
+__device__ __forceinline__ bool fp4_is_nan(uint32_t scale) { return (scale & 0x7fu) == kFp4NanScale; }
 
 // The largest of a block's entries by its bits, over the 16 / N neighbouring lanes (``mask``) that hold N each.
 template <int N>

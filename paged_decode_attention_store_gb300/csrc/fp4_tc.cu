@@ -696,7 +696,7 @@ __device__ __forceinline__ void values(const Args& a, const Smem& s, const Stage
       uint32_t who = 0;  // tokens whose block g is NaN; their scale is zero from here on
 #pragma unroll
       for (int y = 0; y < 4; ++y)
-        if ((two >> (8 * y) & 0xff) == kFp4NanScale) {
+        if (fp4_is_nan(two >> (8 * y))) {
           who |= 1u << ((y & 1 ? p.vt1 : p.vt0) + (y & 2 ? 8 : 0));
           if (y < 2) sc0 &= y ? 0xffu : 0xff00u;
           else sc1 &= y & 1 ? 0xffu : 0xff00u;

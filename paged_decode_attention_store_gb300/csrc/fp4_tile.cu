@@ -116,7 +116,7 @@ __device__ __forceinline__ uint32_t turn(const Row<DT>& r, int D, bool v, unsign
     if (16 * i >= D) break;
     const uint4 c = r.codes[i / 2];
     uint32_t s = r.scales[i / 4] >> (8 * (i & 3)) & 0xffu;
-    if (v && s == kFp4NanScale) {
+    if (v && fp4_is_nan(s)) {
       nan |= 1u << i;
       s = 0;
     }
