@@ -232,6 +232,7 @@ class PagedKVCache:
         r = np.ascontiguousarray(rids, dtype=np.int32)
         ctx = self.lengths[r] + M
         out_loc = self.append(np.repeat(r, M))
+        bound = self._bound_of(ctx)
         lens = self._to_device(ctx)
         rows = self._to_device(r)
         host_out = not out[0].is_cuda
@@ -244,12 +245,16 @@ class PagedKVCache:
             self.store(layer, kd, vd, out_loc)
             od = torch.empty_like(qd) if host_out else out[layer]
             if kind == "verify":
-                self.verify(layer, qd, lens, window, scale, od, table_rows=rows, sinks=sinks)
+                self.verify(layer, qd, lens, window, scale, od, table_rows=rows, sinks=sinks, **bound)
             else:
-                self.prefill(layer, qd, lens, window, scale, od, table_rows=rows, sinks=sinks)
+                self.prefill(layer, qd, lens, window, scale, od, table_rows=rows, sinks=sinks, **bound)
             if host_out:
                 out[layer].copy_(od, non_blocking=True)
         torch.cuda.current_stream(self.dev).synchronize()
+
+    def _bound_of(self, lengths):
+        """What a step's attention is told of its requests' lengths."""
+        return {}
 
     def check(self):
         """Raise if a device-side error was recorded since the last check."""
@@ -563,26 +568,33 @@ class PagedFp4Cache(PagedKVCache):
             self._ws[self._largest] = torch.empty(self._largest, dtype=torch.uint8, device=self.dev)
         return self._ws[self._largest]
 
+    def _bound_of(self, lengths):
+        """A bound of these lengths, in steps of 256: the workspace of a chunk holds as many rows a request."""
+        return {"max_context": max(1, -(-int(lengths.max()) // 256)) * 256}
+
     def attend(self, layer, q, context_lens, window, scale, out, q_lens=None, table_rows=None, sinks=0, max_context=None):
         """Attention over the stored rows: q, out [B, Hq, D] (one token a
         request) or [B, C, Hq, D], query j of request b at position
         context_lens[b] - q_lens[b] + j (q_lens None: C). ``max_context``: a
-        bound of context_lens; None: the longest request's length so far, in
-        steps of 256 (a graph that is replayed with longer contexts gives
-        theirs)."""
+        bound of context_lens; None: the length of the cache's longest request
+        so far, in steps of 256 (a graph that is replayed with longer contexts
+        gives theirs; short requests beside a long one theirs, as chunks need a
+        workspace of as many rows a request). :meth:`step`, prefill_step and
+        verify_step give that of their own requests."""
         if q.dim() == 3:
             q, out = q[:, None], out[:, None]
         if max_context is None:
-            max_context = max(1, -(-int(self.lengths.max()) // 256)) * 256
+            max_context = self._bound_of(self.lengths)["max_context"]
         ws = self.workspace(q.shape[0], q.shape[2], q.shape[1], max_context)
         kb.paged_fp4_attention(self.pool, layer, q, self.table, self.table_mode, context_lens, window, scale, out, ws,
                                q_lens=q_lens, table_rows=table_rows, sinks=sinks, max_context=max_context)
 
-    def verify(self, layer, q, context_lens, window, scale, out, table_rows=None, sinks=0):
-        self.attend(layer, q, context_lens, window, scale, out, table_rows=table_rows, sinks=sinks)
+    def verify(self, layer, q, context_lens, window, scale, out, table_rows=None, sinks=0, max_context=None):
+        self.attend(layer, q, context_lens, window, scale, out, table_rows=table_rows, sinks=sinks, max_context=max_context)
 
-    def prefill(self, layer, q, context_lens, window, scale, out, q_lens=None, table_rows=None, sinks=0):
-        self.attend(layer, q, context_lens, window, scale, out, q_lens=q_lens, table_rows=table_rows, sinks=sinks)
+    def prefill(self, layer, q, context_lens, window, scale, out, q_lens=None, table_rows=None, sinks=0, max_context=None):
+        self.attend(layer, q, context_lens, window, scale, out, q_lens=q_lens, table_rows=table_rows, sinks=sinks,
+                    max_context=max_context)
 
     def step(self, rids, q, k, v, rope, out, window, scale, sinks=0, positions=None):
         """One step for requests ``rids``, all layers, C new tokens each (C = 1:
@@ -597,6 +609,7 @@ class PagedFp4Cache(PagedKVCache):
         B, C, Hq, D = q[0].shape
 
         def work(lens, rows, places, out_loc):
+            bound = self._bound_of(self.lengths[np.asarray(rids)])
             pos = positions
             if rope is not None and pos is None:
                 pos = _on_axes(places, rope)
@@ -605,7 +618,7 @@ class PagedFp4Cache(PagedKVCache):
                     self.store(layer, k[layer], v[layer], out_loc)
                 else:
                     self.rotary_store(layer, q[layer].view(B * C, Hq, D), k[layer], v[layer], pos, out_loc, rope)
-                self.attend(layer, q[layer], lens, window, scale, out[layer], table_rows=rows, sinks=sinks)
+                self.attend(layer, q[layer], lens, window, scale, out[layer], table_rows=rows, sinks=sinks, **bound)
 
         self._append_and(work, rids, B, C, window, sinks)
 
