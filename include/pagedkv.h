@@ -458,10 +458,16 @@ int load_cache_fp4(const kvp_pool* pool, int layer, const int32_t* slots, int n,
  *   out  device, likewise; rows j >= q_lens[b] are not written.
  *   q_lens  device int32 [batch], 1 <= q_lens[b] <= min(chunk, L), or NULL.
  *   max_context  a bound of context_lens that the host knows (an upper bound is
- *        fine); chunks need a workspace for as many rows a request.
+ *        fine).
  *   workspace  device, >= paged_fp4_attention_workspace_size() bytes, 256-byte
  *        aligned; contents need no initialisation and are clobbered; calls that
  *        may overlap on the GPU (captured graphs among them) need separate ones.
+ *        For chunks on the chunk kernel (bf16, head_dim 128, a group that divides
+ *        128, more than 64 (token, head) columns a KV head) it holds rows of
+ *        kv_heads * head_dim * 4 bytes, max_context of them for each request; 4 GiB
+ *        at most, through which the requests then go in groups. It does not shrink
+ *        with more requests or a higher bound: one for the largest call serves the
+ *        smaller ones of that chunk and those heads.
  * Device-detected errors set KVP_ERR_BAD_INDEX: the rows of a request whose
  * length (0, above max_context or the table's columns), q_lens entry or table
  * row is invalid are zero-filled; an attended table entry that is a hole or out

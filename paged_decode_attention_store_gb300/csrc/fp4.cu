@@ -8,7 +8,8 @@
 // once a call (16 chunks of 512 tokens: 975 us by fp4_tile.cu, 258 so). So a call
 // turns the attended rows into bf16 (exactly) in its workspace, request b's as
 // the one page b of a pool whose pages are as long as the longest context, and
-// runs the chunk kernel of bf16 pools (prefill_tc.cu) over them. Bytes: 1.1 KB
+// runs the chunk kernel of bf16 pools (prefill_tc.cu) over them, for as many
+// requests at a time as 4 GiB of rows hold. Bytes: 1.1 KB
 // read and 4 KB written a token of eight heads, and read again by the chunk
 // kernel, mostly from L2. Of the 258 us the unpacking takes 32, the chunk kernel
 // 221, the look for NaN 4; five prompts of 33-600 tokens 48 us (7, 38, 3).
@@ -560,16 +561,38 @@ kvp_pool chunk_pool(const kvp_pool* pool, int B, const ChunkLayout& l, char* ws)
   return p;
 }
 
-// Whether a call goes through the chunk kernel of bf16 pools. Up to 64 (token, head) columns a KV head are the decode
+// Rows turned back take 3.6 times the bytes that they have in the pool, and the longest context's for every request. So they
+// are bounded, and the requests of a call go through them in groups: 16 chunks of 512 tokens on 131,072 rows 14.8 ms (at once,
+// in 8 GiB, 14.7), 64 on 32,768 15.0 (14.5), 64 of 40 tokens on them 5.2 (4.6).
+constexpr size_t kChunkBytes = (size_t)4 << 30;
+
+// Requests of a group, 0 where not even one fits.
+int chunk_group(const kvp_pool* pool, int B, int longest) {
+  const long long page = ((long long)longest + 15) / 16 * 16;
+  const size_t each = 2 * sizeof(int32_t) + sizeof(int32_t) * (page / 2) + (size_t)page * pool->kv_heads * pool->head_dim * 4;
+  long long n = (long long)((kChunkBytes - 3 * 256) / each);  // the layout's parts are aligned to 256 bytes
+  if (n * page > 0x7fffffffLL) n = 0x7fffffffLL / page;
+  return (int)(n < 65535 ? (n < B ? n : B) : (B < 65535 ? B : 65535));
+}
+
+// Whether the chunk kernel of bf16 pools takes a call's shape.
+bool chunk_shape(const kvp_pool* pool, int B, int C, int H, float scale) {
+  const long long columns = (long long)C * (H / pool->kv_heads);
+  const bool few = columns <= kChunkColumns || (long long)B * pool->kv_heads < pool->num_sms;
+  return !(few && fp4_tc_eligible(pool, C, H)) && prefill_tc_eligible(pool, H, C, scale);
+}
+
+// Whether a call goes through the chunk kernel. Up to 64 (token, head) columns a KV head are the decode
 // kernel's, which splits contexts over the SMs; it takes up to 128, and above 64 a CTA has one KV head alone. 64 requests of
 // 512-4096 rows, 8 KV heads, decode kernel against chunk kernel: 64 columns 229 and 348 us, 96 397 and 347. Where the chunk
 // kernel would have less than a CTA an SM, the decode kernel keeps them all: 4 requests, 128 columns 36 and 46 us.
+// Groups of requests that leave three of four SMs idle are the tile kernel's, which takes 3.8 times as long as the chunk kernel
+// on all of them (16 chunks of 512 tokens) and has all requests at once; so is a request whose rows do not fit.
 bool chunk_eligible(const kvp_pool* pool, int B, int C, int H, int longest, float scale) {
-  const long long columns = (long long)C * (H / pool->kv_heads);
-  const bool few = columns <= kChunkColumns || (long long)B * pool->kv_heads < pool->num_sms;
-  if (few && fp4_tc_eligible(pool, C, H)) return false;
-  return pool->dtype == KVP_BF16 && (long long)B * (((long long)longest + 15) / 16 * 16) <= 0x7fffffffLL && B <= 65535 &&
-         prefill_tc_eligible(pool, H, C, scale);
+  if (!chunk_shape(pool, B, C, H, scale)) return false;
+  const int group = chunk_group(pool, B, longest), G = H / pool->kv_heads;
+  const long long tiles = ((long long)C * G + 127) / 128;
+  return group >= B || (group > 0 && 4 * group * tiles * pool->kv_heads >= pool->num_sms);
 }
 
 // Few query tokens of few short contexts: the tile kernel's one launch, whose clusters join their parts, before the decode
@@ -579,6 +602,24 @@ bool chunk_eligible(const kvp_pool* pool, int B, int C, int H, int longest, floa
 bool short_eligible(const kvp_pool* pool, int B, int C, int H, int longest) {
   return pool->dtype == KVP_BF16 && (long long)C * (H / pool->kv_heads) <= 16 && longest <= 256 &&
          (long long)B * pool->kv_heads <= pool->num_sms;
+}
+
+// Requests b0 .. b0 + n - 1 of a call as one of its own.
+Fp4Call requests_of(const Fp4Call& all, int b0, int n) {
+  Fp4Call c = all;
+  const size_t at = (size_t)b0 * c.C * c.H * c.pool->head_dim * c.pool->elem;
+  c.q = static_cast<const char*>(c.q) + at;
+  c.out = static_cast<char*>(c.out) + at;
+  c.B = n;
+  c.context_lens += b0;
+  if (c.q_lens) c.q_lens += b0;
+  if (c.table_rows) {
+    c.table_rows += b0;
+  } else {  // request b's row is b
+    c.T.table += (size_t)b0 * c.T.cols;
+    c.T.rows_total -= b0;
+  }
+  return c;
 }
 
 int launch_chunk(const Fp4Call& c, int longest, cudaStream_t st) {
@@ -636,8 +677,10 @@ extern "C" int paged_fp4_attention_workspace_size(const kvp_pool* pool, int batc
   if (!bytes || !shape_ok(pool, batch, chunk, num_q_heads, max_context)) return KVP_ERR_INVALID_ARG;
   // whatever the scale's sign, which decides between chunk kernel and the others
   size_t need = fp4_tc_workspace(pool, chunk, num_q_heads);
-  if (chunk_eligible(pool, batch, chunk, num_q_heads, max_context, 1.f)) {
-    const size_t rows = chunk_layout(pool, batch, max_context).total;
+  if (chunk_shape(pool, batch, chunk, num_q_heads, 1.f)) {
+    // no less than for fewer requests or a lower bound, which may fit where these do not
+    const bool fits = chunk_group(pool, batch, max_context) >= batch;
+    const size_t rows = fits ? chunk_layout(pool, batch, max_context).total : kChunkBytes;
     if (rows > need) need = rows;
   }
   *bytes = need ? need : 256;  // the other kernels need none
@@ -680,7 +723,14 @@ extern "C" int paged_fp4_attention(const kvp_pool* pool, int layer, const void* 
   c.scale = scale;
   c.workspace = workspace;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (chunk_eligible(pool, batch, chunk, num_q_heads, max_context, scale)) return launch_chunk(c, max_context, st);
+  if (chunk_eligible(pool, batch, chunk, num_q_heads, max_context, scale)) {
+    const int group = chunk_group(pool, batch, max_context);
+    for (int b0 = 0; b0 < batch; b0 += group) {
+      const int rc = launch_chunk(requests_of(c, b0, batch - b0 < group ? batch - b0 : group), max_context, st);
+      if (rc != KVP_OK) return rc;
+    }
+    return KVP_OK;
+  }
   if (fp4_tc_eligible(pool, chunk, num_q_heads) && !short_eligible(pool, batch, chunk, num_q_heads, max_context))
     return launch_fp4_tc(c, st);
   return pool->dtype == KVP_BF16 ? launch_fp4_tile(c, st) : launch_f32(c, st);
