@@ -295,6 +295,41 @@ PyObject* attend(PyObject*, PyObject* const* args, Py_ssize_t count) {
   });
 }
 
+// Tensor ``i`` of a list or tuple.
+const at::Tensor* item(PyObject* list, Py_ssize_t i) {
+  PyObject* o = nullptr;
+  if (PyList_CheckExact(list) && i < PyList_GET_SIZE(list)) o = PyList_GET_ITEM(list, i);
+  else if (PyTuple_CheckExact(list) && i < PyTuple_GET_SIZE(list)) o = PyTuple_GET_ITEM(list, i);
+  return o && THPVariable_CheckExact(o) ? &THPVariable_Unpack(o) : nullptr;
+}
+
+// (dtype, device, layers, q, out, k, v, B, C, heads, K/V heads, head_dim): whether every layer's tensors are what a four-bit
+// cache's step takes; None where one is not, or is nothing plain.
+PyObject* step(PyObject*, PyObject* const* args, Py_ssize_t count) {
+  return guarded([&]() -> PyObject* {
+    Args a{args, count};
+    const Where w = where(a);
+    const long long layers = a.integer();
+    PyObject *q = a.next(), *out = a.next(), *k = a.next(), *v = a.next();
+    const long long B = a.integer(), C = a.integer(), H = a.integer(), hkv = a.integer(), D = a.integer();
+    if (!a.ok || a.left) return none();
+    for (long long l = 0; l < layers; ++l) {
+      for (PyObject* list : {q, out}) {
+        const at::Tensor* t = item(list, l);
+        if (!w.holds(t) || t->dim() != 4 || t->size(0) != B || t->size(1) != C || t->size(2) != H || t->size(3) != D ||
+            !t->is_contiguous() || (reinterpret_cast<uintptr_t>(t->data_ptr()) & 15))
+          return none();
+      }
+      for (PyObject* list : {k, v}) {
+        const at::Tensor* t = item(list, l);
+        long long stride;
+        if (!w.holds(t) || !rows_view(t, w, B * C, hkv, D, &stride)) return none();
+      }
+    }
+    Py_RETURN_TRUE;
+  });
+}
+
 template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
 PyCFunction entry() {
   return reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(F));
@@ -303,6 +338,7 @@ PyCFunction entry() {
 PyMethodDef methods[] = {{"rotary", entry<rotary>(), METH_FASTCALL, nullptr},
                          {"load", entry<load>(), METH_FASTCALL, nullptr},
                          {"attend", entry<attend>(), METH_FASTCALL, nullptr},
+                         {"step", entry<step>(), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -596,6 +596,24 @@ class PagedFp4Cache(PagedKVCache):
         self.attend(layer, q, context_lens, window, scale, out, q_lens=q_lens, table_rows=table_rows, sinks=sinks,
                     max_context=max_context)
 
+    def _check_step(self, q, k, v, out, window, scale, sinks, max_context):
+        """Refuses what a layer's attention or a later layer would refuse, before the first turns its q in place."""
+        B, C, Hq, D = shape = q[0].shape
+        if scale != scale or sinks < 0 or (window and 0 < window <= sinks):
+            raise ValueError(f"scale, window and sinks cannot be {scale}, {window} and {sinks}")
+        self.workspace(B, Hq, C, max_context)
+        index = self.pool.device_index
+        native = kb._native()
+        if native is not None and native.step(self.pool.dtype, index, self.layers, q, out, k, v, B, C, Hq, self.Hkv, self.D):
+            return
+        for layer in range(self.layers):
+            for t, name in ((q[layer], "q"), (out[layer], "out")):
+                kb._on(t, index, self.tdt, name)
+                if t.shape != shape or D != self.D or t.data_ptr() % 16:
+                    raise ValueError(f"{name} must be [{B}, {C}, {Hq}, {self.D}] on 16 bytes in every layer, got {tuple(t.shape)}")
+            for t, name in ((k[layer], "k"), (v[layer], "v")):
+                kb._rows_view(t, index, self.tdt, name, B * C, self.Hkv, self.D)
+
     def step(self, rids, q, k, v, rope, out, window, scale, sinks=0, positions=None):
         """One step for requests ``rids``, all layers, C new tokens each (C = 1:
         decode): append, then per layer rotate, store and attend. Per-layer
@@ -604,12 +622,13 @@ class PagedFp4Cache(PagedKVCache):
         or [axes, B * C] for a plan of several axes; None: the tokens' places in
         their requests, on every axis. ``rope`` None: q and k as they are. With a
         window, the pages it leaves are released afterwards. A step that is
-        refused leaves the lengths and pages as they were. Asynchronous on the
-        current stream."""
+        refused leaves the lengths and pages as they were, and every layer's q.
+        Asynchronous on the current stream."""
         B, C, Hq, D = q[0].shape
+        bound = self._bound_of(self.lengths[np.ascontiguousarray(rids, dtype=np.int32)] + C)
+        self._check_step(q, k, v, out, window, scale, sinks, bound["max_context"])
 
         def work(lens, rows, places, out_loc):
-            bound = self._bound_of(self.lengths[np.asarray(rids)])
             pos = positions
             if rope is not None and pos is None:
                 pos = _on_axes(places, rope)

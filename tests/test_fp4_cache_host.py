@@ -74,3 +74,49 @@ def test_verify_and_prefill_take_a_bound(cache):
     cache.prefill(0, q, lens, 0, 0.125, q, q_lens=lens, max_context=96)
     cache.prefill(0, q, lens, 0, 0.125, q)  # without one: of the whole cache
     assert [m for _, m in attended(cache)] == [64, 96, 5120]
+
+
+def bad_steps():
+    short = lambda ts: [ts[0], ts[1][:, :1]]  # noqa: E731
+    q, k = rnd(1, 3, H, D), rnd(3, HKV, D)
+    odd = torch.zeros(3 * H * D + 1, dtype=torch.bfloat16)[1:].view(1, 3, H, D)
+    return {
+        "q of another shape": dict(q=short(q)), "q of another type": dict(q=[q[0], q[1].float()]),
+        "q that is not contiguous": dict(q=[q[0], torch.zeros((1, H, 3, D), dtype=torch.bfloat16).transpose(1, 2)]),
+        "q off 16 bytes": dict(q=[q[0], odd]), "q of one layer": dict(q=q[:1]), "q of no tensor": dict(q=[q[0], None]),
+        "out of another shape": dict(out=short(q)), "out of another type": dict(out=[q[0].float(), q[1]]),
+        "out off 16 bytes": dict(out=[odd, q[1]]), "out of one layer": dict(out=q[:1]),
+        "k of fewer tokens": dict(k=[k[0], k[1][:2]]), "v of other heads": dict(v=[k[0], k[1][:, :1]]),
+        "v of one layer": dict(v=k[:1]), "k of another type": dict(k=[k[0], k[1].float()]),
+        "rows of k apart": dict(k=[k[0], torch.zeros((3, HKV, 2 * D), dtype=torch.bfloat16)[..., ::2]]),
+        "scale": dict(scale=float("nan")), "sinks": dict(window=4, sinks=4), "fewer than none": dict(sinks=-1),
+        "width": dict(q=rnd(1, 3, H, D // 2), out=rnd(1, 3, H, D // 2)),
+    }
+
+
+@pytest.mark.parametrize("what", bad_steps())
+def test_a_refused_step_turns_no_queries(cache, what):
+    cache.new(0)
+    step(cache, [0], 20)
+    cache.calls.clear()
+    before = (cache.lengths.copy(), cache.host.used(), cache.host.block_row(0))
+    with pytest.raises((ValueError, TypeError, IndexError)):
+        step(cache, [0], 3, **bad_steps()[what])
+    assert [c[0] for c in cache.calls if c[0] not in ("size", "page_table_write")] == []
+    assert (cache.lengths == before[0]).all() and (cache.host.used(), cache.host.block_row(0)) == before[1:]
+    step(cache, [0], 3)
+    assert len(attended(cache)) == LAYERS
+
+
+def test_heads_that_do_not_divide(cache, monkeypatch):
+    """What the workspace's size refuses is refused before anything else."""
+    kb = ensure_built()
+    cache.new(0)
+
+    def refuse(*a):
+        raise kb.KvpError(kb.KVP_ERR_INVALID_ARG, "paged_fp4_attention_workspace_size")
+
+    monkeypatch.setattr(kb, "paged_fp4_attention_workspace_size", refuse)
+    with pytest.raises(kb.KvpError):
+        step(cache, [0], 3)
+    assert cache.calls == [] and cache.lengths[0] == 0
