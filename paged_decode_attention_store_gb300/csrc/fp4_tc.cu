@@ -44,8 +44,8 @@
 // lane sees a NaN scale (a compare, and only with several query tokens) its scale counts as zero and the columns that
 // attend it get the NaN by hand.
 //
-// Every wait is bounded (2 s): on timeout the CTA records KVP_ERR_TIMEOUT, waits (bounded) for its own copies and
-// returns.
+// Every wait is bounded (2 s): on timeout the CTA records KVP_ERR_TIMEOUT and returns; its producers wait (4 s) for the copies
+// that they issued, whoever gave up.
 #include <cuda_fp16.h>
 #include <cudaTypedefs.h>
 
@@ -513,14 +513,14 @@ __device__ void produce(const Args& a, const Smem& s, const Plan& pl, int me, in
     if (!more) break;
     cur = nxt;
   }
-  if (!ok) {  // let the copies land before the CTA ends
-    *s.abort_flag = 1;
-    for (int k2 = k - PW; k2 >= 0 && k2 >= k - PW - S; k2 -= PW) {
-      const uint64_t t_start = global_timer_ns();
-      while (!mbar_try_wait(&s.full[k2 % S], (uint32_t)(k2 / S & 1)))
-        if (global_timer_ns() - t_start > 100000000ull) break;
-    }
-  }
+  if (!ok) *s.abort_flag = 1;
+  // The copies land (bounded) before the CTA ends, also when all of them went out: a consumer may give up and leave later. The
+  // last ones of each buffer; older ones' buffers were filled again.
+  const long long from = ok ? pl.R1 - pl.R0 - S : (long long)k - PW - S + 1;
+  const uint64_t start = global_timer_ns();
+  for (int k2 = k - PW; k2 >= 0 && k2 >= from; k2 -= PW)
+    while (!mbar_try_wait(&s.full[k2 % S], (uint32_t)(k2 / S & 1)))
+      if (global_timer_ns() - start > 2 * kWaitNs) return;
 }
 
 // ---------------------------------------------------------------------------
