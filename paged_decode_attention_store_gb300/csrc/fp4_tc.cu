@@ -405,6 +405,7 @@ __device__ __forceinline__ void load_rows(const Args& a, const Smem& s, Hdr h, i
   }
   __syncwarp();
   if (together && j == 0) {  // lanes 0 and 16
+    fence_proxy_async_smem();  // the buffer's scales may have come by cp.async before, and these are another proxy's writes
     tma_load_4d(sbuf + grp * s.code_group, &a.map, 0, base, h.group * HG, a.layer, full);
     bulk_g2s(scb + grp * s.scale_group, a.scales + fp4_scale_offset(base, h.group * HG, a.Hkv, kD), (uint32_t)s.scale_group,
              full);

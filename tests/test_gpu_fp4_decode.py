@@ -90,3 +90,23 @@ def test_many_rows_far_below_one(kb, C, at, gap):  # noqa: F811
         # a weight is off by half a step of fp16, or, below 2^-14 of a largest one that is 2^7 at least, by 2^-32 of that
         bound = bound + (2.0 ** -32 - 2.0 ** -25) * (p + 1) * c.v[sl, 0].abs().amax()
         R.check(c.out[:, j].cpu(), want.expand(B, 8, -1), bound.expand(B, 8, -1), f"query {j}")
+
+
+@pytest.mark.parametrize("C,H,hkv", [(1, 32, 8), (4, 32, 8), (1, 8, 2)])
+def test_groups_together_and_apart_in_turn(kb, C, H, hkv):  # noqa: F811
+    """A raw table whose groups of 16 rows lie together (one copy) and apart (row by row) by turns of odd length, so that a
+    buffer's scales come now by the one and now by the other kind of copy; the same bits each time."""
+    c = Case(kb, "bf16", [1500 + i for i in range(40)], C, H, hkv, 128, 16, raw=True, seed=4)
+    g = torch.Generator().manual_seed(5)
+    table = c.table.cpu()
+    for b, sl in enumerate(c.slots):
+        for t in range(0, len(sl) - 16, 16):
+            if (t // 16) % 7 in (2, 3, 5):
+                sl[t:t + 16] = [sl[t + i] for i in torch.randperm(16, generator=g).tolist()]
+        table[b, :len(sl)] = torch.tensor(sl)
+    c.table.copy_(table)
+    first = c.run().clone()
+    c.verify(only=[0, 13, 39])
+    for _ in range(5):
+        c.run()
+        assert torch.equal(first, c.out)
