@@ -5,13 +5,16 @@ CUDA tensors (PyTorch supplies device memory and streams); every step of the
 path runs in the library's kernels. A missing library or a non-zero status
 raises: there is no fallback. The calls that a step makes once a layer hand
 plain arguments to the library through _marshal.so (csrc/python/marshal.cpp),
-the others, and whatever is not plain, through ctypes.
+the others, and whatever is not plain, through ctypes; without that module, or
+with one that was built against another torch or Python, all of them do, at 5 us
+or so a call more.
 """
 
 from __future__ import annotations
 
 import ctypes
 import os
+import warnings
 
 import torch
 
@@ -153,22 +156,29 @@ def lib():
     return _lib
 
 
-_marshal = None
+_marshal = None  # the module, or False: none that fits
 
 
 def _native():
-    """The argument marshalling in C++ (_marshal.so, built with the library), None where another library stands in for it."""
+    """The argument marshalling in C++ (_marshal.so, built with the library); None where another library stands in for it, and,
+    with a warning, where there is no module that fits this torch and Python."""
     global _marshal
     if lib() is not _lib:
         return None
     if _marshal is None:
+        from .build import marshal_for
+
         try:
             from . import _marshal as m
-        except ImportError as e:
-            raise RuntimeError(f"_marshal.so cannot be loaded ({e}): build it first (python -c 'import __graft_entry__ as g; "
-                               "g.build()')") from e
-        _marshal = m
-    return _marshal
+
+            why = None if m.built_for == marshal_for() else f"built for {m.built_for}, not {marshal_for()}"
+        except (ImportError, AttributeError) as e:
+            why = str(e)
+        if why:
+            warnings.warn(f"_marshal.so is not used ({why}), every call goes through ctypes: build it (python -c "
+                          "'import __graft_entry__ as g; g.build()')", RuntimeWarning, stacklevel=3)
+        _marshal = False if why else m
+    return _marshal or None
 
 
 def _address(what):

@@ -28,6 +28,7 @@ LIB = os.path.join(HERE, "libpagedkv.so")
 TRACE_LIB = os.path.join(HERE, "libpagedkv_trace.so")
 MARSHAL_SRC = os.path.join(CSRC, "python", "marshal.cpp")
 MARSHAL = os.path.join(HERE, "_marshal.so")
+MARSHAL_FOR = os.path.join(BUILD, "marshal_for")  # the torch and Python that it was built against
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -61,23 +62,41 @@ def _run(cmd):
     return r.stdout + r.stderr
 
 
+def marshal_for() -> str:
+    """The torch and Python whose headers' layouts the marshalling takes for granted."""
+    import torch
+
+    return f"torch {torch.__version__} Python {sys.version_info[0]}.{sys.version_info[1]}"
+
+
+def marshal_is_new() -> bool:
+    if not (os.path.exists(MARSHAL) and os.path.exists(MARSHAL_FOR)):
+        return False
+    with open(MARSHAL_FOR) as f:
+        return f.read() == marshal_for() and os.path.getmtime(MARSHAL) > os.path.getmtime(MARSHAL_SRC)
+
+
 def build_marshal(force: bool = False) -> str:
     """Compile the binding's argument marshalling; returns its path."""
-    if not force and os.path.exists(MARSHAL) and os.path.getmtime(MARSHAL) > os.path.getmtime(MARSHAL_SRC):
+    if not force and marshal_is_new():
         return MARSHAL
     import sysconfig
 
     import torch
 
+    os.makedirs(BUILD, exist_ok=True)
     home = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(_nvcc()))
     tmp = MARSHAL + ".tmp"
     _run(["g++", "-O2", "-std=c++20", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"], "-I", os.path.join(home, "include"),
           "-I", os.path.join(home, "include", "torch", "csrc", "api", "include"), "-I", os.path.join(cuda, "include"),
-          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", MARSHAL_SRC, "-o", tmp,
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DKVP_BUILT_FOR="{marshal_for()}"',
+          MARSHAL_SRC, "-o", tmp,
           "-L", os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
           "-Wl,-rpath," + os.path.join(home, "lib")])
     os.replace(tmp, MARSHAL)
+    with open(MARSHAL_FOR, "w") as f:
+        f.write(marshal_for())
     return MARSHAL
 
 
