@@ -55,7 +55,12 @@ struct Args {
     PyObject* o = next();
     if (PyFloat_CheckExact(o)) return PyFloat_AS_DOUBLE(o);
     if (!PyLong_CheckExact(o)) ok = false;
-    return ok ? PyLong_AsDouble(o) : 0.0;
+    const double x = ok ? PyLong_AsDouble(o) : 0.0;
+    if (PyErr_Occurred()) {  // past a double's range: Python's way says so
+      PyErr_Clear();
+      ok = false;
+    }
+    return x;
   }
   // None: the current stream
   void* stream() {
