@@ -440,6 +440,14 @@ def _raw_stream(stream):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _int32(x, name):
+    """An argument that a C int holds (ctypes would cut it down to one)."""
+    x = int(x)
+    if not -(1 << 31) <= x < 1 << 31:
+        raise OverflowError(f"{name} must be an int32, got {x}")
+    return x
+
+
 def _heads_view(t, index, dt, name, heads, width):
     """(address, stride of a token, stride of a head, heads) of a [n, heads, width] view on device ``index`` whose last
     axis is contiguous."""
@@ -516,6 +524,7 @@ def _rotary_call(what, pool, layer, q, first, second, positions, out_loc, rope, 
                              None if stream is None else _raw_stream(stream))
         if code is not None:
             return _check(code, name)
+    layer = _int32(layer, "layer")
     if (k is None) != (v is None):
         raise ValueError(f"{first[1]} and {second[1]} come together")
     freqs = of_pair = rot = layout = pos = apart = 0
@@ -608,6 +617,7 @@ def load_cache_fp4(pool, layer, slots, k_out, v_out, stream=None):
                            pool.kv_heads * pool.head_dim, None if stream is None else _raw_stream(stream))
         if code is not None:
             return _check(code, "load_cache_fp4")
+    layer = _int32(layer, "layer")
     n = _on(slots, dev, torch.int32, "slots").numel()
     for t, name in ((k_out, "k_out"), (v_out, "v_out")):
         if _on(t, dev, dt, name).numel() != n * pool.kv_heads * pool.head_dim:
@@ -643,6 +653,8 @@ def paged_fp4_attention(pool, layer, q, table, table_mode, context_lens, window,
                              out, workspace, None if stream is None else _raw_stream(stream))
         if code is not None:
             return _check(code, "paged_fp4_attention")
+    layer, sinks, most = _int32(layer, "layer"), _int32(sinks, "sinks"), (1 << 31) - 1
+    window = max(0, min(int(window or 0), most))  # one that no context can fill is none
     _on(q, dev, dt, "q")
     _on(out, dev, dt, "out")
     _on(table, dev, torch.int32, "table")
@@ -662,10 +674,10 @@ def paged_fp4_attention(pool, layer, q, table, table_mode, context_lens, window,
     rows, cols = table.shape
     if max_context is None:
         max_context = cols if table_mode == KVP_RAW_LOCATIONS else cols * pool.page_size
-    max_context = min(int(max_context), (1 << 31) - 1)
+    max_context = max(0, min(int(max_context), most))
     _check(lib().paged_fp4_attention(pool.handle, layer, q.data_ptr(), B, C, Hq, per[0], table.data_ptr(), rows, cols,
-                                     table_mode, per[1], context_lens.data_ptr(), max_context, int(window or 0),
-                                     int(sinks), float(scale), out.data_ptr(), _on(workspace, dev, None, "workspace").data_ptr(),
+                                     table_mode, per[1], context_lens.data_ptr(), max_context, window, sinks,
+                                     float(scale), out.data_ptr(), _on(workspace, dev, None, "workspace").data_ptr(),
                                      workspace.nbytes, _raw_stream(stream)), "paged_fp4_attention")
 
 

@@ -8,7 +8,8 @@ from test_gpu_marshalling import DEV, kb, rnd  # noqa: F401
 pytestmark = pytest.mark.gpu
 
 
-@pytest.mark.parametrize("bad", [dict(scale=10 ** 400), dict(scale=-10 ** 400)])
+@pytest.mark.parametrize("bad", [dict(scale=10 ** 400), dict(scale=-10 ** 400), dict(layer=1 << 32), dict(layer=-1 << 70),
+                                 dict(sinks=1 << 40), dict(max_context=-1 << 40)])
 def test_numbers_past_their_range(kb, bad):  # noqa: F811
     pool = kb.kv_fp4_pool_create(8, 16, 2, 64, kb.KVP_BF16, 1, device=DEV, zero=True)
     q = rnd(2, 1, 8, 64)
@@ -24,6 +25,17 @@ def test_numbers_past_their_range(kb, bad):  # noqa: F811
         attend()
     torch.cuda.synchronize()
     assert bool((out == 5.0).all()) and kb.kvp_sync_error(pool) == 0
-    a = dict(a, scale=0.1)
+    a = dict(layer=0, window=1 << 40, sinks=3, scale=0.1, max_context=1 << 40)  # no window, any context
     attend()
     assert kb.kvp_sync_error(pool) == 0 and not bool((out == 5.0).any())
+
+
+@pytest.mark.parametrize("layer", [1 << 32, 1 << 70, -1 << 32])
+def test_layers_past_their_range(kb, layer):  # noqa: F811
+    pool = kb.kv_fp4_pool_create(8, 16, 2, 64, kb.KVP_BF16, 1, device=DEV, zero=True)
+    x, i = rnd(3, 2, 64), torch.arange(3, dtype=torch.int32, device=DEV)
+    with pytest.raises(OverflowError):
+        kb.store_cache_fp4(pool, layer, x, x, i)
+    with pytest.raises(OverflowError):
+        kb.load_cache_fp4(pool, layer, i, x, x)
+    assert not bool(pool.codes.any())
