@@ -92,6 +92,89 @@ def test_many_rows_far_below_one(kb, C, at, gap):  # noqa: F811
         R.check(c.out[:, j].cpu(), want.expand(B, 8, -1), bound.expand(B, 8, -1), f"query {j}")
 
 
+@pytest.mark.parametrize("C,raw,sign", [(1, False, 1), (1, False, -1), (1, True, 1), (4, False, 1), (4, True, -1), (20, False, 1)])
+def test_scores_that_rise_stage_by_stage(kb, C, raw, sign):  # noqa: F811
+    """Every 32 rows score 10 above the 32 before in log2: the maximum is raised with each, in both directions of time."""
+    L = 32 * 63 - 5
+    c = Case(kb, "bf16", [L] * 20 + [33], C, 8, 8, 128, 1 if raw else 16, raw, seed=1)
+    g = torch.Generator().manual_seed(2)
+    k, v = torch.zeros(L, 128), torch.randn(L, 128, generator=g)
+    at = torch.arange(L) // 32
+    for i in range(6):
+        k[:, 16 * i] = torch.where(at >> i & 1 > 0, 2.0 ** i, 0.0)
+    rewrite(c, k, v)
+    c.q.zero_()
+    c.q[..., ::16] = float(sign)
+    c.scale = 10 / LOG2E
+    c.run()
+    c.verify(only=[0, 7, 19, 20], few=True)
+
+
+@pytest.mark.parametrize("most", [250, 257, FAR])
+@pytest.mark.parametrize("C,H,hkv", [(1, 32, 8), (4, 32, 8), (1, 32, 16), (2, 4, 1)])
+@pytest.mark.parametrize("times,fill", [(1, 0x00), (1, 0x3C), (60, 0x00), (200, 0x3C)])
+def test_bad_requests_are_zeros_and_recorded(kb, C, H, hkv, times, fill, most):  # noqa: F811
+    """Invalid requests among few, whose pieces are recorded by request, and among many, by CTA; in workspaces of zeros and
+    of small numbers."""
+    lens = [200, 4, 220, 170, 250] * times
+    c = bounded(Case(kb, "bf16", lens, C, H, hkv, 128, 16, seed=6), most, fill)
+    clens, rows = torch.tensor(lens), torch.arange(5 * times)
+    clens[1::5], clens[2::5], rows[3::5] = 0, 100000, 5 * times + 7
+    clens[3::15] = -3
+    c.clens.copy_(clens)
+    c.run(table_rows=rows.to(torch.int32).to(DEV))
+    assert kb.kvp_sync_error(c.pool) == kb.KVP_ERR_BAD_INDEX
+    for i in (1, 2, 3):
+        assert bool((c.out[i::5] == 0).all()), i
+    last = 5 * times
+    c.verify(only=sorted({0, 4, last - 5, last - 1}))
+
+
+@pytest.mark.parametrize("C,raw,P", [(1, False, 16), (4, False, 16), (1, False, 4), (1, True, 16), (4, True, 1), (20, True, 1)])
+def test_holes_are_skipped_and_recorded(kb, C, raw, P):  # noqa: F811
+    """Holes, entries past the pool and far past it, in pages that come whole and in rows that come one by one."""
+    c = bounded(Case(kb, "bf16", [200, 220, 300], C, 32, 8, 128, P, raw, seed=6), FAR)
+    c.table[0, 3] = -1
+    c.table[0, 5] = 1 << 30
+    c.table[0, 11] = c.pool.num_pages * (P if raw else 1)
+    c.table[2] = -1
+    c.run()
+    assert kb.kvp_sync_error(c.pool) == kb.KVP_ERR_BAD_INDEX
+    c.verify(only=[1])
+
+
+@pytest.mark.parametrize("C,raw", [(1, False), (4, False), (1, True)])
+def test_queries_of_any_size(kb, C, raw):  # noqa: F811
+    c = bounded(Case(kb, "bf16", [150, 99, 400], C, 32, 8, 128, 1 if raw else 16, raw, seed=9), FAR)
+    for h, e in ((0, -100), (1, -40), (3, 100), (6, -126)):
+        c.q[:, :, h] *= 2.0 ** e
+    c.q[:, :, 4] = 0
+    c.q[:, :, 5, ::3] *= 2.0 ** -30
+    c.run()
+    out = c.out.cpu()
+    assert not bool(out.isnan().any())
+    for b in range(3):
+        for j in range(C):
+            w, bound = c.want(b, j, C)
+            keep = [h for h in range(32) if h != 3]
+            R.check(out[b, j, keep], w[keep], bound[keep])
+            R.check(out[b, j, 3], w[3], R.u(torch.bfloat16) * w[3].abs() + 1e-30)  # one key has all the weight
+
+
+@pytest.mark.parametrize("C", [1, 4])
+def test_queries_that_are_not_finite(kb, C):  # noqa: F811
+    c = bounded(Case(kb, "bf16", [150, 700], C, 32, 8, 128, 16, seed=9), FAR)
+    c.q[0, 0, 3, 7] = float("nan")
+    c.q[1, C - 1, 9, 7] = float("inf")
+    c.run()
+    bad = c.out.isnan().all(-1).cpu()
+    assert bool(bad[0, 0, 3]) and bool(bad[1, C - 1, 9]) and int(c.out.isnan().any(-1).sum()) == 2
+    for b, j, h in ((0, 0, 3), (1, C - 1, 9)):
+        w, bound = c.want(b, j, C)
+        keep = [x for x in range(32) if x != h]
+        R.check(c.out[b, j, keep].cpu(), w[keep], bound[keep])
+
+
 @pytest.mark.parametrize("C,H,hkv", [(1, 32, 8), (4, 32, 8), (1, 8, 2)])
 def test_groups_together_and_apart_in_turn(kb, C, H, hkv):  # noqa: F811
     """A raw table whose groups of 16 rows lie together (one copy) and apart (row by row) by turns of odd length, so that a
