@@ -265,7 +265,7 @@ class PagedKVCache:
     def _append_and(self, work, rids, B, C, window, sinks):
         """A step of B distinct requests, C new tokens each: append, then ``work(lens, rows, positions, out_loc)`` (int32 on
         the device: contexts and table rows [B], positions and slots [B * C]), then the pages that the window leaves are
-        released. A step that is refused leaves the lengths and pages as they were."""
+        released. A step that is refused leaves the lengths and pages as they were, but for a copy of a shared last page."""
         r = np.ascontiguousarray(rids, dtype=np.int32)
         if len(r) != B or len(np.unique(r)) != B:
             raise ValueError(f"step takes {B} distinct requests, got {list(map(int, r))}")
@@ -473,7 +473,8 @@ class PagedLatentCache(PagedKVCache):
         latent_dim], ``k_pe`` [B * C, rope_dim] (request-major), ``out`` [B, C,
         Hq, latent_dim]. With a window, the pages it leaves are released
         afterwards. A step that is refused leaves the lengths and pages as they
-        were. Asynchronous on the current stream."""
+        were, but that a shared last page may have been copied. Asynchronous on
+        the current stream."""
         B, C, Hq, W = q[0].shape
 
         def work(lens, rows, positions, out_loc):
@@ -596,13 +597,21 @@ class PagedFp4Cache(PagedKVCache):
         self.attend(layer, q, context_lens, window, scale, out, q_lens=q_lens, table_rows=table_rows, sinks=sinks,
                     max_context=max_context)
 
-    def _check_step(self, q, k, v, out, window, scale, sinks, max_context):
-        """Refuses what a layer's attention or a later layer would refuse, before the first turns its q in place."""
+    def _check_step(self, q, k, v, rope, out, window, scale, sinks, positions, max_context):
+        """Refuses what a layer would refuse, before tokens are appended (an append may copy a shared page, which stays) and
+        before the first layer turns its q in place."""
         B, C, Hq, D = shape = q[0].shape
         if scale != scale or sinks < 0 or (window and 0 < window <= sinks):
             raise ValueError(f"scale, window and sinks cannot be {scale}, {window} and {sinks}")
-        self.workspace(B, Hq, C, max_context)
         index = self.pool.device_index
+        if rope is not None:
+            if positions is not None and kb._positions_of(positions, index, rope.axes)[1] != B * C:
+                raise ValueError(f"positions must be those of {B * C} tokens, got {tuple(positions.shape)}")
+            if rope.rotary_dim > self.D or rope.attn_factor != rope.attn_factor:
+                raise ValueError(f"the plan turns {rope.rotary_dim} entries of {self.D}, by {rope.attn_factor}")
+            if rope.rotary_dim and rope.freqs.get_device() != index:
+                kb._elsewhere(rope.freqs, index, "the plan's frequencies")
+        self.workspace(B, Hq, C, max_context)
         native = kb._native()
         if native is not None and native.step(self.pool.dtype, index, self.layers, q, out, k, v, B, C, Hq, self.Hkv, self.D):
             return
@@ -626,7 +635,7 @@ class PagedFp4Cache(PagedKVCache):
         Asynchronous on the current stream."""
         B, C, Hq, D = q[0].shape
         bound = self._bound_of(self.lengths[np.ascontiguousarray(rids, dtype=np.int32)] + C)
-        self._check_step(q, k, v, out, window, scale, sinks, bound["max_context"])
+        self._check_step(q, k, v, rope, out, window, scale, sinks, positions, bound["max_context"])
 
         def work(lens, rows, places, out_loc):
             pos = positions

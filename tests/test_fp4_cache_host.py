@@ -120,3 +120,26 @@ def test_heads_that_do_not_divide(cache, monkeypatch):
     with pytest.raises(kb.KvpError):
         step(cache, [0], 3)
     assert cache.calls == [] and cache.lengths[0] == 0
+
+
+@pytest.mark.parametrize("what", ["width", "positions", "axes", "factor", "device", "layer"])
+def test_a_refused_step_keeps_shared_pages(cache, what):
+    """A request that shares its last page: an append would copy it, a refused step does not."""
+    kb = ensure_built()
+    cache.new(0)
+    step(cache, [0], 20)
+    cache.fork(0, 1)
+    before = (cache.host.used(), cache.host.block_row(0), cache.host.block_row(1), cache.host.refcounts())
+    cache.calls.clear()
+    elsewhere = plan(kb)
+    elsewhere.freqs = types.SimpleNamespace(get_device=lambda: 1, is_cuda=True, device="cuda:1")
+    bad = {"width": dict(rope=kb.RotaryPlan(2 * D, device="cpu")), "positions": dict(positions=torch.zeros(2, dtype=torch.int32)),
+           "axes": dict(rope=kb.RotaryPlan(D, device="cpu", sections=(16, 16)), positions=torch.zeros(3, dtype=torch.int32)),
+           "factor": dict(rope=kb.RotaryPlan(D, device="cpu", attn_factor=float("nan"))), "device": dict(rope=elsewhere),
+           "layer": dict(v=[torch.zeros((3, HKV, D), dtype=torch.bfloat16), None])}[what]
+    with pytest.raises((ValueError, TypeError)):
+        step(cache, [1], 3, **bad)
+    assert (cache.host.used(), cache.host.block_row(0), cache.host.block_row(1), cache.host.refcounts()) == before
+    assert [x for x in cache.calls if x[0] != "size"] == [] and cache.lengths[1] == 20
+    step(cache, [1], 3)
+    assert cache.host.used() == before[0] + 1
