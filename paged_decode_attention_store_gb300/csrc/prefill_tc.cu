@@ -935,13 +935,9 @@ int launch_prefill_tc(const kvp_pool* pool, int layer, const void* q, int batch,
   a.sinks = sinks;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.err = pool->err;
-  static bool attr = false;
-  if (!attr) {
-    if (cudaFuncSetAttribute(prefill_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPrefillSmem) !=
-        cudaSuccess)
-      return KVP_ERR_CUDA;
-    attr = true;
-  }
+  // set at every call: it belongs to the current device
+  if (cudaFuncSetAttribute(prefill_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPrefillSmem) != cudaSuccess)
+    return KVP_ERR_CUDA;
   const long long grid = (long long)a.tiles * batch * pool->kv_heads;
   if (grid <= 0 || grid > 0x7fffffffLL) return KVP_ERR_INVALID_ARG;
   prefill_tc_kernel<<<(unsigned)grid, kPThreads, kPrefillSmem, stream>>>(a);
