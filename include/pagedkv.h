@@ -475,7 +475,11 @@ int load_cache_fp4(const kvp_pool* pool, int layer, const int32_t* slots, int n,
  * otherwise unspecified. Rows past the context, out of a query's window and in
  * other pages may hold anything. A block that reads as NaN reaches the queries
  * that attend it and no others: one of K makes that head's output NaN, one of V
- * its 16 entries. The pool's device must be current.
+ * its 16 entries. Scores are fp32: one that overflows to minus infinity weighs
+ * nothing, a query all of whose scores do gets zeros, and plus infinity makes the
+ * head's output NaN. bf16 pools hold a query row in fp16, scaled to its largest
+ * entry: one below 2^-14 of that is off by 2^-25 of it at most. The pool's device
+ * must be current.
  * ---------------------------------------------------------------------- */
 int paged_fp4_attention_workspace_size(const kvp_pool* pool, int batch, int chunk,
                                        int num_q_heads, int max_context,

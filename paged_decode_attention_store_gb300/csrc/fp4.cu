@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(32 * kF32Warps, I == 1 ? 2 : 1) fp4_f32_kernel
              cluster.map_shared_rank(&part_l[0][0], k / kParts)[from(k)];
 #pragma unroll
     for (int sh = 16; sh > 0; sh >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, sh);
-    const float inv = a.gv / sum;
+    const float inv = sum == 0.f ? 0.f : a.gv / sum;  // every score minus infinity: zeros, as in the other kernels
     float* dst = a.out + column(col);
     for (int e = 4 * lane; e < D; e += 128) {
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);

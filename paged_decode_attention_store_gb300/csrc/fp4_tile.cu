@@ -322,7 +322,7 @@ __device__ __forceinline__ void tile_item(const TileArgs& a, unsigned char* smem
     for (int y = 0; y < 2; ++y) {
       const int col = col0 + 16 * ct + g + 8 * y;
       if (col >= cols || col / a.G > j1) continue;
-      const float inv = a.gv / l[y];
+      const float inv = l[y] == 0.f ? 0.f : a.gv / l[y];  // every score minus infinity: zeros, as in the other kernels
       uint32_t* dst = reinterpret_cast<uint32_t*>(column_out(col));
 #pragma unroll
       for (int d = 0; d < DT / 8; ++d)
@@ -379,7 +379,7 @@ __device__ __forceinline__ void tile_item(const TileArgs& a, unsigned char* smem
           acc[i].y += scale * x.y;
         }
     }
-    const float inv = a.gv / sum;
+    const float inv = sum == 0.f ? 0.f : a.gv / sum;
     uint32_t* dst = reinterpret_cast<uint32_t*>(column_out(col));
 #pragma unroll
     for (int i = 0; i < DT / 64; ++i)
