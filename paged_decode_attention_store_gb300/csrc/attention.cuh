@@ -160,7 +160,7 @@ cudaError_t launch_tc(const TcArgs& a, const CombineArgs& c, cudaStream_t stream
 // ---------------------------------------------------------------------------
 // Latent pools (latent.cu, latent_tc.cu) and expanded prompts (expanded.cu).
 // ---------------------------------------------------------------------------
-constexpr int kFp4MaxDim = 256;  // head_dim of four-bit pools: the general kernel's registers hold 8 entries a lane
+constexpr int kFp4MaxDim = 256;  // head_dim of four-bit pools: the tile kernel's columns have 32 sums of four entries a lane
 constexpr int kLatentMaxDim = 1024;  // the general kernel's registers hold 32 floats a lane
 
 TableRef make_table(const kvp_pool* pool, const int32_t* table, int rows_total, int cols, int mode);

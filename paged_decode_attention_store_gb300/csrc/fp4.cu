@@ -12,7 +12,8 @@
 // requests at a time as 4 GiB of rows hold. Bytes: 1.1 KB
 // read and 4 KB written a token of eight heads, and read again by the chunk
 // kernel, mostly from L2. Of the 258 us the unpacking takes 32, the chunk kernel
-// 221, the look for NaN 4; five prompts of 33-600 tokens 48 us (7, 38, 3).
+// 221, the look for NaN 4; five prompts of 33-600 tokens 48 us (7, 38, 3); called
+// one by one, without a graph, 267 and 55.
 // That kernel multiplies V by weights of zero where a query does not attend, so a
 // block that reads as NaN would reach more queries than it should: a request with
 // one in its span is noticed on the way and done again (fp4_tile.cu; 383 us with

@@ -37,8 +37,9 @@
 // Measured (8 KV heads of 128, pages of 16): 256 requests of 512-4096 rows, 32 query heads, 136 us (0.73 of a copy's rate);
 // 64 of them 46.8 us (0.57); with 4 tokens each 62 us; one of 777 rows 11 us, of which about 2 us are the work split, 1 the
 // table, 3 the first rows' way and 3.5 the join: chains of memory latencies, as in the other small calls. 32 requests of
-// 8,192-32,768 scattered rows, 64 query heads, 192 us (0.61): a row's scales, 16 bytes a head, cost a sector of 32
-// each (161 us with the scales left out).
+// 8,192-32,768 scattered rows, 64 query heads, 192 us (0.61; 116 at a copy's rate): a row's scales, 16 bytes a head, cost a
+// sector of 32 each, 31 us of that (161 with the scales left out); what the other 44 are, the rows' single copies or their
+// issue, has not been measured.
 //
 // A block of V that reads as NaN may be attended by some of the columns only: 0 * NaN would reach the others, so when a
 // lane sees a NaN scale (a compare, and only with several query tokens) its scale counts as zero and the columns that

@@ -14,7 +14,9 @@
 // A row is turned back once for every 64 columns, not once a call as in the chunk path, so long chunks are bound by the
 // conversions and by mma's rate; few columns by the loads' latency, which other CTAs of the SM hide. 64 requests of 512-4096
 // rows, 32 query heads on 8: head_dim 64 98 us (13 at the memory's rate; a block a query head on CUDA cores 474), 256 307
-// (51; 1537). 16 chunks of 512 tokens on up to 2048 rows, head_dim 64: 532 us (29,107).
+// (51; 1537). 16 chunks of 512 tokens on up to 2048 rows, head_dim 64: 532 us (29,107; some 45 at the matrix rate). Rows come
+// by one thread's plain loads a row, one block ahead, between two barriers a block; a ring of asynchronous copies, as the decode
+// kernel's, has not been built for these widths.
 //
 // A block of V that reads as NaN counts as zero; the columns that attend it get the NaN by hand.
 #include <cooperative_groups.h>
