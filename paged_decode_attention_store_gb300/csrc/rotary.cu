@@ -36,8 +36,8 @@
 // 64 tokens 5.3 us (queries alone 2.5, as one launch with chains for both); 8,192 tokens
 // 37 us (3.8 TB/s; queries 23.8, keys and values alone 25.2, of which bytes need 6.3); 30,011
 // tokens of 64 heads, half of each turned, slot by slot, 231 us (158 and 82). Keys and values
-// wait for this code's instructions (68 % of the issue slots), and not for the turn's: rows
-// as they are take 23. What of them the rounding cannot do without has not been measured.
+// wait for this code's instructions (over two thirds of the issue slots), and not for the turn's:
+// rows as they are take 23. What of them the rounding cannot do without has not been measured.
 #include "fp4.cuh"
 
 #include <cmath>
