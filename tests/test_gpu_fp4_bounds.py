@@ -82,3 +82,23 @@ def test_few_columns_of_many_long_contexts(kb):  # noqa: F811
     assert c.ws.numel() == LIMIT
     c.run()
     c.verify()
+
+
+def test_groups_captured_and_replayed(kb):  # noqa: F811
+    """Requests that go through the workspace in groups, over a raw table, in a graph that is replayed with other lengths."""
+    c = bounded(Case(kb, "bf16", [300, 411, 177, 500], 140, 32, 8, 128, 16, raw=True, seed=5), 400000)
+    want = c.run().clone()
+    g = torch.cuda.CUDAGraph()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(g, stream=s):
+        kb.paged_fp4_attention(c.pool, 0, c.q, c.table, kb.KVP_RAW_LOCATIONS, c.clens, 0, c.scale, c.out, c.ws, max_context=c.most)
+    for lens in ([300, 411, 177, 500], [150, 411, 140, 260], [300, 411, 177, 500]):
+        c.clens.copy_(torch.tensor(lens))
+        c.out.fill_(5.0)
+        c.lens = lens
+        g.replay()
+        torch.cuda.synchronize()
+        assert kb.kvp_sync_error(c.pool) == 0
+        c.verify(few=True)
+    assert torch.equal(c.out, want)
